@@ -549,6 +549,164 @@ int zero_copy(void* dst, const void* src, int64_t bytes, zero_stream_t stream);
  * count afterwards.  Errors: EINVAL (timeouts NULL), ECUDA. */
 int zero_async_status(int64_t* timeouts, int32_t reset);
 
+/* --------------------------------------------- layer computation (ops) --
+ * No counterpart on the pages beyond "[P4] Implementation Strategy": stage 3
+ * gathers a layer's parameters before its forward and backward pass and
+ * discards them after.  These calls are that pass for a feed-forward
+ * sublayer: they read weights where zero_gather_layer put them (bf16) and
+ * write weight gradients where zero_step_group reads them (bf16 or fp32).
+ *
+ * Conventions of this section
+ *   - A matrix [rows, cols] is a device pointer and a row distance ld in
+ *     elements (ld >= cols; each row is contiguous).  Any element-aligned
+ *     base and any ld are accepted; bases and rows on 16-byte boundaries
+ *     take the fast paths.  Sizes and ld are below 2^31, except that rows
+ *     may be spread over more than 2^31 elements.
+ *   - A size of 0 is valid: nothing is written where no element exists, and
+ *     a sum over nothing is 0.
+ *   - Sums, statistics and everything between load and store are fp32; a
+ *     result is rounded once, to its output's dtype (nearest even).
+ *   - Results do not depend on the run: no atomics, fixed orders of sums.
+ *   - Inputs and outputs must not overlap, except where an argument says so.
+ *   - Pointers marked "or NULL" are optional and leave out their term.
+ */
+typedef enum {
+  ZERO_ACT_NONE = 0,
+  ZERO_ACT_RELU = 1,
+  ZERO_ACT_GELU = 2,      /* z * Phi(z), Phi by the error function */
+  ZERO_ACT_GELU_TANH = 3, /* z/2 * (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
+  ZERO_ACT_SILU = 4       /* z / (1 + exp(-z)) */
+} zero_act_t;
+
+/* How a weight of a product from k inputs to n outputs is stored. */
+typedef enum {
+  ZERO_W_NK = 0, /* [n, k], one row per output (Llama's projections) */
+  ZERO_W_KN = 1  /* [k, n], one row per input (GPT-2's projections) */
+} zero_w_layout_t;
+
+/* Dropout's random numbers: element (row, col) of a matrix takes word
+ * col % 4 of Philox4x32-10 [Salmon, Moraes, Dror and Shaw, "Parallel random
+ * numbers: as easy as 1, 2, 3" (2011)] with key `seed` (low word first) and
+ * counter (col / 4, row, offset low, offset high), where offset is `offset`
+ * plus *d_offset (mod 2^64); it is kept when word >= floor(p * 2^32) and then
+ * scaled by 1 / (1 - p).  Nothing is stored: the gradient's call with the
+ * same seed and offset draws the same mask.  Give every use in a step its
+ * own offset.  d_offset (device memory, or NULL) lets a replayed CUDA graph
+ * draw new masks: write a new value between replays. */
+typedef struct {
+  float p;           /* probability of dropping, 0 <= p <= 1; p = 1 drops all */
+  uint32_t reserved; /* 0 */
+  uint64_t seed, offset;
+  const uint64_t* d_offset; /* 8-byte aligned device word, or NULL */
+} zero_dropout_t;
+
+/* What follows the product in zero_linear. */
+typedef struct {
+  const void* bias; /* [n], or NULL */
+  int32_t bias_dtype;
+  int32_t act;     /* zero_act_t */
+  void* pre;       /* out: bf16 [m, n], z before the activation, or NULL */
+  int64_t ldpre;
+  const void* gate; /* bf16 [m, n], multiplies the activation, or NULL */
+  int64_t ldgate;
+  const void* residual; /* [m, n], added last, or NULL; may be y itself */
+  int64_t ldres;
+  int32_t res_dtype;
+  int32_t reserved;              /* 0 */
+  const zero_dropout_t* dropout; /* host struct, or NULL: before the residual */
+} zero_linear_epilogue_t;
+
+/* What follows the product in zero_linear_dinput: the gradient of the
+ * activation that made the product's input. */
+typedef struct {
+  int32_t act; /* zero_act_t */
+  int32_t reserved;
+  const void* pre; /* bf16 [m, k]: that activation's z */
+  int64_t ldpre;
+  const void* gate; /* bf16 [m, k]: its gate, or NULL */
+  int64_t ldgate;
+  void* dgate; /* out: bf16 [m, k], the gate's gradient; with gate only */
+  int64_t lddgate;
+} zero_act_grad_t;
+
+/* zero_linear: y = residual + dropout(act(z) * gate), z = x W + bias, with
+ * x bf16 [m, k], W bf16 in `w_layout`, y [m, n] in ydtype.  `ep` may be NULL
+ * (y = x W).  One launch; z reaches memory only as `pre`.  k = 0 gives
+ * z = bias.  Errors: EINVAL (NULL pointer, negative size, ld below its row,
+ * unknown act, layout or nonzero reserved word, p outside [0, 1], y or pre
+ * the same pointer as x or w or each other), EALIGN (a pointer not aligned
+ * to its element), EDTYPE, ERANGE (size or ld of 2^31 or more), ECUDA. */
+int zero_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, int32_t w_layout,
+                int64_t m, int64_t n, int64_t k, const zero_linear_epilogue_t* ep, void* y,
+                int64_t ldy, zero_dtype_t ydtype, zero_stream_t stream);
+
+/* zero_linear_dinput: the gradient that reaches a product's input: da = dy
+ * W^T with dy bf16 [m, n] and W bf16 [k -> n] in `w_layout`; dx = da, or with
+ * `ag` (not NULL) through the activation that made the input:
+ * dx = da * act'(pre) * gate and dgate = da * act(pre).  dx [m, k] in dxdtype.
+ * act'(0) of RELU is 0.  n = 0 gives da = 0.  Errors as zero_linear. */
+int zero_linear_dinput(const void* dy, int64_t lddy, const void* w, int64_t ldw,
+                       int32_t w_layout, int64_t m, int64_t n, int64_t k,
+                       const zero_act_grad_t* ag, void* dx, int64_t lddx, zero_dtype_t dxdtype,
+                       zero_stream_t stream);
+
+/* zero_linear_dweight: the weight's gradient dw = dy^T x in layout ZERO_W_NK
+ * ([n, k]) or x^T dy in ZERO_W_KN ([k, n]), and the bias's dbias = sum of
+ * dy's rows ([n], or NULL), for dy bf16 [m, n] and x bf16 [m, k]; dw and
+ * dbias in dwdtype and dbdtype.  accumulate != 0 adds to what they hold
+ * (micro-batches), rounding the fp32 sum once.  Errors as zero_linear. */
+int zero_linear_dweight(const void* dy, int64_t lddy, const void* x, int64_t ldx, int64_t m,
+                        int64_t n, int64_t k, int32_t w_layout, void* dw, int64_t lddw,
+                        zero_dtype_t dwdtype, void* dbias, zero_dtype_t dbdtype,
+                        int32_t accumulate, zero_stream_t stream);
+
+/* zero_dropout: y = residual + keep(x) / (1 - p) for x, residual (or NULL)
+ * and y [m, n].  A dropped element contributes exactly 0, whatever x holds
+ * there.  The gradient of x is the same call on dy (residual NULL, the same
+ * rng); the residual's gradient is dy.  y may be x or residual itself (same
+ * ld and dtype).  Errors as zero_linear, and EINVAL for rng NULL. */
+int zero_dropout(const void* x, int64_t ldx, zero_dtype_t xdtype, const void* residual,
+                 int64_t ldres, zero_dtype_t res_dtype, int64_t m, int64_t n,
+                 const zero_dropout_t* rng, void* y, int64_t ldy, zero_dtype_t ydtype,
+                 zero_stream_t stream);
+
+typedef enum {
+  ZERO_NORM_LAYER = 0, /* (x - mean) * rstd * weight + bias */
+  ZERO_NORM_RMS = 1    /* x * rstd * weight + bias, mean taken as 0 */
+} zero_norm_t;
+
+/* zero_layer_norm: normalises each row of x [m, n] into y [m, n]: rstd =
+ * 1 / sqrt(mean of (x - mean)^2 + eps) with weight and bias (or NULL) [n] in
+ * pdtype.  mean and rstd: fp32 [m] outputs for the backward pass, or NULL.
+ * y may be x itself (same ld and dtype).  eps >= 0, finite.  Errors as
+ * zero_linear, and EINVAL (mean given with ZERO_NORM_RMS, bad eps). */
+int zero_layer_norm(const void* x, int64_t ldx, zero_dtype_t xdtype, const void* weight,
+                    const void* bias, zero_dtype_t pdtype, int64_t m, int64_t n, int32_t kind,
+                    float eps, void* y, int64_t ldy, zero_dtype_t ydtype, float* mean,
+                    float* rstd, zero_stream_t stream);
+
+/* zero_layer_norm_workspace: bytes of scratch zero_layer_norm_backward needs
+ * for [m, n] on the current device.  Errors: EINVAL, ERANGE. */
+int zero_layer_norm_workspace(int64_t m, int64_t n, int64_t* bytes);
+
+/* zero_layer_norm_backward: with h = (x - mean) * rstd (mean NULL: 0) and
+ * g = dy * weight: dx = dres + rstd * (g - mean(g) - h * mean(g h)) (no
+ * mean(g) term for ZERO_NORM_RMS), dweight = sum over rows of dy * h, dbias
+ * (or NULL) = sum of dy; dweight and dbias [n] in gdtype, added to what they
+ * hold when accumulate != 0.  dx is in dxdtype, as dres is (or NULL; may be
+ * dx itself): the gradient that arrives over the residual branch.  dx must
+ * not be dy or x.  workspace: 16-byte aligned device scratch of
+ * zero_layer_norm_workspace() bytes.  Errors as zero_linear, and EINVAL
+ * (workspace too small). */
+int zero_layer_norm_backward(const void* dy, int64_t lddy, zero_dtype_t dydtype, const void* x,
+                             int64_t ldx, zero_dtype_t xdtype, const void* weight,
+                             zero_dtype_t pdtype, const float* mean, const float* rstd,
+                             int64_t m, int64_t n, int32_t kind, const void* dres,
+                             int64_t lddres, void* dx, int64_t lddx, zero_dtype_t dxdtype,
+                             void* dweight, void* dbias, zero_dtype_t gdtype,
+                             int32_t accumulate, void* workspace, int64_t workspace_bytes,
+                             zero_stream_t stream);
+
 /* ------------------------------------------------------ checked build --
  * No counterpart on the pages: a stand-in for a device memory checker.  The
  * library built with -DZERO_CHECKED (libzero_checked.so, same ABI) tests
@@ -574,6 +732,10 @@ int zero_async_status(int64_t* timeouts, int32_t reset);
 #define ZERO_SITE_GATHER_OUT 13  /* stage-3 gather: layer buffer */
 #define ZERO_SITE_CHECKSUM 14    /* layer checksum: layer buffer */
 #define ZERO_SITE_COPY 15        /* zero_copy */
+#define ZERO_SITE_LINEAR_IN 16   /* products: x, dy, w read by plain loads */
+#define ZERO_SITE_LINEAR_OUT 17  /* products: epilogue operands and outputs */
+#define ZERO_SITE_DROPOUT 18     /* zero_dropout: x, residual, y */
+#define ZERO_SITE_LNORM 19       /* layer norm: x, dy, dres, y, dx, parameters */
 
 typedef struct {
   int32_t checked; /* 1 in the checked build */

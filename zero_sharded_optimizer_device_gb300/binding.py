@@ -36,6 +36,9 @@ ZERO_OCC_FUSED, ZERO_OCC_RS, ZERO_OCC_ADAM, ZERO_OCC_GATHER, ZERO_OCC_STREAM, \
     ZERO_OCC_CONSUMER, ZERO_OCC_PREFETCH = range(7)
 ZERO_MAX_CONSUMER_ROUNDS = 4096
 ZERO_MAX_COALESCE = 64
+ZERO_ACT_NONE, ZERO_ACT_RELU, ZERO_ACT_GELU, ZERO_ACT_GELU_TANH, ZERO_ACT_SILU = range(5)
+ZERO_W_NK, ZERO_W_KN = range(2)
+ZERO_NORM_LAYER, ZERO_NORM_RMS = range(2)
 
 _NAMES = {0: "ZERO_OK", -1: "ZERO_EINVAL", -2: "ZERO_EALIGN", -3: "ZERO_ERANGE",
           -4: "ZERO_EDTYPE", -5: "ZERO_ENOMEM", -6: "ZERO_ECUDA", -7: "ZERO_ETIMEOUT"}
@@ -90,6 +93,23 @@ class zero_bounds_t(ctypes.Structure):
 
 
 ZERO_SITE_PROBE = 1
+
+
+class zero_dropout_t(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_float), ("reserved", ctypes.c_uint32),
+                ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64), ("d_offset", c_vp)]
+
+
+class zero_linear_epilogue_t(ctypes.Structure):
+    _fields_ = [("bias", c_vp), ("bias_dtype", c_i32), ("act", c_i32), ("pre", c_vp),
+                ("ldpre", c_i64), ("gate", c_vp), ("ldgate", c_i64), ("residual", c_vp),
+                ("ldres", c_i64), ("res_dtype", c_i32), ("reserved", c_i32),
+                ("dropout", P(zero_dropout_t))]
+
+
+class zero_act_grad_t(ctypes.Structure):
+    _fields_ = [("act", c_i32), ("reserved", c_i32), ("pre", c_vp), ("ldpre", c_i64),
+                ("gate", c_vp), ("ldgate", c_i64), ("dgate", c_vp), ("lddgate", c_i64)]
 
 
 def adam_hp(step: int, grad_scale: float, lr: float = 1e-3, beta1: float = 0.9,
@@ -153,6 +173,21 @@ _SIGS = {
     "zero_bounds_report": (c_i32, [P(zero_bounds_t), c_i32]),
     "zero_async_status": (c_i32, [P(c_i64), c_i32]),
     "zero_bounds_probe": (c_i32, [c_vp]),
+    "zero_linear": (c_i32, [c_vp, c_i64, c_vp, c_i64, c_i32, c_i64, c_i64, c_i64,
+                            P(zero_linear_epilogue_t), c_vp, c_i64, c_i32, c_vp]),
+    "zero_linear_dinput": (c_i32, [c_vp, c_i64, c_vp, c_i64, c_i32, c_i64, c_i64, c_i64,
+                                   P(zero_act_grad_t), c_vp, c_i64, c_i32, c_vp]),
+    "zero_linear_dweight": (c_i32, [c_vp, c_i64, c_vp, c_i64, c_i64, c_i64, c_i64, c_i32, c_vp,
+                                    c_i64, c_i32, c_vp, c_i32, c_i32, c_vp]),
+    "zero_dropout": (c_i32, [c_vp, c_i64, c_i32, c_vp, c_i64, c_i32, c_i64, c_i64,
+                             P(zero_dropout_t), c_vp, c_i64, c_i32, c_vp]),
+    "zero_layer_norm": (c_i32, [c_vp, c_i64, c_i32, c_vp, c_vp, c_i32, c_i64, c_i64, c_i32,
+                                ctypes.c_float, c_vp, c_i64, c_i32, c_vp, c_vp, c_vp]),
+    "zero_layer_norm_workspace": (c_i32, [c_i64, c_i64, P(c_i64)]),
+    "zero_layer_norm_backward": (c_i32, [c_vp, c_i64, c_i32, c_vp, c_i64, c_i32, c_vp, c_i32,
+                                         c_vp, c_vp, c_i64, c_i64, c_i32, c_vp, c_i64, c_vp,
+                                         c_i64, c_i32, c_vp, c_vp, c_i32, c_i32, c_vp, c_i64,
+                                         c_vp]),
 }
 
 _LIB = None
@@ -742,3 +777,154 @@ def zero_async_status(reset: bool = False) -> int:
     n = c_i64()
     _check(_lib().zero_async_status(ctypes.byref(n), 1 if reset else 0), "zero_async_status")
     return n.value
+
+
+# ------------------------------------------------------- layer computation --
+_TORCH_NAMES = {ZERO_F32: "torch.float32", ZERO_BF16: "torch.bfloat16"}
+
+
+def _mat(x, rows: int, cols: int, ld: int, dtype: int, what: str):
+    """Address of a matrix argument.  A tensor must be of the dtype the call
+    names and its memory must hold rows of cols elements ld apart, counted
+    from its first element; raw integer addresses pass as they are."""
+    if x is None or isinstance(x, int):
+        return x
+    es = _ESIZE.get(dtype)
+    if es is not None:
+        if str(x.dtype) != _TORCH_NAMES[dtype]:
+            raise ValueError(f"{what}: a {x.dtype} tensor passed as {_TORCH_NAMES[dtype]}")
+        if rows > 0 and cols > 0:
+            have = x.untyped_storage().nbytes() - x.storage_offset() * es
+            need = ((rows - 1) * ld + cols) * es
+            if have < need:
+                raise ValueError(f"{what}: holds {have} bytes, the call touches {need}")
+    return _ptr(x)
+
+
+class _Side:
+    """An operand remembered until its sizes are known, with the struct that
+    will carry its address (and so kept alive with it)."""
+    __slots__ = ("struct", "mats", "keep")
+
+    def __init__(self, struct, mats, keep=None):
+        self.struct, self.mats, self.keep = struct, mats, keep
+
+    def checked(self, rows: int, cols: int):
+        for name, x, one_row, ld, dtype in self.mats:
+            setattr(self.struct, name, _mat(x, 1 if one_row else rows, cols, ld, dtype, name))
+        return self.struct
+
+
+def dropout_rng(p: float, seed: int, offset: int = 0, d_offset=None) -> zero_dropout_t:
+    """Dropout's rate and random numbers (zero_dropout_t); d_offset: a device
+    int64 added to offset, for masks that change between graph replays."""
+    if d_offset is not None:
+        _need(d_offset, 8, "d_offset")
+    r = zero_dropout_t(p, 0, seed, offset, _ptr(d_offset))
+    r.keep = d_offset
+    return r
+
+
+def linear_epilogue(bias=None, bias_dtype: int = ZERO_BF16, act: int = ZERO_ACT_NONE, pre=None,
+                    ldpre: int = 0, gate=None, ldgate: int = 0, residual=None, ldres: int = 0,
+                    res_dtype: int = ZERO_BF16, dropout: zero_dropout_t | None = None) -> _Side:
+    """What follows the product in zero_linear (zero_linear_epilogue_t); may be
+    kept and used for many calls."""
+    e = zero_linear_epilogue_t(None, bias_dtype, act, None, ldpre, None, ldgate, None, ldres,
+                               res_dtype, 0, ctypes.pointer(dropout) if dropout else None)
+    mats = []
+    if bias is not None:
+        mats.append(("bias", bias, True, 0, bias_dtype))
+    if pre is not None:
+        mats.append(("pre", pre, False, ldpre, ZERO_BF16))
+    if gate is not None:
+        mats.append(("gate", gate, False, ldgate, ZERO_BF16))
+    if residual is not None:
+        mats.append(("residual", residual, False, ldres, res_dtype))
+    return _Side(e, mats, dropout)
+
+
+def linear_act_grad(act: int, pre, ldpre: int, gate=None, ldgate: int = 0, dgate=None,
+                    lddgate: int = 0) -> _Side:
+    """What follows the product in zero_linear_dinput (zero_act_grad_t)."""
+    a = zero_act_grad_t(act, 0, None, ldpre, None, ldgate, None, lddgate)
+    mats = [("pre", pre, False, ldpre, ZERO_BF16)]
+    if gate is not None:
+        mats.append(("gate", gate, False, ldgate, ZERO_BF16))
+    if dgate is not None:
+        mats.append(("dgate", dgate, False, lddgate, ZERO_BF16))
+    return _Side(a, mats)
+
+
+def _weight(w, ldw: int, w_layout: int, n: int, k: int, dtype: int, what: str):
+    rows, cols = (k, n) if w_layout == ZERO_W_KN else (n, k)
+    return _mat(w, rows, cols, ldw, dtype, what)
+
+
+def zero_linear(x, ldx: int, w, ldw: int, w_layout: int, m: int, n: int, k: int, ep, y, ldy: int,
+                ydtype: int = ZERO_BF16, stream=None) -> None:
+    _check(_lib().zero_linear(
+        _mat(x, m, k, ldx, ZERO_BF16, "x"), ldx, _weight(w, ldw, w_layout, n, k, ZERO_BF16, "w"),
+        ldw, w_layout, m, n, k, None if ep is None else ctypes.byref(ep.checked(m, n)),
+        _mat(y, m, n, ldy, ydtype, "y"), ldy, ydtype, _stream(stream)), "zero_linear")
+
+
+def zero_linear_dinput(dy, lddy: int, w, ldw: int, w_layout: int, m: int, n: int, k: int, ag, dx,
+                       lddx: int, dxdtype: int = ZERO_BF16, stream=None) -> None:
+    _check(_lib().zero_linear_dinput(
+        _mat(dy, m, n, lddy, ZERO_BF16, "dy"), lddy,
+        _weight(w, ldw, w_layout, n, k, ZERO_BF16, "w"), ldw, w_layout, m, n, k,
+        None if ag is None else ctypes.byref(ag.checked(m, k)),
+        _mat(dx, m, k, lddx, dxdtype, "dx"), lddx, dxdtype, _stream(stream)),
+        "zero_linear_dinput")
+
+
+def zero_linear_dweight(dy, lddy: int, x, ldx: int, m: int, n: int, k: int, w_layout: int, dw,
+                        lddw: int, dwdtype: int = ZERO_BF16, dbias=None,
+                        dbdtype: int = ZERO_BF16, accumulate=False, stream=None) -> None:
+    _check(_lib().zero_linear_dweight(
+        _mat(dy, m, n, lddy, ZERO_BF16, "dy"), lddy, _mat(x, m, k, ldx, ZERO_BF16, "x"), ldx,
+        m, n, k, w_layout, _weight(dw, lddw, w_layout, n, k, dwdtype, "dw"), lddw, dwdtype,
+        _mat(dbias, 1, n, 0, dbdtype, "dbias"), dbdtype, int(accumulate), _stream(stream)),
+        "zero_linear_dweight")
+
+
+def zero_dropout(x, ldx: int, xdtype: int, residual, ldres: int, res_dtype: int, m: int, n: int,
+                 rng: zero_dropout_t, y, ldy: int, ydtype: int = ZERO_BF16, stream=None) -> None:
+    _check(_lib().zero_dropout(
+        _mat(x, m, n, ldx, xdtype, "x"), ldx, xdtype,
+        _mat(residual, m, n, ldres, res_dtype, "residual"), ldres, res_dtype, m, n,
+        ctypes.byref(rng), _mat(y, m, n, ldy, ydtype, "y"), ldy, ydtype, _stream(stream)),
+        "zero_dropout")
+
+
+def zero_layer_norm(x, ldx: int, xdtype: int, weight, bias, pdtype: int, m: int, n: int,
+                    kind: int, eps: float, y, ldy: int, ydtype: int = ZERO_BF16, mean=None,
+                    rstd=None, stream=None) -> None:
+    _check(_lib().zero_layer_norm(
+        _mat(x, m, n, ldx, xdtype, "x"), ldx, xdtype, _mat(weight, 1, n, 0, pdtype, "weight"),
+        _mat(bias, 1, n, 0, pdtype, "bias"), pdtype, m, n, kind, eps,
+        _mat(y, m, n, ldy, ydtype, "y"), ldy, ydtype, _mat(mean, 1, m, 0, ZERO_F32, "mean"),
+        _mat(rstd, 1, m, 0, ZERO_F32, "rstd"), _stream(stream)), "zero_layer_norm")
+
+
+def zero_layer_norm_workspace(m: int, n: int) -> int:
+    out = c_i64()
+    _check(_lib().zero_layer_norm_workspace(m, n, ctypes.byref(out)), "zero_layer_norm_workspace")
+    return out.value
+
+
+def zero_layer_norm_backward(dy, lddy: int, dydtype: int, x, ldx: int, xdtype: int, weight,
+                             pdtype: int, mean, rstd, m: int, n: int, kind: int, dres,
+                             lddres: int, dx, lddx: int, dxdtype: int, dweight, dbias,
+                             gdtype: int, accumulate, workspace, workspace_bytes: int,
+                             stream=None) -> None:
+    _need(workspace, workspace_bytes, "workspace")
+    _check(_lib().zero_layer_norm_backward(
+        _mat(dy, m, n, lddy, dydtype, "dy"), lddy, dydtype, _mat(x, m, n, ldx, xdtype, "x"), ldx,
+        xdtype, _mat(weight, 1, n, 0, pdtype, "weight"), pdtype,
+        _mat(mean, 1, m, 0, ZERO_F32, "mean"), _mat(rstd, 1, m, 0, ZERO_F32, "rstd"), m, n, kind,
+        _mat(dres, m, n, lddres, dxdtype, "dres"), lddres, _mat(dx, m, n, lddx, dxdtype, "dx"),
+        lddx, dxdtype, _mat(dweight, 1, n, 0, gdtype, "dweight"),
+        _mat(dbias, 1, n, 0, gdtype, "dbias"), gdtype, int(accumulate), _ptr(workspace),
+        workspace_bytes, _stream(stream)), "zero_layer_norm_backward")

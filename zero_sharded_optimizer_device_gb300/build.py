@@ -22,9 +22,13 @@ LIB = os.path.join(HERE, "libzero.so")
 LIB_CHECKED = os.path.join(HERE, "libzero_checked.so")
 
 SOURCES = ["zero_plan.cpp", "zero_api.cpp", "zero_sched.cpp", "zero_rs.cu", "zero_kernels.cu",
-           "zero_noalloc.cu"]
+           "zero_noalloc.cu", "zero_ops_api.cpp", "zero_linear.cu", "zero_dropout.cu",
+           "zero_lnorm.cu"]
+# The step's kernels follow the oracle operation by operation (no contraction
+# into FMA); the layer operators' sums are fp32 FMA chains.
+FMA = {"zero_linear.cu", "zero_dropout.cu", "zero_lnorm.cu"}
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-COMMON = ["-O3", "-std=c++17", "-lineinfo", "-fmad=false", "-I", INCLUDE, "-I", CSRC,
+COMMON = ["-O3", "-std=c++17", "-lineinfo", "-I", INCLUDE, "-I", CSRC,
           "-Xcompiler", "-fPIC,-ffp-contract=off,-O2"]
 
 
@@ -38,7 +42,8 @@ def nvcc() -> str:
 
 def _compile(src: str, extra: list[str], outdir: str = BUILD) -> str:
     obj = os.path.join(outdir, os.path.splitext(src)[0] + ".o")
-    cmd = [nvcc(), *COMMON, *ARCH, *extra, "-c", os.path.join(CSRC, src), "-o", obj]
+    fmad = "-fmad=true" if src in FMA else "-fmad=false"
+    cmd = [nvcc(), *COMMON, fmad, *ARCH, *extra, "-c", os.path.join(CSRC, src), "-o", obj]
     if src.endswith(".cpp"):
         cmd[cmd.index("-c"):cmd.index("-c")] = ["-x", "cu"]
     r = subprocess.run(cmd, capture_output=True, text=True)

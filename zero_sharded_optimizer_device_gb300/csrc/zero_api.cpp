@@ -7,7 +7,7 @@
 
 #include <nvtx3/nvToolsExt.h>
 
-#include "zero_internal.h"
+#include "zero_ops.h"
 
 namespace {
 
@@ -605,10 +605,13 @@ extern "C" int zero_bounds_report(zero_bounds_t* out, int32_t reset) {
   *out = zero_bounds_t{};
 #ifdef ZERO_CHECKED
   out->checked = 1;
-  zk::BoundsRec rec[2] = {};
+  zk::BoundsRec rec[5] = {};
   cudaError_t e = cudaDeviceSynchronize();
   if (e == cudaSuccess) e = zk::bounds_rs(&rec[0], reset != 0);
   if (e == cudaSuccess) e = zk::bounds_kernels(&rec[1], reset != 0);
+  if (e == cudaSuccess) e = zk::bounds_linear(&rec[2], reset != 0);
+  if (e == cudaSuccess) e = zk::bounds_dropout(&rec[3], reset != 0);
+  if (e == cudaSuccess) e = zk::bounds_lnorm(&rec[4], reset != 0);
   if (e != cudaSuccess) return cuda_status(e);
   for (const zk::BoundsRec& r : rec) {
     if (r.count && !out->count) {  // the first unit with a record gives the details
@@ -631,10 +634,11 @@ extern "C" int zero_bounds_probe(zero_stream_t stream) {
 
 extern "C" int zero_async_status(int64_t* timeouts, int32_t reset) {
   if (!timeouts) return ZERO_EINVAL;
-  unsigned long long n = 0;
+  unsigned long long n = 0, ops = 0;
   cudaError_t e = cudaDeviceSynchronize();
   if (e == cudaSuccess) e = zk::async_timeouts(&n, reset != 0);
+  if (e == cudaSuccess) e = zk::ops_timeouts(&ops, reset != 0);
   if (e != cudaSuccess) return cuda_status(e);
-  *timeouts = (int64_t)n;
+  *timeouts = (int64_t)(n + ops);
   return ZERO_OK;
 }
