@@ -1,116 +1,756 @@
 // Products of bf16 matrices with what follows them fused in: the forward
 // product, its input's and its weight's gradients (see zero_linear*,
 // include/zero.h).
+//
+// D[i][j] = sum over c of A(i, c) B(j, c) on the 5th-generation tensor cores.
+// A pair of CTAs (a cluster of two SMs) computes a tile of 256 x BN: each CTA
+// keeps 128 rows of A and BN / 2 rows of B in shared memory and 128 x BN fp32
+// sums in its tensor memory, so every operand byte is read from shared memory
+// by both halves of the tile but stored once.  Warp roles per CTA:
+//   warp 0        loads operand tiles 64 deep by TMA into a ring of stages
+//   warp 1        (first CTA of the pair) issues the tensor-core instructions
+//   warp 2        allocates and frees tensor memory
+//   warps 4-11    epilogue: tensor memory -> registers -> a transposing patch
+//                 of shared memory -> 8 consecutive columns per thread, with
+//                 which every side matrix is read and the output written
+//   warps 12-15   (GEN) load operands whose base or rows lie off 16-byte
+//                 boundaries, which TMA cannot, with plain loads
+// Tiles are walked persistently with two sets of sums, so one tile's epilogue
+// runs under the next one's products.  Where there are too few tiles to fill
+// the GPU the contraction is split over the S pairs of a larger cluster, whose
+// sums meet in shared memory in a fixed order (no atomics, no workspace).
+#include <cuda.h>
+
+#include <atomic>
+
 #include "zero_ops_device.cuh"
 
 namespace zk {
 
-// ---------------------------------------------------------------------------
-// Plain tiles: 64 x 64 outputs per block, 4 x 4 fp32 sums per thread, operands
-// staged 16 deep through shared memory.
-// ---------------------------------------------------------------------------
-constexpr int kTile = 64, kDepth = 16;
+constexpr int kRowsCta = 128;          // rows of A per CTA (tensor-memory lanes)
+constexpr int kDeep = 64;              // contraction per stage: 128 bytes, one swizzle row
+constexpr int kBytesA = kRowsCta * kDeep * 2;
+constexpr int kEpiWarp0 = 4, kEpiWarps = 8, kGenWarp0 = 12, kGenWarps = 4;
+constexpr int kPatch = 32 * 36;        // floats of a 32 x 32 patch, rows 36 apart
+constexpr int kMaxStages = 9;
+constexpr int kOnesBytes = 2048;
+constexpr int kSmemMost = 232448;      // shared memory one CTA may have
+constexpr unsigned long long kWaitNs = 2000000000ull;
 
-__device__ __forceinline__ float operand(const Mat& a, bool contig, int64_t i, int64_t c,
-                                         int64_t rows, int64_t depth) {
-  if (i >= rows || c >= depth) return 0.0f;
-  const int64_t at = contig ? i * a.ld + c : c * a.ld + i;
-  const int64_t last = contig ? (rows - 1) * a.ld + depth : (depth - 1) * a.ld + rows;
-  if (!in_extent(at, at + 1, 0, last, ZERO_SITE_LINEAR_IN)) return 0.0f;
-  return __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.p)[at] << 16);
+static __device__ unsigned long long g_ops_timeouts;
+
+// How a launch walks its product (host-made).
+struct TileK {
+  int tiles_i, tiles_j, bias_tiles;  // bias_tiles: tiles_i more, summing A alone
+  int kblocks, splits, bn, stages;
+  int i_fast;                        // consecutive tiles differ in i (else in j)
+  int gen_a, gen_b;                  // elements per plain load; 0: by TMA
+  uint32_t tmem_cols;
+};
+
+// ------------------------------------------------------------ PTX wrappers --
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+  return (uint32_t)__cvta_generic_to_shared(p);
+}
+__device__ __forceinline__ uint64_t now_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t remote(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; "
+      "selp.u32 %0, 1, 0, p; }"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done;
+}
+// Wait for the phase of this parity.  Gives up after kWaitNs, or once another
+// role of the CTA has (*dead), counts the first giving up and returns false:
+// the role then leaves its loop, and the kernel returns.
+__device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, volatile int* dead) {
+  const uint64_t t0 = now_ns();
+  while (!bar_try(bar, parity)) {
+    if (*dead) return false;
+    if (now_ns() - t0 > kWaitNs) {
+      *dead = 1;
+      atomicAdd(&g_ops_timeouts, 1ull);
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
+  if (bar_try(bar, parity)) return true;
+  return bar_wait_slow(bar, parity, dead);
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+               : "memory");
+}
+// One arrival on a barrier of any CTA of the cluster.
+__device__ __forceinline__ void bar_arrive_cluster(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
+               : "memory");
+}
+// A box of a matrix into this CTA's shared memory, counted on the barrier of
+// the pair's first CTA.  x is a multiple of 64 elements.
+__device__ __forceinline__ void tma_load(const CUtensorMap* map, uint32_t dst, int x, int y,
+                                         uint32_t cluster_bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile"
+      ".mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(cluster_bar)
+      : "memory");
+}
+// Tensor-core arrivals: when every instruction issued so far is done, one
+// arrival on this barrier of both CTAs of the pair.
+__device__ __forceinline__ void commit_pair(uint32_t bar, uint16_t mask) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], %1;" ::"r"(bar),
+      "h"(mask)
+      : "memory");
+}
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                         uint32_t add) {
+  asm volatile(
+      "{ .reg .pred p; setp.ne.u32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(add)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t r[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void st_shared4(uint32_t addr, float a, float b, float c, float d) {
+  asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "f"(a), "f"(b), "f"(c),
+               "f"(d)
+               : "memory");
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
 }
 
-template <int MODE>
-__global__ void __launch_bounds__(256) product_plain_kernel(ProductK k) {
-  __shared__ float a[kDepth][kTile + 4], b[kDepth][kTile + 4];
-  __shared__ float d[kTile][kTile + 4];
-  const int t = threadIdx.x, ti = (t / 16) * 4, tj = (t % 16) * 4;
-  const int64_t i0 = (int64_t)blockIdx.y * kTile, j0 = (int64_t)blockIdx.x * kTile;
-  float s[4][4] = {};
-  for (int64_t c0 = 0; c0 < k.depth; c0 += kDepth) {
-    for (int q = t; q < kTile * kDepth; q += 256) {
-      const int ai = k.a_c ? q / kDepth : q % kTile, ac = k.a_c ? q % kDepth : q / kTile;
-      a[ac][ai] = operand(k.a, k.a_c, i0 + ai, c0 + ac, k.rows, k.depth);
-      const int bi = k.b_c ? q / kDepth : q % kTile, bc = k.b_c ? q % kDepth : q / kTile;
-      b[bc][bi] = operand(k.b, k.b_c, j0 + bi, c0 + bc, k.cols, k.depth);
-    }
-    __syncthreads();
+// Shared-memory descriptor of an operand tile in 128-byte swizzle rows.
+// Contiguous contraction: rows of 64 values, 8-row groups 1024 bytes apart.
+// Contiguous rows: blocks of 64 rows x 64 deep (8192 bytes apart: the leading
+// offset), 8-deep groups 1024 bytes apart.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, bool contig) {
+  const uint64_t lead = contig ? 1 : (8192 >> 4), stride = 1024 >> 4;
+  return (uint64_t)((addr & 0x3FFFF) >> 4) | (lead << 16) | (stride << 32) | (1ull << 46) |
+         (2ull << 61);
+}
+
+// 8 elements from index `at` on, `valid` of them inside, W per load.
+template <int W>
+__device__ __forceinline__ uint4 gen_load(const uint16_t* p, int valid) {
+  uint32_t w[4] = {0, 0, 0, 0};
+  if constexpr (W == 4) {
 #pragma unroll
-    for (int c = 0; c < kDepth; ++c)
+    for (int j = 0; j < 2; ++j)
+      if (valid >= 4 * j + 4) {
+        const uint2 u = *reinterpret_cast<const uint2*>(p + 4 * j);
+        w[2 * j] = u.x;
+        w[2 * j + 1] = u.y;
+      } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+        for (int e = 4 * j; e < 4 * j + 4; ++e)
+          if (e < valid) w[e / 2] |= (uint32_t)p[e] << (16 * (e & 1));
+      }
+  } else if constexpr (W == 2) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[i][j] += a[c][ti + i] * b[c][tj + j];
-    __syncthreads();
+    for (int j = 0; j < 4; ++j)
+      if (valid >= 2 * j + 2)
+        w[j] = *reinterpret_cast<const uint32_t*>(p + 2 * j);
+      else if (valid > 2 * j)
+        w[j] = p[2 * j];
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < valid) w[e / 2] |= (uint32_t)p[e] << (16 * (e & 1));
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (k.out_t)
-        d[tj + j][ti + i] = s[i][j];
-      else
-        d[ti + i][tj + j] = s[i][j];
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Rows [i0, i0 + count) x contraction [c0, c0 + 64) of an operand into its
+// swizzled tile, by the GEN warps' 128 threads (t).
+template <int W>
+__device__ __forceinline__ void gen_tile(const Mat& a, bool contig, int64_t rows, int64_t depth,
+                                         int64_t i0, int count, int64_t c0, uint32_t dst, int t) {
+  const uint16_t* base = static_cast<const uint16_t*>(a.p);
+#pragma unroll 4
+  for (int q = t; q < count * 8; q += kGenWarps * 32) {
+    // 8 units of 8 elements run along the contiguous index
+    const int unit = q & 7, line = q >> 3;
+    int64_t at;
+    int valid;
+    uint32_t to;
+    if (contig) {
+      const int64_t i = i0 + line, c = c0 + unit * 8;
+      valid = i < rows && c < depth ? (int)(depth - c < 8 ? depth - c : 8) : 0;
+      at = i * a.ld + c;
+      to = line * 128 + ((unit ^ (line & 7)) << 4);
+    } else {
+      const int block = line >> 6, deep = line & 63;  // 64 lines of depth per 64 rows
+      const int64_t c = c0 + deep, i = i0 + block * 64 + unit * 8;
+      valid = c < depth && i < rows ? (int)(rows - i < 8 ? rows - i : 8) : 0;
+      at = c * a.ld + i;
+      to = block * 8192 + deep * 128 + ((unit ^ (deep & 7)) << 4);
     }
-  __syncthreads();
-  const int64_t r0 = k.out_t ? j0 : i0, c0 = k.out_t ? i0 : j0;
-  const Extent e{k.out_t ? k.cols : k.rows, k.out_t ? k.rows : k.cols};
-  const uint64_t offset = MODE == LIN_FORWARD && k.epi.drop.on ? drop_offset(k.epi.drop) : 0;
-  for (int q = t; q < kTile * kTile / 8; q += 256) {
-    const int r = q / 8, c = (q % 8) * 8;
-    if (r0 + r >= e.rows || c0 + c >= e.cols) continue;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    const int64_t last = contig ? (rows - 1) * a.ld + depth : (depth - 1) * a.ld + rows;
+    if (valid > 0 && in_extent(at, at + valid, 0, last, ZERO_SITE_LINEAR_IN))
+      v = gen_load<W>(base + at, valid);
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + to), "r"(v.x), "r"(v.y),
+                 "r"(v.z), "r"(v.w)
+                 : "memory");
+  }
+}
+__device__ __forceinline__ void gen_operand(int width, const Mat& a, bool contig, int64_t rows,
+                                            int64_t depth, int64_t i0, int count, int64_t c0,
+                                            uint32_t dst, int t) {
+  if (width == 4)
+    gen_tile<4>(a, contig, rows, depth, i0, count, c0, dst, t);
+  else if (width == 2)
+    gen_tile<2>(a, contig, rows, depth, i0, count, c0, dst, t);
+  else
+    gen_tile<1>(a, contig, rows, depth, i0, count, c0, dst, t);
+}
+
+// The tile of index t: its row and column, or the bias column (j < 0).
+__device__ __forceinline__ void tile_at(const TileK& g, int t, int& i, int& j) {
+  const int main = g.tiles_i * g.tiles_j;
+  if (t >= main) {
+    i = t - main;
+    j = -1;
+  } else if (g.i_fast) {
+    i = t % g.tiles_i;
+    j = t / g.tiles_i;
+  } else {
+    j = t % g.tiles_j;
+    i = t / g.tiles_j;
+  }
+}
+
+// One 32 x 32 block of sums, spread over a patch of `pairs` CTAs' shared
+// memory (at the same address in each; this CTA's alone where pairs = 1),
+// through the epilogue.  The patch holds the output's orientation: row r of it
+// is output row row0 + r.
+template <int MODE>
+__device__ __forceinline__ void finish_patch(const ProductK& k, uint64_t offset, uint32_t patch,
+                                             int pairs, uint32_t half, int64_t row0, int64_t col0,
+                                             const Extent& e, int lane) {
+#pragma unroll
+  for (int it = 0; it < 4; ++it) {
+    const int r = it * 8 + (lane >> 2), c = (lane & 3) * 8;
+    const int64_t row = row0 + r, col = col0 + c;
+    const uint32_t at = patch + (uint32_t)(r * 36 + c) * 4;
     float v[8];
+    if (pairs == 1) {
+      const float4 x = ld_cluster4(at), y = ld_cluster4(at + 16);
+      v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+      v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+    } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = d[r][c + j];
-    epilogue8<MODE>(k.epi, offset, r0 + r, c0 + c,
-                    e.cols - c0 - c < 8 ? (int)(e.cols - c0 - c) : 8, v, e);
+      for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+      for (int p = 0; p < pairs; ++p) {
+        const uint32_t from = remote(at, 2 * p + half);
+        const float4 x = ld_cluster4(from), y = ld_cluster4(from + 16);
+        v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+        v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+      }
+    }
+    if (row < e.rows && col < e.cols)
+      epilogue8<MODE>(k.epi, offset, row, col, e.cols - col < 8 ? (int)(e.cols - col) : 8, v, e);
   }
 }
 
-// Sums over the contraction of A (k.a_c == 0): 32 of its rows per block.
-__global__ void __launch_bounds__(256) column_sum_kernel(ProductK k) {
-  __shared__ float sum[8][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t i = (int64_t)blockIdx.x * 32 + lane;
-  float s = 0.0f;
-  for (int64_t c = warp; c < k.depth; c += 8) s += operand(k.a, false, i, c, k.rows, k.depth);
-  sum[warp][lane] = s;
-  __syncthreads();
-  if (warp == 0 && i < k.rows && in_extent(i, i + 1, 0, k.rows, ZERO_SITE_LINEAR_OUT)) {
-    s = 0.0f;
-    for (int w = 0; w < 8; ++w) s += sum[w][lane];
-    if (k.epi.accumulate) s += load1(k.dbias, i);
-    store1(k.dbias, i, s);
+template <int MODE, bool GEN>
+__global__ void __launch_bounds__((GEN ? 16 : 12) * 32, 1)
+    product_kernel(const __grid_constant__ CUtensorMap map_a,
+                   const __grid_constant__ CUtensorMap map_b, const __grid_constant__ ProductK k,
+                   const __grid_constant__ TileK g) {
+  extern __shared__ __align__(1024) unsigned char smem[];
+  __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 4];
+  __shared__ uint32_t tmem_at;
+  __shared__ int dead;
+  const uint32_t rank = cluster_rank(), half = rank & 1, leader = rank & ~1u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int split = (int)(rank >> 1), S = g.splits;
+  const uint32_t stage_bytes = kBytesA + g.bn * kDeep;  // bn / 2 rows of 128 bytes
+  const uint32_t ring = smem_u32(smem);
+  const uint32_t patches = ring + g.stages * stage_bytes;
+  const uint32_t ones = patches + (S == 1 ? kEpiWarps * kPatch * 4 : 0);
+  const uint32_t full = smem_u32(bars), empty = full + 8 * kMaxStages;
+  const uint32_t tfull = empty + 8 * kMaxStages, tempty = tfull + 16;
+
+  if (warp == 0 && lane == 0) {
+    dead = 0;
+    for (int s = 0; s < g.stages; ++s) {
+      bar_init(full + 8 * s, 1 + (GEN ? 2 * kGenWarps : 0));
+      bar_init(empty + 8 * s, 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      bar_init(tfull + 8 * a, 1);
+      bar_init(tempty + 8 * a, 2 * kEpiWarps);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (warp == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&tmem_at)),
+                 "r"(g.tmem_cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  }
+  if (MODE == LIN_DWEIGHT && g.bias_tiles && warp == 3) {
+    for (int q = lane; q < kOnesBytes / 16; q += 32)  // bf16 1.0 twice
+      asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(ones + q * 16),
+                   "r"(0x3F803F80u)
+                   : "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  cluster_sync();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = *(volatile uint32_t*)&tmem_at;
+
+  // this cluster's tiles, and this pair's share of the contraction
+  const int clusters = gridDim.x / (2 * S), first = blockIdx.x / (2 * S);
+  const int tiles = g.tiles_i * g.tiles_j + g.bias_tiles;
+  const int kb0 = (int)((int64_t)g.kblocks * split / S);
+  const int kb1 = (int)((int64_t)g.kblocks * (split + 1) / S);
+  const bool a_c = k.a_c, b_c = k.b_c;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint32_t full_lead = remote(full, leader);
+      uint32_t s = 0, ph = 0;
+      bool ok = true;
+      for (int t = first; t < tiles && ok; t += clusters) {
+        int ti, tj;
+        tile_at(g, t, ti, tj);
+        const int i0 = ti * 256 + (int)half * kRowsCta;
+        const int j0 = tj * g.bn + (int)half * (g.bn / 2);
+        const bool load_a = g.gen_a == 0, load_b = g.gen_b == 0 && tj >= 0;
+        const uint32_t bytes =
+            2 * ((load_a ? kBytesA : 0) + (load_b ? (uint32_t)g.bn * kDeep : 0));
+        for (int kb = kb0; kb < kb1; ++kb) {
+          ok = bar_wait(empty + 8 * s, ph ^ 1, &dead);
+          if (!ok) break;
+          if (half == 0) bar_expect(full + 8 * s, bytes);
+          const uint32_t a_at = ring + s * stage_bytes, b_at = a_at + kBytesA;
+          if (load_a) {
+            if (a_c) {
+              tma_load(&map_a, a_at, kb * kDeep, i0, full_lead + 8 * s);
+            } else {
+              tma_load(&map_a, a_at, i0, kb * kDeep, full_lead + 8 * s);
+              tma_load(&map_a, a_at + 8192, i0 + 64, kb * kDeep, full_lead + 8 * s);
+            }
+          }
+          if (load_b) {
+            if (b_c)
+              tma_load(&map_b, b_at, kb * kDeep, j0, full_lead + 8 * s);
+            else
+              for (int q = 0; q < g.bn / 128; ++q)
+                tma_load(&map_b, b_at + q * 8192, j0 + q * 64, kb * kDeep, full_lead + 8 * s);
+          }
+          if (++s == (uint32_t)g.stages) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      // a wait gave up: let the loads in flight land before the CTAs return
+      // (a ring slot holds at most one load; waits are again limited)
+      if (!ok && half == 0)
+        for (int q = 0; q < g.stages; ++q) {
+          const uint64_t t0 = now_ns();
+          while (!bar_try(full + 8 * q, ph) && now_ns() - t0 < kWaitNs / 8) {
+          }
+        }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0 && half == 0) {
+      const uint16_t mask = (uint16_t)(3u << leader);
+      // fp32 sums of bf16 values, M = 256; N = bn, or 32 columns of ones
+      const uint32_t base = (1u << 4) | (1u << 7) | (1u << 10) | ((a_c ? 0u : 1u) << 15) |
+                            (16u << 24);
+      const uint32_t idesc_n = base | ((b_c ? 0u : 1u) << 16) | ((uint32_t)(g.bn >> 3) << 17);
+      const uint32_t idesc_1 = base | (4u << 17);
+      const uint32_t step_a = a_c ? 2 : 128, step_b = b_c ? 2 : 128;  // 16 deep, in 16 bytes
+      uint32_t s = 0, ph = 0, acc = 0, aph = 0;
+      bool ok = true;
+      for (int t = first; t < tiles && ok; t += clusters) {
+        int ti, tj;
+        tile_at(g, t, ti, tj);
+        ok = bar_wait(tempty + 8 * acc, aph ^ 1, &dead);
+        if (!ok) break;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint32_t d = tmem + acc * g.bn;
+        for (int kb = kb0; kb < kb1; ++kb) {
+          ok = bar_wait(full + 8 * s, ph, &dead);
+          if (!ok) break;
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          const uint32_t a_at = ring + s * stage_bytes;
+          const uint64_t da = operand_desc(a_at, a_c);
+          const uint64_t db = tj >= 0 ? operand_desc(a_at + kBytesA, b_c)
+                                      : operand_desc(ones, true);
+          const uint32_t idesc = tj >= 0 ? idesc_n : idesc_1, sb = tj >= 0 ? step_b : 0;
+#pragma unroll
+          for (int q = 0; q < kDeep / 16; ++q)
+            mma_pair(d, da + q * step_a, db + q * sb, idesc, kb > kb0 || q > 0);
+          commit_pair(empty + 8 * s, mask);
+          if (++s == (uint32_t)g.stages) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+        if (ok) commit_pair(tfull + 8 * acc, mask);
+        if ((acc ^= 1) == 0) aph ^= 1;
+      }
+    }
+    __syncwarp();
+  } else if (warp >= kEpiWarp0 && warp < kEpiWarp0 + kEpiWarps) {
+    const int w = (warp - kEpiWarp0) & 3, set = (warp - kEpiWarp0) >> 2;  // lanes 32 w...
+    const uint32_t tempty_lead = remote(tempty, leader);
+    const Extent e{k.out_t ? k.cols : k.rows, k.out_t ? k.rows : k.cols};
+    const uint64_t offset =
+        MODE == LIN_FORWARD && k.epi.drop.on ? drop_offset(k.epi.drop) : 0ull;
+    const uint32_t mine = patches + (uint32_t)(warp - kEpiWarp0) * kPatch * 4;
+    uint32_t acc = 0, aph = 0;
+    bool ok = true;
+    for (int t = first; t < tiles && ok; t += clusters) {
+      int ti, tj;
+      tile_at(g, t, ti, tj);
+      ok = bar_wait(tfull + 8 * acc, aph, &dead);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const int64_t i0 = (int64_t)ti * 256 + half * kRowsCta + w * 32;
+      const int chunks = tj >= 0 ? g.bn / 32 : 1;
+      const uint32_t d = tmem + acc * g.bn + ((uint32_t)(w * 32) << 16);
+      for (int cc = set; cc < chunks; cc += 2) {
+        const int64_t j0 = (int64_t)tj * g.bn + cc * 32;
+        if (S == 1 && tj >= 0 && (i0 >= k.rows || j0 >= k.cols)) continue;
+        uint32_t r[32];
+        tmem_load32(d + cc * 32, r);
+        if (kb1 == kb0) {
+#pragma unroll
+          for (int q = 0; q < 32; ++q) r[q] = 0;  // an empty contraction
+        }
+        const uint32_t patch = S == 1 ? mine : ring + (uint32_t)(cc * 4 + w) * kPatch * 4;
+        if (S == 1 && MODE == LIN_DWEIGHT && tj < 0) {
+          const int64_t i = i0 + lane;
+          if (i < k.rows && in_extent(i, i + 1, 0, k.rows, ZERO_SITE_LINEAR_OUT)) {
+            float v = __uint_as_float(r[0]);
+            if (k.epi.accumulate) v += load1(k.dbias, i);
+            store1(k.dbias, i, v);
+          }
+          continue;
+        }
+        if (k.out_t) {
+#pragma unroll
+          for (int q = 0; q < 32; ++q)
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(patch + (q * 36 + lane) * 4), "r"(r[q])
+                         : "memory");
+        } else {
+#pragma unroll
+          for (int q = 0; q < 32; q += 4)
+            st_shared4(patch + (lane * 36 + q) * 4, __uint_as_float(r[q]),
+                       __uint_as_float(r[q + 1]), __uint_as_float(r[q + 2]),
+                       __uint_as_float(r[q + 3]));
+        }
+        if (S == 1) {
+          __syncwarp();
+          finish_patch<MODE>(k, offset, patch, 1, half, k.out_t ? j0 : i0, k.out_t ? i0 : j0, e,
+                             lane);
+          __syncwarp();
+        }
+      }
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) bar_arrive_cluster(tempty_lead + 8 * acc);
+      if ((acc ^= 1) == 0) aph ^= 1;
+    }
+  } else if (GEN && warp >= kGenWarp0) {
+    const int t128 = threadIdx.x - kGenWarp0 * 32;
+    const uint32_t full_lead = remote(full, leader);
+    uint32_t s = 0, ph = 0;
+    bool ok = true;
+    for (int t = first; t < tiles && ok; t += clusters) {
+      int ti, tj;
+      tile_at(g, t, ti, tj);
+      const int64_t i0 = (int64_t)ti * 256 + half * kRowsCta;
+      const int64_t j0 = (int64_t)tj * g.bn + half * (g.bn / 2);
+      for (int kb = kb0; kb < kb1; ++kb) {
+        ok = bar_wait(empty + 8 * s, ph ^ 1, &dead);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t a_at = ring + s * stage_bytes, b_at = a_at + kBytesA;
+        const int64_t c0 = (int64_t)kb * kDeep;
+        if (g.gen_a)
+          gen_operand(g.gen_a, k.a, a_c, k.rows, k.depth, i0, kRowsCta, c0, a_at, t128);
+        if (g.gen_b && tj >= 0)
+          gen_operand(g.gen_b, k.b, b_c, k.cols, k.depth, j0, g.bn / 2, c0, b_at, t128);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) bar_arrive_cluster(full_lead + 8 * s);
+        if (++s == (uint32_t)g.stages) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
+    }
+  }
+  __syncwarp();
+
+  if (S > 1) {
+    // every pair's sums now lie in its own shared memory: pair p finishes the
+    // blocks p, p + S, ... of its half, adding the pairs' parts in order
+    cluster_sync();
+    if (warp >= kEpiWarp0 && warp < kEpiWarp0 + kEpiWarps && !dead) {
+      const Extent e{k.out_t ? k.cols : k.rows, k.out_t ? k.rows : k.cols};
+      const uint64_t offset =
+          MODE == LIN_FORWARD && k.epi.drop.on ? drop_offset(k.epi.drop) : 0ull;
+      int ti, tj;
+      tile_at(g, first, ti, tj);
+      const int blocks = 4 * (tj >= 0 ? g.bn / 32 : 1);
+      for (int b = split + S * (warp - kEpiWarp0); b < blocks; b += S * kEpiWarps) {
+        const int64_t i0 = (int64_t)ti * 256 + half * kRowsCta + (b & 3) * 32;
+        const int64_t j0 = (int64_t)tj * g.bn + (b >> 2) * 32;
+        const uint32_t patch = ring + (uint32_t)b * kPatch * 4;
+        if (MODE == LIN_DWEIGHT && tj < 0) {
+          const int64_t i = i0 + lane;
+          if (i < k.rows && in_extent(i, i + 1, 0, k.rows, ZERO_SITE_LINEAR_OUT)) {
+            const uint32_t at = patch + (k.out_t ? lane : lane * 36) * 4;
+            float v = 0.0f;
+            for (int p = 0; p < S; ++p) {
+              float x;
+              asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                           : "=f"(x)
+                           : "r"(remote(at, 2 * p + half))
+                           : "memory");
+              v += x;
+            }
+            if (k.epi.accumulate) v += load1(k.dbias, i);
+            store1(k.dbias, i, v);
+          }
+        } else if (i0 < k.rows && j0 < k.cols) {
+          finish_patch<MODE>(k, offset, patch, S, half, k.out_t ? j0 : i0, k.out_t ? i0 : j0, e,
+                             lane);
+        }
+      }
+    }
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  cluster_sync();  // nobody reads this CTA's shared memory or signals it any more
+  if (warp == 2) {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(g.tmem_cols));
+  }
+}
+
+// ------------------------------------------------------------------- host --
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+static EncodeFn encode_fn() {
+  static std::atomic<void*> fn{nullptr};
+  void* f = fn.load();
+  if (!f) {
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    fn.store(f);
+  }
+  return reinterpret_cast<EncodeFn>(f);
+}
+
+// Elements per plain load of an operand, or 0 where TMA can read it: its base
+// and its rows (where there are several) on 16-byte boundaries.
+static int gen_width(const Mat& a, int64_t lines) {
+  const uintptr_t b = (uintptr_t)a.p;
+  const int64_t ld = lines > 1 ? a.ld : 8;
+  if ((b & 15) == 0 && ld % 8 == 0) return 0;
+  if ((b & 7) == 0 && ld % 4 == 0) return 4;
+  if ((b & 3) == 0 && ld % 2 == 0) return 2;
+  return 1;
+}
+
+static bool make_map(CUtensorMap* map, const Mat& a, bool contig, int64_t rows, int64_t depth,
+                     int box_rows) {
+  EncodeFn fn = encode_fn();
+  if (!fn) return false;
+  const int64_t inner = contig ? depth : rows, outer = contig ? rows : depth;
+  const cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
+  const cuuint64_t strides[1] = {
+      (cuuint64_t)(outer > 1 ? a.ld * 2 : (inner * 2 + 15) / 16 * 16)};
+  const cuuint32_t box[2] = {64, (cuuint32_t)(contig ? box_rows : kDeep)};
+  const cuuint32_t one[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.p, dims, strides, box, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+static int stages_for(int bn, int splits) {
+  const int stage = kBytesA + bn * kDeep;
+  const int rest = 1024 + kOnesBytes + 1024 + (splits == 1 ? kEpiWarps * kPatch * 4 : 0);
+  const int n = (kSmemMost - rest) / stage;
+  return n < kMaxStages ? n : kMaxStages;
+}
+
+template <int MODE, bool GEN>
+static cudaError_t launch_tiles(const CUtensorMap& ma, const CUtensorMap& mb, const ProductK& k,
+                                const TileK& g, cudaStream_t st) {
+  static std::atomic<unsigned long long> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  constexpr int most = kSmemMost - 1024;  // the rest is the kernel's static shared memory
+  if (!(done.load() & bit)) {
+    e = cudaFuncSetAttribute(product_kernel<MODE, GEN>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (e != cudaSuccess) return e;
+    done.fetch_or(bit);
+  }
+  const int64_t tiles = (int64_t)g.tiles_i * g.tiles_j + g.bias_tiles;
+  const int64_t pairs = sm_count() / 2;
+  const int64_t clusters = g.splits > 1 || tiles < pairs ? tiles : pairs;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(clusters * 2 * g.splits));
+  cfg.blockDim = dim3((GEN ? 16 : 12) * 32);
+  cfg.dynamicSmemBytes = (size_t)g.stages * (kBytesA + g.bn * kDeep) + kOnesBytes +
+                         (g.splits == 1 ? kEpiWarps * kPatch * 4 : 0);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2 * g.splits;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, product_kernel<MODE, GEN>, ma, mb, k, g);
 }
 
 template <int MODE>
-static cudaError_t launch_plain(const ProductK& k, cudaStream_t st) {
-  // rows run along grid.y (65535 blocks at most): longer products in slices
-  constexpr int64_t most = 65535 * (int64_t)kTile;
-  if (k.rows > most) return cudaErrorInvalidValue;
-  const dim3 grid((unsigned)((k.cols + kTile - 1) / kTile),
-                  (unsigned)((k.rows + kTile - 1) / kTile));
-  product_plain_kernel<MODE><<<grid, 256, 0, st>>>(k);
-  return cudaGetLastError();
+static cudaError_t launch_mode(const ProductK& in, cudaStream_t st) {
+  ProductK k = in;
+  // Few rows (tokens): the weight's side fills the 256 rows of a tile and the
+  // tokens are its columns; the output is written transposed.
+  if (MODE != LIN_DWEIGHT && k.rows <= 128) {
+    const Mat a = k.a;
+    k.a = in.b;
+    k.b = a;
+    k.a_c = in.b_c;
+    k.b_c = in.a_c;
+    k.rows = in.cols;
+    k.cols = in.rows;
+    k.out_t = !in.out_t;
+  }
+  TileK g{};
+  const int64_t kblocks = (k.depth + kDeep - 1) / kDeep;
+  const int64_t tiles_i = (k.rows + 255) / 256;
+  const int64_t pairs = sm_count() / 2;
+  // Width and split by a cost model: waves of tiles times the cycles of one
+  // (512 per 64-deep step at BN = 256) plus what joining the parts takes.
+  double best = 0;
+  for (int bn = 32; bn <= 256; bn *= 2) {
+    if (!k.b_c && bn < 128) continue;          // blocks of 64 rows per CTA
+    if (bn < 128 && k.cols > bn) continue;     // narrow tiles only where one is enough
+    const int64_t tiles_j = (k.cols + bn - 1) / bn;
+    for (int S = 1; S <= 4; S *= 2) {
+      if (S > 1 && (kblocks < 2 * S)) break;
+      const int64_t tiles = tiles_i * tiles_j;
+      const double waves = (double)((tiles * S + pairs - 1) / pairs);
+      const double step = bn == 256 ? 512 : bn == 128 ? 300 : 200;
+      const double cost = waves * ((double)kblocks / S * step + (S > 1 ? 3000 + 10 * bn : 0)) +
+                          8 * bn + 1000;
+      if (best == 0 || cost < best) {
+        best = cost;
+        g.bn = bn;
+        g.splits = S;
+        g.tiles_j = (int)tiles_j;
+      }
+    }
+  }
+  if (tiles_i * (g.tiles_j + 1) >= (1ll << 28) || kblocks >= (1ll << 30)) return cudaErrorInvalidValue;
+  g.tiles_i = (int)tiles_i;
+  g.kblocks = (int)kblocks;
+  g.stages = stages_for(g.bn, g.splits);
+  g.bias_tiles = k.dbias.p ? g.tiles_i : 0;
+  g.i_fast = k.rows <= k.cols;
+  g.tmem_cols = 2 * g.bn;
+  CUtensorMap ma{}, mb{};
+  if (k.depth > 0) {
+    g.gen_a = gen_width(k.a, k.a_c ? k.rows : k.depth);
+    g.gen_b = k.cols > 0 ? gen_width(k.b, k.b_c ? k.cols : k.depth) : 0;
+    if (!g.gen_a && !make_map(&ma, k.a, k.a_c, k.rows, k.depth, kRowsCta))
+      return cudaErrorInvalidValue;
+    if (!g.gen_b && k.cols > 0 && !make_map(&mb, k.b, k.b_c, k.cols, k.depth, g.bn / 2))
+      return cudaErrorInvalidValue;
+  }
+  if (g.gen_a || g.gen_b) return launch_tiles<MODE, true>(ma, mb, k, g, st);
+  return launch_tiles<MODE, false>(ma, mb, k, g, st);
 }
 
 cudaError_t launch_product(const ProductK& k, int mode, cudaStream_t st) {
-  if (k.rows <= 0) return cudaSuccess;
-  if (k.dbias.p) {
-    column_sum_kernel<<<(unsigned)((k.rows + 31) / 32), 256, 0, st>>>(k);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-  }
-  if (k.cols <= 0) return cudaSuccess;
-  if (mode == LIN_FORWARD) return launch_plain<LIN_FORWARD>(k, st);
-  if (mode == LIN_DINPUT) return launch_plain<LIN_DINPUT>(k, st);
-  return launch_plain<LIN_DWEIGHT>(k, st);
+  if (k.rows <= 0 || (k.cols <= 0 && !k.dbias.p)) return cudaSuccess;
+  if (mode == LIN_FORWARD) return launch_mode<LIN_FORWARD>(k, st);
+  if (mode == LIN_DINPUT) return launch_mode<LIN_DINPUT>(k, st);
+  return launch_mode<LIN_DWEIGHT>(k, st);
 }
 
-cudaError_t ops_timeouts(unsigned long long* out, bool) {
-  *out = 0;  // no bounded wait in these kernels
-  return cudaSuccess;
+cudaError_t ops_timeouts(unsigned long long* out, bool reset) {
+  cudaError_t e = cudaMemcpyFromSymbol(out, g_ops_timeouts, sizeof(unsigned long long));
+  if (e == cudaSuccess && reset) {
+    const unsigned long long zero = 0;
+    e = cudaMemcpyToSymbol(g_ops_timeouts, &zero, sizeof(zero));
+  }
+  return e;
 }
 
 cudaError_t bounds_linear(BoundsRec* out, bool reset) { return bounds_record(out, reset); }
