@@ -267,22 +267,124 @@ __device__ __forceinline__ void tile_at(const TileK& g, int t, int& i, int& j) {
   }
 }
 
-// One 32 x 32 block of sums, spread over a patch of `pairs` CTAs' shared
-// memory (at the same address in each; this CTA's alone where pairs = 1),
-// through the epilogue.  The patch holds the output's orientation: row r of it
-// is output row row0 + r.
+// A warp finishes a 32 x 32 block of the output (rows row0.., columns col0..)
+// as four steps of 8 rows, a lane taking 8 consecutive columns of one row in
+// each: 16-byte accesses of bf16, 64 consecutive bytes per row.
+struct Block {
+  int64_t row, col;  // this lane's in step 0; step it adds 8 it rows
+  int valid;         // its columns inside the output
+};
+__device__ __forceinline__ Block block_of(int64_t row0, int64_t col0, const Extent& e, int lane) {
+  Block b;
+  b.row = row0 + (lane >> 2);
+  b.col = col0 + (lane & 3) * 8;
+  b.valid = b.col >= e.cols ? 0 : (e.cols - b.col < 8 ? (int)(e.cols - b.col) : 8);
+  return b;
+}
+
+// The side operands of a block, read before the sums are at hand.
 template <int MODE>
-__device__ __forceinline__ void finish_patch(const ProductK& k, uint64_t offset, uint32_t patch,
-                                             int pairs, uint32_t half, int64_t row0, int64_t col0,
-                                             const Extent& e, int lane) {
+struct Sides {
+  uint4 p[4];  // forward: gate; dinput: pre
+  Raw8 q[4];   // forward: residual; dinput: gate; dweight: what dw holds
+};
+template <int MODE>
+__device__ __forceinline__ void load_sides(const EpiK& k, const Block& b, const Extent& e,
+                                           Sides<MODE>& s) {
+  constexpr int site = ZERO_SITE_LINEAR_OUT;
 #pragma unroll
   for (int it = 0; it < 4; ++it) {
-    const int r = it * 8 + (lane >> 2), c = (lane & 3) * 8;
-    const int64_t row = row0 + r, col = col0 + c;
-    const uint32_t at = patch + (uint32_t)(r * 36 + c) * 4;
+    const int64_t row = b.row + it * 8;
+    if (row >= e.rows || !b.valid) continue;
+    if constexpr (MODE == LIN_FORWARD) {
+      if (k.gate.p) s.p[it] = raw8_bf16(k.gate, row, b.col, b.valid, e, site);
+      if (k.residual.p) s.q[it] = raw8(k.residual, row, b.col, b.valid, e, site);
+    } else if constexpr (MODE == LIN_DINPUT) {
+      if (k.pre.p) s.p[it] = raw8_bf16(k.pre, row, b.col, b.valid, e, site);
+      if (k.gate.p) s.q[it].a = raw8_bf16(k.gate, row, b.col, b.valid, e, site);
+    } else {
+      if (k.accumulate) s.q[it] = raw8(k.out, row, b.col, b.valid, e, site);
+    }
+  }
+}
+
+// What follows the product for 8 columns of row `row`, v holding their sums.
+template <int MODE>
+__device__ __forceinline__ void finish8(const EpiK& k, uint64_t offset, int64_t row,
+                                        const Block& b, const Extent& e, const float bias[8],
+                                        const uint4& p, const Raw8& q, float v[8]) {
+  constexpr int site = ZERO_SITE_LINEAR_OUT;
+  float f[8];
+  if constexpr (MODE == LIN_FORWARD) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += bias[j];
+    if (k.pre.p) store8(k.pre, row, b.col, b.valid, v, e, site);
+    activate8(v, k.act);
+    if (k.gate.p) {
+      from_bf16(p, f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= f[j];
+    }
+    if (k.drop.on) drop8(k.drop, offset, (uint32_t)row, b.col, v);
+    if (k.residual.p) {
+      from_raw(k.residual, q, f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] += f[j];
+    }
+  } else if constexpr (MODE == LIN_DINPUT) {
+    if (k.pre.p) {
+      float value[8], slope[8];
+      from_bf16(p, f);
+      activate_grad8(f, k.act, value, slope);
+      if (k.gate.p) {
+        from_bf16(q.a, f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          value[j] *= v[j];
+          slope[j] *= f[j];
+        }
+        if (k.dgate.p) store8(k.dgate, row, b.col, b.valid, value, e, site);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= slope[j];
+    }
+  } else {
+    if (k.accumulate) {
+      from_raw(k.out, q, f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] += f[j];
+    }
+  }
+  store8(k.out, row, b.col, b.valid, v, e, site);
+}
+
+__device__ __forceinline__ float4 ld_shared4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// The block's sums, lying in the patch in the output's orientation (row r of
+// the patch is output row row0 + r): in this CTA's shared memory, or as
+// `pairs` parts at the same address in the cluster's CTAs of this half.
+template <int MODE, bool PARTS>
+__device__ __forceinline__ void finish_block(const EpiK& k, uint64_t offset, uint32_t patch,
+                                             int pairs, uint32_t half, const Block& b,
+                                             const Extent& e, const Sides<MODE>& s, int lane) {
+  float bias[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) bias[j] = 0.0f;
+  if (MODE == LIN_FORWARD && k.bias.p && b.valid)
+    load8(k.bias, 0, b.col, b.valid, bias, Extent{1, e.cols}, ZERO_SITE_LINEAR_OUT);
+#pragma unroll
+  for (int it = 0; it < 4; ++it) {
+    const uint32_t at = patch + (uint32_t)((it * 8 + (lane >> 2)) * 36 + (lane & 3) * 8) * 4;
     float v[8];
-    if (pairs == 1) {
-      const float4 x = ld_cluster4(at), y = ld_cluster4(at + 16);
+    if constexpr (!PARTS) {
+      const float4 x = ld_shared4(at), y = ld_shared4(at + 16);
       v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
       v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
     } else {
@@ -295,8 +397,9 @@ __device__ __forceinline__ void finish_patch(const ProductK& k, uint64_t offset,
         v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
       }
     }
-    if (row < e.rows && col < e.cols)
-      epilogue8<MODE>(k.epi, offset, row, col, e.cols - col < 8 ? (int)(e.cols - col) : 8, v, e);
+    const int64_t row = b.row + it * 8;
+    if (row < e.rows && b.valid)
+      finish8<MODE>(k, offset, row, b, e, bias, s.p[it], s.q[it], v);
   }
 }
 
@@ -470,6 +573,9 @@ __global__ void __launch_bounds__((GEN ? 16 : 12) * 32, 1)
       for (int cc = set; cc < chunks; cc += 2) {
         const int64_t j0 = (int64_t)tj * g.bn + cc * 32;
         if (S == 1 && tj >= 0 && (i0 >= k.rows || j0 >= k.cols)) continue;
+        const Block b = block_of(k.out_t ? j0 : i0, k.out_t ? i0 : j0, e, lane);
+        Sides<MODE> sides;
+        if (S == 1 && tj >= 0) load_sides<MODE>(k.epi, b, e, sides);
         uint32_t r[32];
         tmem_load32(d + cc * 32, r);
         if (kb1 == kb0) {
@@ -500,8 +606,7 @@ __global__ void __launch_bounds__((GEN ? 16 : 12) * 32, 1)
         }
         if (S == 1) {
           __syncwarp();
-          finish_patch<MODE>(k, offset, patch, 1, half, k.out_t ? j0 : i0, k.out_t ? i0 : j0, e,
-                             lane);
+          finish_block<MODE, false>(k.epi, offset, patch, 1, half, b, e, sides, lane);
           __syncwarp();
         }
       }
@@ -574,8 +679,10 @@ __global__ void __launch_bounds__((GEN ? 16 : 12) * 32, 1)
             store1(k.dbias, i, v);
           }
         } else if (i0 < k.rows && j0 < k.cols) {
-          finish_patch<MODE>(k, offset, patch, S, half, k.out_t ? j0 : i0, k.out_t ? i0 : j0, e,
-                             lane);
+          const Block o = block_of(k.out_t ? j0 : i0, k.out_t ? i0 : j0, e, lane);
+          Sides<MODE> sides;
+          load_sides<MODE>(k.epi, o, e, sides);
+          finish_block<MODE, true>(k.epi, offset, patch, S, half, o, e, sides, lane);
         }
       }
     }

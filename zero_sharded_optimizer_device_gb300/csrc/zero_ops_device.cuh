@@ -105,6 +105,65 @@ __device__ __forceinline__ void store1(const Mat& a, int64_t i, float v) {
     static_cast<uint16_t*>(a.p)[i] = to_bf16(v);
 }
 
+// 8 columns as they lie in memory (bf16 fills `a` alone), so that a load can
+// be in flight while other work goes on.
+struct Raw8 {
+  uint4 a, b;
+};
+__device__ __forceinline__ uint4 ld16(const void* p) {
+  uint4 u;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+               : "l"(p));
+  return u;
+}
+__device__ __forceinline__ uint4 raw8_bf16(const Mat& a, int64_t row, int64_t col, int valid,
+                                           const Extent& e, int site) {
+  const int64_t i = row * a.ld + col;
+  if (!in_extent(i, i + valid, row * a.ld, row * a.ld + e.cols, site) ||
+      !in_extent(row, row + 1, 0, e.rows, site))
+    return make_uint4(0, 0, 0, 0);
+  const uint16_t* p = static_cast<const uint16_t*>(a.p) + i;
+  if (a.vec && valid == 8) return ld16(p);
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j < valid) w[j / 2] |= (uint32_t)p[j] << (16 * (j & 1));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ Raw8 raw8(const Mat& a, int64_t row, int64_t col, int valid,
+                                     const Extent& e, int site) {
+  Raw8 r;
+  if (a.dtype != ZERO_F32) {
+    r.a = raw8_bf16(a, row, col, valid, e, site);
+    r.b = make_uint4(0, 0, 0, 0);
+    return r;
+  }
+  float f[8];
+  load8(a, row, col, valid, f, e, site);
+  r.a = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                   __float_as_uint(f[3]));
+  r.b = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]),
+                   __float_as_uint(f[7]));
+  return r;
+}
+__device__ __forceinline__ void from_bf16(const uint4& u, float f[8]) {
+  f[0] = bf16_lo(u.x); f[1] = bf16_hi(u.x);
+  f[2] = bf16_lo(u.y); f[3] = bf16_hi(u.y);
+  f[4] = bf16_lo(u.z); f[5] = bf16_hi(u.z);
+  f[6] = bf16_lo(u.w); f[7] = bf16_hi(u.w);
+}
+__device__ __forceinline__ void from_raw(const Mat& a, const Raw8& r, float f[8]) {
+  if (a.dtype != ZERO_F32) {
+    from_bf16(r.a, f);
+  } else {
+    f[0] = __uint_as_float(r.a.x); f[1] = __uint_as_float(r.a.y);
+    f[2] = __uint_as_float(r.a.z); f[3] = __uint_as_float(r.a.w);
+    f[4] = __uint_as_float(r.b.x); f[5] = __uint_as_float(r.b.y);
+    f[6] = __uint_as_float(r.b.z); f[7] = __uint_as_float(r.b.w);
+  }
+}
+
 // ------------------------------------------------------------------------
 // Activations.  Both GELU forms and SiLU are z times a distribution function
 // s(z); the tanh form's (1 + tanh u) / 2 is the logistic function of 2u, so
@@ -117,44 +176,73 @@ constexpr float kGeluB = 0.044715f;
 constexpr float kRsqrt2 = 0.70710678118654752f;
 constexpr float kRsqrt2Pi = 0.39894228040143268f;
 
-__device__ __forceinline__ float activate(float z, int act) {
+// 8 values through an activation, in place.
+__device__ __forceinline__ void activate8(float z[8], int act) {
   switch (act) {
-    case ZERO_ACT_RELU: return z < 0.0f ? 0.0f : z;  // NaN stays NaN
-    case ZERO_ACT_GELU: return 0.5f * z * (1.0f + erff(z * kRsqrt2));
-    case ZERO_ACT_GELU_TANH: return z * logistic(kGeluA * (z + kGeluB * z * z * z));
-    case ZERO_ACT_SILU: return z * logistic(z);
-    default: return z;
+    case ZERO_ACT_RELU:
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z[j] = z[j] < 0.0f ? 0.0f : z[j];  // NaN stays NaN
+      break;
+    case ZERO_ACT_GELU:
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z[j] = 0.5f * z[j] * (1.0f + erff(z[j] * kRsqrt2));
+      break;
+    case ZERO_ACT_GELU_TANH:
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        z[j] = z[j] * logistic(z[j] * (kGeluA + kGeluA * kGeluB * z[j] * z[j]));
+      break;
+    case ZERO_ACT_SILU:
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z[j] = z[j] * logistic(z[j]);
+      break;
+    default:
+      break;
   }
 }
 
-// act(z) and d act / dz.
-__device__ __forceinline__ void activate_grad(float z, int act, float& value, float& slope) {
+// act(z) and d act / dz of 8 values.
+__device__ __forceinline__ void activate_grad8(const float z[8], int act, float value[8],
+                                               float slope[8]) {
   switch (act) {
     case ZERO_ACT_RELU:
-      value = z < 0.0f ? 0.0f : z;
-      slope = z > 0.0f ? 1.0f : 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        value[j] = z[j] < 0.0f ? 0.0f : z[j];
+        slope[j] = z[j] > 0.0f ? 1.0f : 0.0f;
+      }
       break;
-    case ZERO_ACT_GELU: {
-      const float s = 0.5f * (1.0f + erff(z * kRsqrt2));
-      value = z * s;
-      slope = s + z * kRsqrt2Pi * __expf(-0.5f * z * z);
+    case ZERO_ACT_GELU:
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float s = 0.5f * (1.0f + erff(z[j] * kRsqrt2));
+        value[j] = z[j] * s;
+        slope[j] = s + z[j] * kRsqrt2Pi * __expf(-0.5f * z[j] * z[j]);
+      }
       break;
-    }
-    case ZERO_ACT_GELU_TANH: {
-      const float s = logistic(kGeluA * (z + kGeluB * z * z * z));
-      value = z * s;
-      slope = s + value * (1.0f - s) * (kGeluA * (1.0f + 3.0f * kGeluB * z * z));
+    case ZERO_ACT_GELU_TANH:
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float q = z[j] * z[j];
+        const float s = logistic(z[j] * (kGeluA + kGeluA * kGeluB * q));
+        value[j] = z[j] * s;
+        slope[j] = s + value[j] * (1.0f - s) * (kGeluA + 3.0f * kGeluA * kGeluB * q);
+      }
       break;
-    }
-    case ZERO_ACT_SILU: {
-      const float s = logistic(z);
-      value = z * s;
-      slope = s + value * (1.0f - s);
+    case ZERO_ACT_SILU:
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float s = logistic(z[j]);
+        value[j] = z[j] * s;
+        slope[j] = s + value[j] * (1.0f - s);
+      }
       break;
-    }
     default:
-      value = z;
-      slope = 1.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        value[j] = z[j];
+        slope[j] = 1.0f;
+      }
   }
 }
 
@@ -192,65 +280,6 @@ __device__ __forceinline__ void drop8(const DropK& d, uint64_t offset, uint32_t 
     for (int j = 0; j < 4; ++j)
       f[4 * h + j] = (u[j] >= d.least && !d.all) ? f[4 * h + j] * d.scale : 0.0f;
   }
-}
-
-// ------------------------------------------------------------------------
-// What follows a product: 8 consecutive columns of output row `row` (of an
-// output of e.rows x e.cols), v holding the fp32 sums on entry.
-// ------------------------------------------------------------------------
-template <int MODE>
-__device__ __forceinline__ void epilogue8(const EpiK& k, uint64_t offset, int64_t row,
-                                          int64_t col, int valid, float v[8], const Extent& e) {
-  constexpr int site = ZERO_SITE_LINEAR_OUT;
-  float f[8];
-  if constexpr (MODE == LIN_FORWARD) {
-    if (k.bias.p) {
-      load8(k.bias, 0, col, valid, f, Extent{1, e.cols}, site);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] += f[j];
-    }
-    if (k.pre.p) store8(k.pre, row, col, valid, v, e, site);
-    if (k.act != ZERO_ACT_NONE) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = activate(v[j], k.act);
-    }
-    if (k.gate.p) {
-      load8(k.gate, row, col, valid, f, e, site);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= f[j];
-    }
-    if (k.drop.on) drop8(k.drop, offset, (uint32_t)row, col, v);
-    if (k.residual.p) {
-      load8(k.residual, row, col, valid, f, e, site);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] += f[j];
-    }
-  } else if constexpr (MODE == LIN_DINPUT) {
-    if (k.pre.p) {
-      float value[8], slope[8];
-      load8(k.pre, row, col, valid, f, e, site);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) activate_grad(f[j], k.act, value[j], slope[j]);
-      if (k.gate.p) {
-        load8(k.gate, row, col, valid, f, e, site);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          value[j] *= v[j];
-          slope[j] *= f[j];
-        }
-        if (k.dgate.p) store8(k.dgate, row, col, valid, value, e, site);
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= slope[j];
-    }
-  } else {
-    if (k.accumulate) {
-      load8(k.out, row, col, valid, f, e, site);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] += f[j];
-    }
-  }
-  store8(k.out, row, col, valid, v, e, site);
 }
 
 }  // namespace zk
