@@ -128,6 +128,44 @@ def test_linear_strides_and_alignments(cuda, Z, m, n, k, kn, pad, skew):
     run_linear(Z, m, n, k, kn, bias=BF, act="gelu", pre=True, residual=F32, pad=pad, skew=skew)
 
 
+@pytest.mark.parametrize("kn", [False, True], ids=["nk", "kn"])
+@pytest.mark.parametrize("m,n,k", [(300, 259, 331), (300, 256, 331), (600, 1001, 77), (90, 203, 131)])
+def test_odd_sizes_in_aligned_rows(cuda, Z, m, n, k, kn):
+    """Odd sizes whose rows are padded to 16 bytes: what lies in the gaps
+    (-77) enters no sum, and no store reaches into them."""
+    g = torch.Generator().manual_seed(m + n + k)
+
+    def mk(t):
+        rows, cols = t.shape
+        return Guarded(rows, cols, t.dtype, -cols % 8, 0, t)
+
+    x, w = randn(g, m, k), randn(g, *((k, n) if kn else (n, k)), scale=k ** -0.5)
+    r, dy, pre, u = randn(g, m, n), randn(g, m, n), randn(g, m, k), randn(g, m, k)
+    X, W, Q, DY, P, U = (mk(t) for t in (x, w, r, dy, pre, u))
+    lay = Z.ZERO_W_KN if kn else Z.ZERO_W_NK
+    for out in (BF, F32):
+        Y, PRE = mk(torch.zeros(m, n, dtype=out)), mk(torch.zeros(m, n, dtype=BF))
+        ep = Z.linear_epilogue(act=Z.ZERO_ACT_SILU, pre=PRE.t, ldpre=PRE.ld, residual=Q.t, ldres=Q.ld)
+        Z.zero_linear(X.t, X.ld, W.t, W.ld, lay, m, n, k, ep, Y.t, Y.ld, code(Z, out))
+        y, z, ey, ez = R.linear(x, w, kn, None, "silu", residual=r)
+        R.assert_within(Y.t, y, ey, "y")
+        R.assert_within(PRE.t, z, ez, "pre")
+        DX, DU = mk(torch.zeros(m, k, dtype=out)), mk(torch.zeros(m, k, dtype=BF))
+        ag = Z.linear_act_grad(Z.ZERO_ACT_GELU, P.t, P.ld, U.t, U.ld, DU.t, DU.ld)
+        Z.zero_linear_dinput(DY.t, DY.ld, W.t, W.ld, lay, m, n, k, ag, DX.t, DX.ld, code(Z, out))
+        dx, du, ex, eu = R.linear_dinput(dy, w, kn, "gelu", pre, u)
+        R.assert_within(DX.t, dx, ex, "dx")
+        R.assert_within(DU.t, du, eu, "dgate")
+        DW, DB = mk(torch.zeros(w.shape, dtype=out)), mk(torch.zeros(1, n, dtype=out))
+        Z.zero_linear_dweight(DY.t, DY.ld, X.t, X.ld, m, n, k, lay, DW.t, DW.ld, code(Z, out),
+                              DB.t[0], code(Z, out), False)
+        dw, db, ew, eb = R.linear_dweight(dy, x, kn)
+        R.assert_within(DW.t, dw, ew, "dw")
+        R.assert_within(DB.t[0], db, eb, "dbias")
+        for what, t in (("y", Y), ("pre", PRE), ("dx", DX), ("dgate", DU), ("dw", DW), ("dbias", DB)):
+            t.check(what)
+
+
 @pytest.mark.parametrize("p", [0.0, 1.0, 0.9999])
 def test_linear_dropout_extremes(cuda, Z, p):
     run_linear(Z, 65, 70, 80, True, p=p, residual=BF)
@@ -255,6 +293,18 @@ def test_linear_dweight_of_no_rows(cuda, Z):
         Z.zero_linear_dweight(None, 24, None, 40, 0, 24, 40, 0, dw, 40, Z.ZERO_BF16, db, Z.ZERO_F32,
                               acc)
         assert bool((dw == (3.0 if acc else 0.0)).all()) and bool((db == (5.0 if acc else 0.0)).all())
+
+
+@pytest.mark.parametrize("kn", [False, True], ids=["nk", "kn"])
+def test_linear_dweight_of_no_inputs(cuda, Z, kn):
+    """k = 0: there is no weight, but the bias still has its gradient."""
+    m, n = 70, 300
+    dy = randn(torch.Generator().manual_seed(5), m, n)
+    db = torch.zeros(n, device="cuda")
+    Z.zero_linear_dweight(dy.cuda(), n, None, 0, m, n, 0, Z.ZERO_W_KN if kn else Z.ZERO_W_NK, None,
+                          n if kn else 0, Z.ZERO_BF16, db, Z.ZERO_F32)
+    _, want, _, err = R.linear_dweight(dy, torch.zeros(m, 0), kn)
+    R.assert_within(db, want, err, "dbias")
 
 
 def test_gradients_against_differences(cuda, Z):

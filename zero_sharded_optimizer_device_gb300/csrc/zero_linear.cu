@@ -10,10 +10,18 @@
 //   warp 0        loads operand tiles 64 deep by TMA into a ring of stages
 //   warp 1        (first CTA of the pair) issues the tensor-core instructions
 //   warp 2        allocates and frees tensor memory
-//   warps 4-11    epilogue: tensor memory -> registers -> a transposing patch
-//                 of shared memory -> 8 consecutive columns per thread, with
-//                 which every side matrix is read and the output written
-//   warps 12-15   (GEN) load operands whose base or rows lie off 16-byte
+//   warp 3        (boxes) loads the side operands' boxes by TMA ahead of the
+//                 epilogue and stores the finished ones
+//   warps 4-11    epilogue, in one of two forms:
+//                 boxes: a thread keeps its row of sums as tensor memory gives
+//                 it (no exchange between threads), reads the side operands
+//                 from the boxes warp 3 brought and writes its results in
+//                 their place; addresses, bounds and coalescing are TMA's
+//                 patches: 32 x 32 sums cross a patch of shared memory, and a
+//                 thread goes on with 8 consecutive columns by plain loads and
+//                 stores; for transposed outputs, joined parts of a split
+//                 contraction and rows off 16-byte boundaries
+//   warps 12-15   (gen) load operands whose base or rows lie off 16-byte
 //                 boundaries, which TMA cannot, with plain loads
 // Tiles are walked persistently with two sets of sums, so one tile's epilogue
 // runs under the next one's products.  Where there are too few tiles to fill
@@ -34,18 +42,36 @@ constexpr int kEpiWarp0 = 4, kEpiWarps = 8, kGenWarp0 = 12, kGenWarps = 4;
 constexpr int kPatch = 32 * 36;        // floats of a 32 x 32 patch, rows 36 apart
 constexpr int kMaxStages = 9;
 constexpr int kOnesBytes = 2048;
+constexpr int kSlot = 16384;           // a box of 128 rows of 128 bytes
+constexpr int kMostBoxes = 3;          // chunks of boxes in the ring
 constexpr int kSmemMost = 232448;      // shared memory one CTA may have
 constexpr unsigned long long kWaitNs = 2000000000ull;
 
 static __device__ unsigned long long g_ops_timeouts;
 
+// Forms of the kernel: how operands come in and results go out.
+enum Form : int {
+  PATCH = 0,      // operands by TMA, results over patches
+  PATCH_GEN = 1,  // an operand by plain loads, results over patches
+  BOX_BF16 = 2,   // operands by TMA, results in boxes of 64 bf16 columns
+  BOX_F32 = 3     // operands by TMA, results in boxes of 32 fp32 columns
+};
+
 // How a launch walks its product (host-made).
 struct TileK {
-  int tiles_i, tiles_j, bias_tiles;  // bias_tiles: tiles_i more, summing A alone
+  int tiles_i, tiles_j, bias_tiles;  // bias_tiles more sum one operand's rows alone
+  int bias_b;                        // ... those of B (else of A)
   int kblocks, splits, bn, stages;
   int i_fast;                        // consecutive tiles differ in i (else in j)
   int gen_a, gen_b;                  // elements per plain load; 0: by TMA
+  int boxes;                         // ring of box chunks (box forms)
+  int two_slots;                     // a chunk holds two slots
   uint32_t tmem_cols;
+};
+
+// Box forms: the side operands and outputs (see box_chunk).
+struct BoxMaps {
+  CUtensorMap out, pre, gate, extra;  // extra: forward residual, dinput dgate
 };
 
 // ------------------------------------------------------------ PTX wrappers --
@@ -121,6 +147,24 @@ __device__ __forceinline__ void tma_load(const CUtensorMap* map, uint32_t dst, i
       ".mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
       "l"(map), "r"(x), "r"(y), "r"(cluster_bar)
       : "memory");
+}
+// Boxes of side operands and results: this CTA's own barrier and memory.
+__device__ __forceinline__ void box_load(const CUtensorMap* map, uint32_t dst, int x, int y,
+                                         uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void box_store(const CUtensorMap* map, uint32_t src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::
+                   "l"(map),
+               "r"(x), "r"(y), "r"(src)
+               : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // Tensor-core arrivals: when every instruction issued so far is done, one
 // arrival on this barrier of both CTAs of the pair.
@@ -403,13 +447,252 @@ __device__ __forceinline__ void finish_block(const EpiK& k, uint64_t offset, uin
   }
 }
 
-template <int MODE, bool GEN>
-__global__ void __launch_bounds__((GEN ? 16 : 12) * 32, 1)
+// ---------------------------------------------------------------------------
+// Box forms.  A chunk is 64 bf16 or 32 fp32 columns of the tile's 128 rows,
+// one or two slots of 16 KiB in which results take the place of operands:
+//   forward, bf16: slot 0 gate -> pre, slot 1 residual -> y
+//   forward, fp32: the same, slot 0 rows being 64 bytes
+//   dinput,  bf16: slot 0 pre -> dx, slot 1 gate -> dgate
+//   dinput,  fp32: slot 0 dx, slot 1 pre (first half) and gate -> dgate
+//   dweight:       slot 0 what dw holds -> dw
+// (forward without gate and pre keeps slot 1 alone, at the chunk's start).
+// Rows of 128 bytes are swizzled in 16-byte units by row mod 8, rows of 64 by
+// row / 2 mod 4, so that a warp's threads, a row each, meet no bank twice.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t at128(int row, int unit) {
+  return (uint32_t)(row * 128 + ((unit ^ (row & 7)) << 4));
+}
+__device__ __forceinline__ uint32_t at64(int row, int unit) {
+  return (uint32_t)(row * 64 + ((unit ^ ((row >> 1) & 3)) << 4));
+}
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+  uint4 u;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+               : "r"(addr)
+               : "memory");
+  return u;
+}
+__device__ __forceinline__ void sts16(uint32_t addr, uint4 u) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(u.x), "r"(u.y), "r"(u.z),
+               "r"(u.w)
+               : "memory");
+}
+__device__ __forceinline__ void lds_f32(uint32_t base, int row, int i, float f[8]) {
+  const uint4 a = lds16(base + at128(row, 2 * i)), b = lds16(base + at128(row, 2 * i + 1));
+  f[0] = __uint_as_float(a.x); f[1] = __uint_as_float(a.y);
+  f[2] = __uint_as_float(a.z); f[3] = __uint_as_float(a.w);
+  f[4] = __uint_as_float(b.x); f[5] = __uint_as_float(b.y);
+  f[6] = __uint_as_float(b.z); f[7] = __uint_as_float(b.w);
+}
+__device__ __forceinline__ void sts_f32(uint32_t base, int row, int i, const float f[8]) {
+  sts16(base + at128(row, 2 * i),
+        make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                   __float_as_uint(f[3])));
+  sts16(base + at128(row, 2 * i + 1),
+        make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]),
+                   __float_as_uint(f[7])));
+}
+
+// A thread's 32 sums of row `row` of the tile, columns col.. of the output,
+// through the epilogue; unit0: their first 16-byte unit in a bf16 row.
+template <int MODE, int FORM>
+__device__ __forceinline__ void box_chunk(const EpiK& k, uint64_t offset, uint32_t chunk,
+                                          int two_slots, int row, int64_t out_row, int64_t col,
+                                          int unit0, int64_t cols, const uint32_t r[32]) {
+  constexpr bool wide = FORM == BOX_F32;
+  const uint32_t slot1 = chunk + (two_slots ? kSlot : 0);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float v[8], f[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(r[8 * i + j]);
+    const int64_t c = col + 8 * i;
+    if constexpr (MODE == LIN_FORWARD) {
+      const uint32_t s0 = chunk + (wide ? at64(row, i) : at128(row, unit0 + i));
+      const uint32_t s1 = slot1 + at128(row, unit0 + i);
+      if (k.bias.p && c < cols) {
+        load8(k.bias, 0, c, cols - c < 8 ? (int)(cols - c) : 8, f, Extent{1, cols},
+              ZERO_SITE_LINEAR_OUT);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] += f[j];
+      }
+      uint4 g;
+      if (k.gate.p) g = lds16(s0);
+      if (k.pre.p) sts16(s0, pack8(v));
+      activate8(v, k.act);
+      if (k.gate.p) {
+        from_bf16(g, f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] *= f[j];
+      }
+      if (k.drop.on) drop8(k.drop, offset, (uint32_t)out_row, c, v);
+      if (k.residual.p) {
+        if constexpr (wide)
+          lds_f32(slot1, row, i, f);
+        else
+          from_bf16(lds16(s1), f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] += f[j];
+      }
+      if constexpr (wide)
+        sts_f32(slot1, row, i, v);
+      else
+        sts16(s1, pack8(v));
+    } else if constexpr (MODE == LIN_DINPUT) {
+      const uint32_t pre_at = wide ? slot1 + at64(row, i) : chunk + at128(row, unit0 + i);
+      const uint32_t gate_at =
+          wide ? slot1 + kSlot / 2 + at64(row, i) : slot1 + at128(row, unit0 + i);
+      if (k.pre.p) {
+        float value[8], slope[8];
+        from_bf16(lds16(pre_at), f);
+        activate_grad8(f, k.act, value, slope);
+        if (k.gate.p) {
+          from_bf16(lds16(gate_at), f);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            value[j] *= v[j];
+            slope[j] *= f[j];
+          }
+          if (k.dgate.p) sts16(gate_at, pack8(value));
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] *= slope[j];
+      }
+      if constexpr (wide)
+        sts_f32(chunk, row, i, v);
+      else
+        sts16(chunk + at128(row, unit0 + i), pack8(v));
+    } else {
+      if (k.accumulate) {
+        if constexpr (wide)
+          lds_f32(chunk, row, i, f);
+        else
+          from_bf16(lds16(chunk + at128(row, unit0 + i)), f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] += f[j];
+      }
+      if constexpr (wide)
+        sts_f32(chunk, row, i, v);
+      else
+        sts16(chunk + at128(row, unit0 + i), pack8(v));
+    }
+  }
+}
+
+// A walk over the chunks of this CTA's tiles, in order.
+struct ChunkWalk {
+  int t, ti, tj, cc, count;
+};
+template <int WIDTH>
+__device__ __forceinline__ void enter_tile(const TileK& g, int64_t cols, ChunkWalk& w) {
+  tile_at(g, w.t, w.ti, w.tj);
+  w.cc = 0;
+  const int64_t left = cols - (int64_t)w.tj * g.bn;
+  w.count = w.tj < 0 ? 0 : (int)((left < g.bn ? left : g.bn) + WIDTH - 1) / WIDTH;
+}
+template <int WIDTH>
+__device__ __forceinline__ void next_chunk(const TileK& g, int64_t cols, int tiles, int step,
+                                           ChunkWalk& w) {
+  ++w.cc;
+  while (w.cc >= w.count) {
+    w.t += step;
+    if (w.t >= tiles) return;
+    enter_tile<WIDTH>(g, cols, w);
+  }
+}
+
+// Warp 3's thread: brings the side operands of up to g.boxes chunks ahead and
+// stores each chunk when the epilogue is done with it.
+template <int MODE, int FORM>
+__device__ __forceinline__ void box_traffic(const BoxMaps& maps, const ProductK& k,
+                                            const TileK& g, uint32_t boxes, uint32_t efull,
+                                            uint32_t edone, int first, int tiles, int step,
+                                            uint32_t half, volatile int* dead) {
+  constexpr bool wide = FORM == BOX_F32;
+  constexpr int W = wide ? 32 : 64;
+  const uint32_t chunk_bytes = kSlot * (g.two_slots ? 2 : 1);
+  constexpr uint32_t narrow = wide ? kSlot / 2 : kSlot;  // a bf16 box
+  const bool gate = MODE != LIN_DWEIGHT && k.epi.gate.p;
+  const bool res = MODE == LIN_FORWARD && k.epi.residual.p;
+  const bool pre_in = MODE == LIN_DINPUT && k.epi.pre.p;
+  const bool old = MODE == LIN_DWEIGHT && k.epi.accumulate;
+  const uint32_t bytes = (gate ? narrow : 0) + (res || old ? kSlot : 0) + (pre_in ? narrow : 0);
+  ChunkWalk in, out;
+  in.t = first;
+  in.count = in.cc = 0;
+  if (first < tiles) {
+    enter_tile<W>(g, k.cols, in);
+    in.cc = -1;
+    next_chunk<W>(g, k.cols, tiles, step, in);
+  }
+  out = in;
+  uint32_t loaded = 0, stored = 0, lb = 0, sb = 0, sph = 0;
+  while (out.t < tiles) {
+    while (in.t < tiles && loaded < stored + g.boxes) {
+      const uint32_t at = boxes + lb * chunk_bytes, slot1 = at + (g.two_slots ? kSlot : 0);
+      const uint32_t bar = efull + 8 * lb;
+      const int x = in.tj * g.bn + in.cc * W, y = in.ti * 256 + (int)half * kRowsCta;
+      bar_expect(bar, bytes);
+      if constexpr (MODE == LIN_FORWARD) {
+        if (gate) box_load(&maps.gate, at, x, y, bar);
+        if (res) box_load(&maps.extra, slot1, x, y, bar);
+      } else if constexpr (MODE == LIN_DINPUT) {
+        if (pre_in) box_load(&maps.pre, wide ? slot1 : at, x, y, bar);
+        if (gate) box_load(&maps.gate, wide ? slot1 + kSlot / 2 : slot1, x, y, bar);
+      } else {
+        if (old) box_load(&maps.out, at, x, y, bar);
+      }
+      ++loaded;
+      if (++lb == (uint32_t)g.boxes) lb = 0;
+      next_chunk<W>(g, k.cols, tiles, step, in);
+    }
+    if (!bar_wait(edone + 8 * sb, sph, dead)) break;
+    const uint32_t at = boxes + sb * chunk_bytes, slot1 = at + (g.two_slots ? kSlot : 0);
+    const int x = out.tj * g.bn + out.cc * W, y = out.ti * 256 + (int)half * kRowsCta;
+    if (y < k.rows) {
+      if constexpr (MODE == LIN_FORWARD) {
+        if (k.epi.pre.p) box_store(&maps.pre, at, x, y);
+        box_store(&maps.out, slot1, x, y);
+      } else if constexpr (MODE == LIN_DINPUT) {
+        if (k.epi.dgate.p) box_store(&maps.extra, wide ? slot1 + kSlot / 2 : slot1, x, y);
+        box_store(&maps.out, at, x, y);
+      } else {
+        box_store(&maps.out, at, x, y);
+      }
+    }
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    ++stored;
+    if (++sb == (uint32_t)g.boxes) {
+      sb = 0;
+      sph ^= 1;
+    }
+    next_chunk<W>(g, k.cols, tiles, step, out);
+  }
+  // after a wait that gave up: the boxes in flight land before the CTA returns
+  for (; stored < loaded; ++stored) {
+    const uint64_t t0 = now_ns();
+    while (!bar_try(efull + 8 * sb, sph) && now_ns() - t0 < kWaitNs / 8) {
+    }
+    if (++sb == (uint32_t)g.boxes) {
+      sb = 0;
+      sph ^= 1;
+    }
+  }
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
+template <int MODE, int FORM>
+__global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
     product_kernel(const __grid_constant__ CUtensorMap map_a,
-                   const __grid_constant__ CUtensorMap map_b, const __grid_constant__ ProductK k,
+                   const __grid_constant__ CUtensorMap map_b,
+                   const __grid_constant__ BoxMaps maps, const __grid_constant__ ProductK k,
                    const __grid_constant__ TileK g) {
+  constexpr bool GEN = FORM == PATCH_GEN, BOX = FORM == BOX_BF16 || FORM == BOX_F32;
+  constexpr int kWidth = FORM == BOX_F32 ? 32 : 64;  // columns of a chunk
   extern __shared__ __align__(1024) unsigned char smem[];
-  __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 4];
+  __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 4 + 2 * kMostBoxes];
   __shared__ uint32_t tmem_at;
   __shared__ int dead;
   const uint32_t rank = cluster_rank(), half = rank & 1, leader = rank & ~1u;
@@ -418,9 +701,11 @@ __global__ void __launch_bounds__((GEN ? 16 : 12) * 32, 1)
   const uint32_t stage_bytes = kBytesA + g.bn * kDeep;  // bn / 2 rows of 128 bytes
   const uint32_t ring = smem_u32(smem);
   const uint32_t patches = ring + g.stages * stage_bytes;
-  const uint32_t ones = patches + (S == 1 ? kEpiWarps * kPatch * 4 : 0);
+  const uint32_t ones = patches + (BOX ? g.boxes * kSlot * (g.two_slots ? 2 : 1)
+                                       : S == 1 ? kEpiWarps * kPatch * 4 : 0);
   const uint32_t full = smem_u32(bars), empty = full + 8 * kMaxStages;
   const uint32_t tfull = empty + 8 * kMaxStages, tempty = tfull + 16;
+  const uint32_t efull = tempty + 16, edone = efull + 8 * kMostBoxes;
 
   if (warp == 0 && lane == 0) {
     dead = 0;
@@ -432,6 +717,12 @@ __global__ void __launch_bounds__((GEN ? 16 : 12) * 32, 1)
       bar_init(tfull + 8 * a, 1);
       bar_init(tempty + 8 * a, 2 * kEpiWarps);
     }
+    if (BOX)
+      for (int b = 0; b < g.boxes; ++b) {
+        bar_init(efull + 8 * b, 1);
+        // 64 columns are shared by both sets of epilogue warps, 32 taken by one
+        bar_init(edone + 8 * b, kWidth == 64 ? kEpiWarps : kEpiWarps / 2);
+      }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 2) {
@@ -471,7 +762,9 @@ __global__ void __launch_bounds__((GEN ? 16 : 12) * 32, 1)
         tile_at(g, t, ti, tj);
         const int i0 = ti * 256 + (int)half * kRowsCta;
         const int j0 = tj * g.bn + (int)half * (g.bn / 2);
-        const bool load_a = g.gen_a == 0, load_b = g.gen_b == 0 && tj >= 0;
+        const bool load_a = tj < 0 && g.bias_b ? g.gen_b == 0 : g.gen_a == 0;
+        const bool load_b = g.gen_b == 0 && tj >= 0;
+        const CUtensorMap* map_i = tj < 0 && g.bias_b ? &map_b : &map_a;
         const uint32_t bytes =
             2 * ((load_a ? kBytesA : 0) + (load_b ? (uint32_t)g.bn * kDeep : 0));
         for (int kb = kb0; kb < kb1; ++kb) {
@@ -481,10 +774,10 @@ __global__ void __launch_bounds__((GEN ? 16 : 12) * 32, 1)
           const uint32_t a_at = ring + s * stage_bytes, b_at = a_at + kBytesA;
           if (load_a) {
             if (a_c) {
-              tma_load(&map_a, a_at, kb * kDeep, i0, full_lead + 8 * s);
+              tma_load(map_i, a_at, kb * kDeep, i0, full_lead + 8 * s);
             } else {
-              tma_load(&map_a, a_at, i0, kb * kDeep, full_lead + 8 * s);
-              tma_load(&map_a, a_at + 8192, i0 + 64, kb * kDeep, full_lead + 8 * s);
+              tma_load(map_i, a_at, i0, kb * kDeep, full_lead + 8 * s);
+              tma_load(map_i, a_at + 8192, i0 + 64, kb * kDeep, full_lead + 8 * s);
             }
           }
           if (load_b) {
@@ -551,6 +844,11 @@ __global__ void __launch_bounds__((GEN ? 16 : 12) * 32, 1)
       }
     }
     __syncwarp();
+  } else if (BOX && warp == 3) {
+    if (lane == 0)
+      box_traffic<MODE, FORM>(maps, k, g, patches, efull, edone, first, tiles, clusters, half,
+                              &dead);
+    __syncwarp();
   } else if (warp >= kEpiWarp0 && warp < kEpiWarp0 + kEpiWarps) {
     const int w = (warp - kEpiWarp0) & 3, set = (warp - kEpiWarp0) >> 2;  // lanes 32 w...
     const uint32_t tempty_lead = remote(tempty, leader);
@@ -558,7 +856,7 @@ __global__ void __launch_bounds__((GEN ? 16 : 12) * 32, 1)
     const uint64_t offset =
         MODE == LIN_FORWARD && k.epi.drop.on ? drop_offset(k.epi.drop) : 0ull;
     const uint32_t mine = patches + (uint32_t)(warp - kEpiWarp0) * kPatch * 4;
-    uint32_t acc = 0, aph = 0;
+    uint32_t acc = 0, aph = 0, eb = 0, eph = 0;
     bool ok = true;
     for (int t = first; t < tiles && ok; t += clusters) {
       int ti, tj;
@@ -570,6 +868,36 @@ __global__ void __launch_bounds__((GEN ? 16 : 12) * 32, 1)
       const int64_t i0 = (int64_t)ti * 256 + half * kRowsCta + w * 32;
       const int chunks = tj >= 0 ? g.bn / 32 : 1;
       const uint32_t d = tmem + acc * g.bn + ((uint32_t)(w * 32) << 16);
+      if (BOX && tj >= 0) {
+        const int64_t left = k.cols - (int64_t)tj * g.bn;
+        const int count = (int)((left < g.bn ? left : g.bn) + kWidth - 1) / kWidth;
+        for (int cc = 0; cc < count; ++cc) {
+          const uint32_t b = eb, bph = eph;
+          if (++eb == (uint32_t)g.boxes) {
+            eb = 0;
+            eph ^= 1;
+          }
+          if (kWidth == 32 && (cc & 1) != set) continue;
+          const int inner = kWidth == 64 ? set * 32 : 0;
+          uint32_t r[32];
+          tmem_load32(d + cc * kWidth + inner, r);
+          if (kb1 == kb0) {
+#pragma unroll
+            for (int q = 0; q < 32; ++q) r[q] = 0;  // an empty contraction
+          }
+          ok = bar_wait(efull + 8 * b, bph, &dead);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const int row = w * 32 + lane;
+          box_chunk<MODE, FORM>(k.epi, offset,
+                                patches + b * (kSlot * (g.two_slots ? 2 : 1)), g.two_slots, row,
+                                i0 + lane, (int64_t)tj * g.bn + cc * kWidth + inner, set * 4,
+                                k.cols, r);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) bar_arrive(edone + 8 * b);
+        }
+      } else
       for (int cc = set; cc < chunks; cc += 2) {
         const int64_t j0 = (int64_t)tj * g.bn + cc * 32;
         if (S == 1 && tj >= 0 && (i0 >= k.rows || j0 >= k.cols)) continue;
@@ -584,8 +912,8 @@ __global__ void __launch_bounds__((GEN ? 16 : 12) * 32, 1)
         }
         const uint32_t patch = S == 1 ? mine : ring + (uint32_t)(cc * 4 + w) * kPatch * 4;
         if (S == 1 && MODE == LIN_DWEIGHT && tj < 0) {
-          const int64_t i = i0 + lane;
-          if (i < k.rows && in_extent(i, i + 1, 0, k.rows, ZERO_SITE_LINEAR_OUT)) {
+          const int64_t i = i0 + lane, n = g.bias_b ? k.cols : k.rows;
+          if (i < n && in_extent(i, i + 1, 0, n, ZERO_SITE_LINEAR_OUT)) {
             float v = __uint_as_float(r[0]);
             if (k.epi.accumulate) v += load1(k.dbias, i);
             store1(k.dbias, i, v);
@@ -631,8 +959,12 @@ __global__ void __launch_bounds__((GEN ? 16 : 12) * 32, 1)
         if (!ok) break;
         const uint32_t a_at = ring + s * stage_bytes, b_at = a_at + kBytesA;
         const int64_t c0 = (int64_t)kb * kDeep;
-        if (g.gen_a)
+        if (tj < 0 && g.bias_b) {
+          if (g.gen_b)
+            gen_operand(g.gen_b, k.b, b_c, k.cols, k.depth, i0, kRowsCta, c0, a_at, t128);
+        } else if (g.gen_a) {
           gen_operand(g.gen_a, k.a, a_c, k.rows, k.depth, i0, kRowsCta, c0, a_at, t128);
+        }
         if (g.gen_b && tj >= 0)
           gen_operand(g.gen_b, k.b, b_c, k.cols, k.depth, j0, g.bn / 2, c0, b_at, t128);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -663,8 +995,8 @@ __global__ void __launch_bounds__((GEN ? 16 : 12) * 32, 1)
         const int64_t j0 = (int64_t)tj * g.bn + (b >> 2) * 32;
         const uint32_t patch = ring + (uint32_t)b * kPatch * 4;
         if (MODE == LIN_DWEIGHT && tj < 0) {
-          const int64_t i = i0 + lane;
-          if (i < k.rows && in_extent(i, i + 1, 0, k.rows, ZERO_SITE_LINEAR_OUT)) {
+          const int64_t i = i0 + lane, n = g.bias_b ? k.cols : k.rows;
+          if (i < n && in_extent(i, i + 1, 0, n, ZERO_SITE_LINEAR_OUT)) {
             const uint32_t at = patch + (k.out_t ? lane : lane * 36) * 4;
             float v = 0.0f;
             for (int p = 0; p < S; ++p) {
@@ -728,31 +1060,54 @@ static int gen_width(const Mat& a, int64_t lines) {
   return 1;
 }
 
-static bool make_map(CUtensorMap* map, const Mat& a, bool contig, int64_t rows, int64_t depth,
-                     int box_rows) {
+static bool encode(CUtensorMap* map, bool f32, void* p, int64_t inner, int64_t outer, int64_t ld,
+                   int box_x, int box_y, CUtensorMapSwizzle swizzle) {
   EncodeFn fn = encode_fn();
   if (!fn) return false;
-  const int64_t inner = contig ? depth : rows, outer = contig ? rows : depth;
+  const int es = f32 ? 4 : 2;
   const cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
+  // a single line has no distance to the next: any multiple of 16 bytes will do
   const cuuint64_t strides[1] = {
-      (cuuint64_t)(outer > 1 ? a.ld * 2 : (inner * 2 + 15) / 16 * 16)};
-  const cuuint32_t box[2] = {64, (cuuint32_t)(contig ? box_rows : kDeep)};
+      (cuuint64_t)(outer > 1 ? ld * es : (inner * es + 15) / 16 * 16)};
+  const cuuint32_t box[2] = {(cuuint32_t)box_x, (cuuint32_t)box_y};
   const cuuint32_t one[2] = {1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.p, dims, strides, box, one,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  return fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p,
+            dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-static int stages_for(int bn, int splits) {
-  const int stage = kBytesA + bn * kDeep;
-  const int rest = 1024 + kOnesBytes + 1024 + (splits == 1 ? kEpiWarps * kPatch * 4 : 0);
-  const int n = (kSmemMost - rest) / stage;
+// An operand's tiles: 64 deep x box_rows, or blocks of 64 rows x 64 deep.
+static bool operand_map(CUtensorMap* map, const Mat& a, bool contig, int64_t rows, int64_t depth,
+                        int box_rows) {
+  return contig ? encode(map, false, a.p, depth, rows, a.ld, kDeep, box_rows,
+                         CU_TENSOR_MAP_SWIZZLE_128B)
+                : encode(map, false, a.p, rows, depth, a.ld, 64, kDeep,
+                         CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// A side operand's or output's boxes of `width` columns x 128 rows.
+static bool box_map(CUtensorMap* map, const Mat& a, int64_t rows, int64_t cols, int width) {
+  if (!a.p) return true;
+  const bool f32 = a.dtype == ZERO_F32;
+  return encode(map, f32, a.p, cols, rows, a.ld, width, kRowsCta,
+                width * (f32 ? 4 : 2) == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                             : CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
+// Shared memory beside the operand ring, and the ring's stages in what is left.
+static int side_bytes(const TileK& g, int form) {
+  return (g.bias_tiles ? kOnesBytes : 0) + (form >= BOX_BF16 ? g.boxes * kSlot * (g.two_slots ? 2 : 1)
+                       : g.splits == 1 ? kEpiWarps * kPatch * 4 : 0);
+}
+static int stages_for(const TileK& g, int form) {
+  const int n = (kSmemMost - 1024 - side_bytes(g, form)) / (kBytesA + g.bn * kDeep);
   return n < kMaxStages ? n : kMaxStages;
 }
 
-template <int MODE, bool GEN>
-static cudaError_t launch_tiles(const CUtensorMap& ma, const CUtensorMap& mb, const ProductK& k,
-                                const TileK& g, cudaStream_t st) {
+template <int MODE, int FORM>
+static cudaError_t launch_tiles(const CUtensorMap& ma, const CUtensorMap& mb,
+                                const BoxMaps& maps, const ProductK& k, TileK& g,
+                                cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -760,19 +1115,19 @@ static cudaError_t launch_tiles(const CUtensorMap& ma, const CUtensorMap& mb, co
   const unsigned long long bit = 1ull << (dev & 63);
   constexpr int most = kSmemMost - 1024;  // the rest is the kernel's static shared memory
   if (!(done.load() & bit)) {
-    e = cudaFuncSetAttribute(product_kernel<MODE, GEN>,
+    e = cudaFuncSetAttribute(product_kernel<MODE, FORM>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return e;
     done.fetch_or(bit);
   }
+  g.stages = stages_for(g, FORM);
   const int64_t tiles = (int64_t)g.tiles_i * g.tiles_j + g.bias_tiles;
   const int64_t pairs = sm_count() / 2;
   const int64_t clusters = g.splits > 1 || tiles < pairs ? tiles : pairs;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(clusters * 2 * g.splits));
-  cfg.blockDim = dim3((GEN ? 16 : 12) * 32);
-  cfg.dynamicSmemBytes = (size_t)g.stages * (kBytesA + g.bn * kDeep) + kOnesBytes +
-                         (g.splits == 1 ? kEpiWarps * kPatch * 4 : 0);
+  cfg.blockDim = dim3((FORM == PATCH_GEN ? 16 : 12) * 32);
+  cfg.dynamicSmemBytes = (size_t)g.stages * (kBytesA + g.bn * kDeep) + side_bytes(g, FORM);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -780,7 +1135,16 @@ static cudaError_t launch_tiles(const CUtensorMap& ma, const CUtensorMap& mb, co
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, product_kernel<MODE, GEN>, ma, mb, k, g);
+  return cudaLaunchKernelEx(&cfg, product_kernel<MODE, FORM>, ma, mb, maps, k, g);
+}
+
+// Whether a side matrix can move in boxes: absent, or on 16-byte boundaries.
+// A store writes whole 16-byte units, so an output's rows must end with one.
+static bool boxable(const Mat& a, int64_t rows) {
+  return !a.p || a.vec || (rows == 1 && ((uintptr_t)a.p & 15) == 0);
+}
+static bool box_output(const Mat& a, int64_t rows, int64_t cols) {
+  return boxable(a, rows) && (!a.p || (cols * (a.dtype == ZERO_F32 ? 4 : 2)) % 16 == 0);
 }
 
 template <int MODE>
@@ -824,28 +1188,55 @@ static cudaError_t launch_mode(const ProductK& in, cudaStream_t st) {
       }
     }
   }
-  if (tiles_i * (g.tiles_j + 1) >= (1ll << 28) || kblocks >= (1ll << 30)) return cudaErrorInvalidValue;
+  g.bias_b = k.dbias.p && k.bias_b;
+  const int64_t bias_rows = !k.dbias.p ? 0 : g.bias_b ? k.cols : k.rows;
+  if (tiles_i * (g.tiles_j + 1) >= (1ll << 28) || kblocks >= (1ll << 30))
+    return cudaErrorInvalidValue;
   g.tiles_i = (int)tiles_i;
   g.kblocks = (int)kblocks;
-  g.stages = stages_for(g.bn, g.splits);
-  g.bias_tiles = k.dbias.p ? g.tiles_i : 0;
+  g.bias_tiles = (int)((bias_rows + 255) / 256);
   g.i_fast = k.rows <= k.cols;
   g.tmem_cols = 2 * g.bn;
   CUtensorMap ma{}, mb{};
+  BoxMaps maps{};
   if (k.depth > 0) {
-    g.gen_a = gen_width(k.a, k.a_c ? k.rows : k.depth);
+    g.gen_a = k.rows > 0 ? gen_width(k.a, k.a_c ? k.rows : k.depth) : 0;
     g.gen_b = k.cols > 0 ? gen_width(k.b, k.b_c ? k.cols : k.depth) : 0;
-    if (!g.gen_a && !make_map(&ma, k.a, k.a_c, k.rows, k.depth, kRowsCta))
+    if (!g.gen_a && k.rows > 0 &&
+        !operand_map(&ma, k.a, k.a_c, k.rows, k.depth, kRowsCta))
       return cudaErrorInvalidValue;
-    if (!g.gen_b && k.cols > 0 && !make_map(&mb, k.b, k.b_c, k.cols, k.depth, g.bn / 2))
+    if (!g.gen_b && k.cols > 0 &&
+        !operand_map(&mb, k.b, k.b_c, k.cols, k.depth, g.bn / 2))
       return cudaErrorInvalidValue;
   }
-  if (g.gen_a || g.gen_b) return launch_tiles<MODE, true>(ma, mb, k, g, st);
-  return launch_tiles<MODE, false>(ma, mb, k, g, st);
+  if (g.gen_a || g.gen_b) return launch_tiles<MODE, PATCH_GEN>(ma, mb, maps, k, g, st);
+  const EpiK& o = k.epi;
+  const bool pre_ok = MODE == LIN_FORWARD ? box_output(o.pre, k.rows, k.cols)
+                                          : boxable(o.pre, k.rows);
+  if (k.out_t || g.splits > 1 || k.rows <= 0 || k.cols <= 0 || !pre_ok ||
+      !box_output(o.out, k.rows, k.cols) || !boxable(o.gate, k.rows) ||
+      !box_output(o.dgate, k.rows, k.cols) ||
+      !boxable(o.residual, k.rows) || (o.residual.p && o.residual.dtype != o.out.dtype))
+    return launch_tiles<MODE, PATCH>(ma, mb, maps, k, g, st);
+  const bool wide = o.out.dtype == ZERO_F32;
+  const int width = wide ? 32 : 64;
+  const Mat& extra = MODE == LIN_FORWARD ? o.residual : o.dgate;
+  if (!box_map(&maps.out, o.out, k.rows, k.cols, width) ||
+      !box_map(&maps.pre, o.pre, k.rows, k.cols, width) ||
+      !box_map(&maps.gate, o.gate, k.rows, k.cols, width) ||
+      !box_map(&maps.extra, extra, k.rows, k.cols, width))
+    return cudaErrorInvalidValue;
+  g.two_slots = MODE == LIN_FORWARD ? o.gate.p || o.pre.p
+                : MODE == LIN_DINPUT ? o.gate.p || (wide && o.pre.p)
+                                     : 0;
+  g.boxes = kMostBoxes;
+  if (wide) return launch_tiles<MODE, BOX_F32>(ma, mb, maps, k, g, st);
+  return launch_tiles<MODE, BOX_BF16>(ma, mb, maps, k, g, st);
 }
 
 cudaError_t launch_product(const ProductK& k, int mode, cudaStream_t st) {
-  if (k.rows <= 0 || (k.cols <= 0 && !k.dbias.p)) return cudaSuccess;
+  const int64_t sums = !k.dbias.p ? 0 : k.bias_b ? k.cols : k.rows;
+  if ((k.rows <= 0 || k.cols <= 0) && sums <= 0) return cudaSuccess;
   if (mode == LIN_FORWARD) return launch_mode<LIN_FORWARD>(k, st);
   if (mode == LIN_DINPUT) return launch_mode<LIN_DINPUT>(k, st);
   return launch_mode<LIN_DWEIGHT>(k, st);

@@ -57,9 +57,10 @@ struct EpiK {
 struct ProductK {
   Mat a, b;
   int a_c = 1, b_c = 1, out_t = 0;
+  int bias_b = 0;  // dbias sums B's rows (else A's)
   int64_t rows = 0, cols = 0, depth = 0;
   EpiK epi;
-  Mat dbias;  // dweight: [rows] sums of A over c
+  Mat dbias;  // dweight: sums over c of the rows of A or B
 };
 
 cudaError_t launch_product(const ProductK& k, int mode, cudaStream_t st);

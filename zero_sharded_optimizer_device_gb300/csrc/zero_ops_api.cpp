@@ -182,13 +182,15 @@ extern "C" int zero_linear_dweight(const void* dy, int64_t lddy, const void* x, 
   p.epi.out = mat(dw, lddw, dwdtype);
   p.epi.accumulate = accumulate != 0;
   if (dbias) p.dbias = mat(dbias, 0, dbdtype);
-  p.a = mat(dy, lddy, ZERO_BF16);
-  p.b = mat(x, ldx, ZERO_BF16);
+  // rows of dw are the product's rows in either layout
+  const zk::Mat d = mat(dy, lddy, ZERO_BF16), in = mat(x, ldx, ZERO_BF16);
+  p.a = nk ? d : in;
+  p.b = nk ? in : d;
   p.a_c = 0;
   p.b_c = 0;
-  p.out_t = !nk;
-  p.rows = n;
-  p.cols = k;
+  p.rows = nk ? n : k;
+  p.cols = nk ? k : n;
+  p.bias_b = !nk;
   p.depth = m;
   return cuda_status(zk::launch_product(p, zk::LIN_DWEIGHT, (cudaStream_t)stream));
 }
