@@ -45,7 +45,7 @@ constexpr int kOnesBytes = 2048;
 constexpr int kSlot = 16384;           // a box of 128 rows of 128 bytes
 constexpr int kMostBoxes = 3;          // chunks of boxes in the ring
 constexpr int kSmemMost = 232448;      // shared memory one CTA may have
-constexpr unsigned long long kWaitNs = 2000000000ull;
+constexpr long long kWaitCycles = 4000000000ll;  // about 2 s; bounds every wait
 
 static __device__ unsigned long long g_ops_timeouts;
 
@@ -78,11 +78,6 @@ struct BoxMaps {
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return (uint32_t)__cvta_generic_to_shared(p);
 }
-__device__ __forceinline__ uint64_t now_ns() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
-}
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -110,14 +105,14 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
       : "memory");
   return done;
 }
-// Wait for the phase of this parity.  Gives up after kWaitNs, or once another
+// Wait for the phase of this parity.  Gives up after kWaitCycles, or once another
 // role of the CTA has (*dead), counts the first giving up and returns false:
 // the role then leaves its loop, and the kernel returns.
 __device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, volatile int* dead) {
-  const uint64_t t0 = now_ns();
+  const long long t0 = clock64();
   while (!bar_try(bar, parity)) {
     if (*dead) return false;
-    if (now_ns() - t0 > kWaitNs) {
+    if (clock64() - t0 > kWaitCycles) {
       *dead = 1;
       atomicAdd(&g_ops_timeouts, 1ull);
       return false;
@@ -672,8 +667,8 @@ __device__ __forceinline__ void box_traffic(const BoxMaps& maps, const ProductK&
   }
   // after a wait that gave up: the boxes in flight land before the CTA returns
   for (; stored < loaded; ++stored) {
-    const uint64_t t0 = now_ns();
-    while (!bar_try(efull + 8 * sb, sph) && now_ns() - t0 < kWaitNs / 8) {
+    const long long t0 = clock64();
+    while (!bar_try(efull + 8 * sb, sph) && clock64() - t0 < kWaitCycles / 8) {
     }
     if (++sb == (uint32_t)g.boxes) {
       sb = 0;
@@ -707,6 +702,13 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
   const uint32_t tfull = empty + 8 * kMaxStages, tempty = tfull + 16;
   const uint32_t efull = tempty + 16, edone = efull + 8 * kMostBoxes;
 
+  // the next kernel on the stream may set up while this one runs
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (warp == 1 && lane == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&map_a) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&map_b) : "memory");
+    if (BOX) asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.out) : "memory");
+  }
   if (warp == 0 && lane == 0) {
     dead = 0;
     for (int s = 0; s < g.stages; ++s) {
@@ -743,6 +745,8 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
   __syncthreads();
   cluster_sync();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  // what ran before this on the stream is done and its writes are visible
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const uint32_t tmem = *(volatile uint32_t*)&tmem_at;
 
   // this cluster's tiles, and this pair's share of the contraction
@@ -797,8 +801,8 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
       // (a ring slot holds at most one load; waits are again limited)
       if (!ok && half == 0)
         for (int q = 0; q < g.stages; ++q) {
-          const uint64_t t0 = now_ns();
-          while (!bar_try(full + 8 * q, ph) && now_ns() - t0 < kWaitNs / 8) {
+          const long long t0 = clock64();
+          while (!bar_try(full + 8 * q, ph) && clock64() - t0 < kWaitCycles / 8) {
           }
         }
     }
@@ -1129,12 +1133,14 @@ static cudaError_t launch_tiles(const CUtensorMap& ma, const CUtensorMap& mb,
   cfg.blockDim = dim3((FORM == PATCH_GEN ? 16 : 12) * 32);
   cfg.dynamicSmemBytes = (size_t)g.stages * (kBytesA + g.bn * kDeep) + side_bytes(g, FORM);
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2 * g.splits;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, product_kernel<MODE, FORM>, ma, mb, maps, k, g);
 }
 
