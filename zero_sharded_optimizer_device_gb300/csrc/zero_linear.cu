@@ -92,13 +92,27 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 }
+// One lane of a converged warp, always the same.  Roles that issue from one
+// lane still run their loops on the whole warp: only then do addresses and
+// counters live in uniform registers, from which TMA and the tensor cores
+// take their operands.  (A loop inside `if (lane == 0)` took ~650 cycles per
+// stage, more than a step's products.)
+__device__ __forceinline__ bool elect() {
+  uint32_t p;
+  asm volatile(
+      "{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }"
+      : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
+// Acquire at CTA scope: what crosses CTAs here goes through TMA, the tensor
+// cores and their fences.
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
-      "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; "
+      "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; "
       "selp.u32 %0, 1, 0, p; }"
       : "=r"(done)
       : "r"(bar), "r"(parity)
@@ -107,7 +121,8 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
 }
 // Wait for the phase of this parity.  Gives up after kWaitCycles, or once another
 // role of the CTA has (*dead), counts the first giving up and returns false:
-// the role then leaves its loop, and the kernel returns.
+// the role then goes through the rest of its loop without waiting or issuing
+// anything, and the kernel returns.
 __device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, volatile int* dead) {
   const long long t0 = clock64();
   while (!bar_try(bar, parity)) {
@@ -128,8 +143,12 @@ __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                : "memory");
 }
-// One arrival on a barrier of any CTA of the cluster.
+// One arrival on a barrier of any CTA of the cluster; `release`: what this
+// thread wrote by plain stores is visible there first.
 __device__ __forceinline__ void bar_arrive_cluster(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+__device__ __forceinline__ void bar_arrive_cluster_release(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
                : "memory");
 }
@@ -193,17 +212,19 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t r[32]) {
 }
 __device__ __forceinline__ void st_shared4(uint32_t addr, float a, float b, float c, float d) {
   asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "f"(a), "f"(b), "f"(c),
-               "f"(d)
-               : "memory");
+               "f"(d));
 }
 __device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
                : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
+               : "r"(addr));
   return v;
 }
+
+// Reads and writes of shared memory above are volatile, hence kept in order,
+// but do not clobber memory: a clobber makes the compiler fetch every kernel
+// parameter again at its next use, ~70 cycles each in a row.
 
 // Shared-memory descriptor of an operand tile in 128-byte swizzle rows.
 // Contiguous contraction: rows of 64 values, 8-row groups 1024 bytes apart.
@@ -358,7 +379,7 @@ __device__ __forceinline__ void finish8(const EpiK& k, uint64_t offset, int64_t 
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] += bias[j];
     if (k.pre.p) store8(k.pre, row, b.col, b.valid, v, e, site);
-    activate8(v, k.act);
+    activate<8>(v, k.act);
     if (k.gate.p) {
       from_bf16(p, f);
 #pragma unroll
@@ -374,7 +395,9 @@ __device__ __forceinline__ void finish8(const EpiK& k, uint64_t offset, int64_t 
     if (k.pre.p) {
       float value[8], slope[8];
       from_bf16(p, f);
-      activate_grad8(f, k.act, value, slope);
+      #pragma unroll
+      for (int j = 0; j < 8; ++j) value[j] = f[j];
+      activate_grad<8>(value, slope, k.act);
       if (k.gate.p) {
         from_bf16(q.a, f);
 #pragma unroll
@@ -401,8 +424,7 @@ __device__ __forceinline__ float4 ld_shared4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
                : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
+               : "r"(addr));
   return v;
 }
 
@@ -464,14 +486,12 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
   uint4 u;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
-               : "r"(addr)
-               : "memory");
+               : "r"(addr));
   return u;
 }
 __device__ __forceinline__ void sts16(uint32_t addr, uint4 u) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(u.x), "r"(u.y), "r"(u.z),
-               "r"(u.w)
-               : "memory");
+               "r"(u.w));
 }
 __device__ __forceinline__ void lds_f32(uint32_t base, int row, int i, float f[8]) {
   const uint4 a = lds16(base + at128(row, 2 * i)), b = lds16(base + at128(row, 2 * i + 1));
@@ -489,88 +509,148 @@ __device__ __forceinline__ void sts_f32(uint32_t base, int row, int i, const flo
                    __float_as_uint(f[7])));
 }
 
-// A thread's 32 sums of row `row` of the tile, columns col.. of the output,
-// through the epilogue; unit0: their first 16-byte unit in a bf16 row.
+// What the box form asks of the epilogue's parameters, read once per kernel.
+struct BoxEpi {
+  bool bias, gate, pre, residual, dgate, old;
+  int act;
+  DropK drop;
+  Mat b;
+};
+template <int MODE>
+__device__ __forceinline__ BoxEpi box_epi(const EpiK& k) {
+  BoxEpi e;
+  e.bias = MODE == LIN_FORWARD && k.bias.p;
+  e.gate = MODE != LIN_DWEIGHT && k.gate.p;
+  e.pre = MODE != LIN_DWEIGHT && k.pre.p;
+  e.residual = MODE == LIN_FORWARD && k.residual.p;
+  e.dgate = MODE == LIN_DINPUT && k.dgate.p;
+  e.old = MODE == LIN_DWEIGHT && k.accumulate;
+  e.act = k.act;
+  e.drop = k.drop;
+  e.b = k.bias;
+  return e;
+}
+
+// A thread's 32 sums v of row `row` of the tile, columns col.. of the output,
+// through the epilogue; unit0: their first 16-byte unit in a bf16 row.  Each
+// step runs over all 32 before the next: a branch per step, not per value.
 template <int MODE, int FORM>
-__device__ __forceinline__ void box_chunk(const EpiK& k, uint64_t offset, uint32_t chunk,
-                                          int two_slots, int row, int64_t out_row, int64_t col,
-                                          int unit0, int64_t cols, const uint32_t r[32]) {
+__device__ __forceinline__ void box_chunk(const BoxEpi& k, uint64_t offset, uint32_t chunk,
+                                          uint32_t second, int row, int64_t out_row, int64_t col,
+                                          int unit0, int64_t cols, float v[32]) {
   constexpr bool wide = FORM == BOX_F32;
-  const uint32_t slot1 = chunk + (two_slots ? kSlot : 0);
+  const uint32_t slot1 = chunk + second;
+  float f[8];
+  if constexpr (MODE == LIN_FORWARD) {
+    if (k.bias) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float v[8], f[8];
+      for (int i = 0; i < 4; ++i) {
+        const int64_t left = cols - col - 8 * i;
+        if (left > 0) {
+          load8(k.b, 0, col + 8 * i, left < 8 ? (int)left : 8, f, Extent{1, cols},
+                ZERO_SITE_LINEAR_OUT);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(r[8 * i + j]);
-    const int64_t c = col + 8 * i;
-    if constexpr (MODE == LIN_FORWARD) {
-      const uint32_t s0 = chunk + (wide ? at64(row, i) : at128(row, unit0 + i));
-      const uint32_t s1 = slot1 + at128(row, unit0 + i);
-      if (k.bias.p && c < cols) {
-        load8(k.bias, 0, c, cols - c < 8 ? (int)(cols - c) : 8, f, Extent{1, cols},
-              ZERO_SITE_LINEAR_OUT);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] += f[j];
+          for (int j = 0; j < 8; ++j) v[8 * i + j] += f[j];
+        }
       }
-      uint4 g;
-      if (k.gate.p) g = lds16(s0);
-      if (k.pre.p) sts16(s0, pack8(v));
-      activate8(v, k.act);
-      if (k.gate.p) {
-        from_bf16(g, f);
+    }
+    uint4 gate[4];
+    if (k.gate) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= f[j];
+      for (int i = 0; i < 4; ++i)
+        gate[i] = lds16(chunk + (wide ? at64(row, i) : at128(row, unit0 + i)));
+    }
+    if (k.pre) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        sts16(chunk + (wide ? at64(row, i) : at128(row, unit0 + i)), pack8(v + 8 * i));
+    }
+    activate<32>(v, k.act);
+    if (k.gate) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        from_bf16(gate[i], f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[8 * i + j] *= f[j];
       }
-      if (k.drop.on) drop8(k.drop, offset, (uint32_t)out_row, c, v);
-      if (k.residual.p) {
+    }
+    if (k.drop.on) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) drop8(k.drop, offset, (uint32_t)out_row, col + 8 * i, v + 8 * i);
+    }
+    if (k.residual) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
         if constexpr (wide)
           lds_f32(slot1, row, i, f);
         else
-          from_bf16(lds16(s1), f);
+          from_bf16(lds16(slot1 + at128(row, unit0 + i)), f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] += f[j];
+        for (int j = 0; j < 8; ++j) v[8 * i + j] += f[j];
       }
-      if constexpr (wide)
-        sts_f32(slot1, row, i, v);
-      else
-        sts16(s1, pack8(v));
-    } else if constexpr (MODE == LIN_DINPUT) {
-      const uint32_t pre_at = wide ? slot1 + at64(row, i) : chunk + at128(row, unit0 + i);
-      const uint32_t gate_at =
-          wide ? slot1 + kSlot / 2 + at64(row, i) : slot1 + at128(row, unit0 + i);
-      if (k.pre.p) {
-        float value[8], slope[8];
-        from_bf16(lds16(pre_at), f);
-        activate_grad8(f, k.act, value, slope);
-        if (k.gate.p) {
-          from_bf16(lds16(gate_at), f);
+    }
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            value[j] *= v[j];
-            slope[j] *= f[j];
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (wide)
+        sts_f32(slot1, row, i, v + 8 * i);
+      else
+        sts16(slot1 + at128(row, unit0 + i), pack8(v + 8 * i));
+    }
+  } else if constexpr (MODE == LIN_DINPUT) {
+    const uint32_t pre_at = wide ? slot1 : chunk, gate_at = wide ? slot1 + kSlot / 2 : slot1;
+    if (k.pre) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {  // 16 values at a time: three arrays of them are live
+        float value[16], slope[16];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          from_bf16(lds16(pre_at + (wide ? at64(row, 2 * h + i) : at128(row, unit0 + 2 * h + i))),
+                    value + 8 * i);
+        activate_grad<16>(value, slope, k.act);
+        float* w = v + 16 * h;
+        if (k.gate) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t at =
+                gate_at + (wide ? at64(row, 2 * h + i) : at128(row, unit0 + 2 * h + i));
+            from_bf16(lds16(at), f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              value[8 * i + j] *= w[8 * i + j];
+              slope[8 * i + j] *= f[j];
+            }
+            if (k.dgate) sts16(at, pack8(value + 8 * i));
           }
-          if (k.dgate.p) sts16(gate_at, pack8(value));
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= slope[j];
+        for (int j = 0; j < 16; ++j) w[j] *= slope[j];
       }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
       if constexpr (wide)
-        sts_f32(chunk, row, i, v);
+        sts_f32(chunk, row, i, v + 8 * i);
       else
-        sts16(chunk + at128(row, unit0 + i), pack8(v));
-    } else {
-      if (k.accumulate) {
+        sts16(chunk + at128(row, unit0 + i), pack8(v + 8 * i));
+    }
+  } else {
+    if (k.old) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
         if constexpr (wide)
           lds_f32(chunk, row, i, f);
         else
           from_bf16(lds16(chunk + at128(row, unit0 + i)), f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] += f[j];
+        for (int j = 0; j < 8; ++j) v[8 * i + j] += f[j];
       }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
       if constexpr (wide)
-        sts_f32(chunk, row, i, v);
+        sts_f32(chunk, row, i, v + 8 * i);
       else
-        sts16(chunk + at128(row, unit0 + i), pack8(v));
+        sts16(chunk + at128(row, unit0 + i), pack8(v + 8 * i));
     }
   }
 }
@@ -597,8 +677,8 @@ __device__ __forceinline__ void next_chunk(const TileK& g, int64_t cols, int til
   }
 }
 
-// Warp 3's thread: brings the side operands of up to g.boxes chunks ahead and
-// stores each chunk when the epilogue is done with it.
+// Warp 3: brings the side operands of up to g.boxes chunks ahead and stores
+// each chunk when the epilogue is done with it.
 template <int MODE, int FORM>
 __device__ __forceinline__ void box_traffic(const BoxMaps& maps, const ProductK& k,
                                             const TileK& g, uint32_t boxes, uint32_t efull,
@@ -606,71 +686,79 @@ __device__ __forceinline__ void box_traffic(const BoxMaps& maps, const ProductK&
                                             uint32_t half, volatile int* dead) {
   constexpr bool wide = FORM == BOX_F32;
   constexpr int W = wide ? 32 : 64;
-  const uint32_t chunk_bytes = kSlot * (g.two_slots ? 2 : 1);
+  const uint32_t ring = g.boxes, second = g.two_slots ? kSlot : 0, chunk_bytes = kSlot + second;
   constexpr uint32_t narrow = wide ? kSlot / 2 : kSlot;  // a bf16 box
-  const bool gate = MODE != LIN_DWEIGHT && k.epi.gate.p;
-  const bool res = MODE == LIN_FORWARD && k.epi.residual.p;
-  const bool pre_in = MODE == LIN_DINPUT && k.epi.pre.p;
-  const bool old = MODE == LIN_DWEIGHT && k.epi.accumulate;
-  const uint32_t bytes = (gate ? narrow : 0) + (res || old ? kSlot : 0) + (pre_in ? narrow : 0);
+  const BoxEpi e = box_epi<MODE>(k.epi);
+  const uint32_t bytes = (e.gate ? narrow : 0) + (e.residual || e.old ? kSlot : 0) +
+                         (MODE == LIN_DINPUT && e.pre ? narrow : 0);
+  const int64_t rows = k.rows, cols = k.cols;
+  const int bn = g.bn;
   ChunkWalk in, out;
   in.t = first;
   in.count = in.cc = 0;
   if (first < tiles) {
-    enter_tile<W>(g, k.cols, in);
+    enter_tile<W>(g, cols, in);
     in.cc = -1;
-    next_chunk<W>(g, k.cols, tiles, step, in);
+    next_chunk<W>(g, cols, tiles, step, in);
   }
   out = in;
-  uint32_t loaded = 0, stored = 0, lb = 0, sb = 0, sph = 0;
+  uint32_t ahead = 0, lb = 0, sb = 0, sph = 0;  // ahead: chunks loaded and not yet stored
+  bool live = true;
   while (out.t < tiles) {
-    while (in.t < tiles && loaded < stored + g.boxes) {
-      const uint32_t at = boxes + lb * chunk_bytes, slot1 = at + (g.two_slots ? kSlot : 0);
+    while (in.t < tiles && ahead < ring) {
+      const uint32_t at = boxes + lb * chunk_bytes, slot1 = at + second;
       const uint32_t bar = efull + 8 * lb;
-      const int x = in.tj * g.bn + in.cc * W, y = in.ti * 256 + (int)half * kRowsCta;
-      bar_expect(bar, bytes);
-      if constexpr (MODE == LIN_FORWARD) {
-        if (gate) box_load(&maps.gate, at, x, y, bar);
-        if (res) box_load(&maps.extra, slot1, x, y, bar);
-      } else if constexpr (MODE == LIN_DINPUT) {
-        if (pre_in) box_load(&maps.pre, wide ? slot1 : at, x, y, bar);
-        if (gate) box_load(&maps.gate, wide ? slot1 + kSlot / 2 : slot1, x, y, bar);
-      } else {
-        if (old) box_load(&maps.out, at, x, y, bar);
+      const int x = in.tj * bn + in.cc * W, y = in.ti * 256 + (int)half * kRowsCta;
+      if (elect() && live) {
+        bar_expect(bar, bytes);
+        if constexpr (MODE == LIN_FORWARD) {
+          if (e.gate) box_load(&maps.gate, at, x, y, bar);
+          if (e.residual) box_load(&maps.extra, slot1, x, y, bar);
+        } else if constexpr (MODE == LIN_DINPUT) {
+          if (e.pre) box_load(&maps.pre, wide ? slot1 : at, x, y, bar);
+          if (e.gate) box_load(&maps.gate, wide ? slot1 + kSlot / 2 : slot1, x, y, bar);
+        } else {
+          if (e.old) box_load(&maps.out, at, x, y, bar);
+        }
       }
-      ++loaded;
-      if (++lb == (uint32_t)g.boxes) lb = 0;
-      next_chunk<W>(g, k.cols, tiles, step, in);
+      __syncwarp();
+      ++ahead;
+      if (++lb == ring) lb = 0;
+      next_chunk<W>(g, cols, tiles, step, in);
     }
-    if (!bar_wait(edone + 8 * sb, sph, dead)) break;
-    const uint32_t at = boxes + sb * chunk_bytes, slot1 = at + (g.two_slots ? kSlot : 0);
-    const int x = out.tj * g.bn + out.cc * W, y = out.ti * 256 + (int)half * kRowsCta;
-    if (y < k.rows) {
-      if constexpr (MODE == LIN_FORWARD) {
-        if (k.epi.pre.p) box_store(&maps.pre, at, x, y);
-        box_store(&maps.out, slot1, x, y);
-      } else if constexpr (MODE == LIN_DINPUT) {
-        if (k.epi.dgate.p) box_store(&maps.extra, wide ? slot1 + kSlot / 2 : slot1, x, y);
-        box_store(&maps.out, at, x, y);
-      } else {
-        box_store(&maps.out, at, x, y);
+    live = live && bar_wait(edone + 8 * sb, sph, dead);
+    const uint32_t at = boxes + sb * chunk_bytes, slot1 = at + second;
+    const int x = out.tj * bn + out.cc * W, y = out.ti * 256 + (int)half * kRowsCta;
+    if (elect() && live) {
+      if (y < rows) {
+        if constexpr (MODE == LIN_FORWARD) {
+          if (e.pre) box_store(&maps.pre, at, x, y);
+          box_store(&maps.out, slot1, x, y);
+        } else if constexpr (MODE == LIN_DINPUT) {
+          if (e.dgate) box_store(&maps.extra, wide ? slot1 + kSlot / 2 : slot1, x, y);
+          box_store(&maps.out, at, x, y);
+        } else {
+          box_store(&maps.out, at, x, y);
+        }
       }
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+      asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
     }
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-    ++stored;
-    if (++sb == (uint32_t)g.boxes) {
+    __syncwarp();
+    if (!live) break;
+    --ahead;
+    if (++sb == ring) {
       sb = 0;
       sph ^= 1;
     }
-    next_chunk<W>(g, k.cols, tiles, step, out);
+    next_chunk<W>(g, cols, tiles, step, out);
   }
   // after a wait that gave up: the boxes in flight land before the CTA returns
-  for (; stored < loaded; ++stored) {
+  for (; ahead > 0; --ahead) {
     const long long t0 = clock64();
     while (!bar_try(efull + 8 * sb, sph) && clock64() - t0 < kWaitCycles / 8) {
     }
-    if (++sb == (uint32_t)g.boxes) {
+    if (++sb == ring) {
       sb = 0;
       sph ^= 1;
     }
@@ -757,58 +845,63 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
   const bool a_c = k.a_c, b_c = k.b_c;
 
   if (warp == 0) {
-    if (lane == 0) {
-      const uint32_t full_lead = remote(full, leader);
-      uint32_t s = 0, ph = 0;
-      bool ok = true;
-      for (int t = first; t < tiles && ok; t += clusters) {
-        int ti, tj;
-        tile_at(g, t, ti, tj);
-        const int i0 = ti * 256 + (int)half * kRowsCta;
-        const int j0 = tj * g.bn + (int)half * (g.bn / 2);
-        const bool load_a = tj < 0 && g.bias_b ? g.gen_b == 0 : g.gen_a == 0;
-        const bool load_b = g.gen_b == 0 && tj >= 0;
-        const CUtensorMap* map_i = tj < 0 && g.bias_b ? &map_b : &map_a;
-        const uint32_t bytes =
-            2 * ((load_a ? kBytesA : 0) + (load_b ? (uint32_t)g.bn * kDeep : 0));
-        for (int kb = kb0; kb < kb1; ++kb) {
-          ok = bar_wait(empty + 8 * s, ph ^ 1, &dead);
-          if (!ok) break;
+    const uint32_t full_lead = remote(full, leader);
+    const uint32_t stages = g.stages, b_bytes = (uint32_t)g.bn * kDeep;
+    const int bn = g.bn, blocks_b = bn / 128;
+    const bool tma_a = g.gen_a == 0, tma_b = g.gen_b == 0, bias_b = g.bias_b;
+    uint32_t s = 0, ph = 0;
+    bool live = true;
+    for (int t = first; t < tiles; t += clusters) {
+      int ti, tj;
+      tile_at(g, t, ti, tj);
+      const int i0 = ti * 256 + (int)half * kRowsCta;
+      const int j0 = tj * bn + (int)half * (bn / 2);
+      const bool load_a = tj < 0 && bias_b ? tma_b : tma_a;
+      const bool load_b = tma_b && tj >= 0;
+      const CUtensorMap* map_i = tj < 0 && bias_b ? &map_b : &map_a;
+      const uint32_t bytes = 2 * ((load_a ? kBytesA : 0) + (load_b ? b_bytes : 0));
+      for (int kb = kb0; kb < kb1; ++kb) {
+        live = live && bar_wait(empty + 8 * s, ph ^ 1, &dead);
+        const uint32_t a_at = ring + s * stage_bytes, b_at = a_at + kBytesA;
+        const uint32_t bar = full_lead + 8 * s;
+        const int c = kb * kDeep;
+        if (elect() && live) {
           if (half == 0) bar_expect(full + 8 * s, bytes);
-          const uint32_t a_at = ring + s * stage_bytes, b_at = a_at + kBytesA;
           if (load_a) {
             if (a_c) {
-              tma_load(map_i, a_at, kb * kDeep, i0, full_lead + 8 * s);
+              tma_load(map_i, a_at, c, i0, bar);
             } else {
-              tma_load(map_i, a_at, i0, kb * kDeep, full_lead + 8 * s);
-              tma_load(map_i, a_at + 8192, i0 + 64, kb * kDeep, full_lead + 8 * s);
+              tma_load(map_i, a_at, i0, c, bar);
+              tma_load(map_i, a_at + 8192, i0 + 64, c, bar);
             }
           }
           if (load_b) {
-            if (b_c)
-              tma_load(&map_b, b_at, kb * kDeep, j0, full_lead + 8 * s);
-            else
-              for (int q = 0; q < g.bn / 128; ++q)
-                tma_load(&map_b, b_at + q * 8192, j0 + q * 64, kb * kDeep, full_lead + 8 * s);
+            if (b_c) {
+              tma_load(&map_b, b_at, c, j0, bar);
+            } else {
+              tma_load(&map_b, b_at, j0, c, bar);
+              if (blocks_b > 1) tma_load(&map_b, b_at + 8192, j0 + 64, c, bar);
+            }
           }
-          if (++s == (uint32_t)g.stages) {
-            s = 0;
-            ph ^= 1;
-          }
+        }
+        __syncwarp();
+        if (++s == stages) {
+          s = 0;
+          ph ^= 1;
         }
       }
-      // a wait gave up: let the loads in flight land before the CTAs return
-      // (a ring slot holds at most one load; waits are again limited)
-      if (!ok && half == 0)
-        for (int q = 0; q < g.stages; ++q) {
-          const long long t0 = clock64();
-          while (!bar_try(full + 8 * q, ph) && clock64() - t0 < kWaitCycles / 8) {
-          }
-        }
     }
+    // a wait gave up: let the loads in flight land before the CTAs return
+    // (a ring slot holds at most one load; waits are again limited)
+    if (!live && half == 0)
+      for (uint32_t q = 0; q < stages; ++q) {
+        const long long t0 = clock64();
+        while (!bar_try(full + 8 * q, ph) && clock64() - t0 < kWaitCycles / 8) {
+        }
+      }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0 && half == 0) {
+    if (half == 0) {
       const uint16_t mask = (uint16_t)(3u << leader);
       // fp32 sums of bf16 values, M = 256; N = bn, or 32 columns of ones
       const uint32_t base = (1u << 4) | (1u << 7) | (1u << 10) | ((a_c ? 0u : 1u) << 15) |
@@ -816,42 +909,45 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
       const uint32_t idesc_n = base | ((b_c ? 0u : 1u) << 16) | ((uint32_t)(g.bn >> 3) << 17);
       const uint32_t idesc_1 = base | (4u << 17);
       const uint32_t step_a = a_c ? 2 : 128, step_b = b_c ? 2 : 128;  // 16 deep, in 16 bytes
+      const uint32_t stages = g.stages, bn = g.bn;
       uint32_t s = 0, ph = 0, acc = 0, aph = 0;
-      bool ok = true;
-      for (int t = first; t < tiles && ok; t += clusters) {
+      bool live = true;
+      for (int t = first; t < tiles; t += clusters) {
         int ti, tj;
         tile_at(g, t, ti, tj);
-        ok = bar_wait(tempty + 8 * acc, aph ^ 1, &dead);
-        if (!ok) break;
+        live = live && bar_wait(tempty + 8 * acc, aph ^ 1, &dead);
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint32_t d = tmem + acc * g.bn;
+        const uint32_t d = tmem + acc * bn;
+        const uint32_t idesc = tj >= 0 ? idesc_n : idesc_1, sb = tj >= 0 ? step_b : 0;
         for (int kb = kb0; kb < kb1; ++kb) {
-          ok = bar_wait(full + 8 * s, ph, &dead);
-          if (!ok) break;
+          live = live && bar_wait(full + 8 * s, ph, &dead);
+          if (GEN) asm volatile("fence.acq_rel.cluster;" ::: "memory");
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           const uint32_t a_at = ring + s * stage_bytes;
           const uint64_t da = operand_desc(a_at, a_c);
           const uint64_t db = tj >= 0 ? operand_desc(a_at + kBytesA, b_c)
                                       : operand_desc(ones, true);
-          const uint32_t idesc = tj >= 0 ? idesc_n : idesc_1, sb = tj >= 0 ? step_b : 0;
+          if (elect() && live) {
 #pragma unroll
-          for (int q = 0; q < kDeep / 16; ++q)
-            mma_pair(d, da + q * step_a, db + q * sb, idesc, kb > kb0 || q > 0);
-          commit_pair(empty + 8 * s, mask);
-          if (++s == (uint32_t)g.stages) {
+            for (int q = 0; q < kDeep / 16; ++q)
+              mma_pair(d, da + q * step_a, db + q * sb, idesc, kb > kb0 || q > 0);
+            commit_pair(empty + 8 * s, mask);
+          }
+          __syncwarp();
+          if (++s == stages) {
             s = 0;
             ph ^= 1;
           }
         }
-        if (ok) commit_pair(tfull + 8 * acc, mask);
+        if (elect() && live) commit_pair(tfull + 8 * acc, mask);
+        __syncwarp();
         if ((acc ^= 1) == 0) aph ^= 1;
       }
     }
     __syncwarp();
   } else if (BOX && warp == 3) {
-    if (lane == 0)
-      box_traffic<MODE, FORM>(maps, k, g, patches, efull, edone, first, tiles, clusters, half,
-                              &dead);
+    box_traffic<MODE, FORM>(maps, k, g, patches, efull, edone, first, tiles, clusters, half,
+                            &dead);
     __syncwarp();
   } else if (warp >= kEpiWarp0 && warp < kEpiWarp0 + kEpiWarps) {
     const int w = (warp - kEpiWarp0) & 3, set = (warp - kEpiWarp0) >> 2;  // lanes 32 w...
@@ -860,6 +956,12 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
     const uint64_t offset =
         MODE == LIN_FORWARD && k.epi.drop.on ? drop_offset(k.epi.drop) : 0ull;
     const uint32_t mine = patches + (uint32_t)(warp - kEpiWarp0) * kPatch * 4;
+    const BoxEpi be = box_epi<MODE>(k.epi);
+    const bool empty_sum = kb1 == kb0, out_t = k.out_t;
+    const uint32_t boxes = g.boxes, boxes0 = patches, second = g.two_slots ? kSlot : 0,
+                   chunk_bytes = kSlot + second;
+    const int bn = g.bn;
+    const int64_t cols = k.cols, rows = k.rows;
     uint32_t acc = 0, aph = 0, eb = 0, eph = 0;
     bool ok = true;
     for (int t = first; t < tiles && ok; t += clusters) {
@@ -870,14 +972,14 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
       if (!ok) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const int64_t i0 = (int64_t)ti * 256 + half * kRowsCta + w * 32;
-      const int chunks = tj >= 0 ? g.bn / 32 : 1;
-      const uint32_t d = tmem + acc * g.bn + ((uint32_t)(w * 32) << 16);
+      const int chunks = tj >= 0 ? bn / 32 : 1;
+      const uint32_t d = tmem + acc * bn + ((uint32_t)(w * 32) << 16);
       if (BOX && tj >= 0) {
-        const int64_t left = k.cols - (int64_t)tj * g.bn;
-        const int count = (int)((left < g.bn ? left : g.bn) + kWidth - 1) / kWidth;
+        const int64_t left = cols - (int64_t)tj * bn;
+        const int count = (int)((left < bn ? left : bn) + kWidth - 1) / kWidth;
         for (int cc = 0; cc < count; ++cc) {
           const uint32_t b = eb, bph = eph;
-          if (++eb == (uint32_t)g.boxes) {
+          if (++eb == (uint32_t)boxes) {
             eb = 0;
             eph ^= 1;
           }
@@ -885,38 +987,39 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
           const int inner = kWidth == 64 ? set * 32 : 0;
           uint32_t r[32];
           tmem_load32(d + cc * kWidth + inner, r);
-          if (kb1 == kb0) {
+          if (empty_sum) {
 #pragma unroll
             for (int q = 0; q < 32; ++q) r[q] = 0;  // an empty contraction
           }
           ok = bar_wait(efull + 8 * b, bph, &dead);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          const int row = w * 32 + lane;
-          box_chunk<MODE, FORM>(k.epi, offset,
-                                patches + b * (kSlot * (g.two_slots ? 2 : 1)), g.two_slots, row,
-                                i0 + lane, (int64_t)tj * g.bn + cc * kWidth + inner, set * 4,
-                                k.cols, r);
+          float v[32];
+#pragma unroll
+          for (int q = 0; q < 32; ++q) v[q] = __uint_as_float(r[q]);
+          box_chunk<MODE, FORM>(be, offset, boxes0 + b * chunk_bytes, second, w * 32 + lane,
+                                i0 + lane, (int64_t)tj * bn + cc * kWidth + inner, set * 4, cols,
+                                v);
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) bar_arrive(edone + 8 * b);
         }
       } else
       for (int cc = set; cc < chunks; cc += 2) {
-        const int64_t j0 = (int64_t)tj * g.bn + cc * 32;
-        if (S == 1 && tj >= 0 && (i0 >= k.rows || j0 >= k.cols)) continue;
-        const Block b = block_of(k.out_t ? j0 : i0, k.out_t ? i0 : j0, e, lane);
+        const int64_t j0 = (int64_t)tj * bn + cc * 32;
+        if (S == 1 && tj >= 0 && (i0 >= rows || j0 >= cols)) continue;
+        const Block b = block_of(out_t ? j0 : i0, out_t ? i0 : j0, e, lane);
         Sides<MODE> sides;
         if (S == 1 && tj >= 0) load_sides<MODE>(k.epi, b, e, sides);
         uint32_t r[32];
         tmem_load32(d + cc * 32, r);
-        if (kb1 == kb0) {
+        if (empty_sum) {
 #pragma unroll
           for (int q = 0; q < 32; ++q) r[q] = 0;  // an empty contraction
         }
         const uint32_t patch = S == 1 ? mine : ring + (uint32_t)(cc * 4 + w) * kPatch * 4;
         if (S == 1 && MODE == LIN_DWEIGHT && tj < 0) {
-          const int64_t i = i0 + lane, n = g.bias_b ? k.cols : k.rows;
+          const int64_t i = i0 + lane, n = g.bias_b ? cols : rows;
           if (i < n && in_extent(i, i + 1, 0, n, ZERO_SITE_LINEAR_OUT)) {
             float v = __uint_as_float(r[0]);
             if (k.epi.accumulate) v += load1(k.dbias, i);
@@ -924,11 +1027,10 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
           }
           continue;
         }
-        if (k.out_t) {
+        if (out_t) {
 #pragma unroll
           for (int q = 0; q < 32; ++q)
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(patch + (q * 36 + lane) * 4), "r"(r[q])
-                         : "memory");
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(patch + (q * 36 + lane) * 4), "r"(r[q]));
         } else {
 #pragma unroll
           for (int q = 0; q < 32; q += 4)
@@ -973,7 +1075,7 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
           gen_operand(g.gen_b, k.b, b_c, k.cols, k.depth, j0, g.bn / 2, c0, b_at, t128);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) bar_arrive_cluster(full_lead + 8 * s);
+        if (lane == 0) bar_arrive_cluster_release(full_lead + 8 * s);
         if (++s == (uint32_t)g.stages) {
           s = 0;
           ph ^= 1;

@@ -176,73 +176,71 @@ constexpr float kGeluB = 0.044715f;
 constexpr float kRsqrt2 = 0.70710678118654752f;
 constexpr float kRsqrt2Pi = 0.39894228040143268f;
 
-// 8 values through an activation, in place.
-__device__ __forceinline__ void activate8(float z[8], int act) {
+// N values through an activation, in place.
+template <int N>
+__device__ __forceinline__ void activate(float z[N], int act) {
   switch (act) {
     case ZERO_ACT_RELU:
 #pragma unroll
-      for (int j = 0; j < 8; ++j) z[j] = z[j] < 0.0f ? 0.0f : z[j];  // NaN stays NaN
+      for (int j = 0; j < N; ++j) z[j] = z[j] < 0.0f ? 0.0f : z[j];  // NaN stays NaN
       break;
     case ZERO_ACT_GELU:
 #pragma unroll
-      for (int j = 0; j < 8; ++j) z[j] = 0.5f * z[j] * (1.0f + erff(z[j] * kRsqrt2));
+      for (int j = 0; j < N; ++j) z[j] = 0.5f * z[j] * (1.0f + erff(z[j] * kRsqrt2));
       break;
     case ZERO_ACT_GELU_TANH:
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int j = 0; j < N; ++j)
         z[j] = z[j] * logistic(z[j] * (kGeluA + kGeluA * kGeluB * z[j] * z[j]));
       break;
     case ZERO_ACT_SILU:
 #pragma unroll
-      for (int j = 0; j < 8; ++j) z[j] = z[j] * logistic(z[j]);
+      for (int j = 0; j < N; ++j) z[j] = z[j] * logistic(z[j]);
       break;
     default:
       break;
   }
 }
 
-// act(z) and d act / dz of 8 values.
-__device__ __forceinline__ void activate_grad8(const float z[8], int act, float value[8],
-                                               float slope[8]) {
+// act(z) in the place of N values z, and d act / dz.
+template <int N>
+__device__ __forceinline__ void activate_grad(float value[N], float slope[N], int act) {
   switch (act) {
     case ZERO_ACT_RELU:
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        value[j] = z[j] < 0.0f ? 0.0f : z[j];
-        slope[j] = z[j] > 0.0f ? 1.0f : 0.0f;
+      for (int j = 0; j < N; ++j) {
+        slope[j] = value[j] > 0.0f ? 1.0f : 0.0f;
+        value[j] = value[j] < 0.0f ? 0.0f : value[j];
       }
       break;
     case ZERO_ACT_GELU:
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float s = 0.5f * (1.0f + erff(z[j] * kRsqrt2));
-        value[j] = z[j] * s;
-        slope[j] = s + z[j] * kRsqrt2Pi * __expf(-0.5f * z[j] * z[j]);
+      for (int j = 0; j < N; ++j) {
+        const float z = value[j], s = 0.5f * (1.0f + erff(z * kRsqrt2));
+        value[j] = z * s;
+        slope[j] = s + z * kRsqrt2Pi * __expf(-0.5f * z * z);
       }
       break;
     case ZERO_ACT_GELU_TANH:
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float q = z[j] * z[j];
-        const float s = logistic(z[j] * (kGeluA + kGeluA * kGeluB * q));
-        value[j] = z[j] * s;
+      for (int j = 0; j < N; ++j) {
+        const float z = value[j], q = z * z;
+        const float s = logistic(z * (kGeluA + kGeluA * kGeluB * q));
+        value[j] = z * s;
         slope[j] = s + value[j] * (1.0f - s) * (kGeluA + 3.0f * kGeluA * kGeluB * q);
       }
       break;
     case ZERO_ACT_SILU:
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float s = logistic(z[j]);
-        value[j] = z[j] * s;
+      for (int j = 0; j < N; ++j) {
+        const float z = value[j], s = logistic(z);
+        value[j] = z * s;
         slope[j] = s + value[j] * (1.0f - s);
       }
       break;
     default:
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        value[j] = z[j];
-        slope[j] = 1.0f;
-      }
+      for (int j = 0; j < N; ++j) slope[j] = 1.0f;
   }
 }
 
