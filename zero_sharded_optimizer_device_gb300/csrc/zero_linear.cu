@@ -59,9 +59,12 @@ enum Form : int {
 
 // How a launch walks its product (host-made).
 struct TileK {
-  int tiles_i, tiles_j, bias_tiles;  // bias_tiles more sum one operand's rows alone
-  int bias_b;                        // ... those of B (else of A)
+  int tiles_i, tiles_j;
+  int bias_tiles;  // that many more sum one operand's rows alone, or
+  int bias_fused;  // the first tile of every row (column) sums them beside its products
+  int bias_b;      // rows of B (else of A)
   int kblocks, splits, bn, stages;
+  int split_log2, clusters;          // splits = 1 << split_log2; clusters launched
   int i_fast;                        // consecutive tiles differ in i (else in j)
   int gen_a, gen_b;                  // elements per plain load; 0: by TMA
   int boxes;                         // ring of box chunks (box forms)
@@ -88,8 +91,10 @@ __device__ __forceinline__ uint32_t remote(uint32_t addr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
-__device__ __forceinline__ void cluster_sync() {
+__device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 }
 // One lane of a converged warp, always the same.  Roles that issue from one
@@ -327,6 +332,12 @@ __device__ __forceinline__ void tile_at(const TileK& g, int t, int& i, int& j) {
   }
 }
 
+// Where the sums for the bias lie in tensor memory beside the products of set
+// acc: one tile per cluster leaves the second set free, else behind both sets.
+__device__ __forceinline__ uint32_t bias_column(const TileK& g, uint32_t acc) {
+  return (uint32_t)(g.tiles_i * g.tiles_j <= g.clusters ? g.bn : 2 * g.bn) + 32 * acc;
+}
+
 // A warp finishes a 32 x 32 block of the output (rows row0.., columns col0..)
 // as four steps of 8 rows, a lane taking 8 consecutive columns of one row in
 // each: 16-byte accesses of bf16, 64 consecutive bytes per row.
@@ -370,9 +381,10 @@ __device__ __forceinline__ void load_sides(const EpiK& k, const Block& b, const 
 
 // What follows the product for 8 columns of row `row`, v holding their sums.
 template <int MODE>
-__device__ __forceinline__ void finish8(const EpiK& k, uint64_t offset, int64_t row,
+__device__ __forceinline__ void finish8(const EpiK& k, int64_t row,
                                         const Block& b, const Extent& e, const float bias[8],
-                                        const uint4& p, const Raw8& q, float v[8]) {
+                                        const uint4& p, const Raw8& q, uint32_t keep,
+                                        float v[8]) {
   constexpr int site = ZERO_SITE_LINEAR_OUT;
   float f[8];
   if constexpr (MODE == LIN_FORWARD) {
@@ -385,7 +397,7 @@ __device__ __forceinline__ void finish8(const EpiK& k, uint64_t offset, int64_t 
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] *= f[j];
     }
-    if (k.drop.on) drop8(k.drop, offset, (uint32_t)row, b.col, v);
+    if (k.drop.on) apply_keep<8>(keep, k.drop.scale, v);
     if (k.residual.p) {
       from_raw(k.residual, q, f);
 #pragma unroll
@@ -432,7 +444,7 @@ __device__ __forceinline__ float4 ld_shared4(uint32_t addr) {
 // the patch is output row row0 + r): in this CTA's shared memory, or as
 // `pairs` parts at the same address in the cluster's CTAs of this half.
 template <int MODE, bool PARTS>
-__device__ __forceinline__ void finish_block(const EpiK& k, uint64_t offset, uint32_t patch,
+__device__ __forceinline__ void finish_block(const EpiK& k, uint32_t keep, uint32_t patch,
                                              int pairs, uint32_t half, const Block& b,
                                              const Extent& e, const Sides<MODE>& s, int lane) {
   float bias[8];
@@ -460,7 +472,7 @@ __device__ __forceinline__ void finish_block(const EpiK& k, uint64_t offset, uin
     }
     const int64_t row = b.row + it * 8;
     if (row < e.rows && b.valid)
-      finish8<MODE>(k, offset, row, b, e, bias, s.p[it], s.q[it], v);
+      finish8<MODE>(k, row, b, e, bias, s.p[it], s.q[it], keep << (8 * it), v);
   }
 }
 
@@ -511,9 +523,9 @@ __device__ __forceinline__ void sts_f32(uint32_t base, int row, int i, const flo
 
 // What the box form asks of the epilogue's parameters, read once per kernel.
 struct BoxEpi {
-  bool bias, gate, pre, residual, dgate, old;
+  bool bias, gate, pre, residual, dgate, old, drop;
   int act;
-  DropK drop;
+  float scale;
   Mat b;
 };
 template <int MODE>
@@ -526,7 +538,8 @@ __device__ __forceinline__ BoxEpi box_epi(const EpiK& k) {
   e.dgate = MODE == LIN_DINPUT && k.dgate.p;
   e.old = MODE == LIN_DWEIGHT && k.accumulate;
   e.act = k.act;
-  e.drop = k.drop;
+  e.drop = MODE == LIN_FORWARD && k.drop.on;
+  e.scale = k.drop.scale;
   e.b = k.bias;
   return e;
 }
@@ -535,9 +548,9 @@ __device__ __forceinline__ BoxEpi box_epi(const EpiK& k) {
 // through the epilogue; unit0: their first 16-byte unit in a bf16 row.  Each
 // step runs over all 32 before the next: a branch per step, not per value.
 template <int MODE, int FORM>
-__device__ __forceinline__ void box_chunk(const BoxEpi& k, uint64_t offset, uint32_t chunk,
-                                          uint32_t second, int row, int64_t out_row, int64_t col,
-                                          int unit0, int64_t cols, float v[32]) {
+__device__ __forceinline__ void box_chunk(const BoxEpi& k, uint32_t keep, uint32_t chunk,
+                                          uint32_t second, int row, int64_t col, int unit0,
+                                          int64_t cols, float v[32]) {
   constexpr bool wide = FORM == BOX_F32;
   const uint32_t slot1 = chunk + second;
   float f[8];
@@ -574,10 +587,7 @@ __device__ __forceinline__ void box_chunk(const BoxEpi& k, uint64_t offset, uint
         for (int j = 0; j < 8; ++j) v[8 * i + j] *= f[j];
       }
     }
-    if (k.drop.on) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) drop8(k.drop, offset, (uint32_t)out_row, col + 8 * i, v + 8 * i);
-    }
+    if (k.drop) apply_keep<32>(keep, k.scale, v);
     if (k.residual) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -702,7 +712,8 @@ __device__ __forceinline__ void box_traffic(const BoxMaps& maps, const ProductK&
     next_chunk<W>(g, cols, tiles, step, in);
   }
   out = in;
-  uint32_t ahead = 0, lb = 0, sb = 0, sph = 0;  // ahead: chunks loaded and not yet stored
+  uint32_t ahead = 0, lb = 0, sb = 0, sph = 0;  // ahead: chunks whose memory is in use
+  int64_t stored = 0;
   bool live = true;
   while (out.t < tiles) {
     while (in.t < tiles && ahead < ring) {
@@ -742,11 +753,16 @@ __device__ __forceinline__ void box_traffic(const BoxMaps& maps, const ProductK&
         }
       }
       asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-      asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+      // with three chunks the one stored before this is free; with two, this
+      if (ring > 2)
+        asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+      else
+        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
     }
     __syncwarp();
     if (!live) break;
-    --ahead;
+    if (ring == 2 || stored > 0) --ahead;
+    ++stored;
     if (++sb == ring) {
       sb = 0;
       sph ^= 1;
@@ -754,7 +770,7 @@ __device__ __forceinline__ void box_traffic(const BoxMaps& maps, const ProductK&
     next_chunk<W>(g, cols, tiles, step, out);
   }
   // after a wait that gave up: the boxes in flight land before the CTA returns
-  for (; ahead > 0; --ahead) {
+  for (; !live && ahead > 0; --ahead) {
     const long long t0 = clock64();
     while (!bar_try(efull + 8 * sb, sph) && clock64() - t0 < kWaitCycles / 8) {
     }
@@ -766,6 +782,141 @@ __device__ __forceinline__ void box_traffic(const BoxMaps& maps, const ProductK&
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
+// The same for rows off 16-byte boundaries: a lane takes one column and its 32
+// rows, so that a warp's accesses of a row are consecutive whatever its
+// alignment.
+struct Column {
+  int64_t row, col;
+  int count;  // rows this lane has: 0 outside the columns
+};
+__device__ __forceinline__ bool column_in(const Mat& m, const Column& c, int i, const Extent& e) {
+  const int64_t at = (c.row + i) * m.ld;
+  return i < c.count && in_extent(at + c.col, at + c.col + 1, at, at + e.cols,
+                                  ZERO_SITE_LINEAR_OUT) &&
+         in_extent(c.row + i, c.row + i + 1, 0, e.rows, ZERO_SITE_LINEAR_OUT);
+}
+__device__ __forceinline__ void column_load(const Mat& m, const Column& c, const Extent& e,
+                                            float f[32]) {
+  const int64_t at = c.row * m.ld + c.col;
+  if (m.dtype == ZERO_F32) {
+    const float* p = static_cast<const float*>(m.p) + at;
+#pragma unroll
+    for (int i = 0; i < 32; ++i, p += m.ld) f[i] = column_in(m, c, i, e) ? *p : 0.0f;
+  } else {
+    const uint16_t* p = static_cast<const uint16_t*>(m.p) + at;
+#pragma unroll
+    for (int i = 0; i < 32; ++i, p += m.ld)
+      f[i] = column_in(m, c, i, e) ? __uint_as_float((uint32_t)*p << 16) : 0.0f;
+  }
+}
+__device__ __forceinline__ void column_store(const Mat& m, const Column& c, const Extent& e,
+                                             const float f[32]) {
+  const int64_t at = c.row * m.ld + c.col;
+  if (m.dtype == ZERO_F32) {
+    float* p = static_cast<float*>(m.p) + at;
+#pragma unroll
+    for (int i = 0; i < 32; ++i, p += m.ld)
+      if (column_in(m, c, i, e)) *p = f[i];
+  } else {
+    uint16_t* p = static_cast<uint16_t*>(m.p) + at;
+#pragma unroll
+    for (int i = 0; i < 32; ++i, p += m.ld)
+      if (column_in(m, c, i, e)) *p = to_bf16(f[i]);
+  }
+}
+
+// `keep` holds the mask as finish_block would use it.
+template <int MODE>
+__device__ __forceinline__ void finish_columns(const EpiK& k, uint32_t keep, uint32_t patch,
+                                               int64_t row0, int64_t col0, const Extent& e,
+                                               int lane) {
+  Column c;
+  c.row = row0;
+  c.col = col0 + lane;
+  c.count = c.col >= e.cols ? 0 : (int)(e.rows - row0 < 32 ? e.rows - row0 : 32);
+  float v[32], f[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[i]) : "r"(patch + (i * 36 + lane) * 4));
+  if constexpr (MODE == LIN_FORWARD) {
+    if (k.bias.p) {
+      const float b = c.count && in_extent(c.col, c.col + 1, 0, e.cols, ZERO_SITE_LINEAR_OUT)
+                          ? load1(k.bias, c.col)
+                          : 0.0f;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] += b;
+    }
+    if (k.pre.p) column_store(k.pre, c, e, v);
+    activate<32>(v, k.act);
+    if (k.gate.p) {
+      column_load(k.gate, c, e, f);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] *= f[i];
+    }
+    if (k.drop.on) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {  // the lane and bit that hold this element
+        const uint32_t m = __shfl_sync(0xffffffffu, keep, (i & 7) << 2 | lane >> 3);
+        v[i] = m >> (31 - (i >> 3) * 8 - (lane & 7)) & 1 ? v[i] * k.drop.scale : 0.0f;
+      }
+    }
+    if (k.residual.p) {
+      column_load(k.residual, c, e, f);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] += f[i];
+    }
+  } else if constexpr (MODE == LIN_DINPUT) {
+    if (k.pre.p) {
+      column_load(k.pre, c, e, f);
+      float slope[32];
+      activate_grad<32>(f, slope, k.act);
+      if (k.gate.p) {
+        if (k.dgate.p) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) f[i] *= v[i];
+          column_store(k.dgate, c, e, f);
+        }
+        column_load(k.gate, c, e, f);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) slope[i] *= f[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] *= slope[i];
+    }
+  } else {
+    if (k.accumulate) {
+      column_load(k.out, c, e, f);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] += f[i];
+    }
+  }
+  column_store(k.out, c, e, v);
+}
+
+// Dropout's masks of a thread's share of a tile, 32 elements each: drawn while
+// the tile's products are still running, on warps that otherwise wait.
+struct Masks {
+  uint32_t m0, m1, m2, m3;
+  __device__ __forceinline__ uint32_t at(int q) const {
+    return q < 2 ? (q == 0 ? m0 : m1) : (q == 2 ? m2 : m3);
+  }
+  __device__ __forceinline__ void set(int q, uint32_t m) {
+    if (q == 0) m0 = m;
+    if (q == 1) m1 = m;
+    if (q == 2) m2 = m;
+    if (q == 3) m3 = m;
+  }
+};
+
+// The gradient of bias element i.
+__device__ __forceinline__ void store_bias(const ProductK& k, const TileK& g, int64_t i,
+                                           float v) {
+  const int64_t n = g.bias_b ? k.cols : k.rows;
+  if (i >= n || !in_extent(i, i + 1, 0, n, ZERO_SITE_LINEAR_OUT)) return;
+  if (k.epi.accumulate) v += load1(k.dbias, i);
+  store1(k.dbias, i, v);
+}
+
 template <int MODE, int FORM>
 __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
     product_kernel(const __grid_constant__ CUtensorMap map_a,
@@ -775,7 +926,7 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
   constexpr bool GEN = FORM == PATCH_GEN, BOX = FORM == BOX_BF16 || FORM == BOX_F32;
   constexpr int kWidth = FORM == BOX_F32 ? 32 : 64;  // columns of a chunk
   extern __shared__ __align__(1024) unsigned char smem[];
-  __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 4 + 2 * kMostBoxes];
+  __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 5 + 2 * kMostBoxes];
   __shared__ uint32_t tmem_at;
   __shared__ int dead;
   const uint32_t rank = cluster_rank(), half = rank & 1, leader = rank & ~1u;
@@ -787,17 +938,10 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
   const uint32_t ones = patches + (BOX ? g.boxes * kSlot * (g.two_slots ? 2 : 1)
                                        : S == 1 ? kEpiWarps * kPatch * 4 : 0);
   const uint32_t full = smem_u32(bars), empty = full + 8 * kMaxStages;
-  const uint32_t tfull = empty + 8 * kMaxStages, tempty = tfull + 16;
-  const uint32_t efull = tempty + 16, edone = efull + 8 * kMostBoxes;
+  const uint32_t tfull = empty + 8 * kMaxStages, tempty = tfull + 16, ready = tempty + 16;
+  const uint32_t efull = ready + 8, edone = efull + 8 * kMostBoxes;
 
-  // the next kernel on the stream may set up while this one runs
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (warp == 1 && lane == 0) {
-    asm volatile("prefetch.tensormap [%0];" ::"l"(&map_a) : "memory");
-    asm volatile("prefetch.tensormap [%0];" ::"l"(&map_b) : "memory");
-    if (BOX) asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.out) : "memory");
-  }
-  if (warp == 0 && lane == 0) {
+  if (warp == 0 && elect()) {
     dead = 0;
     for (int s = 0; s < g.stages; ++s) {
       bar_init(full + 8 * s, 1 + (GEN ? 2 * kGenWarps : 0));
@@ -807,6 +951,7 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
       bar_init(tfull + 8 * a, 1);
       bar_init(tempty + 8 * a, 2 * kEpiWarps);
     }
+    bar_init(ready, 2);  // tensor memory of both CTAs
     if (BOX)
       for (int b = 0; b < g.boxes; ++b) {
         bar_init(efull + 8 * b, 1);
@@ -815,34 +960,56 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
       }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 2) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_u32(&tmem_at)),
-                 "r"(g.tmem_cols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
-  }
-  if (MODE == LIN_DWEIGHT && g.bias_tiles && warp == 3) {
+  if (MODE == LIN_DWEIGHT && (g.bias_tiles || g.bias_fused) && warp == 3) {
     for (int q = lane; q < kOnesBytes / 16; q += 32)  // bf16 1.0 twice
       asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(ones + q * 16),
                    "r"(0x3F803F80u)
                    : "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-  __syncthreads();
-  cluster_sync();
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  __syncwarp();
+  cluster_arrive();  // this CTA's barriers are ready; what follows needs no other CTA
+  // the next kernel on the stream may set up while this one runs
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (warp == 1 && elect()) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&map_a) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&map_b) : "memory");
+    if (BOX) asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.out) : "memory");
+  }
+  if (warp == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&tmem_at)),
+                 "r"(g.tmem_cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  }
+  // this cluster's tiles, and this pair's share of the contraction
+  const int clusters = g.clusters, first = (int)(blockIdx.x >> (1 + g.split_log2));
+  const int tiles = g.tiles_i * g.tiles_j + g.bias_tiles;
+  const int kb0 = (int)(((int64_t)g.kblocks * split) >> g.split_log2);
+  const int kb1 = (int)(((int64_t)g.kblocks * (split + 1)) >> g.split_log2);
+  const bool a_c = k.a_c, b_c = k.b_c;
+  // fetched before the wait, not when first used after it
+  asm volatile("" ::"r"(clusters), "r"(first), "r"(tiles), "r"(kb0), "r"(kb1), "r"((int)a_c),
+               "r"((int)b_c), "r"(g.stages), "r"(g.gen_a), "r"(g.gen_b), "r"(g.i_fast));
+  cluster_wait();
+  if (warp == 2) {
+    if (elect()) bar_arrive_cluster(remote(ready, leader));
+    __syncwarp();
+  }
   // what ran before this on the stream is done and its writes are visible
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const uint32_t tmem = *(volatile uint32_t*)&tmem_at;
-
-  // this cluster's tiles, and this pair's share of the contraction
-  const int clusters = gridDim.x / (2 * S), first = blockIdx.x / (2 * S);
-  const int tiles = g.tiles_i * g.tiles_j + g.bias_tiles;
-  const int kb0 = (int)((int64_t)g.kblocks * split / S);
-  const int kb1 = (int)((int64_t)g.kblocks * (split + 1) / S);
-  const bool a_c = k.a_c, b_c = k.b_c;
+  uint32_t tmem = 0;
+  if (warp == 1 || warp == 2 || (warp >= kEpiWarp0 && warp < kEpiWarp0 + kEpiWarps)) {
+    asm volatile("bar.sync 1, %0;" ::"n"((kEpiWarps + 2) * 32) : "memory");
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    tmem = *(volatile uint32_t*)&tmem_at;
+  }
+  // The last barrier of the cluster, at which nobody signals another CTA or
+  // reads its memory any more: warp 3 only moves this CTA's own boxes.
+  const bool early = BOX && warp == 3;
+  if (early) cluster_arrive();
 
   if (warp == 0) {
     const uint32_t full_lead = remote(full, leader);
@@ -910,14 +1077,16 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
       const uint32_t idesc_1 = base | (4u << 17);
       const uint32_t step_a = a_c ? 2 : 128, step_b = b_c ? 2 : 128;  // 16 deep, in 16 bytes
       const uint32_t stages = g.stages, bn = g.bn;
+      const bool fused = MODE == LIN_DWEIGHT && g.bias_fused, bias_b = g.bias_b;
       uint32_t s = 0, ph = 0, acc = 0, aph = 0;
-      bool live = true;
+      bool live = bar_wait(ready, 0, &dead);
       for (int t = first; t < tiles; t += clusters) {
         int ti, tj;
         tile_at(g, t, ti, tj);
+        const bool sums = fused && (bias_b ? ti : tj) == 0;
         live = live && bar_wait(tempty + 8 * acc, aph ^ 1, &dead);
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint32_t d = tmem + acc * bn;
+        const uint32_t d = tmem + acc * bn, d_bias = tmem + bias_column(g, acc);
         const uint32_t idesc = tj >= 0 ? idesc_n : idesc_1, sb = tj >= 0 ? step_b : 0;
         for (int kb = kb0; kb < kb1; ++kb) {
           live = live && bar_wait(full + 8 * s, ph, &dead);
@@ -931,6 +1100,13 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
 #pragma unroll
             for (int q = 0; q < kDeep / 16; ++q)
               mma_pair(d, da + q * step_a, db + q * sb, idesc, kb > kb0 || q > 0);
+            if (MODE == LIN_DWEIGHT && sums) {
+              const uint64_t dr = operand_desc(bias_b ? a_at + kBytesA : a_at, a_c);
+              const uint64_t d1 = operand_desc(ones, true);
+#pragma unroll
+              for (int q = 0; q < kDeep / 16; ++q)
+                mma_pair(d_bias, dr + q * step_a, d1, idesc_1, kb > kb0 || q > 0);
+            }
             commit_pair(empty + 8 * s, mask);
           }
           __syncwarp();
@@ -957,6 +1133,7 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
         MODE == LIN_FORWARD && k.epi.drop.on ? drop_offset(k.epi.drop) : 0ull;
     const uint32_t mine = patches + (uint32_t)(warp - kEpiWarp0) * kPatch * 4;
     const BoxEpi be = box_epi<MODE>(k.epi);
+    const DropK drop = k.epi.drop;
     const bool empty_sum = kb1 == kb0, out_t = k.out_t;
     const uint32_t boxes = g.boxes, boxes0 = patches, second = g.two_slots ? kSlot : 0,
                    chunk_bytes = kSlot + second;
@@ -967,12 +1144,27 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
     for (int t = first; t < tiles && ok; t += clusters) {
       int ti, tj;
       tile_at(g, t, ti, tj);
+      const int64_t i0 = (int64_t)ti * 256 + half * kRowsCta + w * 32;
+      const int chunks = tj >= 0 ? bn / 32 : 1;
+      Masks masks{};
+      if (MODE == LIN_FORWARD && S == 1 && drop.on) {
+#pragma unroll 1
+        for (int q = 0; 2 * q + set < chunks; ++q) {
+          // the 32 columns this warp takes q-th, as the loops below take them
+          const int64_t j0 = (int64_t)tj * bn + (2 * q + set) * 32;
+          if (i0 >= rows || j0 >= cols) break;
+          if (BOX) {
+            masks.set(q, keep32<4>(drop, offset, (uint32_t)(i0 + lane), 0, j0));
+          } else {
+            const Block b = block_of(out_t ? j0 : i0, out_t ? i0 : j0, e, lane);
+            masks.set(q, keep32<1>(drop, offset, (uint32_t)b.row, 8, b.col));
+          }
+        }
+      }
       ok = bar_wait(tfull + 8 * acc, aph, &dead);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      const int64_t i0 = (int64_t)ti * 256 + half * kRowsCta + w * 32;
-      const int chunks = tj >= 0 ? bn / 32 : 1;
       const uint32_t d = tmem + acc * bn + ((uint32_t)(w * 32) << 16);
       if (BOX && tj >= 0) {
         const int64_t left = cols - (int64_t)tj * bn;
@@ -997,9 +1189,9 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
           float v[32];
 #pragma unroll
           for (int q = 0; q < 32; ++q) v[q] = __uint_as_float(r[q]);
-          box_chunk<MODE, FORM>(be, offset, boxes0 + b * chunk_bytes, second, w * 32 + lane,
-                                i0 + lane, (int64_t)tj * bn + cc * kWidth + inner, set * 4, cols,
-                                v);
+          box_chunk<MODE, FORM>(be, masks.at(kWidth == 64 ? cc : cc >> 1),
+                                boxes0 + b * chunk_bytes, second, w * 32 + lane,
+                                (int64_t)tj * bn + cc * kWidth + inner, set * 4, cols, v);
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) bar_arrive(edone + 8 * b);
@@ -1010,7 +1202,7 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
         if (S == 1 && tj >= 0 && (i0 >= rows || j0 >= cols)) continue;
         const Block b = block_of(out_t ? j0 : i0, out_t ? i0 : j0, e, lane);
         Sides<MODE> sides;
-        if (S == 1 && tj >= 0) load_sides<MODE>(k.epi, b, e, sides);
+        if (S == 1 && tj >= 0 && k.epi.vec) load_sides<MODE>(k.epi, b, e, sides);
         uint32_t r[32];
         tmem_load32(d + cc * 32, r);
         if (empty_sum) {
@@ -1019,12 +1211,7 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
         }
         const uint32_t patch = S == 1 ? mine : ring + (uint32_t)(cc * 4 + w) * kPatch * 4;
         if (S == 1 && MODE == LIN_DWEIGHT && tj < 0) {
-          const int64_t i = i0 + lane, n = g.bias_b ? cols : rows;
-          if (i < n && in_extent(i, i + 1, 0, n, ZERO_SITE_LINEAR_OUT)) {
-            float v = __uint_as_float(r[0]);
-            if (k.epi.accumulate) v += load1(k.dbias, i);
-            store1(k.dbias, i, v);
-          }
+          store_bias(k, g, i0 + lane, __uint_as_float(r[0]));
           continue;
         }
         if (out_t) {
@@ -1040,9 +1227,25 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
         }
         if (S == 1) {
           __syncwarp();
-          finish_block<MODE, false>(k.epi, offset, patch, 1, half, b, e, sides, lane);
+          if (k.epi.vec)
+            finish_block<MODE, false>(k.epi, masks.at(cc >> 1), patch, 1, half, b, e, sides, lane);
+          else
+            finish_columns<MODE>(k.epi, masks.at(cc >> 1), patch, out_t ? j0 : i0,
+                                 out_t ? i0 : j0, e, lane);
           __syncwarp();
         }
+      }
+      if (MODE == LIN_DWEIGHT && g.bias_fused && (g.bias_b ? ti : tj) == 0 && set == 0) {
+        uint32_t r[32];
+        tmem_load32(tmem + bias_column(g, acc) + ((uint32_t)(w * 32) << 16), r);
+        const float v = empty_sum ? 0.0f : __uint_as_float(r[0]);
+        if (S == 1)
+          store_bias(k, g, (int64_t)(g.bias_b ? tj : ti) * 256 + half * kRowsCta + w * 32 + lane,
+                     v);
+        else  // a block of its own, behind the tile's
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(
+                           ring + (uint32_t)((chunks * 4 + w) * kPatch + lane) * 4),
+                       "f"(v));
       }
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
@@ -1088,46 +1291,49 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
   if (S > 1) {
     // every pair's sums now lie in its own shared memory: pair p finishes the
     // blocks p, p + S, ... of its half, adding the pairs' parts in order
-    cluster_sync();
+    cluster_arrive();
+    cluster_wait();
     if (warp >= kEpiWarp0 && warp < kEpiWarp0 + kEpiWarps && !dead) {
       const Extent e{k.out_t ? k.cols : k.rows, k.out_t ? k.rows : k.cols};
       const uint64_t offset =
           MODE == LIN_FORWARD && k.epi.drop.on ? drop_offset(k.epi.drop) : 0ull;
       int ti, tj;
       tile_at(g, first, ti, tj);
-      const int blocks = 4 * (tj >= 0 ? g.bn / 32 : 1);
+      const int main = 4 * (tj >= 0 ? g.bn / 32 : 1);
+      const bool sums = MODE == LIN_DWEIGHT && g.bias_fused && (g.bias_b ? ti : tj) == 0;
+      const int blocks = main + (sums ? 4 : 0);
       for (int b = split + S * (warp - kEpiWarp0); b < blocks; b += S * kEpiWarps) {
         const int64_t i0 = (int64_t)ti * 256 + half * kRowsCta + (b & 3) * 32;
         const int64_t j0 = (int64_t)tj * g.bn + (b >> 2) * 32;
         const uint32_t patch = ring + (uint32_t)b * kPatch * 4;
-        if (MODE == LIN_DWEIGHT && tj < 0) {
-          const int64_t i = i0 + lane, n = g.bias_b ? k.cols : k.rows;
-          if (i < n && in_extent(i, i + 1, 0, n, ZERO_SITE_LINEAR_OUT)) {
-            const uint32_t at = patch + (k.out_t ? lane : lane * 36) * 4;
-            float v = 0.0f;
-            for (int p = 0; p < S; ++p) {
-              float x;
-              asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                           : "=f"(x)
-                           : "r"(remote(at, 2 * p + half))
-                           : "memory");
-              v += x;
-            }
-            if (k.epi.accumulate) v += load1(k.dbias, i);
-            store1(k.dbias, i, v);
+        if (MODE == LIN_DWEIGHT && (tj < 0 || b >= main)) {
+          const uint32_t at = patch + (k.out_t || tj >= 0 ? lane : lane * 36) * 4;
+          float v = 0.0f;
+          for (int p = 0; p < S; ++p) {
+            float x;
+            asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                         : "=f"(x)
+                         : "r"(remote(at, 2 * p + half)));
+            v += x;
           }
+          const int64_t tile = tj < 0 ? ti : g.bias_b ? tj : ti;
+          store_bias(k, g, tile * 256 + half * kRowsCta + (b & 3) * 32 + lane, v);
         } else if (i0 < k.rows && j0 < k.cols) {
           const Block o = block_of(k.out_t ? j0 : i0, k.out_t ? i0 : j0, e, lane);
           Sides<MODE> sides;
           load_sides<MODE>(k.epi, o, e, sides);
-          finish_block<MODE, true>(k.epi, offset, patch, S, half, o, e, sides, lane);
+          uint32_t keep = 0;
+          if (MODE == LIN_FORWARD && k.epi.drop.on)
+            keep = keep32<1>(k.epi.drop, offset, (uint32_t)o.row, 8, o.col);
+          finish_block<MODE, true>(k.epi, keep, patch, S, half, o, e, sides, lane);
         }
       }
     }
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-  __syncthreads();
-  cluster_sync();  // nobody reads this CTA's shared memory or signals it any more
+  __syncwarp();
+  if (!early) cluster_arrive();
+  cluster_wait();
   if (warp == 2) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
@@ -1202,7 +1408,7 @@ static bool box_map(CUtensorMap* map, const Mat& a, int64_t rows, int64_t cols, 
 
 // Shared memory beside the operand ring, and the ring's stages in what is left.
 static int side_bytes(const TileK& g, int form) {
-  return (g.bias_tiles ? kOnesBytes : 0) + (form >= BOX_BF16 ? g.boxes * kSlot * (g.two_slots ? 2 : 1)
+  return (g.bias_tiles || g.bias_fused ? kOnesBytes : 0) + (form >= BOX_BF16 ? g.boxes * kSlot * (g.two_slots ? 2 : 1)
                        : g.splits == 1 ? kEpiWarps * kPatch * 4 : 0);
 }
 static int stages_for(const TileK& g, int form) {
@@ -1230,6 +1436,8 @@ static cudaError_t launch_tiles(const CUtensorMap& ma, const CUtensorMap& mb,
   const int64_t tiles = (int64_t)g.tiles_i * g.tiles_j + g.bias_tiles;
   const int64_t pairs = sm_count() / 2;
   const int64_t clusters = g.splits > 1 || tiles < pairs ? tiles : pairs;
+  g.clusters = (int)clusters;
+  g.split_log2 = g.splits - 1;  // 1 or 2 parts
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(clusters * 2 * g.splits));
   cfg.blockDim = dim3((FORM == PATCH_GEN ? 16 : 12) * 32);
@@ -1270,24 +1478,30 @@ static cudaError_t launch_mode(const ProductK& in, cudaStream_t st) {
     k.cols = in.rows;
     k.out_t = !in.out_t;
   }
+  for (const Mat* m : {&k.epi.out, &k.epi.pre, &k.epi.gate, &k.epi.dgate, &k.epi.residual})
+    if (m->p && !m->vec) k.epi.vec = 0;
   TileK g{};
   const int64_t kblocks = (k.depth + kDeep - 1) / kDeep;
   const int64_t tiles_i = (k.rows + 255) / 256;
   const int64_t pairs = sm_count() / 2;
-  // Width and split by a cost model: waves of tiles times the cycles of one
-  // (512 per 64-deep step at BN = 256) plus what joining the parts takes.
+  // Width and split by a cost model: waves of tiles times the cycles of one.
+  // A 64-deep step takes 520 cycles at BN = 256 (the tensor cores' own time)
+  // and 430 at 128 and below, where loading A's rows decides; the last tile's
+  // epilogue 30 per column; joining two halves of a contraction 5000 and 42
+  // per column.  (Measured, us, one part / two: 1 x 4096 x 4096 16.9 / 12.9,
+  // 256 x 4096 x 4096 18.3 / 16.8, 2048 x 1024 x 4096 19.0 at BN = 128, 23.4 /
+  // 22.5 at 256; four parts, clusters of 8, always lost.)
   double best = 0;
   for (int bn = 32; bn <= 256; bn *= 2) {
-    if (!k.b_c && bn < 128) continue;          // blocks of 64 rows per CTA
-    if (bn < 128 && k.cols > bn) continue;     // narrow tiles only where one is enough
+    if (!k.b_c && bn < 128) continue;       // blocks of 64 rows per CTA
+    if (bn < 128 && k.cols > bn) continue;  // narrow tiles only where one is enough
     const int64_t tiles_j = (k.cols + bn - 1) / bn;
-    for (int S = 1; S <= 4; S *= 2) {
-      if (S > 1 && (kblocks < 2 * S)) break;
-      const int64_t tiles = tiles_i * tiles_j;
-      const double waves = (double)((tiles * S + pairs - 1) / pairs);
-      const double step = bn == 256 ? 512 : bn == 128 ? 300 : 200;
-      const double cost = waves * ((double)kblocks / S * step + (S > 1 ? 3000 + 10 * bn : 0)) +
-                          8 * bn + 1000;
+    for (int S = 1; S <= 2; ++S) {
+      if (S > 1 && kblocks < 2 * S) break;
+      const double waves = (double)((tiles_i * tiles_j * S + pairs - 1) / pairs);
+      const double step = bn == 256 ? 520 : 430;
+      const double cost =
+          waves * ((double)kblocks / S * step + (S > 1 ? 5000 + 42 * bn : 0)) + 30 * bn;
       if (best == 0 || cost < best) {
         best = cost;
         g.bn = bn;
@@ -1302,9 +1516,15 @@ static cudaError_t launch_mode(const ProductK& in, cudaStream_t st) {
     return cudaErrorInvalidValue;
   g.tiles_i = (int)tiles_i;
   g.kblocks = (int)kblocks;
-  g.bias_tiles = (int)((bias_rows + 255) / 256);
+  // The bias's sums ride on the first tiles' products (an eighth more work on
+  // those) where tensor memory has room for them; else they are tiles of
+  // their own, which cost a row of loads and, past a full wave, a wave.
+  const int64_t main = tiles_i * g.tiles_j;
+  g.bias_fused = bias_rows > 0 && main > 0 && (!g.bias_b || g.bn == 256) &&
+                 (g.splits > 1 || main <= pairs || g.bn == 128);
+  g.bias_tiles = g.bias_fused ? 0 : (int)((bias_rows + 255) / 256);
   g.i_fast = k.rows <= k.cols;
-  g.tmem_cols = 2 * g.bn;
+  g.tmem_cols = g.bias_fused && g.splits == 1 && main > pairs ? 512 : 2 * g.bn;
   CUtensorMap ma{}, mb{};
   BoxMaps maps{};
   if (k.depth > 0) {
@@ -1337,7 +1557,9 @@ static cudaError_t launch_mode(const ProductK& in, cudaStream_t st) {
   g.two_slots = MODE == LIN_FORWARD ? o.gate.p || o.pre.p
                 : MODE == LIN_DINPUT ? o.gate.p || (wide && o.pre.p)
                                      : 0;
-  g.boxes = kMostBoxes;
+  // Two chunks in flight where they are two boxes each: the operands' ring
+  // then keeps 5 stages (gate 4096-11008: 225 us against 252 at 3 and 4).
+  g.boxes = g.two_slots ? 2 : kMostBoxes;
   if (wide) return launch_tiles<MODE, BOX_F32>(ma, mb, maps, k, g, st);
   return launch_tiles<MODE, BOX_BF16>(ma, mb, maps, k, g, st);
 }

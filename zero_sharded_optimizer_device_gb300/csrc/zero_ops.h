@@ -48,6 +48,7 @@ struct EpiK {
   Mat residual;  // forward
   DropK drop;    // forward
   int act = ZERO_ACT_NONE;
+  int vec = 1;         // every matrix of the output's shape present has its vec
   int accumulate = 0;  // dweight
 };
 

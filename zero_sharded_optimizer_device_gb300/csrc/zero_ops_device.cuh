@@ -280,4 +280,52 @@ __device__ __forceinline__ void drop8(const DropK& d, uint64_t offset, uint32_t 
   }
 }
 
+// bits = 2 * bits + (w >= least), for below = 2^32 - least: the carry of w +
+// below, two adds instead of a comparison, a selection and a shift.
+__device__ __forceinline__ void push_keep(uint32_t& bits, uint32_t w, uint32_t below) {
+  asm("{ .reg .u32 t; add.cc.u32 t, %1, %2; addc.u32 %0, %0, %0; }"
+      : "+r"(bits)
+      : "r"(w), "r"(below));
+}
+
+// The mask of 32 elements as 8 groups of 4 columns, 2 PER groups in each of
+// 4 / PER rows `row_step` apart; the first element is the highest bit.  A loop
+// of two blocks, not eight copies: an epilogue runs this a few times per
+// kernel and has to fetch the code as well.
+template <int PER>
+__device__ __forceinline__ uint32_t keep32(const DropK& d, uint64_t offset, uint32_t row,
+                                           uint32_t row_step, int64_t col) {
+  const uint32_t k0 = (uint32_t)d.seed, k1 = (uint32_t)(d.seed >> 32);
+  const uint32_t lo = (uint32_t)offset, hi = (uint32_t)(offset >> 32), below = 0u - d.least;
+  const uint32_t group = (uint32_t)(col >> 2);
+  uint32_t keep = 0;
+#pragma unroll 1
+  for (uint32_t g = 0; g < 8; g += 2) {
+    uint4 w[2];
+#pragma unroll
+    for (uint32_t h = 0; h < 2; ++h)
+      w[h] = philox(make_uint4(group + (g + h) % (2 * PER),
+                               row + row_step * ((g + h) / (2 * PER)), lo, hi),
+                    k0, k1);
+#pragma unroll
+    for (uint32_t h = 0; h < 2; ++h) {
+      push_keep(keep, w[h].x, below);
+      push_keep(keep, w[h].y, below);
+      push_keep(keep, w[h].z, below);
+      push_keep(keep, w[h].w, below);
+    }
+  }
+  return d.all ? 0u : d.least == 0 ? 0xFFFFFFFFu : keep;
+}
+
+// N values whose mask bits are the highest of `keep`.
+template <int N>
+__device__ __forceinline__ void apply_keep(uint32_t keep, float scale, float v[N]) {
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    v[j] = (int32_t)keep < 0 ? v[j] * scale : 0.0f;
+    keep += keep;
+  }
+}
+
 }  // namespace zk
