@@ -780,24 +780,59 @@ def zero_async_status(reset: bool = False) -> int:
 
 
 # ------------------------------------------------------- layer computation --
-_TORCH_NAMES = {ZERO_F32: "torch.float32", ZERO_BF16: "torch.bfloat16"}
+class _Torch:
+    """What the calls below ask torch for, looked up once: a call on a few
+    tokens takes less time on the GPU than the public ways to ask."""
+    ready = False
+
+    @classmethod
+    def load(cls):
+        import torch
+        cls.dtypes = {ZERO_F32: torch.float32, ZERO_BF16: torch.bfloat16}
+        cls.device = staticmethod(torch.cuda.current_device)
+        cls.raw_stream = staticmethod(
+            getattr(torch._C, "_cuda_getCurrentRawStream", None) or
+            (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
+        cls.cuda = torch.cuda.is_available()
+        if cls.cuda:
+            torch.cuda.current_device()                  # initialises CUDA
+            cls.device = staticmethod(getattr(torch._C, "_cuda_getDevice", cls.device))
+        cls.ready = True
+
+
+def _ops_stream(s) -> int | None:
+    if s is not None:
+        return s if isinstance(s, int) else s.cuda_stream
+    if not _Torch.ready:
+        _Torch.load()
+    return _Torch.raw_stream(_Torch.device()) if _Torch.cuda else None
 
 
 def _mat(x, rows: int, cols: int, ld: int, dtype: int, what: str):
     """Address of a matrix argument.  A tensor must be of the dtype the call
-    names and its memory must hold rows of cols elements ld apart, counted
-    from its first element; raw integer addresses pass as they are."""
+    names, its rows contiguous, and its memory must hold rows of cols elements
+    ld apart, counted from its first element; raw integer addresses pass as
+    they are."""
     if x is None or isinstance(x, int):
         return x
-    es = _ESIZE.get(dtype)
-    if es is not None:
-        if str(x.dtype) != _TORCH_NAMES[dtype]:
-            raise ValueError(f"{what}: a {x.dtype} tensor passed as {_TORCH_NAMES[dtype]}")
+    if not _Torch.ready:
+        _Torch.load()
+    want = _Torch.dtypes.get(dtype)
+    if want is not None:
+        if x.dtype is not want:
+            raise ValueError(f"{what}: a {x.dtype} tensor passed as {want}")
         if rows > 0 and cols > 0:
-            have = x.untyped_storage().nbytes() - x.storage_offset() * es
-            need = ((rows - 1) * ld + cols) * es
-            if have < need:
-                raise ValueError(f"{what}: holds {have} bytes, the call touches {need}")
+            need = (rows - 1) * ld + cols
+            if not (x.is_contiguous() and x.numel() >= need):
+                if cols > 1 and x.dim() > 0 and x.shape[-1] > 1 and x.stride(-1) != 1:
+                    raise ValueError(f"{what}: the elements of a row are {x.stride(-1)} apart")
+                es = _ESIZE[dtype]
+                have = x.untyped_storage().nbytes() - x.storage_offset() * es
+                if have < need * es:
+                    raise ValueError(f"{what}: holds {have} bytes, the call touches {need * es}")
+    dev = x.get_device()
+    if dev >= 0 and _Torch.cuda and dev == _Torch.device():
+        return x.data_ptr()
     return _ptr(x)
 
 
@@ -866,7 +901,7 @@ def zero_linear(x, ldx: int, w, ldw: int, w_layout: int, m: int, n: int, k: int,
     _check(_lib().zero_linear(
         _mat(x, m, k, ldx, ZERO_BF16, "x"), ldx, _weight(w, ldw, w_layout, n, k, ZERO_BF16, "w"),
         ldw, w_layout, m, n, k, None if ep is None else ctypes.byref(ep.checked(m, n)),
-        _mat(y, m, n, ldy, ydtype, "y"), ldy, ydtype, _stream(stream)), "zero_linear")
+        _mat(y, m, n, ldy, ydtype, "y"), ldy, ydtype, _ops_stream(stream)), "zero_linear")
 
 
 def zero_linear_dinput(dy, lddy: int, w, ldw: int, w_layout: int, m: int, n: int, k: int, ag, dx,
@@ -875,7 +910,7 @@ def zero_linear_dinput(dy, lddy: int, w, ldw: int, w_layout: int, m: int, n: int
         _mat(dy, m, n, lddy, ZERO_BF16, "dy"), lddy,
         _weight(w, ldw, w_layout, n, k, ZERO_BF16, "w"), ldw, w_layout, m, n, k,
         None if ag is None else ctypes.byref(ag.checked(m, k)),
-        _mat(dx, m, k, lddx, dxdtype, "dx"), lddx, dxdtype, _stream(stream)),
+        _mat(dx, m, k, lddx, dxdtype, "dx"), lddx, dxdtype, _ops_stream(stream)),
         "zero_linear_dinput")
 
 
@@ -885,7 +920,7 @@ def zero_linear_dweight(dy, lddy: int, x, ldx: int, m: int, n: int, k: int, w_la
     _check(_lib().zero_linear_dweight(
         _mat(dy, m, n, lddy, ZERO_BF16, "dy"), lddy, _mat(x, m, k, ldx, ZERO_BF16, "x"), ldx,
         m, n, k, w_layout, _weight(dw, lddw, w_layout, n, k, dwdtype, "dw"), lddw, dwdtype,
-        _mat(dbias, 1, n, 0, dbdtype, "dbias"), dbdtype, int(accumulate), _stream(stream)),
+        _mat(dbias, 1, n, 0, dbdtype, "dbias"), dbdtype, int(accumulate), _ops_stream(stream)),
         "zero_linear_dweight")
 
 
@@ -894,7 +929,7 @@ def zero_dropout(x, ldx: int, xdtype: int, residual, ldres: int, res_dtype: int,
     _check(_lib().zero_dropout(
         _mat(x, m, n, ldx, xdtype, "x"), ldx, xdtype,
         _mat(residual, m, n, ldres, res_dtype, "residual"), ldres, res_dtype, m, n,
-        ctypes.byref(rng), _mat(y, m, n, ldy, ydtype, "y"), ldy, ydtype, _stream(stream)),
+        ctypes.byref(rng), _mat(y, m, n, ldy, ydtype, "y"), ldy, ydtype, _ops_stream(stream)),
         "zero_dropout")
 
 
@@ -905,7 +940,7 @@ def zero_layer_norm(x, ldx: int, xdtype: int, weight, bias, pdtype: int, m: int,
         _mat(x, m, n, ldx, xdtype, "x"), ldx, xdtype, _mat(weight, 1, n, 0, pdtype, "weight"),
         _mat(bias, 1, n, 0, pdtype, "bias"), pdtype, m, n, kind, eps,
         _mat(y, m, n, ldy, ydtype, "y"), ldy, ydtype, _mat(mean, 1, m, 0, ZERO_F32, "mean"),
-        _mat(rstd, 1, m, 0, ZERO_F32, "rstd"), _stream(stream)), "zero_layer_norm")
+        _mat(rstd, 1, m, 0, ZERO_F32, "rstd"), _ops_stream(stream)), "zero_layer_norm")
 
 
 def zero_layer_norm_workspace(m: int, n: int) -> int:
@@ -927,4 +962,4 @@ def zero_layer_norm_backward(dy, lddy: int, dydtype: int, x, ldx: int, xdtype: i
         _mat(dres, m, n, lddres, dxdtype, "dres"), lddres, _mat(dx, m, n, lddx, dxdtype, "dx"),
         lddx, dxdtype, _mat(dweight, 1, n, 0, gdtype, "dweight"),
         _mat(dbias, 1, n, 0, gdtype, "dbias"), gdtype, int(accumulate), _ptr(workspace),
-        workspace_bytes, _stream(stream)), "zero_layer_norm_backward")
+        workspace_bytes, _ops_stream(stream)), "zero_layer_norm_backward")

@@ -1133,7 +1133,7 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
         MODE == LIN_FORWARD && k.epi.drop.on ? drop_offset(k.epi.drop) : 0ull;
     const uint32_t mine = patches + (uint32_t)(warp - kEpiWarp0) * kPatch * 4;
     const BoxEpi be = box_epi<MODE>(k.epi);
-    const DropK drop = k.epi.drop;
+    const DropK& drop = k.epi.drop;
     const bool empty_sum = kb1 == kb0, out_t = k.out_t;
     const uint32_t boxes = g.boxes, boxes0 = patches, second = g.two_slots ? kSlot : 0,
                    chunk_bytes = kSlot + second;

@@ -32,8 +32,9 @@ struct DropK {
   uint32_t all = 0;  // p = 1: every element dropped
   uint32_t least = 0;  // keep a word >= least
   float scale = 1.0f;
-  uint64_t seed = 0, offset = 0;
+  uint64_t offset = 0;
   const uint64_t* d_offset = nullptr;
+  uint32_t keys[20] = {};  // Philox's key of each of the ten rounds, two words
 };
 
 enum LinearMode : int { LIN_FORWARD = 0, LIN_DINPUT = 1, LIN_DWEIGHT = 2 };

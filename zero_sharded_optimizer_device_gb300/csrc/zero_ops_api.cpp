@@ -71,7 +71,10 @@ int drop_k(const zero_dropout_t* r, zk::DropK* out) {
   out->all = least >= 4294967296.0;
   out->least = out->all ? 0xFFFFFFFFu : (uint32_t)least;
   out->scale = out->all ? 0.0f : 1.0f / (1.0f - r->p);
-  out->seed = r->seed;
+  for (uint32_t i = 0; i < 10; ++i) {  // the Weyl sequences of the key's words
+    out->keys[2 * i] = (uint32_t)r->seed + i * 0x9E3779B9u;
+    out->keys[2 * i + 1] = (uint32_t)(r->seed >> 32) + i * 0xBB67AE85u;
+  }
   out->offset = r->offset;
   out->d_offset = r->d_offset;
   return ZERO_OK;

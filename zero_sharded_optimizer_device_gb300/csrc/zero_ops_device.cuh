@@ -7,6 +7,27 @@
 
 namespace zk {
 
+// Launches a kernel that may set up while the one before it on the stream is
+// still running (it executes griddepcontrol.wait before it touches memory).
+template <typename... P, typename... A>
+static cudaError_t launch_next(void (*kernel)(P...), dim3 grid, dim3 block, cudaStream_t st,
+                               A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+__device__ __forceinline__ void after_previous_kernel() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // ------------------------------------------------------------------------
 // 8 consecutive columns of a matrix row as fp32, in one or two 16-byte
 // accesses where the matrix allows it (vec) and all 8 exist, singly
@@ -249,35 +270,24 @@ __device__ __forceinline__ void activate_grad(float value[N], float slope[N], in
 // 2, 3"]: ten rounds of two 32x32 -> 64 multiplications and the Weyl key
 // sequence, integers throughout, so every build draws the same words.
 // ------------------------------------------------------------------------
-__device__ __forceinline__ uint4 philox(uint4 c, uint32_t k0, uint32_t k1) {
+__device__ __forceinline__ uint4 philox(uint4 c, const DropK& d) {
+  // the multipliers from registers: two blocks take 137 cycles per warp, with
+  // immediate operands 172; the rounds' keys straight from the parameters
+  uint32_t m0, m1;
+  asm volatile("mov.u32 %0, 0xD2511F53;" : "=r"(m0));
+  asm volatile("mov.u32 %0, 0xCD9E8D57;" : "=r"(m1));
 #pragma unroll
   for (int r = 0; r < 10; ++r) {
-    const uint64_t p = (uint64_t)c.x * 0xD2511F53u, q = (uint64_t)c.z * 0xCD9E8D57u;
-    c = make_uint4((uint32_t)(q >> 32) ^ c.y ^ k0, (uint32_t)q, (uint32_t)(p >> 32) ^ c.w ^ k1,
-                   (uint32_t)p);
-    k0 += 0x9E3779B9u;
-    k1 += 0xBB67AE85u;
+    const uint64_t p = (uint64_t)c.x * m0, q = (uint64_t)c.z * m1;
+    c = make_uint4((uint32_t)(q >> 32) ^ c.y ^ d.keys[2 * r], (uint32_t)q,
+                   (uint32_t)(p >> 32) ^ c.w ^ d.keys[2 * r + 1], (uint32_t)p);
   }
   return c;
 }
 
-// Drops in place among 8 consecutive columns starting at col (a multiple of
-// 8) of a row; `offset` as drop_offset() gives it.
+// The counter's offset: the host's plus the device's.
 __device__ __forceinline__ uint64_t drop_offset(const DropK& d) {
   return d.offset + (d.d_offset ? *d.d_offset : 0ull);
-}
-__device__ __forceinline__ void drop8(const DropK& d, uint64_t offset, uint32_t row, int64_t col,
-                                      float f[8]) {
-  const uint32_t k0 = (uint32_t)d.seed, k1 = (uint32_t)(d.seed >> 32);
-  const uint32_t g = (uint32_t)(col >> 2), lo = (uint32_t)offset, hi = (uint32_t)(offset >> 32);
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint4 w = philox(make_uint4(g + h, row, lo, hi), k0, k1);
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      f[4 * h + j] = (u[j] >= d.least && !d.all) ? f[4 * h + j] * d.scale : 0.0f;
-  }
 }
 
 // bits = 2 * bits + (w >= least), for below = 2^32 - least: the carry of w +
@@ -295,7 +305,6 @@ __device__ __forceinline__ void push_keep(uint32_t& bits, uint32_t w, uint32_t b
 template <int PER>
 __device__ __forceinline__ uint32_t keep32(const DropK& d, uint64_t offset, uint32_t row,
                                            uint32_t row_step, int64_t col) {
-  const uint32_t k0 = (uint32_t)d.seed, k1 = (uint32_t)(d.seed >> 32);
   const uint32_t lo = (uint32_t)offset, hi = (uint32_t)(offset >> 32), below = 0u - d.least;
   const uint32_t group = (uint32_t)(col >> 2);
   uint32_t keep = 0;
@@ -306,7 +315,7 @@ __device__ __forceinline__ uint32_t keep32(const DropK& d, uint64_t offset, uint
     for (uint32_t h = 0; h < 2; ++h)
       w[h] = philox(make_uint4(group + (g + h) % (2 * PER),
                                row + row_step * ((g + h) / (2 * PER)), lo, hi),
-                    k0, k1);
+                    d);
 #pragma unroll
     for (uint32_t h = 0; h < 2; ++h) {
       push_keep(keep, w[h].x, below);
