@@ -72,7 +72,7 @@ extern "C" {
 #define ZERO_OK 0
 #define ZERO_EINVAL (-1)   /* null/negative/invalid argument */
 #define ZERO_EALIGN (-2)   /* device pointer not 16-byte aligned */
-#define ZERO_ERANGE (-3)   /* group, rank, tensor or window outside the plan */
+#define ZERO_ERANGE (-3)   /* group, rank, tensor or window outside the plan; size too large */
 #define ZERO_EDTYPE (-4)   /* dtype not supported by this call */
 #define ZERO_ENOMEM (-5)   /* host allocation failed */
 #define ZERO_ECUDA (-6)    /* CUDA runtime error; see zero_last_cuda_error() */
@@ -560,8 +560,8 @@ int zero_async_status(int64_t* timeouts, int32_t reset);
  *   - A matrix [rows, cols] is a device pointer and a row distance ld in
  *     elements (ld >= cols; each row is contiguous).  Any element-aligned
  *     base and any ld are accepted; bases and rows on 16-byte boundaries
- *     take the fast paths.  Sizes and ld are below 2^31, except that rows
- *     may be spread over more than 2^31 elements.
+ *     take the fast paths.  Sizes are below 2^31 - 1024 and ld below 2^31;
+ *     a matrix may span more than 2^31 elements.
  *   - A size of 0 is valid: nothing is written where no element exists, and
  *     a sum over nothing is 0.
  *   - Sums, statistics and everything between load and store are fp32; a
@@ -635,7 +635,7 @@ typedef struct {
  * z = bias.  Errors: EINVAL (NULL pointer, negative size, ld below its row,
  * unknown act, layout or nonzero reserved word, p outside [0, 1], y or pre
  * the same pointer as x or w or each other), EALIGN (a pointer not aligned
- * to its element), EDTYPE, ERANGE (size or ld of 2^31 or more), ECUDA. */
+ * to its element), EDTYPE, ERANGE (size or ld beyond the limits above), ECUDA. */
 int zero_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, int32_t w_layout,
                 int64_t m, int64_t n, int64_t k, const zero_linear_epilogue_t* ep, void* y,
                 int64_t ldy, zero_dtype_t ydtype, zero_stream_t stream);

@@ -219,12 +219,9 @@ __device__ __forceinline__ void st_shared4(uint32_t addr, float a, float b, floa
   asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "f"(a), "f"(b), "f"(c),
                "f"(d));
 }
-__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr));
-  return v;
+__device__ __forceinline__ void st_cluster4(uint32_t addr, const uint32_t r[4]) {
+  asm volatile("st.shared::cluster.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]));
 }
 
 // Reads and writes of shared memory above are volatile, hence kept in order,
@@ -441,12 +438,11 @@ __device__ __forceinline__ float4 ld_shared4(uint32_t addr) {
 }
 
 // The block's sums, lying in the patch in the output's orientation (row r of
-// the patch is output row row0 + r): in this CTA's shared memory, or as
-// `pairs` parts at the same address in the cluster's CTAs of this half.
-template <int MODE, bool PARTS>
+// the patch is output row row0 + r).
+template <int MODE>
 __device__ __forceinline__ void finish_block(const EpiK& k, uint32_t keep, uint32_t patch,
-                                             int pairs, uint32_t half, const Block& b,
-                                             const Extent& e, const Sides<MODE>& s, int lane) {
+                                             const Block& b, const Extent& e,
+                                             const Sides<MODE>& s, int lane) {
   float bias[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) bias[j] = 0.0f;
@@ -455,21 +451,8 @@ __device__ __forceinline__ void finish_block(const EpiK& k, uint32_t keep, uint3
 #pragma unroll
   for (int it = 0; it < 4; ++it) {
     const uint32_t at = patch + (uint32_t)((it * 8 + (lane >> 2)) * 36 + (lane & 3) * 8) * 4;
-    float v[8];
-    if constexpr (!PARTS) {
-      const float4 x = ld_shared4(at), y = ld_shared4(at + 16);
-      v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-      v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-      for (int p = 0; p < pairs; ++p) {
-        const uint32_t from = remote(at, 2 * p + half);
-        const float4 x = ld_cluster4(from), y = ld_cluster4(from + 16);
-        v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
-        v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
-      }
-    }
+    const float4 x = ld_shared4(at), y = ld_shared4(at + 16);
+    float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
     const int64_t row = b.row + it * 8;
     if (row < e.rows && b.valid)
       finish8<MODE>(k, row, b, e, bias, s.p[it], s.q[it], keep << (8 * it), v);
@@ -670,20 +653,26 @@ struct ChunkWalk {
   int t, ti, tj, cc, count;
 };
 template <int WIDTH>
-__device__ __forceinline__ void enter_tile(const TileK& g, int64_t cols, ChunkWalk& w) {
+__device__ __forceinline__ void enter_tile(const TileK& g, int64_t cols, int split,
+                                           ChunkWalk& w) {
   tile_at(g, w.t, w.ti, w.tj);
   w.cc = 0;
   const int64_t left = cols - (int64_t)w.tj * g.bn;
   w.count = w.tj < 0 ? 0 : (int)((left < g.bn ? left : g.bn) + WIDTH - 1) / WIDTH;
+  if (g.splits > 1) {  // half of the tile's columns
+    const int half = g.bn / WIDTH / 2;
+    w.cc = split * half;
+    if (w.count > w.cc + half) w.count = w.cc + half;
+  }
 }
 template <int WIDTH>
-__device__ __forceinline__ void next_chunk(const TileK& g, int64_t cols, int tiles, int step,
-                                           ChunkWalk& w) {
+__device__ __forceinline__ void next_chunk(const TileK& g, int64_t cols, int split, int tiles,
+                                           int step, ChunkWalk& w) {
   ++w.cc;
   while (w.cc >= w.count) {
     w.t += step;
     if (w.t >= tiles) return;
-    enter_tile<WIDTH>(g, cols, w);
+    enter_tile<WIDTH>(g, cols, split, w);
   }
 }
 
@@ -693,7 +682,7 @@ template <int MODE, int FORM>
 __device__ __forceinline__ void box_traffic(const BoxMaps& maps, const ProductK& k,
                                             const TileK& g, uint32_t boxes, uint32_t efull,
                                             uint32_t edone, int first, int tiles, int step,
-                                            uint32_t half, volatile int* dead) {
+                                            uint32_t half, int split, volatile int* dead) {
   constexpr bool wide = FORM == BOX_F32;
   constexpr int W = wide ? 32 : 64;
   const uint32_t ring = g.boxes, second = g.two_slots ? kSlot : 0, chunk_bytes = kSlot + second;
@@ -707,9 +696,9 @@ __device__ __forceinline__ void box_traffic(const BoxMaps& maps, const ProductK&
   in.t = first;
   in.count = in.cc = 0;
   if (first < tiles) {
-    enter_tile<W>(g, cols, in);
-    in.cc = -1;
-    next_chunk<W>(g, cols, tiles, step, in);
+    enter_tile<W>(g, cols, split, in);
+    --in.cc;
+    next_chunk<W>(g, cols, split, tiles, step, in);
   }
   out = in;
   uint32_t ahead = 0, lb = 0, sb = 0, sph = 0;  // ahead: chunks whose memory is in use
@@ -735,7 +724,7 @@ __device__ __forceinline__ void box_traffic(const BoxMaps& maps, const ProductK&
       __syncwarp();
       ++ahead;
       if (++lb == ring) lb = 0;
-      next_chunk<W>(g, cols, tiles, step, in);
+      next_chunk<W>(g, cols, split, tiles, step, in);
     }
     live = live && bar_wait(edone + 8 * sb, sph, dead);
     const uint32_t at = boxes + sb * chunk_bytes, slot1 = at + second;
@@ -767,7 +756,7 @@ __device__ __forceinline__ void box_traffic(const BoxMaps& maps, const ProductK&
       sb = 0;
       sph ^= 1;
     }
-    next_chunk<W>(g, cols, tiles, step, out);
+    next_chunk<W>(g, cols, split, tiles, step, out);
   }
   // after a wait that gave up: the boxes in flight land before the CTA returns
   for (; !live && ahead > 0; --ahead) {
@@ -908,6 +897,35 @@ struct Masks {
   }
 };
 
+// ---------------------------------------------------------------------------
+// A contraction split in two: both pairs of a cluster hold sums of the whole
+// tile.  Each pair finishes half of its 32 x 32 blocks; it writes the sums of
+// the other half into the memory of the partner's CTA with the same rows (the
+// operand ring, free by then) and adds what it finds in its own.  Two addends:
+// the same result whichever pair adds.  4 KiB per block, 16-byte units of
+// consecutive threads side by side.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ bool owns_block(int split, int cc, int chunks, int w) {
+  return (chunks == 1 ? (w & 1) : (int)(cc >= chunks / 2)) == split;
+}
+__device__ __forceinline__ uint32_t part_at(uint32_t ring, int cc, int w, int lane) {
+  return ring + (uint32_t)((cc * 4 + w) * 4096 + lane * 16);
+}
+__device__ __forceinline__ void push_part(uint32_t there, const uint32_t r[32]) {
+#pragma unroll
+  for (int u = 0; u < 8; ++u) st_cluster4(there + u * 512, r + 4 * u);
+}
+__device__ __forceinline__ void add_part(uint32_t here, uint32_t r[32]) {
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const float4 x = ld_shared4(here + u * 512);
+    r[4 * u] = __float_as_uint(__uint_as_float(r[4 * u]) + x.x);
+    r[4 * u + 1] = __float_as_uint(__uint_as_float(r[4 * u + 1]) + x.y);
+    r[4 * u + 2] = __float_as_uint(__uint_as_float(r[4 * u + 2]) + x.z);
+    r[4 * u + 3] = __float_as_uint(__uint_as_float(r[4 * u + 3]) + x.w);
+  }
+}
+
 // The gradient of bias element i.
 __device__ __forceinline__ void store_bias(const ProductK& k, const TileK& g, int64_t i,
                                            float v) {
@@ -936,7 +954,7 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
   const uint32_t ring = smem_u32(smem);
   const uint32_t patches = ring + g.stages * stage_bytes;
   const uint32_t ones = patches + (BOX ? g.boxes * kSlot * (g.two_slots ? 2 : 1)
-                                       : S == 1 ? kEpiWarps * kPatch * 4 : 0);
+                                       : kEpiWarps * kPatch * 4);
   const uint32_t full = smem_u32(bars), empty = full + 8 * kMaxStages;
   const uint32_t tfull = empty + 8 * kMaxStages, tempty = tfull + 16, ready = tempty + 16;
   const uint32_t efull = ready + 8, edone = efull + 8 * kMostBoxes;
@@ -1008,8 +1026,9 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
   }
   // The last barrier of the cluster, at which nobody signals another CTA or
   // reads its memory any more: warp 3 only moves this CTA's own boxes.
-  const bool early = BOX && warp == 3;
+  const bool early = BOX && warp == 3 && S == 1;
   if (early) cluster_arrive();
+  int barriers = 0;  // of a split's two, passed so far
 
   if (warp == 0) {
     const uint32_t full_lead = remote(full, leader);
@@ -1122,8 +1141,12 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
     }
     __syncwarp();
   } else if (BOX && warp == 3) {
+    for (; S > 1 && barriers < 2; ++barriers) {  // its boxes come after the exchange
+      cluster_arrive();
+      cluster_wait();
+    }
     box_traffic<MODE, FORM>(maps, k, g, patches, efull, edone, first, tiles, clusters, half,
-                            &dead);
+                            split, &dead);
     __syncwarp();
   } else if (warp >= kEpiWarp0 && warp < kEpiWarp0 + kEpiWarps) {
     const int w = (warp - kEpiWarp0) & 3, set = (warp - kEpiWarp0) >> 2;  // lanes 32 w...
@@ -1147,12 +1170,13 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
       const int64_t i0 = (int64_t)ti * 256 + half * kRowsCta + w * 32;
       const int chunks = tj >= 0 ? bn / 32 : 1;
       Masks masks{};
-      if (MODE == LIN_FORWARD && S == 1 && drop.on) {
+      if (MODE == LIN_FORWARD && drop.on) {
 #pragma unroll 1
         for (int q = 0; 2 * q + set < chunks; ++q) {
           // the 32 columns this warp takes q-th, as the loops below take them
           const int64_t j0 = (int64_t)tj * bn + (2 * q + set) * 32;
           if (i0 >= rows || j0 >= cols) break;
+          if (S > 1 && !owns_block(split, 2 * q + set, chunks, w)) continue;
           if (BOX) {
             masks.set(q, keep32<4>(drop, offset, (uint32_t)(i0 + lane), 0, j0));
           } else {
@@ -1166,19 +1190,40 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
       if (!ok) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint32_t d = tmem + acc * bn + ((uint32_t)(w * 32) << 16);
+      const bool sums =
+          MODE == LIN_DWEIGHT && g.bias_fused && (g.bias_b ? ti : tj) == 0 && set == 0;
+      if (S > 1) {
+        cluster_arrive();
+        cluster_wait();  // both pairs' products are done: the rings are free
+        for (int cc = set; cc < chunks; cc += 2) {
+          if (tj < 0 ? split == 0 : owns_block(split, cc, chunks, w)) continue;
+          uint32_t r[32];
+          tmem_load32(d + cc * 32, r);
+          push_part(remote(part_at(ring, cc, w, lane), rank ^ 2), r);
+        }
+        if (sums && split == 1) {
+          uint32_t r[32];
+          tmem_load32(tmem + bias_column(g, acc) + ((uint32_t)(w * 32) << 16), r);
+          push_part(remote(part_at(ring, chunks, w, lane), rank ^ 2), r);
+        }
+        cluster_arrive();
+        cluster_wait();
+        barriers = 2;
+      }
       if (BOX && tj >= 0) {
-        const int64_t left = cols - (int64_t)tj * bn;
-        const int count = (int)((left < bn ? left : bn) + kWidth - 1) / kWidth;
-        for (int cc = 0; cc < count; ++cc) {
+        ChunkWalk at{t, ti, tj, 0, 0};
+        enter_tile<kWidth>(g, cols, split, at);
+        for (int cc = at.cc; cc < at.count; ++cc) {
           const uint32_t b = eb, bph = eph;
-          if (++eb == (uint32_t)boxes) {
+          if (++eb == boxes) {
             eb = 0;
             eph ^= 1;
           }
           if (kWidth == 32 && (cc & 1) != set) continue;
-          const int inner = kWidth == 64 ? set * 32 : 0;
+          const int block = kWidth == 64 ? 2 * cc + set : cc;
           uint32_t r[32];
-          tmem_load32(d + cc * kWidth + inner, r);
+          tmem_load32(d + block * 32, r);
+          if (S > 1) add_part(part_at(ring, block, w, lane), r);
           if (empty_sum) {
 #pragma unroll
             for (int q = 0; q < 32; ++q) r[q] = 0;  // an empty contraction
@@ -1189,63 +1234,57 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
           float v[32];
 #pragma unroll
           for (int q = 0; q < 32; ++q) v[q] = __uint_as_float(r[q]);
-          box_chunk<MODE, FORM>(be, masks.at(kWidth == 64 ? cc : cc >> 1),
-                                boxes0 + b * chunk_bytes, second, w * 32 + lane,
-                                (int64_t)tj * bn + cc * kWidth + inner, set * 4, cols, v);
+          box_chunk<MODE, FORM>(be, masks.at(block >> 1), boxes0 + b * chunk_bytes, second,
+                                w * 32 + lane, (int64_t)tj * bn + block * 32, set * 4, cols, v);
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) bar_arrive(edone + 8 * b);
         }
-      } else
-      for (int cc = set; cc < chunks; cc += 2) {
-        const int64_t j0 = (int64_t)tj * bn + cc * 32;
-        if (S == 1 && tj >= 0 && (i0 >= rows || j0 >= cols)) continue;
-        const Block b = block_of(out_t ? j0 : i0, out_t ? i0 : j0, e, lane);
-        Sides<MODE> sides;
-        if (S == 1 && tj >= 0 && k.epi.vec) load_sides<MODE>(k.epi, b, e, sides);
-        uint32_t r[32];
-        tmem_load32(d + cc * 32, r);
-        if (empty_sum) {
+      } else {
+        for (int cc = set; cc < chunks; cc += 2) {
+          const int64_t j0 = (int64_t)tj * bn + cc * 32;
+          if (tj >= 0 && (i0 >= rows || j0 >= cols)) continue;
+          if (S > 1 && !(tj < 0 ? split == 0 : owns_block(split, cc, chunks, w))) continue;
+          const Block b = block_of(out_t ? j0 : i0, out_t ? i0 : j0, e, lane);
+          Sides<MODE> sides;
+          if (tj >= 0 && k.epi.vec) load_sides<MODE>(k.epi, b, e, sides);
+          uint32_t r[32];
+          tmem_load32(d + cc * 32, r);
+          if (S > 1) add_part(part_at(ring, cc, w, lane), r);
+          if (empty_sum) {
 #pragma unroll
-          for (int q = 0; q < 32; ++q) r[q] = 0;  // an empty contraction
-        }
-        const uint32_t patch = S == 1 ? mine : ring + (uint32_t)(cc * 4 + w) * kPatch * 4;
-        if (S == 1 && MODE == LIN_DWEIGHT && tj < 0) {
-          store_bias(k, g, i0 + lane, __uint_as_float(r[0]));
-          continue;
-        }
-        if (out_t) {
+            for (int q = 0; q < 32; ++q) r[q] = 0;  // an empty contraction
+          }
+          if (MODE == LIN_DWEIGHT && tj < 0) {
+            store_bias(k, g, i0 + lane, __uint_as_float(r[0]));
+            continue;
+          }
+          if (out_t) {
 #pragma unroll
-          for (int q = 0; q < 32; ++q)
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(patch + (q * 36 + lane) * 4), "r"(r[q]));
-        } else {
+            for (int q = 0; q < 32; ++q)
+              asm volatile("st.shared.b32 [%0], %1;" ::"r"(mine + (q * 36 + lane) * 4), "r"(r[q]));
+          } else {
 #pragma unroll
-          for (int q = 0; q < 32; q += 4)
-            st_shared4(patch + (lane * 36 + q) * 4, __uint_as_float(r[q]),
-                       __uint_as_float(r[q + 1]), __uint_as_float(r[q + 2]),
-                       __uint_as_float(r[q + 3]));
-        }
-        if (S == 1) {
+            for (int q = 0; q < 32; q += 4)
+              st_shared4(mine + (lane * 36 + q) * 4, __uint_as_float(r[q]),
+                         __uint_as_float(r[q + 1]), __uint_as_float(r[q + 2]),
+                         __uint_as_float(r[q + 3]));
+          }
           __syncwarp();
           if (k.epi.vec)
-            finish_block<MODE, false>(k.epi, masks.at(cc >> 1), patch, 1, half, b, e, sides, lane);
+            finish_block<MODE>(k.epi, masks.at(cc >> 1), mine, b, e, sides, lane);
           else
-            finish_columns<MODE>(k.epi, masks.at(cc >> 1), patch, out_t ? j0 : i0,
+            finish_columns<MODE>(k.epi, masks.at(cc >> 1), mine, out_t ? j0 : i0,
                                  out_t ? i0 : j0, e, lane);
           __syncwarp();
         }
       }
-      if (MODE == LIN_DWEIGHT && g.bias_fused && (g.bias_b ? ti : tj) == 0 && set == 0) {
+      if (sums && split == 0) {
         uint32_t r[32];
         tmem_load32(tmem + bias_column(g, acc) + ((uint32_t)(w * 32) << 16), r);
-        const float v = empty_sum ? 0.0f : __uint_as_float(r[0]);
-        if (S == 1)
-          store_bias(k, g, (int64_t)(g.bias_b ? tj : ti) * 256 + half * kRowsCta + w * 32 + lane,
-                     v);
-        else  // a block of its own, behind the tile's
-          asm volatile("st.shared.f32 [%0], %1;" ::"r"(
-                           ring + (uint32_t)((chunks * 4 + w) * kPatch + lane) * 4),
-                       "f"(v));
+        if (S > 1) add_part(part_at(ring, chunks, w, lane), r);
+        store_bias(k, g, (int64_t)(g.bias_b ? tj : ti) * 256 + half * kRowsCta + w * 32 + lane,
+                   empty_sum ? 0.0f : __uint_as_float(r[0]));
       }
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
@@ -1288,47 +1327,11 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
   }
   __syncwarp();
 
-  if (S > 1) {
-    // every pair's sums now lie in its own shared memory: pair p finishes the
-    // blocks p, p + S, ... of its half, adding the pairs' parts in order
+  // The exchange of a split contraction passes two barriers of the cluster:
+  // so do the warps that have no part in it.
+  for (int q = barriers; S > 1 && q < 2; ++q) {
     cluster_arrive();
     cluster_wait();
-    if (warp >= kEpiWarp0 && warp < kEpiWarp0 + kEpiWarps && !dead) {
-      const Extent e{k.out_t ? k.cols : k.rows, k.out_t ? k.rows : k.cols};
-      const uint64_t offset =
-          MODE == LIN_FORWARD && k.epi.drop.on ? drop_offset(k.epi.drop) : 0ull;
-      int ti, tj;
-      tile_at(g, first, ti, tj);
-      const int main = 4 * (tj >= 0 ? g.bn / 32 : 1);
-      const bool sums = MODE == LIN_DWEIGHT && g.bias_fused && (g.bias_b ? ti : tj) == 0;
-      const int blocks = main + (sums ? 4 : 0);
-      for (int b = split + S * (warp - kEpiWarp0); b < blocks; b += S * kEpiWarps) {
-        const int64_t i0 = (int64_t)ti * 256 + half * kRowsCta + (b & 3) * 32;
-        const int64_t j0 = (int64_t)tj * g.bn + (b >> 2) * 32;
-        const uint32_t patch = ring + (uint32_t)b * kPatch * 4;
-        if (MODE == LIN_DWEIGHT && (tj < 0 || b >= main)) {
-          const uint32_t at = patch + (k.out_t || tj >= 0 ? lane : lane * 36) * 4;
-          float v = 0.0f;
-          for (int p = 0; p < S; ++p) {
-            float x;
-            asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                         : "=f"(x)
-                         : "r"(remote(at, 2 * p + half)));
-            v += x;
-          }
-          const int64_t tile = tj < 0 ? ti : g.bias_b ? tj : ti;
-          store_bias(k, g, tile * 256 + half * kRowsCta + (b & 3) * 32 + lane, v);
-        } else if (i0 < k.rows && j0 < k.cols) {
-          const Block o = block_of(k.out_t ? j0 : i0, k.out_t ? i0 : j0, e, lane);
-          Sides<MODE> sides;
-          load_sides<MODE>(k.epi, o, e, sides);
-          uint32_t keep = 0;
-          if (MODE == LIN_FORWARD && k.epi.drop.on)
-            keep = keep32<1>(k.epi.drop, offset, (uint32_t)o.row, 8, o.col);
-          finish_block<MODE, true>(k.epi, keep, patch, S, half, o, e, sides, lane);
-        }
-      }
-    }
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncwarp();
@@ -1409,7 +1412,7 @@ static bool box_map(CUtensorMap* map, const Mat& a, int64_t rows, int64_t cols, 
 // Shared memory beside the operand ring, and the ring's stages in what is left.
 static int side_bytes(const TileK& g, int form) {
   return (g.bias_tiles || g.bias_fused ? kOnesBytes : 0) + (form >= BOX_BF16 ? g.boxes * kSlot * (g.two_slots ? 2 : 1)
-                       : g.splits == 1 ? kEpiWarps * kPatch * 4 : 0);
+                           : kEpiWarps * kPatch * 4);
 }
 static int stages_for(const TileK& g, int form) {
   const int n = (kSmemMost - 1024 - side_bytes(g, form)) / (kBytesA + g.bn * kDeep);
@@ -1487,10 +1490,11 @@ static cudaError_t launch_mode(const ProductK& in, cudaStream_t st) {
   // Width and split by a cost model: waves of tiles times the cycles of one.
   // A 64-deep step takes 520 cycles at BN = 256 (the tensor cores' own time)
   // and 430 at 128 and below, where loading A's rows decides; the last tile's
-  // epilogue 30 per column; joining two halves of a contraction 5000 and 42
-  // per column.  (Measured, us, one part / two: 1 x 4096 x 4096 16.9 / 12.9,
-  // 256 x 4096 x 4096 18.3 / 16.8, 2048 x 1024 x 4096 19.0 at BN = 128, 23.4 /
-  // 22.5 at 256; four parts, clusters of 8, always lost.)
+  // epilogue 25 per column; joining two halves of a contraction 2500 and 15
+  // per column, and a further wave of those its start as well.  (Measured, us,
+  // one part / two: 1 x 4096 x 4096 17.4 / 11.9, 1024 x 1024 x 4096 at BN = 128
+  // 18.4 / 14.1, 2048 x 1024 x 4096 at BN = 256 23.4 / 18.0, 1024 x 2304 x 768
+  // at 128 8.8 / 16.6; four parts, clusters of 8, always lost.)
   double best = 0;
   for (int bn = 32; bn <= 256; bn *= 2) {
     if (!k.b_c && bn < 128) continue;       // blocks of 64 rows per CTA
@@ -1501,7 +1505,8 @@ static cudaError_t launch_mode(const ProductK& in, cudaStream_t st) {
       const double waves = (double)((tiles_i * tiles_j * S + pairs - 1) / pairs);
       const double step = bn == 256 ? 520 : 430;
       const double cost =
-          waves * ((double)kblocks / S * step + (S > 1 ? 5000 + 42 * bn : 0)) + 30 * bn;
+          waves * ((double)kblocks / S * step + (S > 1 ? 2500 + 15 * bn : 0)) +
+          (S > 1 ? (waves - 1) * 8000 : 0) + 25 * bn;
       if (best == 0 || cost < best) {
         best = cost;
         g.bn = bn;
@@ -1541,13 +1546,14 @@ static cudaError_t launch_mode(const ProductK& in, cudaStream_t st) {
   const EpiK& o = k.epi;
   const bool pre_ok = MODE == LIN_FORWARD ? box_output(o.pre, k.rows, k.cols)
                                           : boxable(o.pre, k.rows);
-  if (k.out_t || g.splits > 1 || k.rows <= 0 || k.cols <= 0 || !pre_ok ||
+  // (each half of a split contraction stores whole boxes)
+  const int width = o.out.dtype == ZERO_F32 ? 32 : 64;
+  if (k.out_t || g.bn < width * g.splits || k.rows <= 0 || k.cols <= 0 || !pre_ok ||
       !box_output(o.out, k.rows, k.cols) || !boxable(o.gate, k.rows) ||
       !box_output(o.dgate, k.rows, k.cols) ||
       !boxable(o.residual, k.rows) || (o.residual.p && o.residual.dtype != o.out.dtype))
     return launch_tiles<MODE, PATCH>(ma, mb, maps, k, g, st);
   const bool wide = o.out.dtype == ZERO_F32;
-  const int width = wide ? 32 : 64;
   const Mat& extra = MODE == LIN_FORWARD ? o.residual : o.dgate;
   if (!box_map(&maps.out, o.out, k.rows, k.cols, width) ||
       !box_map(&maps.pre, o.pre, k.rows, k.cols, width) ||

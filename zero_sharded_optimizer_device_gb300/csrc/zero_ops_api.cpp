@@ -26,11 +26,12 @@ int cuda_status(cudaError_t e) {
   return ZERO_ECUDA;
 }
 
-constexpr int64_t kMost = (int64_t)1 << 31;  // sizes and row distances stay below
+constexpr int64_t kMost = (int64_t)1 << 31;   // row distances stay below,
+constexpr int64_t kMostSize = kMost - 1024;  // sizes so far below that tiles rounded up do too
 
 int check_sizes(int64_t a, int64_t b, int64_t c = 0) {
   if (a < 0 || b < 0 || c < 0) return ZERO_EINVAL;
-  return a < kMost && b < kMost && c < kMost ? ZERO_OK : ZERO_ERANGE;
+  return a < kMostSize && b < kMostSize && c < kMostSize ? ZERO_OK : ZERO_ERANGE;
 }
 
 int check_dtype(int d) { return d == ZERO_F32 || d == ZERO_BF16 ? ZERO_OK : ZERO_EDTYPE; }
