@@ -184,6 +184,30 @@ def test_linear_without_inputs(cuda, Z, kn):
         assert bool((Y.buf == -77.0).all())
 
 
+@pytest.mark.parametrize("m,n,k", [(16, 96, 9000), (300, 264, 9000), (300, 259, 9001), (700, 2048, 8192)])
+def test_fp32_results_of_long_sums(cuda, Z, m, n, k):
+    """The tensor cores' additions truncate: each of the 48 of a round of 768
+    terms loses half a unit in the last place (2^-24 of the running sum) on
+    average, and rounds are added to nearest.  So the error of an fp32 result,
+    in 2-norms, stays below 48 * 2^-24 = 2.9e-6 however long the sum."""
+    g = torch.Generator().manual_seed(6)
+    x, w, dy = (randn(g, *s).cuda() for s in ((m, k), (n, k), (k, n)))
+    y, dw, db = torch.empty(m, n, device="cuda"), torch.empty(n, m, device="cuda"), torch.empty(n, device="cuda")
+    rel = lambda a, b: ((a.double() - b).norm() / b.norm()).item()  # noqa: E731
+    Z.zero_linear(x, k, w, k, 0, m, n, k, None, y, n, Z.ZERO_F32)
+    assert rel(y, x.double() @ w.double().T) < 2.9e-6
+    Z.zero_linear_dinput(x, k, w.T.contiguous(), n, 0, m, k, n, None, y, n, Z.ZERO_F32)
+    assert rel(y, x.double() @ w.double().T) < 2.9e-6
+    xt = x.T.contiguous()
+    for kn in (0, 1):
+        out = dw if not kn else dw.view(m, n)
+        Z.zero_linear_dweight(dy, n, xt, m, k, n, m, kn, out, n if kn else m, Z.ZERO_F32, db,
+                              Z.ZERO_F32)
+        want = xt.double().T @ dy.double()
+        assert rel(out, want if kn else want.T) < 2.9e-6
+        assert rel(db, dy.double().sum(0)) < 2.9e-6
+
+
 def test_linear_dropped_elements_hide_infinities(cuda, Z):
     """A dropped element contributes exactly 0, whatever the product holds;
     NaN and infinities reach the kept ones, in their own rows alone."""

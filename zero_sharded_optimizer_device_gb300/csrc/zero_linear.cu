@@ -41,6 +41,7 @@ constexpr int kBytesA = kRowsCta * kDeep * 2;
 constexpr int kEpiWarp0 = 4, kEpiWarps = 8, kGenWarp0 = 12, kGenWarps = 4;
 constexpr int kPatch = 32 * 36;        // floats of a 32 x 32 patch, rows 36 apart
 constexpr int kMaxStages = 9;
+constexpr int kRound = 12;             // 64-deep steps of a round (see launch_mode)
 constexpr int kOnesBytes = 2048;
 constexpr int kSlot = 16384;           // a box of 128 rows of 128 bytes
 constexpr int kMostBoxes = 3;          // chunks of boxes in the ring
@@ -65,11 +66,14 @@ struct TileK {
   int bias_b;      // rows of B (else of A)
   int kblocks, splits, bn, stages;
   int split_log2, clusters;          // splits = 1 << split_log2; clusters launched
+  int round;                         // steps whose sums the tensor cores keep (see launch_mode)
+  int acc_sets;                      // sets of sums in tensor memory used in turn
   int i_fast;                        // consecutive tiles differ in i (else in j)
   int gen_a, gen_b;                  // elements per plain load; 0: by TMA
   int boxes;                         // ring of box chunks (box forms)
   int two_slots;                     // a chunk holds two slots
   uint32_t tmem_cols;
+  int bias_in;                       // bytes of staged forward biases
 };
 
 // Box forms: the side operands and outputs (see box_chunk).
@@ -215,6 +219,44 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t r[32]) {
       : "r"(addr));
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
+__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t r[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t r[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31]), "r"(addr)
+      : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+// r += the 32 (16) columns at addr.
+__device__ __forceinline__ void tmem_add32(uint32_t addr, uint32_t r[32]) {
+  uint32_t q[32];
+  tmem_load32(addr, q);
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    r[i] = __float_as_uint(__uint_as_float(r[i]) + __uint_as_float(q[i]));
+}
+__device__ __forceinline__ void tmem_add16(uint32_t addr, uint32_t r[16]) {
+  uint32_t q[16];
+  tmem_load16(addr, q);
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    r[i] = __float_as_uint(__uint_as_float(r[i]) + __uint_as_float(q[i]));
+}
 __device__ __forceinline__ void st_shared4(uint32_t addr, float a, float b, float c, float d) {
   asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "f"(a), "f"(b), "f"(c),
                "f"(d));
@@ -332,7 +374,16 @@ __device__ __forceinline__ void tile_at(const TileK& g, int t, int& i, int& j) {
 // Where the sums for the bias lie in tensor memory beside the products of set
 // acc: one tile per cluster leaves the second set free, else behind both sets.
 __device__ __forceinline__ uint32_t bias_column(const TileK& g, uint32_t acc) {
+  if (g.round) return (uint32_t)(3 * g.bn) + 32 * acc;
   return (uint32_t)(g.tiles_i * g.tiles_j <= g.clusters ? g.bn : 2 * g.bn) + 32 * acc;
+}
+// Rounds of a contraction (see launch_mode), and the column of the sum of the
+// rounds before the last.
+__device__ __forceinline__ int rounds_of(const TileK& g, int steps) {
+  return g.round && steps > 0 ? (steps + g.round - 1) / g.round : 1;
+}
+__device__ __forceinline__ uint32_t sum_column(const TileK& g) {
+  return (uint32_t)(g.acc_sets * g.bn);
 }
 
 // A warp finishes a 32 x 32 block of the output (rows row0.., columns col0..)
@@ -441,13 +492,14 @@ __device__ __forceinline__ float4 ld_shared4(uint32_t addr) {
 // the patch is output row row0 + r).
 template <int MODE>
 __device__ __forceinline__ void finish_block(const EpiK& k, uint32_t keep, uint32_t patch,
-                                             const Block& b, const Extent& e,
+                                             uint32_t biases, const Block& b, const Extent& e,
                                              const Sides<MODE>& s, int lane) {
-  float bias[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) bias[j] = 0.0f;
-  if (MODE == LIN_FORWARD && k.bias.p && b.valid)
-    load8(k.bias, 0, b.col, b.valid, bias, Extent{1, e.cols}, ZERO_SITE_LINEAR_OUT);
+  float4 b0 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), b1 = b0;
+  if (MODE == LIN_FORWARD && k.bias.p) {
+    b0 = ld_shared4(biases + (uint32_t)(lane & 3) * 32);
+    b1 = ld_shared4(biases + (uint32_t)(lane & 3) * 32 + 16);
+  }
+  const float bias[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
 #pragma unroll
   for (int it = 0; it < 4; ++it) {
     const uint32_t at = patch + (uint32_t)((it * 8 + (lane >> 2)) * 36 + (lane & 3) * 8) * 4;
@@ -509,7 +561,6 @@ struct BoxEpi {
   bool bias, gate, pre, residual, dgate, old, drop;
   int act;
   float scale;
-  Mat b;
 };
 template <int MODE>
 __device__ __forceinline__ BoxEpi box_epi(const EpiK& k) {
@@ -523,128 +574,115 @@ __device__ __forceinline__ BoxEpi box_epi(const EpiK& k) {
   e.act = k.act;
   e.drop = MODE == LIN_FORWARD && k.drop.on;
   e.scale = k.drop.scale;
-  e.b = k.bias;
   return e;
 }
 
-// A thread's 32 sums v of row `row` of the tile, columns col.. of the output,
-// through the epilogue; unit0: their first 16-byte unit in a bf16 row.  Each
-// step runs over all 32 before the next: a branch per step, not per value.
+// Half a block: 16 sums v of a thread's row `row` of the tile through the
+// epilogue; unit: their first 16-byte unit in a bf16 row of the chunk's boxes,
+// f32_unit in an fp32 one; bias: where their columns' biases lie.  Each step
+// runs over all 16 before the next (a branch per step, not per value), and the
+// halves are a loop: fetching longer straight-line code took longer than
+// running it.
 template <int MODE, int FORM>
-__device__ __forceinline__ void box_chunk(const BoxEpi& k, uint32_t keep, uint32_t chunk,
-                                          uint32_t second, int row, int64_t col, int unit0,
-                                          int64_t cols, float v[32]) {
+__device__ __forceinline__ void box_half(const BoxEpi& k, uint32_t keep, uint32_t chunk,
+                                         uint32_t second, int row, int unit, uint32_t bias,
+                                         float v[16]) {
   constexpr bool wide = FORM == BOX_F32;
   const uint32_t slot1 = chunk + second;
   float f[8];
+  // the two bf16 units of slot 0 (dinput: of the box at `base`) and where the
+  // result's two groups of 8 go
+  auto bf16_at = [&](uint32_t base, int i) {
+    return base + (wide ? at64(row, unit + i) : at128(row, unit + i));
+  };
+  auto old8 = [&](uint32_t base, int i) {
+    if constexpr (wide)
+      lds_f32(base, row, unit + i, f);
+    else
+      from_bf16(lds16(base + at128(row, unit + i)), f);
+  };
+  auto put8 = [&](uint32_t base, int i) {
+    if constexpr (wide)
+      sts_f32(base, row, unit + i, v + 8 * i);
+    else
+      sts16(base + at128(row, unit + i), pack8(v + 8 * i));
+  };
   if constexpr (MODE == LIN_FORWARD) {
     if (k.bias) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int64_t left = cols - col - 8 * i;
-        if (left > 0) {
-          load8(k.b, 0, col + 8 * i, left < 8 ? (int)left : 8, f, Extent{1, cols},
-                ZERO_SITE_LINEAR_OUT);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[8 * i + j] += f[j];
-        }
+        const float4 b = ld_shared4(bias + 16 * i);
+        v[4 * i] += b.x;
+        v[4 * i + 1] += b.y;
+        v[4 * i + 2] += b.z;
+        v[4 * i + 3] += b.w;
       }
     }
-    uint4 gate[4];
+    uint4 gate[2];
     if (k.gate) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        gate[i] = lds16(chunk + (wide ? at64(row, i) : at128(row, unit0 + i)));
+      gate[0] = lds16(bf16_at(chunk, 0));
+      gate[1] = lds16(bf16_at(chunk, 1));
     }
     if (k.pre) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        sts16(chunk + (wide ? at64(row, i) : at128(row, unit0 + i)), pack8(v + 8 * i));
+      sts16(bf16_at(chunk, 0), pack8(v));
+      sts16(bf16_at(chunk, 1), pack8(v + 8));
     }
-    activate<32>(v, k.act);
+    activate<16>(v, k.act);
     if (k.gate) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 2; ++i) {
         from_bf16(gate[i], f);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[8 * i + j] *= f[j];
       }
     }
-    if (k.drop) apply_keep<32>(keep, k.scale, v);
+    if (k.drop) apply_keep<16>(keep, k.scale, v);
     if (k.residual) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (wide)
-          lds_f32(slot1, row, i, f);
-        else
-          from_bf16(lds16(slot1 + at128(row, unit0 + i)), f);
+      for (int i = 0; i < 2; ++i) {
+        old8(slot1, i);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[8 * i + j] += f[j];
       }
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (wide)
-        sts_f32(slot1, row, i, v + 8 * i);
-      else
-        sts16(slot1 + at128(row, unit0 + i), pack8(v + 8 * i));
-    }
+    put8(slot1, 0);
+    put8(slot1, 1);
   } else if constexpr (MODE == LIN_DINPUT) {
-    const uint32_t pre_at = wide ? slot1 : chunk, gate_at = wide ? slot1 + kSlot / 2 : slot1;
+    const uint32_t pre_box = wide ? slot1 : chunk, gate_box = wide ? slot1 + kSlot / 2 : slot1;
     if (k.pre) {
+      float value[16], slope[16];
+      from_bf16(lds16(bf16_at(pre_box, 0)), value);
+      from_bf16(lds16(bf16_at(pre_box, 1)), value + 8);
+      activate_grad<16>(value, slope, k.act);
+      if (k.gate) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {  // 16 values at a time: three arrays of them are live
-        float value[16], slope[16];
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t at = bf16_at(gate_box, i);
+          from_bf16(lds16(at), f);
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          from_bf16(lds16(pre_at + (wide ? at64(row, 2 * h + i) : at128(row, unit0 + 2 * h + i))),
-                    value + 8 * i);
-        activate_grad<16>(value, slope, k.act);
-        float* w = v + 16 * h;
-        if (k.gate) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t at =
-                gate_at + (wide ? at64(row, 2 * h + i) : at128(row, unit0 + 2 * h + i));
-            from_bf16(lds16(at), f);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              value[8 * i + j] *= w[8 * i + j];
-              slope[8 * i + j] *= f[j];
-            }
-            if (k.dgate) sts16(at, pack8(value + 8 * i));
+          for (int j = 0; j < 8; ++j) {
+            value[8 * i + j] *= v[8 * i + j];
+            slope[8 * i + j] *= f[j];
           }
+          if (k.dgate) sts16(at, pack8(value + 8 * i));
         }
-#pragma unroll
-        for (int j = 0; j < 16; ++j) w[j] *= slope[j];
       }
-    }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (wide)
-        sts_f32(chunk, row, i, v + 8 * i);
-      else
-        sts16(chunk + at128(row, unit0 + i), pack8(v + 8 * i));
+      for (int j = 0; j < 16; ++j) v[j] *= slope[j];
     }
+    put8(chunk, 0);
+    put8(chunk, 1);
   } else {
     if (k.old) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (wide)
-          lds_f32(chunk, row, i, f);
-        else
-          from_bf16(lds16(chunk + at128(row, unit0 + i)), f);
+      for (int i = 0; i < 2; ++i) {
+        old8(chunk, i);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[8 * i + j] += f[j];
       }
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (wide)
-        sts_f32(chunk, row, i, v + 8 * i);
-      else
-        sts16(chunk + at128(row, unit0 + i), pack8(v + 8 * i));
-    }
+    put8(chunk, 0);
+    put8(chunk, 1);
   }
 }
 
@@ -703,6 +741,7 @@ __device__ __forceinline__ void box_traffic(const BoxMaps& maps, const ProductK&
   out = in;
   uint32_t ahead = 0, lb = 0, sb = 0, sph = 0;  // ahead: chunks whose memory is in use
   int64_t stored = 0;
+  const bool lag = bytes == 0 && ring > 2;
   bool live = true;
   while (out.t < tiles) {
     while (in.t < tiles && ahead < ring) {
@@ -742,15 +781,16 @@ __device__ __forceinline__ void box_traffic(const BoxMaps& maps, const ProductK&
         }
       }
       asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-      // with three chunks the one stored before this is free; with two, this
-      if (ring > 2)
+      // with nothing to load the next chunk may wait: then the one stored
+      // before this is free, else this one
+      if (lag)
         asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
       else
         asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
     }
     __syncwarp();
     if (!live) break;
-    if (ring == 2 || stored > 0) --ahead;
+    if (!lag || stored > 0) --ahead;
     ++stored;
     if (++sb == ring) {
       sb = 0;
@@ -817,7 +857,7 @@ __device__ __forceinline__ void column_store(const Mat& m, const Column& c, cons
 // `keep` holds the mask as finish_block would use it.
 template <int MODE>
 __device__ __forceinline__ void finish_columns(const EpiK& k, uint32_t keep, uint32_t patch,
-                                               int64_t row0, int64_t col0, const Extent& e,
+                                               uint32_t biases, int64_t row0, int64_t col0, const Extent& e,
                                                int lane) {
   Column c;
   c.row = row0;
@@ -829,9 +869,8 @@ __device__ __forceinline__ void finish_columns(const EpiK& k, uint32_t keep, uin
     asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[i]) : "r"(patch + (i * 36 + lane) * 4));
   if constexpr (MODE == LIN_FORWARD) {
     if (k.bias.p) {
-      const float b = c.count && in_extent(c.col, c.col + 1, 0, e.cols, ZERO_SITE_LINEAR_OUT)
-                          ? load1(k.bias, c.col)
-                          : 0.0f;
+      float b;
+      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(b) : "r"(biases + (uint32_t)lane * 4));
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] += b;
     }
@@ -915,9 +954,10 @@ __device__ __forceinline__ void push_part(uint32_t there, const uint32_t r[32]) 
 #pragma unroll
   for (int u = 0; u < 8; ++u) st_cluster4(there + u * 512, r + 4 * u);
 }
-__device__ __forceinline__ void add_part(uint32_t here, uint32_t r[32]) {
+template <int N>
+__device__ __forceinline__ void add_part(uint32_t here, uint32_t r[N]) {
 #pragma unroll
-  for (int u = 0; u < 8; ++u) {
+  for (int u = 0; u < N / 4; ++u) {
     const float4 x = ld_shared4(here + u * 512);
     r[4 * u] = __float_as_uint(__uint_as_float(r[4 * u]) + x.x);
     r[4 * u + 1] = __float_as_uint(__uint_as_float(r[4 * u + 1]) + x.y);
@@ -955,6 +995,7 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
   const uint32_t patches = ring + g.stages * stage_bytes;
   const uint32_t ones = patches + (BOX ? g.boxes * kSlot * (g.two_slots ? 2 : 1)
                                        : kEpiWarps * kPatch * 4);
+  const uint32_t bias_smem = ones + (g.bias_tiles || g.bias_fused ? kOnesBytes : 0);
   const uint32_t full = smem_u32(bars), empty = full + 8 * kMaxStages;
   const uint32_t tfull = empty + 8 * kMaxStages, tempty = tfull + 16, ready = tempty + 16;
   const uint32_t efull = ready + 8, edone = efull + 8 * kMostBoxes;
@@ -1095,7 +1136,8 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
       const uint32_t idesc_n = base | ((b_c ? 0u : 1u) << 16) | ((uint32_t)(g.bn >> 3) << 17);
       const uint32_t idesc_1 = base | (4u << 17);
       const uint32_t step_a = a_c ? 2 : 128, step_b = b_c ? 2 : 128;  // 16 deep, in 16 bytes
-      const uint32_t stages = g.stages, bn = g.bn;
+      const uint32_t stages = g.stages, bn = g.bn, sets = g.acc_sets;
+      const int round = g.round, rounds = rounds_of(g, kb1 - kb0);
       const bool fused = MODE == LIN_DWEIGHT && g.bias_fused, bias_b = g.bias_b;
       uint32_t s = 0, ph = 0, acc = 0, aph = 0;
       bool live = bar_wait(ready, 0, &dead);
@@ -1103,40 +1145,47 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
         int ti, tj;
         tile_at(g, t, ti, tj);
         const bool sums = fused && (bias_b ? ti : tj) == 0;
-        live = live && bar_wait(tempty + 8 * acc, aph ^ 1, &dead);
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint32_t d = tmem + acc * bn, d_bias = tmem + bias_column(g, acc);
         const uint32_t idesc = tj >= 0 ? idesc_n : idesc_1, sb = tj >= 0 ? step_b : 0;
-        for (int kb = kb0; kb < kb1; ++kb) {
-          live = live && bar_wait(full + 8 * s, ph, &dead);
-          if (GEN) asm volatile("fence.acq_rel.cluster;" ::: "memory");
+        int kb = kb0;
+        for (int r = 0; r < rounds; ++r) {
+          live = live && bar_wait(tempty + 8 * acc, aph ^ 1, &dead);
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          const uint32_t a_at = ring + s * stage_bytes;
-          const uint64_t da = operand_desc(a_at, a_c);
-          const uint64_t db = tj >= 0 ? operand_desc(a_at + kBytesA, b_c)
-                                      : operand_desc(ones, true);
-          if (elect() && live) {
-#pragma unroll
-            for (int q = 0; q < kDeep / 16; ++q)
-              mma_pair(d, da + q * step_a, db + q * sb, idesc, kb > kb0 || q > 0);
-            if (MODE == LIN_DWEIGHT && sums) {
-              const uint64_t dr = operand_desc(bias_b ? a_at + kBytesA : a_at, a_c);
-              const uint64_t d1 = operand_desc(ones, true);
+          const uint32_t d = tmem + acc * bn, d_bias = tmem + bias_column(g, acc);
+          const int start = kb, end = r + 1 < rounds ? kb + round : kb1;
+          for (; kb < end; ++kb) {
+            live = live && bar_wait(full + 8 * s, ph, &dead);
+            if (GEN) asm volatile("fence.acq_rel.cluster;" ::: "memory");
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const uint32_t a_at = ring + s * stage_bytes;
+            const uint64_t da = operand_desc(a_at, a_c);
+            const uint64_t db = tj >= 0 ? operand_desc(a_at + kBytesA, b_c)
+                                        : operand_desc(ones, true);
+            if (elect() && live) {
 #pragma unroll
               for (int q = 0; q < kDeep / 16; ++q)
-                mma_pair(d_bias, dr + q * step_a, d1, idesc_1, kb > kb0 || q > 0);
+                mma_pair(d, da + q * step_a, db + q * sb, idesc, kb > start || q > 0);
+              if (MODE == LIN_DWEIGHT && sums) {
+                const uint64_t dr = operand_desc(bias_b ? a_at + kBytesA : a_at, a_c);
+                const uint64_t d1 = operand_desc(ones, true);
+#pragma unroll
+                for (int q = 0; q < kDeep / 16; ++q)
+                  mma_pair(d_bias, dr + q * step_a, d1, idesc_1, kb > start || q > 0);
+              }
+              commit_pair(empty + 8 * s, mask);
             }
-            commit_pair(empty + 8 * s, mask);
+            __syncwarp();
+            if (++s == stages) {
+              s = 0;
+              ph ^= 1;
+            }
           }
+          if (elect() && live) commit_pair(tfull + 8 * acc, mask);
           __syncwarp();
-          if (++s == stages) {
-            s = 0;
-            ph ^= 1;
+          if (++acc == sets) {
+            acc = 0;
+            aph ^= 1;
           }
         }
-        if (elect() && live) commit_pair(tfull + 8 * acc, mask);
-        __syncwarp();
-        if ((acc ^= 1) == 0) aph ^= 1;
       }
     }
     __syncwarp();
@@ -1156,11 +1205,14 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
         MODE == LIN_FORWARD && k.epi.drop.on ? drop_offset(k.epi.drop) : 0ull;
     const uint32_t mine = patches + (uint32_t)(warp - kEpiWarp0) * kPatch * 4;
     const BoxEpi be = box_epi<MODE>(k.epi);
+    // this warp's biases of a tile, 32 per block, fetched under the products
+    const uint32_t biases = bias_smem + (uint32_t)(warp - kEpiWarp0) * 512;
     const DropK& drop = k.epi.drop;
     const bool empty_sum = kb1 == kb0, out_t = k.out_t;
     const uint32_t boxes = g.boxes, boxes0 = patches, second = g.two_slots ? kSlot : 0,
                    chunk_bytes = kSlot + second;
-    const int bn = g.bn;
+    const int bn = g.bn, rounds = rounds_of(g, kb1 - kb0);
+    const uint32_t sets = g.acc_sets;
     const int64_t cols = k.cols, rows = k.rows;
     uint32_t acc = 0, aph = 0, eb = 0, eph = 0;
     bool ok = true;
@@ -1169,6 +1221,15 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
       tile_at(g, t, ti, tj);
       const int64_t i0 = (int64_t)ti * 256 + half * kRowsCta + w * 32;
       const int chunks = tj >= 0 ? bn / 32 : 1;
+      if (MODE == LIN_FORWARD && be.bias) {
+        for (int q = 0; 2 * q + set < chunks; ++q) {
+          const int64_t c = (out_t ? i0 : (int64_t)tj * bn + (2 * q + set) * 32) + lane;
+          const bool in = c < e.cols && in_extent(c, c + 1, 0, e.cols, ZERO_SITE_LINEAR_OUT);
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(biases + (uint32_t)(q * 32 + lane) * 4),
+                       "f"(in ? load1(k.epi.bias, c) : 0.0f));
+        }
+        __syncwarp();
+      }
       Masks masks{};
       if (MODE == LIN_FORWARD && drop.on) {
 #pragma unroll 1
@@ -1185,13 +1246,45 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
           }
         }
       }
+      const bool sums =
+          MODE == LIN_DWEIGHT && g.bias_fused && (g.bias_b ? ti : tj) == 0 && set == 0;
+      const uint32_t lanes = tmem + ((uint32_t)(w * 32) << 16);
+      float bias_sum = 0.0f;
+      // rounds before the last: their sums leave the tensor cores' set, which
+      // the next round but one writes again, for a set of their own
+      for (int r = 1; r < rounds && ok; ++r) {
+        ok = bar_wait(tfull + 8 * acc, aph, &dead);
+        ok = __all_sync(0xffffffffu, ok);
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        uint32_t v[32];
+        for (int cc = set; cc < chunks; cc += 2) {
+          tmem_load32(lanes + acc * bn + cc * 32, v);
+          if (r > 1) tmem_add32(lanes + sum_column(g) + cc * 32, v);
+          tmem_store32(lanes + sum_column(g) + cc * 32, v);
+        }
+        if (sums) {
+          tmem_load32(lanes + bias_column(g, acc), v);
+          bias_sum += __uint_as_float(v[0]);
+        }
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) bar_arrive_cluster(tempty_lead + 8 * acc);
+        if (++acc == sets) {
+          acc = 0;
+          aph ^= 1;
+        }
+      }
+      if (!ok) break;
       ok = bar_wait(tfull + 8 * acc, aph, &dead);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      const uint32_t d = tmem + acc * bn + ((uint32_t)(w * 32) << 16);
-      const bool sums =
-          MODE == LIN_DWEIGHT && g.bias_fused && (g.bias_b ? ti : tj) == 0 && set == 0;
+      const uint32_t d = lanes + acc * bn;
+      if (sums) {
+        uint32_t v[32];
+        tmem_load32(lanes + bias_column(g, acc), v);
+        bias_sum += __uint_as_float(v[0]);
+      }
       if (S > 1) {
         cluster_arrive();
         cluster_wait();  // both pairs' products are done: the rings are free
@@ -1199,13 +1292,13 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
           if (tj < 0 ? split == 0 : owns_block(split, cc, chunks, w)) continue;
           uint32_t r[32];
           tmem_load32(d + cc * 32, r);
+          if (rounds > 1) tmem_add32(lanes + sum_column(g) + cc * 32, r);
           push_part(remote(part_at(ring, cc, w, lane), rank ^ 2), r);
         }
-        if (sums && split == 1) {
-          uint32_t r[32];
-          tmem_load32(tmem + bias_column(g, acc) + ((uint32_t)(w * 32) << 16), r);
-          push_part(remote(part_at(ring, chunks, w, lane), rank ^ 2), r);
-        }
+        if (sums && split == 1)
+          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(
+                           remote(part_at(ring, chunks, w, lane), rank ^ 2)),
+                       "f"(bias_sum));
         cluster_arrive();
         cluster_wait();
         barriers = 2;
@@ -1221,21 +1314,24 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
           }
           if (kWidth == 32 && (cc & 1) != set) continue;
           const int block = kWidth == 64 ? 2 * cc + set : cc;
-          uint32_t r[32];
-          tmem_load32(d + block * 32, r);
-          if (S > 1) add_part(part_at(ring, block, w, lane), r);
-          if (empty_sum) {
-#pragma unroll
-            for (int q = 0; q < 32; ++q) r[q] = 0;  // an empty contraction
-          }
           ok = bar_wait(efull + 8 * b, bph, &dead);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          float v[32];
+          uint32_t keep = masks.at(block >> 1);
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            uint32_t r[16];
+            tmem_load16(d + block * 32 + 16 * h, r);
+            if (rounds > 1) tmem_add16(lanes + sum_column(g) + block * 32 + 16 * h, r);
+            if (S > 1) add_part<16>(part_at(ring, block, w, lane) + 2048 * h, r);
+            float v[16];
 #pragma unroll
-          for (int q = 0; q < 32; ++q) v[q] = __uint_as_float(r[q]);
-          box_chunk<MODE, FORM>(be, masks.at(block >> 1), boxes0 + b * chunk_bytes, second,
-                                w * 32 + lane, (int64_t)tj * bn + block * 32, set * 4, cols, v);
+            for (int q = 0; q < 16; ++q) v[q] = empty_sum ? 0.0f : __uint_as_float(r[q]);
+            box_half<MODE, FORM>(be, keep, boxes0 + b * chunk_bytes, second, w * 32 + lane,
+                                 (kWidth == 64 ? set * 4 : 0) + 2 * h,
+                                 biases + (uint32_t)((block >> 1) * 32 + 16 * h) * 4, v);
+            keep <<= 16;
+          }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) bar_arrive(edone + 8 * b);
@@ -1250,7 +1346,8 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
           if (tj >= 0 && k.epi.vec) load_sides<MODE>(k.epi, b, e, sides);
           uint32_t r[32];
           tmem_load32(d + cc * 32, r);
-          if (S > 1) add_part(part_at(ring, cc, w, lane), r);
+          if (rounds > 1) tmem_add32(lanes + sum_column(g) + cc * 32, r);
+          if (S > 1) add_part<32>(part_at(ring, cc, w, lane), r);
           if (empty_sum) {
 #pragma unroll
             for (int q = 0; q < 32; ++q) r[q] = 0;  // an empty contraction
@@ -1272,24 +1369,31 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
           }
           __syncwarp();
           if (k.epi.vec)
-            finish_block<MODE>(k.epi, masks.at(cc >> 1), mine, b, e, sides, lane);
+            finish_block<MODE>(k.epi, masks.at(cc >> 1), mine, biases + (cc >> 1) * 128, b, e, sides,
+                               lane);
           else
-            finish_columns<MODE>(k.epi, masks.at(cc >> 1), mine, out_t ? j0 : i0,
+            finish_columns<MODE>(k.epi, masks.at(cc >> 1), mine, biases + (cc >> 1) * 128,
+                                 out_t ? j0 : i0,
                                  out_t ? i0 : j0, e, lane);
           __syncwarp();
         }
       }
       if (sums && split == 0) {
-        uint32_t r[32];
-        tmem_load32(tmem + bias_column(g, acc) + ((uint32_t)(w * 32) << 16), r);
-        if (S > 1) add_part(part_at(ring, chunks, w, lane), r);
+        if (S > 1) {
+          float other;
+          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(other) : "r"(part_at(ring, chunks, w, lane)));
+          bias_sum += other;
+        }
         store_bias(k, g, (int64_t)(g.bias_b ? tj : ti) * 256 + half * kRowsCta + w * 32 + lane,
-                   empty_sum ? 0.0f : __uint_as_float(r[0]));
+                   empty_sum ? 0.0f : bias_sum);
       }
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
       if (lane == 0) bar_arrive_cluster(tempty_lead + 8 * acc);
-      if ((acc ^= 1) == 0) aph ^= 1;
+      if (++acc == sets) {
+        acc = 0;
+        aph ^= 1;
+      }
     }
   } else if (GEN && warp >= kGenWarp0) {
     const int t128 = threadIdx.x - kGenWarp0 * 32;
@@ -1411,7 +1515,7 @@ static bool box_map(CUtensorMap* map, const Mat& a, int64_t rows, int64_t cols, 
 
 // Shared memory beside the operand ring, and the ring's stages in what is left.
 static int side_bytes(const TileK& g, int form) {
-  return (g.bias_tiles || g.bias_fused ? kOnesBytes : 0) + (form >= BOX_BF16 ? g.boxes * kSlot * (g.two_slots ? 2 : 1)
+  return (g.bias_tiles || g.bias_fused ? kOnesBytes : 0) + g.bias_in + (form >= BOX_BF16 ? g.boxes * kSlot * (g.two_slots ? 2 : 1)
                            : kEpiWarps * kPatch * 4);
 }
 static int stages_for(const TileK& g, int form) {
@@ -1495,6 +1599,24 @@ static cudaError_t launch_mode(const ProductK& in, cudaStream_t st) {
   // one part / two: 1 x 4096 x 4096 17.4 / 11.9, 1024 x 1024 x 4096 at BN = 128
   // 18.4 / 14.1, 2048 x 1024 x 4096 at BN = 256 23.4 / 18.0, 1024 x 2304 x 768
   // at 128 8.8 / 16.6; four parts, clusters of 8, always lost.)
+  // The tensor cores add to their sums without rounding to nearest, so a long
+  // contraction loses digits: 7e-7 of the result after 768 terms, 7e-6 after
+  // 6000 (in units of its size).  fp32 results therefore take the sums out
+  // every `round` steps and add them in fp32 proper, in a third set of tensor
+  // memory, where three fit (BN = 128) while the products go on; bf16 results
+  // only where that loss would reach their own rounding.
+  const bool f32 = k.epi.out.dtype == ZERO_F32 || (k.dbias.p && k.dbias.dtype == ZERO_F32);
+  const bool exact = f32 ? kblocks > kRound : kblocks > 512;
+  g.bias_b = k.dbias.p && k.bias_b;
+  const int64_t bias_rows = !k.dbias.p ? 0 : g.bias_b ? k.cols : k.rows;
+  // The bias's sums ride on the first tiles' products (an eighth more work on
+  // those) where tensor memory has room for them; else they are tiles of
+  // their own, which cost a row of loads and, past a full wave, a wave.
+  auto fuses_bias = [&](int bn, int S, int64_t tiles_j) {
+    const int64_t main = tiles_i * tiles_j;
+    return bias_rows > 0 && main > 0 && (!g.bias_b || bn == 256) &&
+           (exact ? bn == 128 : S > 1 || main <= pairs || bn == 128);
+  };
   double best = 0;
   for (int bn = 32; bn <= 256; bn *= 2) {
     if (!k.b_c && bn < 128) continue;       // blocks of 64 rows per CTA
@@ -1502,11 +1624,13 @@ static cudaError_t launch_mode(const ProductK& in, cudaStream_t st) {
     const int64_t tiles_j = (k.cols + bn - 1) / bn;
     for (int S = 1; S <= 2; ++S) {
       if (S > 1 && kblocks < 2 * S) break;
-      const double waves = (double)((tiles_i * tiles_j * S + pairs - 1) / pairs);
-      const double step = bn == 256 ? 520 : 430;
+      const bool fused = fuses_bias(bn, S, tiles_j);
+      const int64_t tiles = tiles_i * tiles_j + (fused ? 0 : (bias_rows + 255) / 256);
+      const double waves = (double)((tiles * S + pairs - 1) / pairs);
+      const double step = bn == 256 ? (exact ? 520 + 1500.0 / kRound : 520) : 430;
       const double cost =
           waves * ((double)kblocks / S * step + (S > 1 ? 2500 + 15 * bn : 0)) +
-          (S > 1 ? (waves - 1) * 8000 : 0) + 25 * bn;
+          (S > 1 || (exact && bn == 256) ? (waves - 1) * 8000 : 0) + 25 * bn;
       if (best == 0 || cost < best) {
         best = cost;
         g.bn = bn;
@@ -1515,21 +1639,17 @@ static cudaError_t launch_mode(const ProductK& in, cudaStream_t st) {
       }
     }
   }
-  g.bias_b = k.dbias.p && k.bias_b;
-  const int64_t bias_rows = !k.dbias.p ? 0 : g.bias_b ? k.cols : k.rows;
   if (tiles_i * (g.tiles_j + 1) >= (1ll << 28) || kblocks >= (1ll << 30))
     return cudaErrorInvalidValue;
+  g.bias_in = k.epi.bias.p ? kEpiWarps * 512 : 0;
   g.tiles_i = (int)tiles_i;
   g.kblocks = (int)kblocks;
-  // The bias's sums ride on the first tiles' products (an eighth more work on
-  // those) where tensor memory has room for them; else they are tiles of
-  // their own, which cost a row of loads and, past a full wave, a wave.
-  const int64_t main = tiles_i * g.tiles_j;
-  g.bias_fused = bias_rows > 0 && main > 0 && (!g.bias_b || g.bn == 256) &&
-                 (g.splits > 1 || main <= pairs || g.bn == 128);
+  g.round = exact ? kRound : 0;
+  g.acc_sets = exact && g.bn == 256 ? 1 : 2;
+  g.bias_fused = fuses_bias(g.bn, g.splits, g.tiles_j);
   g.bias_tiles = g.bias_fused ? 0 : (int)((bias_rows + 255) / 256);
   g.i_fast = k.rows <= k.cols;
-  g.tmem_cols = g.bias_fused && g.splits == 1 && main > pairs ? 512 : 2 * g.bn;
+  g.tmem_cols = g.bn >= 128 && (exact || g.bias_fused) ? 512 : (exact ? 4 : 2) * g.bn;
   CUtensorMap ma{}, mb{};
   BoxMaps maps{};
   if (k.depth > 0) {

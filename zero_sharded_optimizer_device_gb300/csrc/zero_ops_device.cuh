@@ -194,8 +194,22 @@ __device__ __forceinline__ float logistic(float x) { return __fdividef(1.0f, 1.0
 
 constexpr float kGeluA = 1.5957691216057308f;  // 2 sqrt(2/pi)
 constexpr float kGeluB = 0.044715f;
-constexpr float kRsqrt2 = 0.70710678118654752f;
 constexpr float kRsqrt2Pi = 0.39894228040143268f;
+
+// The normal distribution's mass below z, and e = exp(-z^2 / 2), by formula
+// 7.1.26 of Abramowitz and Stegun (Hastings 1955; |error| < 7.5e-8 here): with
+// t = 1 / (1 + p |z| / sqrt 2) the mass beyond |z| is t (a1 + ... + a5 t^4) e / 2.
+// No branch, and the exponential serves the slope too (erff: a division into
+// cases and three times the code).
+__device__ __forceinline__ float normal_mass(float z, float& e) {
+  const float t = __fdividef(1.0f, 1.0f + 0.3275911f * 0.70710678f * fabsf(z));
+  e = __expf(-0.5f * z * z);
+  const float p = t * (0.127414796f +
+                       t * (-0.142248368f +
+                            t * (0.7107068705f + t * (-0.7265760135f + t * 0.5307027145f))));
+  const float tail = p * e;
+  return z < 0.0f ? tail : 1.0f - tail;
+}
 
 // N values through an activation, in place.
 template <int N>
@@ -207,7 +221,10 @@ __device__ __forceinline__ void activate(float z[N], int act) {
       break;
     case ZERO_ACT_GELU:
 #pragma unroll
-      for (int j = 0; j < N; ++j) z[j] = 0.5f * z[j] * (1.0f + erff(z[j] * kRsqrt2));
+      for (int j = 0; j < N; ++j) {
+        float e;
+        z[j] = z[j] * normal_mass(z[j], e);
+      }
       break;
     case ZERO_ACT_GELU_TANH:
 #pragma unroll
@@ -237,9 +254,10 @@ __device__ __forceinline__ void activate_grad(float value[N], float slope[N], in
     case ZERO_ACT_GELU:
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        const float z = value[j], s = 0.5f * (1.0f + erff(z * kRsqrt2));
+        float e;
+        const float z = value[j], s = normal_mass(z, e);
         value[j] = z * s;
-        slope[j] = s + z * kRsqrt2Pi * __expf(-0.5f * z * z);
+        slope[j] = s + z * kRsqrt2Pi * e;
       }
       break;
     case ZERO_ACT_GELU_TANH:
