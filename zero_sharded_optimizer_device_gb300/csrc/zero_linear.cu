@@ -12,15 +12,15 @@
 //   warp 2        allocates and frees tensor memory
 //   warp 3        (boxes) loads the side operands' boxes by TMA ahead of the
 //                 epilogue and stores the finished ones
-//   warps 4-11    epilogue, in one of two forms:
-//                 boxes: a thread keeps its row of sums as tensor memory gives
-//                 it (no exchange between threads), reads the side operands
-//                 from the boxes warp 3 brought and writes its results in
-//                 their place; addresses, bounds and coalescing are TMA's
-//                 patches: 32 x 32 sums cross a patch of shared memory, and a
-//                 thread goes on with 8 consecutive columns by plain loads and
-//                 stores; for transposed outputs, joined parts of a split
-//                 contraction and rows off 16-byte boundaries
+//   warps 4-      epilogue, in one of two forms:
+//                 boxes (16 warps): a thread keeps its row of sums as tensor
+//                 memory gives it, reads the side operands from the boxes warp
+//                 3 brought and writes its results in their place; addresses,
+//                 bounds and coalescing are TMA's
+//                 patches (8 warps): 32 x 32 sums cross a patch of shared
+//                 memory, and a thread goes on with 8 consecutive columns by
+//                 plain loads and stores; for transposed outputs and rows off
+//                 16-byte boundaries
 //   warps 12-15   (gen) load operands whose base or rows lie off 16-byte
 //                 boundaries, which TMA cannot, with plain loads
 // Tiles are walked persistently with two sets of sums, so one tile's epilogue
@@ -38,7 +38,7 @@ namespace zk {
 constexpr int kRowsCta = 128;          // rows of A per CTA (tensor-memory lanes)
 constexpr int kDeep = 64;              // contraction per stage: 128 bytes, one swizzle row
 constexpr int kBytesA = kRowsCta * kDeep * 2;
-constexpr int kEpiWarp0 = 4, kEpiWarps = 8, kGenWarp0 = 12, kGenWarps = 4;
+constexpr int kEpiWarp0 = 4, kPatchWarps = 8, kBoxWarps = 16, kGenWarp0 = 12, kGenWarps = 4;
 constexpr int kPatch = 32 * 36;        // floats of a 32 x 32 patch, rows 36 apart
 constexpr int kMaxStages = 9;
 constexpr int kRound = 12;             // 64-deep steps of a round (see launch_mode)
@@ -57,6 +57,11 @@ enum Form : int {
   BOX_BF16 = 2,   // operands by TMA, results in boxes of 64 bf16 columns
   BOX_F32 = 3     // operands by TMA, results in boxes of 32 fp32 columns
 };
+
+constexpr int threads_of(int form) {
+  return 32 * (form == PATCH_GEN ? kGenWarp0 + kGenWarps
+                                 : kEpiWarp0 + (form == PATCH ? kPatchWarps : kBoxWarps));
+}
 
 // How a launch walks its product (host-made).
 struct TileK {
@@ -242,19 +247,37 @@ __device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t r[32]
       : "memory");
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
-// r += the 32 (16) columns at addr.
-__device__ __forceinline__ void tmem_add32(uint32_t addr, uint32_t r[32]) {
-  uint32_t q[32];
-  tmem_load32(addr, q);
-#pragma unroll
-  for (int i = 0; i < 32; ++i)
-    r[i] = __float_as_uint(__uint_as_float(r[i]) + __uint_as_float(q[i]));
+__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t r[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(addr)
+      : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void tmem_add16(uint32_t addr, uint32_t r[16]) {
-  uint32_t q[16];
-  tmem_load16(addr, q);
+template <int N>
+__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t r[N]) {
+  if constexpr (N == 32)
+    tmem_load32(addr, r);
+  else
+    tmem_load16(addr, r);
+}
+template <int N>
+__device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t r[N]) {
+  if constexpr (N == 32)
+    tmem_store32(addr, r);
+  else
+    tmem_store16(addr, r);
+}
+// r += the N columns at addr.
+template <int N>
+__device__ __forceinline__ void tmem_add(uint32_t addr, uint32_t r[N]) {
+  uint32_t q[N];
+  tmem_load<N>(addr, q);
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
+  for (int i = 0; i < N; ++i)
     r[i] = __float_as_uint(__uint_as_float(r[i]) + __uint_as_float(q[i]));
 }
 __device__ __forceinline__ void st_shared4(uint32_t addr, float a, float b, float c, float d) {
@@ -577,21 +600,18 @@ __device__ __forceinline__ BoxEpi box_epi(const EpiK& k) {
   return e;
 }
 
-// Half a block: 16 sums v of a thread's row `row` of the tile through the
-// epilogue; unit: their first 16-byte unit in a bf16 row of the chunk's boxes,
-// f32_unit in an fp32 one; bias: where their columns' biases lie.  Each step
-// runs over all 16 before the next (a branch per step, not per value), and the
-// halves are a loop: fetching longer straight-line code took longer than
-// running it.
+// 16 sums v of a thread's row `row` of the tile through the epilogue; unit:
+// their first 16-byte unit in a bf16 row of the chunk's boxes; bias: where
+// their columns' biases lie.  Each step runs over all 16 before the next: a
+// branch per step, not per value.
 template <int MODE, int FORM>
-__device__ __forceinline__ void box_half(const BoxEpi& k, uint32_t keep, uint32_t chunk,
+__device__ __forceinline__ void box_piece(const BoxEpi& k, uint32_t keep, uint32_t chunk,
                                          uint32_t second, int row, int unit, uint32_t bias,
                                          float v[16]) {
   constexpr bool wide = FORM == BOX_F32;
   const uint32_t slot1 = chunk + second;
   float f[8];
-  // the two bf16 units of slot 0 (dinput: of the box at `base`) and where the
-  // result's two groups of 8 go
+  // the two bf16 units of a box, and groups of 8 in the output's dtype
   auto bf16_at = [&](uint32_t base, int i) {
     return base + (wide ? at64(row, unit + i) : at128(row, unit + i));
   };
@@ -924,7 +944,7 @@ __device__ __forceinline__ void finish_columns(const EpiK& k, uint32_t keep, uin
 // Dropout's masks of a thread's share of a tile, 32 elements each: drawn while
 // the tile's products are still running, on warps that otherwise wait.
 struct Masks {
-  uint32_t m0, m1, m2, m3;
+  uint32_t m0, m1, m2, m3;  // highest bit first
   __device__ __forceinline__ uint32_t at(int q) const {
     return q < 2 ? (q == 0 ? m0 : m1) : (q == 2 ? m2 : m3);
   }
@@ -938,21 +958,23 @@ struct Masks {
 
 // ---------------------------------------------------------------------------
 // A contraction split in two: both pairs of a cluster hold sums of the whole
-// tile.  Each pair finishes half of its 32 x 32 blocks; it writes the sums of
-// the other half into the memory of the partner's CTA with the same rows (the
+// tile.  Each pair finishes half of its pieces; it writes the sums of the
+// other half into the memory of the partner's CTA with the same rows (the
 // operand ring, free by then) and adds what it finds in its own.  Two addends:
-// the same result whichever pair adds.  4 KiB per block, 16-byte units of
-// consecutive threads side by side.
+// the same result whichever pair adds.  A warp's piece of N columns takes
+// 128 N bytes, 16-byte units of consecutive threads side by side.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ bool owns_block(int split, int cc, int chunks, int w) {
-  return (chunks == 1 ? (w & 1) : (int)(cc >= chunks / 2)) == split;
+__device__ __forceinline__ bool owns_piece(int split, int piece, int pieces, int w) {
+  return (pieces == 1 ? (w & 1) : (int)(piece >= pieces / 2)) == split;
 }
-__device__ __forceinline__ uint32_t part_at(uint32_t ring, int cc, int w, int lane) {
-  return ring + (uint32_t)((cc * 4 + w) * 4096 + lane * 16);
+template <int N>
+__device__ __forceinline__ uint32_t part_at(uint32_t ring, int piece, int w, int lane) {
+  return ring + (uint32_t)((piece * 4 + w) * (N * 128) + lane * 16);
 }
-__device__ __forceinline__ void push_part(uint32_t there, const uint32_t r[32]) {
+template <int N>
+__device__ __forceinline__ void push_part(uint32_t there, const uint32_t r[N]) {
 #pragma unroll
-  for (int u = 0; u < 8; ++u) st_cluster4(there + u * 512, r + 4 * u);
+  for (int u = 0; u < N / 4; ++u) st_cluster4(there + u * 512, r + 4 * u);
 }
 template <int N>
 __device__ __forceinline__ void add_part(uint32_t here, uint32_t r[N]) {
@@ -976,13 +998,19 @@ __device__ __forceinline__ void store_bias(const ProductK& k, const TileK& g, in
 }
 
 template <int MODE, int FORM>
-__global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
+__global__ void __launch_bounds__(threads_of(FORM), 1)
     product_kernel(const __grid_constant__ CUtensorMap map_a,
                    const __grid_constant__ CUtensorMap map_b,
                    const __grid_constant__ BoxMaps maps, const __grid_constant__ ProductK k,
                    const __grid_constant__ TileK g) {
   constexpr bool GEN = FORM == PATCH_GEN, BOX = FORM == BOX_BF16 || FORM == BOX_F32;
   constexpr int kWidth = FORM == BOX_F32 ? 32 : 64;  // columns of a chunk
+  // The epilogue's warps in sets of four (one per 32 rows); a set takes every
+  // kSets-th piece of kPiece columns of a tile.  Boxes want twice the warps,
+  // as half of their time is latency (8192 x 1024 x 4096 with a GELU gradient:
+  // 63 us with 8).
+  constexpr int kEpiWarps = BOX ? kBoxWarps : kPatchWarps;
+  constexpr int kPiece = BOX ? 16 : 32, kSets = kEpiWarps / 4;
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 5 + 2 * kMostBoxes];
   __shared__ uint32_t tmem_at;
@@ -994,7 +1022,7 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
   const uint32_t ring = smem_u32(smem);
   const uint32_t patches = ring + g.stages * stage_bytes;
   const uint32_t ones = patches + (BOX ? g.boxes * kSlot * (g.two_slots ? 2 : 1)
-                                       : kEpiWarps * kPatch * 4);
+                                       : kPatchWarps * kPatch * 4);
   const uint32_t bias_smem = ones + (g.bias_tiles || g.bias_fused ? kOnesBytes : 0);
   const uint32_t full = smem_u32(bars), empty = full + 8 * kMaxStages;
   const uint32_t tfull = empty + 8 * kMaxStages, tempty = tfull + 16, ready = tempty + 16;
@@ -1014,7 +1042,7 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
     if (BOX)
       for (int b = 0; b < g.boxes; ++b) {
         bar_init(efull + 8 * b, 1);
-        // 64 columns are shared by both sets of epilogue warps, 32 taken by one
+        // 64 columns are shared by all sets of epilogue warps, 32 by half
         bar_init(edone + 8 * b, kWidth == 64 ? kEpiWarps : kEpiWarps / 2);
       }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -1031,8 +1059,11 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
   // the next kernel on the stream may set up while this one runs
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp == 1 && elect()) {
-    asm volatile("prefetch.tensormap [%0];" ::"l"(&map_a) : "memory");
-    asm volatile("prefetch.tensormap [%0];" ::"l"(&map_b) : "memory");
+    // (an operand that comes by plain loads, or is empty, has no map)
+    if (!g.gen_a && g.kblocks > 0 && k.rows > 0)
+      asm volatile("prefetch.tensormap [%0];" ::"l"(&map_a) : "memory");
+    if (!g.gen_b && g.kblocks > 0 && k.cols > 0)
+      asm volatile("prefetch.tensormap [%0];" ::"l"(&map_b) : "memory");
     if (BOX) asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.out) : "memory");
   }
   if (warp == 2) {
@@ -1205,8 +1236,8 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
         MODE == LIN_FORWARD && k.epi.drop.on ? drop_offset(k.epi.drop) : 0ull;
     const uint32_t mine = patches + (uint32_t)(warp - kEpiWarp0) * kPatch * 4;
     const BoxEpi be = box_epi<MODE>(k.epi);
-    // this warp's biases of a tile, 32 per block, fetched under the products
-    const uint32_t biases = bias_smem + (uint32_t)(warp - kEpiWarp0) * 512;
+    // this warp's biases of a tile, those of its pieces in a row
+    const uint32_t biases = bias_smem + (uint32_t)(warp - kEpiWarp0) * (kPiece * 16);
     const DropK& drop = k.epi.drop;
     const bool empty_sum = kb1 == kb0, out_t = k.out_t;
     const uint32_t boxes = g.boxes, boxes0 = patches, second = g.two_slots ? kSlot : 0,
@@ -1220,50 +1251,58 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
       int ti, tj;
       tile_at(g, t, ti, tj);
       const int64_t i0 = (int64_t)ti * 256 + half * kRowsCta + w * 32;
-      const int chunks = tj >= 0 ? bn / 32 : 1;
+      const int pieces = tj >= 0 ? bn / kPiece : 1;
+      // While the products run: the biases and dropout masks of this warp's
+      // pieces, the q-th being piece kSets q + set.
       if (MODE == LIN_FORWARD && be.bias) {
-        for (int q = 0; 2 * q + set < chunks; ++q) {
-          const int64_t c = (out_t ? i0 : (int64_t)tj * bn + (2 * q + set) * 32) + lane;
-          const bool in = c < e.cols && in_extent(c, c + 1, 0, e.cols, ZERO_SITE_LINEAR_OUT);
-          asm volatile("st.shared.f32 [%0], %1;" ::"r"(biases + (uint32_t)(q * 32 + lane) * 4),
-                       "f"(in ? load1(k.epi.bias, c) : 0.0f));
+        for (int q = 0; kSets * q + set < pieces; ++q) {
+          const int64_t c =
+              (out_t ? i0 : (int64_t)tj * bn + (kSets * q + set) * kPiece) + lane;
+          const bool in = c < e.cols && lane < kPiece &&
+                          in_extent(c, c + 1, 0, e.cols, ZERO_SITE_LINEAR_OUT);
+          const float b = in ? load1(k.epi.bias, c) : 0.0f;
+          if (lane < kPiece)
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(biases + (uint32_t)(q * kPiece + lane) * 4),
+                         "f"(b));
         }
         __syncwarp();
       }
       Masks masks{};
       if (MODE == LIN_FORWARD && drop.on) {
 #pragma unroll 1
-        for (int q = 0; 2 * q + set < chunks; ++q) {
-          // the 32 columns this warp takes q-th, as the loops below take them
-          const int64_t j0 = (int64_t)tj * bn + (2 * q + set) * 32;
+        for (int q = 0; kSets * q + set < pieces; ++q) {
+          const int piece = kSets * q + set;
+          const int64_t j0 = (int64_t)tj * bn + piece * kPiece;
           if (i0 >= rows || j0 >= cols) break;
-          if (S > 1 && !owns_block(split, 2 * q + set, chunks, w)) continue;
+          if (S > 1 && !owns_piece(split, piece, pieces, w)) continue;
           if (BOX) {
-            masks.set(q, keep32<4>(drop, offset, (uint32_t)(i0 + lane), 0, j0));
+            masks.set(q, keep_mask<4, 4>(drop, offset, (uint32_t)(i0 + lane), 0, j0));
           } else {
             const Block b = block_of(out_t ? j0 : i0, out_t ? i0 : j0, e, lane);
-            masks.set(q, keep32<1>(drop, offset, (uint32_t)b.row, 8, b.col));
+            masks.set(q, keep_mask<8, 2>(drop, offset, (uint32_t)b.row, 8, b.col));
           }
         }
       }
       const bool sums =
           MODE == LIN_DWEIGHT && g.bias_fused && (g.bias_b ? ti : tj) == 0 && set == 0;
       const uint32_t lanes = tmem + ((uint32_t)(w * 32) << 16);
+      const uint32_t summed = lanes + sum_column(g);
       float bias_sum = 0.0f;
       // rounds before the last: their sums leave the tensor cores' set, which
-      // the next round but one writes again, for a set of their own
+      // a later round writes again, for a set of their own
       for (int r = 1; r < rounds && ok; ++r) {
         ok = bar_wait(tfull + 8 * acc, aph, &dead);
         ok = __all_sync(0xffffffffu, ok);
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        uint32_t v[32];
-        for (int cc = set; cc < chunks; cc += 2) {
-          tmem_load32(lanes + acc * bn + cc * 32, v);
-          if (r > 1) tmem_add32(lanes + sum_column(g) + cc * 32, v);
-          tmem_store32(lanes + sum_column(g) + cc * 32, v);
+        for (int piece = set; piece < pieces; piece += kSets) {
+          uint32_t v[kPiece];
+          tmem_load<kPiece>(lanes + acc * bn + piece * kPiece, v);
+          if (r > 1) tmem_add<kPiece>(summed + piece * kPiece, v);
+          tmem_store<kPiece>(summed + piece * kPiece, v);
         }
         if (sums) {
-          tmem_load32(lanes + bias_column(g, acc), v);
+          uint32_t v[16];
+          tmem_load16(lanes + bias_column(g, acc), v);
           bias_sum += __uint_as_float(v[0]);
         }
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -1281,29 +1320,44 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint32_t d = lanes + acc * bn;
       if (sums) {
-        uint32_t v[32];
-        tmem_load32(lanes + bias_column(g, acc), v);
+        uint32_t v[16];
+        tmem_load16(lanes + bias_column(g, acc), v);
         bias_sum += __uint_as_float(v[0]);
       }
       if (S > 1) {
         cluster_arrive();
         cluster_wait();  // both pairs' products are done: the rings are free
-        for (int cc = set; cc < chunks; cc += 2) {
-          if (tj < 0 ? split == 0 : owns_block(split, cc, chunks, w)) continue;
-          uint32_t r[32];
-          tmem_load32(d + cc * 32, r);
-          if (rounds > 1) tmem_add32(lanes + sum_column(g) + cc * 32, r);
-          push_part(remote(part_at(ring, cc, w, lane), rank ^ 2), r);
+        for (int piece = set; piece < pieces; piece += kSets) {
+          if (tj < 0 ? split == 0 : owns_piece(split, piece, pieces, w)) continue;
+          uint32_t r[kPiece];
+          tmem_load<kPiece>(d + piece * kPiece, r);
+          if (rounds > 1) tmem_add<kPiece>(summed + piece * kPiece, r);
+          push_part<kPiece>(remote(part_at<kPiece>(ring, piece, w, lane), rank ^ 2), r);
         }
         if (sums && split == 1)
           asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(
-                           remote(part_at(ring, chunks, w, lane), rank ^ 2)),
+                           remote(part_at<kPiece>(ring, pieces, w, lane), rank ^ 2)),
                        "f"(bias_sum));
         cluster_arrive();
         cluster_wait();
         barriers = 2;
       }
-      if (BOX && tj >= 0) {
+      // The sums of a piece: this round's, the rounds' before, the partner's.
+      auto piece_sums = [&](int piece, float v[kPiece]) {
+        uint32_t r[kPiece];
+        tmem_load<kPiece>(d + piece * kPiece, r);
+        if (rounds > 1) tmem_add<kPiece>(summed + piece * kPiece, r);
+        if (S > 1) add_part<kPiece>(part_at<kPiece>(ring, piece, w, lane), r);
+#pragma unroll
+        for (int q = 0; q < kPiece; ++q) v[q] = empty_sum ? 0.0f : __uint_as_float(r[q]);
+      };
+      if (tj < 0) {  // a tile of bias sums: its first column
+        if (set == 0 && (S == 1 || split == 0)) {
+          float v[kPiece];
+          piece_sums(0, v);
+          store_bias(k, g, i0 + lane, v[0]);
+        }
+      } else if constexpr (BOX) {
         ChunkWalk at{t, ti, tj, 0, 0};
         enter_tile<kWidth>(g, cols, split, at);
         for (int cc = at.cc; cc < at.count; ++cc) {
@@ -1312,68 +1366,46 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
             eb = 0;
             eph ^= 1;
           }
-          if (kWidth == 32 && (cc & 1) != set) continue;
-          const int block = kWidth == 64 ? 2 * cc + set : cc;
+          if (kWidth == 32 && (cc & 1) != set >> 1) continue;
+          const int piece = kWidth == 64 ? 4 * cc + set : 2 * cc + (set & 1);
+          const int unit = kWidth == 64 ? 2 * set : 2 * (set & 1);  // of a bf16 row
           ok = bar_wait(efull + 8 * b, bph, &dead);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          uint32_t keep = masks.at(block >> 1);
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            uint32_t r[16];
-            tmem_load16(d + block * 32 + 16 * h, r);
-            if (rounds > 1) tmem_add16(lanes + sum_column(g) + block * 32 + 16 * h, r);
-            if (S > 1) add_part<16>(part_at(ring, block, w, lane) + 2048 * h, r);
-            float v[16];
-#pragma unroll
-            for (int q = 0; q < 16; ++q) v[q] = empty_sum ? 0.0f : __uint_as_float(r[q]);
-            box_half<MODE, FORM>(be, keep, boxes0 + b * chunk_bytes, second, w * 32 + lane,
-                                 (kWidth == 64 ? set * 4 : 0) + 2 * h,
-                                 biases + (uint32_t)((block >> 1) * 32 + 16 * h) * 4, v);
-            keep <<= 16;
-          }
+          float v[kPiece];
+          piece_sums(piece, v);
+          box_piece<MODE, FORM>(be, masks.at(piece >> 2), boxes0 + b * chunk_bytes, second,
+                               w * 32 + lane, unit, biases + (uint32_t)(piece >> 2) * (kPiece * 4),
+                               v);
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) bar_arrive(edone + 8 * b);
         }
       } else {
-        for (int cc = set; cc < chunks; cc += 2) {
-          const int64_t j0 = (int64_t)tj * bn + cc * 32;
-          if (tj >= 0 && (i0 >= rows || j0 >= cols)) continue;
-          if (S > 1 && !(tj < 0 ? split == 0 : owns_block(split, cc, chunks, w))) continue;
+        for (int piece = set; piece < pieces; piece += kSets) {
+          const int64_t j0 = (int64_t)tj * bn + piece * kPiece;
+          if (i0 >= rows || j0 >= cols) continue;
+          if (S > 1 && !owns_piece(split, piece, pieces, w)) continue;
           const Block b = block_of(out_t ? j0 : i0, out_t ? i0 : j0, e, lane);
+          const uint32_t bias = biases + (uint32_t)(piece >> 1) * (kPiece * 4);
           Sides<MODE> sides;
-          if (tj >= 0 && k.epi.vec) load_sides<MODE>(k.epi, b, e, sides);
-          uint32_t r[32];
-          tmem_load32(d + cc * 32, r);
-          if (rounds > 1) tmem_add32(lanes + sum_column(g) + cc * 32, r);
-          if (S > 1) add_part<32>(part_at(ring, cc, w, lane), r);
-          if (empty_sum) {
-#pragma unroll
-            for (int q = 0; q < 32; ++q) r[q] = 0;  // an empty contraction
-          }
-          if (MODE == LIN_DWEIGHT && tj < 0) {
-            store_bias(k, g, i0 + lane, __uint_as_float(r[0]));
-            continue;
-          }
+          if (k.epi.vec) load_sides<MODE>(k.epi, b, e, sides);
+          float v[kPiece];
+          piece_sums(piece, v);
           if (out_t) {
 #pragma unroll
             for (int q = 0; q < 32; ++q)
-              asm volatile("st.shared.b32 [%0], %1;" ::"r"(mine + (q * 36 + lane) * 4), "r"(r[q]));
+              asm volatile("st.shared.f32 [%0], %1;" ::"r"(mine + (q * 36 + lane) * 4), "f"(v[q]));
           } else {
 #pragma unroll
             for (int q = 0; q < 32; q += 4)
-              st_shared4(mine + (lane * 36 + q) * 4, __uint_as_float(r[q]),
-                         __uint_as_float(r[q + 1]), __uint_as_float(r[q + 2]),
-                         __uint_as_float(r[q + 3]));
+              st_shared4(mine + (lane * 36 + q) * 4, v[q], v[q + 1], v[q + 2], v[q + 3]);
           }
           __syncwarp();
           if (k.epi.vec)
-            finish_block<MODE>(k.epi, masks.at(cc >> 1), mine, biases + (cc >> 1) * 128, b, e, sides,
-                               lane);
+            finish_block<MODE>(k.epi, masks.at(piece >> 1), mine, bias, b, e, sides, lane);
           else
-            finish_columns<MODE>(k.epi, masks.at(cc >> 1), mine, biases + (cc >> 1) * 128,
-                                 out_t ? j0 : i0,
+            finish_columns<MODE>(k.epi, masks.at(piece >> 1), mine, bias, out_t ? j0 : i0,
                                  out_t ? i0 : j0, e, lane);
           __syncwarp();
         }
@@ -1381,7 +1413,9 @@ __global__ void __launch_bounds__((FORM == PATCH_GEN ? 16 : 12) * 32, 1)
       if (sums && split == 0) {
         if (S > 1) {
           float other;
-          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(other) : "r"(part_at(ring, chunks, w, lane)));
+          asm volatile("ld.shared.f32 %0, [%1];"
+                       : "=f"(other)
+                       : "r"(part_at<kPiece>(ring, pieces, w, lane)));
           bias_sum += other;
         }
         store_bias(k, g, (int64_t)(g.bias_b ? tj : ti) * 256 + half * kRowsCta + w * 32 + lane,
@@ -1516,7 +1550,7 @@ static bool box_map(CUtensorMap* map, const Mat& a, int64_t rows, int64_t cols, 
 // Shared memory beside the operand ring, and the ring's stages in what is left.
 static int side_bytes(const TileK& g, int form) {
   return (g.bias_tiles || g.bias_fused ? kOnesBytes : 0) + g.bias_in + (form >= BOX_BF16 ? g.boxes * kSlot * (g.two_slots ? 2 : 1)
-                           : kEpiWarps * kPatch * 4);
+                           : kPatchWarps * kPatch * 4);
 }
 static int stages_for(const TileK& g, int form) {
   const int n = (kSmemMost - 1024 - side_bytes(g, form)) / (kBytesA + g.bn * kDeep);
@@ -1547,7 +1581,7 @@ static cudaError_t launch_tiles(const CUtensorMap& ma, const CUtensorMap& mb,
   g.split_log2 = g.splits - 1;  // 1 or 2 parts
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(clusters * 2 * g.splits));
-  cfg.blockDim = dim3((FORM == PATCH_GEN ? 16 : 12) * 32);
+  cfg.blockDim = dim3(threads_of(FORM));
   cfg.dynamicSmemBytes = (size_t)g.stages * (kBytesA + g.bn * kDeep) + side_bytes(g, FORM);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -1641,7 +1675,7 @@ static cudaError_t launch_mode(const ProductK& in, cudaStream_t st) {
   }
   if (tiles_i * (g.tiles_j + 1) >= (1ll << 28) || kblocks >= (1ll << 30))
     return cudaErrorInvalidValue;
-  g.bias_in = k.epi.bias.p ? kEpiWarps * 512 : 0;
+  g.bias_in = k.epi.bias.p ? 4096 : 0;  // 8 warps of 32 columns 4 times, or 16 of 16
   g.tiles_i = (int)tiles_i;
   g.kblocks = (int)kblocks;
   g.round = exact ? kRound : 0;

@@ -316,23 +316,22 @@ __device__ __forceinline__ void push_keep(uint32_t& bits, uint32_t w, uint32_t b
       : "r"(w), "r"(below));
 }
 
-// The mask of 32 elements as 8 groups of 4 columns, 2 PER groups in each of
-// 4 / PER rows `row_step` apart; the first element is the highest bit.  A loop
-// of two blocks, not eight copies: an epilogue runs this a few times per
-// kernel and has to fetch the code as well.
-template <int PER>
-__device__ __forceinline__ uint32_t keep32(const DropK& d, uint64_t offset, uint32_t row,
-                                           uint32_t row_step, int64_t col) {
+// The mask of 4 G elements as G groups of 4 columns, PER groups in each of
+// G / PER rows `row_step` apart; the first element is the highest bit.  A loop
+// of two blocks, not G copies: an epilogue runs this a few times per kernel
+// and has to fetch the code as well.
+template <int G, int PER>
+__device__ __forceinline__ uint32_t keep_mask(const DropK& d, uint64_t offset, uint32_t row,
+                                              uint32_t row_step, int64_t col) {
   const uint32_t lo = (uint32_t)offset, hi = (uint32_t)(offset >> 32), below = 0u - d.least;
   const uint32_t group = (uint32_t)(col >> 2);
   uint32_t keep = 0;
 #pragma unroll 1
-  for (uint32_t g = 0; g < 8; g += 2) {
+  for (uint32_t g = 0; g < G; g += 2) {
     uint4 w[2];
 #pragma unroll
     for (uint32_t h = 0; h < 2; ++h)
-      w[h] = philox(make_uint4(group + (g + h) % (2 * PER),
-                               row + row_step * ((g + h) / (2 * PER)), lo, hi),
+      w[h] = philox(make_uint4(group + (g + h) % PER, row + row_step * ((g + h) / PER), lo, hi),
                     d);
 #pragma unroll
     for (uint32_t h = 0; h < 2; ++h) {
@@ -342,6 +341,7 @@ __device__ __forceinline__ uint32_t keep32(const DropK& d, uint64_t offset, uint
       push_keep(keep, w[h].w, below);
     }
   }
+  keep <<= 32 - 4 * G;
   return d.all ? 0u : d.least == 0 ? 0xFFFFFFFFu : keep;
 }
 
