@@ -21,8 +21,9 @@
 //                 memory, and a thread goes on with 8 consecutive columns by
 //                 plain loads and stores; for transposed outputs and rows off
 //                 16-byte boundaries
-//   warps 12-15   (gen) load operands whose base or rows lie off 16-byte
-//                 boundaries, which TMA cannot, with plain loads
+//   warps 12-19   (gen) load operands whose base or rows lie off 16-byte
+//                 boundaries, which TMA cannot, with plain loads; warp 3 tells
+//                 the pair's first CTA of each tile they have filled
 // Tiles are walked persistently with two sets of sums, so one tile's epilogue
 // runs under the next one's products.  Where there are too few tiles to fill
 // the GPU the contraction is split over the S pairs of a larger cluster, whose
@@ -38,7 +39,7 @@ namespace zk {
 constexpr int kRowsCta = 128;          // rows of A per CTA (tensor-memory lanes)
 constexpr int kDeep = 64;              // contraction per stage: 128 bytes, one swizzle row
 constexpr int kBytesA = kRowsCta * kDeep * 2;
-constexpr int kEpiWarp0 = 4, kPatchWarps = 8, kBoxWarps = 16, kGenWarp0 = 12, kGenWarps = 4;
+constexpr int kEpiWarp0 = 4, kPatchWarps = 8, kBoxWarps = 16, kGenWarp0 = 12, kGenWarps = 8;
 constexpr int kPatch = 32 * 36;        // floats of a 32 x 32 patch, rows 36 apart
 constexpr int kMaxStages = 9;
 constexpr int kRound = 12;             // 64-deep steps of a round (see launch_mode)
@@ -74,7 +75,7 @@ struct TileK {
   int round;                         // steps whose sums the tensor cores keep (see launch_mode)
   int acc_sets;                      // sets of sums in tensor memory used in turn
   int i_fast;                        // consecutive tiles differ in i (else in j)
-  int gen_a, gen_b;                  // elements per plain load; 0: by TMA
+  int gen_a, gen_b;                  // operand by plain loads (else TMA)
   int boxes;                         // ring of box chunks (box forms)
   int two_slots;                     // a chunk holds two slots
   uint32_t tmem_cols;
@@ -303,80 +304,97 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr, bool contig) {
          (2ull << 61);
 }
 
-// 8 elements from index `at` on, `valid` of them inside, W per load.
-template <int W>
-__device__ __forceinline__ uint4 gen_load(const uint16_t* p, int valid) {
-  uint32_t w[4] = {0, 0, 0, 0};
-  if constexpr (W == 4) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      if (valid >= 4 * j + 4) {
-        const uint2 u = *reinterpret_cast<const uint2*>(p + 4 * j);
-        w[2 * j] = u.x;
-        w[2 * j + 1] = u.y;
-      } else {
-#pragma unroll
-        for (int e = 4 * j; e < 4 * j + 4; ++e)
-          if (e < valid) w[e / 2] |= (uint32_t)p[e] << (16 * (e & 1));
-      }
-  } else if constexpr (W == 2) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (valid >= 2 * j + 2)
-        w[j] = *reinterpret_cast<const uint32_t*>(p + 2 * j);
-      else if (valid > 2 * j)
-        w[j] = p[2 * j];
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e < valid) w[e / 2] |= (uint32_t)p[e] << (16 * (e & 1));
+// ---------------------------------------------------------------------------
+// Operands off 16-byte boundaries, by plain loads of the GEN warps' 256
+// threads.  A unit of a tile is 16 bytes of its swizzled rows: 8 consecutive
+// elements, read as the two 16-byte words of memory that hold them and shifted
+// into place.  A thread takes up to 4 units of an operand's tile, 32 lines
+// apart, and reads the next tile's before it stores these, over steps and
+// tiles.  Units that are cut by the matrix's edge, or whose words reach outside
+// its memory, are gathered element by element when they are stored.
+// ---------------------------------------------------------------------------
+constexpr int kUnits = 4;
+struct GenBatch {
+  uint4 lo[kUnits], hi[kUnits];
+  uint32_t how;  // a byte per unit: the shift in bytes, or 1: gather at the store
+};
+struct GenWhat {
+  const Mat* a;
+  bool contig;
+  int64_t rows, depth, i0, c0;  // rows i0.. x contraction c0..c0+63
+  int lines, count;             // of the tile; units per thread
+};
+// Unit q of thread t: its first element's index, and how many lie inside.
+__device__ __forceinline__ int64_t gen_unit(const GenWhat& b, int t, int q, int& valid) {
+  const int unit = t & 7, l0 = t >> 3;  // 8 units run along the contiguous index
+  if (b.contig) {
+    const int64_t i = b.i0 + l0 + 32 * q, c = b.c0 + unit * 8, left = b.depth - c;
+    valid = i < b.rows && l0 + 32 * q < b.lines && left > 0 ? (int)(left < 8 ? left : 8) : 0;
+    return i * b.a->ld + c;
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  // 64 lines of depth per 64 rows
+  const int64_t c = b.c0 + l0 + 32 * (q & 1), i = b.i0 + (q >> 1) * 64 + unit * 8,
+                left = b.rows - i;
+  valid = c < b.depth && left > 0 ? (int)(left < 8 ? left : 8) : 0;
+  return c * b.a->ld + i;
 }
-
-// Rows [i0, i0 + count) x contraction [c0, c0 + 64) of an operand into its
-// swizzled tile, by the GEN warps' 128 threads (t).
-template <int W>
-__device__ __forceinline__ void gen_tile(const Mat& a, bool contig, int64_t rows, int64_t depth,
-                                         int64_t i0, int count, int64_t c0, uint32_t dst, int t) {
-  const uint16_t* base = static_cast<const uint16_t*>(a.p);
-#pragma unroll 4
-  for (int q = t; q < count * 8; q += kGenWarps * 32) {
-    // 8 units of 8 elements run along the contiguous index
-    const int unit = q & 7, line = q >> 3;
-    int64_t at;
+// Predicated, not branched around: a branch made each load wait for the last.
+__device__ __forceinline__ void load_if(bool p, const void* from, uint4& u) {
+  asm volatile(
+      "{ .reg .pred p; setp.ne.u32 p, %5, 0; @p ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4]; }"
+      : "+r"(u.x), "+r"(u.y), "+r"(u.z), "+r"(u.w)
+      : "l"(from), "r"((uint32_t)p));
+}
+__device__ __forceinline__ void gen_fetch(const GenWhat& b, int t, GenBatch& g) {
+  const char* base = static_cast<const char*>(b.a->p);
+  const int64_t last =
+      b.contig ? (b.rows - 1) * b.a->ld + b.depth : (b.depth - 1) * b.a->ld + b.rows;
+  const char* end = base + 2 * last;
+  g.how = 0;
+#pragma unroll
+  for (int q = 0; q < kUnits; ++q) {
     int valid;
-    uint32_t to;
-    if (contig) {
-      const int64_t i = i0 + line, c = c0 + unit * 8;
-      valid = i < rows && c < depth ? (int)(depth - c < 8 ? depth - c : 8) : 0;
-      at = i * a.ld + c;
-      to = line * 128 + ((unit ^ (line & 7)) << 4);
-    } else {
-      const int block = line >> 6, deep = line & 63;  // 64 lines of depth per 64 rows
-      const int64_t c = c0 + deep, i = i0 + block * 64 + unit * 8;
-      valid = c < depth && i < rows ? (int)(rows - i < 8 ? rows - i : 8) : 0;
-      at = c * a.ld + i;
-      to = block * 8192 + deep * 128 + ((unit ^ (deep & 7)) << 4);
-    }
-    uint4 v = make_uint4(0, 0, 0, 0);
-    const int64_t last = contig ? (rows - 1) * a.ld + depth : (depth - 1) * a.ld + rows;
-    if (valid > 0 && in_extent(at, at + valid, 0, last, ZERO_SITE_LINEAR_IN))
-      v = gen_load<W>(base + at, valid);
-    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + to), "r"(v.x), "r"(v.y),
-                 "r"(v.z), "r"(v.w)
-                 : "memory");
+    const int64_t at = gen_unit(b, t, q, valid);
+    const bool in = q < b.count && valid > 0 &&
+                    in_extent(at, at + valid, 0, last, ZERO_SITE_LINEAR_IN);
+    const char* p = base + 2 * at;
+    const uint32_t shift = (uint32_t)((uintptr_t)p & 15);
+    const char* word = p - shift;
+    const bool whole = in && valid == 8 && word >= base && word + (shift ? 32 : 16) <= end;
+    g.lo[q] = g.hi[q] = make_uint4(0, 0, 0, 0);
+    load_if(whole, word, g.lo[q]);
+    load_if(whole && shift, word + 16, g.hi[q]);
+    g.how |= (whole ? shift : in ? 1u : 0u) << (8 * q);
   }
 }
-__device__ __forceinline__ void gen_operand(int width, const Mat& a, bool contig, int64_t rows,
-                                            int64_t depth, int64_t i0, int count, int64_t c0,
-                                            uint32_t dst, int t) {
-  if (width == 4)
-    gen_tile<4>(a, contig, rows, depth, i0, count, c0, dst, t);
-  else if (width == 2)
-    gen_tile<2>(a, contig, rows, depth, i0, count, c0, dst, t);
-  else
-    gen_tile<1>(a, contig, rows, depth, i0, count, c0, dst, t);
+__device__ __forceinline__ void gen_store(const GenWhat& b, int t, const GenBatch& g,
+                                          uint32_t tile) {
+  const int unit = t & 7, l0 = t >> 3;
+  const uint32_t to = tile + l0 * 128 + ((unit ^ (l0 & 7)) << 4);
+#pragma unroll
+  for (int q = 0; q < kUnits; ++q) {
+    const uint32_t how = g.how >> (8 * q) & 0xFF;
+    uint32_t x[8] = {g.lo[q].x, g.lo[q].y, g.lo[q].z, g.lo[q].w,
+                     g.hi[q].x, g.hi[q].y, g.hi[q].z, g.hi[q].w};
+#pragma unroll
+    for (int i = 0; i < 6; ++i) x[i] = how & 8 ? x[i + 2] : x[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) x[i] = how & 4 ? x[i + 1] : x[i];
+    const uint32_t bits = (how & 2) * 8;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = __funnelshift_r(x[i], x[i + 1], bits);
+    if (how & 1) {
+      int valid;
+      const uint16_t* e = static_cast<const uint16_t*>(b.a->p) + gen_unit(b, t, q, valid);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k < valid) x[k / 2] |= (uint32_t)e[k] << (16 * (k & 1));
+    }
+    // 32 lines are 4096 bytes, of either kind of tile
+    if (q < b.count && l0 + 32 * q < b.lines)
+      asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to + q * 4096), "r"(x[0]),
+                   "r"(x[1]), "r"(x[2]), "r"(x[3]));
+  }
 }
 
 // The tile of index t: its row and column, or the bias column (j < 0).
@@ -1012,7 +1030,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
   constexpr int kEpiWarps = BOX ? kBoxWarps : kPatchWarps;
   constexpr int kPiece = BOX ? 16 : 32, kSets = kEpiWarps / 4;
   extern __shared__ __align__(1024) unsigned char smem[];
-  __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 5 + 2 * kMostBoxes];
+  __shared__ __align__(8) uint64_t bars[3 * kMaxStages + 5 + 2 * kMostBoxes];
   __shared__ uint32_t tmem_at;
   __shared__ int dead;
   const uint32_t rank = cluster_rank(), half = rank & 1, leader = rank & ~1u;
@@ -1027,11 +1045,13 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
   const uint32_t full = smem_u32(bars), empty = full + 8 * kMaxStages;
   const uint32_t tfull = empty + 8 * kMaxStages, tempty = tfull + 16, ready = tempty + 16;
   const uint32_t efull = ready + 8, edone = efull + 8 * kMostBoxes;
+  const uint32_t filled = edone + 8 * kMostBoxes;  // by the GEN warps
 
   if (warp == 0 && elect()) {
     dead = 0;
     for (int s = 0; s < g.stages; ++s) {
-      bar_init(full + 8 * s, 1 + (GEN ? 2 * kGenWarps : 0));
+      bar_init(full + 8 * s, GEN ? 3 : 1);
+      if (GEN) bar_init(filled + 8 * s, kGenWarps);
       bar_init(empty + 8 * s, 1);
     }
     for (int a = 0; a < 2; ++a) {
@@ -1430,38 +1450,75 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
       }
     }
   } else if (GEN && warp >= kGenWarp0) {
-    const int t128 = threadIdx.x - kGenWarp0 * 32;
+    const int t256 = threadIdx.x - kGenWarp0 * 32;
+    const int bn = g.bn, stages = g.stages;
+    // One batch of registers per operand: stored when the step's slot is free,
+    // fetched for the next step right after.
+    struct Step {
+      int t, ti, tj, kb;
+    };
+    auto has_a = [&](const Step& c) { return (c.tj < 0 && g.bias_b ? g.gen_b : g.gen_a) != 0; };
+    auto has_b = [&](const Step& c) { return c.tj >= 0 && g.gen_b; };
+    auto of_a = [&](const Step& c) {  // for a tile of B's bias sums, B in A's place
+      const bool b = c.tj < 0 && g.bias_b;
+      return GenWhat{b ? &k.b : &k.a, b ? b_c : a_c, b ? k.cols : k.rows, k.depth,
+                     (int64_t)c.ti * 256 + half * kRowsCta, (int64_t)c.kb * kDeep, kRowsCta,
+                     kRowsCta / 32};
+    };
+    auto of_b = [&](const Step& c) {
+      return GenWhat{&k.b, b_c, k.cols, k.depth, (int64_t)c.tj * bn + half * (bn / 2),
+                     (int64_t)c.kb * kDeep, bn / 2, (bn / 2 + 31) / 32};
+    };
+    Step now{first, 0, 0, kb0};
+    GenBatch ra, rb;
+    uint32_t s = 0, ph = 0;
+    bool ok = kb0 < kb1;
+    if (ok && now.t < tiles) {
+      tile_at(g, now.t, now.ti, now.tj);
+      if (has_a(now)) gen_fetch(of_a(now), t256, ra);
+      if (has_b(now)) gen_fetch(of_b(now), t256, rb);
+    }
+    while (ok && now.t < tiles) {
+      Step next = now;
+      if (++next.kb >= kb1) {
+        next.kb = kb0;
+        next.t += clusters;
+        if (next.t < tiles) tile_at(g, next.t, next.ti, next.tj);
+      }
+      ok = bar_wait(empty + 8 * s, ph ^ 1, &dead);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const uint32_t a_at = ring + s * stage_bytes;
+      if (has_a(now)) gen_store(of_a(now), t256, ra, a_at);
+      if (next.t < tiles && has_a(next)) gen_fetch(of_a(next), t256, ra);
+      if (has_b(now)) gen_store(of_b(now), t256, rb, a_at + kBytesA);
+      if (next.t < tiles && has_b(next)) gen_fetch(of_b(next), t256, rb);
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) bar_arrive(filled + 8 * s);
+      if (++s == (uint32_t)stages) {
+        s = 0;
+        ph ^= 1;
+      }
+      now = next;
+    }
+  } else if (GEN && warp == 3) {
+    // The arrival at the pair's first CTA releases to the cluster, which waits
+    // for every access of the thread before it: on a warp of its own it does
+    // not wait for the next tile's loads (1300 cycles a step).
     const uint32_t full_lead = remote(full, leader);
     uint32_t s = 0, ph = 0;
-    bool ok = true;
-    for (int t = first; t < tiles && ok; t += clusters) {
-      int ti, tj;
-      tile_at(g, t, ti, tj);
-      const int64_t i0 = (int64_t)ti * 256 + half * kRowsCta;
-      const int64_t j0 = (int64_t)tj * g.bn + half * (g.bn / 2);
+    bool live = true;
+    for (int t = first; t < tiles; t += clusters)
       for (int kb = kb0; kb < kb1; ++kb) {
-        ok = bar_wait(empty + 8 * s, ph ^ 1, &dead);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        const uint32_t a_at = ring + s * stage_bytes, b_at = a_at + kBytesA;
-        const int64_t c0 = (int64_t)kb * kDeep;
-        if (tj < 0 && g.bias_b) {
-          if (g.gen_b)
-            gen_operand(g.gen_b, k.b, b_c, k.cols, k.depth, i0, kRowsCta, c0, a_at, t128);
-        } else if (g.gen_a) {
-          gen_operand(g.gen_a, k.a, a_c, k.rows, k.depth, i0, kRowsCta, c0, a_at, t128);
-        }
-        if (g.gen_b && tj >= 0)
-          gen_operand(g.gen_b, k.b, b_c, k.cols, k.depth, j0, g.bn / 2, c0, b_at, t128);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        live = live && bar_wait(filled + 8 * s, ph, &dead);
+        if (elect() && live) bar_arrive_cluster_release(full_lead + 8 * s);
         __syncwarp();
-        if (lane == 0) bar_arrive_cluster_release(full_lead + 8 * s);
         if (++s == (uint32_t)g.stages) {
           s = 0;
           ph ^= 1;
         }
       }
-    }
   }
   __syncwarp();
 
@@ -1502,15 +1559,10 @@ static EncodeFn encode_fn() {
   return reinterpret_cast<EncodeFn>(f);
 }
 
-// Elements per plain load of an operand, or 0 where TMA can read it: its base
-// and its rows (where there are several) on 16-byte boundaries.
-static int gen_width(const Mat& a, int64_t lines) {
-  const uintptr_t b = (uintptr_t)a.p;
-  const int64_t ld = lines > 1 ? a.ld : 8;
-  if ((b & 15) == 0 && ld % 8 == 0) return 0;
-  if ((b & 7) == 0 && ld % 4 == 0) return 4;
-  if ((b & 3) == 0 && ld % 2 == 0) return 2;
-  return 1;
+// Whether an operand has to come by plain loads: its base or its rows (where
+// there are several) lie off 16-byte boundaries.
+static bool by_loads(const Mat& a, int64_t lines) {
+  return ((uintptr_t)a.p & 15) != 0 || (lines > 1 && a.ld % 8 != 0);
 }
 
 static bool encode(CUtensorMap* map, bool f32, void* p, int64_t inner, int64_t outer, int64_t ld,
@@ -1687,8 +1739,8 @@ static cudaError_t launch_mode(const ProductK& in, cudaStream_t st) {
   CUtensorMap ma{}, mb{};
   BoxMaps maps{};
   if (k.depth > 0) {
-    g.gen_a = k.rows > 0 ? gen_width(k.a, k.a_c ? k.rows : k.depth) : 0;
-    g.gen_b = k.cols > 0 ? gen_width(k.b, k.b_c ? k.cols : k.depth) : 0;
+    g.gen_a = k.rows > 0 ? by_loads(k.a, k.a_c ? k.rows : k.depth) : 0;
+    g.gen_b = k.cols > 0 ? by_loads(k.b, k.b_c ? k.cols : k.depth) : 0;
     if (!g.gen_a && k.rows > 0 &&
         !operand_map(&ma, k.a, k.a_c, k.rows, k.depth, kRowsCta))
       return cudaErrorInvalidValue;
