@@ -42,6 +42,7 @@ constexpr int kBytesA = kRowsCta * kDeep * 2;
 constexpr int kEpiWarp0 = 4, kPatchWarps = 8, kBoxWarps = 16, kGenWarp0 = 12, kGenWarps = 8;
 constexpr int kPatch = 32 * 36;        // floats of a 32 x 32 patch, rows 36 apart
 constexpr int kMaxStages = 9;
+constexpr int kRaw = 2;                // raw buffers of the GEN warps
 constexpr int kRound = 12;             // 64-deep steps of a round (see launch_mode)
 constexpr int kOnesBytes = 2048;
 constexpr int kSlot = 16384;           // a box of 128 rows of 128 bytes
@@ -290,6 +291,17 @@ __device__ __forceinline__ void st_cluster4(uint32_t addr, const uint32_t r[4]) 
                "r"(r[2]), "r"(r[3]));
 }
 
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+  uint4 u;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+               : "r"(addr));
+  return u;
+}
+__device__ __forceinline__ void sts16(uint32_t addr, uint4 u) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(u.x), "r"(u.y), "r"(u.z),
+               "r"(u.w));
+}
 // Reads and writes of shared memory above are volatile, hence kept in order,
 // but do not clobber memory: a clobber makes the compiler fetch every kernel
 // parameter again at its next use, ~70 cycles each in a row.
@@ -305,96 +317,137 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr, bool contig) {
 }
 
 // ---------------------------------------------------------------------------
-// Operands off 16-byte boundaries, by plain loads of the GEN warps' 256
-// threads.  A unit of a tile is 16 bytes of its swizzled rows: 8 consecutive
-// elements, read as the two 16-byte words of memory that hold them and shifted
-// into place.  A thread takes up to 4 units of an operand's tile, 32 lines
-// apart, and reads the next tile's before it stores these, over steps and
-// tiles.  Units that are cut by the matrix's edge, or whose words reach outside
-// its memory, are gathered element by element when they are stored.
+// Operands off 16-byte boundaries, by the GEN warps' 256 threads.  A line of a
+// tile (64 consecutive elements: a row's contraction, or 64 rows at one depth)
+// lies in nine aligned 16-byte words of memory, which asynchronous copies bring
+// to a raw buffer some steps ahead; each warp then shifts the 16 lines that it
+// fetched into the swizzled tile.  Nothing outside the matrix's memory is read:
+// a copy at its end is cut short, and a word that begins before its start is
+// gathered element by element.
+//
+// The loops are small and what can be is carried from step to step: these warps
+// run little else, and longer code waits for its instructions (3873 x 1614 by
+// 9592 x 1614, odd rows: unrolled 781 us, so 536; by loads into registers 877;
+// by 2-byte loads 2181).
 // ---------------------------------------------------------------------------
-constexpr int kUnits = 4;
-struct GenBatch {
-  uint4 lo[kUnits], hi[kUnits];
-  uint32_t how;  // a byte per unit: the shift in bytes, or 1: gather at the store
-};
+constexpr int kRawLine = 9 * 16;
 struct GenWhat {
   const Mat* a;
   bool contig;
-  int64_t rows, depth, i0, c0;  // rows i0.. x contraction c0..c0+63
-  int lines, count;             // of the tile; units per thread
+  int64_t rows, depth, i0;  // rows i0.. of the operand, contraction from kb * 64
+  int lines;                // of the tile; 16 per warp
 };
-// Unit q of thread t: its first element's index, and how many lie inside.
-__device__ __forceinline__ int64_t gen_unit(const GenWhat& b, int t, int q, int& valid) {
-  const int unit = t & 7, l0 = t >> 3;  // 8 units run along the contiguous index
+// Thread t brings half of line t / 2: words 0-4 or 5-8.
+struct GenIssue {
+  const char *base, *end, *p;  // the matrix's memory; this line of the next step
+  int64_t step;                // bytes to its next
+  int64_t left;                // steps' depth before the line leaves the matrix
+  int by;                      // what a step takes off it
+};
+__device__ __forceinline__ void gen_enter(const GenWhat& b, int t, int kb, GenIssue& g) {
+  const int line = t >> 1;
+  const int64_t ld = b.a->ld, c0 = (int64_t)kb * kDeep;
+  g.base = static_cast<const char*>(b.a->p);
+  g.end = g.base +
+          2 * (b.contig ? (b.rows - 1) * ld + b.depth : (b.depth - 1) * ld + b.rows);
+  int64_t at;
   if (b.contig) {
-    const int64_t i = b.i0 + l0 + 32 * q, c = b.c0 + unit * 8, left = b.depth - c;
-    valid = i < b.rows && l0 + 32 * q < b.lines && left > 0 ? (int)(left < 8 ? left : 8) : 0;
-    return i * b.a->ld + c;
+    const int64_t i = b.i0 + line;
+    at = i * ld + c0;
+    g.step = 2 * kDeep;
+    g.left = i < b.rows ? 1 : 0;
+    g.by = 0;
+  } else {
+    const int64_t c = c0 + (line & 63), i = b.i0 + (line & ~63);  // 64 lines per 64 rows
+    at = c * ld + i;
+    g.step = 2 * kDeep * ld;
+    g.left = i < b.rows ? b.depth - c : 0;
+    g.by = kDeep;
   }
-  // 64 lines of depth per 64 rows
-  const int64_t c = b.c0 + l0 + 32 * (q & 1), i = b.i0 + (q >> 1) * 64 + unit * 8,
-                left = b.rows - i;
-  valid = c < b.depth && left > 0 ? (int)(left < 8 ? left : 8) : 0;
-  return c * b.a->ld + i;
+  if (line >= b.lines) g.left = 0;
+  g.p = g.base + 2 * at;
 }
-// Predicated, not branched around: a branch made each load wait for the last.
-__device__ __forceinline__ void load_if(bool p, const void* from, uint4& u) {
-  asm volatile(
-      "{ .reg .pred p; setp.ne.u32 p, %5, 0; @p ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4]; }"
-      : "+r"(u.x), "+r"(u.y), "+r"(u.z), "+r"(u.w)
-      : "l"(from), "r"((uint32_t)p));
+__device__ __noinline__ void gen_first_word(const char* word, const char* base, const char* end,
+                                            uint32_t to) {
+  uint32_t x[4] = {0, 0, 0, 0};
+  for (int e = 0; e < 8; ++e)
+    if (word + 2 * e >= base && word + 2 * e < end)
+      x[e / 2] |= (uint32_t)*reinterpret_cast<const uint16_t*>(word + 2 * e) << (16 * (e & 1));
+  sts16(to, make_uint4(x[0], x[1], x[2], x[3]));
 }
-__device__ __forceinline__ void gen_fetch(const GenWhat& b, int t, GenBatch& g) {
-  const char* base = static_cast<const char*>(b.a->p);
-  const int64_t last =
-      b.contig ? (b.rows - 1) * b.a->ld + b.depth : (b.depth - 1) * b.a->ld + b.rows;
-  const char* end = base + 2 * last;
-  g.how = 0;
-#pragma unroll
-  for (int q = 0; q < kUnits; ++q) {
-    int valid;
-    const int64_t at = gen_unit(b, t, q, valid);
-    const bool in = q < b.count && valid > 0 &&
-                    in_extent(at, at + valid, 0, last, ZERO_SITE_LINEAR_IN);
-    const char* p = base + 2 * at;
-    const uint32_t shift = (uint32_t)((uintptr_t)p & 15);
-    const char* word = p - shift;
-    const bool whole = in && valid == 8 && word >= base && word + (shift ? 32 : 16) <= end;
-    g.lo[q] = g.hi[q] = make_uint4(0, 0, 0, 0);
-    load_if(whole, word, g.lo[q]);
-    load_if(whole && shift, word + 16, g.hi[q]);
-    g.how |= (whole ? shift : in ? 1u : 0u) << (8 * q);
+__device__ __forceinline__ void gen_issue(GenIssue& g, int t, uint32_t raw) {
+  const int w0 = (t & 1) * 5, words = 5 - (t & 1);
+  const int64_t at = (g.p - g.base) / 2;
+  const bool on = g.left > 0 &&
+                  in_extent(at, at + 1, 0, (g.end - g.base) / 2, ZERO_SITE_LINEAR_IN);
+  const char* word = g.p - ((uintptr_t)g.p & 15) + 16 * w0;
+  uint32_t to = raw + (uint32_t)((t >> 1) * kRawLine + 16 * w0);
+#pragma unroll 1
+  for (int j = 0; j < words; ++j, word += 16, to += 16) {
+    if (on && word < g.base) {
+      gen_first_word(word, g.base, g.end, to);
+      continue;
+    }
+    const int64_t rest = on ? g.end - word : 0;
+    const uint32_t n = rest <= 0 ? 0u : rest < 16 ? (uint32_t)rest : 16u;
+    // nothing is read where n is 0 (any aligned address of the matrix will do)
+    const char* from = n ? word : g.base + (-(uintptr_t)g.base & 15);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(n)
+                 : "memory");
   }
+  g.p += g.step;
+  g.left -= g.by;
 }
-__device__ __forceinline__ void gen_store(const GenWhat& b, int t, const GenBatch& g,
-                                          uint32_t tile) {
-  const int unit = t & 7, l0 = t >> 3;
-  const uint32_t to = tile + l0 * 128 + ((unit ^ (l0 & 7)) << 4);
+// The warp's 16 lines from the raw buffer to the tile: a thread has unit t % 8
+// (8 elements) of four lines, four apart.
+struct GenShift {
+  uint32_t shifts;  // a byte per line: where it begins in its first word
+  int64_t left;     // elements of the unit inside the matrix, 8 or more: all
+  int by;           // what a step takes off it
+};
+__device__ __forceinline__ void gen_enter(const GenWhat& b, int t, int kb, GenShift& g) {
+  const int unit = t & 7, first = (t >> 5) * 16 + ((t & 31) >> 3);
+  const uint32_t base = (uint32_t)(uintptr_t)b.a->p, ld = (uint32_t)b.a->ld;
+  g.shifts = 0;
+  for (int q = 0; q < 4; ++q) {
+    const int line = first + 4 * q;
+    const uint32_t at =
+        b.contig ? (uint32_t)(b.i0 + line) * ld
+                 : (uint32_t)(line & 63) * ld + (uint32_t)(b.i0 + (line & ~63));
+    g.shifts |= ((base + 2 * at) & 15) << (8 * q);  // a step is a multiple of 16 bytes
+  }
+  g.left = b.contig ? b.depth - (int64_t)kb * kDeep - unit * 8
+                    : b.rows - b.i0 - (first & ~63) - unit * 8;
+  g.by = b.contig ? kDeep : 0;
+}
+__device__ __forceinline__ void gen_shift(GenShift& g, int t, uint32_t raw, uint32_t tile) {
+  const int unit = t & 7, first = (t >> 5) * 16 + ((t & 31) >> 3), row = first & 63;
+  uint32_t from = raw + (uint32_t)(first * kRawLine + unit * 16);
+  // 64 lines are 8192 bytes in either kind of tile; four lines on, the swizzle
+  // flips the unit's highest bit
+  uint32_t to = tile + (uint32_t)((first >> 6) * 8192 + row * 128 + ((unit ^ (row & 7)) << 4));
+  uint32_t shifts = g.shifts;
+#pragma unroll 1
+  for (int q = 0; q < 4; ++q, from += 4 * kRawLine, to = (to ^ 64) + 512, shifts >>= 8) {
+    const uint4 lo = lds16(from), hi = lds16(from + 16);
+    uint32_t x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-  for (int q = 0; q < kUnits; ++q) {
-    const uint32_t how = g.how >> (8 * q) & 0xFF;
-    uint32_t x[8] = {g.lo[q].x, g.lo[q].y, g.lo[q].z, g.lo[q].w,
-                     g.hi[q].x, g.hi[q].y, g.hi[q].z, g.hi[q].w};
+    for (int i = 0; i < 6; ++i) x[i] = shifts & 8 ? x[i + 2] : x[i];
 #pragma unroll
-    for (int i = 0; i < 6; ++i) x[i] = how & 8 ? x[i + 2] : x[i];
-#pragma unroll
-    for (int i = 0; i < 5; ++i) x[i] = how & 4 ? x[i + 1] : x[i];
-    const uint32_t bits = (how & 2) * 8;
+    for (int i = 0; i < 5; ++i) x[i] = shifts & 4 ? x[i + 1] : x[i];
+    const uint32_t bits = (shifts & 2) * 8;
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = __funnelshift_r(x[i], x[i + 1], bits);
-    if (how & 1) {
-      int valid;
-      const uint16_t* e = static_cast<const uint16_t*>(b.a->p) + gen_unit(b, t, q, valid);
+    if (g.left < 8) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (k < valid) x[k / 2] |= (uint32_t)e[k] << (16 * (k & 1));
+      for (int i = 0; i < 4; ++i) {
+        if (2 * i >= g.left) x[i] = 0;
+        else if (2 * i + 1 >= g.left) x[i] &= 0xFFFF;
+      }
     }
-    // 32 lines are 4096 bytes, of either kind of tile
-    if (q < b.count && l0 + 32 * q < b.lines)
-      asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to + q * 4096), "r"(x[0]),
-                   "r"(x[1]), "r"(x[2]), "r"(x[3]));
+    sts16(to, make_uint4(x[0], x[1], x[2], x[3]));
   }
+  g.left -= g.by;
 }
 
 // The tile of index t: its row and column, or the bias column (j < 0).
@@ -569,17 +622,6 @@ __device__ __forceinline__ uint32_t at128(int row, int unit) {
 }
 __device__ __forceinline__ uint32_t at64(int row, int unit) {
   return (uint32_t)(row * 64 + ((unit ^ ((row >> 1) & 3)) << 4));
-}
-__device__ __forceinline__ uint4 lds16(uint32_t addr) {
-  uint4 u;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
-               : "r"(addr));
-  return u;
-}
-__device__ __forceinline__ void sts16(uint32_t addr, uint4 u) {
-  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(u.x), "r"(u.y), "r"(u.z),
-               "r"(u.w));
 }
 __device__ __forceinline__ void lds_f32(uint32_t base, int row, int i, float f[8]) {
   const uint4 a = lds16(base + at128(row, 2 * i)), b = lds16(base + at128(row, 2 * i + 1));
@@ -985,9 +1027,15 @@ struct Masks {
 __device__ __forceinline__ bool owns_piece(int split, int piece, int pieces, int w) {
   return (pieces == 1 ? (w & 1) : (int)(piece >= pieces / 2)) == split;
 }
+// Where the owner of a piece finds the other's sums: its own pieces in order,
+// then those of the bias (piece == pieces): at most 80 KiB of the ring, which
+// has 96 at least.
 template <int N>
-__device__ __forceinline__ uint32_t part_at(uint32_t ring, int piece, int w, int lane) {
-  return ring + (uint32_t)((piece * 4 + w) * (N * 128) + lane * 16);
+__device__ __forceinline__ uint32_t part_at(uint32_t ring, int piece, int pieces, int w,
+                                            int lane) {
+  const int half = pieces > 1 ? pieces / 2 : 1;
+  const int at = piece == pieces ? half : piece % half;
+  return ring + (uint32_t)((at * 4 + w) * (N * 128) + lane * 16);
 }
 template <int N>
 __device__ __forceinline__ void push_part(uint32_t there, const uint32_t r[N]) {
@@ -1352,11 +1400,11 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
           uint32_t r[kPiece];
           tmem_load<kPiece>(d + piece * kPiece, r);
           if (rounds > 1) tmem_add<kPiece>(summed + piece * kPiece, r);
-          push_part<kPiece>(remote(part_at<kPiece>(ring, piece, w, lane), rank ^ 2), r);
+          push_part<kPiece>(remote(part_at<kPiece>(ring, piece, pieces, w, lane), rank ^ 2), r);
         }
         if (sums && split == 1)
           asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(
-                           remote(part_at<kPiece>(ring, pieces, w, lane), rank ^ 2)),
+                           remote(part_at<kPiece>(ring, pieces, pieces, w, lane), rank ^ 2)),
                        "f"(bias_sum));
         cluster_arrive();
         cluster_wait();
@@ -1367,7 +1415,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
         uint32_t r[kPiece];
         tmem_load<kPiece>(d + piece * kPiece, r);
         if (rounds > 1) tmem_add<kPiece>(summed + piece * kPiece, r);
-        if (S > 1) add_part<kPiece>(part_at<kPiece>(ring, piece, w, lane), r);
+        if (S > 1) add_part<kPiece>(part_at<kPiece>(ring, piece, pieces, w, lane), r);
 #pragma unroll
         for (int q = 0; q < kPiece; ++q) v[q] = empty_sum ? 0.0f : __uint_as_float(r[q]);
       };
@@ -1435,7 +1483,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
           float other;
           asm volatile("ld.shared.f32 %0, [%1];"
                        : "=f"(other)
-                       : "r"(part_at<kPiece>(ring, pieces, w, lane)));
+                       : "r"(part_at<kPiece>(ring, pieces, pieces, w, lane)));
           bias_sum += other;
         }
         store_bias(k, g, (int64_t)(g.bias_b ? tj : ti) * 256 + half * kRowsCta + w * 32 + lane,
@@ -1452,60 +1500,83 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
   } else if (GEN && warp >= kGenWarp0) {
     const int t256 = threadIdx.x - kGenWarp0 * 32;
     const int bn = g.bn, stages = g.stages;
-    // One batch of registers per operand: stored when the step's slot is free,
-    // fetched for the next step right after.
     struct Step {
       int t, ti, tj, kb;
+      bool a, b;  // which operands' tiles this warp has lines of
     };
     auto has_a = [&](const Step& c) { return (c.tj < 0 && g.bias_b ? g.gen_b : g.gen_a) != 0; };
     auto has_b = [&](const Step& c) { return c.tj >= 0 && g.gen_b; };
     auto of_a = [&](const Step& c) {  // for a tile of B's bias sums, B in A's place
       const bool b = c.tj < 0 && g.bias_b;
       return GenWhat{b ? &k.b : &k.a, b ? b_c : a_c, b ? k.cols : k.rows, k.depth,
-                     (int64_t)c.ti * 256 + half * kRowsCta, (int64_t)c.kb * kDeep, kRowsCta,
-                     kRowsCta / 32};
+                     (int64_t)c.ti * 256 + half * kRowsCta, kRowsCta};
     };
     auto of_b = [&](const Step& c) {
-      return GenWhat{&k.b, b_c, k.cols, k.depth, (int64_t)c.tj * bn + half * (bn / 2),
-                     (int64_t)c.kb * kDeep, bn / 2, (bn / 2 + 31) / 32};
+      return GenWhat{&k.b, b_c, k.cols, k.depth, (int64_t)c.tj * bn + half * (bn / 2), bn / 2};
     };
-    Step now{first, 0, 0, kb0};
-    GenBatch ra, rb;
+    auto enter = [&](Step& c, auto& a, auto& b) {
+      if (c.t >= tiles) return;
+      tile_at(g, c.t, c.ti, c.tj);
+      c.kb = kb0;
+      c.a = has_a(c);
+      c.b = has_b(c) && (t256 >> 5) * 16 < bn / 2;
+      if (c.a) gen_enter(of_a(c), t256, kb0, a);
+      if (c.b) gen_enter(of_b(c), t256, kb0, b);
+    };
+    const uint32_t raw0 = bias_smem + g.bias_in, raw_step = (kRowsCta + bn / 2) * kRawLine;
+    Step ahead{first, 0, 0, kb0, false, false}, now = ahead;
+    GenIssue ia, ib;
+    GenShift sa, sb;
+    uint32_t rb = 0, wb = 0;  // raw buffers: shifted next, filled next
+    auto issue = [&]() {      // one group of copies per step, empty past the last
+      if (ahead.t < tiles) {
+        const uint32_t raw = raw0 + wb * raw_step;
+        if (ahead.a) gen_issue(ia, t256, raw);
+        if (ahead.b) gen_issue(ib, t256, raw + kRowsCta * kRawLine);
+        if (++wb == kRaw) wb = 0;
+        if (++ahead.kb >= kb1) {
+          ahead.t += clusters;
+          enter(ahead, ia, ib);
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
     uint32_t s = 0, ph = 0;
     bool ok = kb0 < kb1;
-    if (ok && now.t < tiles) {
-      tile_at(g, now.t, now.ti, now.tj);
-      if (has_a(now)) gen_fetch(of_a(now), t256, ra);
-      if (has_b(now)) gen_fetch(of_b(now), t256, rb);
+    if (ok) {
+      enter(ahead, ia, ib);
+      enter(now, sa, sb);
+#pragma unroll 1
+      for (int q = 0; q < kRaw - 1; ++q) issue();
     }
     while (ok && now.t < tiles) {
-      Step next = now;
-      if (++next.kb >= kb1) {
-        next.kb = kb0;
-        next.t += clusters;
-        if (next.t < tiles) tile_at(g, next.t, next.ti, next.tj);
-      }
+      issue();
       ok = bar_wait(empty + 8 * s, ph ^ 1, &dead);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      const uint32_t a_at = ring + s * stage_bytes;
-      if (has_a(now)) gen_store(of_a(now), t256, ra, a_at);
-      if (next.t < tiles && has_a(next)) gen_fetch(of_a(next), t256, ra);
-      if (has_b(now)) gen_store(of_b(now), t256, rb, a_at + kBytesA);
-      if (next.t < tiles && has_b(next)) gen_fetch(of_b(next), t256, rb);
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      asm volatile("cp.async.wait_group %0;" ::"n"(kRaw - 1) : "memory");
       __syncwarp();
+      const uint32_t a_at = ring + s * stage_bytes, raw = raw0 + rb * raw_step;
+      if (now.a) gen_shift(sa, t256, raw, a_at);
+      if (now.b) gen_shift(sb, t256, raw + kRowsCta * kRawLine, a_at + kBytesA);
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();  // the raw lines are read, the tile's are written
       if (lane == 0) bar_arrive(filled + 8 * s);
       if (++s == (uint32_t)stages) {
         s = 0;
         ph ^= 1;
       }
-      now = next;
+      if (++rb == kRaw) rb = 0;
+      if (++now.kb >= kb1) {
+        now.t += clusters;
+        enter(now, sa, sb);
+      }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (GEN && warp == 3) {
     // The arrival at the pair's first CTA releases to the cluster, which waits
     // for every access of the thread before it: on a warp of its own it does
-    // not wait for the next tile's loads (1300 cycles a step).
+    // not wait for copies in flight (1300 cycles a step).
     const uint32_t full_lead = remote(full, leader);
     uint32_t s = 0, ph = 0;
     bool live = true;
@@ -1601,7 +1672,8 @@ static bool box_map(CUtensorMap* map, const Mat& a, int64_t rows, int64_t cols, 
 
 // Shared memory beside the operand ring, and the ring's stages in what is left.
 static int side_bytes(const TileK& g, int form) {
-  return (g.bias_tiles || g.bias_fused ? kOnesBytes : 0) + g.bias_in + (form >= BOX_BF16 ? g.boxes * kSlot * (g.two_slots ? 2 : 1)
+  return (g.bias_tiles || g.bias_fused ? kOnesBytes : 0) + g.bias_in +
+         (form == PATCH_GEN ? kRaw * (kRowsCta + g.bn / 2) * kRawLine : 0) + (form >= BOX_BF16 ? g.boxes * kSlot * (g.two_slots ? 2 : 1)
                            : kPatchWarps * kPatch * 4);
 }
 static int stages_for(const TileK& g, int form) {
