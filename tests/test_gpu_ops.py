@@ -166,6 +166,19 @@ def test_odd_sizes_in_aligned_rows(cuda, Z, m, n, k, kn):
             t.check(what)
 
 
+@pytest.mark.parametrize("kn", [False, True], ids=["nk", "kn"])
+@pytest.mark.parametrize("m,n,k,pad", [(2100, 2500, 72, 0), (2100, 2500, 840, 4), (2050, 2563, 90, 0)])
+def test_more_tiles_than_the_gpu_holds(cuda, Z, m, n, k, pad, kn):
+    """Several tiles per pair of CTAs, the last ragged both ways: sums in turn,
+    boxes and masks carried over, fp32 rounds, bias tiles of their own."""
+    run_linear(Z, m, n, k, kn, bias=BF, act="gelu_tanh", pre=True, gate=True, p=0.1, residual=BF, pad=pad)
+    run_linear(Z, m, n, k, kn, bias=F32, act="silu", residual=F32, out=F32, pad=pad)
+    check_dinput(Z, m, k, n, kn, "silu", True, BF, pad, 0)
+    check_dinput(Z, m, k, n, kn, "gelu", False, F32, pad, 0)
+    check_dweight(Z, k, n, m, kn, BF, BF, True, pad, 0)
+    check_dweight(Z, k, n, m, kn, F32, F32, False, pad, 0)
+
+
 @pytest.mark.parametrize("p", [0.0, 1.0, 0.9999])
 def test_linear_dropout_extremes(cuda, Z, p):
     run_linear(Z, 65, 70, 80, True, p=p, residual=BF)
