@@ -179,6 +179,25 @@ def test_more_tiles_than_the_gpu_holds(cuda, Z, m, n, k, pad, kn):
     check_dweight(Z, k, n, m, kn, F32, F32, False, pad, 0)
 
 
+def test_chain_of_products(cuda, Z):
+    """Each product reads what the one before wrote and starts before it ends;
+    none is waited for on the host."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    for m, n in ((1500, 1800), (200, 512), (3, 1024)):
+        a = torch.randn(m, n, device="cuda", generator=g).to(BF)
+        w = (torch.randn(n, n, device="cuda", generator=g) * n ** -0.5).to(BF)
+        outs = [torch.zeros(m, n, dtype=BF, device="cuda") for _ in range(6)]
+        src = a
+        for y in outs:
+            Z.zero_linear(src, n, w, n, Z.ZERO_W_NK, m, n, n, None, y, n)
+            src = y
+        src = a
+        for y in outs:
+            want = src.double() @ w.double().T
+            assert ((y.double() - want).norm() / want.norm()).item() < R.U16
+            src = y
+
+
 @pytest.mark.parametrize("p", [0.0, 1.0, 0.9999])
 def test_linear_dropout_extremes(cuda, Z, p):
     run_linear(Z, 65, 70, 80, True, p=p, residual=BF)
