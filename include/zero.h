@@ -732,7 +732,7 @@ int zero_layer_norm_backward(const void* dy, int64_t lddy, zero_dtype_t dydtype,
 #define ZERO_SITE_GATHER_OUT 13  /* stage-3 gather: layer buffer */
 #define ZERO_SITE_CHECKSUM 14    /* layer checksum: layer buffer */
 #define ZERO_SITE_COPY 15        /* zero_copy */
-#define ZERO_SITE_LINEAR_IN 16   /* products: x, dy, w read by plain loads */
+#define ZERO_SITE_LINEAR_IN 16   /* products: the forward bias */
 #define ZERO_SITE_LINEAR_OUT 17  /* products: epilogue operands and outputs */
 #define ZERO_SITE_DROPOUT 18     /* zero_dropout: x, residual, y */
 #define ZERO_SITE_LNORM 19       /* layer norm: x, dy, dres, y, dx, parameters */

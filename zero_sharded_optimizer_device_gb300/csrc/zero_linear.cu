@@ -21,9 +21,9 @@
 //                 memory, and a thread goes on with 8 consecutive columns by
 //                 plain loads and stores; for transposed outputs and rows off
 //                 16-byte boundaries
-//   warps 12-19   (gen) load operands whose base or rows lie off 16-byte
-//                 boundaries, which TMA cannot, with plain loads; warp 3 tells
-//                 the pair's first CTA of each tile they have filled
+//   warps 12-19   (gen) bring operands whose base or rows lie off 16-byte
+//                 boundaries, shifted into place; warp 3 tells the pair's
+//                 first CTA of each tile they have filled
 // Tiles are walked persistently with two sets of sums, so one tile's epilogue
 // runs under the next one's products.  Where there are too few tiles to fill
 // the GPU the contraction is split over the S pairs of a larger cluster, whose
@@ -42,7 +42,7 @@ constexpr int kBytesA = kRowsCta * kDeep * 2;
 constexpr int kEpiWarp0 = 4, kPatchWarps = 8, kBoxWarps = 16, kGenWarp0 = 12, kGenWarps = 8;
 constexpr int kPatch = 32 * 36;        // floats of a 32 x 32 patch, rows 36 apart
 constexpr int kMaxStages = 9;
-constexpr int kRaw = 2;                // raw buffers of the GEN warps
+constexpr int kMostRaw = 4;            // raw buffers of a GEN warp
 constexpr int kRound = 12;             // 64-deep steps of a round (see launch_mode)
 constexpr int kOnesBytes = 2048;
 constexpr int kSlot = 16384;           // a box of 128 rows of 128 bytes
@@ -55,7 +55,7 @@ static __device__ unsigned long long g_ops_timeouts;
 // Forms of the kernel: how operands come in and results go out.
 enum Form : int {
   PATCH = 0,      // operands by TMA, results over patches
-  PATCH_GEN = 1,  // an operand by plain loads, results over patches
+  PATCH_GEN = 1,  // an operand off 16-byte boundaries, results over patches
   BOX_BF16 = 2,   // operands by TMA, results in boxes of 64 bf16 columns
   BOX_F32 = 3     // operands by TMA, results in boxes of 32 fp32 columns
 };
@@ -76,7 +76,9 @@ struct TileK {
   int round;                         // steps whose sums the tensor cores keep (see launch_mode)
   int acc_sets;                      // sets of sums in tensor memory used in turn
   int i_fast;                        // consecutive tiles differ in i (else in j)
-  int gen_a, gen_b;                  // operand by plain loads (else TMA)
+  int gen_a, gen_b;                  // operand off 16-byte boundaries
+  int raws;                          // raw buffers of a GEN warp,
+  int raw_a, raw_b;                  // bytes for either operand in each
   int boxes;                         // ring of box chunks (box forms)
   int two_slots;                     // a chunk holds two slots
   uint32_t tmem_cols;
@@ -86,6 +88,18 @@ struct TileK {
 // Box forms: the side operands and outputs (see box_chunk).
 struct BoxMaps {
   CUtensorMap out, pre, gate, extra;  // extra: forward residual, dinput dgate
+};
+// PATCH_GEN: the operands' lines r, r + 8, ... for r = 0..7 (see gen_load).
+struct GenMaps {
+  CUtensorMap a[8], b[8];
+};
+template <int FORM>
+struct MapsOf {
+  using type = BoxMaps;
+};
+template <>
+struct MapsOf<PATCH_GEN> {
+  using type = GenMaps;
 };
 
 // ------------------------------------------------------------ PTX wrappers --
@@ -317,137 +331,73 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr, bool contig) {
 }
 
 // ---------------------------------------------------------------------------
-// Operands off 16-byte boundaries, by the GEN warps' 256 threads.  A line of a
-// tile (64 consecutive elements: a row's contraction, or 64 rows at one depth)
-// lies in nine aligned 16-byte words of memory, which asynchronous copies bring
-// to a raw buffer some steps ahead; each warp then shifts the 16 lines that it
-// fetched into the swizzled tile.  Nothing outside the matrix's memory is read:
-// a copy at its end is cut short, and a word that begins before its start is
-// gathered element by element.
-//
-// The loops are small and what can be is carried from step to step: these warps
-// run little else, and longer code waits for its instructions (3873 x 1614 by
-// 9592 x 1614, odd rows: unrolled 781 us, so 536; by loads into registers 877;
-// by 2-byte loads 2181).
+// Operands off 16-byte boundaries.  A line of a tile is 64 consecutive
+// elements: a row's contraction, or 64 rows at one depth.  Lines 8 apart are
+// 16 ld bytes apart, a multiple of 16 whatever ld is, so that the lines r, r +
+// 8, ... of a matrix, each begun at the 16-byte word it begins in, make a
+// matrix that TMA can read; all of them begin equally far into that word.
+// Eight such maps cover an operand, one per GEN warp, which brings nine words
+// of each of its lines to raw buffers of its own some steps ahead and writes
+// them, shifted by its one distance, to the operand's swizzled tile.  Lines and
+// elements outside the matrix arrive as zeros.  (3873 x 1614 by 9592 x 1614,
+// odd rows: 257 us; by 16-byte asynchronous copies, a line's words in one
+// thread, 536; by plain loads into registers 877; by 2-byte loads 2181.)
 // ---------------------------------------------------------------------------
 constexpr int kRawLine = 9 * 16;
-struct GenWhat {
-  const Mat* a;
-  bool contig;
-  int64_t rows, depth, i0;  // rows i0.. of the operand, contraction from kb * 64
-  int lines;                // of the tile; 16 per warp
-};
-// Thread t brings half of line t / 2: words 0-4 or 5-8.
-struct GenIssue {
-  const char *base, *end, *p;  // the matrix's memory; this line of the next step
-  int64_t step;                // bytes to its next
-  int64_t left;                // steps' depth before the line leaves the matrix
-  int by;                      // what a step takes off it
-};
-__device__ __forceinline__ void gen_enter(const GenWhat& b, int t, int kb, GenIssue& g) {
-  const int line = t >> 1;
-  const int64_t ld = b.a->ld, c0 = (int64_t)kb * kDeep;
-  g.base = static_cast<const char*>(b.a->p);
-  g.end = g.base +
-          2 * (b.contig ? (b.rows - 1) * ld + b.depth : (b.depth - 1) * ld + b.rows);
-  int64_t at;
-  if (b.contig) {
-    const int64_t i = b.i0 + line;
-    at = i * ld + c0;
-    g.step = 2 * kDeep;
-    g.left = i < b.rows ? 1 : 0;
-    g.by = 0;
+// Lines r + 8 j of an operand: those of rows i0.. (contiguous contraction) or
+// of depths c.. and blocks of 64 rows from i0 on.  r is in the map.
+__device__ __forceinline__ void gen_load(const CUtensorMap* map, bool contig, bool any, int i0,
+                                         int c, int lines, uint32_t raw, uint32_t bar) {
+  const int none = 1 << 30;  // a coordinate past every matrix: zeros
+  if (contig) {
+    box_load(map, raw, c, any ? i0 >> 3 : none, bar);
   } else {
-    const int64_t c = c0 + (line & 63), i = b.i0 + (line & ~63);  // 64 lines per 64 rows
-    at = c * ld + i;
-    g.step = 2 * kDeep * ld;
-    g.left = i < b.rows ? b.depth - c : 0;
-    g.by = kDeep;
+    for (int l = 0; l < lines; l += 8, i0 += 64, raw += 8 * kRawLine)
+      box_load(map, raw, i0, any ? c >> 3 : none, bar);
   }
-  if (line >= b.lines) g.left = 0;
-  g.p = g.base + 2 * at;
 }
-__device__ __noinline__ void gen_first_word(const char* word, const char* base, const char* end,
-                                            uint32_t to) {
-  uint32_t x[4] = {0, 0, 0, 0};
-  for (int e = 0; e < 8; ++e)
-    if (word + 2 * e >= base && word + 2 * e < end)
-      x[e / 2] |= (uint32_t)*reinterpret_cast<const uint16_t*>(word + 2 * e) << (16 * (e & 1));
-  sts16(to, make_uint4(x[0], x[1], x[2], x[3]));
-}
-__device__ __forceinline__ void gen_issue(GenIssue& g, int t, uint32_t raw) {
-  const int w0 = (t & 1) * 5, words = 5 - (t & 1);
-  const int64_t at = (g.p - g.base) / 2;
-  const bool on = g.left > 0 &&
-                  in_extent(at, at + 1, 0, (g.end - g.base) / 2, ZERO_SITE_LINEAR_IN);
-  const char* word = g.p - ((uintptr_t)g.p & 15) + 16 * w0;
-  uint32_t to = raw + (uint32_t)((t >> 1) * kRawLine + 16 * w0);
+// `lines` lines from the raw buffer to line r, r + 8, ... of the tile: a lane
+// has unit lane % 8 (8 elements) of every fourth.  The result begins `bits`
+// into word FIRST of a unit's eight.
+template <int FIRST>
+__device__ __forceinline__ void gen_shift(uint32_t raw, uint32_t tile, int lines, int r,
+                                          uint32_t bits, int lane) {
+  const int unit = lane & 7;
+  uint32_t from = raw + (uint32_t)((lane >> 3) * kRawLine + unit * 16);
+  uint32_t to = tile + (uint32_t)((lane >> 3) * 1024 + r * 128 + ((unit ^ r) << 4));
 #pragma unroll 1
-  for (int j = 0; j < words; ++j, word += 16, to += 16) {
-    if (on && word < g.base) {
-      gen_first_word(word, g.base, g.end, to);
-      continue;
+  for (int l = lane >> 3; l < lines; l += 8, from += 8 * kRawLine, to += 8192) {
+    const bool two = l + 4 < lines;
+    uint4 a = lds16(from), b = lds16(from + 16), c = a, d = b;
+    if (two) {
+      c = lds16(from + 4 * kRawLine);
+      d = lds16(from + 4 * kRawLine + 16);
     }
-    const int64_t rest = on ? g.end - word : 0;
-    const uint32_t n = rest <= 0 ? 0u : rest < 16 ? (uint32_t)rest : 16u;
-    // nothing is read where n is 0 (any aligned address of the matrix will do)
-    const char* from = n ? word : g.base + (-(uintptr_t)g.base & 15);
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(n)
-                 : "memory");
-  }
-  g.p += g.step;
-  g.left -= g.by;
-}
-// The warp's 16 lines from the raw buffer to the tile: a thread has unit t % 8
-// (8 elements) of four lines, four apart.
-struct GenShift {
-  uint32_t shifts;  // a byte per line: where it begins in its first word
-  int64_t left;     // elements of the unit inside the matrix, 8 or more: all
-  int by;           // what a step takes off it
-};
-__device__ __forceinline__ void gen_enter(const GenWhat& b, int t, int kb, GenShift& g) {
-  const int unit = t & 7, first = (t >> 5) * 16 + ((t & 31) >> 3);
-  const uint32_t base = (uint32_t)(uintptr_t)b.a->p, ld = (uint32_t)b.a->ld;
-  g.shifts = 0;
-  for (int q = 0; q < 4; ++q) {
-    const int line = first + 4 * q;
-    const uint32_t at =
-        b.contig ? (uint32_t)(b.i0 + line) * ld
-                 : (uint32_t)(line & 63) * ld + (uint32_t)(b.i0 + (line & ~63));
-    g.shifts |= ((base + 2 * at) & 15) << (8 * q);  // a step is a multiple of 16 bytes
-  }
-  g.left = b.contig ? b.depth - (int64_t)kb * kDeep - unit * 8
-                    : b.rows - b.i0 - (first & ~63) - unit * 8;
-  g.by = b.contig ? kDeep : 0;
-}
-__device__ __forceinline__ void gen_shift(GenShift& g, int t, uint32_t raw, uint32_t tile) {
-  const int unit = t & 7, first = (t >> 5) * 16 + ((t & 31) >> 3), row = first & 63;
-  uint32_t from = raw + (uint32_t)(first * kRawLine + unit * 16);
-  // 64 lines are 8192 bytes in either kind of tile; four lines on, the swizzle
-  // flips the unit's highest bit
-  uint32_t to = tile + (uint32_t)((first >> 6) * 8192 + row * 128 + ((unit ^ (row & 7)) << 4));
-  uint32_t shifts = g.shifts;
-#pragma unroll 1
-  for (int q = 0; q < 4; ++q, from += 4 * kRawLine, to = (to ^ 64) + 512, shifts >>= 8) {
-    const uint4 lo = lds16(from), hi = lds16(from + 16);
-    uint32_t x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    const uint32_t x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    const uint32_t y[8] = {c.x, c.y, c.z, c.w, d.x, d.y, d.z, d.w};
+    uint32_t u[4], v[4];
 #pragma unroll
-    for (int i = 0; i < 6; ++i) x[i] = shifts & 8 ? x[i + 2] : x[i];
-#pragma unroll
-    for (int i = 0; i < 5; ++i) x[i] = shifts & 4 ? x[i + 1] : x[i];
-    const uint32_t bits = (shifts & 2) * 8;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = __funnelshift_r(x[i], x[i + 1], bits);
-    if (g.left < 8) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (2 * i >= g.left) x[i] = 0;
-        else if (2 * i + 1 >= g.left) x[i] &= 0xFFFF;
-      }
+    for (int i = 0; i < 4; ++i) {
+      u[i] = __funnelshift_r(x[FIRST + i], x[FIRST + i + 1], bits);
+      v[i] = __funnelshift_r(y[FIRST + i], y[FIRST + i + 1], bits);
     }
-    sts16(to, make_uint4(x[0], x[1], x[2], x[3]));
+    sts16(to, make_uint4(u[0], u[1], u[2], u[3]));
+    if (two) sts16(to + 4096, make_uint4(v[0], v[1], v[2], v[3]));
   }
-  g.left -= g.by;
+}
+__device__ __forceinline__ void gen_shift(uint32_t raw, uint32_t tile, int lines, int r,
+                                          uint32_t distance, int lane) {
+  const uint32_t bits = (distance & 2) * 8;
+  switch (distance >> 2) {
+    case 0: gen_shift<0>(raw, tile, lines, r, bits, lane); break;
+    case 1: gen_shift<1>(raw, tile, lines, r, bits, lane); break;
+    case 2: gen_shift<2>(raw, tile, lines, r, bits, lane); break;
+    default: gen_shift<3>(raw, tile, lines, r, bits, lane);
+  }
+}
+// How far into its 16-byte word line r begins.
+__device__ __forceinline__ uint32_t gen_distance(const Mat& a, int r) {
+  return ((uint32_t)(uintptr_t)a.p + 2 * (uint32_t)r * (uint32_t)a.ld) & 15;
 }
 
 // The tile of index t: its row and column, or the bias column (j < 0).
@@ -900,22 +850,32 @@ struct Column {
 };
 __device__ __forceinline__ bool column_in(const Mat& m, const Column& c, int i, const Extent& e) {
   const int64_t at = (c.row + i) * m.ld;
-  return i < c.count && in_extent(at + c.col, at + c.col + 1, at, at + e.cols,
-                                  ZERO_SITE_LINEAR_OUT) &&
+  return in_extent(at + c.col, at + c.col + 1, at, at + e.cols, ZERO_SITE_LINEAR_OUT) &&
          in_extent(c.row + i, c.row + i + 1, 0, e.rows, ZERO_SITE_LINEAR_OUT);
+}
+// Past its rows a lane reads the last one again: loads without a condition
+// each are all in flight together (7615 x 80 by 4624 with SiLU, a gate and its
+// input kept, odd rows: 213 us, 289 with conditions).
+template <typename T>
+__device__ __forceinline__ void column_words(const T* p, const Mat& m, const Column& c,
+                                             const Extent& e, T u[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    u[i] = column_in(m, c, i < c.count ? i : c.count - 1, e) ? *p : T(0);
+    p += i + 1 < c.count ? m.ld : 0;
+  }
 }
 __device__ __forceinline__ void column_load(const Mat& m, const Column& c, const Extent& e,
                                             float f[32]) {
+  if (c.count <= 0) return;
   const int64_t at = c.row * m.ld + c.col;
   if (m.dtype == ZERO_F32) {
-    const float* p = static_cast<const float*>(m.p) + at;
-#pragma unroll
-    for (int i = 0; i < 32; ++i, p += m.ld) f[i] = column_in(m, c, i, e) ? *p : 0.0f;
+    column_words(static_cast<const float*>(m.p) + at, m, c, e, f);
   } else {
-    const uint16_t* p = static_cast<const uint16_t*>(m.p) + at;
+    uint16_t u[32];
+    column_words(static_cast<const uint16_t*>(m.p) + at, m, c, e, u);
 #pragma unroll
-    for (int i = 0; i < 32; ++i, p += m.ld)
-      f[i] = column_in(m, c, i, e) ? __uint_as_float((uint32_t)*p << 16) : 0.0f;
+    for (int i = 0; i < 32; ++i) f[i] = __uint_as_float((uint32_t)u[i] << 16);
   }
 }
 __device__ __forceinline__ void column_store(const Mat& m, const Column& c, const Extent& e,
@@ -925,12 +885,12 @@ __device__ __forceinline__ void column_store(const Mat& m, const Column& c, cons
     float* p = static_cast<float*>(m.p) + at;
 #pragma unroll
     for (int i = 0; i < 32; ++i, p += m.ld)
-      if (column_in(m, c, i, e)) *p = f[i];
+      if (i < c.count && column_in(m, c, i, e)) *p = f[i];
   } else {
     uint16_t* p = static_cast<uint16_t*>(m.p) + at;
 #pragma unroll
     for (int i = 0; i < 32; ++i, p += m.ld)
-      if (column_in(m, c, i, e)) *p = to_bf16(f[i]);
+      if (i < c.count && column_in(m, c, i, e)) *p = to_bf16(f[i]);
   }
 }
 
@@ -1067,7 +1027,8 @@ template <int MODE, int FORM>
 __global__ void __launch_bounds__(threads_of(FORM), 1)
     product_kernel(const __grid_constant__ CUtensorMap map_a,
                    const __grid_constant__ CUtensorMap map_b,
-                   const __grid_constant__ BoxMaps maps, const __grid_constant__ ProductK k,
+                   const __grid_constant__ typename MapsOf<FORM>::type maps,
+                   const __grid_constant__ ProductK k,
                    const __grid_constant__ TileK g) {
   constexpr bool GEN = FORM == PATCH_GEN, BOX = FORM == BOX_BF16 || FORM == BOX_F32;
   constexpr int kWidth = FORM == BOX_F32 ? 32 : 64;  // columns of a chunk
@@ -1079,6 +1040,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
   constexpr int kPiece = BOX ? 16 : 32, kSets = kEpiWarps / 4;
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ __align__(8) uint64_t bars[3 * kMaxStages + 5 + 2 * kMostBoxes];
+  __shared__ __align__(8) uint64_t raw_bars[GEN ? kGenWarps * kMostRaw : 1];
   __shared__ uint32_t tmem_at;
   __shared__ int dead;
   const uint32_t rank = cluster_rank(), half = rank & 1, leader = rank & ~1u;
@@ -1102,6 +1064,8 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
       if (GEN) bar_init(filled + 8 * s, kGenWarps);
       bar_init(empty + 8 * s, 1);
     }
+    if (GEN)
+      for (int q = 0; q < kGenWarps * kMostRaw; ++q) bar_init(smem_u32(raw_bars + q), 1);
     for (int a = 0; a < 2; ++a) {
       bar_init(tfull + 8 * a, 1);
       bar_init(tempty + 8 * a, 2 * kEpiWarps);
@@ -1127,12 +1091,12 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
   // the next kernel on the stream may set up while this one runs
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp == 1 && elect()) {
-    // (an operand that comes by plain loads, or is empty, has no map)
+    // (an operand off 16-byte boundaries, or an empty one, has no such map)
     if (!g.gen_a && g.kblocks > 0 && k.rows > 0)
       asm volatile("prefetch.tensormap [%0];" ::"l"(&map_a) : "memory");
     if (!g.gen_b && g.kblocks > 0 && k.cols > 0)
       asm volatile("prefetch.tensormap [%0];" ::"l"(&map_b) : "memory");
-    if (BOX) asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.out) : "memory");
+    if constexpr (BOX) asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.out) : "memory");
   }
   if (warp == 2) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -1293,7 +1257,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
       cluster_arrive();
       cluster_wait();
     }
-    box_traffic<MODE, FORM>(maps, k, g, patches, efull, edone, first, tiles, clusters, half,
+    if constexpr (BOX) box_traffic<MODE, FORM>(maps, k, g, patches, efull, edone, first, tiles, clusters, half,
                             split, &dead);
     __syncwarp();
   } else if (warp >= kEpiWarp0 && warp < kEpiWarp0 + kEpiWarps) {
@@ -1327,7 +1291,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
           const int64_t c =
               (out_t ? i0 : (int64_t)tj * bn + (kSets * q + set) * kPiece) + lane;
           const bool in = c < e.cols && lane < kPiece &&
-                          in_extent(c, c + 1, 0, e.cols, ZERO_SITE_LINEAR_OUT);
+                          in_extent(c, c + 1, 0, e.cols, ZERO_SITE_LINEAR_IN);
           const float b = in ? load1(k.epi.bias, c) : 0.0f;
           if (lane < kPiece)
             asm volatile("st.shared.f32 [%0], %1;" ::"r"(biases + (uint32_t)(q * kPiece + lane) * 4),
@@ -1498,85 +1462,97 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
       }
     }
   } else if (GEN && warp >= kGenWarp0) {
-    const int t256 = threadIdx.x - kGenWarp0 * 32;
-    const int bn = g.bn, stages = g.stages;
+   if constexpr (GEN) {
+    const int r = warp - kGenWarp0, bn = g.bn, stages = g.stages, raws = g.raws;
+    const bool gen_a = g.gen_a, gen_b = g.gen_b, bias_b = g.bias_b;
+    const int lines_a = kRowsCta / 8, lines_b = bn / 16;
+    const bool any_a = (a_c ? k.rows : k.depth) > r, any_b = (b_c ? k.cols : k.depth) > r;
+    const uint32_t by_a = gen_distance(k.a, r), by_b = gen_distance(k.b, r);
+    const uint32_t raw0 = bias_smem + g.bias_in + (uint32_t)r * (g.raw_a + g.raw_b),
+                   raw_step = (uint32_t)kGenWarps * (g.raw_a + g.raw_b);
+    const uint32_t landed = smem_u32(raw_bars + r * kMostRaw);
     struct Step {
       int t, ti, tj, kb;
-      bool a, b;  // which operands' tiles this warp has lines of
     };
-    auto has_a = [&](const Step& c) { return (c.tj < 0 && g.bias_b ? g.gen_b : g.gen_a) != 0; };
-    auto has_b = [&](const Step& c) { return c.tj >= 0 && g.gen_b; };
-    auto of_a = [&](const Step& c) {  // for a tile of B's bias sums, B in A's place
-      const bool b = c.tj < 0 && g.bias_b;
-      return GenWhat{b ? &k.b : &k.a, b ? b_c : a_c, b ? k.cols : k.rows, k.depth,
-                     (int64_t)c.ti * 256 + half * kRowsCta, kRowsCta};
-    };
-    auto of_b = [&](const Step& c) {
-      return GenWhat{&k.b, b_c, k.cols, k.depth, (int64_t)c.tj * bn + half * (bn / 2), bn / 2};
-    };
-    auto enter = [&](Step& c, auto& a, auto& b) {
-      if (c.t >= tiles) return;
-      tile_at(g, c.t, c.ti, c.tj);
+    auto enter = [&](Step& c) {
+      if (c.t < tiles) tile_at(g, c.t, c.ti, c.tj);
       c.kb = kb0;
-      c.a = has_a(c);
-      c.b = has_b(c) && (t256 >> 5) * 16 < bn / 2;
-      if (c.a) gen_enter(of_a(c), t256, kb0, a);
-      if (c.b) gen_enter(of_b(c), t256, kb0, b);
     };
-    const uint32_t raw0 = bias_smem + g.bias_in, raw_step = (kRowsCta + bn / 2) * kRawLine;
-    Step ahead{first, 0, 0, kb0, false, false}, now = ahead;
-    GenIssue ia, ib;
-    GenShift sa, sb;
-    uint32_t rb = 0, wb = 0;  // raw buffers: shifted next, filled next
-    auto issue = [&]() {      // one group of copies per step, empty past the last
-      if (ahead.t < tiles) {
-        const uint32_t raw = raw0 + wb * raw_step;
-        if (ahead.a) gen_issue(ia, t256, raw);
-        if (ahead.b) gen_issue(ib, t256, raw + kRowsCta * kRawLine);
-        if (++wb == kRaw) wb = 0;
-        if (++ahead.kb >= kb1) {
-          ahead.t += clusters;
-          enter(ahead, ia, ib);
-        }
+    auto next = [&](Step& c) {
+      if (++c.kb < kb1) return;
+      c.t += clusters;
+      enter(c);
+    };
+    // for a tile of B's bias sums, B is in A's place
+    auto swapped = [&](const Step& c) { return c.tj < 0 && bias_b; };
+    Step ahead{first, 0, 0, kb0}, now = ahead;
+    int flying = 0;  // buffers filled, or being filled, ahead of their use
+    uint32_t wb = 0, rb = 0, rph = 0;  // buffers: filled next, used next
+    auto issue = [&]() {
+      if (ahead.t >= tiles) return;
+      const bool swap = swapped(ahead), a = swap ? gen_b : gen_a, b = ahead.tj >= 0 && gen_b;
+      if (elect()) {
+        const uint32_t raw = raw0 + wb * raw_step, bar = landed + 8 * wb;
+        const int c = ahead.kb * kDeep;
+        bar_expect(bar, (uint32_t)((a ? lines_a : 0) + (b ? lines_b : 0)) * kRawLine);
+        if (a)
+          gen_load(swap ? &maps.b[r] : &maps.a[r], swap ? b_c : a_c, swap ? any_b : any_a,
+                   ahead.ti * 256 + (int)half * kRowsCta, c, lines_a, raw, bar);
+        if (b)
+          gen_load(&maps.b[r], b_c, any_b, ahead.tj * bn + (int)half * (bn / 2), c, lines_b,
+                   raw + g.raw_a, bar);
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
+      __syncwarp();
+      ++flying;
+      if (++wb == (uint32_t)raws) wb = 0;
+      next(ahead);
     };
     uint32_t s = 0, ph = 0;
     bool ok = kb0 < kb1;
     if (ok) {
-      enter(ahead, ia, ib);
-      enter(now, sa, sb);
-#pragma unroll 1
-      for (int q = 0; q < kRaw - 1; ++q) issue();
+      enter(ahead);
+      enter(now);
+      for (int q = 0; q < raws; ++q) issue();
     }
     while (ok && now.t < tiles) {
-      issue();
-      ok = bar_wait(empty + 8 * s, ph ^ 1, &dead);
+      ok = bar_wait(landed + 8 * rb, rph, &dead) && bar_wait(empty + 8 * s, ph ^ 1, &dead);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      asm volatile("cp.async.wait_group %0;" ::"n"(kRaw - 1) : "memory");
-      __syncwarp();
+      const bool swap = swapped(now);
       const uint32_t a_at = ring + s * stage_bytes, raw = raw0 + rb * raw_step;
-      if (now.a) gen_shift(sa, t256, raw, a_at);
-      if (now.b) gen_shift(sb, t256, raw + kRowsCta * kRawLine, a_at + kBytesA);
+      if (swap ? gen_b : gen_a) gen_shift(raw, a_at, lines_a, r, swap ? by_b : by_a, lane);
+      if (now.tj >= 0 && gen_b)
+        gen_shift(raw + g.raw_a, a_at + kBytesA, lines_b, r, by_b, lane);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();  // the raw lines are read, the tile's are written
       if (lane == 0) bar_arrive(filled + 8 * s);
+      --flying;
       if (++s == (uint32_t)stages) {
         s = 0;
         ph ^= 1;
       }
-      if (++rb == kRaw) rb = 0;
-      if (++now.kb >= kb1) {
-        now.t += clusters;
-        enter(now, sa, sb);
+      if (++rb == (uint32_t)raws) {
+        rb = 0;
+        rph ^= 1;
+      }
+      next(now);
+      issue();
+    }
+    // after a wait that gave up: what is in flight lands before the CTA returns
+    for (; flying > 0; --flying) {
+      const long long t0 = clock64();
+      while (!bar_try(landed + 8 * rb, rph) && clock64() - t0 < kWaitCycles / 8) {
+      }
+      if (++rb == (uint32_t)raws) {
+        rb = 0;
+        rph ^= 1;
       }
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
+   }
   } else if (GEN && warp == 3) {
     // The arrival at the pair's first CTA releases to the cluster, which waits
-    // for every access of the thread before it: on a warp of its own it does
-    // not wait for copies in flight (1300 cycles a step).
+    // for every access of the thread before it: on a warp of its own there are
+    // none.
     const uint32_t full_lead = remote(full, leader);
     uint32_t s = 0, ph = 0;
     bool live = true;
@@ -1630,9 +1606,9 @@ static EncodeFn encode_fn() {
   return reinterpret_cast<EncodeFn>(f);
 }
 
-// Whether an operand has to come by plain loads: its base or its rows (where
-// there are several) lie off 16-byte boundaries.
-static bool by_loads(const Mat& a, int64_t lines) {
+// Whether an operand lies off 16-byte boundaries: its base or its rows (where
+// there are several).
+static bool off_words(const Mat& a, int64_t lines) {
   return ((uintptr_t)a.p & 15) != 0 || (lines > 1 && a.ld % 8 != 0);
 }
 
@@ -1661,6 +1637,21 @@ static bool operand_map(CUtensorMap* map, const Mat& a, bool contig, int64_t row
                          CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// The eight maps of such an operand: lines r, r + 8, ... of `lines` lines of
+// `inner` elements, each from the 16-byte word it begins in (which for the
+// first may begin before the matrix; what lies there is shifted out).
+static bool gen_maps(CUtensorMap map[8], const Mat& a, int64_t lines, int64_t inner, int box_y) {
+  for (int r = 0; r < 8; ++r) {
+    const int64_t at = r < lines ? r : 0;  // (no such line: any map will do)
+    char* p = static_cast<char*>(a.p) + 2 * at * a.ld;
+    const int into = (int)((uintptr_t)p & 15);
+    if (!encode(&map[r], false, p - into, inner + into / 2, (lines - at + 7) / 8, 8 * a.ld,
+                kRawLine / 2, box_y, CU_TENSOR_MAP_SWIZZLE_NONE))
+      return false;
+  }
+  return true;
+}
+
 // A side operand's or output's boxes of `width` columns x 128 rows.
 static bool box_map(CUtensorMap* map, const Mat& a, int64_t rows, int64_t cols, int width) {
   if (!a.p) return true;
@@ -1673,8 +1664,8 @@ static bool box_map(CUtensorMap* map, const Mat& a, int64_t rows, int64_t cols, 
 // Shared memory beside the operand ring, and the ring's stages in what is left.
 static int side_bytes(const TileK& g, int form) {
   return (g.bias_tiles || g.bias_fused ? kOnesBytes : 0) + g.bias_in +
-         (form == PATCH_GEN ? kRaw * (kRowsCta + g.bn / 2) * kRawLine : 0) + (form >= BOX_BF16 ? g.boxes * kSlot * (g.two_slots ? 2 : 1)
-                           : kPatchWarps * kPatch * 4);
+         (form == PATCH_GEN ? g.raws * kGenWarps * (g.raw_a + g.raw_b) : 0) +
+         (form >= BOX_BF16 ? g.boxes * kSlot * (g.two_slots ? 2 : 1) : kPatchWarps * kPatch * 4);
 }
 static int stages_for(const TileK& g, int form) {
   const int n = (kSmemMost - 1024 - side_bytes(g, form)) / (kBytesA + g.bn * kDeep);
@@ -1683,7 +1674,8 @@ static int stages_for(const TileK& g, int form) {
 
 template <int MODE, int FORM>
 static cudaError_t launch_tiles(const CUtensorMap& ma, const CUtensorMap& mb,
-                                const BoxMaps& maps, const ProductK& k, TileK& g,
+                                const typename MapsOf<FORM>::type& maps, const ProductK& k,
+                                TileK& g,
                                 cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
   int dev = 0;
@@ -1811,8 +1803,8 @@ static cudaError_t launch_mode(const ProductK& in, cudaStream_t st) {
   CUtensorMap ma{}, mb{};
   BoxMaps maps{};
   if (k.depth > 0) {
-    g.gen_a = k.rows > 0 ? by_loads(k.a, k.a_c ? k.rows : k.depth) : 0;
-    g.gen_b = k.cols > 0 ? by_loads(k.b, k.b_c ? k.cols : k.depth) : 0;
+    g.gen_a = k.rows > 0 ? off_words(k.a, k.a_c ? k.rows : k.depth) : 0;
+    g.gen_b = k.cols > 0 ? off_words(k.b, k.b_c ? k.cols : k.depth) : 0;
     if (!g.gen_a && k.rows > 0 &&
         !operand_map(&ma, k.a, k.a_c, k.rows, k.depth, kRowsCta))
       return cudaErrorInvalidValue;
@@ -1820,7 +1812,21 @@ static cudaError_t launch_mode(const ProductK& in, cudaStream_t st) {
         !operand_map(&mb, k.b, k.b_c, k.cols, k.depth, g.bn / 2))
       return cudaErrorInvalidValue;
   }
-  if (g.gen_a || g.gen_b) return launch_tiles<MODE, PATCH_GEN>(ma, mb, maps, k, g, st);
+  if (g.gen_a || g.gen_b) {
+    GenMaps gen{};
+    if (g.gen_a && !gen_maps(gen.a, k.a, k.a_c ? k.rows : k.depth, k.a_c ? k.depth : k.rows,
+                             k.a_c ? kRowsCta / 8 : 8))
+      return cudaErrorInvalidValue;
+    if (g.gen_b && !gen_maps(gen.b, k.b, k.b_c ? k.cols : k.depth, k.b_c ? k.depth : k.cols,
+                             k.b_c ? g.bn / 16 : 8))
+      return cudaErrorInvalidValue;
+    // (TMA writes to 128-byte boundaries)
+    g.raw_a = g.gen_a || (g.bias_tiles && g.bias_b) ? kRowsCta / 8 * kRawLine : 0;
+    g.raw_b = g.gen_b ? (g.bn / 16 * kRawLine + 127) / 128 * 128 : 0;
+    for (g.raws = kMostRaw; g.raws > 2 && stages_for(g, PATCH_GEN) < 4; --g.raws) {
+    }
+    return launch_tiles<MODE, PATCH_GEN>(ma, mb, gen, k, g, st);
+  }
   const EpiK& o = k.epi;
   const bool pre_ok = MODE == LIN_FORWARD ? box_output(o.pre, k.rows, k.cols)
                                           : boxable(o.pre, k.rows);
