@@ -21,9 +21,9 @@
 //                 memory, and a thread goes on with 8 consecutive columns by
 //                 plain loads and stores; for transposed outputs and rows off
 //                 16-byte boundaries
-//   warps 12-19   (gen) bring operands whose base or rows lie off 16-byte
-//                 boundaries, shifted into place; warp 3 tells the pair's
-//                 first CTA of each tile they have filled
+//   warps 12-19   (gen) shift operands whose base or rows lie off 16-byte
+//                 boundaries into place; warps 2 (A's) and 3 (B's) bring
+//                 them to raw buffers
 // Tiles are walked persistently with two sets of sums, so one tile's epilogue
 // runs under the next one's products.  Where there are too few tiles to fill
 // the GPU the contraction is split over the S pairs of a larger cluster, whose
@@ -42,7 +42,7 @@ constexpr int kBytesA = kRowsCta * kDeep * 2;
 constexpr int kEpiWarp0 = 4, kPatchWarps = 8, kBoxWarps = 16, kGenWarp0 = 12, kGenWarps = 8;
 constexpr int kPatch = 32 * 36;        // floats of a 32 x 32 patch, rows 36 apart
 constexpr int kMaxStages = 9;
-constexpr int kMostRaw = 4;            // raw buffers of a GEN warp
+constexpr int kMostRaw = 4;            // raw buffers
 constexpr int kRound = 12;             // 64-deep steps of a round (see launch_mode)
 constexpr int kOnesBytes = 2048;
 constexpr int kSlot = 16384;           // a box of 128 rows of 128 bytes
@@ -77,8 +77,8 @@ struct TileK {
   int acc_sets;                      // sets of sums in tensor memory used in turn
   int i_fast;                        // consecutive tiles differ in i (else in j)
   int gen_a, gen_b;                  // operand off 16-byte boundaries
-  int raws;                          // raw buffers of a GEN warp,
-  int raw_a, raw_b;                  // bytes for either operand in each
+  int raws;                          // raw buffers: a GEN warp's bytes
+  int raw_a, raw_b;                  // of either operand in each
   int boxes;                         // ring of box chunks (box forms)
   int two_slots;                     // a chunk holds two slots
   uint32_t tmem_cols;
@@ -173,14 +173,9 @@ __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                : "memory");
 }
-// One arrival on a barrier of any CTA of the cluster; `release`: what this
-// thread wrote by plain stores is visible there first.
+// One arrival on a barrier of any CTA of the cluster.
 __device__ __forceinline__ void bar_arrive_cluster(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
-}
-__device__ __forceinline__ void bar_arrive_cluster_release(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
-               : "memory");
 }
 // A box of a matrix into this CTA's shared memory, counted on the barrier of
 // the pair's first CTA.  x is a multiple of 64 elements.
@@ -336,63 +331,63 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr, bool contig) {
 // 16 ld bytes apart, a multiple of 16 whatever ld is, so that the lines r, r +
 // 8, ... of a matrix, each begun at the 16-byte word it begins in, make a
 // matrix that TMA can read; all of them begin equally far into that word.
-// Eight such maps cover an operand, one per GEN warp, which brings nine words
-// of each of its lines to raw buffers of its own some steps ahead and writes
-// them, shifted by its one distance, to the operand's swizzled tile.  Lines and
-// elements outside the matrix arrive as zeros.  (3873 x 1614 by 9592 x 1614,
-// odd rows: 257 us; by 16-byte asynchronous copies, a line's words in one
+// Eight such maps cover an operand.  A warp brings nine words of each line of a
+// tile to a raw buffer some steps ahead; a GEN warp writes the lines of one
+// map, shifted by their one distance, to the operand's swizzled tile.  Lines
+// and elements outside the matrix arrive as zeros.  (3873 x 1614 by 9592 x 1614,
+// odd rows: 194 us; by 16-byte asynchronous copies, a line's words in one
 // thread, 536; by plain loads into registers 877; by 2-byte loads 2181.)
 // ---------------------------------------------------------------------------
 constexpr int kRawLine = 9 * 16;
-// Lines r + 8 j of an operand: those of rows i0.. (contiguous contraction) or
-// of depths c.. and blocks of 64 rows from i0 on.  r is in the map.
-__device__ __forceinline__ void gen_load(const CUtensorMap* map, bool contig, bool any, int i0,
-                                         int c, int lines, uint32_t raw, uint32_t bar) {
-  const int none = 1 << 30;  // a coordinate past every matrix: zeros
-  if (contig) {
-    box_load(map, raw, c, any ? i0 >> 3 : none, bar);
-  } else {
-    for (int l = 0; l < lines; l += 8, i0 += 64, raw += 8 * kRawLine)
-      box_load(map, raw, i0, any ? c >> 3 : none, bar);
+// A tile's lines by one thread: those of rows i0.. (contiguous contraction), or
+// of depths c.. and blocks of 64 rows from i0 on; `all` lines exist.
+__device__ __forceinline__ void gen_load(const CUtensorMap* maps, bool contig, int64_t all, int i0,
+                                         int c, int lines, uint32_t raw, uint32_t raw_warp,
+                                         uint32_t bar) {
+  constexpr int kNone = 1 << 30;  // a coordinate past every matrix: zeros
+  const int x = contig ? c : i0, y = contig ? i0 >> 3 : c >> 3;
+  const bool two = !contig && lines > 8;
+#pragma unroll
+  for (int r = 0; r < kGenWarps; ++r, raw += raw_warp) {
+    const int at = all > r ? y : kNone;
+    box_load(maps + r, raw, x, at, bar);
+    if (two) box_load(maps + r, raw + 8 * kRawLine, x + 64, at, bar);
   }
 }
 // `lines` lines from the raw buffer to line r, r + 8, ... of the tile: a lane
-// has unit lane % 8 (8 elements) of every fourth.  The result begins `bits`
-// into word FIRST of a unit's eight.
-template <int FIRST>
-__device__ __forceinline__ void gen_shift(uint32_t raw, uint32_t tile, int lines, int r,
-                                          uint32_t bits, int lane) {
-  const int unit = lane & 7;
-  uint32_t from = raw + (uint32_t)((lane >> 3) * kRawLine + unit * 16);
-  uint32_t to = tile + (uint32_t)((lane >> 3) * 1024 + r * 128 + ((unit ^ r) << 4));
-#pragma unroll 1
-  for (int l = lane >> 3; l < lines; l += 8, from += 8 * kRawLine, to += 8192) {
-    const bool two = l + 4 < lines;
-    uint4 a = lds16(from), b = lds16(from + 16), c = a, d = b;
-    if (two) {
-      c = lds16(from + 4 * kRawLine);
-      d = lds16(from + 4 * kRawLine + 16);
-    }
-    const uint32_t x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    const uint32_t y[8] = {c.x, c.y, c.z, c.w, d.x, d.y, d.z, d.w};
-    uint32_t u[4], v[4];
+// has unit lane % 8 (8 elements) of every fourth, N of them at a time.  The
+// result begins `bits` into word FIRST of a unit's eight.
+template <int FIRST, int N>
+__device__ __forceinline__ void gen_units(uint32_t from, uint32_t to, int lines, uint32_t bits) {
+  uint4 a[N], b[N];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      u[i] = __funnelshift_r(x[FIRST + i], x[FIRST + i + 1], bits);
-      v[i] = __funnelshift_r(y[FIRST + i], y[FIRST + i + 1], bits);
+  for (int q = 0; q < N; ++q) {
+    a[q] = b[q] = make_uint4(0, 0, 0, 0);
+    if (4 * q < lines) {
+      a[q] = lds16(from + 4 * q * kRawLine);
+      b[q] = lds16(from + 4 * q * kRawLine + 16);
     }
-    sts16(to, make_uint4(u[0], u[1], u[2], u[3]));
-    if (two) sts16(to + 4096, make_uint4(v[0], v[1], v[2], v[3]));
+  }
+#pragma unroll
+  for (int q = 0; q < N; ++q) {
+    const uint32_t x[8] = {a[q].x, a[q].y, a[q].z, a[q].w, b[q].x, b[q].y, b[q].z, b[q].w};
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = __funnelshift_r(x[FIRST + i], x[FIRST + i + 1], bits);
+    if (4 * q < lines) sts16(to + 4096 * q, make_uint4(u[0], u[1], u[2], u[3]));
   }
 }
 __device__ __forceinline__ void gen_shift(uint32_t raw, uint32_t tile, int lines, int r,
                                           uint32_t distance, int lane) {
+  const int unit = lane & 7, line = lane >> 3;
+  const uint32_t from = raw + (uint32_t)(line * kRawLine + unit * 16);
+  const uint32_t to = tile + (uint32_t)(line * 1024 + r * 128 + ((unit ^ r) << 4));
   const uint32_t bits = (distance & 2) * 8;
   switch (distance >> 2) {
-    case 0: gen_shift<0>(raw, tile, lines, r, bits, lane); break;
-    case 1: gen_shift<1>(raw, tile, lines, r, bits, lane); break;
-    case 2: gen_shift<2>(raw, tile, lines, r, bits, lane); break;
-    default: gen_shift<3>(raw, tile, lines, r, bits, lane);
+    case 0: gen_units<0, 4>(from, to, lines - line, bits); break;
+    case 1: gen_units<1, 4>(from, to, lines - line, bits); break;
+    case 2: gen_units<2, 4>(from, to, lines - line, bits); break;
+    default: gen_units<3, 4>(from, to, lines - line, bits);
   }
 }
 // How far into its 16-byte word line r begins.
@@ -855,7 +850,8 @@ __device__ __forceinline__ bool column_in(const Mat& m, const Column& c, int i, 
 }
 // Past its rows a lane reads the last one again: loads without a condition
 // each are all in flight together (7615 x 80 by 4624 with SiLU, a gate and its
-// input kept, odd rows: 213 us, 289 with conditions).
+// input kept, odd rows: 209 us, 289 with conditions; eight
+// rows at a time in a loop, 372).
 template <typename T>
 __device__ __forceinline__ void column_words(const T* p, const Mat& m, const Column& c,
                                              const Extent& e, T u[32]) {
@@ -1039,8 +1035,8 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
   constexpr int kEpiWarps = BOX ? kBoxWarps : kPatchWarps;
   constexpr int kPiece = BOX ? 16 : 32, kSets = kEpiWarps / 4;
   extern __shared__ __align__(1024) unsigned char smem[];
-  __shared__ __align__(8) uint64_t bars[3 * kMaxStages + 5 + 2 * kMostBoxes];
-  __shared__ __align__(8) uint64_t raw_bars[GEN ? kGenWarps * kMostRaw : 1];
+  __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 5 + 2 * kMostBoxes];
+  __shared__ __align__(8) uint64_t raw_bars[GEN ? 2 * kMostRaw : 1];
   __shared__ uint32_t tmem_at;
   __shared__ int dead;
   const uint32_t rank = cluster_rank(), half = rank & 1, leader = rank & ~1u;
@@ -1055,17 +1051,19 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
   const uint32_t full = smem_u32(bars), empty = full + 8 * kMaxStages;
   const uint32_t tfull = empty + 8 * kMaxStages, tempty = tfull + 16, ready = tempty + 16;
   const uint32_t efull = ready + 8, edone = efull + 8 * kMostBoxes;
-  const uint32_t filled = edone + 8 * kMostBoxes;  // by the GEN warps
+  const uint32_t landed = smem_u32(raw_bars), used = landed + 8 * kMostRaw;  // raw buffers
 
   if (warp == 0 && elect()) {
     dead = 0;
     for (int s = 0; s < g.stages; ++s) {
-      bar_init(full + 8 * s, GEN ? 3 : 1);
-      if (GEN) bar_init(filled + 8 * s, kGenWarps);
+      bar_init(full + 8 * s, GEN ? 1 + 2 * kGenWarps : 1);
       bar_init(empty + 8 * s, 1);
     }
     if (GEN)
-      for (int q = 0; q < kGenWarps * kMostRaw; ++q) bar_init(smem_u32(raw_bars + q), 1);
+      for (int q = 0; q < g.raws; ++q) {
+        bar_init(landed + 8 * q, 2);
+        bar_init(used + 8 * q, kGenWarps);
+      }
     for (int a = 0; a < 2; ++a) {
       bar_init(tfull + 8 * a, 1);
       bar_init(tempty + 8 * a, 2 * kEpiWarps);
@@ -1217,7 +1215,6 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
           const int start = kb, end = r + 1 < rounds ? kb + round : kb1;
           for (; kb < end; ++kb) {
             live = live && bar_wait(full + 8 * s, ph, &dead);
-            if (GEN) asm volatile("fence.acq_rel.cluster;" ::: "memory");
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t a_at = ring + s * stage_bytes;
             const uint64_t da = operand_desc(a_at, a_c);
@@ -1462,110 +1459,90 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
       }
     }
   } else if (GEN && warp >= kGenWarp0) {
-   if constexpr (GEN) {
     const int r = warp - kGenWarp0, bn = g.bn, stages = g.stages, raws = g.raws;
     const bool gen_a = g.gen_a, gen_b = g.gen_b, bias_b = g.bias_b;
-    const int lines_a = kRowsCta / 8, lines_b = bn / 16;
-    const bool any_a = (a_c ? k.rows : k.depth) > r, any_b = (b_c ? k.cols : k.depth) > r;
-    const uint32_t by_a = gen_distance(k.a, r), by_b = gen_distance(k.b, r);
-    const uint32_t raw0 = bias_smem + g.bias_in + (uint32_t)r * (g.raw_a + g.raw_b),
-                   raw_step = (uint32_t)kGenWarps * (g.raw_a + g.raw_b);
-    const uint32_t landed = smem_u32(raw_bars + r * kMostRaw);
-    struct Step {
-      int t, ti, tj, kb;
-    };
-    auto enter = [&](Step& c) {
-      if (c.t < tiles) tile_at(g, c.t, c.ti, c.tj);
-      c.kb = kb0;
-    };
-    auto next = [&](Step& c) {
-      if (++c.kb < kb1) return;
-      c.t += clusters;
-      enter(c);
-    };
-    // for a tile of B's bias sums, B is in A's place
-    auto swapped = [&](const Step& c) { return c.tj < 0 && bias_b; };
-    Step ahead{first, 0, 0, kb0}, now = ahead;
-    int flying = 0;  // buffers filled, or being filled, ahead of their use
-    uint32_t wb = 0, rb = 0, rph = 0;  // buffers: filled next, used next
-    auto issue = [&]() {
-      if (ahead.t >= tiles) return;
-      const bool swap = swapped(ahead), a = swap ? gen_b : gen_a, b = ahead.tj >= 0 && gen_b;
-      if (elect()) {
-        const uint32_t raw = raw0 + wb * raw_step, bar = landed + 8 * wb;
-        const int c = ahead.kb * kDeep;
-        bar_expect(bar, (uint32_t)((a ? lines_a : 0) + (b ? lines_b : 0)) * kRawLine);
-        if (a)
-          gen_load(swap ? &maps.b[r] : &maps.a[r], swap ? b_c : a_c, swap ? any_b : any_a,
-                   ahead.ti * 256 + (int)half * kRowsCta, c, lines_a, raw, bar);
-        if (b)
-          gen_load(&maps.b[r], b_c, any_b, ahead.tj * bn + (int)half * (bn / 2), c, lines_b,
-                   raw + g.raw_a, bar);
-      }
-      __syncwarp();
-      ++flying;
-      if (++wb == (uint32_t)raws) wb = 0;
-      next(ahead);
-    };
-    uint32_t s = 0, ph = 0;
-    bool ok = kb0 < kb1;
-    if (ok) {
-      enter(ahead);
-      enter(now);
-      for (int q = 0; q < raws; ++q) issue();
-    }
-    while (ok && now.t < tiles) {
-      ok = bar_wait(landed + 8 * rb, rph, &dead) && bar_wait(empty + 8 * s, ph ^ 1, &dead);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      const bool swap = swapped(now);
-      const uint32_t a_at = ring + s * stage_bytes, raw = raw0 + rb * raw_step;
-      if (swap ? gen_b : gen_a) gen_shift(raw, a_at, lines_a, r, swap ? by_b : by_a, lane);
-      if (now.tj >= 0 && gen_b)
-        gen_shift(raw + g.raw_a, a_at + kBytesA, lines_b, r, by_b, lane);
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();  // the raw lines are read, the tile's are written
-      if (lane == 0) bar_arrive(filled + 8 * s);
-      --flying;
-      if (++s == (uint32_t)stages) {
-        s = 0;
-        ph ^= 1;
-      }
-      if (++rb == (uint32_t)raws) {
-        rb = 0;
-        rph ^= 1;
-      }
-      next(now);
-      issue();
-    }
-    // after a wait that gave up: what is in flight lands before the CTA returns
-    for (; flying > 0; --flying) {
-      const long long t0 = clock64();
-      while (!bar_try(landed + 8 * rb, rph) && clock64() - t0 < kWaitCycles / 8) {
-      }
-      if (++rb == (uint32_t)raws) {
-        rb = 0;
-        rph ^= 1;
-      }
-    }
-   }
-  } else if (GEN && warp == 3) {
-    // The arrival at the pair's first CTA releases to the cluster, which waits
-    // for every access of the thread before it: on a warp of its own there are
-    // none.
+    const int lines_b = bn / 16;
     const uint32_t full_lead = remote(full, leader);
-    uint32_t s = 0, ph = 0;
-    bool live = true;
-    for (int t = first; t < tiles; t += clusters)
+    const uint32_t by_a = gen_distance(k.a, r), by_b = gen_distance(k.b, r);
+    const uint32_t raw_a = g.raw_a, raw0 = bias_smem + g.bias_in + (uint32_t)r * (raw_a + g.raw_b),
+                   raw_step = (uint32_t)kGenWarps * (raw_a + g.raw_b);
+    uint32_t s = 0, ph = 0, rb = 0, rph = 0;
+    bool ok = true;
+    for (int t = first; t < tiles && ok; t += clusters) {
+      int ti, tj;
+      tile_at(g, t, ti, tj);
+      // for a tile of B's bias sums, B is in A's place
+      const bool swap = tj < 0 && bias_b, a = swap ? gen_b : gen_a, b = tj >= 0 && gen_b;
+      const uint32_t by = swap ? by_b : by_a;
       for (int kb = kb0; kb < kb1; ++kb) {
-        live = live && bar_wait(filled + 8 * s, ph, &dead);
-        if (elect() && live) bar_arrive_cluster_release(full_lead + 8 * s);
-        __syncwarp();
-        if (++s == (uint32_t)g.stages) {
+        ok = bar_wait(landed + 8 * rb, rph, &dead) && bar_wait(empty + 8 * s, ph ^ 1, &dead);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t a_at = ring + s * stage_bytes, raw = raw0 + rb * raw_step;
+        if (a) gen_shift(raw, a_at, kRowsCta / 8, r, by, lane);
+        if (b) gen_shift(raw + raw_a, a_at + kBytesA, lines_b, r, by_b, lane);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();  // the raw lines are read, the tile's are written
+        // The reader is this SM's tensor core, at the word of the pair's first
+        // CTA: the fence has put the writes where it finds them before this
+        // arrival leaves.  (One that releases to the cluster takes 1300 cycles.)
+        if (lane == 0) {
+          bar_arrive_cluster(full_lead + 8 * s);
+          bar_arrive(used + 8 * rb);
+        }
+        if (++s == (uint32_t)stages) {
           s = 0;
           ph ^= 1;
         }
+        if (++rb == (uint32_t)raws) {
+          rb = 0;
+          rph ^= 1;
+        }
       }
+    }
+  } else if (GEN && (warp == 2 || warp == 3)) {
+    if constexpr (GEN) {
+      const bool for_a = warp == 2, bias_b = g.bias_b;
+      const int bn = g.bn, lines = for_a ? kRowsCta / 8 : bn / 16;
+      const uint32_t raw_warp = g.raw_a + g.raw_b, raws = g.raws;
+      const uint32_t raw0 = bias_smem + g.bias_in + (for_a ? 0 : g.raw_a);
+      uint32_t issued = 0, wb = 0, wph = 0;
+      bool live = true;
+      for (int t = first; t < tiles; t += clusters) {
+        int ti, tj;
+        tile_at(g, t, ti, tj);
+        // for a tile of B's bias sums, B is in A's place
+        const bool b = !for_a || (tj < 0 && bias_b), contig = b ? b_c : a_c;
+        const bool on = (b ? g.gen_b : g.gen_a) && (for_a || tj >= 0);
+        const int64_t all = b ? (b_c ? k.cols : k.depth) : (a_c ? k.rows : k.depth);
+        const CUtensorMap* of = b ? maps.b : maps.a;
+        const int i0 = for_a ? ti * 256 + (int)half * kRowsCta : tj * bn + (int)half * (bn / 2);
+        const uint32_t bytes = on ? (uint32_t)lines * (kRawLine * kGenWarps) : 0;
+        for (int kb = kb0; kb < kb1; ++kb) {
+          live = live && bar_wait(used + 8 * wb, wph ^ 1, &dead);
+          if (elect() && live) {
+            const uint32_t bar = landed + 8 * wb;
+            bar_expect(bar, bytes);
+            if (on)
+              gen_load(of, contig, all, i0, kb * kDeep, lines, raw0 + wb * kGenWarps * raw_warp,
+                       raw_warp, bar);
+          }
+          __syncwarp();
+          issued += live;
+          if (++wb == raws) {
+            wb = 0;
+            wph ^= 1;
+          }
+        }
+      }
+      // after a wait that gave up: what is in flight lands before the CTA returns
+      for (uint32_t q = issued > raws ? issued - raws : 0; !live && q < issued; ++q) {
+        const long long t0 = clock64();
+        while (!bar_try(landed + 8 * (q % raws), (q / raws) & 1) &&
+               clock64() - t0 < kWaitCycles / 8) {
+        }
+      }
+    }
   }
   __syncwarp();
 
