@@ -1725,7 +1725,9 @@ static cudaError_t launch_mode(const ProductK& in, cudaStream_t st) {
   // per column, and a further wave of those its start as well.  (Measured, us,
   // one part / two: 1 x 4096 x 4096 17.4 / 11.9, 1024 x 1024 x 4096 at BN = 128
   // 18.4 / 14.1, 2048 x 1024 x 4096 at BN = 256 23.4 / 18.0, 1024 x 2304 x 768
-  // at 128 8.8 / 16.6; four parts, clusters of 8, always lost.)
+  // at 128 8.8 / 16.6; four parts, clusters of 8, always lost.)  Lines off
+  // 16-byte boundaries bound a step by shifting them: 870 cycles for 144 of
+  // them, 1040 for 192, 1430 for 256.
   // The tensor cores add to their sums without rounding to nearest, so a long
   // contraction loses digits: 7e-7 of the result after 768 terms, 7e-6 after
   // 6000 (in units of its size).  fp32 results therefore take the sums out
@@ -1744,6 +1746,8 @@ static cudaError_t launch_mode(const ProductK& in, cudaStream_t st) {
     return bias_rows > 0 && main > 0 && (!g.bias_b || bn == 256) &&
            (exact ? bn == 128 : S > 1 || main <= pairs || bn == 128);
   };
+  const bool gen_a = k.depth > 0 && k.rows > 0 && off_words(k.a, k.a_c ? k.rows : k.depth);
+  const bool gen_b = k.depth > 0 && k.cols > 0 && off_words(k.b, k.b_c ? k.cols : k.depth);
   double best = 0;
   for (int bn = 32; bn <= 256; bn *= 2) {
     if (!k.b_c && bn < 128) continue;       // blocks of 64 rows per CTA
@@ -1754,7 +1758,9 @@ static cudaError_t launch_mode(const ProductK& in, cudaStream_t st) {
       const bool fused = fuses_bias(bn, S, tiles_j);
       const int64_t tiles = tiles_i * tiles_j + (fused ? 0 : (bias_rows + 255) / 256);
       const double waves = (double)((tiles * S + pairs - 1) / pairs);
-      const double step = bn == 256 ? (exact ? 520 + 1500.0 / kRound : 520) : 430;
+      double step = bn == 256 ? (exact ? 520 + 1500.0 / kRound : 520) : 430;
+      const double shift = 300 + 4.2 * ((gen_a ? kRowsCta : 0) + (gen_b ? bn / 2 : 0));
+      if ((gen_a || gen_b) && step < shift) step = shift;
       const double cost =
           waves * ((double)kblocks / S * step + (S > 1 ? 2500 + 15 * bn : 0)) +
           (S > 1 || (exact && bn == 256) ? (waves - 1) * 8000 : 0) + 25 * bn;
@@ -1780,8 +1786,8 @@ static cudaError_t launch_mode(const ProductK& in, cudaStream_t st) {
   CUtensorMap ma{}, mb{};
   BoxMaps maps{};
   if (k.depth > 0) {
-    g.gen_a = k.rows > 0 ? off_words(k.a, k.a_c ? k.rows : k.depth) : 0;
-    g.gen_b = k.cols > 0 ? off_words(k.b, k.b_c ? k.cols : k.depth) : 0;
+    g.gen_a = gen_a;
+    g.gen_b = gen_b;
     if (!g.gen_a && k.rows > 0 &&
         !operand_map(&ma, k.a, k.a_c, k.rows, k.depth, kRowsCta))
       return cudaErrorInvalidValue;
