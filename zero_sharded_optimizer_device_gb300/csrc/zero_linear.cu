@@ -850,111 +850,136 @@ __device__ __forceinline__ bool column_in(const Mat& m, const Column& c, int i, 
 }
 // Past its rows a lane reads the last one again: loads without a condition
 // each are all in flight together (7615 x 80 by 4624 with SiLU, a gate and its
-// input kept, odd rows: 209 us, 289 with conditions; eight
-// rows at a time in a loop, 372).
-template <typename T>
-__device__ __forceinline__ void column_words(const T* p, const Mat& m, const Column& c,
-                                             const Extent& e, T u[32]) {
+// input kept, odd rows: 242 us, 289 with conditions).
+template <int R, typename T>
+__device__ __forceinline__ void column_words(const T* p, const Mat& m, const Column& c, int i0,
+                                             const Extent& e, T u[R]) {
+  const int last = c.count - 1;
+  int i = i0 < last ? i0 : last;
+  p += (c.row + i) * m.ld + c.col;
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    u[i] = column_in(m, c, i < c.count ? i : c.count - 1, e) ? *p : T(0);
-    p += i + 1 < c.count ? m.ld : 0;
+  for (int j = 0; j < R; ++j) {
+    u[j] = column_in(m, c, i, e) ? *p : T(0);
+    const bool on = i < last;
+    p += on ? m.ld : 0;
+    i += on;
   }
 }
-__device__ __forceinline__ void column_load(const Mat& m, const Column& c, const Extent& e,
-                                            float f[32]) {
+template <int R>
+__device__ __forceinline__ void column_load(const Mat& m, const Column& c, int i0,
+                                            const Extent& e, float f[R]) {
   if (c.count <= 0) return;
-  const int64_t at = c.row * m.ld + c.col;
   if (m.dtype == ZERO_F32) {
-    column_words(static_cast<const float*>(m.p) + at, m, c, e, f);
+    column_words<R>(static_cast<const float*>(m.p), m, c, i0, e, f);
   } else {
-    uint16_t u[32];
-    column_words(static_cast<const uint16_t*>(m.p) + at, m, c, e, u);
+    uint16_t u[R];
+    column_words<R>(static_cast<const uint16_t*>(m.p), m, c, i0, e, u);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) f[i] = __uint_as_float((uint32_t)u[i] << 16);
+    for (int j = 0; j < R; ++j) f[j] = __uint_as_float((uint32_t)u[j] << 16);
   }
 }
-__device__ __forceinline__ void column_store(const Mat& m, const Column& c, const Extent& e,
-                                             const float f[32]) {
-  const int64_t at = c.row * m.ld + c.col;
+template <int R>
+__device__ __forceinline__ void column_store(const Mat& m, const Column& c, int i0,
+                                             const Extent& e, const float f[R]) {
+  const int64_t at = (c.row + i0) * m.ld + c.col;
   if (m.dtype == ZERO_F32) {
     float* p = static_cast<float*>(m.p) + at;
 #pragma unroll
-    for (int i = 0; i < 32; ++i, p += m.ld)
-      if (i < c.count && column_in(m, c, i, e)) *p = f[i];
+    for (int j = 0; j < R; ++j, p += m.ld)
+      if (i0 + j < c.count && column_in(m, c, i0 + j, e)) *p = f[j];
   } else {
     uint16_t* p = static_cast<uint16_t*>(m.p) + at;
 #pragma unroll
-    for (int i = 0; i < 32; ++i, p += m.ld)
-      if (i < c.count && column_in(m, c, i, e)) *p = to_bf16(f[i]);
+    for (int j = 0; j < R; ++j, p += m.ld)
+      if (i0 + j < c.count && column_in(m, c, i0 + j, e)) *p = to_bf16(f[j]);
   }
 }
 
-// `keep` holds the mask as finish_block would use it.
-template <int MODE>
+// R rows at a time.  `keep` holds the mask as finish_block would use it.
+template <int MODE, int R, bool SIDES>
 __device__ __forceinline__ void finish_columns(const EpiK& k, uint32_t keep, uint32_t patch,
-                                               uint32_t biases, int64_t row0, int64_t col0, const Extent& e,
-                                               int lane) {
+                                               uint32_t biases, int64_t row0, int64_t col0,
+                                               const Extent& e, int lane) {
   Column c;
   c.row = row0;
   c.col = col0 + lane;
   c.count = c.col >= e.cols ? 0 : (int)(e.rows - row0 < 32 ? e.rows - row0 : 32);
-  float v[32], f[32];
+  float bias = 0.0f;
+  if (MODE == LIN_FORWARD && k.bias.p)
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(bias) : "r"(biases + (uint32_t)lane * 4));
+#pragma unroll 1
+  for (int i0 = 0; i0 < 32 && row0 + i0 < e.rows; i0 += R) {
+    float v[R], f[R];
 #pragma unroll
-  for (int i = 0; i < 32; ++i)
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[i]) : "r"(patch + (i * 36 + lane) * 4));
-  if constexpr (MODE == LIN_FORWARD) {
-    if (k.bias.p) {
-      float b;
-      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(b) : "r"(biases + (uint32_t)lane * 4));
+    for (int i = 0; i < R; ++i)
+      asm volatile("ld.shared.f32 %0, [%1];"
+                   : "=f"(v[i])
+                   : "r"(patch + ((i0 + i) * 36 + lane) * 4));
+    if constexpr (MODE == LIN_FORWARD) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] += b;
-    }
-    if (k.pre.p) column_store(k.pre, c, e, v);
-    activate<32>(v, k.act);
-    if (k.gate.p) {
-      column_load(k.gate, c, e, f);
+      for (int i = 0; i < R; ++i) v[i] += bias;
+      if (SIDES && k.pre.p) column_store<R>(k.pre, c, i0, e, v);
+      activate<R>(v, k.act);
+      if (SIDES && k.gate.p) {
+        column_load<R>(k.gate, c, i0, e, f);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] *= f[i];
-    }
-    if (k.drop.on) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {  // the lane and bit that hold this element
-        const uint32_t m = __shfl_sync(0xffffffffu, keep, (i & 7) << 2 | lane >> 3);
-        v[i] = m >> (31 - (i >> 3) * 8 - (lane & 7)) & 1 ? v[i] * k.drop.scale : 0.0f;
+        for (int i = 0; i < R; ++i) v[i] *= f[i];
       }
-    }
-    if (k.residual.p) {
-      column_load(k.residual, c, e, f);
+      if (k.drop.on) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] += f[i];
-    }
-  } else if constexpr (MODE == LIN_DINPUT) {
-    if (k.pre.p) {
-      column_load(k.pre, c, e, f);
-      float slope[32];
-      activate_grad<32>(f, slope, k.act);
-      if (k.gate.p) {
-        if (k.dgate.p) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) f[i] *= v[i];
-          column_store(k.dgate, c, e, f);
+        for (int i = 0; i < R; ++i) {  // the lane and bit that hold this element
+          const uint32_t m = __shfl_sync(0xffffffffu, keep, (i & 7) << 2 | lane >> 3);
+          v[i] = m >> (31 - ((i0 + i) >> 3) * 8 - (lane & 7)) & 1 ? v[i] * k.drop.scale : 0.0f;
         }
-        column_load(k.gate, c, e, f);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) slope[i] *= f[i];
       }
+      if (SIDES && k.residual.p) {
+        column_load<R>(k.residual, c, i0, e, f);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] *= slope[i];
-    }
-  } else {
-    if (k.accumulate) {
-      column_load(k.out, c, e, f);
+        for (int i = 0; i < R; ++i) v[i] += f[i];
+      }
+    } else if constexpr (MODE == LIN_DINPUT) {
+      if (SIDES && k.pre.p) {
+        column_load<R>(k.pre, c, i0, e, f);
+        float slope[R];
+        activate_grad<R>(f, slope, k.act);
+        if (SIDES && k.gate.p) {
+          if (k.dgate.p) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] += f[i];
+            for (int i = 0; i < R; ++i) f[i] *= v[i];
+            column_store<R>(k.dgate, c, i0, e, f);
+          }
+          column_load<R>(k.gate, c, i0, e, f);
+#pragma unroll
+          for (int i = 0; i < R; ++i) slope[i] *= f[i];
+        }
+#pragma unroll
+        for (int i = 0; i < R; ++i) v[i] *= slope[i];
+      }
+    } else {
+      if (SIDES && k.accumulate) {
+        column_load<R>(k.out, c, i0, e, f);
+#pragma unroll
+        for (int i = 0; i < R; ++i) v[i] += f[i];
+      }
     }
+    column_store<R>(k.out, c, i0, e, v);
   }
-  column_store(k.out, c, e, v);
+}
+
+// Without side operands 32 rows in one go (768 to 50257 fp32: 45 us, 49 by 16
+// rows); with them 16, as 32 leave too few registers (gradient of 4868 x 1134
+// inputs through 192 outputs and a gated GELU: 50.5 us, 53.7 by 32 rows).
+template <int MODE>
+__device__ __forceinline__ void finish_any_columns(const EpiK& k, uint32_t keep, uint32_t patch,
+                                                   uint32_t biases, int64_t row0, int64_t col0,
+                                                   const Extent& e, int lane) {
+  const bool sides = MODE == LIN_FORWARD  ? k.pre.p || k.gate.p || k.residual.p
+                     : MODE == LIN_DINPUT ? k.pre.p != nullptr
+                                          : k.accumulate != 0;
+  if (sides)
+    finish_columns<MODE, 16, true>(k, keep, patch, biases, row0, col0, e, lane);
+  else
+    finish_columns<MODE, 32, false>(k, keep, patch, biases, row0, col0, e, lane);
 }
 
 // Dropout's masks of a thread's share of a tile, 32 elements each: drawn while
@@ -1419,23 +1444,33 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
           const uint32_t bias = biases + (uint32_t)(piece >> 1) * (kPiece * 4);
           Sides<MODE> sides;
           if (k.epi.vec) load_sides<MODE>(k.epi, b, e, sides);
-          float v[kPiece];
-          piece_sums(piece, v);
-          if (out_t) {
+          // (half a piece at a time: the side operands take many registers)
 #pragma unroll
-            for (int q = 0; q < 32; ++q)
-              asm volatile("st.shared.f32 [%0], %1;" ::"r"(mine + (q * 36 + lane) * 4), "f"(v[q]));
-          } else {
+          for (int h = 0; h < 32; h += 16) {
+            uint32_t r[16];
+            tmem_load16(d + piece * 32 + h, r);
+            if (rounds > 1) tmem_add<16>(summed + piece * 32 + h, r);
+            if (S > 1) add_part<16>(part_at<32>(ring, piece, pieces, w, lane) + h / 4 * 512, r);
+            float v[16];
 #pragma unroll
-            for (int q = 0; q < 32; q += 4)
-              st_shared4(mine + (lane * 36 + q) * 4, v[q], v[q + 1], v[q + 2], v[q + 3]);
+            for (int q = 0; q < 16; ++q) v[q] = empty_sum ? 0.0f : __uint_as_float(r[q]);
+            if (out_t) {
+#pragma unroll
+              for (int q = 0; q < 16; ++q)
+                asm volatile("st.shared.f32 [%0], %1;" ::"r"(mine + ((h + q) * 36 + lane) * 4),
+                             "f"(v[q]));
+            } else {
+#pragma unroll
+              for (int q = 0; q < 16; q += 4)
+                st_shared4(mine + (lane * 36 + h + q) * 4, v[q], v[q + 1], v[q + 2], v[q + 3]);
+            }
           }
           __syncwarp();
           if (k.epi.vec)
             finish_block<MODE>(k.epi, masks.at(piece >> 1), mine, bias, b, e, sides, lane);
           else
-            finish_columns<MODE>(k.epi, masks.at(piece >> 1), mine, bias, out_t ? j0 : i0,
-                                 out_t ? i0 : j0, e, lane);
+            finish_any_columns<MODE>(k.epi, masks.at(piece >> 1), mine, bias, out_t ? j0 : i0,
+                                     out_t ? i0 : j0, e, lane);
           __syncwarp();
         }
       }
