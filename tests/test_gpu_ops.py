@@ -121,6 +121,36 @@ def test_linear_activations(cuda, Z, act, out):
     run_linear(Z, 140, 200, 96, False, act=act, out=out)
 
 
+@pytest.mark.parametrize("pad,skew", [(0, 0), (8, 0), (1, 3)])
+@pytest.mark.parametrize("kn", [False, True], ids=["nk", "kn"])
+@pytest.mark.parametrize("n,k", [(1, 4099), (31, 8), (260, 1000), (33, 264), (1000, 64), (520, 2056)])
+@pytest.mark.parametrize("m", [1, 2, 3, 4, 5, 8, 9])
+def test_few_rows(cuda, Z, m, n, k, kn, pad, skew):
+    """Tokens being generated: every count of rows, outputs that end inside a
+    warp's four and a block's 32, contractions of one piece and of many."""
+    run_linear(Z, m, n, k, kn, bias=F32, act="silu", pre=True, gate=True, residual=BF, p=0.25,
+               pad=pad, skew=skew)
+    run_linear(Z, m, n, k, kn, out=F32, pad=pad, skew=skew)
+
+
+@pytest.mark.parametrize("kn", [False, True], ids=["nk", "kn"])
+@pytest.mark.parametrize("m,n,k", [(1, 1000, 33), (3, 264, 512), (7, 129, 260), (8, 2056, 40)])
+def test_few_rows_gradient(cuda, Z, m, n, k, kn):
+    g = torch.Generator().manual_seed(m * n + k)
+    dy, w = randn(g, m, n), randn(g, *((k, n) if kn else (n, k)), scale=n ** -0.5)
+    pre, u = randn(g, m, k), randn(g, m, k)
+    lay = Z.ZERO_W_KN if kn else Z.ZERO_W_NK
+    DX, DU = Guarded(m, k, F32, 1), Guarded(m, k, BF, 3, 5)
+    D, W, P, U = (t.cuda() for t in (dy, w, pre, u))
+    ag = Z.linear_act_grad(Z.ZERO_ACT_GELU, P, k, U, k, DU.t, DU.ld)
+    Z.zero_linear_dinput(D, n, W, W.shape[1], lay, m, n, k, ag, DX.t, DX.ld, Z.ZERO_F32)
+    dx, du, ex, eu = R.linear_dinput(dy, w, kn, "gelu", pre, u)
+    R.assert_within(DX.t, dx, ex, "dx")
+    R.assert_within(DU.t, du, eu, "dgate")
+    DX.check("dx")
+    DU.check("dgate")
+
+
 @pytest.mark.parametrize("pad,skew", [(1, 0), (0, 1), (3, 5), (8, 0), (4, 4), (2, 2), (8, 8)])
 @pytest.mark.parametrize("kn", [False, True], ids=["nk", "kn"])
 @pytest.mark.parametrize("m,n,k", [(1, 64, 200), (40, 96, 136), (300, 264, 200)])

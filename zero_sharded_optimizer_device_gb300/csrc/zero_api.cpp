@@ -605,13 +605,14 @@ extern "C" int zero_bounds_report(zero_bounds_t* out, int32_t reset) {
   *out = zero_bounds_t{};
 #ifdef ZERO_CHECKED
   out->checked = 1;
-  zk::BoundsRec rec[5] = {};
+  zk::BoundsRec rec[6] = {};
   cudaError_t e = cudaDeviceSynchronize();
   if (e == cudaSuccess) e = zk::bounds_rs(&rec[0], reset != 0);
   if (e == cudaSuccess) e = zk::bounds_kernels(&rec[1], reset != 0);
   if (e == cudaSuccess) e = zk::bounds_linear(&rec[2], reset != 0);
   if (e == cudaSuccess) e = zk::bounds_dropout(&rec[3], reset != 0);
   if (e == cudaSuccess) e = zk::bounds_lnorm(&rec[4], reset != 0);
+  if (e == cudaSuccess) e = zk::bounds_rows(&rec[5], reset != 0);
   if (e != cudaSuccess) return cuda_status(e);
   for (const zk::BoundsRec& r : rec) {
     if (r.count && !out->count) {  // the first unit with a record gives the details

@@ -66,6 +66,9 @@ struct ProductK {
 };
 
 cudaError_t launch_product(const ProductK& k, int mode, cudaStream_t st);
+// Forward products and input gradients of up to kFewRows rows.
+constexpr int kFewRows = 8;
+cudaError_t launch_rows(const ProductK& k, int mode, cudaStream_t st);
 
 cudaError_t launch_dropout(const Mat& x, const Mat& residual, const Mat& y, int64_t m, int64_t n,
                            const DropK& d, cudaStream_t st);
@@ -95,5 +98,6 @@ cudaError_t ops_timeouts(unsigned long long* out, bool reset);
 cudaError_t bounds_linear(BoundsRec* out, bool reset);
 cudaError_t bounds_dropout(BoundsRec* out, bool reset);
 cudaError_t bounds_lnorm(BoundsRec* out, bool reset);
+cudaError_t bounds_rows(BoundsRec* out, bool reset);
 
 }  // namespace zk
