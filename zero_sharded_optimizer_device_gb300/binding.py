@@ -104,7 +104,7 @@ class zero_linear_epilogue_t(ctypes.Structure):
     _fields_ = [("bias", c_vp), ("bias_dtype", c_i32), ("act", c_i32), ("pre", c_vp),
                 ("ldpre", c_i64), ("gate", c_vp), ("ldgate", c_i64), ("residual", c_vp),
                 ("ldres", c_i64), ("res_dtype", c_i32), ("reserved", c_i32),
-                ("dropout", P(zero_dropout_t))]
+                ("dropout", c_vp)]
 
 
 class zero_act_grad_t(ctypes.Structure):
@@ -818,6 +818,11 @@ def _mat(x, rows: int, cols: int, ld: int, dtype: int, what: str):
     if not _Torch.ready:
         _Torch.load()
     want = _Torch.dtypes.get(dtype)
+    # as the call describes it: the tensor's own shape says that it holds that much
+    if x.dtype is want and x.stride() == (ld, 1) and x.shape == (rows, cols):
+        dev = x.get_device()
+        if dev >= 0 and _Torch.cuda and dev == _Torch.device():
+            return x.data_ptr()
     if want is not None:
         if x.dtype is not want:
             raise ValueError(f"{what}: a {x.dtype} tensor passed as {want}")
@@ -866,7 +871,7 @@ def linear_epilogue(bias=None, bias_dtype: int = ZERO_BF16, act: int = ZERO_ACT_
     """What follows the product in zero_linear (zero_linear_epilogue_t); may be
     kept and used for many calls."""
     e = zero_linear_epilogue_t(None, bias_dtype, act, None, ldpre, None, ldgate, None, ldres,
-                               res_dtype, 0, ctypes.pointer(dropout) if dropout else None)
+                               res_dtype, 0, ctypes.addressof(dropout) if dropout else None)
     mats = []
     if bias is not None:
         mats.append(("bias", bias, True, 0, bias_dtype))
