@@ -15,7 +15,7 @@
 //           time; rows of A wait in shared memory
 // Lines off 16-byte boundaries are read a value a lane, 32 in a row.
 // One row (4096 outputs of 4096, bf16 weights): along 5.3 us, 6.3 TB/s; across
-// 10.3; in tiles on the tensor cores 12.5.  A lane's loads of several steps are
+// 9.8; in tiles on the tensor cores 12.5.  A lane's loads of several steps are
 // issued together and without conditions between them: across 4096 x 11008 one
 // by one took 50 us, so 24.
 #include "zero_ops_device.cuh"
@@ -246,6 +246,15 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   };
   for (int64_t base = first; base < last; base += kDepth) {
     const int n = (int)(last - base < kDepth ? last - base : kDepth);
+    constexpr int kStep = kWarps * kLines;
+    int r = warp * kLines + lane / kLanes;
+    // the first batch of weights is on its way while A's rows are
+    const bool ahead = VEC == 8 && whole && r + (kAhead - 1) * kStep < n;
+    Word<VEC> w0[kAhead];
+    if (ahead)
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        w0[u] = word_at<VEC>(k.b, base + r + u * kStep, col, depth, cols);
     if (base > first) __syncthreads();
     for (int r = threadIdx.x; r < n; r += kWarps * 32)
 #pragma unroll
@@ -255,8 +264,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
         xs[r][i] = pair(x, x);
       }
     __syncthreads();
-    constexpr int kStep = kWarps * kLines;
-    int r = warp * kLines + lane / kLanes;
+    if (ahead) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) add(w0[u], r + u * kStep);
+      r += kAhead * kStep;
+    }
     if (whole) {  // (no condition around a load: a batch is in flight at once)
       for (; r + (kAhead - 1) * kStep < n; r += kAhead * kStep) {
         Word<VEC> w[kAhead];
