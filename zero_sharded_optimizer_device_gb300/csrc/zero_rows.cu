@@ -206,13 +206,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
 }
 
 // The CTAs of a cluster of `parts` share the contraction of their 32 outputs.
-template <int MODE, int M, int VEC>
-__global__ void __launch_bounds__(kWarps * 32, 2)
+template <int MODE, int M, int VEC, int W>
+__global__ void __launch_bounds__(W * 32, W == kWarps ? 2 : 1)
     across_kernel(const __grid_constant__ ProductK k, int parts) {
   constexpr int kLanes = kAcross / VEC, kLines = 32 / kLanes;  // of a warp
   constexpr int kDepth = M < 4 ? 1024 : 512, kAhead = VEC == 8 ? 4 : 16;
   __shared__ __align__(16) uint64_t xs[kDepth][M];  // each value twice
-  __shared__ float red[kWarps][M * kAcross], sum[M * kAcross];
+  __shared__ float red[W][M * kAcross], sum[M * kAcross];
   after_previous_kernel();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int part = (int)(blockIdx.x % parts);
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   };
   for (int64_t base = first; base < last; base += kDepth) {
     const int n = (int)(last - base < kDepth ? last - base : kDepth);
-    constexpr int kStep = kWarps * kLines;
+    constexpr int kStep = W * kLines;
     int r = warp * kLines + lane / kLanes;
     // the first batch of weights is on its way while A's rows are
     const bool ahead = VEC == 8 && whole && r + (kAhead - 1) * kStep < n;
@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
       for (int u = 0; u < kAhead; ++u)
         w0[u] = word_at<VEC>(k.b, base + r + u * kStep, col, depth, cols);
     if (base > first) __syncthreads();
-    for (int r = threadIdx.x; r < n; r += kWarps * 32)
+    for (int r = threadIdx.x; r < n; r += W * 32)
 #pragma unroll
       for (int i = 0; i < M; ++i) {
         const float x =
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   float v = 0.0f;
   if (t < M * kAcross) {
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) v += red[w][t];
+    for (int w = 0; w < W; ++w) v += red[w][t];
     sum[t] = v;
   }
   if (parts > 1) {
@@ -344,12 +344,21 @@ static cudaError_t launch_vec(const ProductK& k, cudaStream_t st) {
                        dim3(kWarps * 32), st, k, share);
   }
   const int64_t blocks = (k.cols + kAcross - 1) / kAcross;
+  // one row: 32 warps instead of a cluster where all is one batch of loads each
+  // (4096 x 1024: 4.1 us, 6.7 in clusters; two batches each, 768 x 1536: 4.9
+  // and 4.2)
+  constexpr int kMany = M == 1 && VEC == 8 ? 32 : kWarps;
+  const bool many =
+      kMany > kWarps && k.depth > 512 && k.depth <= 1024 && blocks <= sm_count();
   int parts = 1;
-  while (parts < 8 && blocks * parts < 3 * sm_count() && k.depth >= (int64_t)parts * 256)
+  while (!many && parts < 8 && blocks * parts < 3 * sm_count() &&
+         k.depth >= (int64_t)parts * 256)
     parts *= 2;
+  const auto kernel =
+      many ? across_kernel<MODE, M, VEC, kMany> : across_kernel<MODE, M, VEC, kWarps>;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(blocks * parts));
-  cfg.blockDim = dim3(kWarps * 32);
+  cfg.blockDim = dim3((many ? kMany : kWarps) * 32);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -359,7 +368,7 @@ static cudaError_t launch_vec(const ProductK& k, cudaStream_t st) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, across_kernel<MODE, M, VEC>, k, parts);
+  return cudaLaunchKernelEx(&cfg, kernel, k, parts);
 }
 template <int MODE, int M>
 static cudaError_t launch_few(const ProductK& k, cudaStream_t st) {
