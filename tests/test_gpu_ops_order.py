@@ -1,0 +1,102 @@
+"""The layer operators where the order of things decides: boxes that land late,
+operands shifted by two CTAs, calls side by side and back to back.  Results
+are compared with 64 bits and, again and again with a cold cache, with
+themselves: no bit may differ."""
+import pytest
+import torch
+
+import ops_reference as R
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def Z():
+    import zero_sharded_optimizer_device_gb300 as Z
+    return Z
+
+
+@pytest.fixture(scope="module")
+def flush():
+    """Writes more than the L2 holds, so that the next call's operands come
+    from memory."""
+    junk = torch.empty(64 << 20, device="cuda")
+    return lambda v: junk.fill_(v)
+
+
+def rnd(seed, *shape, scale=1.0, dtype=BF):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(*shape, generator=g, device="cuda") * scale).to(dtype)
+
+
+def product_bound(a, b, extra):
+    """a @ b.T in 64 bits and what k fp32 terms in any order may miss of it."""
+    a, b = a.to(R.D), b.to(R.D)
+    return a @ b.T, (a.shape[1] + 4) * R.U32 * (a.abs() @ b.abs().T + extra)
+
+
+def within(got, want, err, what):
+    u = R.U16 if got.dtype == BF else R.U32
+    bad = (got.to(R.D) - want).abs() > err + u * (want.abs() + err) + 1e-37
+    assert not bool(bad.any()), f"{what}: {int(bad.sum())} elements outside their bound"
+
+
+# tiles 256 and 128 wide, whole and with an odd number of 32-column chunks
+BOXES = [(4096, 4096, 512), (2048, 2504, 704), (1100, 3304, 1000), (2100, 2024, 2304)]
+
+
+@pytest.mark.parametrize("m,n,k", BOXES)
+def test_fp32_boxes_with_a_cold_residual(cuda, Z, flush, m, n, k):
+    x, w, r = rnd(1, m, k), rnd(2, n, k, scale=k ** -0.5), rnd(3, m, n, dtype=F32)
+    want, err = product_bound(x, w, r.to(R.D).abs())
+    first = None
+    for i in range(6):
+        y = torch.full((m, n), -7.0, device="cuda")
+        flush(i)
+        ep = Z.linear_epilogue(residual=r, ldres=n, res_dtype=Z.ZERO_F32)
+        Z.zero_linear(x, k, w, k, Z.ZERO_W_NK, m, n, k, ep, y, n, Z.ZERO_F32)
+        if first is None:
+            within(y, want + r.to(R.D), err, "y")
+            first = y
+        assert torch.equal(y, first), f"run {i} differs"
+
+
+@pytest.mark.parametrize("kn", [False, True], ids=["nk", "kn"])
+@pytest.mark.parametrize("n,k,m", [(4096, 4096, 512), (2048, 2504, 704), (2504, 2104, 2304)])
+def test_fp32_boxes_accumulating(cuda, Z, flush, n, k, m, kn):
+    dy, x = rnd(1, m, n), rnd(2, m, k)
+    shape = (k, n) if kn else (n, k)
+    dw0 = rnd(3, *shape, dtype=F32)
+    a, b = (x, dy) if kn else (dy, x)
+    want, err = product_bound(a.T, b.T, dw0.to(R.D).abs())
+    first = None
+    for i in range(6):
+        dw = dw0.clone()
+        flush(i)
+        Z.zero_linear_dweight(dy, n, x, k, m, n, k, Z.ZERO_W_KN if kn else Z.ZERO_W_NK, dw,
+                              shape[1], Z.ZERO_F32, None, Z.ZERO_F32, True)
+        if first is None:
+            within(dw, want + dw0.to(R.D), err, "dw")
+            first = dw
+        assert torch.equal(dw, first), f"run {i} differs"
+
+
+@pytest.mark.parametrize("m,n,k", BOXES)
+def test_fp32_boxes_with_a_gate_and_kept_inputs(cuda, Z, flush, m, n, k):
+    """Two slots a chunk, so two chunks in the ring: a tile with an odd number
+    of chunks swaps the slots of the two sets of warps."""
+    x, w, u = rnd(1, m, k), rnd(2, n, k, scale=k ** -0.5), rnd(3, m, n)
+    z64, err = product_bound(x, w, 0)
+    gate = u.to(R.D)
+    first = None
+    for i in range(6):
+        y, z = torch.full((m, n), -7.0, device="cuda"), torch.full((m, n), -7.0, dtype=BF, device="cuda")
+        flush(i)
+        ep = Z.linear_epilogue(pre=z, ldpre=n, gate=u, ldgate=n)
+        Z.zero_linear(x, k, w, k, Z.ZERO_W_NK, m, n, k, ep, y, n, Z.ZERO_F32)
+        if first is None:
+            within(z, z64, err, "pre")
+            within(y, z64 * gate, err * gate.abs(), "y")
+            first = y, z
+        assert torch.equal(y, first[0]) and torch.equal(z, first[1]), f"run {i} differs"

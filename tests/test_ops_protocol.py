@@ -1,0 +1,119 @@
+"""Models of the product kernel's mbarrier protocols on the CPU: every role is
+a coroutine, a random scheduler interleaves them, copies land when it pleases.
+A barrier is the hardware's: a wait names a phase by its parity alone, so it
+passes whenever the phase before the current one has that parity.  Each
+protocol's earlier form is planted beside the kernel's and must be caught."""
+import random
+
+import pytest
+
+
+class Bar:
+    """An mbarrier: arrivals and copies outstanding in the current phase."""
+
+    def __init__(self, count):
+        self.count, self.phase, self.left, self.tx = count, 0, count, 0
+
+    def _flip(self):
+        if self.left == 0 and self.tx == 0:
+            self.phase, self.left = self.phase + 1, self.count
+
+    def arrive(self, copies=0):
+        assert self.left > 0, "more arrivals than a phase takes"
+        self.left, self.tx = self.left - 1, self.tx + copies
+        self._flip()
+
+    def land(self):
+        self.tx -= 1
+        self._flip()
+
+    def passed(self, parity):
+        return (self.phase & 1) != parity
+
+
+def run(rng, roles, idle=()):
+    """Steps the roles in random order until all but the `idle` ones (copy
+    engines) have ended.  A role yields None (a step) or a condition to wait
+    for.  Now and then a role is left aside for long.  True: all ended."""
+    waits = {n: None for n in roles}
+    lazy = {n: rng.choice((1.0, 1.0, 0.02)) for n in roles}
+    while any(n not in idle for n in roles):
+        ready = [n for n in roles if waits[n] is None or waits[n]()]
+        if not ready:
+            return False
+        n = rng.choices(ready, [lazy[i] for i in ready])[0]
+        try:
+            waits[n] = next(roles[n])
+        except StopIteration:
+            del roles[n]
+    return True
+
+
+# ------------------------------------------------- fp32 boxes of 32 columns --
+def boxes(rng, chunks, ring, everyone):
+    """Chunks of 32 columns with a side operand: even chunks of a tile are one
+    set of warps' work, odd ones the other's.  everyone: all warps pass every
+    phase (wait and arrive); else only a chunk's own set does, as both did
+    before.  Returns None, or what went wrong."""
+    warps = 2                                     # of a set
+    full = [Bar(1) for _ in range(ring)]
+    done = [Bar(2 * warps if everyone else warps) for _ in range(ring)]
+    slot, wrong, flight = [None] * ring, [], []   # slot: what the memory holds
+    order = [c for tile in chunks for c in range(tile)]
+
+    def traffic():
+        at = 0
+        for i in range(len(order)):
+            while at < len(order) and at - i < ring:
+                full[at % ring].arrive(1)
+                flight.append(at)
+                at += 1
+                yield None
+            yield lambda: done[i % ring].passed(i // ring & 1)
+            if slot[i % ring] != ("done", i, warps):
+                wrong.append(f"stored {slot[i % ring]} as chunk {i}")
+            yield None
+
+    def engine():                                 # loads land in any order
+        while True:
+            yield lambda: bool(flight)
+            i = flight.pop(rng.randrange(len(flight)))
+            slot[i % ring] = ("loaded", i, 0)
+            full[i % ring].land()
+
+    def warp(set_):
+        for i, c in enumerate(order):
+            mine = c & 1 == set_
+            if not mine and not everyone:
+                continue
+            yield lambda: full[i % ring].passed(i // ring & 1)
+            if mine:
+                state, j, n = slot[i % ring] or ("empty", i, 0)
+                if j != i or state == "empty":
+                    wrong.append(f"chunk {i} worked on {slot[i % ring]}")
+                slot[i % ring] = ("done", i, n + 1)
+                yield None
+            done[i % ring].arrive()
+
+    roles = {"traffic": traffic(), "engine": engine()}
+    for s in (0, 1):
+        for w in range(warps):
+            roles[f"set {s} warp {w}"] = warp(s)
+    try:
+        if not run(rng, roles, idle=("engine",)) and not wrong:
+            wrong.append("nothing can go on")
+    except AssertionError as e:
+        wrong.append(str(e))
+    return wrong[0] if wrong else None
+
+
+@pytest.mark.parametrize("chunks,ring", [((8,), 3), ((8, 8, 8), 3), ((4,) * 6, 3), ((8, 7, 8, 7), 2),
+                                         ((7, 7, 7), 3), ((1, 1, 3, 8), 2)])
+def test_boxes_of_half_the_warps(chunks, ring):
+    for seed in range(300):
+        assert boxes(random.Random(seed), chunks, ring, True) is None, seed
+
+
+@pytest.mark.parametrize("chunks,ring", [((8,), 3), ((8, 7, 8, 7), 2)])
+def test_boxes_whose_other_warps_skip_are_caught(chunks, ring):
+    assert any(boxes(random.Random(s), chunks, ring, False) for s in range(300))

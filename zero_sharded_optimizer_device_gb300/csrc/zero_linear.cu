@@ -1098,8 +1098,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
     if (BOX)
       for (int b = 0; b < g.boxes; ++b) {
         bar_init(efull + 8 * b, 1);
-        // 64 columns are shared by all sets of epilogue warps, 32 by half
-        bar_init(edone + 8 * b, kWidth == 64 ? kEpiWarps : kEpiWarps / 2);
+        bar_init(edone + 8 * b, kEpiWarps);
       }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -1421,12 +1420,19 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
             eb = 0;
             eph ^= 1;
           }
-          if (kWidth == 32 && (cc & 1) != set >> 1) continue;
-          const int piece = kWidth == 64 ? 4 * cc + set : 2 * cc + (set & 1);
-          const int unit = kWidth == 64 ? 2 * set : 2 * (set & 1);  // of a bf16 row
+          // 64 columns are shared by all sets of epilogue warps, 32 by half.  The
+          // other half passes the chunk's phases too: a wait names its phase
+          // by parity alone, and one who skipped a phase of a slot would take
+          // the phase before it for the one after.
           ok = bar_wait(efull + 8 * b, bph, &dead);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
+          if (kWidth == 32 && (cc & 1) != set >> 1) {
+            if (lane == 0) bar_arrive(edone + 8 * b);
+            continue;
+          }
+          const int piece = kWidth == 64 ? 4 * cc + set : 2 * cc + (set & 1);
+          const int unit = kWidth == 64 ? 2 * set : 2 * (set & 1);  // of a bf16 row
           float v[kPiece];
           piece_sums(piece, v);
           box_piece<MODE, FORM>(be, masks.at(piece >> 2), boxes0 + b * chunk_bytes, second,
