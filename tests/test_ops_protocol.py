@@ -117,3 +117,65 @@ def test_boxes_of_half_the_warps(chunks, ring):
 @pytest.mark.parametrize("chunks,ring", [((8,), 3), ((8, 7, 8, 7), 2)])
 def test_boxes_whose_other_warps_skip_are_caught(chunks, ring):
     assert any(boxes(random.Random(s), chunks, ring, False) for s in range(300))
+
+
+# ------------------------------- a pair of CTAs whose shifting warps fill a ring --
+def pair(rng, steps, stages, idle_walks):
+    """Both operands are shifted: each CTA's shifting warps write a stage, the
+    first CTA's tensor cores read both parts and free it in both.  idle_walks: the second CTA's loading warp, which has
+    nothing to load, still waits for every stage, as it did before."""
+    warps = 2
+    full = [Bar(1 + 2 * warps) for _ in range(stages)]
+    empty, empty2 = [Bar(1) for _ in range(stages)], [Bar(1) for _ in range(stages)]
+    part = [[None] * stages for _ in range(2 * warps)]
+    wrong = []
+
+    def walk():
+        for i in range(steps):
+            yield i, i % stages, i // stages & 1
+
+    def loads(cta):
+        for i, s, ph in walk():
+            if cta == 0 or idle_walks:
+                yield lambda: (empty if cta == 0 else empty2)[s].passed(ph ^ 1)
+            if cta == 0:
+                full[s].arrive()
+
+    def shifts(cta, w):
+        for i, s, ph in walk():
+            yield lambda: (empty if cta == 0 else empty2)[s].passed(ph ^ 1)
+            part[cta * warps + w][s] = i
+            yield None
+            full[s].arrive()
+
+    def tensor():
+        for i, s, ph in walk():
+            yield lambda: full[s].passed(ph)
+            if any(p[s] != i for p in part):
+                wrong.append(f"step {i} read {[p[s] for p in part]}")
+            for e in (empty, empty2):
+                yield None
+                e[s].arrive()
+
+    roles = {"tensor": tensor(), "loads 0": loads(0), "loads 1": loads(1)}
+    for c in (0, 1):
+        for w in range(warps):
+            roles[f"shift {c} {w}"] = shifts(c, w)
+    try:
+        if not run(rng, roles):
+            wrong.append("waits without end: " + ", ".join(roles))
+    except AssertionError as e:
+        wrong.append(str(e))
+    return wrong[0] if wrong else None
+
+
+@pytest.mark.parametrize("steps,stages", [(1, 3), (12, 3), (13, 4), (40, 3)])
+def test_pair_of_shifting_ctas(steps, stages):
+    for seed in range(300):
+        assert pair(random.Random(seed), steps, stages, False) is None, seed
+
+
+def test_pair_whose_idle_loader_walks_is_caught():
+    """It can fall two phases behind and wait for one that never comes."""
+    bad = [pair(random.Random(s), 12, 3, True) for s in range(2000)]
+    assert any(b and "waits without end: loads 1" in b for b in bad)

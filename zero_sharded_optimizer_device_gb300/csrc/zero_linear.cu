@@ -1171,6 +1171,10 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
       const int j0 = tj * bn + (int)half * (bn / 2);
       const bool load_a = tj < 0 && bias_b ? tma_b : tma_a;
       const bool load_b = tma_b && tj >= 0;
+      // The second CTA's warp stops where it has nothing to load (and so
+      // nothing in the tiles after it): no stage waits for it there, so it
+      // could fall two phases behind and wait for one that never comes.
+      if (half != 0 && !load_a && !load_b) break;
       const CUtensorMap* map_i = tj < 0 && bias_b ? &map_b : &map_a;
       const uint32_t bytes = 2 * ((load_a ? kBytesA : 0) + (load_b ? b_bytes : 0));
       for (int kb = kb0; kb < kb1; ++kb) {
