@@ -100,3 +100,58 @@ def test_fp32_boxes_with_a_gate_and_kept_inputs(cuda, Z, flush, m, n, k):
             within(y, z64 * gate, err * gate.abs(), "y")
             first = y, z
         assert torch.equal(y, first[0]) and torch.equal(z, first[1]), f"run {i} differs"
+
+
+# both operands off 16-byte boundaries, either one, rows along and across the contraction
+SHIFTED = [(700, 1000, 1601, 1, 1), (700, 1000, 1600, 1, 0), (700, 1000, 1600, 0, 1),
+           (2500, 3000, 515, 3, 5), (90, 520, 4099, 1, 1)]
+
+
+@pytest.mark.parametrize("kn", [False, True], ids=["nk", "kn"])
+@pytest.mark.parametrize("m,n,k,pad_x,pad_w", SHIFTED)
+def test_shifted_operands_with_a_cold_cache(cuda, Z, flush, m, n, k, pad_x, pad_w, kn):
+    """A pair's second CTA shifts its part of a stage into place and the first
+    one's tensor-core instructions read it: every stage must have arrived."""
+    x = rnd(1, m, k + pad_x)[:, :k]
+    w = rnd(2, *((k, n + pad_w) if kn else (n, k + pad_w)), scale=k ** -0.5)[:, :n if kn else k]
+    want, err = product_bound(x, w.T if kn else w, 0)
+    first = None
+    for i in range(6):
+        y = torch.full((m, n), -7.0, device="cuda")
+        flush(i)
+        Z.zero_linear(x, x.stride(0), w, w.stride(0), Z.ZERO_W_KN if kn else Z.ZERO_W_NK, m, n, k,
+                      None, y, n, Z.ZERO_F32)
+        if first is None:
+            within(y, want, err, "y")
+            first = y
+        assert torch.equal(y, first), f"run {i} differs"
+
+
+def test_products_side_by_side_on_two_streams(cuda, Z):
+    """Calls that share the GPU and come in any order give the bits that each
+    gives alone: aligned and shifted operands, split contractions, few rows."""
+    sizes = [(2048, 2048, 1024, 0), (700, 1000, 1601, 1), (96, 512, 4096, 0), (5, 2048, 2048, 0),
+             (1500, 777, 333, 3), (3000, 2056, 520, 0)]
+    calls = []
+    for i, (m, n, k, pad) in enumerate(sizes):
+        x, w = rnd(i, m, k + pad)[:, :k], rnd(i + 50, n, k + pad, scale=k ** -0.5)[:, :k]
+
+        def call(y, x=x, w=w, m=m, n=n, k=k):
+            Z.zero_linear(x, x.stride(0), w, w.stride(0), Z.ZERO_W_NK, m, n, k, None, y, n, Z.ZERO_F32)
+        alone = torch.empty(m, n, device="cuda")
+        call(alone)
+        calls.append((call, alone))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = []
+    for s, order in zip(streams, (calls, calls[::-1])):
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            for _ in range(4):
+                for call, alone in order:
+                    y = torch.full_like(alone, -7.0)
+                    call(y)
+                    outs.append((y, alone))
+    torch.cuda.synchronize()
+    for y, alone in outs:
+        assert torch.equal(y, alone)
