@@ -179,3 +179,32 @@ def test_pair_whose_idle_loader_walks_is_caught():
     """It can fall two phases behind and wait for one that never comes."""
     bad = [pair(random.Random(s), 12, 3, True) for s in range(2000)]
     assert any(b and "waits without end: loads 1" in b for b in bad)
+
+
+# ------------------------------------ the loads in flight when a wait gives up --
+def drained_too_soon(stages, steps, gave, parity_of):
+    """The walk of `steps` stages gave up before step `gave`; the last load of
+    every slot is in flight.  Slots whose wait would not stop for it."""
+    full = [Bar(1) for _ in range(stages)]
+    flight = set()
+    for i in range(gave):
+        if i % stages in flight:
+            full[i % stages].land()          # the tensor cores have taken it
+        full[i % stages].arrive(1)
+        flight.add(i % stages)
+    return [q for q in range(stages) if full[q].passed(parity_of(q, gave, steps, stages)) != (q not in flight)]
+
+
+def where_it_stopped(q, gave, steps, stages):
+    s, ph = gave % stages, gave // stages & 1
+    return ph if q < s else ph ^ 1
+
+
+def where_the_walk_ends(q, gave, steps, stages):     # as it was before
+    return steps // stages & 1
+
+
+def test_drain_waits_for_every_load_in_flight():
+    cases = [(st, n, g) for st in (3, 4, 9) for n in range(1, 30) for g in range(n)]
+    assert not any(drained_too_soon(*c, where_it_stopped) for c in cases)
+    assert any(drained_too_soon(*c, where_the_walk_ends) for c in cases)

@@ -1180,7 +1180,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
     const uint32_t stages = g.stages, b_bytes = (uint32_t)g.bn * kDeep;
     const int bn = g.bn, blocks_b = bn / 128;
     const bool tma_a = g.gen_a == 0, tma_b = g.gen_b == 0, bias_b = g.bias_b;
-    uint32_t s = 0, ph = 0;
+    uint32_t s = 0, ph = 0, end_s = 0, end_ph = 0;  // end: where a wait gave up
     bool live = true;
     for (int t = first; t < tiles; t += clusters) {
       int ti, tj;
@@ -1196,7 +1196,11 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
       const CUtensorMap* map_i = tj < 0 && bias_b ? &map_b : &map_a;
       const uint32_t bytes = 2 * ((load_a ? kBytesA : 0) + (load_b ? b_bytes : 0));
       for (int kb = kb0; kb < kb1; ++kb) {
-        live = live && bar_wait(empty + 8 * s, ph ^ 1, &dead);
+        if (live) {
+          live = bar_wait(empty + 8 * s, ph ^ 1, &dead);
+          end_s = s;
+          end_ph = ph;
+        }
         const uint32_t a_at = ring + s * stage_bytes, b_at = a_at + kBytesA;
         const uint32_t bar = full_lead + 8 * s;
         const int c = kb * kDeep;
@@ -1227,11 +1231,13 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
       }
     }
     // a wait gave up: let the loads in flight land before the CTAs return
-    // (a ring slot holds at most one load; waits are again limited)
+    // (a ring slot holds at most one load, those from end_s on the lap before's;
+    // waits are again limited)
     if (!live && half == 0)
       for (uint32_t q = 0; q < stages; ++q) {
+        const uint32_t parity = q < end_s ? end_ph : end_ph ^ 1;
         const long long t0 = clock64();
-        while (!bar_try(full + 8 * q, ph) && clock64() - t0 < kWaitCycles / 8) {
+        while (!bar_try(full + 8 * q, parity) && clock64() - t0 < kWaitCycles / 8) {
         }
       }
     __syncwarp();
