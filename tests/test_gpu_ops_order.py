@@ -155,3 +155,81 @@ def test_products_side_by_side_on_two_streams(cuda, Z):
     torch.cuda.synchronize()
     for y, alone in outs:
         assert torch.equal(y, alone)
+
+
+def layer_plan(Z, width, layers, ranks):
+    """A plan of `layers` groups (norm weight, norm bias, product) and a way
+    to give every owner its shard of a flat buffer."""
+    sizes = [width, width, width * width]
+    plan = Z.zero_plan(sizes * layers, ranks, 16, [ell for ell in range(layers) for _ in sizes])
+    info, groups = Z.zero_plan_info(plan), [Z.zero_plan_group(plan, ell) for ell in range(layers)]
+    shards = [torch.zeros(info["shard_total"], dtype=BF, device="cuda") for _ in range(ranks)]
+
+    def give(full):
+        for g in groups:
+            for r in range(ranks):
+                at = g["flat_off"] + r * g["shard"]
+                shards[r][g["rank_off"]:g["rank_off"] + g["shard"]] = full[at:at + g["shard"]]
+    return plan, info, groups, shards, give
+
+
+@pytest.mark.parametrize("width", [256, 1000])
+def test_gathers_and_their_readers_on_one_buffer_in_a_graph(cuda, Z, width):
+    """Gather, norm, product, gather, norm, product on ONE layer buffer, in a
+    replayed graph and straight on the stream: every reader starts while the
+    gather before it still writes, and must see that gather's values; the
+    next gather must not overtake a reader.  Between replays the shards
+    change."""
+    layers, ranks, m = 4, 3, 96
+    plan, info, groups, shards, give = layer_plan(Z, width, layers, ranks)
+    layer = torch.zeros(max(g["psi_pad"] for g in groups), dtype=BF, device="cuda")
+    x = rnd(1, m, width)
+    u = [torch.empty(m, width, dtype=BF, device="cuda") for _ in range(layers)]
+    y = [torch.empty(m, width, device="cuda") for _ in range(layers)]
+    du, dw = torch.empty_like(u[0]), torch.empty(layers, width, device="cuda")
+    rstd = torch.empty(m, device="cuda")
+    size = Z.zero_layer_norm_workspace(m, width)
+    work = torch.empty(size, dtype=torch.uint8, device="cuda")
+    dx = [torch.empty(m, width, device="cuda") for _ in range(layers)]
+    parts = lambda f: (f[:width], f[width:2 * width], f[2 * width:2 * width + width ** 2].view(width, width))  # noqa: E731
+
+    def step():
+        for ell in range(layers):
+            Z.zero_gather_layer(plan, ell, shards, Z.ZERO_BF16, layer)
+            nw, nb, w = parts(layer)
+            Z.zero_layer_norm(x, width, 1, nw, nb, 1, m, width, Z.ZERO_NORM_RMS, 1e-5, u[ell], width, 1,
+                              None, rstd)
+            Z.zero_linear(u[ell], width, w, width, Z.ZERO_W_NK, m, width, width, None, y[ell], width,
+                          Z.ZERO_F32)
+            Z.zero_layer_norm_backward(u[ell], width, 1, x, width, 1, nw, 1, None, rstd, m, width,
+                                       Z.ZERO_NORM_RMS, None, 0, dx[ell], width, 0, dw[ell], None, 0,
+                                       False, work, size)
+
+    def check(full):
+        for ell, g in enumerate(groups):
+            nw, nb, w = parts(full[g["flat_off"]:])
+            r = (x.double().square().mean(1, keepdim=True) + 1e-5).rsqrt()
+            h = x.double() * r
+            want = h * nw.double() + nb.double()
+            rel = lambda a, b: ((a.double() - b).norm() / b.norm()).item()  # noqa: E731
+            assert rel(u[ell], want) < R.U16
+            got = u[ell].double()
+            assert rel(y[ell], got @ w.double().T) < 1e-5
+            gw = got * nw.double()
+            assert rel(dx[ell], r * (gw - h * (gw * h).mean(1, keepdim=True))) < 1e-4
+            assert rel(dw[ell], (got * h).sum(0)) < 1e-4
+
+    full = rnd(5, info["psi_pad"])
+    give(full)
+    step()
+    check(full)
+    graph, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=s):
+        step()
+    for i in range(5):
+        full = rnd(10 + i, info["psi_pad"])
+        give(full)
+        graph.replay()
+        if i % 2:
+            graph.replay()           # back to back: the first gather follows the last reader
+        check(full)

@@ -155,7 +155,16 @@ struct RowVec<true, 1> {
   __device__ __forceinline__ void get(const Mat& m, float f[8]) const { from_raw(m, r, f); }
 };
 
-// 8 parameters: every row reads them again, from L1.
+__device__ __forceinline__ uint4 param16(const void* p) {
+  uint4 u;
+  asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+               : "l"(p));
+  return u;
+}
+// 8 parameters, kept in registers for all rows.  Coherent loads: a gather may
+// write them while this kernel is already resident, waiting for it.  (Read
+// again for every row, from L1, fp32 rows of 4096 take 75 us instead of 65.)
 template <int S>
 __device__ __forceinline__ void param8(const Mat& p, int64_t col, int valid, int64_t n,
                                        float f[8]) {
@@ -170,12 +179,13 @@ __device__ __forceinline__ void param8(const Mat& p, int64_t col, int valid, int
   if (!in_extent(col, col + valid, 0, n, kSite)) valid = 0;
   if (p.vec && valid == 8) {
     if (p.dtype == ZERO_F32) {
-      const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p.p) + col);
-      const float4 u = __ldg(q), v = __ldg(q + 1);
-      f[0] = u.x; f[1] = u.y; f[2] = u.z; f[3] = u.w;
-      f[4] = v.x; f[5] = v.y; f[6] = v.z; f[7] = v.w;
+      const float* q = static_cast<const float*>(p.p) + col;
+      Raw8 r;
+      r.a = param16(q);
+      r.b = param16(q + 4);
+      from_raw(p, r, f);
     } else {
-      from_bf16(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.p) + col)), f);
+      from_bf16(param16(static_cast<const uint16_t*>(p.p) + col), f);
     }
   } else {
 #pragma unroll
