@@ -196,18 +196,28 @@ constexpr float kGeluA = 1.5957691216057308f;  // 2 sqrt(2/pi)
 constexpr float kGeluB = 0.044715f;
 constexpr float kRsqrt2Pi = 0.39894228040143268f;
 
-// The normal distribution's mass below z, and e = exp(-z^2 / 2), by formula
-// 7.1.26 of Abramowitz and Stegun (Hastings 1955; |error| < 7.5e-8 here): with
-// t = 1 / (1 + p |z| / sqrt 2) the mass beyond |z| is t (a1 + ... + a5 t^4) e / 2.
-// No branch, and the exponential serves the slope too (erff: a division into
-// cases and three times the code).
+// The normal distribution's mass below z, and e = exp(-z^2 / 2).  With x = |z| /
+// sqrt 2 the mass beyond |z| is erfc(x) / 2 = t Q(t) e for t = 1 / (1 + 0.33 x),
+// the form of Hastings' approximations (1955).  Q has degree 7 and was fitted
+// here, by weighted least squares, to erfc(x) exp(x^2) for x up to 9.6 with
+// relative error 8e-8: the mass keeps small *relative* error in the negative
+// tail, where GELU is z times it.  In fp32 12 + z^2 ulps at most by the steps'
+// own bounds; measured 4 near 0, 13 down to -8, 27 down to -12.5, where half an
+// ulp of z alone is z^2 / 2 of them.  (Five terms took 60 us instead of 65 for
+// 8192 x 1024 to 4096 with bias and kept z, and were 5e-4 off at -4.)
+// No branch, and the exponential serves the slope too.
 __device__ __forceinline__ float normal_mass(float z, float& e) {
-  const float t = __fdividef(1.0f, 1.0f + 0.3275911f * 0.70710678f * fabsf(z));
+  const float t = __fdividef(1.0f, 1.0f + 0.233345238f * fabsf(z));
   e = __expf(-0.5f * z * z);
-  const float p = t * (0.127414796f +
-                       t * (-0.142248368f +
-                            t * (0.7107068705f + t * (-0.7265760135f + t * 0.5307027145f))));
-  const float tail = p * e;
+  float q = -0.0679643974f;
+  q = q * t + 0.231344119f;
+  q = q * t - 0.177719474f;
+  q = q * t + 0.206270799f;
+  q = q * t + 0.0225053225f;
+  q = q * t + 0.100961916f;
+  q = q * t + 0.0914186239f;
+  q = q * t + 0.0931830555f;
+  const float tail = q * t * e;
   return z < 0.0f ? tail : 1.0f - tail;
 }
 
