@@ -115,3 +115,15 @@ def test_slopes_in_relative_terms(cuda, Z, act, lo, rows):
     z = every_bf16(lo, 100.0)
     _, s, _, es = formulas(z, act)
     check(z, slopes(Z, z, act, rows), s, es, act + "'")
+
+
+@pytest.mark.parametrize("act", [a for a, _ in RANGES])
+def test_values_and_slopes_of_huge_inputs(cuda, Z, act):
+    """Up to bf16's largest finite value: z itself and a slope of 1 on one
+    side, 0 and 0 on the other."""
+    z = torch.cat([every_bf16(-3.4e38, -200.0), every_bf16(200.0, 3.4e38)])
+    up = (z > 0).float()
+    for few in (True, False):
+        assert torch.equal(values(Z, z, act, few).abs(), z.float() * up)
+    for rows in (1, 300):
+        assert torch.equal(slopes(Z, z, act, rows).abs(), up)

@@ -273,7 +273,9 @@ __device__ __forceinline__ void activate_grad(float value[N], float slope[N], in
     case ZERO_ACT_GELU_TANH:
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        const float z = value[j], q = z * z;
+        // s is 0 or 1 long before the cap, under which the factor of its slope
+        // stays finite
+        const float z = value[j], q = fminf(z * z, 1e30f);
         const float s = logistic(z * (kGeluA + kGeluA * kGeluB * q));
         value[j] = z * s;
         slope[j] = s + value[j] * (1.0f - s) * (kGeluA + 3.0f * kGeluA * kGeluB * q);
