@@ -644,7 +644,10 @@ int zero_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, int32_t 
  * W^T with dy bf16 [m, n] and W bf16 [k -> n] in `w_layout`; dx = da, or with
  * `ag` (not NULL) through the activation that made the input:
  * dx = da * act'(pre) * gate and dgate = da * act(pre).  dx [m, k] in dxdtype.
- * act'(0) of RELU is 0.  n = 0 gives da = 0.  Errors as zero_linear. */
+ * act'(0) of RELU is 0.  n = 0 gives da = 0.  Where an input feeds two
+ * products (Llama's gate and up), the second branch's gradient is added by
+ * zero_linear: x its dy, the weight in its other layout, n and k exchanged,
+ * and the first branch's dx as both residual and y.  Errors as zero_linear. */
 int zero_linear_dinput(const void* dy, int64_t lddy, const void* w, int64_t ldw,
                        int32_t w_layout, int64_t m, int64_t n, int64_t k,
                        const zero_act_grad_t* ag, void* dx, int64_t lddx, zero_dtype_t dxdtype,
