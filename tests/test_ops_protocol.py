@@ -208,3 +208,37 @@ def test_drain_waits_for_every_load_in_flight():
     cases = [(st, n, g) for st in (3, 4, 9) for n in range(1, 30) for g in range(n)]
     assert not any(drained_too_soon(*c, where_it_stopped) for c in cases)
     assert any(drained_too_soon(*c, where_the_walk_ends) for c in cases)
+
+
+# ------------------------------------------ a warp's lanes when a wait gives up --
+def lanes_leave(rng, vote, lanes=4, steps=6):
+    """Each lane waits for itself, and one may give up at the moment at which
+    the barrier completes for another; the loop holds a step that all lanes
+    take together.  vote: they agree on going on.  True: all lanes ended."""
+    fails = rng.randrange(steps)
+    gives_up = [rng.random() < 0.5 for _ in range(lanes)]
+    met, votes = [0] * lanes, [[] for _ in range(lanes)]
+
+    def together(i):
+        met[i] += 1
+        want = met[i]
+        return lambda: all(m >= want for m in met)
+
+    def lane(i):
+        for s in range(steps):
+            live = not (s == fails and gives_up[i])
+            if vote:
+                votes[i].append(live)
+                yield lambda: all(len(v) > s for v in votes)
+                live = all(v[s] for v in votes)
+            yield together(i)             # a store issued by one elected lane
+            if not live:
+                return
+            yield together(i)             # the next load's
+
+    return run(rng, {i: lane(i) for i in range(lanes)})
+
+
+def test_lanes_give_up_together():
+    assert all(lanes_leave(random.Random(s), True) for s in range(200))
+    assert not all(lanes_leave(random.Random(s), False) for s in range(200))

@@ -809,6 +809,7 @@ __device__ __forceinline__ void box_traffic(const BoxMaps& maps, const ProductK&
       next_chunk<W>(g, cols, split, tiles, step, in);
     }
     live = live && bar_wait(edone + 8 * sb, sph, dead);
+    live = __all_sync(0xffffffffu, live);  // the lanes leave together
     const uint32_t at = boxes + sb * chunk_bytes, slot1 = at + second;
     const int x = out.tj * bn + out.cc * W, y = out.ti * 256 + (int)half * kRowsCta;
     if (elect() && live) {
