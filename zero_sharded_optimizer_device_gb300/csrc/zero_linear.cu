@@ -353,7 +353,7 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr, bool contig) {
 // tile to a raw buffer some steps ahead; a GEN warp writes the lines of one
 // map, shifted by their one distance, to the operand's swizzled tile.  Lines
 // and elements outside the matrix arrive as zeros.  (3873 x 1614 by 9592 x 1614,
-// odd rows: 194 us; by 16-byte asynchronous copies, a line's words in one
+// odd rows: 195 us; by 16-byte asynchronous copies, a line's words in one
 // thread, 536; by plain loads into registers 877; by 2-byte loads 2181.)
 // ---------------------------------------------------------------------------
 constexpr int kRawLine = 9 * 16;
@@ -1797,12 +1797,19 @@ static cudaError_t launch_mode(const ProductK& in, cudaStream_t st) {
   // at 128 8.8 / 16.6; four parts, clusters of 8, always lost.)  Lines off
   // 16-byte boundaries bound a step by shifting them: 870 cycles for 144 of
   // them, 1040 for 192, 1430 for 256.
-  // The tensor cores add to their sums without rounding to nearest, so a long
-  // contraction loses digits: 7e-7 of the result after 768 terms, 7e-6 after
-  // 6000 (in units of its size).  fp32 results therefore take the sums out
-  // every `round` steps and add them in fp32 proper, in a third set of tensor
-  // memory, where three fit (BN = 128) while the products go on; bf16 results
-  // only where that loss would reach their own rounding.
+  // The tensor cores add to their fp32 sums without rounding to nearest, so a
+  // long contraction loses digits: 7e-7 of the result after 768 terms, 7e-6
+  // after 6000 (in 2-norms).  fp32 results therefore take the sums out every
+  // `round` steps and add them to nearest, in a third set of tensor memory,
+  // where three fit (BN = 128) while the products go on.  Rounds of 12 steps
+  // keep any fp32 result at about 7e-7, which sums to nearest throughout reach
+  // at 6000 terms (2e-7 at 768).  (Rounds of 4, 8, 12, 16, 24 steps: weight
+  // gradient 2048 x 2048 of 6001 rows 57, 42, 39, 38, 36.5 us and 2.5, 4.7,
+  // 7.2, 9.8, 15e-7; 2048 x 1024 to 4096 28, 24, 24, 19, 19 us and 2.3, 4.7,
+  // 6.4, 10, 10e-7; 2048 x 640 to 4096, one round from 12 on, 22.5, 20, 17.5
+  // us and 2.1, 4.3, 6.0e-7.)  bf16 results take them out only where the loss
+  // would come near their own rounding, from 32768 terms on: 4e-5 (6e-5 where
+  // all terms have one sign) against 2e-3.
   const bool f32 = k.epi.out.dtype == ZERO_F32 || (k.dbias.p && k.dbias.dtype == ZERO_F32);
   const bool exact = f32 ? kblocks > kRound : kblocks > 512;
   g.bias_b = k.dbias.p && k.bias_b;
@@ -1899,8 +1906,10 @@ static cudaError_t launch_mode(const ProductK& in, cudaStream_t st) {
   g.two_slots = MODE == LIN_FORWARD ? o.gate.p || o.pre.p
                 : MODE == LIN_DINPUT ? o.gate.p || (wide && o.pre.p)
                                      : 0;
-  // Two chunks in flight where they are two boxes each: the operands' ring
-  // then keeps 5 stages (gate 4096-11008: 225 us against 252 at 3 and 4).
+  // Two chunks in flight where they are two boxes each: at BN = 256 the
+  // operands' ring then keeps 5 stages (gate 4096-11008: 225 us against 252 at
+  // 3 and 4), or 4 beside the biases' 4 KiB (8192 x 1024 to 4096 with GELU and
+  // kept z: 56.3 us with a bias, 52.5 without).
   g.boxes = g.two_slots ? 2 : kMostBoxes;
   if (wide) return launch_tiles<MODE, BOX_F32>(ma, mb, maps, k, g, st);
   return launch_tiles<MODE, BOX_BF16>(ma, mb, maps, k, g, st);

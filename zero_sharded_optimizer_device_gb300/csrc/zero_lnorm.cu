@@ -13,7 +13,9 @@
 namespace zk {
 
 constexpr int kSite = ZERO_SITE_LNORM;
-constexpr int64_t kNormPartials = 456;  // most blocks of the backward pass: 3 per SM
+// Most blocks of the backward pass: 3 on each of this GPU's 152 SMs.  Fixed, so
+// that a workspace's size depends on its matrix alone.
+constexpr int64_t kNormPartials = 456;
 
 int64_t norm_partials(int64_t m) { return m < kNormPartials ? m : kNormPartials; }
 

@@ -344,9 +344,11 @@ static cudaError_t launch_vec(const ProductK& k, cudaStream_t st) {
                        dim3(kWarps * 32), st, k, share);
   }
   const int64_t blocks = (k.cols + kAcross - 1) / kAcross;
-  // one row: 32 warps instead of a cluster where all is one batch of loads each
-  // (4096 x 1024: 4.1 us, 6.7 in clusters; two batches each, 768 x 1536: 4.9
-  // and 4.2)
+  // one row: 32 warps instead of a cluster while one CTA's share of loads is
+  // small.  (us with 32 warps / in clusters: 4096 outputs of 520 to 1016 3.6 to
+  // 3.9 / 6.7 to 7.2, of 1024 3.9 / 6.4; 1024 outputs of 520 to 1024 3.5 to 3.8 /
+  // 3.8 to 4.0; 264 outputs of 520 to 1024 3.6 to 3.9 / 3.6 to 3.8.  Past 1024
+  // A's row takes shared memory twice: 768 outputs of 1536 4.9 / 4.2.)
   constexpr int kMany = M == 1 && VEC == 8 ? 32 : kWarps;
   const bool many =
       kMany > kWarps && k.depth > 512 && k.depth <= 1024 && blocks <= sm_count();
