@@ -233,3 +233,43 @@ def test_gathers_and_their_readers_on_one_buffer_in_a_graph(cuda, Z, width):
         if i % 2:
             graph.replay()           # back to back: the first gather follows the last reader
         check(full)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("m,width", [(64, 512), (3000, 1024)])
+def test_norms_between_gathers(cuda, Z, m, width, dtype):
+    """Gather, norm, gather, norm on one buffer and nothing between: a norm is
+    resident while the one before it still reads the buffer's former values,
+    and must not find those in its caches."""
+    layers, ranks = 6, 2
+    plan = Z.zero_plan([width, width] * layers, ranks, 16, [ell for ell in range(layers) for _ in range(2)])
+    info, groups = Z.zero_plan_info(plan), [Z.zero_plan_group(plan, ell) for ell in range(layers)]
+    code = Z.ZERO_BF16 if dtype == BF else Z.ZERO_F32
+    shards = [torch.zeros(info["shard_total"], dtype=dtype, device="cuda") for _ in range(ranks)]
+    layer = torch.zeros(max(g["psi_pad"] for g in groups), dtype=dtype, device="cuda")
+    x = torch.ones(m, width, dtype=BF, device="cuda")          # normalises to 1: y = weight + bias
+    x[:, 1::2] = -1
+    y = [torch.empty(m, width, device="cuda") for _ in range(layers)]
+
+    def step():
+        for ell in range(layers):
+            Z.zero_gather_layer(plan, ell, shards, code, layer)
+            Z.zero_layer_norm(x, width, 1, layer[:width], layer[width:2 * width], code, m, width,
+                              Z.ZERO_NORM_RMS, 0.0, y[ell], width, Z.ZERO_F32)
+
+    step()
+    graph, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=s):
+        step()
+        step()
+    for i in range(20):
+        full = rnd(i, info["psi_pad"], dtype=dtype)
+        for g in groups:
+            for r in range(ranks):
+                at = g["flat_off"] + r * g["shard"]
+                shards[r][g["rank_off"]:g["rank_off"] + g["shard"]] = full[at:at + g["shard"]]
+        graph.replay()
+        for ell, g in enumerate(groups):
+            w, b = (full[g["flat_off"] + o:g["flat_off"] + o + width].float() for o in (0, width))
+            want = x.float() * w + b
+            assert (y[ell] - want).abs().max().item() <= 4 * R.U32 * 8, (i, ell)
