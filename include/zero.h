@@ -543,7 +543,8 @@ int zero_copy(void* dst, const void* src, int64_t bytes, zero_stream_t stream);
 
 /* zero_async_status: number of bounded waits inside the library's kernels
  * that gave up after about 2 s (the gathers' on a bulk copy, those between the
- * roles of zero_linear* products) on the current device since the last reset;
+ * roles of the products of zero_linear*, zero_fp4_linear* and
+ * zero_orthogonalize) on the current device since the last reset;
  * nonzero means a result is incomplete.  The call that launched the kernel
  * returned ZERO_OK; the kernel still returns (the context stays usable).  No
  * counterpart on the pages.  Synchronizes the device; reset != 0 clears the
@@ -728,6 +729,99 @@ int zero_layer_norm_backward(const void* dy, int64_t lddy, zero_dtype_t dydtype,
                              int32_t accumulate, void* workspace, int64_t workspace_bytes,
                              zero_stream_t stream);
 
+/* --------------------------------------------------- 4-bit layers (ops) --
+ * The layer's products on matrices in microscaled 4-bit numbers ["OCP
+ * Microscaling Formats (MX) Specification", v1.0 (2023), for MX], made from a
+ * gathered layer and its activations.  Conventions of the section above
+ * hold; in addition:
+ *   - An element is a code of E2M1 (sign, two exponent bits, one mantissa
+ *     bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6 for codes 0..7, their negatives for
+ *     8..15) times the scale of its block: consecutive elements of a row,
+ *       ZERO_FP4_MX  32 of them, scale 2^(floor(log2 amax) - 2), one byte
+ *                    E8M0 (2^(byte - 127), at least 2^-127; 255 is NaN);
+ *       ZERO_FP4_NV  16 of them, scale s g: s the E4M3 nearest to
+ *                    amax / (6 g) (at most 448; 127 is NaN), g the tensor's
+ *                    scale, one fp32 in device memory (NULL: 1), positive,
+ *                    2^-100 to 2^100
+ *     with amax the block's largest magnitude.  The code is the nearest (ties
+ *     to the even code, beyond 6 to 6) of x / scale (MX; exact) or of
+ *     fl(x fl(1 / fl(s g))) (NV; fl rounds to fp32).  A last block may be
+ *     short.  A block that holds a NaN or an infinity gets the scale NaN and
+ *     codes 0: all of it reads as NaN.  Where an NV block's s is 0, all of it is 0.
+ *   - A contraction runs along the rows of both operands, so that both have
+ *     their blocks along it: for y = x W^T quantise x [m, k] and W [n, k]
+ *     along k; for dx = dy W quantise dy [m, n] and W's transpose [k, n]
+ *     along n; for dw = dy^T x quantise the transposes [n, m] and [k, m]
+ *     along m.  zero_fp4_quantize writes either direction, or both in one read.
+ *     A weight kept as [k, n] (ZERO_W_KN) gives [n, k] as its transpose.
+ *   - Codes: two a byte, column 2j in the low four bits of byte j; rows `ld`
+ *     bytes apart, ld a multiple of 16; a row fills whole 16 bytes (columns
+ *     past the last are codes 0).
+ *   - Scales: tiles of 128 rows and 4 blocks of 512 bytes, the tiles of
+ *     consecutive blocks side by side, then the next 128 rows: block b of row
+ *     r lies at byte ((r / 128) ceil(B / 4) + b / 4) 512 + 16 (r % 32) +
+ *     4 (r % 128 / 32) + b % 4 of B blocks a row.  What a tile holds of rows
+ *     and blocks that do not exist is 0.
+ *   - Codes and scales lie on 16-byte boundaries (ZERO_EALIGN otherwise).
+ *     Buffers written elsewhere keep to the layout, zeros included. */
+#define ZERO_FP4_MX 0
+#define ZERO_FP4_NV 1
+
+typedef struct {
+  void* codes;
+  int64_t ld;                /* bytes between rows */
+  void* scales;
+  const float* tensor_scale; /* g (NV), or NULL; NULL for MX */
+} zero_fp4_t;
+
+/* zero_fp4_size: bytes that a row of codes fills (the least ld), and of all
+ * the scales, of a matrix [rows, cols].  Errors: EINVAL, ERANGE. */
+int zero_fp4_size(int64_t rows, int64_t cols, int32_t format, int64_t* row_bytes,
+                  int64_t* scale_bytes);
+
+/* zero_fp4_tensor_scale: *tensor_scale = fl(amax / 2688), amax the largest
+ * finite magnitude of x [rows, cols] (2688 = 6 * 448: the block that holds it
+ * then has the largest s), or 1 where there is none but 0.  workspace:
+ * ZERO_FP4_WORKSPACE bytes of 16-byte aligned device scratch.  Errors as
+ * zero_linear, and EINVAL (workspace too small). */
+#define ZERO_FP4_WORKSPACE 4096
+int zero_fp4_tensor_scale(const void* x, int64_t ldx, zero_dtype_t xdtype, int64_t rows,
+                          int64_t cols, float* tensor_scale, void* workspace,
+                          int64_t workspace_bytes, zero_stream_t stream);
+
+/* zero_fp4_quantize: x [rows, cols] to q [rows, cols], blocks along its rows,
+ * and to qt [cols, rows], blocks along its columns; one of them may be NULL.
+ * Given both, they name one tensor_scale.  Errors as zero_linear, and EINVAL
+ * (unknown format, both NULL, ld below a row, buffers of q, qt and x the same,
+ * a tensor_scale with MX, two tensor_scales). */
+int zero_fp4_quantize(const void* x, int64_t ldx, zero_dtype_t xdtype, int64_t rows,
+                      int64_t cols, int32_t format, const zero_fp4_t* q, const zero_fp4_t* qt,
+                      zero_stream_t stream);
+
+/* zero_fp4_dequantize: what q [rows, cols] stands for: fl(code d), d the MX
+ * scale or fl(s g), rounded to ydtype.  Errors as zero_fp4_quantize. */
+int zero_fp4_dequantize(const zero_fp4_t* q, int64_t rows, int64_t cols, int32_t format, void* y,
+                        int64_t ldy, zero_dtype_t ydtype, zero_stream_t stream);
+
+/* zero_fp4_linear, zero_fp4_linear_dinput, zero_fp4_linear_dweight: as
+ * zero_linear, zero_linear_dinput and zero_linear_dweight (without dbias),
+ * with the products' operands in 4 bits, both in `format`:
+ *   linear   x [m, k] and w [n, k]:   y  = epilogue(x w^T)
+ *   dinput   dy [m, n] and w [k, n]:  dx = (dy w^T) through `ag`
+ *   dweight  dy [n, m] and x [k, m]:  dw [n, k] (+)= dy x^T
+ * Products of codes and block scales are exact; they are added on the tensor
+ * cores as those of zero_linear are, 64 at a time, and the sum is multiplied by
+ * fl(g_a g_b) before what follows.  Errors as theirs and zero_fp4_quantize's. */
+int zero_fp4_linear(const zero_fp4_t* x, const zero_fp4_t* w, int32_t format, int64_t m,
+                    int64_t n, int64_t k, const zero_linear_epilogue_t* ep, void* y, int64_t ldy,
+                    zero_dtype_t ydtype, zero_stream_t stream);
+int zero_fp4_linear_dinput(const zero_fp4_t* dy, const zero_fp4_t* w, int32_t format, int64_t m,
+                           int64_t n, int64_t k, const zero_act_grad_t* ag, void* dx,
+                           int64_t lddx, zero_dtype_t dxdtype, zero_stream_t stream);
+int zero_fp4_linear_dweight(const zero_fp4_t* dy, const zero_fp4_t* x, int32_t format, int64_t m,
+                            int64_t n, int64_t k, void* dw, int64_t lddw, zero_dtype_t dwdtype,
+                            int32_t accumulate, zero_stream_t stream);
+
 /* ------------------------------------------------------ checked build --
  * No counterpart on the pages: a stand-in for a device memory checker.  The
  * library built with -DZERO_CHECKED (libzero_checked.so, same ABI) tests
@@ -757,6 +851,8 @@ int zero_layer_norm_backward(const void* dy, int64_t lddy, zero_dtype_t dydtype,
 #define ZERO_SITE_LINEAR_OUT 17  /* products: epilogue operands and outputs */
 #define ZERO_SITE_DROPOUT 18     /* zero_dropout: x, residual, y */
 #define ZERO_SITE_LNORM 19       /* layer norm: x, dy, dres, y, dx, parameters */
+#define ZERO_SITE_FP4 20         /* 4-bit matrices: x, codes, scales, y */
+#define ZERO_SITE_ORTHO 21       /* orthogonalised updates: x, y, flat arrays, workspace */
 
 typedef struct {
   int32_t checked; /* 1 in the checked build */

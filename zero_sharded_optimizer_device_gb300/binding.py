@@ -39,6 +39,8 @@ ZERO_MAX_COALESCE = 64
 ZERO_ACT_NONE, ZERO_ACT_RELU, ZERO_ACT_GELU, ZERO_ACT_GELU_TANH, ZERO_ACT_SILU = range(5)
 ZERO_W_NK, ZERO_W_KN = range(2)
 ZERO_NORM_LAYER, ZERO_NORM_RMS = range(2)
+ZERO_FP4_MX, ZERO_FP4_NV = range(2)
+ZERO_FP4_WORKSPACE = 4096
 
 _NAMES = {0: "ZERO_OK", -1: "ZERO_EINVAL", -2: "ZERO_EALIGN", -3: "ZERO_ERANGE",
           -4: "ZERO_EDTYPE", -5: "ZERO_ENOMEM", -6: "ZERO_ECUDA", -7: "ZERO_ETIMEOUT"}
@@ -110,6 +112,10 @@ class zero_linear_epilogue_t(ctypes.Structure):
 class zero_act_grad_t(ctypes.Structure):
     _fields_ = [("act", c_i32), ("reserved", c_i32), ("pre", c_vp), ("ldpre", c_i64),
                 ("gate", c_vp), ("ldgate", c_i64), ("dgate", c_vp), ("lddgate", c_i64)]
+
+
+class zero_fp4_t(ctypes.Structure):
+    _fields_ = [("codes", c_vp), ("ld", c_i64), ("scales", c_vp), ("tensor_scale", c_vp)]
 
 
 def adam_hp(step: int, grad_scale: float, lr: float = 1e-3, beta1: float = 0.9,
@@ -188,6 +194,18 @@ _SIGS = {
                                          c_vp, c_vp, c_i64, c_i64, c_i32, c_vp, c_i64, c_vp,
                                          c_i64, c_i32, c_vp, c_vp, c_i32, c_i32, c_vp, c_i64,
                                          c_vp]),
+    "zero_fp4_size": (c_i32, [c_i64, c_i64, c_i32, P(c_i64), P(c_i64)]),
+    "zero_fp4_tensor_scale": (c_i32, [c_vp, c_i64, c_i32, c_i64, c_i64, c_vp, c_vp, c_i64, c_vp]),
+    "zero_fp4_quantize": (c_i32, [c_vp, c_i64, c_i32, c_i64, c_i64, c_i32, P(zero_fp4_t),
+                                  P(zero_fp4_t), c_vp]),
+    "zero_fp4_dequantize": (c_i32, [P(zero_fp4_t), c_i64, c_i64, c_i32, c_vp, c_i64, c_i32,
+                                    c_vp]),
+    "zero_fp4_linear": (c_i32, [P(zero_fp4_t), P(zero_fp4_t), c_i32, c_i64, c_i64, c_i64,
+                                P(zero_linear_epilogue_t), c_vp, c_i64, c_i32, c_vp]),
+    "zero_fp4_linear_dinput": (c_i32, [P(zero_fp4_t), P(zero_fp4_t), c_i32, c_i64, c_i64, c_i64,
+                                       P(zero_act_grad_t), c_vp, c_i64, c_i32, c_vp]),
+    "zero_fp4_linear_dweight": (c_i32, [P(zero_fp4_t), P(zero_fp4_t), c_i32, c_i64, c_i64, c_i64,
+                                        c_vp, c_i64, c_i32, c_i32, c_vp]),
 }
 
 _LIB = None
@@ -968,3 +986,99 @@ def zero_layer_norm_backward(dy, lddy: int, dydtype: int, x, ldx: int, xdtype: i
         lddx, dxdtype, _mat(dweight, 1, n, 0, gdtype, "dweight"),
         _mat(dbias, 1, n, 0, gdtype, "dbias"), gdtype, int(accumulate), _ptr(workspace),
         workspace_bytes, _ops_stream(stream)), "zero_layer_norm_backward")
+
+
+# ------------------------------------------------------------- 4-bit layers --
+class _Fp4:
+    """A 4-bit matrix: the struct of its addresses, and its tensors until a
+    call says what they have to hold."""
+    __slots__ = ("struct", "codes", "scales", "tensor_scale")
+
+    def __init__(self, codes, ld, scales, tensor_scale):
+        self.codes, self.scales, self.tensor_scale = codes, scales, tensor_scale
+        self.struct = zero_fp4_t(None, ld, None, None)
+
+    def checked(self, rows: int, cols: int, format: int, what: str):
+        s, c = self.struct, self.codes
+        if rows > 0 and cols > 0:
+            need = (rows - 1) * s.ld + (cols + 31) // 32 * 16
+            if not (c is None or isinstance(c, int) or (c.is_contiguous() and c.nbytes >= need)):
+                if c.element_size() != 1 or (c.shape[-1] > 1 and c.stride(-1) != 1):
+                    raise ValueError(f"{what}.codes: the bytes of a row are not consecutive")
+                have = c.untyped_storage().nbytes() - c.storage_offset()
+                if have < need:
+                    raise ValueError(f"{what}.codes: holds {have} bytes, the call touches {need}")
+            blocks = (cols + 15) // 16 if format == ZERO_FP4_NV else (cols + 31) // 32
+            _need(self.scales, (rows + 127) // 128 * ((blocks + 3) // 4) * 512, what + ".scales")
+        _need(self.tensor_scale, 4, what + ".tensor_scale")
+        s.codes, s.scales, s.tensor_scale = _ptr(c), _ptr(self.scales), _ptr(self.tensor_scale)
+        return ctypes.byref(s)
+
+
+def fp4_matrix(codes, ld: int, scales, tensor_scale=None) -> _Fp4:
+    """A matrix in 4-bit codes (zero_fp4_t): rows of codes ld bytes apart, the
+    scales' tiles, and (ZERO_FP4_NV) the tensor's scale in device memory.  May
+    be kept and used for many calls."""
+    return _Fp4(codes, ld, scales, tensor_scale)
+
+
+def _fp4(q, rows: int, cols: int, format: int, what: str):
+    return None if q is None else q.checked(rows, cols, format, what)
+
+
+def zero_fp4_size(rows: int, cols: int, format: int):
+    """(bytes that a row of codes fills, bytes of the scales)."""
+    a, b = c_i64(), c_i64()
+    _check(_lib().zero_fp4_size(rows, cols, format, ctypes.byref(a), ctypes.byref(b)),
+           "zero_fp4_size")
+    return a.value, b.value
+
+
+def zero_fp4_tensor_scale(x, ldx: int, xdtype: int, rows: int, cols: int, tensor_scale, workspace,
+                          workspace_bytes: int, stream=None) -> None:
+    _need(tensor_scale, 4, "tensor_scale")
+    _need(workspace, workspace_bytes, "workspace")
+    _check(_lib().zero_fp4_tensor_scale(
+        _mat(x, rows, cols, ldx, xdtype, "x"), ldx, xdtype, rows, cols, _ptr(tensor_scale),
+        _ptr(workspace), workspace_bytes, _ops_stream(stream)), "zero_fp4_tensor_scale")
+
+
+def zero_fp4_quantize(x, ldx: int, xdtype: int, rows: int, cols: int, format: int, q, qt=None,
+                      stream=None) -> None:
+    _check(_lib().zero_fp4_quantize(
+        _mat(x, rows, cols, ldx, xdtype, "x"), ldx, xdtype, rows, cols, format,
+        _fp4(q, rows, cols, format, "q"), _fp4(qt, cols, rows, format, "qt"),
+        _ops_stream(stream)), "zero_fp4_quantize")
+
+
+def zero_fp4_dequantize(q, rows: int, cols: int, format: int, y, ldy: int,
+                        ydtype: int = ZERO_BF16, stream=None) -> None:
+    _check(_lib().zero_fp4_dequantize(
+        _fp4(q, rows, cols, format, "q"), rows, cols, format,
+        _mat(y, rows, cols, ldy, ydtype, "y"), ldy, ydtype, _ops_stream(stream)),
+        "zero_fp4_dequantize")
+
+
+def zero_fp4_linear(x, w, format: int, m: int, n: int, k: int, ep, y, ldy: int,
+                    ydtype: int = ZERO_BF16, stream=None) -> None:
+    _check(_lib().zero_fp4_linear(
+        _fp4(x, m, k, format, "x"), _fp4(w, n, k, format, "w"), format, m, n, k,
+        None if ep is None else ctypes.byref(ep.checked(m, n)),
+        _mat(y, m, n, ldy, ydtype, "y"), ldy, ydtype, _ops_stream(stream)), "zero_fp4_linear")
+
+
+def zero_fp4_linear_dinput(dy, w, format: int, m: int, n: int, k: int, ag, dx, lddx: int,
+                           dxdtype: int = ZERO_BF16, stream=None) -> None:
+    _check(_lib().zero_fp4_linear_dinput(
+        _fp4(dy, m, n, format, "dy"), _fp4(w, k, n, format, "w"), format, m, n, k,
+        None if ag is None else ctypes.byref(ag.checked(m, k)),
+        _mat(dx, m, k, lddx, dxdtype, "dx"), lddx, dxdtype, _ops_stream(stream)),
+        "zero_fp4_linear_dinput")
+
+
+def zero_fp4_linear_dweight(dy, x, format: int, m: int, n: int, k: int, dw, lddw: int,
+                            dwdtype: int = ZERO_BF16, accumulate=False, stream=None) -> None:
+    _check(_lib().zero_fp4_linear_dweight(
+        _fp4(dy, n, m, format, "dy"), _fp4(x, k, m, format, "x"), format, m, n, k,
+        _mat(dw, n, k, lddw, dwdtype, "dw"), lddw, dwdtype, int(accumulate),
+        _ops_stream(stream)), "zero_fp4_linear_dweight")

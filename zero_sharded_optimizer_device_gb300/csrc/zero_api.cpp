@@ -605,7 +605,7 @@ extern "C" int zero_bounds_report(zero_bounds_t* out, int32_t reset) {
   *out = zero_bounds_t{};
 #ifdef ZERO_CHECKED
   out->checked = 1;
-  zk::BoundsRec rec[6] = {};
+  zk::BoundsRec rec[8] = {};
   cudaError_t e = cudaDeviceSynchronize();
   if (e == cudaSuccess) e = zk::bounds_rs(&rec[0], reset != 0);
   if (e == cudaSuccess) e = zk::bounds_kernels(&rec[1], reset != 0);
@@ -613,6 +613,8 @@ extern "C" int zero_bounds_report(zero_bounds_t* out, int32_t reset) {
   if (e == cudaSuccess) e = zk::bounds_dropout(&rec[3], reset != 0);
   if (e == cudaSuccess) e = zk::bounds_lnorm(&rec[4], reset != 0);
   if (e == cudaSuccess) e = zk::bounds_rows(&rec[5], reset != 0);
+  if (e == cudaSuccess) e = zk::bounds_fp4(&rec[6], reset != 0);
+  if (e == cudaSuccess) e = zk::bounds_ortho(&rec[7], reset != 0);
   if (e != cudaSuccess) return cuda_status(e);
   for (const zk::BoundsRec& r : rec) {
     if (r.count && !out->count) {  // the first unit with a record gives the details
@@ -635,11 +637,13 @@ extern "C" int zero_bounds_probe(zero_stream_t stream) {
 
 extern "C" int zero_async_status(int64_t* timeouts, int32_t reset) {
   if (!timeouts) return ZERO_EINVAL;
-  unsigned long long n = 0, ops = 0;
+  unsigned long long n = 0, ops[3] = {};
   cudaError_t e = cudaDeviceSynchronize();
   if (e == cudaSuccess) e = zk::async_timeouts(&n, reset != 0);
-  if (e == cudaSuccess) e = zk::ops_timeouts(&ops, reset != 0);
+  if (e == cudaSuccess) e = zk::timeouts_linear(&ops[0], reset != 0);
+  if (e == cudaSuccess) e = zk::timeouts_fp4(&ops[1], reset != 0);
+  if (e == cudaSuccess) e = zk::timeouts_ortho(&ops[2], reset != 0);
   if (e != cudaSuccess) return cuda_status(e);
-  *timeouts = (int64_t)(n + ops);
+  *timeouts = (int64_t)(n + ops[0] + ops[1] + ops[2]);
   return ZERO_OK;
 }

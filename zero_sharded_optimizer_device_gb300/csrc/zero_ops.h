@@ -63,6 +63,13 @@ struct ProductK {
   int64_t rows = 0, cols = 0, depth = 0;
   EpiK epi;
   Mat dbias;  // dweight: sums over c of the rows of A or B
+  // 4-bit operands (then a and b hold four codes per 16-bit element of theirs):
+  // scale tiles of 128 rows and four blocks, scale_tiles of them along the
+  // contraction; what the whole operands are scaled by, or nullptr
+  const void *scales_a = nullptr, *scales_b = nullptr;
+  const float *whole_a = nullptr, *whole_b = nullptr;
+  int blocks_of = 0;  // 16 or 32 codes
+  int64_t scale_tiles = 0;
 };
 
 cudaError_t launch_product(const ProductK& k, int mode, cudaStream_t st);
@@ -93,11 +100,47 @@ struct NormGradK {
 int64_t norm_partials(int64_t m);
 cudaError_t launch_layer_norm_grad(const NormGradK& k, cudaStream_t st);
 
+// A matrix in 4-bit codes and its scales as the kernels see it (zero_fp4_t).
+struct Fp4Mat {
+  unsigned char* codes = nullptr;
+  int64_t ld = 0, line_bytes = 0;  // bytes between rows, and that a row fills
+  unsigned char* scales = nullptr;
+  int64_t scale_tiles = 0, scale_bytes = 0;  // tiles along a row; all of them
+};
+struct QuantK {
+  Mat x;
+  int64_t rows = 0, cols = 0, tiles_j = 0;
+  Fp4Mat q, qt;  // codes nullptr: direction not asked for
+  const float* g = nullptr;
+  int nv = 0;
+};
+cudaError_t launch_quantize(const QuantK& k, cudaStream_t st);
+struct DequantK {
+  Fp4Mat q;
+  const float* g = nullptr;
+  int nv = 0;
+  int64_t rows = 0, cols = 0;
+  Mat y;
+};
+cudaError_t launch_dequantize(const DequantK& k, cudaStream_t st);
+constexpr int kMaxima = ZERO_FP4_WORKSPACE / (int)sizeof(float);
+struct MaxK {
+  Mat x;
+  int64_t rows = 0, cols = 0;
+  float* maxima = nullptr;  // kMaxima
+};
+cudaError_t launch_tensor_scale(const MaxK& k, float* g, cudaStream_t st);
+cudaError_t launch_fp4_product(const ProductK& k, int mode, cudaStream_t st);
+
 // Bounded waits that gave up / out-of-extent records of these units.
-cudaError_t ops_timeouts(unsigned long long* out, bool reset);
+cudaError_t timeouts_linear(unsigned long long* out, bool reset);
+cudaError_t timeouts_fp4(unsigned long long* out, bool reset);
+cudaError_t timeouts_ortho(unsigned long long* out, bool reset);
 cudaError_t bounds_linear(BoundsRec* out, bool reset);
 cudaError_t bounds_dropout(BoundsRec* out, bool reset);
 cudaError_t bounds_lnorm(BoundsRec* out, bool reset);
 cudaError_t bounds_rows(BoundsRec* out, bool reset);
+cudaError_t bounds_fp4(BoundsRec* out, bool reset);
+cudaError_t bounds_ortho(BoundsRec* out, bool reset);
 
 }  // namespace zk

@@ -81,6 +81,49 @@ int drop_k(const zero_dropout_t* r, zk::DropK* out) {
   return ZERO_OK;
 }
 
+// The checked epilogue of a forward product of x and w into y.
+int epilogue_k(const zero_linear_epilogue_t* ep, const void* x, const void* w, int64_t m,
+               int64_t n, const void* y, int64_t ldy, int32_t ydtype, zk::EpiK* out) {
+  ZERO_TRY(check_act(ep->act));
+  if (ep->reserved != 0) return ZERO_EINVAL;
+  ZERO_TRY(check_opt_vec(ep->bias, ep->bias_dtype));
+  ZERO_TRY(check_opt_mat(ep->pre, ep->ldpre, ZERO_BF16, m, n));
+  ZERO_TRY(check_opt_mat(ep->gate, ep->ldgate, ZERO_BF16, m, n));
+  ZERO_TRY(check_opt_mat(ep->residual, ep->ldres, ep->res_dtype, m, n));
+  if (same(ep->pre, x) || same(ep->pre, w) || same(ep->pre, y) || same(ep->pre, ep->gate) ||
+      same(ep->pre, ep->residual) || same(ep->gate, y) || same(ep->bias, y) ||
+      same(ep->bias, ep->pre))
+    return ZERO_EINVAL;
+  if (same(ep->residual, y) && (ep->ldres != ldy || ep->res_dtype != (int32_t)ydtype))
+    return ZERO_EINVAL;
+  if (ep->dropout) ZERO_TRY(drop_k(ep->dropout, &out->drop));
+  out->act = ep->act;
+  if (ep->bias) out->bias = mat(ep->bias, 0, ep->bias_dtype);
+  if (ep->pre) out->pre = mat(ep->pre, ep->ldpre, ZERO_BF16);
+  if (ep->gate) out->gate = mat(ep->gate, ep->ldgate, ZERO_BF16);
+  if (ep->residual) out->residual = mat(ep->residual, ep->ldres, ep->res_dtype);
+  return ZERO_OK;
+}
+// The checked activation gradient behind an input gradient of dy and w into dx.
+int act_grad_k(const zero_act_grad_t* ag, const void* dy, const void* w, int64_t m, int64_t k,
+               const void* dx, zk::EpiK* out) {
+  ZERO_TRY(check_act(ag->act));
+  if (ag->reserved != 0) return ZERO_EINVAL;
+  ZERO_TRY(check_mat(ag->pre, ag->ldpre, ZERO_BF16, m, k));
+  ZERO_TRY(check_opt_mat(ag->gate, ag->ldgate, ZERO_BF16, m, k));
+  ZERO_TRY(check_opt_mat(ag->dgate, ag->lddgate, ZERO_BF16, m, k));
+  if (ag->dgate && !ag->gate) return ZERO_EINVAL;
+  if (same(ag->dgate, dx) || same(ag->dgate, dy) || same(ag->dgate, w) ||
+      same(ag->dgate, ag->pre) || same(ag->dgate, ag->gate) || same(ag->pre, dx) ||
+      same(ag->gate, dx))
+    return ZERO_EINVAL;
+  out->act = ag->act;
+  out->pre = mat(ag->pre, ag->ldpre, ZERO_BF16);
+  if (ag->gate) out->gate = mat(ag->gate, ag->ldgate, ZERO_BF16);
+  if (ag->dgate) out->dgate = mat(ag->dgate, ag->lddgate, ZERO_BF16);
+  return ZERO_OK;
+}
+
 }  // namespace
 
 extern "C" int zero_linear(const void* x, int64_t ldx, const void* w, int64_t ldw,
@@ -97,26 +140,7 @@ extern "C" int zero_linear(const void* x, int64_t ldx, const void* w, int64_t ld
   if (same(y, x) || same(y, w)) return ZERO_EINVAL;
   zk::ProductK p;
   p.epi.out = mat(y, ldy, ydtype);
-  if (ep) {
-    ZERO_TRY(check_act(ep->act));
-    if (ep->reserved != 0) return ZERO_EINVAL;
-    ZERO_TRY(check_opt_vec(ep->bias, ep->bias_dtype));
-    ZERO_TRY(check_opt_mat(ep->pre, ep->ldpre, ZERO_BF16, m, n));
-    ZERO_TRY(check_opt_mat(ep->gate, ep->ldgate, ZERO_BF16, m, n));
-    ZERO_TRY(check_opt_mat(ep->residual, ep->ldres, ep->res_dtype, m, n));
-    if (same(ep->pre, x) || same(ep->pre, w) || same(ep->pre, y) || same(ep->pre, ep->gate) ||
-        same(ep->pre, ep->residual) || same(ep->gate, y) || same(ep->bias, y) ||
-        same(ep->bias, ep->pre))
-      return ZERO_EINVAL;
-    if (same(ep->residual, y) && (ep->ldres != ldy || ep->res_dtype != (int32_t)ydtype))
-      return ZERO_EINVAL;
-    if (ep->dropout) ZERO_TRY(drop_k(ep->dropout, &p.epi.drop));
-    p.epi.act = ep->act;
-    if (ep->bias) p.epi.bias = mat(ep->bias, 0, ep->bias_dtype);
-    if (ep->pre) p.epi.pre = mat(ep->pre, ep->ldpre, ZERO_BF16);
-    if (ep->gate) p.epi.gate = mat(ep->gate, ep->ldgate, ZERO_BF16);
-    if (ep->residual) p.epi.residual = mat(ep->residual, ep->ldres, ep->res_dtype);
-  }
+  if (ep) ZERO_TRY(epilogue_k(ep, x, w, m, n, y, ldy, ydtype, &p.epi));
   p.a = mat(x, ldx, ZERO_BF16);
   p.b = mat(w, ldw, ZERO_BF16);
   p.a_c = 1;
@@ -141,22 +165,7 @@ extern "C" int zero_linear_dinput(const void* dy, int64_t lddy, const void* w, i
   if (same(dx, dy) || same(dx, w)) return ZERO_EINVAL;
   zk::ProductK p;
   p.epi.out = mat(dx, lddx, dxdtype);
-  if (ag) {
-    ZERO_TRY(check_act(ag->act));
-    if (ag->reserved != 0) return ZERO_EINVAL;
-    ZERO_TRY(check_mat(ag->pre, ag->ldpre, ZERO_BF16, m, k));
-    ZERO_TRY(check_opt_mat(ag->gate, ag->ldgate, ZERO_BF16, m, k));
-    ZERO_TRY(check_opt_mat(ag->dgate, ag->lddgate, ZERO_BF16, m, k));
-    if (ag->dgate && !ag->gate) return ZERO_EINVAL;
-    if (same(ag->dgate, dx) || same(ag->dgate, dy) || same(ag->dgate, w) ||
-        same(ag->dgate, ag->pre) || same(ag->dgate, ag->gate) || same(ag->pre, dx) ||
-        same(ag->gate, dx))
-      return ZERO_EINVAL;
-    p.epi.act = ag->act;
-    p.epi.pre = mat(ag->pre, ag->ldpre, ZERO_BF16);
-    if (ag->gate) p.epi.gate = mat(ag->gate, ag->ldgate, ZERO_BF16);
-    if (ag->dgate) p.epi.dgate = mat(ag->dgate, ag->lddgate, ZERO_BF16);
-  }
+  if (ag) ZERO_TRY(act_grad_k(ag, dy, w, m, k, dx, &p.epi));
   p.a = mat(dy, lddy, ZERO_BF16);
   p.b = mat(w, ldw, ZERO_BF16);
   p.a_c = 1;
@@ -307,4 +316,185 @@ extern "C" int zero_layer_norm_backward(
   k.rstd = rstd;
   k.partials = static_cast<float*>(workspace);
   return cuda_status(zk::launch_layer_norm_grad(k, (cudaStream_t)stream));
+}
+
+namespace {
+
+int check_format(int32_t format) {
+  return format == ZERO_FP4_MX || format == ZERO_FP4_NV ? ZERO_OK : ZERO_EINVAL;
+}
+
+// A 4-bit matrix of rows x cols.
+int fp4_k(const zero_fp4_t* q, int32_t format, int64_t rows, int64_t cols, zk::Fp4Mat* out) {
+  if (!q) return ZERO_EINVAL;
+  ZERO_TRY(zero_fp4_size(rows, cols, format, &out->line_bytes, &out->scale_bytes));
+  if (q->ld < out->line_bytes) return ZERO_EINVAL;
+  if (q->ld >= kMost) return ZERO_ERANGE;
+  if (rows > 0 && cols > 0 && (!q->codes || !q->scales)) return ZERO_EINVAL;
+  if (format == ZERO_FP4_MX && q->tensor_scale) return ZERO_EINVAL;
+  if ((((uintptr_t)q->codes | (uintptr_t)q->scales | (uintptr_t)q->ld) & 15u) != 0 ||
+      ((uintptr_t)q->tensor_scale & 3u) != 0)
+    return ZERO_EALIGN;
+  if (same(q->codes, q->scales) || same(q->codes, q->tensor_scale) ||
+      same(q->scales, q->tensor_scale))
+    return ZERO_EINVAL;
+  out->codes = static_cast<unsigned char*>(q->codes);
+  out->ld = q->ld;
+  out->scales = static_cast<unsigned char*>(q->scales);
+  const int64_t size = format == ZERO_FP4_NV ? 16 : 32, blocks = (cols + size - 1) / size;
+  out->scale_tiles = (blocks + 3) / 4;
+  return ZERO_OK;
+}
+
+// Whether p is one of q's buffers.
+bool within(const void* p, const zero_fp4_t* q) {
+  return q && (same(p, q->codes) || same(p, q->scales) || same(p, q->tensor_scale));
+}
+
+// a [rows, depth] times b [cols, depth] transposed.
+int fp4_product(const zero_fp4_t* a, const zero_fp4_t* b, int32_t format, int64_t rows,
+                int64_t cols, int64_t depth, zk::ProductK* p) {
+  zk::Fp4Mat qa, qb;
+  ZERO_TRY(fp4_k(a, format, rows, depth, &qa));
+  ZERO_TRY(fp4_k(b, format, cols, depth, &qb));
+  p->a = mat(qa.codes, qa.ld / 2, ZERO_BF16);
+  p->b = mat(qb.codes, qb.ld / 2, ZERO_BF16);
+  p->rows = rows;
+  p->cols = cols;
+  p->depth = qa.line_bytes / 2;
+  p->scales_a = qa.scales;
+  p->scales_b = qb.scales;
+  p->whole_a = a->tensor_scale;
+  p->whole_b = b->tensor_scale;
+  p->blocks_of = format == ZERO_FP4_NV ? 16 : 32;
+  p->scale_tiles = qa.scale_tiles;
+  return ZERO_OK;
+}
+
+}  // namespace
+
+extern "C" int zero_fp4_size(int64_t rows, int64_t cols, int32_t format, int64_t* row_bytes,
+                             int64_t* scale_bytes) {
+  if (!row_bytes || !scale_bytes) return ZERO_EINVAL;
+  ZERO_TRY(check_format(format));
+  ZERO_TRY(check_sizes(rows, cols));
+  const int64_t size = format == ZERO_FP4_NV ? 16 : 32, blocks = (cols + size - 1) / size;
+  *row_bytes = (cols + 31) / 32 * 16;
+  *scale_bytes = (rows + 127) / 128 * ((blocks + 3) / 4) * 512;
+  return ZERO_OK;
+}
+
+extern "C" int zero_fp4_tensor_scale(const void* x, int64_t ldx, zero_dtype_t xdtype,
+                                     int64_t rows, int64_t cols, float* tensor_scale,
+                                     void* workspace, int64_t workspace_bytes,
+                                     zero_stream_t stream) {
+  NvtxRange nvtx("zero_fp4_tensor_scale");
+  ZERO_TRY(check_sizes(rows, cols));
+  ZERO_TRY(check_mat(x, ldx, xdtype, rows, cols));
+  if (!tensor_scale || !workspace || workspace_bytes < ZERO_FP4_WORKSPACE) return ZERO_EINVAL;
+  if (((uintptr_t)tensor_scale & 3u) != 0 || ((uintptr_t)workspace & 15u) != 0)
+    return ZERO_EALIGN;
+  if (same(tensor_scale, x) || same(workspace, x) || same(workspace, tensor_scale))
+    return ZERO_EINVAL;
+  zk::MaxK k;
+  k.x = mat(x, ldx, xdtype);
+  k.rows = rows;
+  k.cols = cols;
+  k.maxima = static_cast<float*>(workspace);
+  return cuda_status(zk::launch_tensor_scale(k, tensor_scale, (cudaStream_t)stream));
+}
+
+extern "C" int zero_fp4_quantize(const void* x, int64_t ldx, zero_dtype_t xdtype, int64_t rows,
+                                 int64_t cols, int32_t format, const zero_fp4_t* q,
+                                 const zero_fp4_t* qt, zero_stream_t stream) {
+  NvtxRange nvtx("zero_fp4_quantize");
+  ZERO_TRY(check_format(format));
+  ZERO_TRY(check_sizes(rows, cols));
+  ZERO_TRY(check_mat(x, ldx, xdtype, rows, cols));
+  if (!q && !qt) return ZERO_EINVAL;
+  zk::QuantK k;
+  if (q) ZERO_TRY(fp4_k(q, format, rows, cols, &k.q));
+  if (qt) ZERO_TRY(fp4_k(qt, format, cols, rows, &k.qt));
+  if (q && qt &&
+      (q->tensor_scale != qt->tensor_scale || within(q->codes, qt) || within(q->scales, qt)))
+    return ZERO_EINVAL;
+  if (within(x, q) || within(x, qt)) return ZERO_EINVAL;
+  k.x = mat(x, ldx, xdtype);
+  k.rows = rows;
+  k.cols = cols;
+  k.g = (q ? q : qt)->tensor_scale;
+  k.nv = format == ZERO_FP4_NV;
+  return cuda_status(zk::launch_quantize(k, (cudaStream_t)stream));
+}
+
+extern "C" int zero_fp4_dequantize(const zero_fp4_t* q, int64_t rows, int64_t cols,
+                                   int32_t format, void* y, int64_t ldy, zero_dtype_t ydtype,
+                                   zero_stream_t stream) {
+  NvtxRange nvtx("zero_fp4_dequantize");
+  ZERO_TRY(check_format(format));
+  ZERO_TRY(check_sizes(rows, cols));
+  zk::DequantK k;
+  ZERO_TRY(fp4_k(q, format, rows, cols, &k.q));
+  ZERO_TRY(check_mat(y, ldy, ydtype, rows, cols));
+  if (within(y, q)) return ZERO_EINVAL;
+  k.g = q->tensor_scale;
+  k.nv = format == ZERO_FP4_NV;
+  k.rows = rows;
+  k.cols = cols;
+  k.y = mat(y, ldy, ydtype);
+  return cuda_status(zk::launch_dequantize(k, (cudaStream_t)stream));
+}
+
+extern "C" int zero_fp4_linear(const zero_fp4_t* x, const zero_fp4_t* w, int32_t format,
+                               int64_t m, int64_t n, int64_t k,
+                               const zero_linear_epilogue_t* ep, void* y, int64_t ldy,
+                               zero_dtype_t ydtype, zero_stream_t stream) {
+  NvtxRange nvtx("zero_fp4_linear");
+  ZERO_TRY(check_format(format));
+  ZERO_TRY(check_sizes(m, n, k));
+  zk::ProductK p;
+  ZERO_TRY(fp4_product(x, w, format, m, n, k, &p));
+  ZERO_TRY(check_mat(y, ldy, ydtype, m, n));
+  if (within(y, x) || within(y, w)) return ZERO_EINVAL;
+  p.epi.out = mat(y, ldy, ydtype);
+  if (ep) {
+    if (within(ep->pre, x) || within(ep->pre, w)) return ZERO_EINVAL;
+    ZERO_TRY(epilogue_k(ep, nullptr, nullptr, m, n, y, ldy, ydtype, &p.epi));
+  }
+  return cuda_status(zk::launch_fp4_product(p, zk::LIN_FORWARD, (cudaStream_t)stream));
+}
+
+extern "C" int zero_fp4_linear_dinput(const zero_fp4_t* dy, const zero_fp4_t* w, int32_t format,
+                                      int64_t m, int64_t n, int64_t k, const zero_act_grad_t* ag,
+                                      void* dx, int64_t lddx, zero_dtype_t dxdtype,
+                                      zero_stream_t stream) {
+  NvtxRange nvtx("zero_fp4_linear_dinput");
+  ZERO_TRY(check_format(format));
+  ZERO_TRY(check_sizes(m, n, k));
+  zk::ProductK p;
+  ZERO_TRY(fp4_product(dy, w, format, m, k, n, &p));
+  ZERO_TRY(check_mat(dx, lddx, dxdtype, m, k));
+  if (within(dx, dy) || within(dx, w)) return ZERO_EINVAL;
+  p.epi.out = mat(dx, lddx, dxdtype);
+  if (ag) {
+    if (within(ag->dgate, dy) || within(ag->dgate, w)) return ZERO_EINVAL;
+    ZERO_TRY(act_grad_k(ag, nullptr, nullptr, m, k, dx, &p.epi));
+  }
+  return cuda_status(zk::launch_fp4_product(p, zk::LIN_DINPUT, (cudaStream_t)stream));
+}
+
+extern "C" int zero_fp4_linear_dweight(const zero_fp4_t* dy, const zero_fp4_t* x, int32_t format,
+                                       int64_t m, int64_t n, int64_t k, void* dw, int64_t lddw,
+                                       zero_dtype_t dwdtype, int32_t accumulate,
+                                       zero_stream_t stream) {
+  NvtxRange nvtx("zero_fp4_linear_dweight");
+  ZERO_TRY(check_format(format));
+  ZERO_TRY(check_sizes(m, n, k));
+  zk::ProductK p;
+  ZERO_TRY(fp4_product(dy, x, format, n, k, m, &p));
+  ZERO_TRY(check_mat(dw, lddw, dwdtype, n, k));
+  if (within(dw, dy) || within(dw, x)) return ZERO_EINVAL;
+  p.epi.out = mat(dw, lddw, dwdtype);
+  if (accumulate) p.epi.residual = p.epi.out;
+  return cuda_status(zk::launch_fp4_product(p, zk::LIN_FORWARD, (cudaStream_t)stream));
 }

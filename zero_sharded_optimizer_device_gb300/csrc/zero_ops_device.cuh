@@ -10,9 +10,10 @@ namespace zk {
 // Launches a kernel that may set up while the one before it on the stream is
 // still running (it executes griddepcontrol.wait before it touches memory).
 template <typename... P, typename... A>
-static cudaError_t launch_next(void (*kernel)(P...), dim3 grid, dim3 block, cudaStream_t st,
-                               A... args) {
+static cudaError_t launch_next_with(size_t shared_bytes, void (*kernel)(P...), dim3 grid,
+                                    dim3 block, cudaStream_t st, A... args) {
   cudaLaunchConfig_t cfg = {};
+  cfg.dynamicSmemBytes = shared_bytes;
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.stream = st;
@@ -22,6 +23,11 @@ static cudaError_t launch_next(void (*kernel)(P...), dim3 grid, dim3 block, cuda
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+template <typename... P, typename... A>
+static cudaError_t launch_next(void (*kernel)(P...), dim3 grid, dim3 block, cudaStream_t st,
+                               A... args) {
+  return launch_next_with(0, kernel, grid, block, st, args...);
 }
 __device__ __forceinline__ void after_previous_kernel() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
