@@ -729,6 +729,79 @@ int zero_layer_norm_backward(const void* dy, int64_t lddy, zero_dtype_t dydtype,
                              int32_t accumulate, void* workspace, int64_t workspace_bytes,
                              zero_stream_t stream);
 
+/* -------------------------------------------- orthogonalised updates (ops) --
+ * No counterpart on the pages, which name Adam alone.  The update of a weight
+ * matrix by its momentum made orthogonal ["Muon": Jordan et al. 2024; the
+ * steps are Newton and Schulz's, of degree 5], over the same plan and flat
+ * arrays as zero_adam_shard.  A matrix is needed whole: the calls take the
+ * arrays of all owners, and a tensor's matrix is its numel elements from
+ * zero_plan_tensor's flat_off on, row after row.
+ *
+ * zero_newton_schulz_t: X0 = x / (|x| + eps), |x| the Frobenius norm, then
+ * `steps` times, with coefficients (a, b, c) of each step,
+ *   X <- a X + (b G + c G^2) X,  G = X X^T (equally: a X + X (b G + c G^2),
+ *   G = X^T X),
+ * which takes every singular value s of X to a s + b s^3 + c s^5.  0 <= steps
+ * <= ZERO_NS_MOST; steps have to keep singular values below 2 (the usual
+ * (3.4445, -4.7750, 2.0315) stay below 1.21), or results are infinite or NaN.
+ * A matrix of zeros stays zero; one that holds a NaN or an infinity becomes
+ * NaN.  Products take fp16 operands and are summed in fp32; X and the
+ * diagonals of G are held to more digits: five such steps are off by 5e-4 to
+ * 1e-3 of the result (in 2-norms), before it is rounded. */
+#define ZERO_NS_MOST 16
+typedef struct {
+  int32_t steps;
+  float eps;
+  float coef[ZERO_NS_MOST][3];
+} zero_newton_schulz_t;
+
+/* zero_orthogonalize: y = the last X of each of `batch` matrices x [m, n],
+ * stride_x (stride_y) elements apart, in xdtype (bf16 or fp32); y is bf16 and
+ * may be x itself (bf16, same ld and stride).  workspace: 16-byte aligned
+ * device scratch of zero_orthogonalize_workspace() bytes (about six bytes for
+ * each element of the batch and four for each of the smaller sides' squares,
+ * in rows rounded up to 256), to be used by one call at a time.  Errors as
+ * zero_linear, and EINVAL (ns NULL, steps, eps or coefficients out of range,
+ * matrices that overlap, workspace too small), ERANGE (batch of 65536 or
+ * more, or 2^31 rows in all). */
+int zero_orthogonalize_workspace(int64_t m, int64_t n, int64_t batch, int64_t* bytes);
+int zero_orthogonalize(const void* x, int64_t ldx, int64_t stride_x, zero_dtype_t xdtype,
+                       int64_t m, int64_t n, int64_t batch, const zero_newton_schulz_t* ns,
+                       void* y, int64_t ldy, int64_t stride_y, void* workspace,
+                       int64_t workspace_bytes, zero_stream_t stream);
+
+typedef struct {
+  float lr, momentum, weight_decay;
+  float grad_scale;  /* multiplies the reduced sum; 1/N averages */
+  float scale;       /* of the update: e.g. 0.2 sqrt(max(rows, cols)), the size of Adam's */
+  int32_t nesterov;
+  int32_t reserved;  /* 0 */
+  zero_newton_schulz_t ns;
+} zero_muon_t;
+
+/* zero_muon_step: for each of `count` tensors of the plan (host array of their
+ * indices, none twice), all of numel rows * cols, at their places f of the flat
+ * arrays:
+ *   grad = reduced[f] * grad_scale (* *d_coef when d_coef != NULL)
+ *   momentum = mu * momentum + grad
+ *   u = grad + mu * momentum (nesterov) or momentum
+ *   O = Newton-Schulz steps of u as a matrix [rows, cols]
+ *   master -= (lr*wd) * master (when lr*wd != 0);  master -= (lr*scale) * O
+ * element by element in fp32, one rounding per operation, O as
+ * zero_orthogonalize computes it (rounded to fp16).  If out != NULL also
+ * writes out[f] = cast(master) as zero_adam_shard does.  Elements of other
+ * tensors are not touched.  0 <= momentum < 1.  workspace: as
+ * zero_orthogonalize's, zero_muon_workspace() bytes.  Errors: EINVAL (also a
+ * tensor of another numel or given twice, one array in two roles), EALIGN,
+ * ERANGE (tensor outside the plan, more than ZERO_MUON_MOST tensors, sizes as
+ * zero_orthogonalize), EDTYPE, ECUDA. */
+#define ZERO_MUON_MOST 128
+int zero_muon_workspace(int64_t rows, int64_t cols, int32_t count, int64_t* bytes);
+int zero_muon_step(const zero_plan_t* plan, const int64_t* tensors, int32_t count, int64_t rows,
+                   int64_t cols, float* master, float* momentum, const float* reduced,
+                   const zero_muon_t* hp, const float* d_coef, void* out, zero_dtype_t out_dtype,
+                   void* workspace, int64_t workspace_bytes, zero_stream_t stream);
+
 /* --------------------------------------------------- 4-bit layers (ops) --
  * The layer's products on matrices in microscaled 4-bit numbers ["OCP
  * Microscaling Formats (MX) Specification", v1.0 (2023), for MX], made from a

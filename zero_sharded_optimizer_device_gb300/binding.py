@@ -41,6 +41,8 @@ ZERO_W_NK, ZERO_W_KN = range(2)
 ZERO_NORM_LAYER, ZERO_NORM_RMS = range(2)
 ZERO_FP4_MX, ZERO_FP4_NV = range(2)
 ZERO_FP4_WORKSPACE = 4096
+ZERO_NS_MOST = 16
+ZERO_MUON_MOST = 128
 
 _NAMES = {0: "ZERO_OK", -1: "ZERO_EINVAL", -2: "ZERO_EALIGN", -3: "ZERO_ERANGE",
           -4: "ZERO_EDTYPE", -5: "ZERO_ENOMEM", -6: "ZERO_ECUDA", -7: "ZERO_ETIMEOUT"}
@@ -116,6 +118,18 @@ class zero_act_grad_t(ctypes.Structure):
 
 class zero_fp4_t(ctypes.Structure):
     _fields_ = [("codes", c_vp), ("ld", c_i64), ("scales", c_vp), ("tensor_scale", c_vp)]
+
+
+class zero_newton_schulz_t(ctypes.Structure):
+    _fields_ = [("steps", c_i32), ("eps", ctypes.c_float),
+                ("coef", (ctypes.c_float * 3) * ZERO_NS_MOST)]
+
+
+class zero_muon_t(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_float), ("momentum", ctypes.c_float),
+                ("weight_decay", ctypes.c_float), ("grad_scale", ctypes.c_float),
+                ("scale", ctypes.c_float), ("nesterov", c_i32), ("reserved", c_i32),
+                ("ns", zero_newton_schulz_t)]
 
 
 def adam_hp(step: int, grad_scale: float, lr: float = 1e-3, beta1: float = 0.9,
@@ -194,6 +208,13 @@ _SIGS = {
                                          c_vp, c_vp, c_i64, c_i64, c_i32, c_vp, c_i64, c_vp,
                                          c_i64, c_i32, c_vp, c_vp, c_i32, c_i32, c_vp, c_i64,
                                          c_vp]),
+    "zero_orthogonalize_workspace": (c_i32, [c_i64, c_i64, c_i64, P(c_i64)]),
+    "zero_orthogonalize": (c_i32, [c_vp, c_i64, c_i64, c_i32, c_i64, c_i64, c_i64,
+                                   P(zero_newton_schulz_t), c_vp, c_i64, c_i64, c_vp, c_i64,
+                                   c_vp]),
+    "zero_muon_workspace": (c_i32, [c_i64, c_i64, c_i32, P(c_i64)]),
+    "zero_muon_step": (c_i32, [c_vp, P(c_i64), c_i32, c_i64, c_i64, c_vp, c_vp, c_vp,
+                               P(zero_muon_t), c_vp, c_vp, c_i32, c_vp, c_i64, c_vp]),
     "zero_fp4_size": (c_i32, [c_i64, c_i64, c_i32, P(c_i64), P(c_i64)]),
     "zero_fp4_tensor_scale": (c_i32, [c_vp, c_i64, c_i32, c_i64, c_i64, c_vp, c_vp, c_i64, c_vp]),
     "zero_fp4_quantize": (c_i32, [c_vp, c_i64, c_i32, c_i64, c_i64, c_i32, P(zero_fp4_t),
@@ -986,6 +1007,91 @@ def zero_layer_norm_backward(dy, lddy: int, dydtype: int, x, ldx: int, xdtype: i
         lddx, dxdtype, _mat(dweight, 1, n, 0, gdtype, "dweight"),
         _mat(dbias, 1, n, 0, gdtype, "dbias"), gdtype, int(accumulate), _ptr(workspace),
         workspace_bytes, _ops_stream(stream)), "zero_layer_norm_backward")
+
+
+# -------------------------------------------------- orthogonalised updates --
+def newton_schulz(steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315),
+                  eps: float = 1e-7) -> zero_newton_schulz_t:
+    """The iteration (zero_newton_schulz_t); coefficients: (a, b, c) of every
+    step, or a list of such triples, one for each."""
+    ns = zero_newton_schulz_t(steps, eps)
+    each = list(coefficients)
+    if each and not hasattr(each[0], "__len__"):
+        each = [each] * min(max(steps, 0), ZERO_NS_MOST)
+    if 0 <= steps <= ZERO_NS_MOST and len(each) != steps:
+        raise ValueError(f"coefficients: {len(each)} triples for {steps} steps")
+    for row, triple in zip(ns.coef, each):
+        row[0], row[1], row[2] = triple
+    return ns
+
+
+def muon_hp(lr: float, momentum: float = 0.95, weight_decay: float = 0.0, grad_scale: float = 1.0,
+            nesterov: bool = True, scale: float = 1.0,
+            ns: zero_newton_schulz_t | None = None) -> zero_muon_t:
+    return zero_muon_t(lr, momentum, weight_decay, grad_scale, scale, int(nesterov), 0,
+                       newton_schulz() if ns is None else ns)
+
+
+def _batch(x, m: int, n: int, batch: int, ld: int, stride: int, dtype: int, what: str):
+    """Address of `batch` matrices stride elements apart: as _mat, for all of them."""
+    if x is None or isinstance(x, int) or batch <= 0 or m <= 0 or n <= 0:
+        return _mat(x, 0, n, ld, dtype, what)
+    if not _Torch.ready:
+        _Torch.load()
+    want = _Torch.dtypes.get(dtype)
+    if want is not None:
+        if x.dtype is not want:
+            raise ValueError(f"{what}: a {x.dtype} tensor passed as {want}")
+        need = (batch - 1) * stride + (m - 1) * ld + n
+        if not (x.is_contiguous() and x.numel() >= need):
+            if n > 1 and x.dim() > 0 and x.shape[-1] > 1 and x.stride(-1) != 1:
+                raise ValueError(f"{what}: the elements of a row are {x.stride(-1)} apart")
+            es = _ESIZE[dtype]
+            have = x.untyped_storage().nbytes() - x.storage_offset() * es
+            if have < need * es:
+                raise ValueError(f"{what}: holds {have} bytes, the call touches {need * es}")
+    return _ptr(x)
+
+
+def zero_orthogonalize_workspace(m: int, n: int, batch: int) -> int:
+    out = c_i64()
+    _check(_lib().zero_orthogonalize_workspace(m, n, batch, ctypes.byref(out)),
+           "zero_orthogonalize_workspace")
+    return out.value
+
+
+def zero_orthogonalize(x, ldx: int, stride_x: int, xdtype: int, m: int, n: int, batch: int, ns, y,
+                       ldy: int, stride_y: int, workspace, workspace_bytes: int,
+                       stream=None) -> None:
+    _need(workspace, workspace_bytes, "workspace")
+    _check(_lib().zero_orthogonalize(
+        _batch(x, m, n, batch, ldx, stride_x, xdtype, "x"), ldx, stride_x, xdtype, m, n, batch,
+        None if ns is None else ctypes.byref(ns),
+        _batch(y, m, n, batch, ldy, stride_y, ZERO_BF16, "y"), ldy, stride_y, _ptr(workspace),
+        workspace_bytes, _ops_stream(stream)), "zero_orthogonalize")
+
+
+def zero_muon_workspace(rows: int, cols: int, count: int) -> int:
+    out = c_i64()
+    _check(_lib().zero_muon_workspace(rows, cols, count, ctypes.byref(out)),
+           "zero_muon_workspace")
+    return out.value
+
+
+def zero_muon_step(plan, tensors, rows: int, cols: int, master, momentum, reduced, hp, d_coef,
+                   out, out_dtype: int = ZERO_BF16, workspace=None, workspace_bytes: int = 0,
+                   stream=None) -> None:
+    """tensors: indices of the plan's tensors that are updated, each [rows, cols]."""
+    total = plan.geometry()["psi_pad"]
+    for x, what in ((master, "master"), (momentum, "momentum"), (reduced, "reduced")):
+        _need(x, total * 4, what)
+    _need(out, total * _ESIZE.get(out_dtype, 0), "out")
+    _need(d_coef, 4, "d_coef")
+    _need(workspace, workspace_bytes, "workspace")
+    _check(_lib().zero_muon_step(
+        plan, (c_i64 * max(1, len(tensors)))(*tensors), len(tensors), rows, cols, _ptr(master),
+        _ptr(momentum), _ptr(reduced), ctypes.byref(hp), _ptr(d_coef), _ptr(out), out_dtype,
+        _ptr(workspace), workspace_bytes, _ops_stream(stream)), "zero_muon_step")
 
 
 # ------------------------------------------------------------- 4-bit layers --

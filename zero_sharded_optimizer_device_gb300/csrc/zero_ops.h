@@ -132,6 +132,55 @@ struct MaxK {
 cudaError_t launch_tensor_scale(const MaxK& k, float* g, cudaStream_t st);
 cudaError_t launch_fp4_product(const ProductK& k, int mode, cudaStream_t st);
 
+// Matrices of a batch: `stride` elements apart, or (listed) from these elements on.
+struct OrthoPlaces {
+  int listed = 0;
+  int64_t stride = 0;
+  int64_t offset[ZERO_MUON_MOST] = {};
+};
+// What is orthogonalised: x, or the gradients and momenta of tensors.
+struct OrthoSource {
+  OrthoPlaces places;
+  Mat x;         // muon: the reduced gradient
+  Mat momentum;  // muon
+  int64_t m = 0, n = 0;
+  int muon = 0, nesterov = 0;
+  float mu = 0.0f, grad_scale = 1.0f, eps = 0.0f;
+  const float* coef = nullptr;
+  // the workspace's (see ortho_space)
+  int64_t rows = 0, ld = 0;
+  int blocks = 0;
+  double* partials = nullptr;
+  uint16_t *hi = nullptr, *lo = nullptr;
+};
+struct OrthoFinish {
+  OrthoPlaces places;
+  Mat y;    // the result, or master weights
+  Mat out;  // update: the gathered parameters, or absent
+  int update = 0;
+  float rate = 0.0f, decay = 0.0f;
+  int64_t m = 0, n = 0, rows = 0, ld = 0;
+  const uint16_t* x = nullptr;
+};
+struct OrthoCall {
+  OrthoSource source;
+  OrthoFinish finish;
+  int64_t batch = 0;
+  int steps = 0;
+  float coef[ZERO_NS_MOST][3] = {};
+  void* workspace = nullptr;
+};
+// Byte offsets of a call's workspace.  X is stored in rows of ld columns, `rows`
+// of them a matrix (whole tiles, zeros around it); G and P in `side` of `side`.
+struct OrthoSpace {
+  int64_t rows, ld, side, blocks;
+  int64_t hi[2], lo, gram, poly, diag_gram, diag_poly, partials, bytes;
+};
+// Whether the kernels' counters hold such a batch.
+bool ortho_fits(int64_t m, int64_t n, int64_t batch);
+OrthoSpace ortho_space(int64_t m, int64_t n, int64_t batch);
+cudaError_t launch_orthogonalize(const OrthoCall& c, cudaStream_t st);
+
 // Bounded waits that gave up / out-of-extent records of these units.
 cudaError_t timeouts_linear(unsigned long long* out, bool reset);
 cudaError_t timeouts_fp4(unsigned long long* out, bool reset);

@@ -1,6 +1,9 @@
 // C entry points of the layer-computation operators: argument checks and
 // kernel parameters.  Every rejected call returns before any launch.
 #include <math.h>
+
+#include <initializer_list>
+
 #include <nvtx3/nvToolsExt.h>
 
 #include "zero_ops.h"
@@ -497,4 +500,147 @@ extern "C" int zero_fp4_linear_dweight(const zero_fp4_t* dy, const zero_fp4_t* x
   p.epi.out = mat(dw, lddw, dwdtype);
   if (accumulate) p.epi.residual = p.epi.out;
   return cuda_status(zk::launch_fp4_product(p, zk::LIN_FORWARD, (cudaStream_t)stream));
+}
+
+namespace {
+
+int check_ns(const zero_newton_schulz_t* ns) {
+  if (!ns || ns->steps < 0 || ns->steps > ZERO_NS_MOST) return ZERO_EINVAL;
+  if (!isfinite(ns->eps) || ns->eps < 0.0f) return ZERO_EINVAL;
+  for (int i = 0; i < ns->steps; ++i)
+    for (float c : ns->coef[i])
+      if (!isfinite(c)) return ZERO_EINVAL;
+  return ZERO_OK;
+}
+void put_ns(const zero_newton_schulz_t* ns, zk::OrthoCall* c) {
+  c->steps = ns->steps;
+  c->source.eps = ns->eps;
+  for (int i = 0; i < ns->steps; ++i)
+    for (int q = 0; q < 3; ++q) c->coef[i][q] = ns->coef[i][q];
+}
+
+int check_batch(int64_t m, int64_t n, int64_t batch) {
+  ZERO_TRY(check_sizes(m, n, batch));
+  return zk::ortho_fits(m, n, batch) ? ZERO_OK : ZERO_ERANGE;
+}
+
+int check_scratch(const void* workspace, int64_t bytes, int64_t m, int64_t n, int64_t batch) {
+  const int64_t need = m > 0 && n > 0 && batch > 0 ? zk::ortho_space(m, n, batch).bytes : 0;
+  if (bytes < need || (need > 0 && !workspace)) return ZERO_EINVAL;
+  return ((uintptr_t)workspace & 15u) == 0 ? ZERO_OK : ZERO_EALIGN;
+}
+
+// Matrices of a batch: none begins inside the one before.
+int check_stride(int64_t stride, int64_t ld, int64_t m, int64_t n, int64_t batch) {
+  if (batch <= 1 || m == 0 || n == 0) return ZERO_OK;
+  if (stride < (m - 1) * ld + n) return ZERO_EINVAL;
+  return stride < ((int64_t)1 << 62) / batch ? ZERO_OK : ZERO_ERANGE;
+}
+
+int check_flat(const void* p) {
+  if (!p) return ZERO_EINVAL;
+  return ((uintptr_t)p & 15u) == 0 ? ZERO_OK : ZERO_EALIGN;
+}
+
+}  // namespace
+
+extern "C" int zero_orthogonalize_workspace(int64_t m, int64_t n, int64_t batch,
+                                            int64_t* bytes) {
+  if (!bytes) return ZERO_EINVAL;
+  ZERO_TRY(check_batch(m, n, batch));
+  *bytes = m > 0 && n > 0 && batch > 0 ? zk::ortho_space(m, n, batch).bytes : 0;
+  return ZERO_OK;
+}
+
+extern "C" int zero_orthogonalize(const void* x, int64_t ldx, int64_t stride_x,
+                                  zero_dtype_t xdtype, int64_t m, int64_t n, int64_t batch,
+                                  const zero_newton_schulz_t* ns, void* y, int64_t ldy,
+                                  int64_t stride_y, void* workspace, int64_t workspace_bytes,
+                                  zero_stream_t stream) {
+  NvtxRange nvtx("zero_orthogonalize");
+  ZERO_TRY(check_batch(m, n, batch));
+  ZERO_TRY(check_ns(ns));
+  ZERO_TRY(check_mat(x, ldx, xdtype, batch ? m : 0, n));
+  ZERO_TRY(check_mat(y, ldy, ZERO_BF16, batch ? m : 0, n));
+  ZERO_TRY(check_stride(stride_x, ldx, m, n, batch));
+  ZERO_TRY(check_stride(stride_y, ldy, m, n, batch));
+  if (same(y, x) && (xdtype != ZERO_BF16 || ldy != ldx || (batch > 1 && stride_y != stride_x)))
+    return ZERO_EINVAL;
+  ZERO_TRY(check_scratch(workspace, workspace_bytes, m, n, batch));
+  if (same(workspace, x) || same(workspace, y)) return ZERO_EINVAL;
+  zk::OrthoCall c;
+  put_ns(ns, &c);
+  c.source.x = mat(x, ldx, xdtype);
+  c.source.places.stride = stride_x;
+  c.source.m = m;
+  c.source.n = n;
+  c.finish.y = mat(y, ldy, ZERO_BF16);
+  c.finish.places.stride = stride_y;
+  c.batch = batch;
+  c.workspace = workspace;
+  return cuda_status(zk::launch_orthogonalize(c, (cudaStream_t)stream));
+}
+
+extern "C" int zero_muon_workspace(int64_t rows, int64_t cols, int32_t count, int64_t* bytes) {
+  if (count < 0) return ZERO_EINVAL;
+  if (count > ZERO_MUON_MOST) return ZERO_ERANGE;
+  return zero_orthogonalize_workspace(rows, cols, count, bytes);
+}
+
+extern "C" int zero_muon_step(const zero_plan_t* plan, const int64_t* tensors, int32_t count,
+                              int64_t rows, int64_t cols, float* master, float* momentum,
+                              const float* reduced, const zero_muon_t* hp, const float* d_coef,
+                              void* out, zero_dtype_t out_dtype, void* workspace,
+                              int64_t workspace_bytes, zero_stream_t stream) {
+  NvtxRange nvtx("zero_muon_step");
+  if (!plan || count < 0 || (count > 0 && !tensors)) return ZERO_EINVAL;
+  if (count > ZERO_MUON_MOST) return ZERO_ERANGE;
+  ZERO_TRY(check_batch(rows, cols, count));
+  if (!hp || hp->reserved != 0) return ZERO_EINVAL;
+  for (float v : {hp->lr, hp->momentum, hp->weight_decay, hp->grad_scale, hp->scale})
+    if (!isfinite(v)) return ZERO_EINVAL;
+  if (!(hp->momentum >= 0.0f && hp->momentum < 1.0f)) return ZERO_EINVAL;
+  ZERO_TRY(check_ns(&hp->ns));
+  ZERO_TRY(check_flat(master));
+  ZERO_TRY(check_flat(momentum));
+  ZERO_TRY(check_flat(reduced));
+  if (out) {
+    ZERO_TRY(check_dtype(out_dtype));
+    ZERO_TRY(check_flat(out));
+  }
+  if (((uintptr_t)d_coef & 3u) != 0) return ZERO_EALIGN;
+  if (same(master, momentum) || same(master, reduced) || same(momentum, reduced) ||
+      same(out, master) || same(out, momentum) || same(out, reduced))
+    return ZERO_EINVAL;
+  zk::OrthoCall c;
+  for (int32_t i = 0; i < count; ++i) {
+    ZERO_TRY(zero_plan_tensor(plan, tensors[i], &c.source.places.offset[i], nullptr, nullptr));
+    if (plan->numels[tensors[i]] != rows * cols) return ZERO_EINVAL;
+    for (int32_t j = 0; j < i; ++j)
+      if (tensors[j] == tensors[i]) return ZERO_EINVAL;
+  }
+  ZERO_TRY(check_scratch(workspace, workspace_bytes, rows, cols, count));
+  if (same(workspace, master) || same(workspace, momentum) || same(workspace, reduced) ||
+      same(workspace, out))
+    return ZERO_EINVAL;
+  put_ns(&hp->ns, &c);
+  c.source.places.listed = 1;
+  c.source.x = mat(reduced, cols, ZERO_F32);
+  c.source.momentum = mat(momentum, cols, ZERO_F32);
+  c.source.m = rows;
+  c.source.n = cols;
+  c.source.muon = 1;
+  c.source.nesterov = hp->nesterov != 0;
+  c.source.mu = hp->momentum;
+  c.source.grad_scale = hp->grad_scale;
+  c.source.coef = d_coef;
+  c.finish.places = c.source.places;
+  c.finish.y = mat(master, cols, ZERO_F32);
+  if (out) c.finish.out = mat(out, cols, out_dtype);
+  c.finish.update = 1;
+  c.finish.rate = hp->lr * hp->scale;
+  c.finish.decay = hp->lr * hp->weight_decay;
+  c.batch = count;
+  c.workspace = workspace;
+  return cuda_status(zk::launch_orthogonalize(c, (cudaStream_t)stream));
 }
