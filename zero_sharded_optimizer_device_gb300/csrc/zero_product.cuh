@@ -863,18 +863,21 @@ __device__ __forceinline__ void mma_pair_fp4(uint32_t d, uint64_t a, uint64_t b,
         : "memory");
 }
 // The products of a stage, 256 deep.  The scales of 128 (MX) or 64 (NV) codes
-// of 128 rows make a tile.  B's columns begin `shift` rows of 32 into theirs.
-template <bool NV>
+// of 128 rows make a tile; CHUNKS tiles over B's columns, which begin `shift`
+// rows of 32 into theirs.  Straight code: what issues these instructions is
+// the bottleneck otherwise (a step of 256 x 192, NV: 1184 cycles with a loop
+// over the chunks, 580 without, where loading the operands decides).
+template <bool NV, int CHUNKS>
 __device__ __forceinline__ void mma_stage_fp4(uint32_t d, uint32_t tmem, uint64_t da, uint64_t db,
-                                              uint32_t scales, uint32_t chunks, uint32_t shift,
-                                              uint32_t bn, bool first) {
+                                              uint32_t scales, uint32_t shift, uint32_t bn,
+                                              bool first) {
   constexpr uint32_t deep = NV ? 4 : 2;
   const uint32_t sa = tmem + kScaleColumn, sb = sa + 4 * deep;
 #pragma unroll
   for (uint32_t t = 0; t < deep; ++t) {
     scales_copy(sa + 4 * t, scales + t * kScaleTile);
-    for (uint32_t c = 0; c < chunks; ++c)
-      scales_copy(sb + 8 * t + 4 * c, scales + ((1 + c) * deep + t) * kScaleTile);
+    scales_copy(sb + 8 * t, scales + (deep + t) * kScaleTile);
+    if (CHUNKS > 1) scales_copy(sb + 8 * t + 4, scales + (2 * deep + t) * kScaleTile);
   }
   // E2M1 both, M = 256; MX: scales E8M0, of which a product takes the first or
   // second two of a tile's four
@@ -1101,6 +1104,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
         tile_at(g, t, ti, tj);
         const bool sums = fused && (bias_b ? ti : tj) == 0;
         const uint32_t idesc = tj >= 0 ? idesc_n : idesc_1, sb = tj >= 0 ? step_b : 0;
+        const uint32_t shift = FP4 ? (uint32_t)tj * bn % kRowsCta / 32 : 0;
         int kb = kb0;
         for (int r = 0; r < rounds; ++r) {
           live = live && bar_wait(tempty + 8 * acc, aph ^ 1, &dead);
@@ -1116,12 +1120,19 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
                                         : operand_desc(ones, true);
             if (elect() && live) {
               if constexpr (FP4) {
-                const uint32_t scales = a_at + kBytesA + bn * kDeep, chunks = g.scale_chunks;
-                const uint32_t shift = (uint32_t)tj * bn % kRowsCta / 32;
-                if (g.scale_deep == 4)
-                  mma_stage_fp4<true>(d, tmem, da, db, scales, chunks, shift, bn, kb == start);
-                else
-                  mma_stage_fp4<false>(d, tmem, da, db, scales, chunks, shift, bn, kb == start);
+                const uint32_t scales = a_at + kBytesA + bn * kDeep;
+                const bool one = g.scale_chunks == 1;
+                if (g.scale_deep == 4) {
+                  if (one)
+                    mma_stage_fp4<true, 1>(d, tmem, da, db, scales, shift, bn, kb == start);
+                  else
+                    mma_stage_fp4<true, 2>(d, tmem, da, db, scales, shift, bn, kb == start);
+                } else {
+                  if (one)
+                    mma_stage_fp4<false, 1>(d, tmem, da, db, scales, shift, bn, kb == start);
+                  else
+                    mma_stage_fp4<false, 2>(d, tmem, da, db, scales, shift, bn, kb == start);
+                }
               } else {
 #pragma unroll
                 for (int q = 0; q < kDeep / 16; ++q)
