@@ -151,6 +151,7 @@ struct OrthoSource {
   int64_t rows = 0, ld = 0;
   int blocks = 0;
   double* partials = nullptr;
+  uint32_t* done = nullptr;  // finished tiles of each matrix
   uint16_t *hi = nullptr, *lo = nullptr;
 };
 struct OrthoFinish {
@@ -174,7 +175,7 @@ struct OrthoCall {
 // of them a matrix (whole tiles, zeros around it); G and P in `side` of `side`.
 struct OrthoSpace {
   int64_t rows, ld, side, blocks;
-  int64_t hi[2], lo, gram, poly, diag_gram, diag_poly, partials, bytes;
+  int64_t hi[2], lo, gram, poly, diag_gram, diag_poly, done, partials, bytes;
 };
 // Whether the kernels' counters hold such a batch.
 bool ortho_fits(int64_t m, int64_t n, int64_t batch);

@@ -19,6 +19,8 @@
 
 #include <cuda_fp16.h>
 
+#include <initializer_list>
+
 namespace zk {
 
 // Powers of two that operands are stored times: X, O of G, O of P.
@@ -27,64 +29,117 @@ constexpr float kScaleX = 4096.0f, kScaleG = 256.0f, kScaleP = 64.0f;
 constexpr int kBoxChunks = 2;                    // chunks in flight, two boxes each
 constexpr int kBox = 16384;                      // 128 rows of 64 fp16 columns
 constexpr int kSideBytes = 2 * kBoxChunks * kBox;
-constexpr int kStagesMost = 8;
+constexpr int kStageBytes = kBytesA + 256 * kDeep;
+constexpr int kOrthoStages = (kSmemMost - 1024 - kSideBytes) / kStageBytes;
 constexpr int kEpi0 = 4, kEpis = 16;             // epilogue warps
 constexpr int kOrthoThreads = 32 * (kEpi0 + kEpis);
 
-// ------------------------------------------------------------- the product --
-enum OrthoStep : int { GRAM = 0, POLY = 1, GROW = 2 };
+// ------------------------------------------------------------ the products --
+// One launch runs every product of every step.  A task is a tile of 256 x bn of
+// one product of one matrix; pairs of CTAs take tasks in turn, in the order
+// step, product, matrix, tile.  A task waits until its matrix has all tiles of
+// the products before, which a counter of finished tiles tells: with several
+// matrices in a batch nobody waits, and no wave of tiles ends in idle pairs.
+// Tasks only wait for tasks before them and every pair is resident (a
+// cooperative launch), so that the first unfinished task can always go on.
+enum OrthoProduct : int { GRAM = 0, POLY = 1, GROW = 2 };
 
-// D = A B over the contraction, with 256 x bn tiles of one matrix of the batch.
 struct OrthoK {
-  int kblocks, stages, bn, bn_log2;
-  int tiles, tiles_each;    // all, of one matrix
+  int kblocks, bn, bn_log2;
+  int tiles;                // of one matrix
+  int before;               // of a step's products before this one
   int tiles_j;              // GROW: across
-  int cols;                 // GROW: columns of X as stored
   int a_c, b_c;             // the operand's contraction index is the contiguous one
   int rows_a, rows_b, rows_out;  // rows of the batch's matrices, one below the other
-  int by_column;            // GROW: P's diagonal goes by column
-  int last;                 // GROW: the remainder is not needed any more
-  float a, b, c;
-  const float* diag_in;     // POLY: of G; GROW: of P
-  float* diag_out;          // GRAM, POLY
-  int diag_rows;            // of each matrix
 };
 struct OrthoMaps {
-  CUtensorMap in0, in1;     // POLY: G; GROW: X's two parts
-  CUtensorMap out0, out1;   // GRAM, POLY: result, and in boxes of 64 x 64; GROW: X's two parts
+  CUtensorMap x_a[2], x_b[2];  // GRAM's operands
+  CUtensorMap gram_a, gram_b;  // POLY's
+  CUtensorMap poly, x[2];      // GROW's
+  CUtensorMap hi[2], lo, gram, gram_t, poly_out, poly_t;  // boxes; _t of 64 x 64
+};
+struct OrthoSteps {
+  OrthoMaps maps;
+  OrthoK k[3];
+  int steps, batch, group, tiles_step;  // matrices in turn; tiles of a matrix's step
+  int cols;                 // of X as stored
+  int tall;                 // P's diagonal goes by column
+  int side;                 // elements of a diagonal
+  float *diag_gram, *diag_poly;
+  uint32_t* done;           // finished tiles of each matrix, both CTAs'
+  float coef[ZERO_NS_MOST][3];
 };
 
-struct OrthoTile {
-  int b, i0, j0, chunks;    // matrix, first row and column, 64-column pieces
+struct OrthoTask {
+  int step, product, b;
+  int i0, j0, chunks;       // first row and column, 64-column pieces
+  uint32_t needs;           // finished tiles of matrix b
+  bool mirror;              // the result's transpose has to be stored too
 };
-// Tiles of symmetric results are those of the lower triangle, row by row: row i
-// of 256 has i + 1 squares of 256, each of 256 / bn tiles.
-template <int STEP>
-__device__ __forceinline__ OrthoTile ortho_tile(const OrthoK& k, int t) {
-  OrthoTile o;
-  o.b = t / k.tiles_each;
-  t -= o.b * k.tiles_each;
-  if (STEP == GROW) {
+// Tasks of a group of matrices after those of the group before.  Tiles of
+// symmetric results are those of the lower triangle, row by row: row i of 256
+// has i + 1 squares of 256, each of 256 / bn tiles.
+__device__ __forceinline__ OrthoTask ortho_task(const OrthoSteps& s, int t) {
+  OrthoTask o;
+  const int full = s.group * s.tiles_step * s.steps, turn = t / full;
+  t -= turn * full;
+  const int left = s.batch - turn * s.group, group = left < s.group ? left : s.group;
+  const int each = group * s.tiles_step;
+  o.step = t / each;
+  t -= o.step * each;
+  o.product = t < group * s.k[POLY].before ? GRAM : t < group * s.k[GROW].before ? POLY : GROW;
+  const OrthoK& k = s.k[o.product];
+  t -= group * k.before;
+  const int b = t / k.tiles;
+  t -= b * k.tiles;
+  o.b = turn * s.group + b;
+  o.needs = 2u * (uint32_t)(o.step * s.tiles_step + k.before);
+  if (o.product == GROW) {
     const int i = t / k.tiles_j;
     o.i0 = i * 256;
     o.j0 = (t - i * k.tiles_j) << k.bn_log2;
-    const int left = k.cols - o.j0;
-    o.chunks = (left < k.bn ? left : k.bn) / 64;
+    const int rest = s.cols - o.j0;
+    o.chunks = (rest < k.bn ? rest : k.bn) / 64;
+    o.mirror = false;
   } else {
-    const int s = 8 - k.bn_log2, square = t >> s;
+    const int sub = 8 - k.bn_log2, square = t >> sub;
     int i = (int)((sqrtf(8.0f * (float)square + 1.0f) - 1.0f) * 0.5f);
     while (i * (i + 1) / 2 > square) --i;
     while ((i + 1) * (i + 2) / 2 <= square) ++i;
     o.i0 = i * 256;
-    o.j0 = (square - i * (i + 1) / 2) * 256 + ((t & ((1 << s) - 1)) << k.bn_log2);
+    o.j0 = (square - i * (i + 1) / 2) * 256 + ((t & ((1 << sub) - 1)) << k.bn_log2);
     o.chunks = k.bn / 64;
+    o.mirror = o.j0 + k.bn <= o.i0;
   }
   return o;
 }
-// Whether the result's transpose has to be stored too.
-template <int STEP>
-__device__ __forceinline__ bool mirrored(const OrthoK& k, const OrthoTile& o) {
-  return STEP != GROW && o.j0 + k.bn <= o.i0;
+__device__ __forceinline__ bool ortho_met(const OrthoSteps& s, const OrthoTask& o) {
+  uint32_t have;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(have) : "l"(s.done + o.b) : "memory");
+  return __all_sync(0xffffffffu, have >= o.needs);
+}
+// Until matrix o.b has the tiles that the task needs.  Limited as the other
+// waits are; the whole warp calls it.
+__device__ __forceinline__ bool ortho_wait(const OrthoSteps& s, const OrthoTask& o,
+                                           volatile int* dead) {
+  const long long t0 = clock64();
+  while (true) {
+    if (ortho_met(s, o)) return true;
+    int stop = *dead;
+    if (!stop && clock64() - t0 > kWaitCycles) {
+      stop = 1;
+      if (elect()) {
+        *dead = 1;
+        atomicAdd(&g_ops_timeouts, 1ull);
+      }
+    }
+    if (__any_sync(0xffffffffu, stop)) return false;
+  }
+}
+// What other CTAs' tensor copies stored before a wait is in place for this
+// thread's, and the other way round.
+__device__ __forceinline__ void fence_copies() {
+  asm volatile("fence.proxy.async;" ::: "memory");
 }
 
 __device__ __forceinline__ uint32_t box_at(int row, int unit) {  // 16-byte units, 128-byte swizzle
@@ -117,25 +172,38 @@ __device__ __forceinline__ uint4 split_halves8(float v[8]) {
   return hi;
 }
 
-// Warp 3: brings the operands of the epilogue's chunks and stores its results.
-template <int STEP>
-__device__ __forceinline__ void ortho_traffic(const OrthoMaps& maps, const OrthoK& k,
-                                              uint32_t boxes, uint32_t efull, uint32_t edone,
-                                              int first, int step, int half, volatile int* dead) {
-  constexpr uint32_t bytes = STEP == GRAM ? 0 : STEP == POLY ? kBox : 2 * kBox;
-  OrthoTile in{}, out{};
+// Warp 3: brings the operands of the epilogue's chunks, stores its results and
+// counts finished tiles.
+__device__ __forceinline__ void ortho_traffic(const OrthoSteps& s, uint32_t boxes, uint32_t efull,
+                                              uint32_t edone, int first, int tasks, int step,
+                                              int half, volatile int* dead) {
+  OrthoTask in{}, out{};
   int in_t = first, out_t = first, in_c = 0, out_c = 0;
-  if (first < k.tiles) in = out = ortho_tile<STEP>(k, first);
+  if (first < tasks) in = out = ortho_task(s, first);
   uint32_t ahead = 0, lb = 0, sb = 0, sph = 0;
-  bool live = true;
-  while (out_t < k.tiles) {
-    while (in_t < k.tiles && ahead < kBoxChunks) {
+  bool live = true, met = false;  // met: the tiles that `in` needs are there
+  while (out_t < tasks) {
+    while (in_t < tasks && ahead < kBoxChunks) {
+      if (!met && live) {
+        // (what this warp has to store may be what those wait for whom it
+        // would wait for: it waits with nothing left to store)
+        if (!ortho_met(s, in)) {
+          if (in_t != out_t) break;
+          live = ortho_wait(s, in, dead);
+        }
+        fence_copies();
+      }
+      met = true;
       const uint32_t at = boxes + lb * 2 * kBox, bar = efull + 8 * lb;
-      const int x = in.j0 + 64 * in_c, y = in.b * k.rows_out + in.i0 + half * kRowsCta;
+      const int x = in.j0 + 64 * in_c;
+      const int y = in.b * s.k[in.product].rows_out + in.i0 + half * kRowsCta;
       if (elect() && live) {
-        bar_expect(bar, bytes);
-        if (STEP != GRAM) box_load(&maps.in0, at, x, y, bar);
-        if (STEP == GROW) box_load(&maps.in1, at + kBox, x, y, bar);
+        bar_expect(bar, in.product * kBox);
+        if (in.product == POLY) box_load(&s.maps.gram, at, x, y, bar);
+        if (in.product == GROW) {
+          box_load(&s.maps.hi[in.step & 1], at, x, y, bar);
+          box_load(&s.maps.lo, at + kBox, x, y, bar);
+        }
       }
       __syncwarp();
       ++ahead;
@@ -143,7 +211,8 @@ __device__ __forceinline__ void ortho_traffic(const OrthoMaps& maps, const Ortho
       if (++in_c == in.chunks) {
         in_c = 0;
         in_t += step;
-        if (in_t < k.tiles) in = ortho_tile<STEP>(k, in_t);
+        met = false;
+        if (in_t < tasks) in = ortho_task(s, in_t);
       }
     }
     live = live && bar_wait(edone + 8 * sb, sph, dead);
@@ -151,16 +220,29 @@ __device__ __forceinline__ void ortho_traffic(const OrthoMaps& maps, const Ortho
     if (!live) break;
     const uint32_t at = boxes + sb * 2 * kBox;
     const int x = out.j0 + 64 * out_c, row = out.i0 + half * kRowsCta;
+    const int y = out.b * s.k[out.product].rows_out;
+    const bool last = out_c + 1 == out.chunks;
     if (elect()) {
-      box_store(&maps.out0, at, x, out.b * k.rows_out + row);
-      if (STEP == GROW) {
-        if (!k.last) box_store(&maps.out1, at + kBox, x, out.b * k.rows_out + row);
-      } else if (mirrored<STEP>(k, out)) {
-        box_store(&maps.out1, at + kBox, row, out.b * k.rows_out + x);
-        box_store(&maps.out1, at + kBox + kBox / 2, row + 64, out.b * k.rows_out + x);
+      if (out.product == GROW) {
+        box_store(&s.maps.hi[~out.step & 1], at, x, y + row);
+        if (out.step + 1 < s.steps) box_store(&s.maps.lo, at + kBox, x, y + row);
+      } else {
+        box_store(out.product == GRAM ? &s.maps.gram : &s.maps.poly_out, at, x, y + row);
+        if (out.mirror) {
+          const CUtensorMap* t = out.product == GRAM ? &s.maps.gram_t : &s.maps.poly_t;
+          box_store(t, at + kBox, row, y + x);
+          box_store(t, at + kBox + kBox / 2, row + 64, y + x);
+        }
       }
       asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-      asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+      if (last) {
+        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        fence_copies();
+        // behind this tile's boxes and (through the chunks' barriers) diagonals
+        asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(s.done + out.b) : "memory");
+      } else {
+        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+      }
     }
     __syncwarp();
     --ahead;
@@ -168,10 +250,11 @@ __device__ __forceinline__ void ortho_traffic(const OrthoMaps& maps, const Ortho
       sb = 0;
       sph ^= 1;
     }
-    if (++out_c == out.chunks) {
+    ++out_c;
+    if (last) {
       out_c = 0;
       out_t += step;
-      if (out_t < k.tiles) out = ortho_tile<STEP>(k, out_t);
+      if (out_t < tasks) out = ortho_task(s, out_t);
     }
   }
   // after a wait that gave up: the boxes in flight land before the CTA returns
@@ -189,12 +272,13 @@ __device__ __forceinline__ void ortho_traffic(const OrthoMaps& maps, const Ortho
 
 // 16 sums v of row `row` of the box (row `i` of the matrix), columns j.. of the
 // matrix from 16-byte unit `unit` of the box on.
-template <int STEP>
-__device__ __forceinline__ void ortho_piece(const OrthoK& k, const float* diag_in, float diag_row,
-                                            float* diag_out, bool mirror, uint32_t at, int row,
-                                            int i, int j, int unit, float v[16]) {
+template <int PRODUCT>
+__device__ __forceinline__ void ortho_piece(float ca, float cb, float cc, bool by_column,
+                                            const float* diag_in, float diag_row, float* diag_out,
+                                            bool mirror, uint32_t at, int row, int i, int j,
+                                            int unit, float v[16]) {
   float d[16];
-  if (STEP == POLY || (STEP == GROW && k.by_column)) {
+  if (PRODUCT == POLY || (PRODUCT == GROW && by_column)) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const float4 x = ld_state(diag_in + j + 4 * q);
@@ -206,7 +290,7 @@ __device__ __forceinline__ void ortho_piece(const OrthoK& k, const float* diag_i
     const uint32_t p0 = at + box_at(row, unit + h), p1 = p0 + kBox;
     float* w = v + 8 * h;
     const int on_diag = i - (j + 8 * h);  // which of the eight, if any
-    if (STEP == GRAM) {
+    if (PRODUCT == GRAM) {
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
         if (on_diag == q) {
@@ -216,15 +300,15 @@ __device__ __forceinline__ void ortho_piece(const OrthoK& k, const float* diag_i
         w[q] *= kScaleG / (kScaleX * kScaleX);
       }
       sts16(p0, to_halves8(w));
-    } else if (STEP == POLY) {
+    } else if (PRODUCT == POLY) {
       float o[8];
       halves8(lds16(p0), o);
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
-        const float s = w[q] * (1.0f / (kScaleG * kScaleG)), g = o[q] * (1.0f / kScaleG);
-        float r = k.b * g + k.c * (s + (diag_row + d[8 * h + q]) * g);
+        const float sq = w[q] * (1.0f / (kScaleG * kScaleG)), g = o[q] * (1.0f / kScaleG);
+        float r = cb * g + cc * (sq + (diag_row + d[8 * h + q]) * g);
         if (on_diag == q) {
-          diag_out[i] = k.b * diag_row + k.c * (s + diag_row * diag_row);
+          diag_out[i] = cb * diag_row + cc * (sq + diag_row * diag_row);
           r = 0.0f;
         }
         w[q] = r * kScaleP;
@@ -236,14 +320,14 @@ __device__ __forceinline__ void ortho_piece(const OrthoK& k, const float* diag_i
       halves8(lds16(p1), y);
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
-        const float f = k.a + (k.by_column ? d[8 * h + q] : diag_row);
+        const float f = ca + (by_column ? d[8 * h + q] : diag_row);
         w[q] = f * x[q] + (f * y[q] + w[q] * (1.0f / kScaleP));
       }
       sts16(p0, split_halves8(w));
       sts16(p1, to_halves8(w));
     }
   }
-  if (STEP != GROW && mirror) {
+  if (PRODUCT != GROW && mirror) {
     // element (row, c) of the box to row c, column row of two boxes of 64 x 64
     const uint32_t to = at + kBox + (uint32_t)(row >> 6) * (kBox / 2) + (uint32_t)(row & 7) * 2;
     const int u = (row & 63) >> 3;
@@ -256,28 +340,25 @@ __device__ __forceinline__ void ortho_piece(const OrthoK& k, const float* diag_i
   }
 }
 
-template <int STEP>
 __global__ void __launch_bounds__(kOrthoThreads, 1)
-    ortho_kernel(const __grid_constant__ CUtensorMap map_a,
-                 const __grid_constant__ CUtensorMap map_b, const __grid_constant__ OrthoMaps maps,
-                 const __grid_constant__ OrthoK k) {
+    ortho_kernel(const __grid_constant__ OrthoSteps s, int tasks) {
   extern __shared__ __align__(1024) unsigned char ortho_smem[];
-  __shared__ __align__(8) uint64_t bars[2 * kStagesMost + 5 + 2 * kBoxChunks];
+  __shared__ __align__(8) uint64_t bars[2 * kOrthoStages + 5 + 2 * kBoxChunks];
   __shared__ uint32_t tmem_at;
   __shared__ int dead;
+  constexpr uint32_t stages = kOrthoStages;
   const uint32_t rank = cluster_rank(), half = rank & 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t stage_bytes = kBytesA + k.bn * kDeep;
-  const uint32_t ring = smem_u32(ortho_smem), boxes = ring + k.stages * stage_bytes;
-  const uint32_t full = smem_u32(bars), empty = full + 8 * kStagesMost;
-  const uint32_t tfull = empty + 8 * kStagesMost, tempty = tfull + 16, ready = tempty + 16;
+  const uint32_t ring = smem_u32(ortho_smem), boxes = ring + stages * kStageBytes;
+  const uint32_t full = smem_u32(bars), empty = full + 8 * stages;
+  const uint32_t tfull = empty + 8 * stages, tempty = tfull + 16, ready = tempty + 16;
   const uint32_t efull = ready + 8, edone = efull + 8 * kBoxChunks;
 
   if (warp == 0 && elect()) {
     dead = 0;
-    for (int s = 0; s < k.stages; ++s) {
-      bar_init(full + 8 * s, 1);
-      bar_init(empty + 8 * s, 1);
+    for (uint32_t q = 0; q < stages; ++q) {
+      bar_init(full + 8 * q, 1);
+      bar_init(empty + 8 * q, 1);
     }
     for (int a = 0; a < 2; ++a) {
       bar_init(tfull + 8 * a, 1);
@@ -292,16 +373,10 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
   }
   __syncwarp();
   cluster_arrive();
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (warp == 1 && elect()) {
-    asm volatile("prefetch.tensormap [%0];" ::"l"(&map_a) : "memory");
-    asm volatile("prefetch.tensormap [%0];" ::"l"(&map_b) : "memory");
-    asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.out0) : "memory");
-  }
   if (warp == 2) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(&tmem_at)),
-                 "r"(2 * k.bn)
+                 "r"(512)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -312,7 +387,6 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
     if (elect()) bar_arrive_cluster(remote(ready, 0));
     __syncwarp();
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   uint32_t tmem = 0;
   if (warp == 1 || warp == 2 || warp >= kEpi0) {
     asm volatile("bar.sync 1, %0;" ::"n"((kEpis + 2) * 32) : "memory");
@@ -323,41 +397,57 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
   if (early) cluster_arrive();
 
   if (warp == 0) {
-    const uint32_t full_lead = remote(full, 0), stages = k.stages, b_bytes = k.bn * kDeep;
-    const bool a_c = k.a_c, b_c = k.b_c;
-    uint32_t s = 0, ph = 0, end_s = 0, end_ph = 0;  // end: where a wait gave up
+    const uint32_t full_lead = remote(full, 0);
+    uint32_t st = 0, ph = 0, end_s = 0, end_ph = 0;  // end: where a wait gave up
     bool live = true;
-    for (int t = first; t < k.tiles; t += clusters) {
-      const OrthoTile o = ortho_tile<STEP>(k, t);
+    for (int t = first; t < tasks; t += clusters) {
+      const OrthoTask o = ortho_task(s, t);
+      const OrthoK& k = s.k[o.product];
       const int i0 = o.i0 + (int)half * kRowsCta, j0 = o.j0 + (int)half * (k.bn / 2);
-      const int ya = o.b * k.rows_a, yb = o.b * k.rows_b;
-      for (int kb = 0; kb < k.kblocks; ++kb) {
+      const int ya = o.b * k.rows_a, yb = o.b * k.rows_b, kblocks = k.kblocks;
+      const uint32_t b_bytes = k.bn * kDeep;
+      const bool a_c = k.a_c, b_c = k.b_c, wide = k.bn > 128;
+      const int now = o.step & 1;
+      const CUtensorMap* x = &s.maps.x[now];
+      const CUtensorMap* map_a = o.product == GRAM   ? &s.maps.x_a[now]
+                                 : o.product == POLY ? &s.maps.gram_a
+                                 : s.tall            ? x
+                                                     : &s.maps.poly;
+      const CUtensorMap* map_b = o.product == GRAM   ? &s.maps.x_b[now]
+                                 : o.product == POLY ? &s.maps.gram_b
+                                 : s.tall            ? &s.maps.poly
+                                                     : x;
+      if (live) {
+        live = ortho_wait(s, o, &dead);
+        fence_copies();
+      }
+      for (int kb = 0; kb < kblocks; ++kb) {
         if (live) {
-          live = bar_wait(empty + 8 * s, ph ^ 1, &dead);
-          end_s = s;
+          live = bar_wait(empty + 8 * st, ph ^ 1, &dead);
+          end_s = st;
           end_ph = ph;
         }
-        const uint32_t a_at = ring + s * stage_bytes, b_at = a_at + kBytesA;
-        const uint32_t bar = full_lead + 8 * s;
+        const uint32_t a_at = ring + st * kStageBytes, b_at = a_at + kBytesA;
+        const uint32_t bar = full_lead + 8 * st;
         const int c = kb * kDeep;
         if (elect() && live) {
-          if (half == 0) bar_expect(full + 8 * s, 2 * (kBytesA + b_bytes));
+          if (half == 0) bar_expect(full + 8 * st, 2 * (kBytesA + b_bytes));
           if (a_c) {
-            tma_load(&map_a, a_at, c, ya + i0, bar);
+            tma_load(map_a, a_at, c, ya + i0, bar);
           } else {
-            tma_load(&map_a, a_at, i0, ya + c, bar);
-            tma_load(&map_a, a_at + 8192, i0 + 64, ya + c, bar);
+            tma_load(map_a, a_at, i0, ya + c, bar);
+            tma_load(map_a, a_at + 8192, i0 + 64, ya + c, bar);
           }
           if (b_c) {
-            tma_load(&map_b, b_at, c, yb + j0, bar);
+            tma_load(map_b, b_at, c, yb + j0, bar);
           } else {
-            tma_load(&map_b, b_at, j0, yb + c, bar);
-            if (k.bn > 128) tma_load(&map_b, b_at + 8192, j0 + 64, yb + c, bar);
+            tma_load(map_b, b_at, j0, yb + c, bar);
+            if (wide) tma_load(map_b, b_at + 8192, j0 + 64, yb + c, bar);
           }
         }
         __syncwarp();
-        if (++s == stages) {
-          s = 0;
+        if (++st == stages) {
+          st = 0;
           ph ^= 1;
         }
       }
@@ -374,32 +464,33 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
   } else if (warp == 1) {
     if (half == 0) {
       const uint16_t mask = 3;
-      const bool a_c = k.a_c, b_c = k.b_c;
-      // fp32 sums of fp16 values, M = 256, N = bn
-      const uint32_t idesc = (1u << 4) | ((a_c ? 0u : 1u) << 15) | ((b_c ? 0u : 1u) << 16) |
-                             ((uint32_t)(k.bn >> 3) << 17) | (16u << 24);
-      const uint32_t step_a = a_c ? 2 : 128, step_b = b_c ? 2 : 128;
-      const uint32_t stages = k.stages;
-      uint32_t s = 0, ph = 0, acc = 0, aph = 0;
+      uint32_t st = 0, ph = 0, acc = 0, aph = 0;
       bool live = bar_wait(ready, 0, &dead);
-      for (int t = first; t < k.tiles; t += clusters) {
+      for (int t = first; t < tasks; t += clusters) {
+        const OrthoK& k = s.k[ortho_task(s, t).product];
+        const bool a_c = k.a_c, b_c = k.b_c;
+        const int kblocks = k.kblocks;
+        // fp32 sums of fp16 values, M = 256, N = bn
+        const uint32_t idesc = (1u << 4) | ((a_c ? 0u : 1u) << 15) | ((b_c ? 0u : 1u) << 16) |
+                               ((uint32_t)(k.bn >> 3) << 17) | (16u << 24);
+        const uint32_t step_a = a_c ? 2 : 128, step_b = b_c ? 2 : 128;
         live = live && bar_wait(tempty + 8 * acc, aph ^ 1, &dead);
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint32_t d = tmem + acc * k.bn;
-        for (int kb = 0; kb < k.kblocks; ++kb) {
-          live = live && bar_wait(full + 8 * s, ph, &dead);
+        const uint32_t d = tmem + acc * 256;
+        for (int kb = 0; kb < kblocks; ++kb) {
+          live = live && bar_wait(full + 8 * st, ph, &dead);
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          const uint32_t a_at = ring + s * stage_bytes;
+          const uint32_t a_at = ring + st * kStageBytes;
           const uint64_t da = operand_desc(a_at, a_c), db = operand_desc(a_at + kBytesA, b_c);
           if (elect() && live) {
 #pragma unroll
             for (int q = 0; q < kDeep / 16; ++q)
               mma_pair(d, da + q * step_a, db + q * step_b, idesc, kb > 0 || q > 0);
-            commit_pair(empty + 8 * s, mask);
+            commit_pair(empty + 8 * st, mask);
           }
           __syncwarp();
-          if (++s == stages) {
-            s = 0;
+          if (++st == stages) {
+            st = 0;
             ph ^= 1;
           }
         }
@@ -413,29 +504,34 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
     }
     __syncwarp();
   } else if (warp == 3) {
-    ortho_traffic<STEP>(maps, k, boxes, efull, edone, first, clusters, (int)half, &dead);
+    ortho_traffic(s, boxes, efull, edone, first, tasks, clusters, (int)half, &dead);
     __syncwarp();
   } else if (warp >= kEpi0) {
     const int w = (warp - kEpi0) & 3, set = (warp - kEpi0) >> 2;
     const int row = w * 32 + lane;
     const uint32_t tempty_lead = remote(tempty, 0);
+    const bool tall = s.tall;
     uint32_t acc = 0, aph = 0, eb = 0, eph = 0;
     bool ok = true;
-    for (int t = first; t < k.tiles && ok; t += clusters) {
-      const OrthoTile o = ortho_tile<STEP>(k, t);
+    for (int t = first; t < tasks && ok; t += clusters) {
+      const OrthoTask o = ortho_task(s, t);
       const int i = o.i0 + (int)half * kRowsCta + row;
-      const float* diag_in = STEP == GRAM ? nullptr : k.diag_in + (int64_t)o.b * k.diag_rows;
-      float* diag_out = STEP == GROW ? nullptr : k.diag_out + (int64_t)o.b * k.diag_rows;
-      const float diag_row =
-          STEP == POLY || (STEP == GROW && !k.by_column) ? *(volatile const float*)(diag_in + i)
-                                                         : 0.0f;
-      const bool mirror = mirrored<STEP>(k, o);
+      const int64_t diag = (int64_t)o.b * s.side;
+      const float* diag_in = (o.product == POLY ? s.diag_gram : s.diag_poly) + diag;
+      float* diag_out = (o.product == GRAM ? s.diag_gram : s.diag_poly) + diag;
+      const float ca = s.coef[o.step][0], cb = s.coef[o.step][1], cc = s.coef[o.step][2];
+      float diag_row = 0.0f;
+      if (o.product != GRAM) {  // (the diagonal, under the tile's products)
+        ok = ortho_wait(s, o, &dead);
+        if (!ok) break;
+        if (o.product == POLY || !tall) diag_row = *(volatile const float*)(diag_in + i);
+      }
       ok = bar_wait(tfull + 8 * acc, aph, &dead);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      const uint32_t d = tmem + ((uint32_t)(w * 32) << 16) + acc * k.bn + set * 16;
-      for (int cc = 0; cc < o.chunks; ++cc) {
+      const uint32_t d = tmem + ((uint32_t)(w * 32) << 16) + acc * 256 + set * 16;
+      for (int c = 0; c < o.chunks; ++c) {
         const uint32_t b = eb;
         ok = bar_wait(efull + 8 * b, eph, &dead);
         ok = __all_sync(0xffffffffu, ok);
@@ -445,12 +541,21 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
           eph ^= 1;
         }
         uint32_t r[16];
-        tmem_load16(d + cc * 64, r);
+        tmem_load16(d + c * 64, r);
         float v[16];
 #pragma unroll
         for (int q = 0; q < 16; ++q) v[q] = __uint_as_float(r[q]);
-        ortho_piece<STEP>(k, diag_in, diag_row, diag_out, mirror, boxes + b * 2 * kBox, row, i,
-                          o.j0 + cc * 64 + set * 16, set * 2, v);
+        const uint32_t at = boxes + b * 2 * kBox;
+        const int j = o.j0 + c * 64 + set * 16;
+        if (o.product == GRAM)
+          ortho_piece<GRAM>(ca, cb, cc, tall, diag_in, diag_row, diag_out, o.mirror, at, row, i, j,
+                            set * 2, v);
+        else if (o.product == POLY)
+          ortho_piece<POLY>(ca, cb, cc, tall, diag_in, diag_row, diag_out, o.mirror, at, row, i, j,
+                            set * 2, v);
+        else
+          ortho_piece<GROW>(ca, cb, cc, tall, diag_in, diag_row, diag_out, o.mirror, at, row, i, j,
+                            set * 2, v);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) bar_arrive(edone + 8 * b);
@@ -471,8 +576,7 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
   cluster_wait();
   if (warp == 2) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                 "r"(2 * k.bn));
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
   }
 }
 
@@ -558,6 +662,7 @@ __global__ void __launch_bounds__(kThreads) ortho_scale(const __grid_constant__ 
   __shared__ float factor_at;
   after_previous_kernel();
   const int b = blockIdx.y;
+  if (blockIdx.x == 0 && threadIdx.x == 0) s.done[b] = 0;
   if (threadIdx.x < 32) {
     double sum[3] = {};
     for (int i = threadIdx.x; i < s.blocks; i += 32)
@@ -651,8 +756,8 @@ bool ortho_fits(int64_t m, int64_t n, int64_t batch) {
   // rows one below the other, tiles and grids in 32 bits; sizes far from 64
   const int64_t k = up(m < n ? m : n, 256), rows = up(m, 256), cols = up(n, 128);
   return batch < 65536 && rows * batch < (1ll << 31) && k * batch < (1ll << 31) &&
-         rows / 256 * (cols / 128) < (1ll << 30) / (batch + 1) &&
-         k / 256 * (k / 256 + 1) < (1ll << 30) / (batch + 1);
+         rows / 256 * (cols / 128) < (1ll << 25) / (batch + 1) &&
+         k / 256 * (k / 256 + 1) < (1ll << 25) / (batch + 1);
 }
 
 OrthoSpace ortho_space(int64_t m, int64_t n, int64_t batch) {
@@ -680,6 +785,7 @@ OrthoSpace ortho_space(int64_t m, int64_t n, int64_t batch) {
   w.poly = take(g);
   w.diag_gram = take(batch * w.side * 4);
   w.diag_poly = take(batch * w.side * 4);
+  w.done = take(batch * 4);
   w.partials = take(batch * w.blocks * 3 * 8);
   w.bytes = at;
   return w;
@@ -697,39 +803,44 @@ static bool half_map(CUtensorMap* map, void* p, int64_t cols, int64_t rows, int 
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int STEP>
-static cudaError_t launch_ortho(const CUtensorMap& a, const CUtensorMap& b, const OrthoMaps& maps,
-                                OrthoK& k, cudaStream_t st) {
-  static std::atomic<unsigned long long> done{0};
+// Pairs of CTAs that are resident together: what a cooperative launch may have.
+static cudaError_t ortho_pairs(cudaLaunchConfig_t& cfg, int* pairs) {
+  static std::atomic<int> known[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  const unsigned long long bit = 1ull << (dev & 63);
-  constexpr int most = kSmemMost - 1024;  // the rest is the kernel's static shared memory
-  if (!(done.load() & bit)) {
-    e = cudaFuncSetAttribute(ortho_kernel<STEP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             most);
+  int n = known[dev & 63].load();
+  if (n == 0) {
+    e = cudaFuncSetAttribute(ortho_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)cfg.dynamicSmemBytes);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, ortho_kernel, &cfg);
     if (e != cudaSuccess) return e;
-    done.fetch_or(bit);
+    if (n < 1) return cudaErrorInvalidConfiguration;
+    known[dev & 63].store(n);
   }
-  const int stage = kBytesA + k.bn * kDeep;
-  k.stages = (most - kSideBytes) / stage;
-  if (k.stages > kStagesMost) k.stages = kStagesMost;
-  const int pairs = sm_count() / 2, clusters = k.tiles < pairs ? k.tiles : pairs;
+  *pairs = n;
+  return cudaSuccess;
+}
+static cudaError_t launch_ortho(const OrthoSteps& s, int64_t tasks, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)clusters * 2);
+  cfg.gridDim = dim3((unsigned)(sm_count() / 2 * 2));
   cfg.blockDim = dim3(kOrthoThreads);
-  cfg.dynamicSmemBytes = (size_t)k.stages * stage + kSideBytes;
+  cfg.dynamicSmemBytes = (size_t)kOrthoStages * kStageBytes + kSideBytes;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeCooperative;
+  attr[1].val.cooperative = 1;
   cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int pairs = 0;
+  cudaError_t e = ortho_pairs(cfg, &pairs);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3((unsigned)(2 * (tasks < pairs ? tasks : pairs)));
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, ortho_kernel<STEP>, a, b, maps, k);
+  return cudaLaunchKernelEx(&cfg, ortho_kernel, s, (int)tasks);
 }
 
 // Tile width: waves of tiles times a tile's steps (see zero_product.cuh's
@@ -753,6 +864,7 @@ cudaError_t launch_orthogonalize(const OrthoCall& c, cudaStream_t st) {
   s.rows = w.rows;
   s.ld = w.ld;
   s.blocks = (int)w.blocks;
+  s.done = reinterpret_cast<uint32_t*>(base + w.done);
   s.partials = reinterpret_cast<double*>(base + w.partials);
   s.hi = reinterpret_cast<uint16_t*>(base + w.hi[0]);
   s.lo = reinterpret_cast<uint16_t*>(base + w.lo);
@@ -765,86 +877,72 @@ cudaError_t launch_orthogonalize(const OrthoCall& c, cudaStream_t st) {
   e = launch_next(ortho_scale, grid, dim3(kThreads), st, s);
   if (e != cudaSuccess) return e;
 
-  void* hi[2] = {base + w.hi[0], base + w.hi[1]};
-  void *gram = base + w.gram, *poly = base + w.poly, *lo = base + w.lo;
-  const int64_t all = batch * w.rows, sides = batch * w.side;
-  const int64_t kb_far = (far + kDeep - 1) / kDeep, kb_k = (k + kDeep - 1) / kDeep;
-  const int bn_gram = tile_width(batch * squares, batch * squares * 2, kb_far);
-  const int bn_poly = tile_width(batch * squares, batch * squares * 2, kb_k);
-  const int bn_grow = tile_width(batch * rows * (up(w.ld, 256) / 256),
-                                 batch * rows * (up(w.ld, 128) / 128), kb_k);
-  // Operands by rows (boxes of 128 rows, or half a tile's width of them) or, where
-  // the contraction runs down the rows, in boxes of 64 of them.
-  CUtensorMap x_a[2], x_b[2], gram_a, gram_b, poly_a, poly_b;
-  OrthoMaps g{}, p{}, x[2];
-  bool ok = true;
-  for (int i = 0; i < 2; ++i) {
-    // in the Gram product, and in the last product of a step
-    ok = ok && half_map(&x_a[i], hi[i], w.ld, all, tall ? 64 : kRowsCta) &&
-         half_map(&x_b[i], hi[i], w.ld, all, tall ? 64 : bn_gram / 2);
-    x[i] = OrthoMaps{};
-    ok = ok && half_map(&x[i].in0, hi[i], w.ld, all, kRowsCta) &&
-         half_map(&x[i].in1, lo, w.ld, all, kRowsCta) &&
-         half_map(&x[i].out0, hi[1 - i], w.ld, all, kRowsCta) &&
-         half_map(&x[i].out1, lo, w.ld, all, kRowsCta);
-  }
-  CUtensorMap grow_x[2];
-  for (int i = 0; i < 2; ++i)
-    ok = ok && half_map(&grow_x[i], hi[i], w.ld, all, tall ? kRowsCta : 64);
-  ok = ok && half_map(&gram_a, gram, w.side, sides, kRowsCta) &&
-       half_map(&gram_b, gram, w.side, sides, bn_poly / 2) &&
-       half_map(&poly_a, poly, w.side, sides, kRowsCta) &&
-       half_map(&poly_b, poly, w.side, sides, bn_grow / 2) &&
-       half_map(&g.out0, gram, w.side, sides, kRowsCta) &&
-       half_map(&g.out1, gram, w.side, sides, 64) &&
-       half_map(&p.in0, gram, w.side, sides, kRowsCta) &&
-       half_map(&p.out0, poly, w.side, sides, kRowsCta) &&
-       half_map(&p.out1, poly, w.side, sides, 64);
-  if (!ok) return cudaErrorInvalidValue;
-
-  auto log2_of = [](int bn) { return bn == 256 ? 8 : 7; };
-  OrthoK kg{}, kp{}, kx{};
-  kg.kblocks = (int)kb_far;
-  kg.bn = bn_gram;
-  kg.a_c = kg.b_c = !tall;
-  kg.rows_a = kg.rows_b = (int)w.rows;
-  kg.rows_out = (int)w.side;
-  kg.diag_out = reinterpret_cast<float*>(base + w.diag_gram);
-  kp.kblocks = (int)kb_k;
-  kp.bn = bn_poly;
-  kp.a_c = kp.b_c = 1;
-  kp.rows_a = kp.rows_b = kp.rows_out = (int)w.side;
-  kp.diag_in = kg.diag_out;
-  kp.diag_out = reinterpret_cast<float*>(base + w.diag_poly);
-  kx.kblocks = (int)kb_k;
-  kx.bn = bn_grow;
-  kx.a_c = 1;
-  kx.b_c = tall;
-  kx.rows_a = (int)(tall ? w.rows : w.side);
-  kx.rows_b = (int)(tall ? w.side : w.rows);
-  kx.rows_out = (int)w.rows;
-  kx.by_column = tall;
-  kx.cols = (int)w.ld;
-  kx.tiles_j = (int)(up(w.ld, bn_grow) / bn_grow);
-  kx.tiles_each = (int)(rows * kx.tiles_j);
-  kx.diag_in = kp.diag_out;
-  for (OrthoK* q : {&kg, &kp, &kx}) {
-    q->bn_log2 = log2_of(q->bn);
-    q->diag_rows = (int)w.side;
-    if (q != &kx) q->tiles_each = (int)(squares * (256 / q->bn));
-    q->tiles = (int)(batch * q->tiles_each);
-  }
-  int now = 0;
-  for (int step = 0; step < c.steps; ++step, now ^= 1) {
-    kp.b = c.coef[step][1];
-    kp.c = c.coef[step][2];
-    kx.a = c.coef[step][0];
-    kx.last = step + 1 == c.steps;
-    e = launch_ortho<GRAM>(x_a[now], x_b[now], g, kg, st);
-    if (e == cudaSuccess) e = launch_ortho<POLY>(gram_a, gram_b, p, kp, st);
-    if (e == cudaSuccess)
-      e = launch_ortho<GROW>(tall ? grow_x[now] : poly_a, tall ? poly_b : grow_x[now], x[now], kx,
-                             st);
+  if (c.steps > 0) {
+    OrthoSteps p{};
+    const int64_t sq = batch * squares, kb_far = (far + kDeep - 1) / kDeep,
+                  kb_k = (k + kDeep - 1) / kDeep;
+    const int bn_gram = tile_width(sq, sq * 2, kb_far), bn_poly = tile_width(sq, sq * 2, kb_k);
+    const int bn_grow = tile_width(batch * rows * (up(w.ld, 256) / 256),
+                                   batch * rows * (up(w.ld, 128) / 128), kb_k);
+    // Operands by rows (boxes of 128 rows, or half a tile's width of them) or,
+    // where the contraction runs down the rows, in boxes of 64 of them.
+    const int64_t all = batch * w.rows, sides = batch * w.side;
+    void *gram = base + w.gram, *poly = base + w.poly;
+    OrthoMaps& m = p.maps;
+    bool ok = true;
+    for (int i = 0; i < 2; ++i) {
+      void* hi = base + w.hi[i];
+      ok = ok && half_map(&m.x_a[i], hi, w.ld, all, tall ? 64 : kRowsCta) &&
+           half_map(&m.x_b[i], hi, w.ld, all, tall ? 64 : bn_gram / 2) &&
+           half_map(&m.x[i], hi, w.ld, all, tall ? kRowsCta : 64) &&
+           half_map(&m.hi[i], hi, w.ld, all, kRowsCta);
+    }
+    ok = ok && half_map(&m.lo, base + w.lo, w.ld, all, kRowsCta) &&
+         half_map(&m.gram_a, gram, w.side, sides, kRowsCta) &&
+         half_map(&m.gram_b, gram, w.side, sides, bn_poly / 2) &&
+         half_map(&m.poly, poly, w.side, sides, tall ? bn_grow / 2 : kRowsCta) &&
+         half_map(&m.gram, gram, w.side, sides, kRowsCta) &&
+         half_map(&m.gram_t, gram, w.side, sides, 64) &&
+         half_map(&m.poly_out, poly, w.side, sides, kRowsCta) &&
+         half_map(&m.poly_t, poly, w.side, sides, 64);
+    if (!ok) return cudaErrorInvalidValue;
+    OrthoK &g = p.k[GRAM], &q = p.k[POLY], &x = p.k[GROW];
+    g.kblocks = (int)kb_far;
+    g.bn = bn_gram;
+    g.a_c = g.b_c = !tall;
+    g.rows_a = g.rows_b = (int)w.rows;
+    g.rows_out = (int)w.side;
+    g.tiles = (int)(squares * (256 / g.bn));
+    q.kblocks = (int)kb_k;
+    q.bn = bn_poly;
+    q.a_c = q.b_c = 1;
+    q.rows_a = q.rows_b = q.rows_out = (int)w.side;
+    q.tiles = (int)(squares * (256 / q.bn));
+    q.before = g.tiles;
+    x.kblocks = (int)kb_k;
+    x.bn = bn_grow;
+    x.a_c = 1;
+    x.b_c = tall;
+    x.rows_a = (int)(tall ? w.rows : w.side);
+    x.rows_b = (int)(tall ? w.side : w.rows);
+    x.rows_out = (int)w.rows;
+    x.tiles_j = (int)(up(w.ld, x.bn) / x.bn);
+    x.tiles = (int)(rows * x.tiles_j);
+    x.before = q.before + q.tiles;
+    for (OrthoK* o : {&g, &q, &x}) o->bn_log2 = o->bn == 256 ? 8 : 7;
+    p.steps = c.steps;
+    p.batch = (int)batch;
+    p.tiles_step = x.before + x.tiles;
+    p.group = (int)batch;
+    p.cols = (int)w.ld;
+    p.tall = tall;
+    p.side = (int)w.side;
+    p.diag_gram = reinterpret_cast<float*>(base + w.diag_gram);
+    p.diag_poly = reinterpret_cast<float*>(base + w.diag_poly);
+    p.done = s.done;
+    for (int i = 0; i < c.steps; ++i)
+      for (int j = 0; j < 3; ++j) p.coef[i][j] = c.coef[i][j];
+    e = launch_ortho(p, (int64_t)p.tiles_step * batch * c.steps, st);
     if (e != cudaSuccess) return e;
   }
   OrthoFinish f = c.finish;
@@ -852,7 +950,7 @@ cudaError_t launch_orthogonalize(const OrthoCall& c, cudaStream_t st) {
   f.n = n;
   f.rows = w.rows;
   f.ld = w.ld;
-  f.x = reinterpret_cast<const uint16_t*>(hi[now]);
+  f.x = reinterpret_cast<const uint16_t*>(base + w.hi[c.steps & 1]);
   const int64_t units = ((n + 7) / 8 * m + kThreads - 1) / kThreads;
   return launch_next(ortho_finish, dim3((unsigned)(units < share ? units : share), (unsigned)batch),
                      dim3(kThreads), st, f);
