@@ -26,7 +26,10 @@ namespace zk {
 // Powers of two that operands are stored times: X, O of G, O of P.
 constexpr float kScaleX = 4096.0f, kScaleG = 256.0f, kScaleP = 64.0f;
 
-constexpr int kBoxChunks = 2;                    // chunks in flight, two boxes each
+// A chunk of 64 columns is in flight for ~4000 cycles (operands 1300, epilogue
+// 1300, store 1500) and a tile 64 deep per operand stage 520: three chunks of
+// two boxes beside four stages.
+constexpr int kBoxChunks = 3;
 constexpr int kBox = 16384;                      // 128 rows of 64 fp16 columns
 constexpr int kSideBytes = 2 * kBoxChunks * kBox;
 constexpr int kStageBytes = kBytesA + 256 * kDeep;
@@ -172,100 +175,102 @@ __device__ __forceinline__ uint4 split_halves8(float v[8]) {
   return hi;
 }
 
-// Warp 3: brings the operands of the epilogue's chunks, stores its results and
-// counts finished tiles.
-__device__ __forceinline__ void ortho_traffic(const OrthoSteps& s, uint32_t boxes, uint32_t efull,
-                                              uint32_t edone, int first, int tasks, int step,
-                                              int half, volatile int* dead) {
-  OrthoTask in{}, out{};
-  int in_t = first, out_t = first, in_c = 0, out_c = 0;
-  if (first < tasks) in = out = ortho_task(s, first);
-  uint32_t ahead = 0, lb = 0, sb = 0, sph = 0;
-  bool live = true, met = false;  // met: the tiles that `in` needs are there
-  while (out_t < tasks) {
-    while (in_t < tasks && ahead < kBoxChunks) {
-      if (!met && live) {
-        // (what this warp has to store may be what those wait for whom it
-        // would wait for: it waits with nothing left to store)
-        if (!ortho_met(s, in)) {
-          if (in_t != out_t) break;
-          live = ortho_wait(s, in, dead);
-        }
-        fence_copies();
-      }
-      met = true;
-      const uint32_t at = boxes + lb * 2 * kBox, bar = efull + 8 * lb;
-      const int x = in.j0 + 64 * in_c;
-      const int y = in.b * s.k[in.product].rows_out + in.i0 + half * kRowsCta;
-      if (elect() && live) {
-        bar_expect(bar, in.product * kBox);
-        if (in.product == POLY) box_load(&s.maps.gram, at, x, y, bar);
-        if (in.product == GROW) {
-          box_load(&s.maps.hi[in.step & 1], at, x, y, bar);
-          box_load(&s.maps.lo, at + kBox, x, y, bar);
-        }
-      }
-      __syncwarp();
-      ++ahead;
-      if (++lb == kBoxChunks) lb = 0;
-      if (++in_c == in.chunks) {
-        in_c = 0;
-        in_t += step;
-        met = false;
-        if (in_t < tasks) in = ortho_task(s, in_t);
+// A walk over the chunks of a pair's tasks, in order, and the ring's slots.
+struct OrthoWalk {
+  OrthoTask o{};
+  int t, c = 0;
+  uint32_t slot = 0, phase = 0;
+  __device__ __forceinline__ OrthoWalk(const OrthoSteps& s, int first, int tasks) : t(first) {
+    if (t < tasks) o = ortho_task(s, t);
+  }
+  __device__ __forceinline__ bool next(const OrthoSteps& s, int tasks, int step) {
+    if (++slot == kBoxChunks) {
+      slot = 0;
+      phase ^= 1;
+    }
+    if (++c < o.chunks) return false;
+    c = 0;
+    t += step;
+    if (t < tasks) o = ortho_task(s, t);
+    return true;  // another task
+  }
+};
+
+// Warp 2: brings the operands of the epilogue's chunks.
+__device__ __forceinline__ void ortho_bring(const OrthoSteps& s, uint32_t boxes, uint32_t efull,
+                                            uint32_t bfree, int first, int tasks, int step,
+                                            int half, volatile int* dead) {
+  OrthoWalk w(s, first, tasks);
+  bool live = true, task = true;
+  uint32_t issued = 0;
+  while (w.t < tasks) {
+    live = live && bar_wait(bfree + 8 * w.slot, w.phase ^ 1, dead);
+    if (task && live && w.o.product != GRAM) {
+      live = ortho_wait(s, w.o, dead);
+      fence_copies();
+    }
+    live = __all_sync(0xffffffffu, live);
+    if (!live) break;
+    const uint32_t at = boxes + w.slot * 2 * kBox, bar = efull + 8 * w.slot;
+    const int x = w.o.j0 + 64 * w.c;
+    const int y = w.o.b * s.k[w.o.product].rows_out + w.o.i0 + half * kRowsCta;
+    if (elect()) {
+      bar_expect(bar, w.o.product * kBox);
+      if (w.o.product == POLY) box_load(&s.maps.gram, at, x, y, bar);
+      if (w.o.product == GROW) {
+        box_load(&s.maps.hi[w.o.step & 1], at, x, y, bar);
+        box_load(&s.maps.lo, at + kBox, x, y, bar);
       }
     }
-    live = live && bar_wait(edone + 8 * sb, sph, dead);
+    __syncwarp();
+    ++issued;
+    task = w.next(s, tasks, step);
+  }
+  // after a wait that gave up: the boxes in flight land before the CTA returns
+  for (uint32_t q = issued > kBoxChunks ? issued - kBoxChunks : 0; !live && q < issued; ++q) {
+    const long long t0 = clock64();
+    while (!bar_try(efull + 8 * (q % kBoxChunks), (q / kBoxChunks) & 1) &&
+           clock64() - t0 < kWaitCycles / 8) {
+    }
+  }
+}
+
+// Warp 3: stores the finished chunks and counts finished tiles.
+__device__ __forceinline__ void ortho_store(const OrthoSteps& s, uint32_t boxes, uint32_t edone,
+                                            uint32_t bfree, int first, int tasks, int step,
+                                            int half, volatile int* dead) {
+  OrthoWalk w(s, first, tasks);
+  while (w.t < tasks) {
+    bool live = bar_wait(edone + 8 * w.slot, w.phase, dead);
     live = __all_sync(0xffffffffu, live);  // the lanes leave together
     if (!live) break;
-    const uint32_t at = boxes + sb * 2 * kBox;
-    const int x = out.j0 + 64 * out_c, row = out.i0 + half * kRowsCta;
-    const int y = out.b * s.k[out.product].rows_out;
-    const bool last = out_c + 1 == out.chunks;
+    const uint32_t at = boxes + w.slot * 2 * kBox;
+    const int x = w.o.j0 + 64 * w.c, row = w.o.i0 + half * kRowsCta;
+    const int y = w.o.b * s.k[w.o.product].rows_out;
     if (elect()) {
-      if (out.product == GROW) {
-        box_store(&s.maps.hi[~out.step & 1], at, x, y + row);
-        if (out.step + 1 < s.steps) box_store(&s.maps.lo, at + kBox, x, y + row);
+      if (w.o.product == GROW) {
+        box_store(&s.maps.hi[~w.o.step & 1], at, x, y + row);
+        if (w.o.step + 1 < s.steps) box_store(&s.maps.lo, at + kBox, x, y + row);
       } else {
-        box_store(out.product == GRAM ? &s.maps.gram : &s.maps.poly_out, at, x, y + row);
-        if (out.mirror) {
-          const CUtensorMap* t = out.product == GRAM ? &s.maps.gram_t : &s.maps.poly_t;
+        box_store(w.o.product == GRAM ? &s.maps.gram : &s.maps.poly_out, at, x, y + row);
+        if (w.o.mirror) {
+          const CUtensorMap* t = w.o.product == GRAM ? &s.maps.gram_t : &s.maps.poly_t;
           box_store(t, at + kBox, row, y + x);
           box_store(t, at + kBox + kBox / 2, row + 64, y + x);
         }
       }
       asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-      if (last) {
+      asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+      bar_arrive(bfree + 8 * w.slot);
+      if (w.c + 1 == w.o.chunks) {
         asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         fence_copies();
         // behind this tile's boxes and (through the chunks' barriers) diagonals
-        asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(s.done + out.b) : "memory");
-      } else {
-        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(s.done + w.o.b) : "memory");
       }
     }
     __syncwarp();
-    --ahead;
-    if (++sb == kBoxChunks) {
-      sb = 0;
-      sph ^= 1;
-    }
-    ++out_c;
-    if (last) {
-      out_c = 0;
-      out_t += step;
-      if (out_t < tasks) out = ortho_task(s, out_t);
-    }
-  }
-  // after a wait that gave up: the boxes in flight land before the CTA returns
-  for (; !live && ahead > 0; --ahead) {
-    const long long t0 = clock64();
-    while (!bar_try(efull + 8 * sb, sph) && clock64() - t0 < kWaitCycles / 8) {
-    }
-    if (++sb == kBoxChunks) {
-      sb = 0;
-      sph ^= 1;
-    }
+    w.next(s, tasks, step);
   }
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
@@ -274,17 +279,9 @@ __device__ __forceinline__ void ortho_traffic(const OrthoSteps& s, uint32_t boxe
 // matrix from 16-byte unit `unit` of the box on.
 template <int PRODUCT>
 __device__ __forceinline__ void ortho_piece(float ca, float cb, float cc, bool by_column,
-                                            const float* diag_in, float diag_row, float* diag_out,
+                                            const float d[16], float diag_row, float* diag_out,
                                             bool mirror, uint32_t at, int row, int i, int j,
                                             int unit, float v[16]) {
-  float d[16];
-  if (PRODUCT == POLY || (PRODUCT == GROW && by_column)) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const float4 x = ld_state(diag_in + j + 4 * q);
-      d[4 * q] = x.x; d[4 * q + 1] = x.y; d[4 * q + 2] = x.z; d[4 * q + 3] = x.w;
-    }
-  }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const uint32_t p0 = at + box_at(row, unit + h), p1 = p0 + kBox;
@@ -343,7 +340,7 @@ __device__ __forceinline__ void ortho_piece(float ca, float cb, float cc, bool b
 __global__ void __launch_bounds__(kOrthoThreads, 1)
     ortho_kernel(const __grid_constant__ OrthoSteps s, int tasks) {
   extern __shared__ __align__(1024) unsigned char ortho_smem[];
-  __shared__ __align__(8) uint64_t bars[2 * kOrthoStages + 5 + 2 * kBoxChunks];
+  __shared__ __align__(8) uint64_t bars[2 * kOrthoStages + 5 + 3 * kBoxChunks];
   __shared__ uint32_t tmem_at;
   __shared__ int dead;
   constexpr uint32_t stages = kOrthoStages;
@@ -353,6 +350,7 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
   const uint32_t full = smem_u32(bars), empty = full + 8 * stages;
   const uint32_t tfull = empty + 8 * stages, tempty = tfull + 16, ready = tempty + 16;
   const uint32_t efull = ready + 8, edone = efull + 8 * kBoxChunks;
+  const uint32_t bfree = edone + 8 * kBoxChunks;
 
   if (warp == 0 && elect()) {
     dead = 0;
@@ -368,6 +366,7 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
     for (int b = 0; b < kBoxChunks; ++b) {
       bar_init(efull + 8 * b, 1);
       bar_init(edone + 8 * b, kEpis);
+      bar_init(bfree + 8 * b, 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -393,7 +392,7 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     tmem = *(volatile uint32_t*)&tmem_at;
   }
-  const bool early = warp == 3;  // only moves this CTA's own boxes from here on
+  const bool early = warp == 3;  // only stores this CTA's own boxes from here on
   if (early) cluster_arrive();
 
   if (warp == 0) {
@@ -503,8 +502,11 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
       }
     }
     __syncwarp();
+  } else if (warp == 2) {
+    ortho_bring(s, boxes, efull, bfree, first, tasks, clusters, (int)half, &dead);
+    __syncwarp();
   } else if (warp == 3) {
-    ortho_traffic(s, boxes, efull, edone, first, tasks, clusters, (int)half, &dead);
+    ortho_store(s, boxes, edone, bfree, first, tasks, clusters, (int)half, &dead);
     __syncwarp();
   } else if (warp >= kEpi0) {
     const int w = (warp - kEpi0) & 3, set = (warp - kEpi0) >> 2;
@@ -520,11 +522,22 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
       const float* diag_in = (o.product == POLY ? s.diag_gram : s.diag_poly) + diag;
       float* diag_out = (o.product == GRAM ? s.diag_gram : s.diag_poly) + diag;
       const float ca = s.coef[o.step][0], cb = s.coef[o.step][1], cc = s.coef[o.step][2];
-      float diag_row = 0.0f;
-      if (o.product != GRAM) {  // (the diagonal, under the tile's products)
+      // The diagonal, under the tile's products: of this thread's row, and of
+      // this warp's 16 columns of each chunk (two chunks across a register's lanes).
+      const bool by_column = o.product == POLY || (o.product == GROW && tall);
+      float diag_row = 0.0f, diag_col[2] = {0.0f, 0.0f};
+      if (o.product != GRAM) {
         ok = ortho_wait(s, o, &dead);
         if (!ok) break;
         if (o.product == POLY || !tall) diag_row = *(volatile const float*)(diag_in + i);
+        if (by_column)
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const int c = 2 * q + (lane >> 4);
+            if (c < o.chunks)
+              diag_col[q] =
+                  *(volatile const float*)(diag_in + o.j0 + c * 64 + set * 16 + (lane & 15));
+          }
       }
       ok = bar_wait(tfull + 8 * acc, aph, &dead);
       ok = __all_sync(0xffffffffu, ok);
@@ -533,6 +546,16 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
       const uint32_t d = tmem + ((uint32_t)(w * 32) << 16) + acc * 256 + set * 16;
       for (int c = 0; c < o.chunks; ++c) {
         const uint32_t b = eb;
+        uint32_t r[16];
+        tmem_load16(d + c * 64, r);
+        float v[16], dc[16];
+#pragma unroll
+        for (int q = 0; q < 16; ++q) v[q] = __uint_as_float(r[q]);
+        if (by_column)
+#pragma unroll
+          for (int q = 0; q < 16; ++q)
+            dc[q] = __shfl_sync(0xffffffffu, c < 2 ? diag_col[0] : diag_col[1],
+                                (c & 1) * 16 + q);
         ok = bar_wait(efull + 8 * b, eph, &dead);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -540,21 +563,16 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
           eb = 0;
           eph ^= 1;
         }
-        uint32_t r[16];
-        tmem_load16(d + c * 64, r);
-        float v[16];
-#pragma unroll
-        for (int q = 0; q < 16; ++q) v[q] = __uint_as_float(r[q]);
         const uint32_t at = boxes + b * 2 * kBox;
         const int j = o.j0 + c * 64 + set * 16;
         if (o.product == GRAM)
-          ortho_piece<GRAM>(ca, cb, cc, tall, diag_in, diag_row, diag_out, o.mirror, at, row, i, j,
+          ortho_piece<GRAM>(ca, cb, cc, tall, dc, diag_row, diag_out, o.mirror, at, row, i, j,
                             set * 2, v);
         else if (o.product == POLY)
-          ortho_piece<POLY>(ca, cb, cc, tall, diag_in, diag_row, diag_out, o.mirror, at, row, i, j,
+          ortho_piece<POLY>(ca, cb, cc, tall, dc, diag_row, diag_out, o.mirror, at, row, i, j,
                             set * 2, v);
         else
-          ortho_piece<GROW>(ca, cb, cc, tall, diag_in, diag_row, diag_out, o.mirror, at, row, i, j,
+          ortho_piece<GROW>(ca, cb, cc, tall, dc, diag_row, diag_out, o.mirror, at, row, i, j,
                             set * 2, v);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
