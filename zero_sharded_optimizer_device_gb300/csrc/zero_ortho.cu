@@ -32,8 +32,11 @@ constexpr float kScaleX = 4096.0f, kScaleG = 256.0f, kScaleP = 64.0f;
 constexpr int kBoxChunks = 3;
 constexpr int kBox = 16384;                      // 128 rows of 64 fp16 columns
 constexpr int kSideBytes = 2 * kBoxChunks * kBox;
+// What the epilogue has to know of a tile: the task, and the diagonal of its
+// rows (128 of this CTA) and of its columns (256).
+constexpr int kNoteInts = 8, kNoteBytes = 2048;
 constexpr int kStageBytes = kBytesA + 256 * kDeep;
-constexpr int kOrthoStages = (kSmemMost - 1024 - kSideBytes) / kStageBytes;
+constexpr int kOrthoStages = (kSmemMost - 1024 - kSideBytes - kNoteBytes) / kStageBytes;
 constexpr int kEpi0 = 4, kEpis = 16;             // epilogue warps
 constexpr int kOrthoThreads = 32 * (kEpi0 + kEpis);
 
@@ -196,19 +199,52 @@ struct OrthoWalk {
   }
 };
 
-// Warp 2: brings the operands of the epilogue's chunks.
-__device__ __forceinline__ void ortho_bring(const OrthoSteps& s, uint32_t boxes, uint32_t efull,
-                                            uint32_t bfree, int first, int tasks, int step,
-                                            int half, volatile int* dead) {
+// Warp 2: brings the operands of the epilogue's chunks, and before a tile's
+// first the note of the tile, once the epilogue has read the one before
+// (noted).  The epilogue takes it behind that chunk's barrier.
+__device__ __forceinline__ void ortho_bring(const OrthoSteps& s, uint32_t boxes, uint32_t note,
+                                            uint32_t efull, uint32_t bfree, uint32_t noted,
+                                            int first, int tasks, int step, int half, int lane,
+                                            volatile int* dead) {
   OrthoWalk w(s, first, tasks);
   bool live = true, task = true;
-  uint32_t issued = 0;
+  uint32_t issued = 0, note_phase = 1;
   while (w.t < tasks) {
-    live = live && bar_wait(bfree + 8 * w.slot, w.phase ^ 1, dead);
-    if (task && live && w.o.product != GRAM) {
-      live = ortho_wait(s, w.o, dead);
-      fence_copies();
+    if (task) {
+      live = live && bar_wait(noted, note_phase, dead);
+      note_phase ^= 1;
+      live = __all_sync(0xffffffffu, live);
+      if (live && w.o.product != GRAM) {
+        live = ortho_wait(s, w.o, dead);
+        fence_copies();
+      }
+      if (live) {
+        const int vals[kNoteInts] = {w.o.product, w.o.step, w.o.b,           w.o.i0,
+                                     w.o.j0,      w.o.chunks, w.o.mirror, 0};
+#pragma unroll
+        for (int q = 0; q < kNoteInts; ++q)
+          if (lane == q) asm volatile("st.shared.u32 [%0], %1;" ::"r"(note + 4 * q), "r"(vals[q]));
+        if (w.o.product != GRAM) {
+          const float* diag = (w.o.product == POLY ? s.diag_gram : s.diag_poly) +
+                              (int64_t)w.o.b * s.side;
+          const bool by_row = w.o.product == POLY || !s.tall;
+          const bool by_column = w.o.product == POLY || s.tall;
+          float4 r = make_float4(0.0f, 0.0f, 0.0f, 0.0f), c[2] = {r, r};
+          if (by_row) r = ld_state(diag + w.o.i0 + half * kRowsCta + 4 * lane);
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+            if (by_column && q * 128 < w.o.chunks * 64)
+              c[q] = ld_state(diag + w.o.j0 + q * 128 + 4 * lane);
+          const uint32_t at = note + 4 * kNoteInts + 16 * lane;
+          st_shared4(at, r.x, r.y, r.z, r.w);
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+            st_shared4(at + 512 * (q + 1), c[q].x, c[q].y, c[q].z, c[q].w);
+        }
+        __syncwarp();  // the note is written when the lane below arrives
+      }
     }
+    live = live && bar_wait(bfree + 8 * w.slot, w.phase ^ 1, dead);
     live = __all_sync(0xffffffffu, live);
     if (!live) break;
     const uint32_t at = boxes + w.slot * 2 * kBox, bar = efull + 8 * w.slot;
@@ -340,7 +376,7 @@ __device__ __forceinline__ void ortho_piece(float ca, float cb, float cc, bool b
 __global__ void __launch_bounds__(kOrthoThreads, 1)
     ortho_kernel(const __grid_constant__ OrthoSteps s, int tasks) {
   extern __shared__ __align__(1024) unsigned char ortho_smem[];
-  __shared__ __align__(8) uint64_t bars[2 * kOrthoStages + 5 + 3 * kBoxChunks];
+  __shared__ __align__(8) uint64_t bars[2 * kOrthoStages + 6 + 3 * kBoxChunks];
   __shared__ uint32_t tmem_at;
   __shared__ int dead;
   constexpr uint32_t stages = kOrthoStages;
@@ -350,7 +386,8 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
   const uint32_t full = smem_u32(bars), empty = full + 8 * stages;
   const uint32_t tfull = empty + 8 * stages, tempty = tfull + 16, ready = tempty + 16;
   const uint32_t efull = ready + 8, edone = efull + 8 * kBoxChunks;
-  const uint32_t bfree = edone + 8 * kBoxChunks;
+  const uint32_t bfree = edone + 8 * kBoxChunks, noted = bfree + 8 * kBoxChunks;
+  const uint32_t note = boxes + kSideBytes;
 
   if (warp == 0 && elect()) {
     dead = 0;
@@ -363,6 +400,7 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
       bar_init(tempty + 8 * a, 2 * kEpis);
     }
     bar_init(ready, 2);
+    bar_init(noted, kEpis);
     for (int b = 0; b < kBoxChunks; ++b) {
       bar_init(efull + 8 * b, 1);
       bar_init(edone + 8 * b, kEpis);
@@ -398,9 +436,11 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
   if (warp == 0) {
     const uint32_t full_lead = remote(full, 0);
     uint32_t st = 0, ph = 0, end_s = 0, end_ph = 0;  // end: where a wait gave up
-    bool live = true;
+    bool live = true, met = false;
+    OrthoTask o{}, next{};
+    if (first < tasks) next = ortho_task(s, first);
     for (int t = first; t < tasks; t += clusters) {
-      const OrthoTask o = ortho_task(s, t);
+      o = next;
       const OrthoK& k = s.k[o.product];
       const int i0 = o.i0 + (int)half * kRowsCta, j0 = o.j0 + (int)half * (k.bn / 2);
       const int ya = o.b * k.rows_a, yb = o.b * k.rows_b, kblocks = k.kblocks;
@@ -416,11 +456,18 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
                                  : o.product == POLY ? &s.maps.gram_b
                                  : s.tall            ? &s.maps.poly
                                                      : x;
-      if (live) {
+      if (live && !met) {
         live = ortho_wait(s, o, &dead);
         fence_copies();
       }
+      met = false;
       for (int kb = 0; kb < kblocks; ++kb) {
+        // the next task, and whether it can go on, while this one's loads run
+        if (kb == kblocks / 2 && t + clusters < tasks) {
+          next = ortho_task(s, t + clusters);
+          met = ortho_met(s, next);
+          fence_copies();
+        }
         if (live) {
           live = bar_wait(empty + 8 * st, ph ^ 1, &dead);
           end_s = st;
@@ -503,7 +550,8 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
     }
     __syncwarp();
   } else if (warp == 2) {
-    ortho_bring(s, boxes, efull, bfree, first, tasks, clusters, (int)half, &dead);
+    ortho_bring(s, boxes, note, efull, bfree, noted, first, tasks, clusters, (int)half, lane,
+                &dead);
     __syncwarp();
   } else if (warp == 3) {
     ortho_store(s, boxes, edone, bfree, first, tasks, clusters, (int)half, &dead);
@@ -516,35 +564,38 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
     uint32_t acc = 0, aph = 0, eb = 0, eph = 0;
     bool ok = true;
     for (int t = first; t < tasks && ok; t += clusters) {
-      const OrthoTask o = ortho_task(s, t);
-      const int i = o.i0 + (int)half * kRowsCta + row;
-      const int64_t diag = (int64_t)o.b * s.side;
-      const float* diag_in = (o.product == POLY ? s.diag_gram : s.diag_poly) + diag;
-      float* diag_out = (o.product == GRAM ? s.diag_gram : s.diag_poly) + diag;
-      const float ca = s.coef[o.step][0], cb = s.coef[o.step][1], cc = s.coef[o.step][2];
-      // The diagonal, under the tile's products: of this thread's row, and of
-      // this warp's 16 columns of each chunk (two chunks across a register's lanes).
-      const bool by_column = o.product == POLY || (o.product == GROW && tall);
-      float diag_row = 0.0f, diag_col[2] = {0.0f, 0.0f};
-      if (o.product != GRAM) {
-        ok = ortho_wait(s, o, &dead);
-        if (!ok) break;
-        if (o.product == POLY || !tall) diag_row = *(volatile const float*)(diag_in + i);
-        if (by_column)
+      // the first chunk's operands, and with them the tile's note
+      ok = bar_wait(efull + 8 * eb, eph, &dead);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const uint4 n0 = lds16(note), n1 = lds16(note + 16);
+      const int product = (int)n0.x, step = (int)n0.y, i0 = (int)n0.w, j0 = (int)n1.x,
+                chunks = (int)n1.y;
+      const bool mirror = n1.z != 0;
+      const int i = i0 + (int)half * kRowsCta + row;
+      float* diag_out =
+          (product == GRAM ? s.diag_gram : s.diag_poly) + (int64_t)n0.z * s.side;
+      const float ca = s.coef[step][0], cb = s.coef[step][1], cc = s.coef[step][2];
+      // The diagonal of this thread's row, and of this warp's 16 columns of
+      // each chunk (two chunks across a register's lanes).
+      const bool by_column = product == POLY || (product == GROW && tall);
+      float diag_row, diag_col[2];
+      const uint32_t diag_at = note + 4 * kNoteInts;
+      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(diag_row) : "r"(diag_at + 4 * row));
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const int c = 2 * q + (lane >> 4);
-            if (c < o.chunks)
-              diag_col[q] =
-                  *(volatile const float*)(diag_in + o.j0 + c * 64 + set * 16 + (lane & 15));
-          }
-      }
+      for (int q = 0; q < 2; ++q)
+        asm volatile("ld.shared.f32 %0, [%1];"
+                     : "=f"(diag_col[q])
+                     : "r"(diag_at + 512 + 4 * ((2 * q + (lane >> 4)) * 64 + set * 16 +
+                                                (lane & 15))));
+      __syncwarp();
+      if (lane == 0) bar_arrive(noted);
       ok = bar_wait(tfull + 8 * acc, aph, &dead);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint32_t d = tmem + ((uint32_t)(w * 32) << 16) + acc * 256 + set * 16;
-      for (int c = 0; c < o.chunks; ++c) {
+      for (int c = 0; c < chunks; ++c) {
         const uint32_t b = eb;
         uint32_t r[16];
         tmem_load16(d + c * 64, r);
@@ -564,15 +615,15 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
           eph ^= 1;
         }
         const uint32_t at = boxes + b * 2 * kBox;
-        const int j = o.j0 + c * 64 + set * 16;
-        if (o.product == GRAM)
-          ortho_piece<GRAM>(ca, cb, cc, tall, dc, diag_row, diag_out, o.mirror, at, row, i, j,
+        const int j = j0 + c * 64 + set * 16;
+        if (product == GRAM)
+          ortho_piece<GRAM>(ca, cb, cc, tall, dc, diag_row, diag_out, mirror, at, row, i, j,
                             set * 2, v);
-        else if (o.product == POLY)
-          ortho_piece<POLY>(ca, cb, cc, tall, dc, diag_row, diag_out, o.mirror, at, row, i, j,
+        else if (product == POLY)
+          ortho_piece<POLY>(ca, cb, cc, tall, dc, diag_row, diag_out, mirror, at, row, i, j,
                             set * 2, v);
         else
-          ortho_piece<GROW>(ca, cb, cc, tall, dc, diag_row, diag_out, o.mirror, at, row, i, j,
+          ortho_piece<GROW>(ca, cb, cc, tall, dc, diag_row, diag_out, mirror, at, row, i, j,
                             set * 2, v);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
@@ -843,7 +894,7 @@ static cudaError_t launch_ortho(const OrthoSteps& s, int64_t tasks, cudaStream_t
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(sm_count() / 2 * 2));
   cfg.blockDim = dim3(kOrthoThreads);
-  cfg.dynamicSmemBytes = (size_t)kOrthoStages * kStageBytes + kSideBytes;
+  cfg.dynamicSmemBytes = (size_t)kOrthoStages * kStageBytes + kSideBytes + kNoteBytes;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
