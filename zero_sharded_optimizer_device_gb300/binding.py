@@ -1050,7 +1050,7 @@ def _batch(x, m: int, n: int, batch: int, ld: int, stride: int, dtype: int, what
             have = x.untyped_storage().nbytes() - x.storage_offset() * es
             if have < need * es:
                 raise ValueError(f"{what}: holds {have} bytes, the call touches {need * es}")
-    return _ptr(x)
+    return _here(x)
 
 
 def zero_orthogonalize_workspace(m: int, n: int, batch: int) -> int:
@@ -1067,7 +1067,7 @@ def zero_orthogonalize(x, ldx: int, stride_x: int, xdtype: int, m: int, n: int, 
     _check(_lib().zero_orthogonalize(
         _batch(x, m, n, batch, ldx, stride_x, xdtype, "x"), ldx, stride_x, xdtype, m, n, batch,
         None if ns is None else ctypes.byref(ns),
-        _batch(y, m, n, batch, ldy, stride_y, ZERO_BF16, "y"), ldy, stride_y, _ptr(workspace),
+        _batch(y, m, n, batch, ldy, stride_y, ZERO_BF16, "y"), ldy, stride_y, _here(workspace),
         workspace_bytes, _ops_stream(stream)), "zero_orthogonalize")
 
 
@@ -1091,7 +1091,7 @@ def zero_muon_step(plan, tensors, rows: int, cols: int, master, momentum, reduce
     _check(_lib().zero_muon_step(
         plan, (c_i64 * max(1, len(tensors)))(*tensors), len(tensors), rows, cols, _ptr(master),
         _ptr(momentum), _ptr(reduced), ctypes.byref(hp), _ptr(d_coef), _ptr(out), out_dtype,
-        _ptr(workspace), workspace_bytes, _ops_stream(stream)), "zero_muon_step")
+        _here(workspace), workspace_bytes, _ops_stream(stream)), "zero_muon_step")
 
 
 # ------------------------------------------------------------- 4-bit layers --
@@ -1105,20 +1105,33 @@ class _Fp4:
         self.struct = zero_fp4_t(None, ld, None, None)
 
     def checked(self, rows: int, cols: int, format: int, what: str):
-        s, c = self.struct, self.codes
+        s, c, t, g = self.struct, self.codes, self.scales, self.tensor_scale
         if rows > 0 and cols > 0:
-            need = (rows - 1) * s.ld + (cols + 31) // 32 * 16
-            if not (c is None or isinstance(c, int) or (c.is_contiguous() and c.nbytes >= need)):
-                if c.element_size() != 1 or (c.shape[-1] > 1 and c.stride(-1) != 1):
-                    raise ValueError(f"{what}.codes: the bytes of a row are not consecutive")
-                have = c.untyped_storage().nbytes() - c.storage_offset()
-                if have < need:
-                    raise ValueError(f"{what}.codes: holds {have} bytes, the call touches {need}")
+            if not (c is None or isinstance(c, int)):
+                need = (rows - 1) * s.ld + (cols + 31) // 32 * 16
+                if not (c.is_contiguous() and c.nbytes >= need):
+                    if c.element_size() != 1 or (c.shape[-1] > 1 and c.stride(-1) != 1):
+                        raise ValueError(f"{what}.codes: the bytes of a row are not consecutive")
+                    have = c.untyped_storage().nbytes() - c.storage_offset()
+                    if have < need:
+                        raise ValueError(f"{what}.codes: holds {have} bytes, the call touches "
+                                         f"{need}")
             blocks = (cols + 15) // 16 if format == ZERO_FP4_NV else (cols + 31) // 32
-            _need(self.scales, (rows + 127) // 128 * ((blocks + 3) // 4) * 512, what + ".scales")
-        _need(self.tensor_scale, 4, what + ".tensor_scale")
-        s.codes, s.scales, s.tensor_scale = _ptr(c), _ptr(self.scales), _ptr(self.tensor_scale)
+            _need(t, (rows + 127) // 128 * ((blocks + 3) // 4) * 512, what + ".scales")
+        if g is not None:
+            _need(g, 4, what + ".tensor_scale")
+        s.codes, s.scales, s.tensor_scale = _here(c), _here(t), None if g is None else _here(g)
         return ctypes.byref(s)
+
+
+def _here(x):
+    """_ptr, sooner for a tensor on the current device."""
+    if x is None or isinstance(x, int):
+        return x
+    if not _Torch.ready:
+        _Torch.load()
+    dev = x.get_device()
+    return x.data_ptr() if dev >= 0 and _Torch.cuda and dev == _Torch.device() else _ptr(x)
 
 
 def fp4_matrix(codes, ld: int, scales, tensor_scale=None) -> _Fp4:
@@ -1145,8 +1158,8 @@ def zero_fp4_tensor_scale(x, ldx: int, xdtype: int, rows: int, cols: int, tensor
     _need(tensor_scale, 4, "tensor_scale")
     _need(workspace, workspace_bytes, "workspace")
     _check(_lib().zero_fp4_tensor_scale(
-        _mat(x, rows, cols, ldx, xdtype, "x"), ldx, xdtype, rows, cols, _ptr(tensor_scale),
-        _ptr(workspace), workspace_bytes, _ops_stream(stream)), "zero_fp4_tensor_scale")
+        _mat(x, rows, cols, ldx, xdtype, "x"), ldx, xdtype, rows, cols, _here(tensor_scale),
+        _here(workspace), workspace_bytes, _ops_stream(stream)), "zero_fp4_tensor_scale")
 
 
 def zero_fp4_quantize(x, ldx: int, xdtype: int, rows: int, cols: int, format: int, q, qt=None,

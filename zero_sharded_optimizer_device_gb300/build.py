@@ -23,11 +23,12 @@ LIB_CHECKED = os.path.join(HERE, "libzero_checked.so")
 
 SOURCES = ["zero_plan.cpp", "zero_api.cpp", "zero_sched.cpp", "zero_rs.cu", "zero_kernels.cu",
            "zero_noalloc.cu", "zero_ops_api.cpp", "zero_linear.cu", "zero_dropout.cu",
-           "zero_rows.cu", "zero_lnorm.cu", "zero_fp4.cu", "zero_ortho.cu"]
+           "zero_rows.cu", "zero_lnorm.cu", "zero_fp4.cu", "zero_fp4_rows.cu",
+           "zero_ortho.cu"]
 # The step's kernels follow the oracle operation by operation (no contraction
 # into FMA); the layer operators' sums are fp32 FMA chains.
 FMA = {"zero_linear.cu", "zero_rows.cu", "zero_dropout.cu", "zero_lnorm.cu", "zero_fp4.cu",
-       "zero_ortho.cu"}
+       "zero_fp4_rows.cu", "zero_ortho.cu"}
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-I", INCLUDE, "-I", CSRC,
           "-Xcompiler", "-fPIC,-ffp-contract=off,-O2"]

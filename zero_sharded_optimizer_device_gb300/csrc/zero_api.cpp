@@ -605,7 +605,7 @@ extern "C" int zero_bounds_report(zero_bounds_t* out, int32_t reset) {
   *out = zero_bounds_t{};
 #ifdef ZERO_CHECKED
   out->checked = 1;
-  zk::BoundsRec rec[8] = {};
+  zk::BoundsRec rec[9] = {};
   cudaError_t e = cudaDeviceSynchronize();
   if (e == cudaSuccess) e = zk::bounds_rs(&rec[0], reset != 0);
   if (e == cudaSuccess) e = zk::bounds_kernels(&rec[1], reset != 0);
@@ -615,6 +615,7 @@ extern "C" int zero_bounds_report(zero_bounds_t* out, int32_t reset) {
   if (e == cudaSuccess) e = zk::bounds_rows(&rec[5], reset != 0);
   if (e == cudaSuccess) e = zk::bounds_fp4(&rec[6], reset != 0);
   if (e == cudaSuccess) e = zk::bounds_ortho(&rec[7], reset != 0);
+  if (e == cudaSuccess) e = zk::bounds_fp4_rows(&rec[8], reset != 0);
   if (e != cudaSuccess) return cuda_status(e);
   for (const zk::BoundsRec& r : rec) {
     if (r.count && !out->count) {  // the first unit with a record gives the details

@@ -1,54 +1,10 @@
 // Matrices in microscaled 4-bit numbers (zero_fp4_*, include/zero.h): to E2M1
 // codes with a scale per block and back, and their products on the tensor
 // cores' block-scaled instructions (the kernel of zero_product.cuh).
+#include "zero_fp4.cuh"
 #include "zero_product.cuh"
 
 namespace zk {
-
-// ------------------------------------------------------------- conversions --
-// Eight values to codes, the first in the lowest four bits (nearest, ties to
-// the even code, beyond 6 to 6).
-__device__ __forceinline__ uint32_t to_codes8(const float v[8]) {
-  uint32_t r;
-  asm("{ .reg .b8 a, b, c, d;\n"
-      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n"
-      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
-      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n"
-      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
-      "mov.b32 %0, {a, b, c, d}; }"
-      : "=r"(r)
-      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
-  return r;
-}
-__device__ __forceinline__ void from_codes8(uint32_t codes, float v[8]) {
-  uint32_t h[4];
-  asm("{ .reg .b8 a, b, c, d;\n"
-      "mov.b32 {a, b, c, d}, %4;\n"
-      "cvt.rn.f16x2.e2m1x2 %0, a;\n"
-      "cvt.rn.f16x2.e2m1x2 %1, b;\n"
-      "cvt.rn.f16x2.e2m1x2 %2, c;\n"
-      "cvt.rn.f16x2.e2m1x2 %3, d; }"
-      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-      : "r"(codes));
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    asm("{ .reg .b16 lo, hi; mov.b32 {lo, hi}, %2; cvt.f32.f16 %0, lo; cvt.f32.f16 %1, hi; }"
-        : "=f"(v[2 * i]), "=f"(v[2 * i + 1])
-        : "r"(h[i]));
-}
-// E4M3, nearest, beyond 448 to 448; and back.
-__device__ __forceinline__ uint32_t to_e4m3(float v) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.0f), "f"(v));
-  return r & 0xFFu;
-}
-__device__ __forceinline__ float from_e4m3(uint32_t byte) {
-  uint32_t h;
-  float f;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)byte));
-  asm("{ .reg .b16 lo, hi; mov.b32 {lo, hi}, %1; cvt.f32.f16 %0, lo; }" : "=f"(f) : "r"(h));
-  return f;
-}
 
 // A block's scale byte and the factor that brings its values to codes, from
 // the largest magnitude's bits (NaN and infinity are the largest as integers).
@@ -72,23 +28,7 @@ __device__ __forceinline__ uint32_t block_scale(uint32_t top, float six_g, float
   factor = __uint_as_float((254u - byte) << 23);
   return byte;
 }
-// What a scale byte stands for, times g.
-template <bool NV>
-__device__ __forceinline__ float scale_value(uint32_t byte, float g) {
-  if (NV) return byte == 0x7Fu ? __uint_as_float(0x7FC00000u) : __fmul_rn(from_e4m3(byte), g);
-  if (byte == 0xFFu) return __uint_as_float(0x7FC00000u);
-  return __uint_as_float(byte ? byte << 23 : 0x00400000u);
-}
 
-__device__ __forceinline__ uint32_t top8(const float v[8]) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const uint32_t b = __float_as_uint(v[j]) & 0x7FFFFFFFu;
-    top = b > top ? b : top;
-  }
-  return top;
-}
 // Codes of eight values of a block whose factor is known.
 __device__ __forceinline__ uint32_t codes8(const float v[8], float factor) {
   float s[8];
@@ -98,120 +38,171 @@ __device__ __forceinline__ uint32_t codes8(const float v[8], float factor) {
 }
 
 // ----------------------------------------------------------------- quantise --
-// A block of 256 threads takes 128 x 128 values: their codes and scales are
-// whole scale tiles in both directions, so that every byte of those (padding
-// included) has one writer.  Rows straight from the loads, a lane having 8
-// columns; columns through shared memory, a thread having one block of one.
-constexpr int kQuantTile = 128, kQuantThreads = 256;
+// A block of 256 threads takes 128 x 128 values into shared memory: their codes
+// and scales are whole scale tiles in both directions, so that every byte of
+// those (padding included) has one writer.  Then a thread takes one block of a
+// row after another, and in the other direction the blocks of two columns side
+// by side (bf16: one 32-bit word); largest magnitudes of bf16 are found two at
+// a time as integers, which order NaN and infinity above all numbers.  Codes go
+// out through shared memory, 64 bytes of each line.
+constexpr int kQuantTile = 128, kQuantThreads = 256, kCodeLine = 80;
 
-template <bool NV, bool WIDE>
+template <bool WIDE>
 struct QuantShared {
   static constexpr int kElem = WIDE ? 4 : 2, kLine = kQuantTile * kElem + 16;
   unsigned char tile[kQuantTile * kLine];
-  unsigned char codes[kQuantTile * 80];  // of the columns: 64 bytes each
-  unsigned char scales[2][1024];         // rows', columns'
+  unsigned char codes[kQuantTile * kCodeLine];  // of one direction, 64 bytes a line
+  unsigned char scales[2][1024];                // rows', columns'
 };
 
-template <bool NV>
 __device__ __forceinline__ int scale_at(int line, int block) {  // in a 128-line tile's scales
   return (block >> 2) * kScaleTile + (line & 31) * 16 + (line >> 5) * 4 + (block & 3);
 }
 
-// One direction's scale tiles to memory: tile (line_tile, t) for the t of this
-// 128-wide piece that exist.
-__device__ __forceinline__ void store_scales(const Fp4Mat& o, const unsigned char* from,
-                                             int64_t line_tile, int64_t tile0, int tiles) {
+// One direction's codes and scale tiles to memory.  line0: its first line;
+// byte0: of the lines' codes; tiles (line0 / 128, tile0 + t), t < tiles.
+__device__ __forceinline__ void store_quantized(const Fp4Mat& o, const unsigned char* codes,
+                                                const unsigned char* scales, int64_t line0,
+                                                int64_t lines, int64_t byte0, int64_t tile0,
+                                                int tiles) {
+#pragma unroll
+  for (int p = 0; p < kQuantTile * 4 / kQuantThreads; ++p) {
+    const int u = p * kQuantThreads + threadIdx.x, c = u >> 2;
+    const int64_t line = line0 + c, byte = byte0 + (u & 3) * 16, at = line * o.ld + byte;
+    if (line < lines && byte < o.line_bytes &&
+        in_extent(at, at + 16, line * o.ld, line * o.ld + o.line_bytes, ZERO_SITE_FP4))
+      *reinterpret_cast<uint4*>(o.codes + at) =
+          *reinterpret_cast<const uint4*>(codes + c * kCodeLine + (u & 3) * 16);
+  }
   const int unit = threadIdx.x;  // 16 bytes
   const int64_t t = tile0 + unit / 32;
   if (unit >= tiles * 32 || t >= o.scale_tiles) return;
-  const int64_t at = (line_tile * o.scale_tiles + t) * kScaleTile + unit % 32 * 16;
+  const int64_t at = (line0 / kQuantTile * o.scale_tiles + t) * kScaleTile + unit % 32 * 16;
   if (!in_extent(at, at + 16, 0, o.scale_bytes, ZERO_SITE_FP4)) return;
-  *reinterpret_cast<uint4*>(o.scales + at) = *reinterpret_cast<const uint4*>(from + unit * 16);
+  *reinterpret_cast<uint4*>(o.scales + at) = *reinterpret_cast<const uint4*>(scales + unit * 16);
 }
 
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return a > b ? a : b; }
+// The magnitudes' bits of two bf16.
+__device__ __forceinline__ uint32_t magnitudes2(uint32_t w) { return w & 0x7FFF7FFFu; }
+
 template <bool NV, bool WIDE>
-__global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const __grid_constant__ QuantK k) {
+__global__ void __launch_bounds__(kQuantThreads, WIDE ? 2 : 4)
+    quantize_kernel(const __grid_constant__ QuantK k) {
   extern __shared__ __align__(16) unsigned char quant_smem[];
-  using Shared = QuantShared<NV, WIDE>;
+  using Shared = QuantShared<WIDE>;
   Shared& sh = *reinterpret_cast<Shared*>(quant_smem);
-  constexpr int kSize = NV ? 16 : 32, kTiles = NV ? 2 : 1;
+  constexpr int kSize = NV ? 16 : 32, kTiles = NV ? 2 : 1, kBlocks = kQuantTile / kSize;
   after_previous_kernel();
   const float g = NV && k.g ? *(volatile const float*)k.g : 1.0f;
   const float six_g = __fmul_rn(6.0f, g);
   const int64_t row0 = (int64_t)(blockIdx.x / k.tiles_j) * kQuantTile;
   const int64_t col0 = (int64_t)(blockIdx.x % k.tiles_j) * kQuantTile;
-  const int t = threadIdx.x, line = t >> 4, unit = t & 15;
-  const Extent e{k.rows, k.cols};
-  const int64_t col = col0 + unit * 8;
-  const int valid = col >= k.cols ? 0 : k.cols - col < 8 ? (int)(k.cols - col) : 8;
-  const bool rows = k.q.codes != nullptr, columns = k.qt.codes != nullptr;
-#pragma unroll 4
-  for (int p = 0; p < 8; ++p) {
-    const int r = p * 16 + line;
-    const int64_t row = row0 + r;
-    float v[8] = {};
-    if (row < k.rows && valid) {
-      const Raw8 raw = raw8(k.x, row, col, valid, e, ZERO_SITE_FP4);
-      from_raw(k.x, raw, v);
-    }
-    if (columns) {
-      unsigned char* at = sh.tile + r * Shared::kLine + unit * 8 * Shared::kElem;
-      if (WIDE) {
-        reinterpret_cast<float4*>(at)[0] = make_float4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<float4*>(at)[1] = make_float4(v[4], v[5], v[6], v[7]);
-      } else {
-        *reinterpret_cast<uint4*>(at) = pack8(v);
-      }
-    }
-    if (rows) {
-      uint32_t top = top8(v);
+  const int t = threadIdx.x;
+  {
+    const int line = t >> 4, unit = t & 15;
+    const Extent e{k.rows, k.cols};
+    const int64_t col = col0 + unit * 8;
+    const int valid = col >= k.cols ? 0 : k.cols - col < 8 ? (int)(k.cols - col) : 8;
 #pragma unroll
-      for (int m = 1; m < kSize / 8; m *= 2) {
-        const uint32_t other = __shfl_xor_sync(0xffffffffu, top, m);
-        top = other > top ? other : top;
+    for (int p = 0; p < 8; ++p) {
+      const int r = p * 16 + line;
+      Raw8 raw;
+      raw.a = raw.b = make_uint4(0, 0, 0, 0);
+      if (row0 + r < k.rows && valid) raw = raw8(k.x, row0 + r, col, valid, e, ZERO_SITE_FP4);
+      uint4* at = reinterpret_cast<uint4*>(sh.tile + r * Shared::kLine + unit * 8 * Shared::kElem);
+      at[0] = raw.a;
+      if (WIDE) at[1] = raw.b;
+    }
+  }
+  __syncthreads();
+  const bool rows = k.q.codes != nullptr, columns = k.qt.codes != nullptr;
+  if (rows) {
+    for (int u = t; u < kQuantTile * kBlocks; u += kQuantThreads) {
+      const int r = u % kQuantTile, b = u / kQuantTile;
+      const unsigned char* at = sh.tile + r * Shared::kLine + b * kSize * Shared::kElem;
+      constexpr int kWords = kSize * Shared::kElem / 16;
+      uint4 raw[kWords];
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) raw[i] = reinterpret_cast<const uint4*>(at)[i];
+      uint32_t top = 0;
+      if (WIDE) {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i)
+          top = larger(larger(top, larger(raw[i].x & 0x7FFFFFFFu, raw[i].y & 0x7FFFFFFFu)),
+                       larger(raw[i].z & 0x7FFFFFFFu, raw[i].w & 0x7FFFFFFFu));
+      } else {
+        uint32_t two = 0;
+#pragma unroll
+        for (int i = 0; i < kWords; ++i)
+          two = __vmaxu2(__vmaxu2(two, __vmaxu2(magnitudes2(raw[i].x), magnitudes2(raw[i].y))),
+                         __vmaxu2(magnitudes2(raw[i].z), magnitudes2(raw[i].w)));
+        top = larger(two << 16, two & 0xFFFF0000u);
       }
       float factor;
-      const uint32_t byte = block_scale<NV>(top, six_g, g, factor);
-      const uint32_t codes = top >= kInfBits ? 0u : codes8(v, factor);
-      const int64_t at = row * k.q.ld + col / 2;
-      if (row < k.rows && col / 2 < k.q.line_bytes &&
-          in_extent(at, at + 4, row * k.q.ld, row * k.q.ld + k.q.line_bytes, ZERO_SITE_FP4))
-        *reinterpret_cast<uint32_t*>(k.q.codes + at) = codes;
-      if (unit % (kSize / 8) == 0) sh.scales[0][scale_at<NV>(r, unit * 8 / kSize)] = byte;
+      sh.scales[0][scale_at(r, b)] = (unsigned char)block_scale<NV>(top, six_g, g, factor);
+      uint32_t* out = reinterpret_cast<uint32_t*>(sh.codes + r * kCodeLine + b * (kSize / 2));
+#pragma unroll
+      for (int i = 0; i < kSize / 8; ++i) {
+        float v[8];
+        if (WIDE) {
+          const uint4 x = raw[(2 * i) % kWords], y = raw[(2 * i + 1) % kWords];
+          v[0] = __uint_as_float(x.x); v[1] = __uint_as_float(x.y);
+          v[2] = __uint_as_float(x.z); v[3] = __uint_as_float(x.w);
+          v[4] = __uint_as_float(y.x); v[5] = __uint_as_float(y.y);
+          v[6] = __uint_as_float(y.z); v[7] = __uint_as_float(y.w);
+        } else {
+          from_bf16(raw[i % kWords], v);
+        }
+        out[i] = top >= kInfBits ? 0u : codes8(v, factor);
+      }
     }
+    __syncthreads();
+    store_quantized(k.q, sh.codes, sh.scales[0], row0, k.rows, col0 / 2, col0 / (4 * kSize),
+                    kTiles);
   }
-  __syncthreads();
-  if (rows) store_scales(k.q, sh.scales[0], row0 / kQuantTile, col0 / (4 * kSize), kTiles);
   if (!columns) return;
-  constexpr int kBlocks = kQuantTile / kSize;
-  for (int u = t; u < kQuantTile * kBlocks; u += kQuantThreads) {
-    const int c = u % kQuantTile, b = u / kQuantTile;
-    float v[kSize];
-    uint32_t top = 0;
+  if (rows) __syncthreads();  // the codes are read
+  constexpr int kSide = WIDE ? 1 : 2;  // columns of a thread
+  for (int u = t; u < kQuantTile / kSide * kBlocks; u += kQuantThreads) {
+    const int c = u % (kQuantTile / kSide) * kSide, b = u / (kQuantTile / kSide);
+    const unsigned char* at = sh.tile + b * kSize * Shared::kLine + c * Shared::kElem;
+    uint32_t raw[kSize], top[kSide];
 #pragma unroll
-    for (int i = 0; i < kSize; ++i) {
-      const unsigned char* at = sh.tile + (b * kSize + i) * Shared::kLine + c * Shared::kElem;
-      v[i] = WIDE ? *reinterpret_cast<const float*>(at)
-                  : __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(at) << 16);
-      const uint32_t bits = __float_as_uint(v[i]) & 0x7FFFFFFFu;
-      top = bits > top ? bits : top;
+    for (int i = 0; i < kSize; ++i)
+      raw[i] = *reinterpret_cast<const uint32_t*>(at + i * Shared::kLine);
+    if (WIDE) {
+      top[0] = 0;
+#pragma unroll
+      for (int i = 0; i < kSize; ++i) top[0] = larger(top[0], raw[i] & 0x7FFFFFFFu);
+    } else {
+      uint32_t two = 0;
+#pragma unroll
+      for (int i = 0; i < kSize; ++i) two = __vmaxu2(two, magnitudes2(raw[i]));
+      top[0] = two << 16;
+      top[kSide - 1] = two & 0xFFFF0000u;
     }
-    float factor;
-    sh.scales[1][scale_at<NV>(c, b)] = (unsigned char)block_scale<NV>(top, six_g, g, factor);
-    uint32_t* out = reinterpret_cast<uint32_t*>(sh.codes + c * 80 + b * (kSize / 2));
 #pragma unroll
-    for (int i = 0; i < kSize / 8; ++i) out[i] = top >= kInfBits ? 0u : codes8(v + 8 * i, factor);
+    for (int h = 0; h < kSide; ++h) {
+      float factor;
+      const uint32_t most = !WIDE && h == 0 ? top[0] : top[kSide - 1];
+      sh.scales[1][scale_at(c + h, b)] = (unsigned char)block_scale<NV>(most, six_g, g, factor);
+      uint32_t* out =
+          reinterpret_cast<uint32_t*>(sh.codes + (c + h) * kCodeLine + b * (kSize / 2));
+#pragma unroll
+      for (int i = 0; i < kSize / 8; ++i) {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t w = raw[8 * i + j];
+          v[j] = WIDE ? __uint_as_float(w) : h ? bf16_hi(w) : bf16_lo(w);
+        }
+        out[i] = most >= kInfBits ? 0u : codes8(v, factor);
+      }
+    }
   }
   __syncthreads();
-  for (int u = t; u < kQuantTile * 4; u += kQuantThreads) {
-    const int c = u >> 2;
-    const int64_t to = col0 + c, byte = row0 / 2 + (u & 3) * 16, at = to * k.qt.ld + byte;
-    if (to < k.cols && byte < k.qt.line_bytes &&
-        in_extent(at, at + 16, to * k.qt.ld, to * k.qt.ld + k.qt.line_bytes, ZERO_SITE_FP4))
-      *reinterpret_cast<uint4*>(k.qt.codes + at) =
-          *reinterpret_cast<const uint4*>(sh.codes + c * 80 + (u & 3) * 16);
-  }
-  store_scales(k.qt, sh.scales[1], col0 / kQuantTile, row0 / (4 * kSize), kTiles);
+  store_quantized(k.qt, sh.codes, sh.scales[1], col0, k.cols, row0 / 2, row0 / (4 * kSize), kTiles);
 }
 
 template <bool NV, bool WIDE>
@@ -221,7 +212,7 @@ static cudaError_t launch_quantize_as(const QuantK& k, int64_t blocks, cudaStrea
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const unsigned long long bit = 1ull << (dev & 63);
-  constexpr int bytes = (int)sizeof(QuantShared<NV, WIDE>);
+  constexpr int bytes = (int)sizeof(QuantShared<WIDE>);
   if (!(done.load() & bit)) {
     e = cudaFuncSetAttribute(quantize_kernel<NV, WIDE>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
@@ -245,39 +236,76 @@ cudaError_t launch_quantize(const QuantK& in, cudaStream_t st) {
               : launch_quantize_as<false, false>(k, blocks, st);
 }
 
+// ------------------------------------------------------- walks over a matrix --
+// Units of 8 columns: a block of 256 threads covers `across` units (a power of
+// two, up to 32) of 256 / across rows, and goes on down the rows: no division.
+struct Walk {
+  int log2_across;
+  dim3 grid;
+};
+static Walk walk_over(int64_t rows, int64_t cols, int rows_a_thread) {
+  const int64_t units = (cols + 7) / 8;
+  Walk w;
+  w.log2_across = 0;
+  while (w.log2_across < 5 && (1ll << w.log2_across) < units) ++w.log2_across;
+  const int64_t x = (units + (1 << w.log2_across) - 1) >> w.log2_across;
+  const int64_t each = (int64_t)(kThreads >> w.log2_across) * rows_a_thread;
+  int64_t y = (rows + each - 1) / each, most = (int64_t)sm_count() * 8 / (x < 1 ? 1 : x) + 1;
+  if (most > 65535) most = 65535;
+  if (y > most) y = most;
+  w.grid = dim3((unsigned)x, (unsigned)y);
+  return w;
+}
+
 // --------------------------------------------------------------- dequantise --
-// A thread takes 8 columns of a row: 4 bytes of codes, one scale.
+// A thread takes 8 columns of four rows at a time: 4 bytes of codes, one scale.
 template <bool NV>
-__global__ void __launch_bounds__(kThreads) dequantize_kernel(const __grid_constant__ DequantK k) {
+__global__ void __launch_bounds__(kThreads)
+    dequantize_kernel(const __grid_constant__ DequantK k, int log2_across) {
   after_previous_kernel();
   const float g = NV && k.g ? *(volatile const float*)k.g : 1.0f;
   const Extent e{k.rows, k.cols};
-  const int64_t units = (k.cols + 7) / 8, total = units * k.rows;
-  for (int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x; u < total;
-       u += (int64_t)gridDim.x * kThreads) {
-    const int64_t row = u / units, col = u % units * 8;
-    const int64_t at = row * k.q.ld + col / 2, block = col / (NV ? 16 : 32);
-    const int64_t scale = (row / 128 * k.q.scale_tiles + block / 4) * kScaleTile + row % 32 * 16 +
-                          row % 128 / 32 * 4 + block % 4;
-    if (!in_extent(at, at + 4, row * k.q.ld, row * k.q.ld + k.q.line_bytes, ZERO_SITE_FP4) ||
-        !in_extent(scale, scale + 1, 0, k.q.scale_bytes, ZERO_SITE_FP4))
-      continue;
-    float v[8];
-    from_codes8(*reinterpret_cast<const uint32_t*>(k.q.codes + at), v);
-    const float d = scale_value<NV>(k.q.scales[scale], g);
+  const int across = 1 << log2_across, down = kThreads >> log2_across;
+  const int64_t col = ((int64_t)blockIdx.x * across + (threadIdx.x & (across - 1))) * 8;
+  if (col >= k.cols) return;
+  const int valid = k.cols - col < 8 ? (int)(k.cols - col) : 8;
+  const int64_t block = col / (NV ? 16 : 32), tiles = k.q.scale_tiles;
+  const int64_t scale0 = block / 4 * kScaleTile + block % 4, step = (int64_t)gridDim.y * down;
+  for (int64_t row0 = (int64_t)blockIdx.y * down + (threadIdx.x >> log2_across); row0 < k.rows;
+       row0 += 4 * step) {
+    uint32_t codes[4], scale[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], d);
-    store8(k.y, row, col, k.cols - col < 8 ? (int)(k.cols - col) : 8, v, e, ZERO_SITE_FP4);
+    for (int i = 0; i < 4; ++i) {
+      const int64_t row = row0 + i * step, at = row * k.q.ld + col / 2;
+      const int64_t s = (row >> 7) * tiles * kScaleTile + scale0 + (row & 31) * 16 +
+                        ((row >> 5) & 3) * 4;
+      codes[i] = scale[i] = 0;
+      if (row < k.rows &&
+          in_extent(at, at + 4, row * k.q.ld, row * k.q.ld + k.q.line_bytes, ZERO_SITE_FP4) &&
+          in_extent(s, s + 1, 0, k.q.scale_bytes, ZERO_SITE_FP4)) {
+        codes[i] = *reinterpret_cast<const uint32_t*>(k.q.codes + at);
+        scale[i] = k.q.scales[s];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t row = row0 + i * step;
+      float v[8];
+      from_codes8(codes[i], v);
+      const float d = scale_value<NV>(scale[i], g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], d);
+      if (row < k.rows) store8(k.y, row, col, valid, v, e, ZERO_SITE_FP4);
+    }
   }
 }
 
 cudaError_t launch_dequantize(const DequantK& k, cudaStream_t st) {
-  const int64_t total = (k.cols + 7) / 8 * k.rows;
-  if (total == 0) return cudaSuccess;
-  const int64_t most = (int64_t)sm_count() * 8, blocks = (total + kThreads - 1) / kThreads;
-  const dim3 grid((unsigned)(blocks < most ? blocks : most));
-  return k.nv ? launch_next(dequantize_kernel<true>, grid, dim3(kThreads), st, k)
-              : launch_next(dequantize_kernel<false>, grid, dim3(kThreads), st, k);
+  if (k.rows == 0 || k.cols == 0) return cudaSuccess;
+  const Walk w = walk_over(k.rows, k.cols, 4);
+  return k.nv ? launch_next(dequantize_kernel<true>, w.grid, dim3(kThreads), st, k, w.log2_across)
+              : launch_next(dequantize_kernel<false>, w.grid, dim3(kThreads), st, k,
+                            w.log2_across);
 }
 
 // ------------------------------------------------------- the whole's scale --
@@ -295,40 +323,56 @@ __device__ __forceinline__ float block_max(float v) {
   for (int m = 16; m; m >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, m));
   return v;
 }
-__global__ void __launch_bounds__(kThreads) maxima_kernel(const __grid_constant__ MaxK k) {
+__global__ void __launch_bounds__(kThreads)
+    maxima_kernel(const __grid_constant__ MaxK k, int log2_across) {
   after_previous_kernel();
   const Extent e{k.rows, k.cols};
-  const int64_t units = (k.cols + 7) / 8, total = units * k.rows;
+  const int across = 1 << log2_across, down = kThreads >> log2_across;
+  const int64_t step = (int64_t)gridDim.y * down;
   float top = 0.0f;
-  for (int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x; u < total;
-       u += (int64_t)gridDim.x * kThreads) {
-    const int64_t row = u / units, col = u % units * 8;
-    float v[8];
-    load8(k.x, row, col, k.cols - col < 8 ? (int)(k.cols - col) : 8, v, e, ZERO_SITE_FP4);
+  for (int64_t col = ((int64_t)blockIdx.x * across + (threadIdx.x & (across - 1))) * 8;
+       col < k.cols; col += (int64_t)gridDim.x * across * 8) {
+    const int valid = k.cols - col < 8 ? (int)(k.cols - col) : 8;
+    for (int64_t row0 = (int64_t)blockIdx.y * down + (threadIdx.x >> log2_across); row0 < k.rows;
+         row0 += 4 * step) {
+      Raw8 raw[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float a = fabsf(v[j]);
-      top = a < __uint_as_float(kInfBits) ? fmaxf(top, a) : top;
+      for (int i = 0; i < 4; ++i) {
+        raw[i].a = raw[i].b = make_uint4(0, 0, 0, 0);
+        if (row0 + i * step < k.rows)
+          raw[i] = raw8(k.x, row0 + i * step, col, valid, e, ZERO_SITE_FP4);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float v[8];
+        from_raw(k.x, raw[i], v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float a = fabsf(v[j]);
+          top = a < __uint_as_float(kInfBits) ? fmaxf(top, a) : top;
+        }
+      }
     }
   }
   top = block_max(top);
-  if (threadIdx.x == 0 && in_extent(blockIdx.x, blockIdx.x + 1, 0, kMaxima, ZERO_SITE_FP4))
-    k.maxima[blockIdx.x] = top;
+  const int at = (int)(blockIdx.y * gridDim.x + blockIdx.x);
+  if (threadIdx.x == 0 && in_extent(at, at + 1, 0, kMaxima, ZERO_SITE_FP4)) k.maxima[at] = top;
 }
 __global__ void __launch_bounds__(kMaxima) maximum_kernel(const float* maxima, int n, float* g) {
   after_previous_kernel();
-  float top = (int)threadIdx.x < n ? maxima[threadIdx.x] : 0.0f;
+  float top = (int)threadIdx.x < n ? *(volatile const float*)(maxima + threadIdx.x) : 0.0f;
   top = block_max(top);
   if (threadIdx.x == 0) *g = top > 0.0f ? __fdiv_rn(top, 2688.0f) : 1.0f;
 }
 
 cudaError_t launch_tensor_scale(const MaxK& k, float* g, cudaStream_t st) {
-  const int64_t total = (k.cols + 7) / 8 * k.rows;
-  const int64_t most = (int64_t)sm_count() * 4 < kMaxima ? (int64_t)sm_count() * 4 : kMaxima;
-  const int64_t blocks = (total + kThreads - 1) / kThreads;
-  const int n = (int)(blocks < most ? blocks : most);
-  if (n > 0) {
-    cudaError_t e = launch_next(maxima_kernel, dim3(n), dim3(kThreads), st, k);
+  int n = 0;
+  if (k.rows > 0 && k.cols > 0) {
+    Walk w = walk_over(k.rows, k.cols, 4);
+    if (w.grid.x > kMaxima) w.grid.x = kMaxima;
+    if (w.grid.x * w.grid.y > kMaxima) w.grid.y = kMaxima / w.grid.x;
+    n = (int)(w.grid.x * w.grid.y);
+    cudaError_t e = launch_next(maxima_kernel, w.grid, dim3(kThreads), st, k, w.log2_across);
     if (e != cudaSuccess) return e;
   }
   return launch_next(maximum_kernel, dim3(1), dim3(kMaxima), st, k.maxima, n, g);
@@ -336,6 +380,7 @@ cudaError_t launch_tensor_scale(const MaxK& k, float* g, cudaStream_t st) {
 
 cudaError_t launch_fp4_product(const ProductK& k, int mode, cudaStream_t st) {
   if (k.rows <= 0 || k.cols <= 0) return cudaSuccess;
+  if (k.rows <= kFewRows) return launch_fp4_rows(k, mode, st);
   return mode == LIN_FORWARD ? launch_mode<LIN_FORWARD, OF_FP4>(k, st)
                              : launch_mode<LIN_DINPUT, OF_FP4>(k, st);
 }

@@ -131,6 +131,8 @@ struct MaxK {
 };
 cudaError_t launch_tensor_scale(const MaxK& k, float* g, cudaStream_t st);
 cudaError_t launch_fp4_product(const ProductK& k, int mode, cudaStream_t st);
+// Of up to kFewRows rows of 4-bit operands.
+cudaError_t launch_fp4_rows(const ProductK& k, int mode, cudaStream_t st);
 
 // Matrices of a batch: `stride` elements apart, or (listed) from these elements on.
 struct OrthoPlaces {
@@ -191,6 +193,7 @@ cudaError_t bounds_dropout(BoundsRec* out, bool reset);
 cudaError_t bounds_lnorm(BoundsRec* out, bool reset);
 cudaError_t bounds_rows(BoundsRec* out, bool reset);
 cudaError_t bounds_fp4(BoundsRec* out, bool reset);
+cudaError_t bounds_fp4_rows(BoundsRec* out, bool reset);
 cudaError_t bounds_ortho(BoundsRec* out, bool reset);
 
 }  // namespace zk

@@ -35,6 +35,7 @@
 // memory as tensor memory wants them, are copied there before its products.
 #pragma once
 
+#include "zero_fp4.cuh"
 #include "zero_tile.cuh"
 
 namespace zk {
@@ -47,7 +48,6 @@ constexpr int kRound = 12;             // 64-deep steps of a round (see launch_m
 constexpr int kOnesBytes = 2048;
 constexpr int kSlot = 16384;           // a box of 128 rows of 128 bytes
 constexpr int kMostBoxes = 3;          // chunks of boxes in the ring
-constexpr int kScaleTile = 512;        // scales of 128 rows, four blocks each (OF_FP4)
 constexpr uint32_t kScaleColumn = 384; // where they lie in tensor memory, behind the sums
 
 // What the operands hold.

@@ -22,52 +22,8 @@
 
 namespace zk {
 
-constexpr int kIn = ZERO_SITE_LINEAR_IN, kOut = ZERO_SITE_LINEAR_OUT;
+constexpr int kIn = ZERO_SITE_LINEAR_IN;
 constexpr int kWarps = 8, kOutputs = 4, kAcross = 32;
-
-// What follows the product at one element.
-template <int MODE>
-__device__ __forceinline__ void finish1(const EpiK& k, int64_t row, int64_t col, float v,
-                                        const Extent& e, uint64_t offset) {
-  auto in = [&](const Mat& m) {
-    const int64_t at = row * m.ld;
-    return in_extent(at + col, at + col + 1, at, at + e.cols, kOut) &&
-           in_extent(row, row + 1, 0, e.rows, kOut);
-  };
-  auto get = [&](const Mat& m) { return in(m) ? load1(m, row * m.ld + col) : 0.0f; };
-  auto put = [&](const Mat& m, float x) {
-    if (in(m)) store1(m, row * m.ld + col, x);
-  };
-  if constexpr (MODE == LIN_FORWARD) {
-    const float residual = k.residual.p ? get(k.residual) : 0.0f;
-    const float gate = k.gate.p ? get(k.gate) : 1.0f;
-    if (k.bias.p && in_extent(col, col + 1, 0, e.cols, kIn)) v += load1(k.bias, col);
-    if (k.pre.p) put(k.pre, v);
-    float z[1] = {v};
-    activate<1>(z, k.act);
-    v = z[0];
-    if (k.gate.p) v *= gate;
-    if (k.drop.on) {
-      const uint4 w = philox(make_uint4((uint32_t)(col >> 2), (uint32_t)row, (uint32_t)offset,
-                                        (uint32_t)(offset >> 32)),
-                             k.drop);
-      const uint32_t word = col & 2 ? (col & 1 ? w.w : w.z) : (col & 1 ? w.y : w.x);
-      v = word >= k.drop.least && !k.drop.all ? v * k.drop.scale : 0.0f;
-    }
-    if (k.residual.p) v += residual;
-  } else {
-    if (k.pre.p) {
-      float value[1] = {get(k.pre)}, slope[1];
-      activate_grad<1>(value, slope, k.act);
-      if (k.gate.p) {
-        if (k.dgate.p) put(k.dgate, value[0] * v);
-        slope[0] *= get(k.gate);
-      }
-      v *= slope[0];
-    }
-  }
-  put(k.out, v);
-}
 
 // V = 8 or 1 consecutive values of a line as they lie in memory.
 template <int V>
