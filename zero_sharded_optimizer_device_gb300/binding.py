@@ -1106,6 +1106,22 @@ class _Fp4:
 
     def checked(self, rows: int, cols: int, format: int, what: str):
         s, c, t, g = self.struct, self.codes, self.scales, self.tensor_scale
+        if not _Torch.ready:
+            _Torch.load()
+        blocks = (cols + 15) // 16 if format == ZERO_FP4_NV else (cols + 31) // 32
+        if g is None:
+            s.tensor_scale = None
+        else:
+            _need(g, 4, what + ".tensor_scale")
+            s.tensor_scale = _here(g)
+        # as usual: whole tensors of bytes on the current device that hold enough
+        if _Torch.cuda and not (c is None or t is None or isinstance(c, int) or isinstance(t, int)):
+            dev = _Torch.device()
+            if c.get_device() == dev == t.get_device() and c.is_contiguous() and \
+                    t.is_contiguous() and c.numel() >= rows * s.ld and \
+                    t.numel() >= (rows + 127) // 128 * ((blocks + 3) // 4) * 512:
+                s.codes, s.scales = c.data_ptr(), t.data_ptr()
+                return ctypes.byref(s)
         if rows > 0 and cols > 0:
             if not (c is None or isinstance(c, int)):
                 need = (rows - 1) * s.ld + (cols + 31) // 32 * 16
@@ -1116,11 +1132,8 @@ class _Fp4:
                     if have < need:
                         raise ValueError(f"{what}.codes: holds {have} bytes, the call touches "
                                          f"{need}")
-            blocks = (cols + 15) // 16 if format == ZERO_FP4_NV else (cols + 31) // 32
             _need(t, (rows + 127) // 128 * ((blocks + 3) // 4) * 512, what + ".scales")
-        if g is not None:
-            _need(g, 4, what + ".tensor_scale")
-        s.codes, s.scales, s.tensor_scale = _here(c), _here(t), None if g is None else _here(g)
+        s.codes, s.scales = _here(c), _here(t)
         return ctypes.byref(s)
 
 

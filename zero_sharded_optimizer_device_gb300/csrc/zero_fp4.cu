@@ -9,16 +9,35 @@ namespace zk {
 // A block's scale byte and the factor that brings its values to codes, from
 // the largest magnitude's bits (NaN and infinity are the largest as integers).
 // A block that holds either has scale NaN and codes 0.
+// NV: the quotient by 6 g first by its reciprocal, half a unit of E4M3's
+// sixteenths from it at most where both neighbours at 2^-21 give the same byte;
+// else divided (an IEEE division for each block: __DIV__).
 constexpr uint32_t kInfBits = 0x7F800000u;
+struct Whole {
+  float g, six_g, by_six_g;  // 1 / (6 g)
+};
 template <bool NV>
-__device__ __forceinline__ uint32_t block_scale(uint32_t top, float six_g, float g,
-                                                float& factor) {
+__device__ __forceinline__ Whole whole_of(const float* at) {
+  Whole w;
+  w.g = NV && at ? *(volatile const float*)at : 1.0f;
+  w.six_g = __fmul_rn(6.0f, w.g);
+  w.by_six_g = __frcp_rn(w.six_g);
+  return w;
+}
+template <bool NV>
+__device__ __forceinline__ uint32_t block_scale(uint32_t top, const Whole& w, float& factor) {
   factor = 0.0f;
   if (NV) {
     if (top >= kInfBits) return 0x7Fu;
-    const uint32_t byte = to_e4m3(__fdiv_rn(__uint_as_float(top), six_g));
-    const float d = __fmul_rn(from_e4m3(byte), g);
-    if (d > 0.0f) factor = __fdiv_rn(1.0f, d);
+    const float most = __uint_as_float(top), t = most * w.by_six_g;
+    uint16_t two;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+        : "=h"(two)
+        : "f"(t + t * 0x1p-21f), "f"(t - t * 0x1p-21f));
+    uint32_t byte = two & 0xFFu;
+    if (byte != two >> 8) byte = to_e4m3(__fdiv_rn(most, w.six_g));
+    const float d = __fmul_rn(from_e4m3(byte), w.g);
+    if (d > 0.0f) factor = __frcp_rn(d);
     return byte;
   }
   if (top >= kInfBits) return 0xFFu;
@@ -28,6 +47,72 @@ __device__ __forceinline__ uint32_t block_scale(uint32_t top, float six_g, float
   factor = __uint_as_float((254u - byte) << 23);
   return byte;
 }
+
+// Eight columns of rows some distance apart, as they lie in memory: one or two
+// 16-byte accesses where the matrix and the columns allow it, decided once.
+template <bool WIDE>
+struct Down {
+  const Mat& m;
+  char* p;
+  int64_t step, row, col, rows_apart;
+  int valid;
+  bool fast;
+  __device__ __forceinline__ Down(const Mat& mat, int64_t row0, int64_t apart, int64_t column,
+                                  int count)
+      : m(mat), row(row0), col(column), rows_apart(apart), valid(count) {
+    constexpr int es = WIDE ? 4 : 2;
+    p = static_cast<char*>(m.p) + (row0 * m.ld + column) * es;
+    step = apart * m.ld * es;
+    fast = m.vec && count == 8;
+  }
+  // N rows, zeros from row `rows` on.  One test for all: conditions between the
+  // loads would keep them from being in flight together (maxima of 8192 x 4096
+  // bf16: 31 us so, __MAX__ with one).
+  template <int N>
+  __device__ __forceinline__ void get(Raw8 r[N], int64_t rows, const Extent& e) const {
+    if (fast && in_extent(row, row + 1, 0, e.rows, ZERO_SITE_FP4) &&
+        in_extent(col, col + 8, 0, e.cols, ZERO_SITE_FP4)) {
+      const char* at = p;
+      int64_t here = row;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {  // past the last row the one before again
+        r[i].a = ld16(at);
+        r[i].b = WIDE ? ld16(at + 16) : make_uint4(0, 0, 0, 0);
+        here += rows_apart;
+        at += here < rows ? step : 0;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        r[i].a = r[i].b = make_uint4(0, 0, 0, 0);
+        if (row + i * rows_apart < rows && valid > 0)
+          r[i] = raw8(m, row + i * rows_apart, col, valid, e, ZERO_SITE_FP4);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (row + i * rows_apart >= rows) r[i].a = r[i].b = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void put(int i, const float v[8], const Extent& e) const {
+    const int64_t at = row + i * rows_apart;
+    if (fast && in_extent(at, at + 1, 0, e.rows, ZERO_SITE_FP4) &&
+        in_extent(col, col + 8, 0, e.cols, ZERO_SITE_FP4)) {
+      if (WIDE) {
+        float4* to = reinterpret_cast<float4*>(p + i * step);
+        to[0] = make_float4(v[0], v[1], v[2], v[3]);
+        to[1] = make_float4(v[4], v[5], v[6], v[7]);
+      } else {
+        *reinterpret_cast<uint4*>(p + i * step) = pack8(v);
+      }
+      return;
+    }
+    store8(m, at, col, valid, v, e, ZERO_SITE_FP4);
+  }
+  __device__ __forceinline__ void on(int steps) {
+    p += steps * step;
+    row += steps * rows_apart;
+  }
+};
 
 // Codes of eight values of a block whose factor is known.
 __device__ __forceinline__ uint32_t codes8(const float v[8], float factor) {
@@ -43,8 +128,8 @@ __device__ __forceinline__ uint32_t codes8(const float v[8], float factor) {
 // those (padding included) has one writer.  Then a thread takes one block of a
 // row after another, and in the other direction the blocks of two columns side
 // by side (bf16: one 32-bit word); largest magnitudes of bf16 are found two at
-// a time as integers, which order NaN and infinity above all numbers.  Codes go
-// out through shared memory, 64 bytes of each line.
+// a time, fp32's as integers, which order NaN and infinity above all numbers.
+// Codes go out through shared memory, 64 bytes of each line.
 constexpr int kQuantTile = 128, kQuantThreads = 256, kCodeLine = 80;
 
 template <bool WIDE>
@@ -83,8 +168,11 @@ __device__ __forceinline__ void store_quantized(const Fp4Mat& o, const unsigned 
 }
 
 __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return a > b ? a : b; }
-// The magnitudes' bits of two bf16.
-__device__ __forceinline__ uint32_t magnitudes2(uint32_t w) { return w & 0x7FFF7FFFu; }
+// The larger magnitude of two bf16 in each half; NaN where there is one.
+__device__ __forceinline__ uint32_t larger2(uint32_t top, uint32_t w) {
+  asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(top) : "r"(w & 0x7FFF7FFFu));
+  return top;
+}
 
 template <bool NV, bool WIDE>
 __global__ void __launch_bounds__(kQuantThreads, WIDE ? 2 : 4)
@@ -94,8 +182,7 @@ __global__ void __launch_bounds__(kQuantThreads, WIDE ? 2 : 4)
   Shared& sh = *reinterpret_cast<Shared*>(quant_smem);
   constexpr int kSize = NV ? 16 : 32, kTiles = NV ? 2 : 1, kBlocks = kQuantTile / kSize;
   after_previous_kernel();
-  const float g = NV && k.g ? *(volatile const float*)k.g : 1.0f;
-  const float six_g = __fmul_rn(6.0f, g);
+  const Whole whole = whole_of<NV>(k.g);
   const int64_t row0 = (int64_t)(blockIdx.x / k.tiles_j) * kQuantTile;
   const int64_t col0 = (int64_t)(blockIdx.x % k.tiles_j) * kQuantTile;
   const int t = threadIdx.x;
@@ -104,15 +191,17 @@ __global__ void __launch_bounds__(kQuantThreads, WIDE ? 2 : 4)
     const Extent e{k.rows, k.cols};
     const int64_t col = col0 + unit * 8;
     const int valid = col >= k.cols ? 0 : k.cols - col < 8 ? (int)(k.cols - col) : 8;
+    Raw8 raw[8];
+#pragma unroll
+    for (int p = 0; p < 8; ++p) raw[p].a = raw[p].b = make_uint4(0, 0, 0, 0);
+    if (row0 + line < k.rows)
+      Down<WIDE>(k.x, row0 + line, 16, col, valid).template get<8>(raw, k.rows, e);
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
-      const int r = p * 16 + line;
-      Raw8 raw;
-      raw.a = raw.b = make_uint4(0, 0, 0, 0);
-      if (row0 + r < k.rows && valid) raw = raw8(k.x, row0 + r, col, valid, e, ZERO_SITE_FP4);
-      uint4* at = reinterpret_cast<uint4*>(sh.tile + r * Shared::kLine + unit * 8 * Shared::kElem);
-      at[0] = raw.a;
-      if (WIDE) at[1] = raw.b;
+      uint4* at = reinterpret_cast<uint4*>(sh.tile + (p * 16 + line) * Shared::kLine +
+                                           unit * 8 * Shared::kElem);
+      at[0] = raw[p].a;
+      if (WIDE) at[1] = raw[p].b;
     }
   }
   __syncthreads();
@@ -135,12 +224,11 @@ __global__ void __launch_bounds__(kQuantThreads, WIDE ? 2 : 4)
         uint32_t two = 0;
 #pragma unroll
         for (int i = 0; i < kWords; ++i)
-          two = __vmaxu2(__vmaxu2(two, __vmaxu2(magnitudes2(raw[i].x), magnitudes2(raw[i].y))),
-                         __vmaxu2(magnitudes2(raw[i].z), magnitudes2(raw[i].w)));
+          two = larger2(larger2(larger2(larger2(two, raw[i].x), raw[i].y), raw[i].z), raw[i].w);
         top = larger(two << 16, two & 0xFFFF0000u);
       }
       float factor;
-      sh.scales[0][scale_at(r, b)] = (unsigned char)block_scale<NV>(top, six_g, g, factor);
+      sh.scales[0][scale_at(r, b)] = (unsigned char)block_scale<NV>(top, whole, factor);
       uint32_t* out = reinterpret_cast<uint32_t*>(sh.codes + r * kCodeLine + b * (kSize / 2));
 #pragma unroll
       for (int i = 0; i < kSize / 8; ++i) {
@@ -178,7 +266,7 @@ __global__ void __launch_bounds__(kQuantThreads, WIDE ? 2 : 4)
     } else {
       uint32_t two = 0;
 #pragma unroll
-      for (int i = 0; i < kSize; ++i) two = __vmaxu2(two, magnitudes2(raw[i]));
+      for (int i = 0; i < kSize; ++i) two = larger2(two, raw[i]);
       top[0] = two << 16;
       top[kSide - 1] = two & 0xFFFF0000u;
     }
@@ -186,7 +274,7 @@ __global__ void __launch_bounds__(kQuantThreads, WIDE ? 2 : 4)
     for (int h = 0; h < kSide; ++h) {
       float factor;
       const uint32_t most = !WIDE && h == 0 ? top[0] : top[kSide - 1];
-      sh.scales[1][scale_at(c + h, b)] = (unsigned char)block_scale<NV>(most, six_g, g, factor);
+      sh.scales[1][scale_at(c + h, b)] = (unsigned char)block_scale<NV>(most, whole, factor);
       uint32_t* out =
           reinterpret_cast<uint32_t*>(sh.codes + (c + h) * kCodeLine + b * (kSize / 2));
 #pragma unroll
@@ -243,13 +331,13 @@ struct Walk {
   int log2_across;
   dim3 grid;
 };
-static Walk walk_over(int64_t rows, int64_t cols, int rows_a_thread) {
+static Walk walk_over(int64_t rows, int64_t cols) {
   const int64_t units = (cols + 7) / 8;
   Walk w;
   w.log2_across = 0;
   while (w.log2_across < 5 && (1ll << w.log2_across) < units) ++w.log2_across;
   const int64_t x = (units + (1 << w.log2_across) - 1) >> w.log2_across;
-  const int64_t each = (int64_t)(kThreads >> w.log2_across) * rows_a_thread;
+  const int64_t each = kThreads >> w.log2_across;
   int64_t y = (rows + each - 1) / each, most = (int64_t)sm_count() * 8 / (x < 1 ? 1 : x) + 1;
   if (most > 65535) most = 65535;
   if (y > most) y = most;
@@ -259,7 +347,7 @@ static Walk walk_over(int64_t rows, int64_t cols, int rows_a_thread) {
 
 // --------------------------------------------------------------- dequantise --
 // A thread takes 8 columns of four rows at a time: 4 bytes of codes, one scale.
-template <bool NV>
+template <bool NV, bool WIDE>
 __global__ void __launch_bounds__(kThreads)
     dequantize_kernel(const __grid_constant__ DequantK k, int log2_across) {
   after_previous_kernel();
@@ -269,43 +357,55 @@ __global__ void __launch_bounds__(kThreads)
   const int64_t col = ((int64_t)blockIdx.x * across + (threadIdx.x & (across - 1))) * 8;
   if (col >= k.cols) return;
   const int valid = k.cols - col < 8 ? (int)(k.cols - col) : 8;
-  const int64_t block = col / (NV ? 16 : 32), tiles = k.q.scale_tiles;
-  const int64_t scale0 = block / 4 * kScaleTile + block % 4, step = (int64_t)gridDim.y * down;
-  for (int64_t row0 = (int64_t)blockIdx.y * down + (threadIdx.x >> log2_across); row0 < k.rows;
-       row0 += 4 * step) {
+  const int64_t block = col / (NV ? 16 : 32), per_tile = k.q.scale_tiles * kScaleTile;
+  const unsigned char* scales = k.q.scales + block / 4 * kScaleTile + block % 4;
+  const int64_t step = (int64_t)gridDim.y * down;
+  Down<WIDE> y(k.y, (int64_t)blockIdx.y * down + (threadIdx.x >> log2_across), step, col, valid);
+  const unsigned char* from = k.q.codes + y.row * k.q.ld + col / 2;
+  const int64_t down_bytes = step * k.q.ld;
+  for (; y.row < k.rows; y.on(4), from += 4 * down_bytes) {
     uint32_t codes[4], scale[4];
+    int64_t row = y.row;
+    const unsigned char* at = from;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t row = row0 + i * step, at = row * k.q.ld + col / 2;
-      const int64_t s = (row >> 7) * tiles * kScaleTile + scale0 + (row & 31) * 16 +
-                        ((row >> 5) & 3) * 4;
+    for (int i = 0; i < 4; ++i) {  // past the last row the one before again
+      const uint32_t low = (uint32_t)row;
+      const int64_t s = (row >> 7) * per_tile + ((low & 31) << 4 | (low >> 3 & 12));
       codes[i] = scale[i] = 0;
-      if (row < k.rows &&
-          in_extent(at, at + 4, row * k.q.ld, row * k.q.ld + k.q.line_bytes, ZERO_SITE_FP4) &&
+      if (in_extent(row, row + 1, 0, k.rows, ZERO_SITE_FP4) &&
+          in_extent(col / 2, col / 2 + 4, 0, k.q.line_bytes, ZERO_SITE_FP4) &&
           in_extent(s, s + 1, 0, k.q.scale_bytes, ZERO_SITE_FP4)) {
-        codes[i] = *reinterpret_cast<const uint32_t*>(k.q.codes + at);
-        scale[i] = k.q.scales[s];
+        codes[i] = *reinterpret_cast<const uint32_t*>(at);
+        scale[i] = scales[s];
       }
+      const bool more = row + step < k.rows;
+      row += more ? step : 0;
+      at += more ? down_bytes : 0;
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int64_t row = row0 + i * step;
       float v[8];
       from_codes8(codes[i], v);
       const float d = scale_value<NV>(scale[i], g);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], d);
-      if (row < k.rows) store8(k.y, row, col, valid, v, e, ZERO_SITE_FP4);
+      if (y.row + i * step < k.rows) y.put(i, v, e);
     }
   }
 }
 
+template <bool NV>
+static cudaError_t launch_dequantize_as(const DequantK& k, cudaStream_t st) {
+  const Walk w = walk_over(k.rows, k.cols);
+  return k.y.dtype == ZERO_F32
+             ? launch_next(dequantize_kernel<NV, true>, w.grid, dim3(kThreads), st, k,
+                           w.log2_across)
+             : launch_next(dequantize_kernel<NV, false>, w.grid, dim3(kThreads), st, k,
+                           w.log2_across);
+}
 cudaError_t launch_dequantize(const DequantK& k, cudaStream_t st) {
   if (k.rows == 0 || k.cols == 0) return cudaSuccess;
-  const Walk w = walk_over(k.rows, k.cols, 4);
-  return k.nv ? launch_next(dequantize_kernel<true>, w.grid, dim3(kThreads), st, k, w.log2_across)
-              : launch_next(dequantize_kernel<false>, w.grid, dim3(kThreads), st, k,
-                            w.log2_across);
+  return k.nv ? launch_dequantize_as<true>(k, st) : launch_dequantize_as<false>(k, st);
 }
 
 // ------------------------------------------------------- the whole's scale --
@@ -323,37 +423,52 @@ __device__ __forceinline__ float block_max(float v) {
   for (int m = 16; m; m >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, m));
   return v;
 }
+// NaN loses every comparison; a thread that met an infinity goes over its
+// values once more and leaves what is not finite out.
+template <bool WIDE>
+__device__ __forceinline__ float unit_top(float top, const Raw8& raw, bool finite) {
+  const uint32_t w[8] = {raw.a.x, raw.a.y, raw.a.z, raw.a.w, raw.b.x, raw.b.y, raw.b.z, raw.b.w};
+  if (WIDE || finite) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float a =
+          fabsf(WIDE ? __uint_as_float(w[j]) : j & 1 ? bf16_hi(w[j / 2]) : bf16_lo(w[j / 2]));
+      top = finite && !(a < __uint_as_float(kInfBits)) ? top : fmaxf(top, a);
+    }
+    return top;
+  }
+  uint32_t two = w[0] & 0x7FFF7FFFu;
+#pragma unroll
+  for (int j = 1; j < 4; ++j)
+    asm("max.bf16x2 %0, %0, %1;" : "+r"(two) : "r"(w[j] & 0x7FFF7FFFu));
+  return fmaxf(top, fmaxf(bf16_lo(two), bf16_hi(two)));
+}
+template <bool WIDE>
 __global__ void __launch_bounds__(kThreads)
     maxima_kernel(const __grid_constant__ MaxK k, int log2_across) {
   after_previous_kernel();
+  constexpr int kAhead = WIDE ? 4 : 8;  // rows whose loads are in flight together
   const Extent e{k.rows, k.cols};
   const int across = 1 << log2_across, down = kThreads >> log2_across;
   const int64_t step = (int64_t)gridDim.y * down;
-  float top = 0.0f;
-  for (int64_t col = ((int64_t)blockIdx.x * across + (threadIdx.x & (across - 1))) * 8;
-       col < k.cols; col += (int64_t)gridDim.x * across * 8) {
-    const int valid = k.cols - col < 8 ? (int)(k.cols - col) : 8;
-    for (int64_t row0 = (int64_t)blockIdx.y * down + (threadIdx.x >> log2_across); row0 < k.rows;
-         row0 += 4 * step) {
-      Raw8 raw[4];
+  auto over = [&](bool finite) {
+    float top = 0.0f;
+    for (int64_t col = ((int64_t)blockIdx.x * across + (threadIdx.x & (across - 1))) * 8;
+         col < k.cols; col += (int64_t)gridDim.x * across * 8) {
+      const int valid = k.cols - col < 8 ? (int)(k.cols - col) : 8;
+      Down<WIDE> x(k.x, (int64_t)blockIdx.y * down + (threadIdx.x >> log2_across), step, col,
+                   valid);
+      for (; x.row < k.rows; x.on(kAhead)) {
+        Raw8 raw[kAhead];
+        x.template get<kAhead>(raw, k.rows, e);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        raw[i].a = raw[i].b = make_uint4(0, 0, 0, 0);
-        if (row0 + i * step < k.rows)
-          raw[i] = raw8(k.x, row0 + i * step, col, valid, e, ZERO_SITE_FP4);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float v[8];
-        from_raw(k.x, raw[i], v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float a = fabsf(v[j]);
-          top = a < __uint_as_float(kInfBits) ? fmaxf(top, a) : top;
-        }
+        for (int i = 0; i < kAhead; ++i) top = unit_top<WIDE>(top, raw[i], finite);
       }
     }
-  }
+    return top;
+  };
+  float top = over(false);
+  if (top >= __uint_as_float(kInfBits)) top = over(true);
   top = block_max(top);
   const int at = (int)(blockIdx.y * gridDim.x + blockIdx.x);
   if (threadIdx.x == 0 && in_extent(at, at + 1, 0, kMaxima, ZERO_SITE_FP4)) k.maxima[at] = top;
@@ -368,11 +483,12 @@ __global__ void __launch_bounds__(kMaxima) maximum_kernel(const float* maxima, i
 cudaError_t launch_tensor_scale(const MaxK& k, float* g, cudaStream_t st) {
   int n = 0;
   if (k.rows > 0 && k.cols > 0) {
-    Walk w = walk_over(k.rows, k.cols, 4);
+    Walk w = walk_over(k.rows, k.cols);
     if (w.grid.x > kMaxima) w.grid.x = kMaxima;
     if (w.grid.x * w.grid.y > kMaxima) w.grid.y = kMaxima / w.grid.x;
     n = (int)(w.grid.x * w.grid.y);
-    cudaError_t e = launch_next(maxima_kernel, w.grid, dim3(kThreads), st, k, w.log2_across);
+    cudaError_t e = launch_next(k.x.dtype == ZERO_F32 ? maxima_kernel<true> : maxima_kernel<false>,
+                                w.grid, dim3(kThreads), st, k, w.log2_across);
     if (e != cudaSuccess) return e;
   }
   return launch_next(maximum_kernel, dim3(1), dim3(kMaxima), st, k.maxima, n, g);
