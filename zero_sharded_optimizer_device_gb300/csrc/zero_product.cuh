@@ -617,6 +617,112 @@ __device__ __forceinline__ void box_traffic(const BoxMaps& maps, const ProductK&
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
+// OF_FP4: a warp each for bringing and for storing (a tile's products are a
+// quarter of bf16's there, and its boxes have to keep up), with a barrier for
+// slots that have been read out.
+template <int MODE, int FORM>
+__device__ __forceinline__ void box_bring(const BoxMaps& maps, const ProductK& k, const TileK& g,
+                                          uint32_t boxes, uint32_t efull, uint32_t bfree,
+                                          int first, int tiles, int step, uint32_t half,
+                                          int split, volatile int* dead) {
+  constexpr bool wide = FORM == BOX_F32;
+  constexpr int W = wide ? 32 : 64;
+  const uint32_t ring = g.boxes, second = g.two_slots ? kSlot : 0, chunk_bytes = kSlot + second;
+  constexpr uint32_t narrow = wide ? kSlot / 2 : kSlot;  // a bf16 box
+  const BoxEpi e = box_epi<MODE>(k.epi);
+  const uint32_t bytes = (e.gate ? narrow : 0) + (e.residual || e.old ? kSlot : 0) +
+                         (MODE == LIN_DINPUT && e.pre ? narrow : 0);
+  const int64_t cols = k.cols;
+  ChunkWalk in;
+  in.t = first;
+  in.count = in.cc = 0;
+  if (first < tiles) {
+    enter_tile<W>(g, cols, split, in);
+    --in.cc;
+    next_chunk<W>(g, cols, split, tiles, step, in);
+  }
+  uint32_t lb = 0, lph = 1, issued = 0;
+  bool live = true;
+  while (in.t < tiles) {
+    live = bar_wait(bfree + 8 * lb, lph, dead);
+    live = __all_sync(0xffffffffu, live);
+    if (!live) break;
+    const uint32_t at = boxes + lb * chunk_bytes, slot1 = at + second, bar = efull + 8 * lb;
+    const int x = in.tj * g.bn + in.cc * W, y = in.ti * 256 + (int)half * kRowsCta;
+    if (elect()) {
+      bar_expect(bar, bytes);
+      if constexpr (MODE == LIN_FORWARD) {
+        if (e.gate) box_load(&maps.gate, at, x, y, bar);
+        if (e.residual) box_load(&maps.extra, slot1, x, y, bar);
+      } else {
+        if (e.pre) box_load(&maps.pre, wide ? slot1 : at, x, y, bar);
+        if (e.gate) box_load(&maps.gate, wide ? slot1 + kSlot / 2 : slot1, x, y, bar);
+      }
+    }
+    __syncwarp();
+    ++issued;
+    if (++lb == ring) {
+      lb = 0;
+      lph ^= 1;
+    }
+    next_chunk<W>(g, cols, split, tiles, step, in);
+  }
+  // after a wait that gave up: the boxes in flight land before the CTA returns
+  for (uint32_t q = issued > ring ? issued - ring : 0; !live && q < issued; ++q) {
+    const long long t0 = clock64();
+    while (!bar_try(efull + 8 * (q % ring), (q / ring) & 1) && clock64() - t0 < kWaitCycles / 8) {
+    }
+  }
+}
+template <int MODE, int FORM>
+__device__ __forceinline__ void box_put(const BoxMaps& maps, const ProductK& k, const TileK& g,
+                                        uint32_t boxes, uint32_t edone, uint32_t bfree, int first,
+                                        int tiles, int step, uint32_t half, int split,
+                                        volatile int* dead) {
+  constexpr bool wide = FORM == BOX_F32;
+  constexpr int W = wide ? 32 : 64;
+  const uint32_t ring = g.boxes, second = g.two_slots ? kSlot : 0, chunk_bytes = kSlot + second;
+  const BoxEpi e = box_epi<MODE>(k.epi);
+  const int64_t rows = k.rows, cols = k.cols;
+  ChunkWalk out;
+  out.t = first;
+  out.count = out.cc = 0;
+  if (first < tiles) {
+    enter_tile<W>(g, cols, split, out);
+    --out.cc;
+    next_chunk<W>(g, cols, split, tiles, step, out);
+  }
+  uint32_t sb = 0, sph = 0;
+  while (out.t < tiles) {
+    bool live = bar_wait(edone + 8 * sb, sph, dead);
+    live = __all_sync(0xffffffffu, live);  // the lanes leave together
+    if (!live) break;
+    const uint32_t at = boxes + sb * chunk_bytes, slot1 = at + second;
+    const int x = out.tj * g.bn + out.cc * W, y = out.ti * 256 + (int)half * kRowsCta;
+    if (elect()) {
+      if (y < rows) {
+        if constexpr (MODE == LIN_FORWARD) {
+          if (e.pre) box_store(&maps.pre, at, x, y);
+          box_store(&maps.out, slot1, x, y);
+        } else {
+          if (e.dgate) box_store(&maps.extra, wide ? slot1 + kSlot / 2 : slot1, x, y);
+          box_store(&maps.out, at, x, y);
+        }
+      }
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+      asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+      bar_arrive(bfree + 8 * sb);
+    }
+    __syncwarp();
+    if (++sb == ring) {
+      sb = 0;
+      sph ^= 1;
+    }
+    next_chunk<W>(g, cols, split, tiles, step, out);
+  }
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
 // The same for rows off 16-byte boundaries: a lane takes one column and its 32
 // rows, so that a warp's accesses of a row are consecutive whatever its
 // alignment.
@@ -909,7 +1015,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
   constexpr int kEpiWarps = BOX ? kBoxWarps : kPatchWarps;
   constexpr int kPiece = BOX ? 16 : 32, kSets = kEpiWarps / 4;
   extern __shared__ __align__(1024) unsigned char smem[];
-  __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 5 + 2 * kMostBoxes];
+  __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 5 + (FP4 ? 3 : 2) * kMostBoxes];
   __shared__ __align__(8) uint64_t raw_bars[GEN ? 2 * kMostRaw : 1];
   __shared__ uint32_t tmem_at;
   __shared__ int dead;
@@ -926,6 +1032,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
   const uint32_t full = smem_u32(bars), empty = full + 8 * kMaxStages;
   const uint32_t tfull = empty + 8 * kMaxStages, tempty = tfull + 16, ready = tempty + 16;
   const uint32_t efull = ready + 8, edone = efull + 8 * kMostBoxes;
+  const uint32_t bfree = edone + 8 * kMostBoxes;  // OF_FP4
   const uint32_t landed = smem_u32(raw_bars), used = landed + 8 * kMostRaw;  // raw buffers
 
   if (warp == 0 && elect()) {
@@ -948,6 +1055,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
       for (int b = 0; b < g.boxes; ++b) {
         bar_init(efull + 8 * b, 1);
         bar_init(edone + 8 * b, kEpiWarps);
+        if (FP4) bar_init(bfree + 8 * b, 1);
       }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -1163,13 +1271,22 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
       }
     }
     __syncwarp();
-  } else if (BOX && warp == 3) {
+  } else if (BOX && (warp == 3 || (FP4 && warp == 2))) {
     for (; S > 1 && barriers < 2; ++barriers) {  // its boxes come after the exchange
       cluster_arrive();
       cluster_wait();
     }
-    if constexpr (BOX) box_traffic<MODE, FORM>(maps, k, g, patches, efull, edone, first, tiles, clusters, half,
-                            split, &dead);
+    if constexpr (BOX && FP4) {
+      if (warp == 2)
+        box_bring<MODE, FORM>(maps, k, g, patches, efull, bfree, first, tiles, clusters, half,
+                              split, &dead);
+      else
+        box_put<MODE, FORM>(maps, k, g, patches, edone, bfree, first, tiles, clusters, half, split,
+                            &dead);
+    } else if constexpr (BOX) {
+      box_traffic<MODE, FORM>(maps, k, g, patches, efull, edone, first, tiles, clusters, half,
+                              split, &dead);
+    }
     __syncwarp();
   } else if (warp >= kEpiWarp0 && warp < kEpiWarp0 + kEpiWarps) {
     const int w = (warp - kEpiWarp0) & 3, set = (warp - kEpiWarp0) >> 2;  // lanes 32 w...
