@@ -3,6 +3,7 @@
 // cores' block-scaled instructions (the kernel of zero_product.cuh).
 #include "zero_fp4.cuh"
 #include "zero_product.cuh"
+#include "zero_walk.cuh"
 
 namespace zk {
 
@@ -48,72 +49,6 @@ __device__ __forceinline__ uint32_t block_scale(uint32_t top, const Whole& w, fl
   return byte;
 }
 
-// Eight columns of rows some distance apart, as they lie in memory: one or two
-// 16-byte accesses where the matrix and the columns allow it, decided once.
-template <bool WIDE>
-struct Down {
-  const Mat& m;
-  char* p;
-  int64_t step, row, col, rows_apart;
-  int valid;
-  bool fast;
-  __device__ __forceinline__ Down(const Mat& mat, int64_t row0, int64_t apart, int64_t column,
-                                  int count)
-      : m(mat), row(row0), col(column), rows_apart(apart), valid(count) {
-    constexpr int es = WIDE ? 4 : 2;
-    p = static_cast<char*>(m.p) + (row0 * m.ld + column) * es;
-    step = apart * m.ld * es;
-    fast = m.vec && count == 8;
-  }
-  // N rows, zeros from row `rows` on.  One test for all: conditions between the
-  // loads would keep them from being in flight together (maxima of 8192 x 4096
-  // bf16: 31 us so, __MAX__ with one).
-  template <int N>
-  __device__ __forceinline__ void get(Raw8 r[N], int64_t rows, const Extent& e) const {
-    if (fast && in_extent(row, row + 1, 0, e.rows, ZERO_SITE_FP4) &&
-        in_extent(col, col + 8, 0, e.cols, ZERO_SITE_FP4)) {
-      const char* at = p;
-      int64_t here = row;
-#pragma unroll
-      for (int i = 0; i < N; ++i) {  // past the last row the one before again
-        r[i].a = ld16(at);
-        r[i].b = WIDE ? ld16(at + 16) : make_uint4(0, 0, 0, 0);
-        here += rows_apart;
-        at += here < rows ? step : 0;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        r[i].a = r[i].b = make_uint4(0, 0, 0, 0);
-        if (row + i * rows_apart < rows && valid > 0)
-          r[i] = raw8(m, row + i * rows_apart, col, valid, e, ZERO_SITE_FP4);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (row + i * rows_apart >= rows) r[i].a = r[i].b = make_uint4(0, 0, 0, 0);
-  }
-  __device__ __forceinline__ void put(int i, const float v[8], const Extent& e) const {
-    const int64_t at = row + i * rows_apart;
-    if (fast && in_extent(at, at + 1, 0, e.rows, ZERO_SITE_FP4) &&
-        in_extent(col, col + 8, 0, e.cols, ZERO_SITE_FP4)) {
-      if (WIDE) {
-        float4* to = reinterpret_cast<float4*>(p + i * step);
-        to[0] = make_float4(v[0], v[1], v[2], v[3]);
-        to[1] = make_float4(v[4], v[5], v[6], v[7]);
-      } else {
-        *reinterpret_cast<uint4*>(p + i * step) = pack8(v);
-      }
-      return;
-    }
-    store8(m, at, col, valid, v, e, ZERO_SITE_FP4);
-  }
-  __device__ __forceinline__ void on(int steps) {
-    p += steps * step;
-    row += steps * rows_apart;
-  }
-};
-
 // Codes of eight values of a block whose factor is known.
 __device__ __forceinline__ uint32_t codes8(const float v[8], float factor) {
   float s[8];
@@ -123,49 +58,13 @@ __device__ __forceinline__ uint32_t codes8(const float v[8], float factor) {
 }
 
 // ----------------------------------------------------------------- quantise --
-// A block of 256 threads takes 128 x 128 values into shared memory: their codes
-// and scales are whole scale tiles in both directions, so that every byte of
-// those (padding included) has one writer.  Then a thread takes one block of a
-// row after another, and in the other direction the blocks of two columns side
-// by side (bf16: one 32-bit word); largest magnitudes of bf16 are found two at
-// a time, fp32's as integers, which order NaN and infinity above all numbers.
-// Codes go out through shared memory, 64 bytes of each line.
-constexpr int kQuantTile = 128, kQuantThreads = 256, kCodeLine = 80;
-
-template <bool WIDE>
-struct QuantShared {
-  static constexpr int kElem = WIDE ? 4 : 2, kLine = kQuantTile * kElem + 16;
-  unsigned char tile[kQuantTile * kLine];
-  unsigned char codes[kQuantTile * kCodeLine];  // of one direction, 64 bytes a line
-  unsigned char scales[2][1024];                // rows', columns'
-};
-
-__device__ __forceinline__ int scale_at(int line, int block) {  // in a 128-line tile's scales
-  return (block >> 2) * kScaleTile + (line & 31) * 16 + (line >> 5) * 4 + (block & 3);
-}
-
-// One direction's codes and scale tiles to memory.  line0: its first line;
-// byte0: of the lines' codes; tiles (line0 / 128, tile0 + t), t < tiles.
-__device__ __forceinline__ void store_quantized(const Fp4Mat& o, const unsigned char* codes,
-                                                const unsigned char* scales, int64_t line0,
-                                                int64_t lines, int64_t byte0, int64_t tile0,
-                                                int tiles) {
-#pragma unroll
-  for (int p = 0; p < kQuantTile * 4 / kQuantThreads; ++p) {
-    const int u = p * kQuantThreads + threadIdx.x, c = u >> 2;
-    const int64_t line = line0 + c, byte = byte0 + (u & 3) * 16, at = line * o.ld + byte;
-    if (line < lines && byte < o.line_bytes &&
-        in_extent(at, at + 16, line * o.ld, line * o.ld + o.line_bytes, ZERO_SITE_FP4))
-      *reinterpret_cast<uint4*>(o.codes + at) =
-          *reinterpret_cast<const uint4*>(codes + c * kCodeLine + (u & 3) * 16);
-  }
-  const int unit = threadIdx.x;  // 16 bytes
-  const int64_t t = tile0 + unit / 32;
-  if (unit >= tiles * 32 || t >= o.scale_tiles) return;
-  const int64_t at = (line0 / kQuantTile * o.scale_tiles + t) * kScaleTile + unit % 32 * 16;
-  if (!in_extent(at, at + 16, 0, o.scale_bytes, ZERO_SITE_FP4)) return;
-  *reinterpret_cast<uint4*>(o.scales + at) = *reinterpret_cast<const uint4*>(scales + unit * 16);
-}
+// Along the rows and along the columns by a kernel each: joined in one, through
+// shared memory both ways, 8192 x 4096 bf16 took 30 us, and the second reads
+// from L2 what the first read from memory.  A block of 256 threads takes whole
+// scale tiles, or halves of them that no other block has, so that every byte of
+// codes and scales, padding included, has one writer.  Bound by instructions:
+// about 9 and 8 a value.
+constexpr int kQuantRows = 128, kQuantThreads = 256;
 
 __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return a > b ? a : b; }
 // The larger magnitude of two bf16 in each half; NaN where there is one.
@@ -173,94 +72,133 @@ __device__ __forceinline__ uint32_t larger2(uint32_t top, uint32_t w) {
   asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(top) : "r"(w & 0x7FFF7FFFu));
   return top;
 }
+__device__ __forceinline__ int scale_at(int line, int block) {  // in a tile of 128 lines
+  return (line & 31) * 16 + (line >> 5) * 4 + block;
+}
 
+// Along the rows: 128 rows by the columns of one scale tile, a thread having 16
+// columns of every 64th (NV) or 32nd row: a block, or half of one.
 template <bool NV, bool WIDE>
-__global__ void __launch_bounds__(kQuantThreads, WIDE ? 2 : 4)
-    quantize_kernel(const __grid_constant__ QuantK k) {
-  extern __shared__ __align__(16) unsigned char quant_smem[];
-  using Shared = QuantShared<WIDE>;
-  Shared& sh = *reinterpret_cast<Shared*>(quant_smem);
-  constexpr int kSize = NV ? 16 : 32, kTiles = NV ? 2 : 1, kBlocks = kQuantTile / kSize;
+__global__ void __launch_bounds__(kQuantThreads)
+    quantize_rows_kernel(const __grid_constant__ QuantK k) {
+  __shared__ __align__(16) unsigned char scales[kScaleTile];
+  constexpr int kSize = NV ? 16 : 32, kAcross = kSize / 4, kDown = kQuantThreads / kAcross;
+  constexpr int kAhead = 2;
   after_previous_kernel();
   const Whole whole = whole_of<NV>(k.g);
-  const int64_t row0 = (int64_t)(blockIdx.x / k.tiles_j) * kQuantTile;
-  const int64_t col0 = (int64_t)(blockIdx.x % k.tiles_j) * kQuantTile;
-  const int t = threadIdx.x;
+  const int64_t line_tile = blockIdx.x / k.tiles, tile = blockIdx.x % k.tiles;
+  const int64_t row0 = line_tile * kQuantRows;
+  const int unit = threadIdx.x % kAcross, line = threadIdx.x / kAcross;
+  const int64_t col = tile * (4 * kSize) + unit * 16;
+  const Extent e{k.rows, k.cols};
+  auto valid = [&](int64_t c) {
+    return c >= k.cols ? 0 : k.cols - c < 8 ? (int)(k.cols - c) : 8;
+  };
+  const bool kept = col / 2 < k.q.line_bytes;
+#pragma unroll
+  for (int p0 = 0; p0 < kQuantRows / kDown; p0 += kAhead) {
+    Raw8 raw[2][kAhead];
+    const int64_t first = row0 + p0 * kDown + line;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (first < k.rows) {
+        Down<WIDE, ZERO_SITE_FP4>(k.x, first, kDown, col + 8 * h, valid(col + 8 * h))
+            .template get<kAhead>(raw[h], k.rows, e);
+      } else {
+#pragma unroll
+        for (int p = 0; p < kAhead; ++p) raw[h][p].a = raw[h][p].b = make_uint4(0, 0, 0, 0);
+      }
+    }
+    unsigned char* to = k.q.codes + first * k.q.ld + col / 2;
+#pragma unroll
+    for (int p = 0; p < kAhead; ++p) {
+      const int64_t row = first + p * kDown;
+      uint32_t top = 0;
+      float v[16];
+      values8<WIDE>(raw[0][p], v);
+      values8<WIDE>(raw[1][p], v + 8);
+      if (WIDE) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) top = larger(top, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+      } else {
+        uint32_t two = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          two = larger2(larger2(larger2(larger2(two, raw[h][p].a.x), raw[h][p].a.y),
+                                raw[h][p].a.z),
+                        raw[h][p].a.w);
+        top = larger(two << 16, two & 0xFFFF0000u);
+      }
+      if (!NV) top = larger(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      float factor;
+      const uint32_t byte = block_scale<NV>(top, whole, factor);
+      uint2 codes = make_uint2(codes8(v, factor), codes8(v + 8, factor));
+      if (top >= kInfBits) codes = make_uint2(0u, 0u);
+      if (row < k.rows && kept && in_extent(row, row + 1, 0, k.rows, ZERO_SITE_FP4) &&
+          in_extent(col / 2, col / 2 + 8, 0, k.q.line_bytes, ZERO_SITE_FP4))
+        *reinterpret_cast<uint2*>(to + p * kDown * k.q.ld) = codes;
+      if (NV || unit % 2 == 0)
+        scales[scale_at(p0 * kDown + p * kDown + line, NV ? unit : unit / 2)] =
+            (unsigned char)byte;
+    }
+  }
+  __syncthreads();
+  const int64_t at = (line_tile * k.q.scale_tiles + tile) * kScaleTile + threadIdx.x * 16;
+  if (threadIdx.x < kScaleTile / 16 && in_extent(at, at + 16, 0, k.q.scale_bytes, ZERO_SITE_FP4))
+    *reinterpret_cast<uint4*>(k.q.scales + at) =
+        *reinterpret_cast<const uint4*>(scales + threadIdx.x * 16);
+}
+
+// Along the columns: 128 rows by 64 columns cross shared memory.  A thread has
+// a block of one column, or (bf16, NV) of two side by side, one 32-bit word of
+// each row.  Codes go out through shared memory, 64 bytes of each line; of a
+// scale tile's 16-byte rows the 64 columns fill half.
+constexpr int kQuantCols = 64, kCodeLine = 80;
+
+template <bool NV, bool WIDE>
+__global__ void __launch_bounds__(kQuantThreads)
+    quantize_cols_kernel(const __grid_constant__ QuantK k) {
+  constexpr int kElem = WIDE ? 4 : 2, kLine = kQuantCols * kElem + 16;
+  constexpr int kSize = NV ? 16 : 32, kBlocks = kQuantRows / kSize, kTiles = NV ? 2 : 1;
+  constexpr int kSide = NV && !WIDE ? 2 : 1;  // columns of a thread
+  __shared__ __align__(16) unsigned char tile[kQuantRows * kLine];
+  __shared__ __align__(16) unsigned char codes[kQuantCols * kCodeLine];
+  __shared__ __align__(16) unsigned char scales[kTiles][32 * 8];
+  after_previous_kernel();
+  const Whole whole = whole_of<NV>(k.g);
+  const int64_t row_tile = blockIdx.x / k.tiles, col0 = blockIdx.x % k.tiles * kQuantCols;
+  const int64_t row0 = row_tile * kQuantRows;
+  const Extent e{k.rows, k.cols};
   {
-    const int line = t >> 4, unit = t & 15;
-    const Extent e{k.rows, k.cols};
+    constexpr int kAcross = kQuantCols / 8, kDown = kQuantThreads / kAcross;  // 4 rows a thread
+    const int unit = threadIdx.x % kAcross, line = threadIdx.x / kAcross;
     const int64_t col = col0 + unit * 8;
     const int valid = col >= k.cols ? 0 : k.cols - col < 8 ? (int)(k.cols - col) : 8;
-    Raw8 raw[8];
+    Raw8 raw[kQuantRows / kDown];
 #pragma unroll
-    for (int p = 0; p < 8; ++p) raw[p].a = raw[p].b = make_uint4(0, 0, 0, 0);
+    for (int p = 0; p < kQuantRows / kDown; ++p) raw[p].a = raw[p].b = make_uint4(0, 0, 0, 0);
     if (row0 + line < k.rows)
-      Down<WIDE>(k.x, row0 + line, 16, col, valid).template get<8>(raw, k.rows, e);
+      Down<WIDE, ZERO_SITE_FP4>(k.x, row0 + line, kDown, col, valid)
+          .template get<kQuantRows / kDown>(raw, k.rows, e);
 #pragma unroll
-    for (int p = 0; p < 8; ++p) {
-      uint4* at = reinterpret_cast<uint4*>(sh.tile + (p * 16 + line) * Shared::kLine +
-                                           unit * 8 * Shared::kElem);
+    for (int p = 0; p < kQuantRows / kDown; ++p) {
+      uint4* at =
+          reinterpret_cast<uint4*>(tile + (p * kDown + line) * kLine + unit * 8 * kElem);
       at[0] = raw[p].a;
       if (WIDE) at[1] = raw[p].b;
     }
   }
   __syncthreads();
-  const bool rows = k.q.codes != nullptr, columns = k.qt.codes != nullptr;
-  if (rows) {
-    for (int u = t; u < kQuantTile * kBlocks; u += kQuantThreads) {
-      const int r = u % kQuantTile, b = u / kQuantTile;
-      const unsigned char* at = sh.tile + r * Shared::kLine + b * kSize * Shared::kElem;
-      constexpr int kWords = kSize * Shared::kElem / 16;
-      uint4 raw[kWords];
-#pragma unroll
-      for (int i = 0; i < kWords; ++i) raw[i] = reinterpret_cast<const uint4*>(at)[i];
-      uint32_t top = 0;
-      if (WIDE) {
-#pragma unroll
-        for (int i = 0; i < kWords; ++i)
-          top = larger(larger(top, larger(raw[i].x & 0x7FFFFFFFu, raw[i].y & 0x7FFFFFFFu)),
-                       larger(raw[i].z & 0x7FFFFFFFu, raw[i].w & 0x7FFFFFFFu));
-      } else {
-        uint32_t two = 0;
-#pragma unroll
-        for (int i = 0; i < kWords; ++i)
-          two = larger2(larger2(larger2(larger2(two, raw[i].x), raw[i].y), raw[i].z), raw[i].w);
-        top = larger(two << 16, two & 0xFFFF0000u);
-      }
-      float factor;
-      sh.scales[0][scale_at(r, b)] = (unsigned char)block_scale<NV>(top, whole, factor);
-      uint32_t* out = reinterpret_cast<uint32_t*>(sh.codes + r * kCodeLine + b * (kSize / 2));
-#pragma unroll
-      for (int i = 0; i < kSize / 8; ++i) {
-        float v[8];
-        if (WIDE) {
-          const uint4 x = raw[(2 * i) % kWords], y = raw[(2 * i + 1) % kWords];
-          v[0] = __uint_as_float(x.x); v[1] = __uint_as_float(x.y);
-          v[2] = __uint_as_float(x.z); v[3] = __uint_as_float(x.w);
-          v[4] = __uint_as_float(y.x); v[5] = __uint_as_float(y.y);
-          v[6] = __uint_as_float(y.z); v[7] = __uint_as_float(y.w);
-        } else {
-          from_bf16(raw[i % kWords], v);
-        }
-        out[i] = top >= kInfBits ? 0u : codes8(v, factor);
-      }
-    }
-    __syncthreads();
-    store_quantized(k.q, sh.codes, sh.scales[0], row0, k.rows, col0 / 2, col0 / (4 * kSize),
-                    kTiles);
-  }
-  if (!columns) return;
-  if (rows) __syncthreads();  // the codes are read
-  constexpr int kSide = WIDE ? 1 : 2;  // columns of a thread
-  for (int u = t; u < kQuantTile / kSide * kBlocks; u += kQuantThreads) {
-    const int c = u % (kQuantTile / kSide) * kSide, b = u / (kQuantTile / kSide);
-    const unsigned char* at = sh.tile + b * kSize * Shared::kLine + c * Shared::kElem;
-    uint32_t raw[kSize], top[kSide];
+#pragma unroll 1
+  for (int u = threadIdx.x; u < kQuantCols / kSide * kBlocks; u += kQuantThreads) {
+    const int c = u % (kQuantCols / kSide) * kSide, b = u / (kQuantCols / kSide);
+    const unsigned char* at = tile + b * kSize * kLine + c * kElem;
+    uint32_t raw[kSize], top[2] = {0, 0};
 #pragma unroll
     for (int i = 0; i < kSize; ++i)
-      raw[i] = *reinterpret_cast<const uint32_t*>(at + i * Shared::kLine);
+      raw[i] = WIDE || kSide == 2 ? *reinterpret_cast<const uint32_t*>(at + i * kLine)
+                                  : *reinterpret_cast<const uint16_t*>(at + i * kLine);
     if (WIDE) {
-      top[0] = 0;
 #pragma unroll
       for (int i = 0; i < kSize; ++i) top[0] = larger(top[0], raw[i] & 0x7FFFFFFFu);
     } else {
@@ -268,15 +206,14 @@ __global__ void __launch_bounds__(kQuantThreads, WIDE ? 2 : 4)
 #pragma unroll
       for (int i = 0; i < kSize; ++i) two = larger2(two, raw[i]);
       top[0] = two << 16;
-      top[kSide - 1] = two & 0xFFFF0000u;
+      top[1] = two & 0xFFFF0000u;
     }
 #pragma unroll
     for (int h = 0; h < kSide; ++h) {
       float factor;
-      const uint32_t most = !WIDE && h == 0 ? top[0] : top[kSide - 1];
-      sh.scales[1][scale_at(c + h, b)] = (unsigned char)block_scale<NV>(most, whole, factor);
-      uint32_t* out =
-          reinterpret_cast<uint32_t*>(sh.codes + (c + h) * kCodeLine + b * (kSize / 2));
+      const uint32_t byte = block_scale<NV>(top[h], whole, factor);
+      scales[b >> 2][((c + h) & 31) * 8 + ((c + h) >> 5) * 4 + (b & 3)] = (unsigned char)byte;
+      uint32_t* out = reinterpret_cast<uint32_t*>(codes + (c + h) * kCodeLine + b * (kSize / 2));
 #pragma unroll
       for (int i = 0; i < kSize / 8; ++i) {
         float v[8];
@@ -285,64 +222,53 @@ __global__ void __launch_bounds__(kQuantThreads, WIDE ? 2 : 4)
           const uint32_t w = raw[8 * i + j];
           v[j] = WIDE ? __uint_as_float(w) : h ? bf16_hi(w) : bf16_lo(w);
         }
-        out[i] = most >= kInfBits ? 0u : codes8(v, factor);
+        out[i] = top[h] >= kInfBits ? 0u : codes8(v, factor);
       }
     }
   }
   __syncthreads();
-  store_quantized(k.qt, sh.codes, sh.scales[1], col0, k.cols, row0 / 2, row0 / (4 * kSize), kTiles);
+  {
+    const int c = threadIdx.x >> 2;
+    const int64_t line = col0 + c, byte = row0 / 2 + (threadIdx.x & 3) * 16;
+    if (line < k.cols && byte < k.qt.line_bytes &&
+        in_extent(line, line + 1, 0, k.cols, ZERO_SITE_FP4) &&
+        in_extent(byte, byte + 16, 0, k.qt.line_bytes, ZERO_SITE_FP4))
+      *reinterpret_cast<uint4*>(k.qt.codes + line * k.qt.ld + byte) =
+          *reinterpret_cast<const uint4*>(codes + c * kCodeLine + (threadIdx.x & 3) * 16);
+  }
+  const int64_t t = row_tile * kTiles + threadIdx.x / 32;
+  const int64_t at = (col0 / 128 * k.qt.scale_tiles + t) * kScaleTile + threadIdx.x % 32 * 16 +
+                     col0 % 128 / 8;
+  if (threadIdx.x < kTiles * 32 && t < k.qt.scale_tiles &&
+      in_extent(at, at + 8, 0, k.qt.scale_bytes, ZERO_SITE_FP4))
+    *reinterpret_cast<uint2*>(k.qt.scales + at) =
+        *reinterpret_cast<const uint2*>(scales[threadIdx.x / 32] + threadIdx.x % 32 * 8);
 }
 
 template <bool NV, bool WIDE>
-static cudaError_t launch_quantize_as(const QuantK& k, int64_t blocks, cudaStream_t st) {
-  static std::atomic<unsigned long long> done{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const unsigned long long bit = 1ull << (dev & 63);
-  constexpr int bytes = (int)sizeof(QuantShared<WIDE>);
-  if (!(done.load() & bit)) {
-    e = cudaFuncSetAttribute(quantize_kernel<NV, WIDE>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+static cudaError_t launch_quantize_as(QuantK k, cudaStream_t st) {
+  const int64_t row_tiles = (k.rows + kQuantRows - 1) / kQuantRows;
+  if (k.q.codes) {
+    k.tiles = k.q.scale_tiles;
+    if (row_tiles * k.tiles >= (1ll << 31)) return cudaErrorInvalidValue;
+    const cudaError_t e = launch_next(quantize_rows_kernel<NV, WIDE>,
+                                      dim3((unsigned)(row_tiles * k.tiles)), dim3(kQuantThreads),
+                                      st, k);
     if (e != cudaSuccess) return e;
-    done.fetch_or(bit);
   }
-  return launch_next_with(bytes, quantize_kernel<NV, WIDE>, dim3((unsigned)blocks),
-                          dim3(kQuantThreads), st, k);
+  if (!k.qt.codes) return cudaSuccess;
+  k.tiles = (k.cols + 127) / 128 * 2;  // the last half too: its scales are padding
+  if (row_tiles * k.tiles >= (1ll << 31)) return cudaErrorInvalidValue;
+  return launch_next(quantize_cols_kernel<NV, WIDE>, dim3((unsigned)(row_tiles * k.tiles)),
+                     dim3(kQuantThreads), st, k);
 }
 
-cudaError_t launch_quantize(const QuantK& in, cudaStream_t st) {
-  QuantK k = in;
-  k.tiles_j = (k.cols + kQuantTile - 1) / kQuantTile;
-  const int64_t blocks = (k.rows + kQuantTile - 1) / kQuantTile * k.tiles_j;
-  if (blocks == 0) return cudaSuccess;
-  if (blocks >= (1ll << 31)) return cudaErrorInvalidValue;
+cudaError_t launch_quantize(const QuantK& k, cudaStream_t st) {
+  if (k.rows == 0 || k.cols == 0) return cudaSuccess;
   const bool wide = k.x.dtype == ZERO_F32;
-  if (k.nv) return wide ? launch_quantize_as<true, true>(k, blocks, st)
-                        : launch_quantize_as<true, false>(k, blocks, st);
-  return wide ? launch_quantize_as<false, true>(k, blocks, st)
-              : launch_quantize_as<false, false>(k, blocks, st);
-}
-
-// ------------------------------------------------------- walks over a matrix --
-// Units of 8 columns: a block of 256 threads covers `across` units (a power of
-// two, up to 32) of 256 / across rows, and goes on down the rows: no division.
-struct Walk {
-  int log2_across;
-  dim3 grid;
-};
-static Walk walk_over(int64_t rows, int64_t cols) {
-  const int64_t units = (cols + 7) / 8;
-  Walk w;
-  w.log2_across = 0;
-  while (w.log2_across < 5 && (1ll << w.log2_across) < units) ++w.log2_across;
-  const int64_t x = (units + (1 << w.log2_across) - 1) >> w.log2_across;
-  const int64_t each = kThreads >> w.log2_across;
-  int64_t y = (rows + each - 1) / each, most = (int64_t)sm_count() * 8 / (x < 1 ? 1 : x) + 1;
-  if (most > 65535) most = 65535;
-  if (y > most) y = most;
-  w.grid = dim3((unsigned)x, (unsigned)y);
-  return w;
+  if (k.nv) return wide ? launch_quantize_as<true, true>(k, st)
+                        : launch_quantize_as<true, false>(k, st);
+  return wide ? launch_quantize_as<false, true>(k, st) : launch_quantize_as<false, false>(k, st);
 }
 
 // --------------------------------------------------------------- dequantise --
@@ -360,7 +286,7 @@ __global__ void __launch_bounds__(kThreads)
   const int64_t block = col / (NV ? 16 : 32), per_tile = k.q.scale_tiles * kScaleTile;
   const unsigned char* scales = k.q.scales + block / 4 * kScaleTile + block % 4;
   const int64_t step = (int64_t)gridDim.y * down;
-  Down<WIDE> y(k.y, (int64_t)blockIdx.y * down + (threadIdx.x >> log2_across), step, col, valid);
+  Down<WIDE, ZERO_SITE_FP4> y(k.y, (int64_t)blockIdx.y * down + (threadIdx.x >> log2_across), step, col, valid);
   const unsigned char* from = k.q.codes + y.row * k.q.ld + col / 2;
   const int64_t down_bytes = step * k.q.ld;
   for (; y.row < k.rows; y.on(4), from += 4 * down_bytes) {
@@ -396,7 +322,7 @@ __global__ void __launch_bounds__(kThreads)
 
 template <bool NV>
 static cudaError_t launch_dequantize_as(const DequantK& k, cudaStream_t st) {
-  const Walk w = walk_over(k.rows, k.cols);
+  const Walk w = walk_over(k.rows, k.cols, (int64_t)sm_count() * 8);
   return k.y.dtype == ZERO_F32
              ? launch_next(dequantize_kernel<NV, true>, w.grid, dim3(kThreads), st, k,
                            w.log2_across)
@@ -456,7 +382,7 @@ __global__ void __launch_bounds__(kThreads)
     for (int64_t col = ((int64_t)blockIdx.x * across + (threadIdx.x & (across - 1))) * 8;
          col < k.cols; col += (int64_t)gridDim.x * across * 8) {
       const int valid = k.cols - col < 8 ? (int)(k.cols - col) : 8;
-      Down<WIDE> x(k.x, (int64_t)blockIdx.y * down + (threadIdx.x >> log2_across), step, col,
+      Down<WIDE, ZERO_SITE_FP4> x(k.x, (int64_t)blockIdx.y * down + (threadIdx.x >> log2_across), step, col,
                    valid);
       for (; x.row < k.rows; x.on(kAhead)) {
         Raw8 raw[kAhead];
@@ -483,7 +409,7 @@ __global__ void __launch_bounds__(kMaxima) maximum_kernel(const float* maxima, i
 cudaError_t launch_tensor_scale(const MaxK& k, float* g, cudaStream_t st) {
   int n = 0;
   if (k.rows > 0 && k.cols > 0) {
-    Walk w = walk_over(k.rows, k.cols);
+    Walk w = walk_over(k.rows, k.cols, (int64_t)sm_count() * 8);
     if (w.grid.x > kMaxima) w.grid.x = kMaxima;
     if (w.grid.x * w.grid.y > kMaxima) w.grid.y = kMaxima / w.grid.x;
     n = (int)(w.grid.x * w.grid.y);

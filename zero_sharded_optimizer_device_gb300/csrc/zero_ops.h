@@ -109,7 +109,7 @@ struct Fp4Mat {
 };
 struct QuantK {
   Mat x;
-  int64_t rows = 0, cols = 0, tiles_j = 0;
+  int64_t rows = 0, cols = 0, tiles = 0;
   Fp4Mat q, qt;  // codes nullptr: direction not asked for
   const float* g = nullptr;
   int nv = 0;
