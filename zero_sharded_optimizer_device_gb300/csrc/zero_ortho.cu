@@ -16,6 +16,7 @@
 // spectrum); with operands alone in fp16, 1.3e-3 on random matrices and 4e-2
 // at rank 16; in bf16 1e-2 and 0.3.
 #include "zero_tile.cuh"
+#include "zero_walk.cuh"
 
 #include <cuda_fp16.h>
 
@@ -675,40 +676,64 @@ struct Squares {
   }
 };
 
+// The eight columns of this thread, the row it begins with, and from that row
+// to its next.
+struct OrthoAt {
+  int64_t col, row, step;
+};
+__device__ __forceinline__ OrthoAt ortho_at(int log2_across) {
+  const int across = 1 << log2_across, down = kThreads >> log2_across;
+  OrthoAt a;
+  a.col = ((int64_t)blockIdx.x * across + (threadIdx.x & (across - 1))) * 8;
+  a.row = (int64_t)blockIdx.y * down + (threadIdx.x >> log2_across);
+  a.step = (int64_t)gridDim.y * down;
+  return a;
+}
+__device__ __forceinline__ int valid8(int64_t col, int64_t cols) {
+  return col >= cols ? 0 : cols - col < 8 ? (int)(cols - col) : 8;
+}
+constexpr int kOrthoAhead = 2;  // rows whose loads are in flight together
+
 // One block's share of a matrix: its new momentum (muon), and its squares.
-__global__ void __launch_bounds__(kThreads) ortho_squares(const __grid_constant__ OrthoSource s) {
+template <bool WIDE, bool MUON>
+__global__ void __launch_bounds__(kThreads)
+    ortho_squares(const __grid_constant__ OrthoSource s, int log2_across) {
   after_previous_kernel();
-  const int b = blockIdx.y;
+  const int b = blockIdx.z;
   const Extent e{s.m, s.n};
-  const int64_t units = (s.n + 7) / 8, total = units * s.m;
+  const OrthoAt at = ortho_at(log2_across);
+  const int valid = valid8(at.col, s.n);
   Squares q;
-  const Mat x = source_mat(s.places, s.x, b);
-  Mat mom;
-  float coef = 1.0f;
-  if (s.muon) {
-    mom = source_mat(s.places, s.momentum, b);
-    if (s.coef) coef = *(volatile const float*)s.coef;
-  }
-  for (int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x; u < total;
-       u += (int64_t)gridDim.x * kThreads) {
-    const int64_t row = u / units, col = u % units * 8;
-    const int valid = s.n - col < 8 ? (int)(s.n - col) : 8;
-    float v[8];
-    load8(x, row, col, valid, v, e, ZERO_SITE_ORTHO);
-    if (s.muon) {
-      float m[8];
-      load8(mom, row, col, valid, m, e, ZERO_SITE_ORTHO);
+  const Mat xm = source_mat(s.places, s.x, b);
+  const Mat mm = MUON ? source_mat(s.places, s.momentum, b) : xm;
+  const float coef = MUON && s.coef ? *(volatile const float*)s.coef : 1.0f;
+  if (valid > 0) {
+    Down<WIDE, ZERO_SITE_ORTHO> x(xm, at.row, at.step, at.col, valid);
+    Down<WIDE, ZERO_SITE_ORTHO> mom(mm, at.row, at.step, at.col, valid);
+    for (; x.row < s.m; x.on(kOrthoAhead), mom.on(kOrthoAhead)) {
+      Raw8 rx[kOrthoAhead], rm[kOrthoAhead];
+      x.template get<kOrthoAhead>(rx, s.m, e);
+      if (MUON) mom.template get<kOrthoAhead>(rm, s.m, e);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float g = muon_grad(s, v[j], coef);
-        m[j] = __fadd_rn(__fmul_rn(s.mu, m[j]), g);
-        v[j] = s.nesterov ? __fadd_rn(g, __fmul_rn(s.mu, m[j])) : m[j];
+      for (int i = 0; i < kOrthoAhead; ++i) {
+        if (x.row + i * at.step >= s.m) break;
+        float v[8];
+        values8<WIDE>(rx[i], v);
+        if (MUON) {
+          float m[8];
+          values8<WIDE>(rm[i], m);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float g = muon_grad(s, v[j], coef);
+            m[j] = __fadd_rn(__fmul_rn(s.mu, m[j]), g);
+            v[j] = s.nesterov ? __fadd_rn(g, __fmul_rn(s.mu, m[j])) : m[j];
+          }
+          mom.put(i, m, e);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) q.add(v[j]);  // (0 past the columns)
       }
-      store8(mom, row, col, valid, m, e, ZERO_SITE_ORTHO);
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < valid) q.add(v[j]);
   }
   __shared__ double part[3][kThreads / 32];
   double sum[3] = {q.mid, q.big, q.small};
@@ -722,25 +747,39 @@ __global__ void __launch_bounds__(kThreads) ortho_squares(const __grid_constant_
   if (threadIdx.x < 3) {
     double t = 0.0;
     for (int w = 0; w < kThreads / 32; ++w) t += part[threadIdx.x][w];
-    s.partials[((int64_t)b * gridDim.x + blockIdx.x) * 3 + threadIdx.x] = t;
+    const int64_t block = ((int64_t)b * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
+    s.partials[block * 3 + threadIdx.x] = t;
   }
 }
 
 // X0 = x / (|x| + eps) in two fp16 numbers, zeros around it.
-__global__ void __launch_bounds__(kThreads) ortho_scale(const __grid_constant__ OrthoSource s) {
+template <bool WIDE, bool MUON>
+__global__ void __launch_bounds__(kThreads)
+    ortho_scale(const __grid_constant__ OrthoSource s, int log2_across) {
+  __shared__ double part[3][kThreads / 32];
   __shared__ float factor_at;
   after_previous_kernel();
-  const int b = blockIdx.y;
-  if (blockIdx.x == 0 && threadIdx.x == 0) s.done[b] = 0;
-  if (threadIdx.x < 32) {
+  const int b = blockIdx.z;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) s.done[b] = 0;
+  {
     double sum[3] = {};
-    for (int i = threadIdx.x; i < s.blocks; i += 32)
-      for (int q = 0; q < 3; ++q) sum[q] += s.partials[((int64_t)b * s.blocks + i) * 3 + q];
+    const double* from = s.partials + (int64_t)b * s.blocks * 3;
+    for (int i = threadIdx.x; i < s.blocks; i += kThreads)
 #pragma unroll
-    for (int q = 0; q < 3; ++q)
+      for (int q = 0; q < 3; ++q) sum[q] += *(volatile const double*)(from + 3 * i + q);
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
 #pragma unroll
       for (int m = 16; m; m >>= 1) sum[q] += __shfl_xor_sync(0xffffffffu, sum[q], m);
+      if ((threadIdx.x & 31) == 0) part[q][threadIdx.x >> 5] = sum[q];
+    }
+    __syncthreads();
     if (threadIdx.x == 0) {
+#pragma unroll
+      for (int q = 0; q < 3; ++q) {
+        sum[q] = 0.0;
+        for (int w = 0; w < kThreads / 32; ++w) sum[q] += part[q][w];
+      }
       // (the plain sum holds unless it is this large or small; NaN stays)
       double square = sum[0];
       if (sum[0] > 1e30) square = sum[1] * 0x1p160;
@@ -755,66 +794,84 @@ __global__ void __launch_bounds__(kThreads) ortho_scale(const __grid_constant__ 
   __syncthreads();
   const float f = factor_at;
   const Extent e{s.m, s.n};
-  const Mat x = source_mat(s.places, s.x, b);
-  Mat mom;
-  float coef = 1.0f;
-  if (s.muon) {
-    mom = source_mat(s.places, s.momentum, b);
-    if (s.coef) coef = *(volatile const float*)s.coef;
-  }
-  const int64_t units = s.ld / 8, total = units * s.rows;
-  for (int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x; u < total;
-       u += (int64_t)gridDim.x * kThreads) {
-    const int64_t row = u / units, col = u % units * 8;
-    float v[8] = {};
-    if (row < s.m && col < s.n) {
-      const int valid = s.n - col < 8 ? (int)(s.n - col) : 8;
-      load8(x, row, col, valid, v, e, ZERO_SITE_ORTHO);
-      if (s.muon) {
+  const OrthoAt at = ortho_at(log2_across);
+  if (at.col >= s.ld) return;
+  const int valid = valid8(at.col, s.n);
+  const Mat xm = source_mat(s.places, s.x, b);
+  const Mat mm = MUON ? source_mat(s.places, s.momentum, b) : xm;
+  const float coef = MUON && s.coef ? *(volatile const float*)s.coef : 1.0f;
+  Down<WIDE, ZERO_SITE_ORTHO> x(xm, at.row, at.step, at.col, valid);
+  Down<WIDE, ZERO_SITE_ORTHO> mom(mm, at.row, at.step, at.col, valid);
+  for (; x.row < s.rows; x.on(kOrthoAhead), mom.on(kOrthoAhead)) {
+    Raw8 rx[kOrthoAhead], rm[kOrthoAhead];
+    x.template get<kOrthoAhead>(rx, s.m, e);  // zeros past the matrix
+    if (MUON) mom.template get<kOrthoAhead>(rm, s.m, e);
+#pragma unroll
+    for (int i = 0; i < kOrthoAhead; ++i) {
+      const int64_t row = x.row + i * at.step;
+      if (row >= s.rows) break;
+      float v[8];
+      values8<WIDE>(rx[i], v);
+      if (MUON) {
         float m[8];
-        load8(mom, row, col, valid, m, e, ZERO_SITE_ORTHO);
+        values8<WIDE>(rm[i], m);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           v[j] = s.nesterov ? __fadd_rn(muon_grad(s, v[j], coef), __fmul_rn(s.mu, m[j])) : m[j];
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = j < valid ? v[j] * f * f : 0.0f;
+      for (int j = 0; j < 8; ++j) v[j] = j < valid && row < s.m ? v[j] * f * f : 0.0f;
+      const int64_t to = ((int64_t)b * s.rows + row) * s.ld + at.col;
+      *reinterpret_cast<uint4*>(s.hi + to) = split_halves8(v);
+      *reinterpret_cast<uint4*>(s.lo + to) = to_halves8(v);
     }
-    const int64_t at = ((int64_t)b * s.rows + row) * s.ld + col;
-    *reinterpret_cast<uint4*>(s.hi + at) = split_halves8(v);
-    *reinterpret_cast<uint4*>(s.lo + at) = to_halves8(v);
   }
 }
 
 // y = X, or the update of the master weights by it.
-__global__ void __launch_bounds__(kThreads) ortho_finish(const __grid_constant__ OrthoFinish s) {
+template <bool UPDATE>
+__global__ void __launch_bounds__(kThreads)
+    ortho_finish(const __grid_constant__ OrthoFinish s, int log2_across) {
   after_previous_kernel();
-  const int b = blockIdx.y;
+  const int b = blockIdx.z;
   const Extent e{s.m, s.n};
-  const int64_t units = (e.cols + 7) / 8, total = units * e.rows;
-  const Mat y = source_mat(s.places, s.y, b);
-  Mat out;
-  if (s.update && s.out.p) out = source_mat(s.places, s.out, b);
-  for (int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x; u < total;
-       u += (int64_t)gridDim.x * kThreads) {
-    const int64_t row = u / units, col = u % units * 8;
-    const int valid = e.cols - col < 8 ? (int)(e.cols - col) : 8;
-    float v[8];
-    halves8(ld16(s.x + ((int64_t)b * s.rows + row) * s.ld + col), v);
-    if (s.update) {
-      float w[8];
-      load8(y, row, col, valid, w, e, ZERO_SITE_ORTHO);
+  const OrthoAt at = ortho_at(log2_across);
+  const int valid = valid8(at.col, s.n);
+  if (valid <= 0) return;
+  const Mat ym = source_mat(s.places, s.y, b);
+  Mat om;
+  if (UPDATE && s.out.p) om = source_mat(s.places, s.out, b);
+  Down<UPDATE, ZERO_SITE_ORTHO> y(ym, at.row, at.step, at.col, valid);  // fp32 or bf16
+  for (; y.row < s.m; y.on(kOrthoAhead)) {
+    Raw8 rw[kOrthoAhead];
+    uint4 rx[kOrthoAhead];
+    if (UPDATE) y.template get<kOrthoAhead>(rw, s.m, e);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (s.decay != 0.0f) w[j] = __fsub_rn(w[j], __fmul_rn(s.decay, w[j]));
-        v[j] = __fsub_rn(w[j], __fmul_rn(s.rate, v[j] * (1.0f / kScaleX)));
-      }
-      if (out.p) store8(out, row, col, valid, v, e, ZERO_SITE_ORTHO);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= 1.0f / kScaleX;
+    for (int i = 0; i < kOrthoAhead; ++i) {  // (rows of whole tiles: they exist)
+      const int64_t row = y.row + i * at.step < s.m ? y.row + i * at.step : y.row;
+      rx[i] = ld16(s.x + ((int64_t)b * s.rows + row) * s.ld + at.col);
     }
-    store8(y, row, col, valid, v, e, ZERO_SITE_ORTHO);
+#pragma unroll
+    for (int i = 0; i < kOrthoAhead; ++i) {
+      const int64_t row = y.row + i * at.step;
+      if (row >= s.m) break;
+      float v[8];
+      halves8(rx[i], v);
+      if (UPDATE) {
+        float w[8];
+        values8<true>(rw[i], w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (s.decay != 0.0f) w[j] = __fsub_rn(w[j], __fmul_rn(s.decay, w[j]));
+          v[j] = __fsub_rn(w[j], __fmul_rn(s.rate, v[j] * (1.0f / kScaleX)));
+        }
+        if (om.p) store8(om, row, at.col, valid, v, e, ZERO_SITE_ORTHO);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] *= 1.0f / kScaleX;
+      }
+      y.put(i, v, e);
+    }
   }
 }
 
@@ -829,17 +886,21 @@ bool ortho_fits(int64_t m, int64_t n, int64_t batch) {
          k / 256 * (k / 256 + 1) < (1ll << 25) / (batch + 1);
 }
 
+// Walks before and after the products: about eight blocks of 256 threads for
+// each of 152 SMs, from the sizes alone (the workspace has a place for each).
+static Walk ortho_walk(int64_t rows, int64_t cols, int64_t batch) {
+  return walk_over(rows, cols, 152 * 8 / (batch > 0 ? batch : 1));
+}
+
 OrthoSpace ortho_space(int64_t m, int64_t n, int64_t batch) {
   OrthoSpace w;
   const int64_t k = m < n ? m : n;
   w.rows = up(m, 256);
   w.ld = up(n, 64);
   w.side = up(k, 256);
-  // blocks of a matrix's norm: about four of 256 threads per SM for the batch
-  const int64_t units = (n + 7) / 8 * m, want = (int64_t)152 * 4 / (batch > 0 ? batch : 1);
-  w.blocks = (units + kThreads - 1) / kThreads;
-  if (w.blocks > want) w.blocks = want;
-  if (w.blocks < 1) w.blocks = 1;
+  // blocks of a matrix's norm
+  const Walk walk = ortho_walk(m, n, batch);
+  w.blocks = (int64_t)walk.grid.x * walk.grid.y;
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     const int64_t here = at;
@@ -937,13 +998,20 @@ cudaError_t launch_orthogonalize(const OrthoCall& c, cudaStream_t st) {
   s.partials = reinterpret_cast<double*>(base + w.partials);
   s.hi = reinterpret_cast<uint16_t*>(base + w.hi[0]);
   s.lo = reinterpret_cast<uint16_t*>(base + w.lo);
-  cudaError_t e = launch_next(ortho_squares, dim3((unsigned)w.blocks, (unsigned)batch),
-                              dim3(kThreads), st, s);
+  const bool wide = s.x.dtype == ZERO_F32;
+  auto grid = [&](const Walk& walk) {
+    return dim3(walk.grid.x, walk.grid.y, (unsigned)batch);
+  };
+  const Walk over = ortho_walk(m, n, batch), padded = ortho_walk(w.rows, w.ld, batch);
+  cudaError_t e = launch_next(s.muon ? ortho_squares<true, true>
+                              : wide ? ortho_squares<true, false>
+                                     : ortho_squares<false, false>,
+                              grid(over), dim3(kThreads), st, s, over.log2_across);
   if (e != cudaSuccess) return e;
-  const int64_t each = (w.rows * w.ld / 8 + kThreads - 1) / kThreads;
-  const int64_t share = (int64_t)sm_count() * 8 / batch + 1;
-  const dim3 grid((unsigned)(each < share ? each : share), (unsigned)batch);
-  e = launch_next(ortho_scale, grid, dim3(kThreads), st, s);
+  e = launch_next(s.muon ? ortho_scale<true, true>
+                  : wide ? ortho_scale<true, false>
+                         : ortho_scale<false, false>,
+                  grid(padded), dim3(kThreads), st, s, padded.log2_across);
   if (e != cudaSuccess) return e;
 
   if (c.steps > 0) {
@@ -1020,9 +1088,8 @@ cudaError_t launch_orthogonalize(const OrthoCall& c, cudaStream_t st) {
   f.rows = w.rows;
   f.ld = w.ld;
   f.x = reinterpret_cast<const uint16_t*>(base + w.hi[c.steps & 1]);
-  const int64_t units = ((n + 7) / 8 * m + kThreads - 1) / kThreads;
-  return launch_next(ortho_finish, dim3((unsigned)(units < share ? units : share), (unsigned)batch),
-                     dim3(kThreads), st, f);
+  return launch_next(f.update ? ortho_finish<true> : ortho_finish<false>, grid(over),
+                     dim3(kThreads), st, f, over.log2_across);
 }
 
 cudaError_t timeouts_ortho(unsigned long long* out, bool reset) {
