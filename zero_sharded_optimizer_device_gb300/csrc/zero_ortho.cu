@@ -36,10 +36,15 @@ constexpr int kSideBytes = 2 * kBoxChunks * kBox;
 // What the epilogue has to know of a tile: the task, and the diagonal of its
 // rows (128 of this CTA) and of its columns (256).
 constexpr int kNoteInts = 8, kNoteBytes = 2048;
+// Tasks on their way from the warp that looks them up to those that load,
+// multiply, bring and store.
+constexpr int kTaskSlots = 4, kTaskAt = 4 * kNoteInts + 3 * 512;
+static_assert(kTaskAt + kTaskSlots * 4 * kNoteInts <= kNoteBytes, "notes");
 constexpr int kStageBytes = kBytesA + 256 * kDeep;
 constexpr int kOrthoStages = (kSmemMost - 1024 - kSideBytes - kNoteBytes) / kStageBytes;
 constexpr int kEpi0 = 4, kEpis = 16;             // epilogue warps
-constexpr int kOrthoThreads = 32 * (kEpi0 + kEpis);
+constexpr int kTaskWarp = kEpi0 + kEpis;         // looks tasks up
+constexpr int kOrthoThreads = 32 * (kTaskWarp + 1);
 
 // ------------------------------------------------------------ the products --
 // One launch runs every product of every step.  A task is a tile of 256 x bn of
@@ -120,18 +125,18 @@ __device__ __forceinline__ OrthoTask ortho_task(const OrthoSteps& s, int t) {
   }
   return o;
 }
-__device__ __forceinline__ bool ortho_met(const OrthoSteps& s, const OrthoTask& o) {
-  uint32_t have;
-  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(have) : "l"(s.done + o.b) : "memory");
-  return __all_sync(0xffffffffu, have >= o.needs);
-}
 // Until matrix o.b has the tiles that the task needs.  Limited as the other
 // waits are; the whole warp calls it.
 __device__ __forceinline__ bool ortho_wait(const OrthoSteps& s, const OrthoTask& o,
                                            volatile int* dead) {
   const long long t0 = clock64();
   while (true) {
-    if (ortho_met(s, o)) return true;
+    uint32_t have;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];"
+                 : "=r"(have)
+                 : "l"(s.done + o.b)
+                 : "memory");
+    if (__all_sync(0xffffffffu, have >= o.needs)) return true;
     int stop = *dead;
     if (!stop && clock64() - t0 > kWaitCycles) {
       stop = 1;
@@ -143,11 +148,80 @@ __device__ __forceinline__ bool ortho_wait(const OrthoSteps& s, const OrthoTask&
     if (__any_sync(0xffffffffu, stop)) return false;
   }
 }
-// What other CTAs' tensor copies stored before a wait is in place for this
-// thread's, and the other way round.
+// What other CTAs' tensor copies stored before a wait is in place for copies
+// behind it, and the other way round.
 __device__ __forceinline__ void fence_copies() {
-  asm volatile("fence.proxy.async;" ::: "memory");
+  asm volatile("fence.proxy.async.global;" ::: "memory");
 }
+
+// A task as the looking-up warp hands it on.
+struct OrthoNote {
+  int product, step, b, i0, j0, chunks;
+  bool mirror;
+};
+__device__ __forceinline__ uint4 note_low(const OrthoTask& o) {
+  return make_uint4((uint32_t)o.product, (uint32_t)o.step, (uint32_t)o.b, (uint32_t)o.i0);
+}
+__device__ __forceinline__ uint4 note_high(const OrthoTask& o) {
+  return make_uint4((uint32_t)o.j0, (uint32_t)o.chunks, (uint32_t)o.mirror, 0u);
+}
+__device__ __forceinline__ OrthoNote note_of(const uint4& lo, const uint4& hi) {
+  OrthoNote n;
+  n.product = (int)lo.x;
+  n.step = (int)lo.y;
+  n.b = (int)lo.z;
+  n.i0 = (int)lo.w;
+  n.j0 = (int)hi.x;
+  n.chunks = (int)hi.y;
+  n.mirror = hi.z != 0;
+  return n;
+}
+// Looks a pair's tasks up and waits for what they need: ~500 cycles of
+// arithmetic, as many for the counter and 1400 for the fence where copies are in
+// flight, which the loading warp would miss (1035 cycles a step there, __STEP__
+// with this warp).
+__device__ __forceinline__ void ortho_tasks(const OrthoSteps& s, uint32_t at, uint32_t sfull,
+                                            uint32_t sempty, int first, int tasks, int step,
+                                            volatile int* dead) {
+  uint32_t slot = 0, phase = 1;
+  bool live = true;
+  for (int t = first; t < tasks && live; t += step) {
+    const OrthoTask o = ortho_task(s, t);
+    live = ortho_wait(s, o, dead) && bar_wait(sempty + 8 * slot, phase, dead);
+    live = __all_sync(0xffffffffu, live);
+    if (!live) break;
+    fence_copies();
+    if (elect()) {
+      sts16(at + slot * 4 * kNoteInts, note_low(o));
+      sts16(at + slot * 4 * kNoteInts + 16, note_high(o));
+      bar_arrive(sfull + 8 * slot);
+    }
+    __syncwarp();
+    if (++slot == kTaskSlots) {
+      slot = 0;
+      phase ^= 1;
+    }
+  }
+}
+// One reader's place in that ring.  False: a wait gave up.
+struct OrthoTasks {
+  uint32_t at, sfull, sempty, slot = 0, phase = 0;
+  OrthoNote o{};
+  __device__ __forceinline__ bool next(volatile int* dead) {
+    bool live = bar_wait(sfull + 8 * slot, phase, dead);
+    live = __all_sync(0xffffffffu, live);
+    if (!live) return false;
+    o = note_of(lds16(at + slot * 4 * kNoteInts), lds16(at + slot * 4 * kNoteInts + 16));
+    __syncwarp();
+    if (elect()) bar_arrive(sempty + 8 * slot);
+    __syncwarp();
+    if (++slot == kTaskSlots) {
+      slot = 0;
+      phase ^= 1;
+    }
+    return true;
+  }
+};
 
 __device__ __forceinline__ uint32_t box_at(int row, int unit) {  // 16-byte units, 128-byte swizzle
   return (uint32_t)(row * 128 + ((unit ^ (row & 7)) << 4));
@@ -179,89 +253,72 @@ __device__ __forceinline__ uint4 split_halves8(float v[8]) {
   return hi;
 }
 
-// A walk over the chunks of a pair's tasks, in order, and the ring's slots.
-struct OrthoWalk {
-  OrthoTask o{};
-  int t, c = 0;
+// The chunk ring's slots.
+struct OrthoSlot {
   uint32_t slot = 0, phase = 0;
-  __device__ __forceinline__ OrthoWalk(const OrthoSteps& s, int first, int tasks) : t(first) {
-    if (t < tasks) o = ortho_task(s, t);
-  }
-  __device__ __forceinline__ bool next(const OrthoSteps& s, int tasks, int step) {
+  __device__ __forceinline__ void next() {
     if (++slot == kBoxChunks) {
       slot = 0;
       phase ^= 1;
     }
-    if (++c < o.chunks) return false;
-    c = 0;
-    t += step;
-    if (t < tasks) o = ortho_task(s, t);
-    return true;  // another task
   }
 };
 
 // Warp 2: brings the operands of the epilogue's chunks, and before a tile's
 // first the note of the tile, once the epilogue has read the one before
 // (noted).  The epilogue takes it behind that chunk's barrier.
-__device__ __forceinline__ void ortho_bring(const OrthoSteps& s, uint32_t boxes, uint32_t note,
-                                            uint32_t efull, uint32_t bfree, uint32_t noted,
-                                            int first, int tasks, int step, int half, int lane,
-                                            volatile int* dead) {
-  OrthoWalk w(s, first, tasks);
-  bool live = true, task = true;
+__device__ __forceinline__ void ortho_bring(const OrthoSteps& s, OrthoTasks in, uint32_t boxes,
+                                            uint32_t note, uint32_t efull, uint32_t bfree,
+                                            uint32_t noted, int first, int tasks, int step,
+                                            int half, int lane, volatile int* dead) {
+  OrthoSlot r;
+  bool live = true;
   uint32_t issued = 0, note_phase = 1;
-  while (w.t < tasks) {
-    if (task) {
-      live = live && bar_wait(noted, note_phase, dead);
-      note_phase ^= 1;
-      live = __all_sync(0xffffffffu, live);
-      if (live && w.o.product != GRAM) {
-        live = ortho_wait(s, w.o, dead);
-        fence_copies();
-      }
-      if (live) {
-        const int vals[kNoteInts] = {w.o.product, w.o.step, w.o.b,           w.o.i0,
-                                     w.o.j0,      w.o.chunks, w.o.mirror, 0};
-#pragma unroll
-        for (int q = 0; q < kNoteInts; ++q)
-          if (lane == q) asm volatile("st.shared.u32 [%0], %1;" ::"r"(note + 4 * q), "r"(vals[q]));
-        if (w.o.product != GRAM) {
-          const float* diag = (w.o.product == POLY ? s.diag_gram : s.diag_poly) +
-                              (int64_t)w.o.b * s.side;
-          const bool by_row = w.o.product == POLY || !s.tall;
-          const bool by_column = w.o.product == POLY || s.tall;
-          float4 r = make_float4(0.0f, 0.0f, 0.0f, 0.0f), c[2] = {r, r};
-          if (by_row) r = ld_state(diag + w.o.i0 + half * kRowsCta + 4 * lane);
-#pragma unroll
-          for (int q = 0; q < 2; ++q)
-            if (by_column && q * 128 < w.o.chunks * 64)
-              c[q] = ld_state(diag + w.o.j0 + q * 128 + 4 * lane);
-          const uint32_t at = note + 4 * kNoteInts + 16 * lane;
-          st_shared4(at, r.x, r.y, r.z, r.w);
-#pragma unroll
-          for (int q = 0; q < 2; ++q)
-            st_shared4(at + 512 * (q + 1), c[q].x, c[q].y, c[q].z, c[q].w);
-        }
-        __syncwarp();  // the note is written when the lane below arrives
-      }
-    }
-    live = live && bar_wait(bfree + 8 * w.slot, w.phase ^ 1, dead);
+  for (int t = first; t < tasks && live; t += step) {
+    live = in.next(dead) && bar_wait(noted, note_phase, dead);
     live = __all_sync(0xffffffffu, live);
     if (!live) break;
-    const uint32_t at = boxes + w.slot * 2 * kBox, bar = efull + 8 * w.slot;
-    const int x = w.o.j0 + 64 * w.c;
-    const int y = w.o.b * s.k[w.o.product].rows_out + w.o.i0 + half * kRowsCta;
-    if (elect()) {
-      bar_expect(bar, w.o.product * kBox);
-      if (w.o.product == POLY) box_load(&s.maps.gram, at, x, y, bar);
-      if (w.o.product == GROW) {
-        box_load(&s.maps.hi[w.o.step & 1], at, x, y, bar);
-        box_load(&s.maps.lo, at + kBox, x, y, bar);
-      }
+    note_phase ^= 1;
+    const OrthoNote& o = in.o;
+    if (lane < 2) {
+      OrthoTask whole{};
+      whole.product = o.product; whole.step = o.step; whole.b = o.b; whole.i0 = o.i0;
+      whole.j0 = o.j0; whole.chunks = o.chunks; whole.mirror = o.mirror;
+      sts16(note + 16 * lane, lane ? note_high(whole) : note_low(whole));
     }
-    __syncwarp();
-    ++issued;
-    task = w.next(s, tasks, step);
+    if (o.product != GRAM) {
+      const float* diag = (o.product == POLY ? s.diag_gram : s.diag_poly) + (int64_t)o.b * s.side;
+      const bool by_row = o.product == POLY || !s.tall, by_column = o.product == POLY || s.tall;
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f), c[2] = {v, v};
+      if (by_row) v = ld_state(diag + o.i0 + half * kRowsCta + 4 * lane);
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        if (by_column && q * 128 < o.chunks * 64) c[q] = ld_state(diag + o.j0 + q * 128 + 4 * lane);
+      const uint32_t at = note + 4 * kNoteInts + 16 * lane;
+      st_shared4(at, v.x, v.y, v.z, v.w);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) st_shared4(at + 512 * (q + 1), c[q].x, c[q].y, c[q].z, c[q].w);
+    }
+    __syncwarp();  // the note is written when the lane below arrives
+    const int y = o.b * s.k[o.product].rows_out + o.i0 + half * kRowsCta;
+    for (int c = 0; c < o.chunks; ++c) {
+      live = bar_wait(bfree + 8 * r.slot, r.phase ^ 1, dead);
+      live = __all_sync(0xffffffffu, live);
+      if (!live) break;
+      const uint32_t at = boxes + r.slot * 2 * kBox, bar = efull + 8 * r.slot;
+      const int x = o.j0 + 64 * c;
+      if (elect()) {
+        bar_expect(bar, o.product * kBox);
+        if (o.product == POLY) box_load(&s.maps.gram, at, x, y, bar);
+        if (o.product == GROW) {
+          box_load(&s.maps.hi[o.step & 1], at, x, y, bar);
+          box_load(&s.maps.lo, at + kBox, x, y, bar);
+        }
+      }
+      __syncwarp();
+      ++issued;
+      r.next();
+    }
   }
   // after a wait that gave up: the boxes in flight land before the CTA returns
   for (uint32_t q = issued > kBoxChunks ? issued - kBoxChunks : 0; !live && q < issued; ++q) {
@@ -273,41 +330,47 @@ __device__ __forceinline__ void ortho_bring(const OrthoSteps& s, uint32_t boxes,
 }
 
 // Warp 3: stores the finished chunks and counts finished tiles.
-__device__ __forceinline__ void ortho_store(const OrthoSteps& s, uint32_t boxes, uint32_t edone,
-                                            uint32_t bfree, int first, int tasks, int step,
-                                            int half, volatile int* dead) {
-  OrthoWalk w(s, first, tasks);
-  while (w.t < tasks) {
-    bool live = bar_wait(edone + 8 * w.slot, w.phase, dead);
-    live = __all_sync(0xffffffffu, live);  // the lanes leave together
+__device__ __forceinline__ void ortho_store(const OrthoSteps& s, OrthoTasks in, uint32_t boxes,
+                                            uint32_t edone, uint32_t bfree, int first, int tasks,
+                                            int step, int half, volatile int* dead) {
+  OrthoSlot r;
+  bool live = true;
+  for (int t = first; t < tasks && live; t += step) {
+    live = in.next(dead);
     if (!live) break;
-    const uint32_t at = boxes + w.slot * 2 * kBox;
-    const int x = w.o.j0 + 64 * w.c, row = w.o.i0 + half * kRowsCta;
-    const int y = w.o.b * s.k[w.o.product].rows_out;
-    if (elect()) {
-      if (w.o.product == GROW) {
-        box_store(&s.maps.hi[~w.o.step & 1], at, x, y + row);
-        if (w.o.step + 1 < s.steps) box_store(&s.maps.lo, at + kBox, x, y + row);
-      } else {
-        box_store(w.o.product == GRAM ? &s.maps.gram : &s.maps.poly_out, at, x, y + row);
-        if (w.o.mirror) {
-          const CUtensorMap* t = w.o.product == GRAM ? &s.maps.gram_t : &s.maps.poly_t;
-          box_store(t, at + kBox, row, y + x);
-          box_store(t, at + kBox + kBox / 2, row + 64, y + x);
+    const OrthoNote& o = in.o;
+    const int row = o.i0 + half * kRowsCta, y = o.b * s.k[o.product].rows_out;
+    for (int c = 0; c < o.chunks; ++c) {
+      live = bar_wait(edone + 8 * r.slot, r.phase, dead);
+      live = __all_sync(0xffffffffu, live);  // the lanes leave together
+      if (!live) break;
+      const uint32_t at = boxes + r.slot * 2 * kBox;
+      const int x = o.j0 + 64 * c;
+      if (elect()) {
+        if (o.product == GROW) {
+          box_store(&s.maps.hi[~o.step & 1], at, x, y + row);
+          if (o.step + 1 < s.steps) box_store(&s.maps.lo, at + kBox, x, y + row);
+        } else {
+          box_store(o.product == GRAM ? &s.maps.gram : &s.maps.poly_out, at, x, y + row);
+          if (o.mirror) {
+            const CUtensorMap* m = o.product == GRAM ? &s.maps.gram_t : &s.maps.poly_t;
+            box_store(m, at + kBox, row, y + x);
+            box_store(m, at + kBox + kBox / 2, row + 64, y + x);
+          }
+        }
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        bar_arrive(bfree + 8 * r.slot);
+        if (c + 1 == o.chunks) {
+          asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+          fence_copies();
+          // behind this tile's boxes and (through the chunks' barriers) diagonals
+          asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(s.done + o.b) : "memory");
         }
       }
-      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-      asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-      bar_arrive(bfree + 8 * w.slot);
-      if (w.c + 1 == w.o.chunks) {
-        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-        fence_copies();
-        // behind this tile's boxes and (through the chunks' barriers) diagonals
-        asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(s.done + w.o.b) : "memory");
-      }
+      __syncwarp();
+      r.next();
     }
-    __syncwarp();
-    w.next(s, tasks, step);
   }
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
@@ -377,7 +440,7 @@ __device__ __forceinline__ void ortho_piece(float ca, float cb, float cc, bool b
 __global__ void __launch_bounds__(kOrthoThreads, 1)
     ortho_kernel(const __grid_constant__ OrthoSteps s, int tasks) {
   extern __shared__ __align__(1024) unsigned char ortho_smem[];
-  __shared__ __align__(8) uint64_t bars[2 * kOrthoStages + 6 + 3 * kBoxChunks];
+  __shared__ __align__(8) uint64_t bars[2 * kOrthoStages + 6 + 3 * kBoxChunks + 2 * kTaskSlots];
   __shared__ uint32_t tmem_at;
   __shared__ int dead;
   constexpr uint32_t stages = kOrthoStages;
@@ -388,6 +451,7 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
   const uint32_t tfull = empty + 8 * stages, tempty = tfull + 16, ready = tempty + 16;
   const uint32_t efull = ready + 8, edone = efull + 8 * kBoxChunks;
   const uint32_t bfree = edone + 8 * kBoxChunks, noted = bfree + 8 * kBoxChunks;
+  const uint32_t sfull = noted + 8, sempty = sfull + 8 * kTaskSlots;
   const uint32_t note = boxes + kSideBytes;
 
   if (warp == 0 && elect()) {
@@ -402,6 +466,10 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
     }
     bar_init(ready, 2);
     bar_init(noted, kEpis);
+    for (int q = 0; q < kTaskSlots; ++q) {
+      bar_init(sfull + 8 * q, 1);
+      bar_init(sempty + 8 * q, half == 0 ? 4 : 3);  // the second CTA issues no products
+    }
     for (int b = 0; b < kBoxChunks; ++b) {
       bar_init(efull + 8 * b, 1);
       bar_init(edone + 8 * b, kEpis);
@@ -426,22 +494,26 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
     __syncwarp();
   }
   uint32_t tmem = 0;
-  if (warp == 1 || warp == 2 || warp >= kEpi0) {
+  if (warp == 1 || warp == 2 || (warp >= kEpi0 && warp < kTaskWarp)) {
     asm volatile("bar.sync 1, %0;" ::"n"((kEpis + 2) * 32) : "memory");
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     tmem = *(volatile uint32_t*)&tmem_at;
   }
-  const bool early = warp == 3;  // only stores this CTA's own boxes from here on
+  const bool early = warp == 3 || warp == kTaskWarp;  // only this CTA's own memory from here on
   if (early) cluster_arrive();
+  OrthoTasks tasks_in;
+  tasks_in.at = note + kTaskAt;
+  tasks_in.sfull = sfull;
+  tasks_in.sempty = sempty;
 
   if (warp == 0) {
     const uint32_t full_lead = remote(full, 0);
     uint32_t st = 0, ph = 0, end_s = 0, end_ph = 0;  // end: where a wait gave up
-    bool live = true, met = false;
-    OrthoTask o{}, next{};
-    if (first < tasks) next = ortho_task(s, first);
+    bool live = true;
     for (int t = first; t < tasks; t += clusters) {
-      o = next;
+      if (live) live = tasks_in.next(&dead);
+      if (!live) break;
+      const OrthoNote& o = tasks_in.o;
       const OrthoK& k = s.k[o.product];
       const int i0 = o.i0 + (int)half * kRowsCta, j0 = o.j0 + (int)half * (k.bn / 2);
       const int ya = o.b * k.rows_a, yb = o.b * k.rows_b, kblocks = k.kblocks;
@@ -457,18 +529,7 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
                                  : o.product == POLY ? &s.maps.gram_b
                                  : s.tall            ? &s.maps.poly
                                                      : x;
-      if (live && !met) {
-        live = ortho_wait(s, o, &dead);
-        fence_copies();
-      }
-      met = false;
       for (int kb = 0; kb < kblocks; ++kb) {
-        // the next task, and whether it can go on, while this one's loads run
-        if (kb == kblocks / 2 && t + clusters < tasks) {
-          next = ortho_task(s, t + clusters);
-          met = ortho_met(s, next);
-          fence_copies();
-        }
         if (live) {
           live = bar_wait(empty + 8 * st, ph ^ 1, &dead);
           end_s = st;
@@ -514,7 +575,9 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
       uint32_t st = 0, ph = 0, acc = 0, aph = 0;
       bool live = bar_wait(ready, 0, &dead);
       for (int t = first; t < tasks; t += clusters) {
-        const OrthoK& k = s.k[ortho_task(s, t).product];
+        live = live && tasks_in.next(&dead);
+        if (!live) break;
+        const OrthoK& k = s.k[tasks_in.o.product];
         const bool a_c = k.a_c, b_c = k.b_c;
         const int kblocks = k.kblocks;
         // fp32 sums of fp16 values, M = 256, N = bn
@@ -551,11 +614,14 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
     }
     __syncwarp();
   } else if (warp == 2) {
-    ortho_bring(s, boxes, note, efull, bfree, noted, first, tasks, clusters, (int)half, lane,
-                &dead);
+    ortho_bring(s, tasks_in, boxes, note, efull, bfree, noted, first, tasks, clusters, (int)half,
+                lane, &dead);
     __syncwarp();
   } else if (warp == 3) {
-    ortho_store(s, boxes, edone, bfree, first, tasks, clusters, (int)half, &dead);
+    ortho_store(s, tasks_in, boxes, edone, bfree, first, tasks, clusters, (int)half, &dead);
+    __syncwarp();
+  } else if (warp == kTaskWarp) {
+    ortho_tasks(s, note + kTaskAt, sfull, sempty, first, tasks, clusters, &dead);
     __syncwarp();
   } else if (warp >= kEpi0) {
     const int w = (warp - kEpi0) & 3, set = (warp - kEpi0) >> 2;
@@ -569,13 +635,12 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
       ok = bar_wait(efull + 8 * eb, eph, &dead);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      const uint4 n0 = lds16(note), n1 = lds16(note + 16);
-      const int product = (int)n0.x, step = (int)n0.y, i0 = (int)n0.w, j0 = (int)n1.x,
-                chunks = (int)n1.y;
-      const bool mirror = n1.z != 0;
+      const OrthoNote o = note_of(lds16(note), lds16(note + 16));
+      const int product = o.product, step = o.step, i0 = o.i0, j0 = o.j0, chunks = o.chunks;
+      const bool mirror = o.mirror;
       const int i = i0 + (int)half * kRowsCta + row;
       float* diag_out =
-          (product == GRAM ? s.diag_gram : s.diag_poly) + (int64_t)n0.z * s.side;
+          (product == GRAM ? s.diag_gram : s.diag_poly) + (int64_t)o.b * s.side;
       const float ca = s.coef[step][0], cb = s.coef[step][1], cc = s.coef[step][2];
       // The diagonal of this thread's row, and of this warp's 16 columns of
       // each chunk (two chunks across a register's lanes).
