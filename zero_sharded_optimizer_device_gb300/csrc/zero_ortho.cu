@@ -27,10 +27,10 @@ namespace zk {
 // Powers of two that operands are stored times: X, O of G, O of P.
 constexpr float kScaleX = 4096.0f, kScaleG = 256.0f, kScaleP = 64.0f;
 
-// A chunk of 64 columns is in flight for ~4000 cycles (operands 1300, epilogue
-// 1300, store 1500) and a tile 64 deep per operand stage 520: three chunks of
-// two boxes beside four stages.
-constexpr int kBoxChunks = 3;
+// Chunks of 64 columns (two boxes each) in flight, beside five operand stages
+// of 32 KiB: with three chunks and four stages 11008 x 4096 takes 2270 us
+// instead of 2126, 24 x 1024 x 1024 546 instead of 530.
+constexpr int kBoxChunks = 2;
 constexpr int kBox = 16384;                      // 128 rows of 64 fp16 columns
 constexpr int kSideBytes = 2 * kBoxChunks * kBox;
 // What the epilogue has to know of a tile: the task, and the diagonal of its
@@ -178,7 +178,7 @@ __device__ __forceinline__ OrthoNote note_of(const uint4& lo, const uint4& hi) {
 }
 // Looks a pair's tasks up and waits for what they need: ~500 cycles of
 // arithmetic, as many for the counter and 1400 for the fence where copies are in
-// flight, which the loading warp would miss (1035 cycles a step there, __STEP__
+// flight, which the loading warp would miss (24 x 1024 x 1024: 508 us for the products so, 457
 // with this warp).
 __device__ __forceinline__ void ortho_tasks(const OrthoSteps& s, uint32_t at, uint32_t sfull,
                                             uint32_t sempty, int first, int tasks, int step,
