@@ -73,7 +73,7 @@ struct OrthoMaps {
 struct OrthoSteps {
   OrthoMaps maps;
   OrthoK k[3];
-  int steps, batch, group, tiles_step;  // matrices in turn; tiles of a matrix's step
+  int steps, batch, tiles_step;  // tiles of a matrix's step
   int cols;                 // of X as stored
   int tall;                 // P's diagonal goes by column
   int side;                 // elements of a diagonal
@@ -88,23 +88,18 @@ struct OrthoTask {
   uint32_t needs;           // finished tiles of matrix b
   bool mirror;              // the result's transpose has to be stored too
 };
-// Tasks of a group of matrices after those of the group before.  Tiles of
-// symmetric results are those of the lower triangle, row by row: row i of 256
-// has i + 1 squares of 256, each of 256 / bn tiles.
+// Tiles of symmetric results are those of the lower triangle, row by row: row i
+// of 256 has i + 1 squares of 256, each of 256 / bn tiles.
 __device__ __forceinline__ OrthoTask ortho_task(const OrthoSteps& s, int t) {
   OrthoTask o;
-  const int full = s.group * s.tiles_step * s.steps, turn = t / full;
-  t -= turn * full;
-  const int left = s.batch - turn * s.group, group = left < s.group ? left : s.group;
-  const int each = group * s.tiles_step;
+  const int each = s.batch * s.tiles_step;
   o.step = t / each;
   t -= o.step * each;
-  o.product = t < group * s.k[POLY].before ? GRAM : t < group * s.k[GROW].before ? POLY : GROW;
+  o.product = t < s.batch * s.k[POLY].before ? GRAM : t < s.batch * s.k[GROW].before ? POLY : GROW;
   const OrthoK& k = s.k[o.product];
-  t -= group * k.before;
-  const int b = t / k.tiles;
-  t -= b * k.tiles;
-  o.b = turn * s.group + b;
+  t -= s.batch * k.before;
+  o.b = t / k.tiles;
+  t -= o.b * k.tiles;
   o.needs = 2u * (uint32_t)(o.step * s.tiles_step + k.before);
   if (o.product == GROW) {
     const int i = t / k.tiles_j;
@@ -1135,7 +1130,6 @@ cudaError_t launch_orthogonalize(const OrthoCall& c, cudaStream_t st) {
     p.steps = c.steps;
     p.batch = (int)batch;
     p.tiles_step = x.before + x.tiles;
-    p.group = (int)batch;
     p.cols = (int)w.ld;
     p.tall = tall;
     p.side = (int)w.side;
