@@ -1783,7 +1783,11 @@ static cudaError_t launch_mode(const ProductK& in, cudaStream_t st) {
   // 18.4 / 14.1, 2048 x 1024 x 4096 at BN = 256 23.4 / 18.0, 1024 x 2304 x 768
   // at 128 8.8 / 16.6; four parts, clusters of 8, always lost.)  Lines off
   // 16-byte boundaries bound a step by shifting them: 870 cycles for 144 of
-  // them, 1040 for 192, 1430 for 256.
+  // them, 1040 for 192, 1430 for 256.  4 bits: a step is 256 codes, 512 cycles at
+  // BN = 128 and below, 596 (NV) and 550 (MX) at 192.  (us at 128 / 192, NV: 1024
+  // x 11008 x 4096 32.0 / 29.0, 1024 x 4096 x 11008 31.0 / 34.3, 4096 x 4096 x 4096
+  // 42.1 / 36.3, 8192 x 11008 x 4096 194 / 153, 1024 x 1024 x 1024 7.1 / 7.5; in
+  // two parts at 128 256 x 4096 x 11008 18.1 / 14.9, 1024 x 1024 x 1024 7.1 / 8.7.)
   // The tensor cores add to their fp32 sums without rounding to nearest, so a
   // long contraction loses digits: 7e-7 of the result after 768 terms, 7e-6
   // after 6000 (in 2-norms).  fp32 results therefore take the sums out every
@@ -1825,6 +1829,7 @@ static cudaError_t launch_mode(const ProductK& in, cudaStream_t st) {
       const int64_t tiles = tiles_i * tiles_j + (fused ? 0 : (bias_rows + 255) / 256);
       const double waves = (double)((tiles * S + pairs - 1) / pairs);
       double step = bn > 128 ? (exact ? 520 + 1500.0 / kRound : 520) : 430;
+      if (FP4) step = bn <= 128 ? 512 : k.blocks_of == 16 ? 596 : 550;
       const double shift = 300 + 4.2 * ((gen_a ? kRowsCta : 0) + (gen_b ? bn / 2 : 0));
       if ((gen_a || gen_b) && step < shift) step = shift;
       const double cost =
