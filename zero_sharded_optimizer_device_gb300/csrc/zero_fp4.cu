@@ -1,6 +1,9 @@
 // Matrices in microscaled 4-bit numbers (zero_fp4_*, include/zero.h): to E2M1
 // codes with a scale per block and back, and their products on the tensor
 // cores' block-scaled instructions (the kernel of zero_product.cuh).
+#include <algorithm>
+#include <cmath>
+
 #include "zero_fp4.cuh"
 #include "zero_product.cuh"
 #include "zero_walk.cuh"
@@ -10,9 +13,9 @@ namespace zk {
 // A block's scale byte and the factor that brings its values to codes, from
 // the largest magnitude's bits (NaN and infinity are the largest as integers).
 // A block that holds either has scale NaN and codes 0.
-// NV: the quotient by 6 g first by its reciprocal, half a unit of E4M3's
-// sixteenths from it at most where both neighbours at 2^-21 give the same byte;
-// else divided (an IEEE division for each block: __DIV__).
+// NV: E4M3 of the quotient by 6 g.  Its product with the reciprocal is within
+// 2^-22 of it; where 2^-21 more and less round to one byte, so does the quotient.
+// Only else is it divided.
 constexpr uint32_t kInfBits = 0x7F800000u;
 struct Whole {
   float g, six_g, by_six_g;  // 1 / (6 g)
@@ -420,9 +423,27 @@ cudaError_t launch_tensor_scale(const MaxK& k, float* g, cudaStream_t st) {
   return launch_next(maximum_kernel, dim3(1), dim3(kMaxima), st, k.maxima, n, g);
 }
 
+// Whether a few rows are quicker by zero_fp4_rows.cu, by the times of both in us:
+// blocks of 16 outputs that share an SM's instruction slots, each taking 2048
+// codes at a time; or tiles of 256 outputs whose steps of 256 codes follow one
+// another.  Neither depends much on the rows, 1 to 8.  (Measured, NV, 8 rows, few
+// rows / tiles, [n, k]: 1024 x 256 2.3 / 4.6, 1024 x 4096 4.6 / 7.9, 4096 x 4096 5.8
+// / 8.5, 4096 x 8192 9.2 / 10.6, 8192 x 2048 7.2 / 7.3, 8192 x 4096 10.3 / 9.7, 11008 x
+// 2048 9.2 / 7.9, 11008 x 4096 12.6 / 10.1, 16384 x 512 8.5 / 6.1, 50257 x 768 22 /
+// 9.3, 256 x 16384 8.6 / 14.0.)
+static bool few_rows_win(const ProductK& k) {
+  if (k.rows > kFewRows) return false;
+  const double codes = 4.0 * (double)k.depth, n = (double)k.cols;
+  const double turns = std::max(0.5, codes / 2048), steps = std::ceil(codes / 256);
+  const double blocks = std::ceil(n / 16 / sm_count()), tiles = std::ceil(n / 256);
+  const double rows_us = 1.7 + blocks * (0.5 + 0.83 * turns);
+  const double tiles_us = 4.9 + 0.16 * steps + 0.022 * tiles + 2e-8 * n * codes;
+  return rows_us <= tiles_us;
+}
+
 cudaError_t launch_fp4_product(const ProductK& k, int mode, cudaStream_t st) {
   if (k.rows <= 0 || k.cols <= 0) return cudaSuccess;
-  if (k.rows <= kFewRows) return launch_fp4_rows(k, mode, st);
+  if (few_rows_win(k)) return launch_fp4_rows(k, mode, st);
   return mode == LIN_FORWARD ? launch_mode<LIN_FORWARD, OF_FP4>(k, st)
                              : launch_mode<LIN_DINPUT, OF_FP4>(k, st);
 }
