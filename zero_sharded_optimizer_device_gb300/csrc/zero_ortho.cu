@@ -20,6 +20,7 @@
 
 #include <cuda_fp16.h>
 
+#include <cmath>
 #include <initializer_list>
 
 namespace zk {
@@ -288,7 +289,8 @@ __device__ __forceinline__ void ortho_bring(const OrthoSteps& s, OrthoTasks in, 
       if (by_row) v = ld_state(diag + o.i0 + half * kRowsCta + 4 * lane);
 #pragma unroll
       for (int q = 0; q < 2; ++q)
-        if (by_column && q * 128 < o.chunks * 64) c[q] = ld_state(diag + o.j0 + q * 128 + 4 * lane);
+        if (by_column && q * 128 + 4 * lane < o.chunks * 64)
+          c[q] = ld_state(diag + o.j0 + q * 128 + 4 * lane);
       const uint32_t at = note + 4 * kNoteInts + 16 * lane;
       st_shared4(at, v.x, v.y, v.z, v.w);
 #pragma unroll
@@ -1034,12 +1036,24 @@ static cudaError_t launch_ortho(const OrthoSteps& s, int64_t tasks, cudaStream_t
 }
 
 // Tile width: waves of tiles times a tile's steps (see zero_product.cuh's
-// measurements of a step at 256 and at 128 columns) and its epilogue.
-static int tile_width(int64_t tiles256, int64_t tiles128, int64_t kblocks) {
-  const int64_t pairs = sm_count() / 2;
-  const double wide = (double)((tiles256 + pairs - 1) / pairs) * (520.0 * kblocks) + 25 * 256;
-  const double narrow = (double)((tiles128 + pairs - 1) / pairs) * (430.0 * kblocks) + 25 * 128;
-  return wide <= narrow ? 256 : 128;
+// measurements of a step at 256 and at 128 columns; at 64 a step is the loads of
+// A's rows) and its epilogue.  64 columns only where the contraction lies
+// along B's rows, as a box of them holds 64 along its own.  (Five
+// steps of 768 x 768, 6 squares of 256 twelve deep, 105 us at 128 columns, 96 with
+// 64; 1024 x 4096 190 and 180; 24 x 1024 x 1024, 240 squares, takes 256.)
+static int tile_width(int64_t squares, int64_t kblocks, bool narrow) {
+  const double pairs = (double)(sm_count() / 2), deep = (double)kblocks;
+  double best = 0;
+  int width = 0;
+  for (int bn = 256; bn >= (narrow ? 64 : 128); bn /= 2) {
+    const double step = bn == 256 ? 520 : bn == 128 ? 430 : 380;
+    const double waves = std::ceil((double)(squares * (256 / bn)) / pairs);
+    const double cost = waves * step * deep + 25 * bn;
+    if (width && cost >= best) continue;
+    best = cost;
+    width = bn;
+  }
+  return width;
 }
 
 cudaError_t launch_orthogonalize(const OrthoCall& c, cudaStream_t st) {
@@ -1078,9 +1092,8 @@ cudaError_t launch_orthogonalize(const OrthoCall& c, cudaStream_t st) {
     OrthoSteps p{};
     const int64_t sq = batch * squares, kb_far = (far + kDeep - 1) / kDeep,
                   kb_k = (k + kDeep - 1) / kDeep;
-    const int bn_gram = tile_width(sq, sq * 2, kb_far), bn_poly = tile_width(sq, sq * 2, kb_k);
-    const int bn_grow = tile_width(batch * rows * (up(w.ld, 256) / 256),
-                                   batch * rows * (up(w.ld, 128) / 128), kb_k);
+    const int bn_gram = tile_width(sq, kb_far, !tall), bn_poly = tile_width(sq, kb_k, true);
+    const int bn_grow = tile_width(batch * rows * (up(w.ld, 256) / 256), kb_k, tall);
     // Operands by rows (boxes of 128 rows, or half a tile's width of them) or,
     // where the contraction runs down the rows, in boxes of 64 of them.
     const int64_t all = batch * w.rows, sides = batch * w.side;
@@ -1126,7 +1139,7 @@ cudaError_t launch_orthogonalize(const OrthoCall& c, cudaStream_t st) {
     x.tiles_j = (int)(up(w.ld, x.bn) / x.bn);
     x.tiles = (int)(rows * x.tiles_j);
     x.before = q.before + q.tiles;
-    for (OrthoK* o : {&g, &q, &x}) o->bn_log2 = o->bn == 256 ? 8 : 7;
+    for (OrthoK* o : {&g, &q, &x}) o->bn_log2 = o->bn == 256 ? 8 : o->bn == 128 ? 7 : 6;
     p.steps = c.steps;
     p.batch = (int)batch;
     p.tiles_step = x.before + x.tiles;
