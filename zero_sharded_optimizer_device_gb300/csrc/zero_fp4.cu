@@ -2,6 +2,7 @@
 // codes with a scale per block and back, and their products on the tensor
 // cores' block-scaled instructions (the kernel of zero_product.cuh).
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "zero_fp4.cuh"
@@ -61,12 +62,15 @@ __device__ __forceinline__ uint32_t codes8(const float v[8], float factor) {
 }
 
 // ----------------------------------------------------------------- quantise --
-// Along the rows and along the columns by a kernel each: joined in one, through
-// shared memory both ways, 8192 x 4096 bf16 took 30 us, and the second reads
-// from L2 what the first read from memory.  A block of 256 threads takes whole
-// scale tiles, or halves of them that no other block has, so that every byte of
-// codes and scales, padding included, has one writer.  Bound by instructions:
-// about 9 and 8 a value.
+// Along the rows, along the columns, and both by a kernel each.  A block of 256
+// threads takes whole scale tiles, or halves of them that no other block has, so
+// that every byte of codes and scales, padding included, has one writer.  Bound by
+// instructions, about 13 a value of each direction, 68 % of the issue slots.  (us,
+// NV, alone along rows, along columns / by the kernel for both, both: 8192 x 4096
+// bf16 19.0, 21.1 / 21.3, 21.8, 31.5 (105 MB); fp32 27.3, 32.8 / 40.4, 41.0, 52.8;
+// 1024 x 1024 bf16 2.8, 2.9 / 3.6, 3.6, 5.0.  Blocks of 256 columns along the rows,
+// a thread having eight rows instead of two, take 17.7 at 8192 x 4096, but at 8192 x
+// 1024 8.2 instead of 7.3 and at 1024 x 1024 4.1 instead of 2.8.)
 constexpr int kQuantRows = 128, kQuantThreads = 256;
 
 __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return a > b ? a : b; }
@@ -248,22 +252,186 @@ __global__ void __launch_bounds__(kQuantThreads)
         *reinterpret_cast<const uint2*>(scales[threadIdx.x / 32] + threadIdx.x % 32 * 8);
 }
 
+// In both directions: 128 x 128 values cross shared memory, where they are whole
+// scale tiles either way.  A thread takes one block of a row after another, then
+// blocks of two columns side by side (bf16: one 32-bit word) or of one.
+template <bool WIDE>
+struct QuantShared {
+  static constexpr int kElem = WIDE ? 4 : 2, kLine = kQuantRows * kElem + 16;
+  unsigned char tile[kQuantRows * kLine];
+  unsigned char codes[kQuantRows * kCodeLine];  // of one direction, 64 bytes a line
+  unsigned char scales[2][1024];                // rows', columns'
+};
+
+// One direction's codes and scale tiles to memory.  line0: its first line;
+// byte0: of the lines' codes; tiles (line0 / 128, tile0 + t), t < tiles.
+__device__ __forceinline__ void store_quantized(const Fp4Mat& o, const unsigned char* codes,
+                                                const unsigned char* scales, int64_t line0,
+                                                int64_t lines, int64_t byte0, int64_t tile0,
+                                                int tiles) {
+#pragma unroll
+  for (int p = 0; p < kQuantRows * 4 / kQuantThreads; ++p) {
+    const int u = p * kQuantThreads + threadIdx.x, c = u >> 2;
+    const int64_t line = line0 + c, byte = byte0 + (u & 3) * 16, at = line * o.ld + byte;
+    if (line < lines && byte < o.line_bytes &&
+        in_extent(at, at + 16, line * o.ld, line * o.ld + o.line_bytes, ZERO_SITE_FP4))
+      *reinterpret_cast<uint4*>(o.codes + at) =
+          *reinterpret_cast<const uint4*>(codes + c * kCodeLine + (u & 3) * 16);
+  }
+  const int unit = threadIdx.x;  // 16 bytes
+  const int64_t t = tile0 + unit / 32;
+  if (unit >= tiles * 32 || t >= o.scale_tiles) return;
+  const int64_t at = (line0 / kQuantRows * o.scale_tiles + t) * kScaleTile + unit % 32 * 16;
+  if (!in_extent(at, at + 16, 0, o.scale_bytes, ZERO_SITE_FP4)) return;
+  *reinterpret_cast<uint4*>(o.scales + at) = *reinterpret_cast<const uint4*>(scales + unit * 16);
+}
+
+template <bool NV, bool WIDE>
+__global__ void __launch_bounds__(kQuantThreads, WIDE ? 2 : 4)
+    quantize_both_kernel(const __grid_constant__ QuantK k) {
+  extern __shared__ __align__(16) unsigned char quant_smem[];
+  using Shared = QuantShared<WIDE>;
+  Shared& sh = *reinterpret_cast<Shared*>(quant_smem);
+  constexpr int kSize = NV ? 16 : 32, kTiles = NV ? 2 : 1, kBlocks = kQuantRows / kSize;
+  after_previous_kernel();
+  const Whole whole = whole_of<NV>(k.g);
+  const int64_t row_tile = blockIdx.x / (uint32_t)k.tiles, row0 = row_tile * kQuantRows;
+  const int64_t col0 = (blockIdx.x - row_tile * k.tiles) * kQuantRows;
+  const int t = threadIdx.x;
+  {
+    const int line = t >> 4, unit = t & 15;
+    const Extent e{k.rows, k.cols};
+    const int64_t col = col0 + unit * 8;
+    const int valid = col >= k.cols ? 0 : k.cols - col < 8 ? (int)(k.cols - col) : 8;
+    Raw8 raw[8];
+#pragma unroll
+    for (int p = 0; p < 8; ++p) raw[p].a = raw[p].b = make_uint4(0, 0, 0, 0);
+    if (row0 + line < k.rows)
+      Down<WIDE, ZERO_SITE_FP4>(k.x, row0 + line, 16, col, valid)
+          .template get<8>(raw, k.rows, e);
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      uint4* at = reinterpret_cast<uint4*>(sh.tile + (p * 16 + line) * Shared::kLine +
+                                           unit * 8 * Shared::kElem);
+      at[0] = raw[p].a;
+      if (WIDE) at[1] = raw[p].b;
+    }
+  }
+  __syncthreads();
+  for (int u = t; u < kQuantRows * kBlocks; u += kQuantThreads) {
+    const int r = u % kQuantRows, b = u / kQuantRows;
+    const unsigned char* at = sh.tile + r * Shared::kLine + b * kSize * Shared::kElem;
+    constexpr int kWords = kSize * Shared::kElem / 16;
+    uint4 raw[kWords];
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) raw[i] = reinterpret_cast<const uint4*>(at)[i];
+    uint32_t top = 0;
+    if (WIDE) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i)
+        top = larger(larger(top, larger(raw[i].x & 0x7FFFFFFFu, raw[i].y & 0x7FFFFFFFu)),
+                     larger(raw[i].z & 0x7FFFFFFFu, raw[i].w & 0x7FFFFFFFu));
+    } else {
+      uint32_t two = 0;
+#pragma unroll
+      for (int i = 0; i < kWords; ++i)
+        two = larger2(larger2(larger2(larger2(two, raw[i].x), raw[i].y), raw[i].z), raw[i].w);
+      top = larger(two << 16, two & 0xFFFF0000u);
+    }
+    float factor;
+    sh.scales[0][(b >> 2) * kScaleTile + scale_at(r, b & 3)] =
+        (unsigned char)block_scale<NV>(top, whole, factor);
+    uint32_t* out = reinterpret_cast<uint32_t*>(sh.codes + r * kCodeLine + b * (kSize / 2));
+#pragma unroll
+    for (int i = 0; i < kSize / 8; ++i) {
+      float v[8];
+      if (WIDE) {
+        const uint4 x = raw[(2 * i) % kWords], y = raw[(2 * i + 1) % kWords];
+        v[0] = __uint_as_float(x.x); v[1] = __uint_as_float(x.y);
+        v[2] = __uint_as_float(x.z); v[3] = __uint_as_float(x.w);
+        v[4] = __uint_as_float(y.x); v[5] = __uint_as_float(y.y);
+        v[6] = __uint_as_float(y.z); v[7] = __uint_as_float(y.w);
+      } else {
+        from_bf16(raw[i % kWords], v);
+      }
+      out[i] = top >= kInfBits ? 0u : codes8(v, factor);
+    }
+  }
+  __syncthreads();
+  store_quantized(k.q, sh.codes, sh.scales[0], row0, k.rows, col0 / 2, col0 / (4 * kSize), kTiles);
+  __syncthreads();  // the codes are read
+  constexpr int kSide = WIDE ? 1 : 2;  // columns of a thread
+  for (int u = t; u < kQuantRows / kSide * kBlocks; u += kQuantThreads) {
+    const int c = u % (kQuantRows / kSide) * kSide, b = u / (kQuantRows / kSide);
+    const unsigned char* at = sh.tile + b * kSize * Shared::kLine + c * Shared::kElem;
+    uint32_t raw[kSize], top[kSide];
+#pragma unroll
+    for (int i = 0; i < kSize; ++i)
+      raw[i] = *reinterpret_cast<const uint32_t*>(at + i * Shared::kLine);
+    if (WIDE) {
+      top[0] = 0;
+#pragma unroll
+      for (int i = 0; i < kSize; ++i) top[0] = larger(top[0], raw[i] & 0x7FFFFFFFu);
+    } else {
+      uint32_t two = 0;
+#pragma unroll
+      for (int i = 0; i < kSize; ++i) two = larger2(two, raw[i]);
+      top[0] = two << 16;
+      top[kSide - 1] = two & 0xFFFF0000u;
+    }
+#pragma unroll
+    for (int h = 0; h < kSide; ++h) {
+      float factor;
+      const uint32_t most = !WIDE && h == 0 ? top[0] : top[kSide - 1];
+      sh.scales[1][(b >> 2) * kScaleTile + scale_at(c + h, b & 3)] =
+          (unsigned char)block_scale<NV>(most, whole, factor);
+      uint32_t* out =
+          reinterpret_cast<uint32_t*>(sh.codes + (c + h) * kCodeLine + b * (kSize / 2));
+#pragma unroll
+      for (int i = 0; i < kSize / 8; ++i) {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t w = raw[8 * i + j];
+          v[j] = WIDE ? __uint_as_float(w) : h ? bf16_hi(w) : bf16_lo(w);
+        }
+        out[i] = most >= kInfBits ? 0u : codes8(v, factor);
+      }
+    }
+  }
+  __syncthreads();
+  store_quantized(k.qt, sh.codes, sh.scales[1], col0, k.cols, row0 / 2, row0 / (4 * kSize), kTiles);
+}
+
+template <bool NV, bool WIDE>
+static cudaError_t launch_quantize_both(const QuantK& k, int64_t blocks, cudaStream_t st) {
+  static std::atomic<unsigned long long> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  constexpr int bytes = (int)sizeof(QuantShared<WIDE>);
+  if (!(done.load() & bit)) {
+    e = cudaFuncSetAttribute(quantize_both_kernel<NV, WIDE>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    done.fetch_or(bit);
+  }
+  return launch_next_with(bytes, quantize_both_kernel<NV, WIDE>, dim3((unsigned)blocks),
+                          dim3(kQuantThreads), st, k);
+}
 template <bool NV, bool WIDE>
 static cudaError_t launch_quantize_as(QuantK k, cudaStream_t st) {
   const int64_t row_tiles = (k.rows + kQuantRows - 1) / kQuantRows;
-  if (k.q.codes) {
-    k.tiles = k.q.scale_tiles;
-    if (row_tiles * k.tiles >= (1ll << 31)) return cudaErrorInvalidValue;
-    const cudaError_t e = launch_next(quantize_rows_kernel<NV, WIDE>,
-                                      dim3((unsigned)(row_tiles * k.tiles)), dim3(kQuantThreads),
-                                      st, k);
-    if (e != cudaSuccess) return e;
-  }
-  if (!k.qt.codes) return cudaSuccess;
-  k.tiles = (k.cols + 127) / 128 * 2;  // the last half too: its scales are padding
-  if (row_tiles * k.tiles >= (1ll << 31)) return cudaErrorInvalidValue;
-  return launch_next(quantize_cols_kernel<NV, WIDE>, dim3((unsigned)(row_tiles * k.tiles)),
-                     dim3(kQuantThreads), st, k);
+  const bool both = k.q.codes && k.qt.codes;
+  // (along the columns the last half too: its scales are padding)
+  k.tiles = both ? (k.cols + kQuantRows - 1) / kQuantRows
+            : k.q.codes ? k.q.scale_tiles : (k.cols + 127) / 128 * 2;
+  const int64_t blocks = row_tiles * k.tiles;
+  if (blocks >= (1ll << 31)) return cudaErrorInvalidValue;
+  if (both) return launch_quantize_both<NV, WIDE>(k, blocks, st);
+  return launch_next(k.q.codes ? quantize_rows_kernel<NV, WIDE> : quantize_cols_kernel<NV, WIDE>,
+                     dim3((unsigned)blocks), dim3(kQuantThreads), st, k);
 }
 
 cudaError_t launch_quantize(const QuantK& k, cudaStream_t st) {
@@ -275,72 +443,97 @@ cudaError_t launch_quantize(const QuantK& k, cudaStream_t st) {
 }
 
 // --------------------------------------------------------------- dequantise --
-// A thread takes 8 columns of four rows at a time: 4 bytes of codes, one scale.
-template <bool NV, bool WIDE>
-__global__ void __launch_bounds__(kThreads)
-    dequantize_kernel(const __grid_constant__ DequantK k, int log2_across) {
+// A warp takes 256 columns of every 8th row of a block's, PASSES of them, a lane 8
+// columns: 4 bytes of codes and one scale of each.  Bound by memory, mostly by the
+// stores: 8192 x 4096 to bf16 (86 MB) 16.5 us.  (Walking down the rows four at a
+// time with every address from the walk's took 19.3, 11 instructions a value.)
+constexpr int kDequantCols = 256, kDequantDown = 8;
+template <bool NV, bool WIDE, int PASSES>
+__global__ void __launch_bounds__(kQuantThreads)
+    dequantize_kernel(const __grid_constant__ DequantK k, int tiles) {
+  constexpr int kElem = WIDE ? 4 : 2, kRows = kDequantDown * PASSES;
   after_previous_kernel();
   const float g = NV && k.g ? *(volatile const float*)k.g : 1.0f;
+  const int64_t part = blockIdx.x / (uint32_t)tiles;
+  const int64_t col = (blockIdx.x - part * tiles) * kDequantCols + threadIdx.x % 32 * 8;
+  const int64_t row0 = part * kRows + threadIdx.x / 32;
+  if (col >= k.cols || row0 >= k.rows) return;
   const Extent e{k.rows, k.cols};
-  const int across = 1 << log2_across, down = kThreads >> log2_across;
-  const int64_t col = ((int64_t)blockIdx.x * across + (threadIdx.x & (across - 1))) * 8;
-  if (col >= k.cols) return;
+  const int there =
+      (int)min((k.rows - row0 + kDequantDown - 1) / kDequantDown, (int64_t)PASSES);
+  const int64_t last = row0 + (there - 1) * kDequantDown;
+  const bool in = in_extent(col / 2, col / 2 + 4, 0, k.q.line_bytes, ZERO_SITE_FP4) &&
+                  in_extent(last, last + 1, 0, k.rows, ZERO_SITE_FP4);
+  // (a block's rows lie in one tile of scales)
+  const int64_t block = col / (NV ? 16 : 32);
+  const int64_t tile = ((row0 >> 7) * k.q.scale_tiles + block / 4) * kScaleTile;
+  const unsigned char* scales = k.q.scales + tile + (block & 3);
+  const unsigned char* from = k.q.codes + row0 * k.q.ld + col / 2;
+  uint32_t codes[PASSES], scale[PASSES];
+#pragma unroll
+  for (int p = 0; p < PASSES; ++p) {
+    const int r = ((int)row0 & 127) + p * kDequantDown, at = (r & 31) * 16 + (r >> 5) * 4;
+    codes[p] = scale[p] = 0;
+    if (p < there && in && in_extent(tile + at, tile + at + 4, 0, k.q.scale_bytes, ZERO_SITE_FP4)) {
+      codes[p] = *reinterpret_cast<const uint32_t*>(from);
+      scale[p] = scales[at];
+    }
+    from += kDequantDown * k.q.ld;
+  }
   const int valid = k.cols - col < 8 ? (int)(k.cols - col) : 8;
-  const int64_t block = col / (NV ? 16 : 32), per_tile = k.q.scale_tiles * kScaleTile;
-  const unsigned char* scales = k.q.scales + block / 4 * kScaleTile + block % 4;
-  const int64_t step = (int64_t)gridDim.y * down;
-  Down<WIDE, ZERO_SITE_FP4> y(k.y, (int64_t)blockIdx.y * down + (threadIdx.x >> log2_across), step, col, valid);
-  const unsigned char* from = k.q.codes + y.row * k.q.ld + col / 2;
-  const int64_t down_bytes = step * k.q.ld;
-  for (; y.row < k.rows; y.on(4), from += 4 * down_bytes) {
-    uint32_t codes[4], scale[4];
-    int64_t row = y.row;
-    const unsigned char* at = from;
+  const bool fast = k.y.vec && valid == 8;
+  char* to = static_cast<char*>(k.y.p) + (row0 * k.y.ld + col) * kElem;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {  // past the last row the one before again
-      const uint32_t low = (uint32_t)row;
-      const int64_t s = (row >> 7) * per_tile + ((low & 31) << 4 | (low >> 3 & 12));
-      codes[i] = scale[i] = 0;
-      if (in_extent(row, row + 1, 0, k.rows, ZERO_SITE_FP4) &&
-          in_extent(col / 2, col / 2 + 4, 0, k.q.line_bytes, ZERO_SITE_FP4) &&
-          in_extent(s, s + 1, 0, k.q.scale_bytes, ZERO_SITE_FP4)) {
-        codes[i] = *reinterpret_cast<const uint32_t*>(at);
-        scale[i] = scales[s];
+  for (int p = 0; p < PASSES; ++p) {
+    if (p >= there) break;
+    const float d = scale_value<NV>(scale[p], g);
+    float v[8];
+    from_codes8(codes[p], v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], d);
+    if (fast && in) {
+      if (WIDE) {
+        reinterpret_cast<float4*>(to)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(to)[1] = make_float4(v[4], v[5], v[6], v[7]);
+      } else {
+        *reinterpret_cast<uint4*>(to) = pack8(v);
       }
-      const bool more = row + step < k.rows;
-      row += more ? step : 0;
-      at += more ? down_bytes : 0;
+    } else {
+      store8(k.y, row0 + p * kDequantDown, col, valid, v, e, ZERO_SITE_FP4);
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float v[8];
-      from_codes8(codes[i], v);
-      const float d = scale_value<NV>(scale[i], g);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], d);
-      if (y.row + i * step < k.rows) y.put(i, v, e);
-    }
+    to += kDequantDown * k.y.ld * kElem;
   }
 }
 
-template <bool NV>
-static cudaError_t launch_dequantize_as(const DequantK& k, cudaStream_t st) {
-  const Walk w = walk_over(k.rows, k.cols, (int64_t)sm_count() * 8);
-  return k.y.dtype == ZERO_F32
-             ? launch_next(dequantize_kernel<NV, true>, w.grid, dim3(kThreads), st, k,
-                           w.log2_across)
-             : launch_next(dequantize_kernel<NV, false>, w.grid, dim3(kThreads), st, k,
-                           w.log2_across);
+template <int PASSES>
+static cudaError_t launch_dequantize_as(const DequantK& k, int64_t tiles, cudaStream_t st) {
+  const int64_t parts = (k.rows + kDequantDown * PASSES - 1) / (kDequantDown * PASSES);
+  if (parts * tiles >= (1ll << 31)) return cudaErrorInvalidValue;
+  const bool wide = k.y.dtype == ZERO_F32;
+  return launch_next(
+      k.nv ? (wide ? dequantize_kernel<true, true, PASSES> : dequantize_kernel<true, false, PASSES>)
+      : wide ? dequantize_kernel<false, true, PASSES>
+             : dequantize_kernel<false, false, PASSES>,
+      dim3((unsigned)(parts * tiles)), dim3(kQuantThreads), st, k, (int)tiles);
 }
 cudaError_t launch_dequantize(const DequantK& k, cudaStream_t st) {
   if (k.rows == 0 || k.cols == 0) return cudaSuccess;
-  return k.nv ? launch_dequantize_as<true>(k, st) : launch_dequantize_as<false>(k, st);
+  const int64_t tiles = (k.cols + kDequantCols - 1) / kDequantCols;
+  // Eight rows a thread where that leaves four blocks for each SM; two else, and
+  // from MX to fp32, where the stores alone count and shorter blocks keep more of
+  // them in flight.  (us with eight / two: 8192 x 4096 NV to fp32 38.2 / 43.1, MX to
+  // fp32 37.8 / 33.5; 6001 x 2048 NV 16.0 / 17.1, MX 17.1 / 14.0.)
+  const bool few_bytes = k.nv || k.y.dtype != ZERO_F32;
+  return few_bytes && (k.rows + 63) / 64 * tiles >= 4 * (int64_t)sm_count()
+             ? launch_dequantize_as<8>(k, tiles, st)
+             : launch_dequantize_as<2>(k, tiles, st);
 }
 
 // ------------------------------------------------------- the whole's scale --
 // g = the largest finite magnitude / 2688 (6 x 448: the largest block's scale
 // is then E4M3's largest), 1 where there is none.  Maxima of blocks, then one
-// block over those; a maximum does not depend on the order.
+// block over those; a maximum does not depend on the order.  Bound by memory: 8192
+// x 4096 bf16 (67 MB) 14.3 us, and 2 to 4 for the second kernel.
 __device__ __forceinline__ float block_max(float v) {
   __shared__ float part[32];
 #pragma unroll
