@@ -1828,8 +1828,9 @@ static cudaError_t launch_mode(const ProductK& in, cudaStream_t st) {
       const bool fused = fuses_bias(bn, S, tiles_j);
       const int64_t tiles = tiles_i * tiles_j + (fused ? 0 : (bias_rows + 255) / 256);
       const double waves = (double)((tiles * S + pairs - 1) / pairs);
-      double step = bn > 128 ? (exact ? 520 + 1500.0 / kRound : 520) : 430;
-      if (FP4) step = bn <= 128 ? 512 : k.blocks_of == 16 ? 596 : 550;
+      const double whole = FP4 ? (bn <= 128 ? 512 : k.blocks_of == 16 ? 596 : 550)
+                               : (bn <= 128 ? 430 : 520);
+      double step = bn > 128 && exact ? whole + 1500.0 / kRound : whole;
       const double shift = 300 + 4.2 * ((gen_a ? kRowsCta : 0) + (gen_b ? bn / 2 : 0));
       if ((gen_a || gen_b) && step < shift) step = shift;
       const double cost =
