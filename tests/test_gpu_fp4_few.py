@@ -58,3 +58,25 @@ def test_rows_do_not_depend_on_their_neighbours(cuda, Z, form):
         z = torch.empty(m, n, device="cuda")
         Z.zero_fp4_linear(x.mat, w.mat, fmt(Z, form), m, n, k, None, z, n, Z.ZERO_F32)
         assert torch.equal(z, y[:m])
+
+
+@pytest.mark.parametrize("form", ["mx", "nv"])
+def test_nothing_to_contract(cuda, Z, form):
+    """k = 0: the bias alone through the epilogue."""
+    run_linear(Z, 3, 40, 0, form, bias=BF, act="silu", residual=F32)
+
+
+@pytest.mark.parametrize("form", ["mx", "nv"])
+@pytest.mark.parametrize("m,n,k", [(700, 1, 40), (700, 8, 130), (4100, 5, 264), (90, 3, 20000)])
+def test_dweight_of_few_outputs(cuda, Z, m, n, k, form):
+    for out, add in ((F32, True), (BF, False), (BF, True)):
+        g = torch.Generator().manual_seed(m + 3 * n + 5 * k)
+        dy, vd, gd = operand(Z, g, n, m, form)
+        x, vx, gx = operand(Z, g, k, m, form, 32)
+        old = randn(g, n, k, dtype=out)
+        DW = Guarded(n, k, out, 5, 1, old)
+        Z.zero_fp4_linear_dweight(dy.mat, x.mat, fmt(Z, form), m, n, k, DW.t, DW.ld, code(Z, out), add)
+        torch.cuda.synchronize()
+        dw, _, ew, _ = R.linear_dweight(vd.T, vx.T * (gd * gx), False, old if add else None)
+        R.assert_within(DW.t, dw, ew, "dw")
+        DW.check("dw")
