@@ -20,6 +20,7 @@
 
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <cmath>
 #include <initializer_list>
 
@@ -41,8 +42,11 @@ constexpr int kNoteInts = 8, kNoteBytes = 2048;
 // multiply, bring and store.
 constexpr int kTaskSlots = 4, kTaskAt = 4 * kNoteInts + 3 * 512;
 static_assert(kTaskAt + kTaskSlots * 4 * kNoteInts <= kNoteBytes, "notes");
-constexpr int kStageBytes = kBytesA + 256 * kDeep;
-constexpr int kOrthoStages = (kSmemMost - 1024 - kSideBytes - kNoteBytes) / kStageBytes;
+// A load is 1100 cycles on its way and a stage some 900 more in use, so that the
+// ring's length bounds a step where tiles are few: where none is wider than 128
+// columns, six stages of 24 KiB (768 x 768: __S__).
+constexpr int kRingBytes = kSmemMost - 1024 - kSideBytes - kNoteBytes;
+constexpr int kMostOrthoStages = 6;
 constexpr int kEpi0 = 4, kEpis = 16;             // epilogue warps
 constexpr int kTaskWarp = kEpi0 + kEpis;         // looks tasks up
 constexpr int kOrthoThreads = 32 * (kTaskWarp + 1);
@@ -78,6 +82,7 @@ struct OrthoSteps {
   int cols;                 // of X as stored
   int tall;                 // P's diagonal goes by column
   int side;                 // elements of a diagonal
+  int stages, stage_bytes;  // of the operands' ring
   float *diag_gram, *diag_poly;
   uint32_t* done;           // finished tiles of each matrix, both CTAs'
   float coef[ZERO_NS_MOST][3];
@@ -434,16 +439,75 @@ __device__ __forceinline__ void ortho_piece(float ca, float cb, float cc, bool b
   }
 }
 
+// The operands' ring as one thread loads or multiplies it: a stage and its phase.
+struct OrthoRing {
+  uint32_t at, full, empty, stages, stage_bytes;
+  uint32_t st = 0, ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++st == stages) {
+      st = 0;
+      ph ^= 1;
+    }
+  }
+};
+// A tile's operands, by one thread.  A_C, B_C: boxes along the contraction, else
+// across it, 64 columns each.
+template <bool A_C, bool B_C>
+__device__ __forceinline__ bool ortho_load(OrthoRing& r, const CUtensorMap* map_a,
+                                           const CUtensorMap* map_b, int xa, int ya, int xb,
+                                           int yb, int kblocks, bool lead, uint32_t full_lead,
+                                           uint32_t bytes, bool wide, volatile int* dead) {
+  int c = 0;
+  for (int kb = 0; kb < kblocks; ++kb, c += kDeep) {
+    if (!bar_wait(r.empty + 8 * r.st, r.ph ^ 1, dead)) return false;
+    const uint32_t a_at = r.at + r.st * r.stage_bytes, b_at = a_at + kBytesA;
+    const uint32_t bar = full_lead + 8 * r.st;
+    if (lead) bar_expect(r.full + 8 * r.st, bytes);
+    if (A_C) {
+      tma_load(map_a, a_at, c, ya, bar);
+    } else {
+      tma_load(map_a, a_at, xa, ya + c, bar);
+      tma_load(map_a, a_at + 8192, xa + 64, ya + c, bar);
+    }
+    if (B_C) {
+      tma_load(map_b, b_at, c, yb, bar);
+    } else {
+      tma_load(map_b, b_at, xb, yb + c, bar);
+      if (wide) tma_load(map_b, b_at + 8192, xb + 64, yb + c, bar);
+    }
+    r.next();
+  }
+  return true;
+}
+// A tile's products, by one thread.
+template <bool A_C, bool B_C>
+__device__ __forceinline__ bool ortho_multiply(OrthoRing& r, uint32_t d, uint32_t idesc,
+                                               int kblocks, volatile int* dead) {
+  constexpr uint32_t step_a = A_C ? 2 : 128, step_b = B_C ? 2 : 128;
+  const uint64_t a0 = operand_desc(r.at, A_C), b0 = operand_desc(r.at + kBytesA, B_C);
+  for (int kb = 0; kb < kblocks; ++kb) {
+    if (!bar_wait(r.full + 8 * r.st, r.ph, dead)) return false;
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    const uint64_t stage = (uint64_t)(r.st * (r.stage_bytes >> 4));  // descriptors count 16 bytes
+#pragma unroll
+    for (int q = 0; q < kDeep / 16; ++q)
+      mma_pair(d, a0 + stage + q * step_a, b0 + stage + q * step_b, idesc, kb > 0 || q > 0);
+    commit_pair(r.empty + 8 * r.st, 3);
+    r.next();
+  }
+  return true;
+}
+
 __global__ void __launch_bounds__(kOrthoThreads, 1)
     ortho_kernel(const __grid_constant__ OrthoSteps s, int tasks) {
   extern __shared__ __align__(1024) unsigned char ortho_smem[];
-  __shared__ __align__(8) uint64_t bars[2 * kOrthoStages + 6 + 3 * kBoxChunks + 2 * kTaskSlots];
+  __shared__ __align__(8) uint64_t bars[2 * kMostOrthoStages + 6 + 3 * kBoxChunks + 2 * kTaskSlots];
   __shared__ uint32_t tmem_at;
   __shared__ int dead;
-  constexpr uint32_t stages = kOrthoStages;
+  const uint32_t stages = s.stages, stage_bytes = s.stage_bytes;
   const uint32_t rank = cluster_rank(), half = rank & 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t ring = smem_u32(ortho_smem), boxes = ring + stages * kStageBytes;
+  const uint32_t ring = smem_u32(ortho_smem), boxes = ring + kRingBytes;
   const uint32_t full = smem_u32(bars), empty = full + 8 * stages;
   const uint32_t tfull = empty + 8 * stages, tempty = tfull + 16, ready = tempty + 16;
   const uint32_t efull = ready + 8, edone = efull + 8 * kBoxChunks;
@@ -505,10 +569,11 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
 
   if (warp == 0) {
     const uint32_t full_lead = remote(full, 0);
-    uint32_t st = 0, ph = 0, end_s = 0, end_ph = 0;  // end: where a wait gave up
+    OrthoRing r{ring, full, empty, stages, stage_bytes};
     bool live = true;
+    const bool one = elect();  // issues all of this warp's copies
     for (int t = first; t < tasks; t += clusters) {
-      if (live) live = tasks_in.next(&dead);
+      live = tasks_in.next(&dead);
       if (!live) break;
       const OrthoNote& o = tasks_in.o;
       const OrthoK& k = s.k[o.product];
@@ -526,41 +591,28 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
                                  : o.product == POLY ? &s.maps.gram_b
                                  : s.tall            ? &s.maps.poly
                                                      : x;
-      for (int kb = 0; kb < kblocks; ++kb) {
-        if (live) {
-          live = bar_wait(empty + 8 * st, ph ^ 1, &dead);
-          end_s = st;
-          end_ph = ph;
-        }
-        const uint32_t a_at = ring + st * kStageBytes, b_at = a_at + kBytesA;
-        const uint32_t bar = full_lead + 8 * st;
-        const int c = kb * kDeep;
-        if (elect() && live) {
-          if (half == 0) bar_expect(full + 8 * st, 2 * (kBytesA + b_bytes));
-          if (a_c) {
-            tma_load(map_a, a_at, c, ya + i0, bar);
-          } else {
-            tma_load(map_a, a_at, i0, ya + c, bar);
-            tma_load(map_a, a_at + 8192, i0 + 64, ya + c, bar);
-          }
-          if (b_c) {
-            tma_load(map_b, b_at, c, yb + j0, bar);
-          } else {
-            tma_load(map_b, b_at, j0, yb + c, bar);
-            if (wide) tma_load(map_b, b_at + 8192, j0 + 64, yb + c, bar);
-          }
-        }
-        __syncwarp();
-        if (++st == stages) {
-          st = 0;
-          ph ^= 1;
-        }
+      if (one) {
+        const int xa = i0, xb = j0, row_a = a_c ? ya + i0 : ya, row_b = b_c ? yb + j0 : yb;
+        const uint32_t bytes = 2 * (kBytesA + b_bytes);
+        const bool lead = half == 0;
+        if (a_c && b_c)
+          live = ortho_load<true, true>(r, map_a, map_b, xa, row_a, xb, row_b, kblocks, lead,
+                                        full_lead, bytes, wide, &dead);
+        else if (a_c)
+          live = ortho_load<true, false>(r, map_a, map_b, xa, row_a, xb, row_b, kblocks, lead,
+                                         full_lead, bytes, wide, &dead);
+        else
+          live = ortho_load<false, false>(r, map_a, map_b, xa, row_a, xb, row_b, kblocks, lead,
+                                          full_lead, bytes, wide, &dead);
       }
+      live = __all_sync(0xffffffffu, live);
+      if (!live) break;
     }
-    // a wait gave up: let the loads in flight land before the CTAs return
-    if (!live && half == 0)
+    // a wait gave up: let the loads in flight land before the CTAs return (stages
+    // before st hold phase ph, the others the one before)
+    if (!live && half == 0 && one)
       for (uint32_t q = 0; q < stages; ++q) {
-        const uint32_t parity = q < end_s ? end_ph : end_ph ^ 1;
+        const uint32_t parity = q < r.st ? r.ph : r.ph ^ 1;
         const long long t0 = clock64();
         while (!bar_try(full + 8 * q, parity) && clock64() - t0 < kWaitCycles / 8) {
         }
@@ -568,11 +620,13 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     if (half == 0) {
-      const uint16_t mask = 3;
-      uint32_t st = 0, ph = 0, acc = 0, aph = 0;
+      OrthoRing r{ring, full, empty, stages, stage_bytes};
+      uint32_t acc = 0, aph = 0;
       bool live = bar_wait(ready, 0, &dead);
-      for (int t = first; t < tasks; t += clusters) {
-        live = live && tasks_in.next(&dead);
+      live = __all_sync(0xffffffffu, live);
+      const bool one = elect();  // issues all of the pair's products
+      for (int t = first; t < tasks && live; t += clusters) {
+        live = tasks_in.next(&dead);
         if (!live) break;
         const OrthoK& k = s.k[tasks_in.o.product];
         const bool a_c = k.a_c, b_c = k.b_c;
@@ -580,29 +634,16 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
         // fp32 sums of fp16 values, M = 256, N = bn
         const uint32_t idesc = (1u << 4) | ((a_c ? 0u : 1u) << 15) | ((b_c ? 0u : 1u) << 16) |
                                ((uint32_t)(k.bn >> 3) << 17) | (16u << 24);
-        const uint32_t step_a = a_c ? 2 : 128, step_b = b_c ? 2 : 128;
-        live = live && bar_wait(tempty + 8 * acc, aph ^ 1, &dead);
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint32_t d = tmem + acc * 256;
-        for (int kb = 0; kb < kblocks; ++kb) {
-          live = live && bar_wait(full + 8 * st, ph, &dead);
+        if (one) {
+          live = bar_wait(tempty + 8 * acc, aph ^ 1, &dead);
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          const uint32_t a_at = ring + st * kStageBytes;
-          const uint64_t da = operand_desc(a_at, a_c), db = operand_desc(a_at + kBytesA, b_c);
-          if (elect() && live) {
-#pragma unroll
-            for (int q = 0; q < kDeep / 16; ++q)
-              mma_pair(d, da + q * step_a, db + q * step_b, idesc, kb > 0 || q > 0);
-            commit_pair(empty + 8 * st, mask);
-          }
-          __syncwarp();
-          if (++st == stages) {
-            st = 0;
-            ph ^= 1;
-          }
+          const uint32_t d = tmem + acc * 256;
+          live = live && (a_c && b_c ? ortho_multiply<true, true>(r, d, idesc, kblocks, &dead)
+                          : a_c      ? ortho_multiply<true, false>(r, d, idesc, kblocks, &dead)
+                                     : ortho_multiply<false, false>(r, d, idesc, kblocks, &dead));
+          if (live) commit_pair(tfull + 8 * acc, 3);
         }
-        if (elect() && live) commit_pair(tfull + 8 * acc, mask);
-        __syncwarp();
+        live = __all_sync(0xffffffffu, live);
         if (++acc == 2) {
           acc = 0;
           aph ^= 1;
@@ -1017,7 +1058,7 @@ static cudaError_t launch_ortho(const OrthoSteps& s, int64_t tasks, cudaStream_t
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(sm_count() / 2 * 2));
   cfg.blockDim = dim3(kOrthoThreads);
-  cfg.dynamicSmemBytes = (size_t)kOrthoStages * kStageBytes + kSideBytes + kNoteBytes;
+  cfg.dynamicSmemBytes = (size_t)kRingBytes + kSideBytes + kNoteBytes;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1146,6 +1187,9 @@ cudaError_t launch_orthogonalize(const OrthoCall& c, cudaStream_t st) {
     p.cols = (int)w.ld;
     p.tall = tall;
     p.side = (int)w.side;
+    const int widest = std::max(g.bn, std::max(q.bn, x.bn));
+    p.stage_bytes = kBytesA + widest * kDeep;
+    p.stages = std::min(kRingBytes / p.stage_bytes, kMostOrthoStages);
     p.diag_gram = reinterpret_cast<float*>(base + w.diag_gram);
     p.diag_poly = reinterpret_cast<float*>(base + w.diag_poly);
     p.done = s.done;
