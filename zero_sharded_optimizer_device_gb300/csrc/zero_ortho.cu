@@ -44,7 +44,9 @@ constexpr int kTaskSlots = 4, kTaskAt = 4 * kNoteInts + 3 * 512;
 static_assert(kTaskAt + kTaskSlots * 4 * kNoteInts <= kNoteBytes, "notes");
 // A load is 1100 cycles on its way and a stage some 900 more in use, so that the
 // ring's length bounds a step where tiles are few: where none is wider than 128
-// columns, six stages of 24 KiB (768 x 768: __S__).
+// columns stages take 24 KiB and are six.  (Five steps of 768 x 768 with four, five
+// and six 92.8, 88.8 and 86.5 us, 257 x 8192 215, 191 and 181; eight beside one
+// chunk 90.7 and 179.)
 constexpr int kRingBytes = kSmemMost - 1024 - kSideBytes - kNoteBytes;
 constexpr int kMostOrthoStages = 6;
 constexpr int kEpi0 = 4, kEpis = 16;             // epilogue warps
@@ -450,7 +452,10 @@ struct OrthoRing {
     }
   }
 };
-// A tile's operands, by one thread.  A_C, B_C: boxes along the contraction, else
+// A tile's operands, by one thread in a loop of its layout, as are the products:
+// with the layouts asked for in each step, and the warps' lanes kept together, either
+// warp took 430 cycles a step of any width (768 x 768 96.3 us, now 86.5; 96 x 8192
+// 196 and 155).  A_C, B_C: boxes along the contraction, else
 // across it, 64 columns each.
 template <bool A_C, bool B_C>
 __device__ __forceinline__ bool ortho_load(OrthoRing& r, const CUtensorMap* map_a,
@@ -1079,9 +1084,10 @@ static cudaError_t launch_ortho(const OrthoSteps& s, int64_t tasks, cudaStream_t
 // Tile width: waves of tiles times a tile's steps (see zero_product.cuh's
 // measurements of a step at 256 and at 128 columns; at 64 a step is the loads of
 // A's rows) and its epilogue.  64 columns only where the contraction lies
-// along B's rows, as a box of them holds 64 along its own.  (Five
-// steps of 768 x 768, 6 squares of 256 twelve deep, 105 us at 128 columns, 96 with
-// 64; 1024 x 4096 190 and 180; 24 x 1024 x 1024, 240 squares, takes 256.)
+// along B's rows, as a box of them holds 64 along its own.  (us of five steps with
+// 64 and with 128 at least: 768 x 768, 6 squares of 256 twelve deep, 86.5 and 97.0;
+// 1024 x 4096 163 and 179; 257 x 8192 181 and 193; 24 x 1024 x 1024, 240 squares,
+// takes 256: 441, and 773 with 128.)
 static int tile_width(int64_t squares, int64_t kblocks, bool narrow) {
   const double pairs = (double)(sm_count() / 2), deep = (double)kblocks;
   double best = 0;
