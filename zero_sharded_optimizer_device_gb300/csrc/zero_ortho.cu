@@ -455,8 +455,8 @@ struct OrthoRing {
 // A tile's operands, by one thread in a loop of its layout, as are the products:
 // with the layouts asked for in each step, and the warps' lanes kept together, either
 // warp took 430 cycles a step of any width (768 x 768 96.3 us, now 86.5; 96 x 8192
-// 196 and 155).  A_C, B_C: boxes along the contraction, else
-// across it, 64 columns each.
+// 196 and 155).  A_C, B_C: boxes along the contraction, else across it, 64 columns
+// each.
 template <bool A_C, bool B_C>
 __device__ __forceinline__ bool ortho_load(OrthoRing& r, const CUtensorMap* map_a,
                                            const CUtensorMap* map_b, int xa, int ya, int xb,
