@@ -1012,6 +1012,92 @@ __device__ __forceinline__ void mma_stage_fp4(uint32_t d, uint32_t tmem, uint64_
   }
 }
 
+// The operands' ring as one thread loads or multiplies it: a stage and its phase.
+struct RingFp4 {
+  uint32_t at, full, empty, stages, stage_bytes;
+  uint32_t s = 0, ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++s == stages) {
+      s = 0;
+      ph ^= 1;
+    }
+  }
+};
+// All of a CTA's copies by one thread: its rows of A and of B, its scales of A and
+// the pair's of B.
+static __device__ __forceinline__ void load_fp4(RingFp4 r, const CUtensorMap& map_a,
+                                                const CUtensorMap& map_b,
+                                                const CUtensorMap& map_sa,
+                                                const CUtensorMap& map_sb, const TileK& g,
+                                                int first, int clusters, int tiles, int kb0,
+                                                int kb1, int half, uint32_t full_lead,
+                                                volatile int* dead) {
+  const int bn = g.bn, deep = g.scale_deep;
+  const uint32_t b_bytes = (uint32_t)bn * kDeep;
+  const uint32_t bytes = 2 * (kBytesA + b_bytes + g.scale_bytes);
+  bool live = true;
+  for (TileWalk walk(g, first, clusters); live && walk.t < tiles; walk.next(g, clusters)) {
+    const int i0 = walk.ti * 256 + half * kRowsCta, j0 = walk.tj * bn + half * (bn / 2);
+    const int rows = walk.ti * 2 + half, cols = walk.tj * bn / kRowsCta;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      live = bar_wait(r.empty + 8 * r.s, r.ph ^ 1, dead);
+      if (!live) break;
+      const uint32_t a_at = r.at + r.s * r.stage_bytes, b_at = a_at + kBytesA;
+      const uint32_t bar = full_lead + 8 * r.s, scales = b_at + b_bytes;
+      if (half == 0) bar_expect(r.full + 8 * r.s, bytes);
+      tma_load(&map_a, a_at, kb * kDeep, i0, bar);
+      tma_load(&map_b, b_at, kb * kDeep, j0, bar);
+      scales_load(&map_sa, scales, kb * deep, rows, bar);
+      scales_load(&map_sb, scales + deep * kScaleTile, kb * deep, cols, bar);
+      r.next();
+    }
+  }
+  // a wait gave up: let the loads in flight land before the CTAs return (stages
+  // before this one hold its phase, the others the one before)
+  if (!live && half == 0)
+    for (uint32_t q = 0; q < r.stages; ++q) {
+      const long long t0 = clock64();
+      while (!bar_try(r.full + 8 * q, q < r.s ? r.ph : r.ph ^ 1) &&
+             clock64() - t0 < kWaitCycles / 8) {
+      }
+    }
+}
+// All of a pair's products, by one thread.
+template <bool NV, int CHUNKS>
+__device__ __forceinline__ void multiply_fp4(RingFp4 r, const TileK& g, int first, int clusters,
+                                             int tiles, int kb0, int kb1, uint32_t tmem,
+                                             uint32_t tfull, uint32_t tempty, uint16_t mask,
+                                             volatile int* dead) {
+  const uint32_t bn = g.bn, sets = g.acc_sets, step = r.stage_bytes >> 4;
+  const int round = g.round, rounds = rounds_of(g, kb1 - kb0);
+  const uint64_t a0 = operand_desc(r.at, true), b0 = operand_desc(r.at + kBytesA, true);
+  uint32_t acc = 0, aph = 0;
+  for (TileWalk walk(g, first, clusters); walk.t < tiles; walk.next(g, clusters)) {
+    const uint32_t shift = (uint32_t)walk.tj * bn % kRowsCta / 32;
+    int kb = kb0;
+    for (int q = 0; q < rounds; ++q) {
+      if (!bar_wait(tempty + 8 * acc, aph ^ 1, dead)) return;
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const int start = kb, end = q + 1 < rounds ? kb + round : kb1;
+      for (; kb < end; ++kb) {
+        if (!bar_wait(r.full + 8 * r.s, r.ph, dead)) return;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint64_t stage = (uint64_t)(r.s * step);  // descriptors count 16 bytes
+        mma_stage_fp4<NV, CHUNKS>(tmem + acc * bn, tmem, a0 + stage, b0 + stage,
+                                  r.at + r.s * r.stage_bytes + kBytesA + bn * kDeep, shift, bn,
+                                  kb == start);
+        commit_pair(r.empty + 8 * r.s, mask);
+        r.next();
+      }
+      commit_pair(tfull + 8 * acc, mask);
+      if (++acc == sets) {
+        acc = 0;
+        aph ^= 1;
+      }
+    }
+  }
+}
+
 template <int MODE, int FORM, int KIND>
 __global__ void __launch_bounds__(threads_of(FORM), 1)
     product_kernel(const __grid_constant__ CUtensorMap map_a,
@@ -1135,7 +1221,38 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
   if (early) cluster_arrive();
   int barriers = 0;  // of a split's two, passed so far
 
-  if (warp == 0) {
+  if (FP4 && warp == 0) {
+    if constexpr (FP4)
+      if (elect())
+        load_fp4(RingFp4{ring, full, empty, (uint32_t)g.stages, stage_bytes}, map_a, map_b,
+                 maps.scale_a, maps.scale_b, g, first, clusters, tiles, kb0, kb1, (int)half,
+                 remote(full, leader), &dead);
+    __syncwarp();
+  } else if (FP4 && warp == 1) {
+    if constexpr (FP4) {
+      if (half == 0) {
+        const uint16_t mask = (uint16_t)(3u << leader);
+        const RingFp4 r{ring, full, empty, (uint32_t)g.stages, stage_bytes};
+        const bool live = bar_wait(ready, 0, &dead);
+        const bool nv = g.scale_deep == 4, two = g.scale_chunks == 2;
+        if (elect() && live) {
+          if (nv && two)
+            multiply_fp4<true, 2>(r, g, first, clusters, tiles, kb0, kb1, tmem, tfull, tempty,
+                                  mask, &dead);
+          else if (nv)
+            multiply_fp4<true, 1>(r, g, first, clusters, tiles, kb0, kb1, tmem, tfull, tempty,
+                                  mask, &dead);
+          else if (two)
+            multiply_fp4<false, 2>(r, g, first, clusters, tiles, kb0, kb1, tmem, tfull, tempty,
+                                   mask, &dead);
+          else
+            multiply_fp4<false, 1>(r, g, first, clusters, tiles, kb0, kb1, tmem, tfull, tempty,
+                                   mask, &dead);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 0) {
     const uint32_t full_lead = remote(full, leader);
     const uint32_t stages = g.stages, b_bytes = (uint32_t)g.bn * kDeep;
     const int bn = g.bn, blocks_b = bn / 128;
@@ -1153,8 +1270,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
       // could fall two phases behind and wait for one that never comes.
       if (half != 0 && !load_a && !load_b) break;
       const CUtensorMap* map_i = tj < 0 && bias_b ? &map_b : &map_a;
-      const uint32_t bytes = 2 * ((load_a ? kBytesA : 0) + (load_b ? b_bytes : 0) +
-                                  (FP4 ? g.scale_bytes : 0));
+      const uint32_t bytes = 2 * ((load_a ? kBytesA : 0) + (load_b ? b_bytes : 0));
       for (int kb = kb0; kb < kb1; ++kb) {
         if (live) {
           live = bar_wait(empty + 8 * s, ph ^ 1, &dead);
@@ -1181,12 +1297,6 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
               tma_load(&map_b, b_at, j0, c, bar);
               if (blocks_b > 1) tma_load(&map_b, b_at + 8192, j0 + 64, c, bar);
             }
-          }
-          if constexpr (FP4) {  // of this CTA's rows of A, and of all of the pair's of B
-            const uint32_t at = b_at + b_bytes, deep = g.scale_deep;
-            scales_load(&maps.scale_a, at, kb * (int)deep, i0 / kRowsCta, bar);
-            scales_load(&maps.scale_b, at + deep * kScaleTile, kb * (int)deep,
-                        tj * bn / kRowsCta, bar);
           }
         }
         __syncwarp();
@@ -1225,7 +1335,6 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
         const int ti = walk.ti, tj = walk.tj;
         const bool sums = fused && (bias_b ? ti : tj) == 0;
         const uint32_t idesc = tj >= 0 ? idesc_n : idesc_1, sb = tj >= 0 ? step_b : 0;
-        const uint32_t shift = FP4 ? (uint32_t)tj * bn % kRowsCta / 32 : 0;
         int kb = kb0;
         for (int r = 0; r < rounds; ++r) {
           live = live && bar_wait(tempty + 8 * acc, aph ^ 1, &dead);
@@ -1240,25 +1349,9 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
             const uint64_t db = tj >= 0 ? operand_desc(a_at + kBytesA, b_c)
                                         : operand_desc(ones, true);
             if (elect() && live) {
-              if constexpr (FP4) {
-                const uint32_t scales = a_at + kBytesA + bn * kDeep;
-                const bool one = g.scale_chunks == 1;
-                if (g.scale_deep == 4) {
-                  if (one)
-                    mma_stage_fp4<true, 1>(d, tmem, da, db, scales, shift, bn, kb == start);
-                  else
-                    mma_stage_fp4<true, 2>(d, tmem, da, db, scales, shift, bn, kb == start);
-                } else {
-                  if (one)
-                    mma_stage_fp4<false, 1>(d, tmem, da, db, scales, shift, bn, kb == start);
-                  else
-                    mma_stage_fp4<false, 2>(d, tmem, da, db, scales, shift, bn, kb == start);
-                }
-              } else {
 #pragma unroll
-                for (int q = 0; q < kDeep / 16; ++q)
-                  mma_pair(d, da + q * step_a, db + q * sb, idesc, kb > start || q > 0);
-              }
+              for (int q = 0; q < kDeep / 16; ++q)
+                mma_pair(d, da + q * step_a, db + q * sb, idesc, kb > start || q > 0);
               if (MODE == LIN_DWEIGHT && sums) {
                 const uint64_t dr = operand_desc(bias_b ? a_at + kBytesA : a_at, a_c);
                 const uint64_t d1 = operand_desc(ones, true);
