@@ -620,17 +620,17 @@ cudaError_t launch_tensor_scale(const MaxK& k, float* g, cudaStream_t st) {
 // blocks of 16 outputs that share an SM's instruction slots, each taking 2048
 // codes at a time; or tiles of 256 outputs whose steps of 256 codes follow one
 // another.  Neither depends much on the rows, 1 to 8.  (Measured, NV, 8 rows, few
-// rows / tiles, [n, k]: 1024 x 256 2.3 / 4.6, 1024 x 4096 4.6 / 7.9, 4096 x 4096 5.8
-// / 8.5, 4096 x 8192 9.2 / 10.6, 8192 x 2048 7.2 / 7.3, 8192 x 4096 10.3 / 9.7, 11008 x
-// 2048 9.2 / 7.9, 11008 x 4096 12.6 / 10.1, 16384 x 512 8.5 / 6.1, 50257 x 768 22 /
-// 9.3, 256 x 16384 8.6 / 14.0.)
+// rows / tiles, [n, k]: 1024 x 256 2.3 / 4.5, 1024 x 4096 4.7 / 7.2, 4096 x 4096 5.8
+// / 7.7, 4096 x 8192 9.2 / 9.4, 4096 x 11008 11.2 / 10.8, 8192 x 1024 5.7 / 5.8, 8192 x
+// 2048 7.2 / 6.6, 11008 x 2048 9.2 / 7.1, 11008 x 4096 12.6 / 9.0, 16384 x 512 8.4 /
+// 5.8, 50257 x 768 22 / 9.2, 256 x 16384 8.6 / 11.0.)
 static bool few_rows_win(const ProductK& k) {
   if (k.rows > kFewRows) return false;
   const double codes = 4.0 * (double)k.depth, n = (double)k.cols;
   const double turns = std::max(0.5, codes / 2048), steps = std::ceil(codes / 256);
   const double blocks = std::ceil(n / 16 / sm_count()), tiles = std::ceil(n / 256);
   const double rows_us = 1.7 + blocks * (0.5 + 0.83 * turns);
-  const double tiles_us = 4.9 + 0.16 * steps + 0.022 * tiles + 2e-8 * n * codes;
+  const double tiles_us = 4.7 + 0.115 * steps + 0.02 * tiles + 2.2e-8 * n * codes;
   return rows_us <= tiles_us;
 }
 

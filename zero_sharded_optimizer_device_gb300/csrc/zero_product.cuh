@@ -987,7 +987,7 @@ __device__ __forceinline__ void mma_pair_fp4(uint32_t d, uint64_t a, uint64_t b,
 // of 128 rows make a tile; CHUNKS tiles over B's columns, which begin `shift`
 // rows of 32 into theirs.  Straight code: what issues these instructions is
 // the bottleneck otherwise (a step of 256 x 192, NV: 1184 cycles with a loop
-// over the chunks, 580 without, where loading the operands decides).
+// over the chunks, 596 without, 470 in a loop that one thread runs alone).
 template <bool NV, int CHUNKS>
 __device__ __forceinline__ void mma_stage_fp4(uint32_t d, uint32_t tmem, uint64_t da, uint64_t db,
                                               uint32_t scales, uint32_t shift, uint32_t bn,
@@ -1024,7 +1024,8 @@ struct RingFp4 {
   }
 };
 // All of a CTA's copies by one thread: its rows of A and of B, its scales of A and
-// the pair's of B.
+// the pair's of B.  (A warp whose lanes met at every step, one of them issuing,
+// bounded steps: 8192 x 11008 x 4096 152 us, now 124, 2048 x 2048 x 8192 24.7 and 20.8.)
 static __device__ __forceinline__ void load_fp4(RingFp4 r, const CUtensorMap& map_a,
                                                 const CUtensorMap& map_b,
                                                 const CUtensorMap& map_sa,
@@ -1876,11 +1877,11 @@ static cudaError_t launch_mode(const ProductK& in, cudaStream_t st) {
   // 18.4 / 14.1, 2048 x 1024 x 4096 at BN = 256 23.4 / 18.0, 1024 x 2304 x 768
   // at 128 8.8 / 16.6; four parts, clusters of 8, always lost.)  Lines off
   // 16-byte boundaries bound a step by shifting them: 870 cycles for 144 of
-  // them, 1040 for 192, 1430 for 256.  4 bits: a step is 256 codes, 512 cycles at
-  // BN = 128 and below, 596 (NV) and 550 (MX) at 192.  (us at 128 / 192, NV: 1024
-  // x 11008 x 4096 32.0 / 29.0, 1024 x 4096 x 11008 31.0 / 34.3, 4096 x 4096 x 4096
-  // 42.1 / 36.3, 8192 x 11008 x 4096 194 / 153, 1024 x 1024 x 1024 7.1 / 7.5; in
-  // two parts at 128 256 x 4096 x 11008 18.1 / 14.9, 1024 x 1024 x 1024 7.1 / 8.7.)
+  // them, 1040 for 192, 1430 for 256.  4 bits: a step is 256 codes, 400 cycles at
+  // BN = 128 and below, 470 (NV) and 445 (MX) at 192.  (us at 128 / 192, NV: 1024
+  // x 11008 x 4096 26.8 / 25.4, 1024 x 4096 x 11008 26.1 / 31.2, 4096 x 4096 x 4096
+  // 34.5 / 31.5, 8192 x 11008 x 4096 145 / 124, 1024 x 1024 x 1024 6.8 / 7.2; in
+  // two parts at 128 256 x 4096 x 11008 16.4 / 14.5, 1024 x 1024 x 1024 6.8 / 9.0.)
   // The tensor cores add to their fp32 sums without rounding to nearest, so a
   // long contraction loses digits: 7e-7 of the result after 768 terms, 7e-6
   // after 6000 (in 2-norms).  fp32 results therefore take the sums out every
@@ -1921,7 +1922,7 @@ static cudaError_t launch_mode(const ProductK& in, cudaStream_t st) {
       const bool fused = fuses_bias(bn, S, tiles_j);
       const int64_t tiles = tiles_i * tiles_j + (fused ? 0 : (bias_rows + 255) / 256);
       const double waves = (double)((tiles * S + pairs - 1) / pairs);
-      const double whole = FP4 ? (bn <= 128 ? 512 : k.blocks_of == 16 ? 596 : 550)
+      const double whole = FP4 ? (bn <= 128 ? 400 : k.blocks_of == 16 ? 470 : 445)
                                : (bn <= 128 ? 430 : 520);
       double step = bn > 128 && exact ? whole + 1500.0 / kRound : whole;
       const double shift = 300 + 4.2 * ((gen_a ? kRowsCta : 0) + (gen_b ? bn / 2 : 0));
