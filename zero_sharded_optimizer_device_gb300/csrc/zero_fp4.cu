@@ -578,8 +578,8 @@ __global__ void __launch_bounds__(kThreads)
     for (int64_t col = ((int64_t)blockIdx.x * across + (threadIdx.x & (across - 1))) * 8;
          col < k.cols; col += (int64_t)gridDim.x * across * 8) {
       const int valid = k.cols - col < 8 ? (int)(k.cols - col) : 8;
-      Down<WIDE, ZERO_SITE_FP4> x(k.x, (int64_t)blockIdx.y * down + (threadIdx.x >> log2_across), step, col,
-                   valid);
+      const int64_t first = (int64_t)blockIdx.y * down + (threadIdx.x >> log2_across);
+      Down<WIDE, ZERO_SITE_FP4> x(k.x, first, step, col, valid);
       for (; x.row < k.rows; x.on(kAhead)) {
         Raw8 raw[kAhead];
         x.template get<kAhead>(raw, k.rows, e);

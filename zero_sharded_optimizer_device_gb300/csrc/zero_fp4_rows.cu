@@ -129,8 +129,9 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2)
   const int64_t first = few_output(group, lane >> 3);
   const int lines = min(4, left_of(cols - first, 32));
   const unsigned char* codes_at = w + first * ldw + warp * kFewDeep + unit * 16;
-  const unsigned char* scales_at = ws + ((group >> 3) * tiles + warp * kTiles + (lane >> 2)) * kScaleTile +
-                                   (group & 7) * 64 + (lane & 3) * 16;
+  const int64_t tile0 = (group >> 3) * tiles + warp * kTiles + (lane >> 2);
+  const unsigned char* scales_at =
+      ws + tile0 * kScaleTile + (group & 7) * 64 + (lane & 3) * 16;
   auto issue = [&](int i) {  // in order
     const uint32_t to = ring + i % kFewStages * kFewStage;
 #pragma unroll

@@ -1822,7 +1822,8 @@ static cudaError_t launch_tiles(const CUtensorMap& ma, const CUtensorMap& mb,
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(clusters * 2 * g.splits));
   cfg.blockDim = dim3(threads_of(FORM));
-  cfg.dynamicSmemBytes = (size_t)g.stages * (kBytesA + g.bn * kDeep + g.scale_bytes) + side_bytes(g, FORM);
+  cfg.dynamicSmemBytes =
+      (size_t)g.stages * (kBytesA + g.bn * kDeep + g.scale_bytes) + side_bytes(g, FORM);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
