@@ -814,13 +814,14 @@ int zero_muon_step(const zero_plan_t* plan, const int64_t* tensors, int32_t coun
  *                    E8M0 (2^(byte - 127), at least 2^-127; 255 is NaN);
  *       ZERO_FP4_NV  16 of them, scale s g: s the E4M3 nearest to
  *                    amax / (6 g) (at most 448; 127 is NaN), g the tensor's
- *                    scale, one fp32 in device memory (NULL: 1), positive,
- *                    2^-100 to 2^100
+ *                    scale, one fp32 in device memory (NULL: 1), from
+ *                    2^-117 to FLT_MAX / 2688
  *     with amax the block's largest magnitude.  The code is the nearest (ties
  *     to the even code, beyond 6 to 6) of x / scale (MX; exact) or of
  *     fl(x fl(1 / fl(s g))) (NV; fl rounds to fp32).  A last block may be
  *     short.  A block that holds a NaN or an infinity gets the scale NaN and
- *     codes 0: all of it reads as NaN.  Where an NV block's s is 0, all of it is 0.
+ *     codes 0: all of it reads as NaN.  Where an NV block's s is 0, all of it is
+ *     0; that of a block of zeros is 0 whatever g is.
  *   - A contraction runs along the rows of both operands, so that both have
  *     their blocks along it: for y = x W^T quantise x [m, k] and W [n, k]
  *     along k; for dx = dy W quantise dy [m, n] and W's transpose [k, n]
@@ -854,7 +855,9 @@ int zero_fp4_size(int64_t rows, int64_t cols, int32_t format, int64_t* row_bytes
 
 /* zero_fp4_tensor_scale: *tensor_scale = fl(amax / 2688), amax the largest
  * finite magnitude of x [rows, cols] (2688 = 6 * 448: the block that holds it
- * then has the largest s), or 1 where there is none but 0.  workspace:
+ * then has the largest s), but 2^-117 at least (amax below 1.6e-32: s is then
+ * smaller, and 0 in blocks up to 3.5e-38), or 1 where there is none but 0.
+ * workspace:
  * ZERO_FP4_WORKSPACE bytes of 16-byte aligned device scratch.  Errors as
  * zero_linear, and EINVAL (workspace too small). */
 #define ZERO_FP4_WORKSPACE 4096
@@ -884,7 +887,8 @@ int zero_fp4_dequantize(const zero_fp4_t* q, int64_t rows, int64_t cols, int32_t
  *   dweight  dy [n, m] and x [k, m]:  dw [n, k] (+)= dy x^T
  * Products of codes and block scales are exact; they are added on the tensor
  * cores as those of zero_linear are, 64 at a time, and the sum is multiplied by
- * fl(g_a g_b) before what follows.  Errors as theirs and zero_fp4_quantize's. */
+ * fl(g_a g_b), which has to be finite, before what follows.  Errors as theirs
+ * and zero_fp4_quantize's. */
 int zero_fp4_linear(const zero_fp4_t* x, const zero_fp4_t* w, int32_t format, int64_t m,
                     int64_t n, int64_t k, const zero_linear_epilogue_t* ep, void* y, int64_t ldy,
                     zero_dtype_t ydtype, zero_stream_t stream);

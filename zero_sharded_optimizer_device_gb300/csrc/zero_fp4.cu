@@ -34,6 +34,7 @@ __device__ __forceinline__ uint32_t block_scale(uint32_t top, const Whole& w, fl
   factor = 0.0f;
   if (NV) {
     if (top >= kInfBits) return 0x7Fu;
+    if (top == 0) return 0u;  // whatever g is
     const float most = __uint_as_float(top), t = most * w.by_six_g;
     uint16_t two;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
@@ -531,9 +532,14 @@ cudaError_t launch_dequantize(const DequantK& k, cudaStream_t st) {
 
 // ------------------------------------------------------- the whole's scale --
 // g = the largest finite magnitude / 2688 (6 x 448: the largest block's scale
-// is then E4M3's largest), 1 where there is none.  Maxima of blocks, then one
-// block over those; a maximum does not depend on the order.  Bound by memory: 8192
-// x 4096 bf16 (67 MB) 14.3 us, and 2 to 4 for the second kernel.
+// is then E4M3's largest), 1 where there is none.  Not below kLeastWhole, from
+// which on the least scale's product with g, 2^-9 g, and the reciprocals of that
+// and of 6 g are normal numbers: below 2^-130 or so they are infinite, and values
+// times them NaN.  What this loses is blocks of values up to 3.5e-38 (6 2^-127).
+// Maxima of blocks, then one block over those; a maximum does not depend on the
+// order.  Bound by memory: 8192 x 4096 bf16 (67 MB) 14.3 us, and 2 to 4 for the
+// second kernel.
+constexpr float kLeastWhole = 0x1p-117f;
 __device__ __forceinline__ float block_max(float v) {
   __shared__ float part[32];
 #pragma unroll
@@ -599,7 +605,7 @@ __global__ void __launch_bounds__(kMaxima) maximum_kernel(const float* maxima, i
   after_previous_kernel();
   float top = (int)threadIdx.x < n ? *(volatile const float*)(maxima + threadIdx.x) : 0.0f;
   top = block_max(top);
-  if (threadIdx.x == 0) *g = top > 0.0f ? __fdiv_rn(top, 2688.0f) : 1.0f;
+  if (threadIdx.x == 0) *g = top > 0.0f ? fmaxf(__fdiv_rn(top, 2688.0f), kLeastWhole) : 1.0f;
 }
 
 cudaError_t launch_tensor_scale(const MaxK& k, float* g, cudaStream_t st) {
