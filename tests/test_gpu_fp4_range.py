@@ -109,3 +109,39 @@ def test_a_given_scale_at_the_ends(cuda, Z, g):
     G = torch.tensor(g, dtype=Q.D)
     q.check(*Q.quantise(x, "nv", G)[:2], "q")
     qt.check(*Q.quantise(x.t(), "nv", G)[:2], "qt")
+
+
+@pytest.mark.parametrize("m", [1, 5, 8, 200])
+@pytest.mark.parametrize("form", ["up", "down", "mixed"])
+def test_mx_scales_far_from_one_another(cuda, Z, m, form):
+    """Blocks scaled by 2^e against 2^-e for e to 127, either operand having the large one: sums of multiples of 1/4 below 2^15, exact in fp32."""
+    n, k = 130, 320
+    g = torch.Generator().manual_seed(m)
+    codes = [torch.randint(0, 16, (r, k), generator=g, dtype=torch.uint8) for r in (m, n)]
+    far = torch.tensor([100, 117, 118, 119, 120, 123, 125, 126, 127, 127])
+    sign = {"up": torch.ones(10), "down": -torch.ones(10), "mixed": torch.tensor([1, -1] * 5)}[form].int()
+    byte = [(127 + s * sign * far).to(torch.uint8).expand(r, 10).contiguous() for r, s in ((m, 1), (n, -1))]
+    x, w = (Packed(Z, r, k, "mx").fill(c, b) for r, c, b in zip((m, n), codes, byte))
+    v = [Q.LEVELS[(c & 7).long()] * torch.where(c > 7, -1.0, 1.0) for c in codes]
+    assert bool((v[0].abs() @ v[1].abs().T < 2 ** 22).all())      # (and every partial sum's quarters below 2^24)
+    y = torch.empty(m, n, device="cuda")
+    Z.zero_fp4_linear(x.mat, w.mat, Z.ZERO_FP4_MX, m, n, k, None, y, n, Z.ZERO_F32)
+    assert torch.equal(y.cpu().double(), v[0] @ v[1].T)
+
+
+@pytest.mark.parametrize("m", [4, 200])
+def test_mx_nan_beside_far_scales(cuda, Z, m):
+    """A block whose scale is NaN makes its row NaN whatever the other operand's scale is."""
+    n, k = 40, 64
+    x, w = torch.full((m, k), 2, dtype=torch.uint8), torch.full((n, k), 2, dtype=torch.uint8)
+    bx, bw = torch.full((m, 2), 127, dtype=torch.uint8), torch.full((n, 2), 127, dtype=torch.uint8)
+    bx[2, 1], bw[7, 0], bw[9] = 255, 255, 254
+    qx, qw = Packed(Z, m, k, "mx").fill(x, bx), Packed(Z, n, k, "mx").fill(w, bw)
+    y = torch.empty(m, n, device="cuda")
+    Z.zero_fp4_linear(qx.mat, qw.mat, Z.ZERO_FP4_MX, m, n, k, None, y, n, Z.ZERO_F32)
+    want = torch.full((m, n), 64.0)
+    want[:, 9] = float("inf")
+    want[2], want[:, 7] = float("nan"), float("nan")
+    y = y.cpu()
+    assert torch.equal(torch.isnan(y), torch.isnan(want))
+    assert torch.equal(torch.nan_to_num(y, nan=0.0, posinf=-1.0), torch.nan_to_num(want, nan=0.0, posinf=-1.0))
