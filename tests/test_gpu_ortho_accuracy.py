@@ -1,0 +1,78 @@
+"""Orthogonalised updates against 64 bits without bf16's rounding: the step from
+weights of zero, with lr = scale = 1, leaves the iteration's result in fp32
+(rounded to fp16)."""
+import pytest
+import torch
+
+import ortho_reference as O
+
+pytestmark = pytest.mark.gpu
+F32, D = torch.float32, torch.float64
+
+
+@pytest.fixture(scope="module")
+def Z():
+    import zero_sharded_optimizer_device_gb300 as Z
+    return Z
+
+
+def result(Z, xs, steps=5, coef=O.JORDAN):
+    """The iteration's result of each matrix of xs [batch, m, n], on the GPU."""
+    batch, m, n = xs.shape
+    plan = Z.zero_plan([m * n] * batch, 1, 16)
+    total = Z.zero_plan_info(plan)["psi_pad"]
+    master, momentum, reduced = (torch.zeros(total, device="cuda") for _ in range(3))
+    at = [Z.zero_plan_tensor(plan, t)[0] for t in range(batch)]
+    for t in range(batch):
+        reduced[at[t]:at[t] + m * n] = xs[t].reshape(-1)
+    size = Z.zero_muon_workspace(m, n, batch)
+    work = torch.empty(size, dtype=torch.uint8, device="cuda")
+    hp = Z.muon_hp(lr=1.0, momentum=0.0, nesterov=False, ns=Z.newton_schulz(steps, coef, 1e-7))
+    Z.zero_muon_step(plan, list(range(batch)), m, n, master, momentum, reduced, hp, None, None, Z.ZERO_BF16, work, size)
+    return [-master[a:a + m * n].view(m, n).to(D) for a in at]
+
+
+def off(Z, xs, steps=5, coef=O.JORDAN):
+    """The largest error of a batch, and the share by which results are too small (negative) or large."""
+    worst, bias = 0.0, 0.0
+    for x, got in zip(xs, result(Z, xs, steps, coef)):
+        want = O.exact(x, steps, coef)
+        worst = max(worst, ((got - want).norm() / want.norm()).item())
+        share = ((got * want).sum() / (want * want).sum()).item() - 1
+        bias = share if abs(share) > abs(bias) else bias
+    return worst, bias
+
+
+def random(batch, m, n, seed=0):
+    return torch.randn(batch, m, n, device="cuda", generator=torch.Generator(device="cuda").manual_seed(seed))
+
+
+def steep(batch, m, n, seed=0):
+    """Some strong directions over noise."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    r = min(m, n, 48)
+    new = lambda *s: torch.randn(*s, device="cuda", generator=g)  # noqa: E731
+    return torch.bmm(new(batch, m, r) * torch.arange(1, r + 1, device="cuda").float().pow(-0.7), new(batch, r, n)) + 0.5 * new(batch, m, n)
+
+
+LONG = [(1, 64, 524288), (1, 524288, 64), (1, 2000003, 32), (2, 96, 50257), (3, 40000, 300), (3, 300, 40000), (5, 16385, 70), (5, 70, 16384), (2, 270, 32769)]
+
+
+@pytest.mark.parametrize("batch,m,n", LONG)
+def test_long_sides(cuda, Z, batch, m, n):
+    """The accuracy that matrices of any length have.  Tensor cores leave 6e-9 of a sum of one sign off with every term, the diagonal of G: 3e-3 of it after 524288 if
+    one accumulator takes them all, 1e-4 where sums are taken out every 16384.  With half of that to spare, and twice for G^2."""
+    assert off(Z, random(batch, m, n), 1, (0.0, 1.0, 0.0))[1] == pytest.approx(0.0, abs=1.5e-4)
+    assert off(Z, random(batch, m, n), 1, (0.0, 0.0, 1.0))[1] == pytest.approx(0.0, abs=3e-4)
+    for x in (random(batch, m, n), steep(batch, m, n)):
+        worst, bias = off(Z, x)
+        assert worst < 1e-3 and abs(bias) < 3e-4
+
+
+def test_the_same_bits_again(cuda, Z):
+    """Several rounds in several tiles of each pair of CTAs."""
+    x = random(24, 520, 33000)
+    a, b = (torch.stack(result(Z, x, 2)) for _ in range(2))
+    assert torch.equal(a, b)
+    one = result(Z, x[7:8], 2)[0]
+    assert torch.equal(one, a[7])

@@ -49,6 +49,11 @@ static_assert(kTaskAt + kTaskSlots * 4 * kNoteInts <= kNoteBytes, "notes");
 // chunk 90.7 and 179.)
 constexpr int kRingBytes = kSmemMost - 1024 - kSideBytes - kNoteBytes;
 constexpr int kMostOrthoStages = 6;
+// The tensor cores add to their fp32 sums without rounding to nearest, and the
+// diagonals of G and G^2 are sums of terms of one sign: after 8192, 16384, 32768 and
+// 524288 terms they are 5e-5, 1e-4, 2e-4 and 3e-3 too small.  So sums leave the tensor
+// cores every 256 steps of 64 and are added to nearest.
+constexpr int kOrthoRound = 256;
 constexpr int kEpi0 = 4, kEpis = 16;             // epilogue warps
 constexpr int kTaskWarp = kEpi0 + kEpis;         // looks tasks up
 constexpr int kOrthoThreads = 32 * (kTaskWarp + 1);
@@ -183,6 +188,7 @@ __device__ __forceinline__ OrthoNote note_of(const uint4& lo, const uint4& hi) {
 // arithmetic, as many for the counter and 1400 for the fence where copies are in
 // flight, which the loading warp would miss (24 x 1024 x 1024: 508 us for the products so, 457
 // with this warp).
+template <bool ROUNDS>
 __device__ __forceinline__ void ortho_tasks(const OrthoSteps& s, uint32_t at, uint32_t sfull,
                                             uint32_t sempty, int first, int tasks, int step,
                                             volatile int* dead) {
@@ -190,7 +196,7 @@ __device__ __forceinline__ void ortho_tasks(const OrthoSteps& s, uint32_t at, ui
   bool live = true;
   for (int t = first; t < tasks && live; t += step) {
     const OrthoTask o = ortho_task(s, t);
-    live = ortho_wait(s, o, dead) && bar_wait(sempty + 8 * slot, phase, dead);
+    live = ortho_wait(s, o, dead) && bar_wait<ROUNDS>(sempty + 8 * slot, phase, dead);
     live = __all_sync(0xffffffffu, live);
     if (!live) break;
     fence_copies();
@@ -210,8 +216,9 @@ __device__ __forceinline__ void ortho_tasks(const OrthoSteps& s, uint32_t at, ui
 struct OrthoTasks {
   uint32_t at, sfull, sempty, slot = 0, phase = 0;
   OrthoNote o{};
+  template <bool ROUNDS>
   __device__ __forceinline__ bool next(volatile int* dead) {
-    bool live = bar_wait(sfull + 8 * slot, phase, dead);
+    bool live = bar_wait<ROUNDS>(sfull + 8 * slot, phase, dead);
     live = __all_sync(0xffffffffu, live);
     if (!live) return false;
     o = note_of(lds16(at + slot * 4 * kNoteInts), lds16(at + slot * 4 * kNoteInts + 16));
@@ -270,6 +277,7 @@ struct OrthoSlot {
 // Warp 2: brings the operands of the epilogue's chunks, and before a tile's
 // first the note of the tile, once the epilogue has read the one before
 // (noted).  The epilogue takes it behind that chunk's barrier.
+template <bool ROUNDS>
 __device__ __forceinline__ void ortho_bring(const OrthoSteps& s, OrthoTasks in, uint32_t boxes,
                                             uint32_t note, uint32_t efull, uint32_t bfree,
                                             uint32_t noted, int first, int tasks, int step,
@@ -278,7 +286,7 @@ __device__ __forceinline__ void ortho_bring(const OrthoSteps& s, OrthoTasks in, 
   bool live = true;
   uint32_t issued = 0, note_phase = 1;
   for (int t = first; t < tasks && live; t += step) {
-    live = in.next(dead) && bar_wait(noted, note_phase, dead);
+    live = in.next<ROUNDS>(dead) && bar_wait<ROUNDS>(noted, note_phase, dead);
     live = __all_sync(0xffffffffu, live);
     if (!live) break;
     note_phase ^= 1;
@@ -306,7 +314,7 @@ __device__ __forceinline__ void ortho_bring(const OrthoSteps& s, OrthoTasks in, 
     __syncwarp();  // the note is written when the lane below arrives
     const int y = o.b * s.k[o.product].rows_out + o.i0 + half * kRowsCta;
     for (int c = 0; c < o.chunks; ++c) {
-      live = bar_wait(bfree + 8 * r.slot, r.phase ^ 1, dead);
+      live = bar_wait<ROUNDS>(bfree + 8 * r.slot, r.phase ^ 1, dead);
       live = __all_sync(0xffffffffu, live);
       if (!live) break;
       const uint32_t at = boxes + r.slot * 2 * kBox, bar = efull + 8 * r.slot;
@@ -334,18 +342,19 @@ __device__ __forceinline__ void ortho_bring(const OrthoSteps& s, OrthoTasks in, 
 }
 
 // Warp 3: stores the finished chunks and counts finished tiles.
+template <bool ROUNDS>
 __device__ __forceinline__ void ortho_store(const OrthoSteps& s, OrthoTasks in, uint32_t boxes,
                                             uint32_t edone, uint32_t bfree, int first, int tasks,
                                             int step, int half, volatile int* dead) {
   OrthoSlot r;
   bool live = true;
   for (int t = first; t < tasks && live; t += step) {
-    live = in.next(dead);
+    live = in.next<ROUNDS>(dead);
     if (!live) break;
     const OrthoNote& o = in.o;
     const int row = o.i0 + half * kRowsCta, y = o.b * s.k[o.product].rows_out;
     for (int c = 0; c < o.chunks; ++c) {
-      live = bar_wait(edone + 8 * r.slot, r.phase, dead);
+      live = bar_wait<ROUNDS>(edone + 8 * r.slot, r.phase, dead);
       live = __all_sync(0xffffffffu, live);  // the lanes leave together
       if (!live) break;
       const uint32_t at = boxes + r.slot * 2 * kBox;
@@ -457,14 +466,14 @@ struct OrthoRing {
 // warp took 430 cycles a step of any width (768 x 768 96.3 us, now 86.5; 96 x 8192
 // 196 and 155).  A_C, B_C: boxes along the contraction, else across it, 64 columns
 // each.
-template <bool A_C, bool B_C>
+template <bool A_C, bool B_C, bool ROUNDS>
 __device__ __forceinline__ bool ortho_load(OrthoRing& r, const CUtensorMap* map_a,
                                            const CUtensorMap* map_b, int xa, int ya, int xb,
                                            int yb, int kblocks, bool lead, uint32_t full_lead,
                                            uint32_t bytes, bool wide, volatile int* dead) {
   int c = 0;
   for (int kb = 0; kb < kblocks; ++kb, c += kDeep) {
-    if (!bar_wait(r.empty + 8 * r.st, r.ph ^ 1, dead)) return false;
+    if (!bar_wait<ROUNDS>(r.empty + 8 * r.st, r.ph ^ 1, dead)) return false;
     const uint32_t a_at = r.at + r.st * r.stage_bytes, b_at = a_at + kBytesA;
     const uint32_t bar = full_lead + 8 * r.st;
     if (lead) bar_expect(r.full + 8 * r.st, bytes);
@@ -485,13 +494,13 @@ __device__ __forceinline__ bool ortho_load(OrthoRing& r, const CUtensorMap* map_
   return true;
 }
 // A tile's products, by one thread.
-template <bool A_C, bool B_C>
+template <bool A_C, bool B_C, bool ROUNDS>
 __device__ __forceinline__ bool ortho_multiply(OrthoRing& r, uint32_t d, uint32_t idesc,
                                                int kblocks, volatile int* dead) {
   constexpr uint32_t step_a = A_C ? 2 : 128, step_b = B_C ? 2 : 128;
   const uint64_t a0 = operand_desc(r.at, A_C), b0 = operand_desc(r.at + kBytesA, B_C);
   for (int kb = 0; kb < kblocks; ++kb) {
-    if (!bar_wait(r.full + 8 * r.st, r.ph, dead)) return false;
+    if (!bar_wait<ROUNDS>(r.full + 8 * r.st, r.ph, dead)) return false;
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint64_t stage = (uint64_t)(r.st * (r.stage_bytes >> 4));  // descriptors count 16 bytes
 #pragma unroll
@@ -503,6 +512,19 @@ __device__ __forceinline__ bool ortho_multiply(OrthoRing& r, uint32_t d, uint32_
   return true;
 }
 
+// The sums at `to` += those at `from`: this warp's 16 of every 64 columns.
+static __device__ __noinline__ void ortho_join(uint32_t to, uint32_t from, int columns) {
+  for (int c = 0; c < columns; c += 64, to += 64, from += 64) {
+    uint32_t r[16];
+    tmem_load16(to, r);
+    tmem_add<16>(from, r);
+    tmem_store16(to, r);
+  }
+}
+
+// ROUNDS: a product has more than kOrthoRound steps.  (One kernel for both takes
+// 768 x 768 in 109.9 us instead of 108.5.)
+template <bool ROUNDS>
 __global__ void __launch_bounds__(kOrthoThreads, 1)
     ortho_kernel(const __grid_constant__ OrthoSteps s, int tasks) {
   extern __shared__ __align__(1024) unsigned char ortho_smem[];
@@ -578,7 +600,7 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
     bool live = true;
     const bool one = elect();  // issues all of this warp's copies
     for (int t = first; t < tasks; t += clusters) {
-      live = tasks_in.next(&dead);
+      live = tasks_in.next<ROUNDS>(&dead);
       if (!live) break;
       const OrthoNote& o = tasks_in.o;
       const OrthoK& k = s.k[o.product];
@@ -601,14 +623,14 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
         const uint32_t bytes = 2 * (kBytesA + b_bytes);
         const bool lead = half == 0;
         if (a_c && b_c)
-          live = ortho_load<true, true>(r, map_a, map_b, xa, row_a, xb, row_b, kblocks, lead,
-                                        full_lead, bytes, wide, &dead);
+          live = ortho_load<true, true, ROUNDS>(r, map_a, map_b, xa, row_a, xb, row_b,
+                                                kblocks, lead, full_lead, bytes, wide, &dead);
         else if (a_c)
-          live = ortho_load<true, false>(r, map_a, map_b, xa, row_a, xb, row_b, kblocks, lead,
-                                         full_lead, bytes, wide, &dead);
+          live = ortho_load<true, false, ROUNDS>(r, map_a, map_b, xa, row_a, xb, row_b,
+                                                 kblocks, lead, full_lead, bytes, wide, &dead);
         else
-          live = ortho_load<false, false>(r, map_a, map_b, xa, row_a, xb, row_b, kblocks, lead,
-                                          full_lead, bytes, wide, &dead);
+          live = ortho_load<false, false, ROUNDS>(r, map_a, map_b, xa, row_a, xb, row_b,
+                                                  kblocks, lead, full_lead, bytes, wide, &dead);
       }
       live = __all_sync(0xffffffffu, live);
       if (!live) break;
@@ -627,11 +649,11 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
     if (half == 0) {
       OrthoRing r{ring, full, empty, stages, stage_bytes};
       uint32_t acc = 0, aph = 0;
-      bool live = bar_wait(ready, 0, &dead);
+      bool live = bar_wait<ROUNDS>(ready, 0, &dead);
       live = __all_sync(0xffffffffu, live);
       const bool one = elect();  // issues all of the pair's products
       for (int t = first; t < tasks && live; t += clusters) {
-        live = tasks_in.next(&dead);
+        live = tasks_in.next<ROUNDS>(&dead);
         if (!live) break;
         const OrthoK& k = s.k[tasks_in.o.product];
         const bool a_c = k.a_c, b_c = k.b_c;
@@ -639,44 +661,71 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
         // fp32 sums of fp16 values, M = 256, N = bn
         const uint32_t idesc = (1u << 4) | ((a_c ? 0u : 1u) << 15) | ((b_c ? 0u : 1u) << 16) |
                                ((uint32_t)(k.bn >> 3) << 17) | (16u << 24);
-        if (one) {
-          live = bar_wait(tempty + 8 * acc, aph ^ 1, &dead);
-          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          const uint32_t d = tmem + acc * 256;
-          live = live && (a_c && b_c ? ortho_multiply<true, true>(r, d, idesc, kblocks, &dead)
-                          : a_c      ? ortho_multiply<true, false>(r, d, idesc, kblocks, &dead)
-                                     : ortho_multiply<false, false>(r, d, idesc, kblocks, &dead));
-          if (live) commit_pair(tfull + 8 * acc, 3);
-        }
-        live = __all_sync(0xffffffffu, live);
-        if (++acc == 2) {
-          acc = 0;
-          aph ^= 1;
-        }
+        int left = kblocks;
+        do {
+          const int steps = ROUNDS && left > kOrthoRound ? kOrthoRound : left;
+          if (one) {
+            live = bar_wait<ROUNDS>(tempty + 8 * acc, aph ^ 1, &dead);
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const uint32_t d = tmem + acc * 256;
+            if (live)
+              live = a_c && b_c ? ortho_multiply<true, true, ROUNDS>(r, d, idesc, steps, &dead)
+                     : a_c ? ortho_multiply<true, false, ROUNDS>(r, d, idesc, steps, &dead)
+                           : ortho_multiply<false, false, ROUNDS>(r, d, idesc, steps, &dead);
+            if (live) commit_pair(tfull + 8 * acc, 3);
+          }
+          live = __all_sync(0xffffffffu, live);
+          if (++acc == 2) {
+            acc = 0;
+            aph ^= 1;
+          }
+          left -= steps;
+        } while (ROUNDS && live && left > 0);
       }
     }
     __syncwarp();
   } else if (warp == 2) {
-    ortho_bring(s, tasks_in, boxes, note, efull, bfree, noted, first, tasks, clusters, (int)half,
-                lane, &dead);
+    ortho_bring<ROUNDS>(s, tasks_in, boxes, note, efull, bfree, noted, first, tasks, clusters,
+                        (int)half, lane, &dead);
     __syncwarp();
   } else if (warp == 3) {
-    ortho_store(s, tasks_in, boxes, edone, bfree, first, tasks, clusters, (int)half, &dead);
+    ortho_store<ROUNDS>(s, tasks_in, boxes, edone, bfree, first, tasks, clusters, (int)half, &dead);
     __syncwarp();
   } else if (warp == kTaskWarp) {
-    ortho_tasks(s, note + kTaskAt, sfull, sempty, first, tasks, clusters, &dead);
+    ortho_tasks<ROUNDS>(s, note + kTaskAt, sfull, sempty, first, tasks, clusters, &dead);
     __syncwarp();
   } else if (warp >= kEpi0) {
     const int w = (warp - kEpi0) & 3, set = (warp - kEpi0) >> 2;
     const int row = w * 32 + lane;
     const uint32_t tempty_lead = remote(tempty, 0);
+    const uint32_t lanes = tmem + ((uint32_t)(w * 32) << 16) + set * 16;
     const bool tall = s.tall;
     uint32_t acc = 0, aph = 0, eb = 0, eph = 0;
     bool ok = true;
     for (int t = first; t < tasks && ok; t += clusters) {
       // the first chunk's operands, and with them the tile's note
-      ok = bar_wait(efull + 8 * eb, eph, &dead);
+      ok = bar_wait<ROUNDS>(efull + 8 * eb, eph, &dead);
       ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      // Rounds: a round's set takes up the sums of the set before, which the round
+      // after it fills.  (Ahead of all that has to be kept in registers else.)
+      for (int left = ROUNDS ? s.k[lds16(note).x].kblocks - kOrthoRound : 0; left > 0;
+           left -= kOrthoRound) {
+        const uint32_t before = acc;
+        ok = bar_wait<ROUNDS>(tfull + 8 * acc, aph, &dead);
+        if (++acc == 2) {
+          acc = 0;
+          aph ^= 1;
+        }
+        ok = ok && bar_wait<ROUNDS>(tfull + 8 * acc, aph, &dead);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        ortho_join(lanes + acc * 256, lanes + before * 256, s.k[lds16(note).x].bn);
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) bar_arrive_fenced(tempty_lead + 8 * before);
+      }
       if (!ok) break;
       const OrthoNote o = note_of(lds16(note), lds16(note + 16));
       const int product = o.product, step = o.step, i0 = o.i0, j0 = o.j0, chunks = o.chunks;
@@ -699,11 +748,11 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
                                                 (lane & 15))));
       __syncwarp();
       if (lane == 0) bar_arrive(noted);
-      ok = bar_wait(tfull + 8 * acc, aph, &dead);
+      ok = bar_wait<ROUNDS>(tfull + 8 * acc, aph, &dead);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      const uint32_t d = tmem + ((uint32_t)(w * 32) << 16) + acc * 256 + set * 16;
+      const uint32_t d = lanes + acc * 256;
       for (int c = 0; c < chunks; ++c) {
         const uint32_t b = eb;
         uint32_t r[16];
@@ -716,7 +765,7 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
           for (int q = 0; q < 16; ++q)
             dc[q] = __shfl_sync(0xffffffffu, c < 2 ? diag_col[0] : diag_col[1],
                                 (c & 1) * 16 + q);
-        ok = bar_wait(efull + 8 * b, eph, &dead);
+        ok = bar_wait<ROUNDS>(efull + 8 * b, eph, &dead);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (++eb == kBoxChunks) {
@@ -1042,6 +1091,7 @@ static bool half_map(CUtensorMap* map, void* p, int64_t cols, int64_t rows, int 
 }
 
 // Pairs of CTAs that are resident together: what a cooperative launch may have.
+template <bool ROUNDS>
 static cudaError_t ortho_pairs(cudaLaunchConfig_t& cfg, int* pairs) {
   static std::atomic<int> known[64];
   int dev = 0;
@@ -1049,9 +1099,9 @@ static cudaError_t ortho_pairs(cudaLaunchConfig_t& cfg, int* pairs) {
   if (e != cudaSuccess) return e;
   int n = known[dev & 63].load();
   if (n == 0) {
-    e = cudaFuncSetAttribute(ortho_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(ortho_kernel<ROUNDS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)cfg.dynamicSmemBytes);
-    if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, ortho_kernel, &cfg);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, ortho_kernel<ROUNDS>, &cfg);
     if (e != cudaSuccess) return e;
     if (n < 1) return cudaErrorInvalidConfiguration;
     known[dev & 63].store(n);
@@ -1059,6 +1109,7 @@ static cudaError_t ortho_pairs(cudaLaunchConfig_t& cfg, int* pairs) {
   *pairs = n;
   return cudaSuccess;
 }
+template <bool ROUNDS>
 static cudaError_t launch_ortho(const OrthoSteps& s, int64_t tasks, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(sm_count() / 2 * 2));
@@ -1074,11 +1125,11 @@ static cudaError_t launch_ortho(const OrthoSteps& s, int64_t tasks, cudaStream_t
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int pairs = 0;
-  cudaError_t e = ortho_pairs(cfg, &pairs);
+  cudaError_t e = ortho_pairs<ROUNDS>(cfg, &pairs);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3((unsigned)(2 * (tasks < pairs ? tasks : pairs)));
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, ortho_kernel, s, (int)tasks);
+  return cudaLaunchKernelEx(&cfg, ortho_kernel<ROUNDS>, s, (int)tasks);
 }
 
 // Tile width: waves of tiles times a tile's steps (see zero_product.cuh's
@@ -1201,7 +1252,8 @@ cudaError_t launch_orthogonalize(const OrthoCall& c, cudaStream_t st) {
     p.done = s.done;
     for (int i = 0; i < c.steps; ++i)
       for (int j = 0; j < 3; ++j) p.coef[i][j] = c.coef[i][j];
-    e = launch_ortho(p, (int64_t)p.tiles_step * batch * c.steps, st);
+    const int64_t tasks = (int64_t)p.tiles_step * batch * c.steps;
+    e = kb_far > kOrthoRound ? launch_ortho<true>(p, tasks, st) : launch_ortho<false>(p, tasks, st);
     if (e != cudaSuccess) return e;
   }
   OrthoFinish f = c.finish;
