@@ -746,8 +746,12 @@ int zero_layer_norm_backward(const void* dy, int64_t lddy, zero_dtype_t dydtype,
  * (3.4445, -4.7750, 2.0315) stay below 1.21), or results are infinite or NaN.
  * A matrix of zeros stays zero; one that holds a NaN or an infinity becomes
  * NaN.  Products take fp16 operands and are summed in fp32; X and the
- * diagonals of G are held to more digits: five such steps are off by 5e-4 to
- * 1e-3 of the result (in 2-norms), before it is rounded. */
+ * diagonals of G are held to more digits.  Five such steps are off (in 2-norms,
+ * before the result is rounded) by up to 1.2e-3 of the result where the smaller
+ * side k is 32 to 256 and the other of any length, 2e-3 from k = 12 on and 5e-3
+ * below.  Beyond 256 they are off by up to 1.2e-3 of random x, but directions that
+ * x lacks are lifted a-fold by each step, and with them the roundings that fall
+ * into them: x of low rank is off by up to 2.5e-3 at 257 and 1.2e-3 at 768. */
 #define ZERO_NS_MOST 16
 typedef struct {
   int32_t steps;
@@ -760,7 +764,8 @@ typedef struct {
  * may be x itself (bf16, same ld and stride).  workspace: 16-byte aligned
  * device scratch of zero_orthogonalize_workspace() bytes (about six bytes for
  * each element of the batch and four for each of the smaller sides' squares,
- * in rows rounded up to 256), to be used by one call at a time.  Errors as
+ * eight and six where those are 256 or less, in rows rounded up to 256), to be
+ * used by one call at a time.  Errors as
  * zero_linear, and EINVAL (ns NULL, steps, eps or coefficients out of range,
  * matrices that overlap, workspace too small), ERANGE (batch of 65536 or
  * more, or 2^31 rows in all). */

@@ -74,5 +74,42 @@ def test_the_same_bits_again(cuda, Z):
     x = random(24, 520, 33000)
     a, b = (torch.stack(result(Z, x, 2)) for _ in range(2))
     assert torch.equal(a, b)
-    one = result(Z, x[7:8], 2)[0]
-    assert torch.equal(one, a[7])
+
+
+# worst of 20 to 100 draws by the model of the number formats, rounded up; the result's rounding to fp16 is 2^-12 of it and adds in squares
+MOST = ((12, 5e-3), (32, 2e-3), (257, 1.2e-3))
+FULL = [(2, 64), (5, 64), (3, 8), (8, 8), (12, 40), (15, 15), (16, 256), (20, 20), (32, 32), (33, 71), (64, 64), (8192, 96), (128, 1024), (256, 256), (257, 300),
+        (768, 768), (1024, 1024), (2048, 1536)]
+
+
+def most(k):
+    return next((bound for below, bound in MOST if k < below), 1.2e-3)
+
+
+@pytest.mark.parametrize("m,n", FULL)
+def test_full_rank(cuda, Z, m, n):
+    assert off(Z, random(8 if m * n < 1 << 18 else 2, m, n, 1))[0] < most(min(m, n))
+
+
+@pytest.mark.parametrize("m,n", [(5, 64), (8, 8), (40, 12), (16, 16), (16, 256), (500, 24), (32, 512), (64, 64), (64, 1024), (8192, 96), (96, 20000), (130, 128),
+                                 (256, 1024), (1024, 255), (256, 256)])
+def test_any_rank_of_a_smaller_side_to_256(cuda, Z, m, n):
+    k = min(m, n)
+    for r in sorted({1, 2, max(1, k // 8), max(1, k // 4), k // 2, k - 1}):
+        xs = torch.bmm(random(4, m, r, 3 + r), random(4, r, n, 4 + r))
+        assert off(Z, xs)[0] < most(k), f"rank {r}"
+
+
+@pytest.mark.parametrize("m,n,rank,bound", [(257, 1024, 1, 2.5e-3), (257, 257, 32, 2.5e-3), (300, 257, 128, 2.5e-3), (768, 768, 1, 1.2e-3), (768, 768, 96, 1.2e-3),
+                                            (768, 768, 384, 1.2e-3)])
+def test_lower_rank_beyond(cuda, Z, m, n, rank, bound):
+    xs = torch.bmm(random(4, m, rank, 3), random(4, rank, n, 4))
+    assert off(Z, xs)[0] < bound
+
+
+def test_a_batch_of_low_rank_and_long_sides(cuda, Z):
+    """Parts of P and X and rounds of the Gram product together, more tiles than pairs of CTAs."""
+    for x in (torch.bmm(random(12, 70, 3, 1), random(12, 3, 20011, 2)), torch.bmm(random(12, 20011, 3, 1), random(12, 3, 70, 2))):
+        assert off(Z, x)[0] < 1.2e-3
+        a, b = (torch.stack(result(Z, x)) for _ in range(2))
+        assert torch.equal(a, b)

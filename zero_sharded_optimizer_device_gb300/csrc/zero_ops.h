@@ -177,7 +177,8 @@ struct OrthoCall {
 // of them a matrix (whole tiles, zeros around it); G and P in `side` of `side`.
 struct OrthoSpace {
   int64_t rows, ld, side, blocks;
-  int64_t hi[2], lo, gram, poly, diag_gram, diag_poly, done, partials, bytes;
+  bool fine;  // see zero_ortho.cu: lo and poly twice
+  int64_t hi[2], lo[2], gram, poly, poly_lo, diag_gram, diag_poly, done, partials, bytes;
 };
 // Whether the kernels' counters hold such a batch.
 bool ortho_fits(int64_t m, int64_t n, int64_t batch);

@@ -12,9 +12,15 @@
 // loses nothing.  The diagonals of G and P, their largest elements, are held
 // apart in fp32, the operands having zeros there, and enter by
 //   G^2 = O^2 + (d_i + d_j) O + d^2,   P X = O_P X + d_P X.
-// Five steps are off by 5e-4 to 7e-4 in 2-norm (random or of any steep
-// spectrum); with operands alone in fp16, 1.3e-3 on random matrices and 4e-2
-// at rank 16; in bf16 1e-2 and 0.3.
+// Five steps are off by 3e-4 to 1e-3 in 2-norm on matrices of full rank; with
+// operands alone in fp16, 1.3e-3 on random matrices and 4e-2 at rank 16; in bf16
+// 1e-2 and 0.3.  Directions that x lacks are lifted a-fold by each step, and what
+// the roundings of P X put there with them, the more the shorter the smaller side
+// k: 1e-3 at 768 (ranks of 96 to 384), 2e-3 at 256, but 2.6e-2 at 16 (rank 1).  So where
+// k is 256 or less (`fine`), P is held in two numbers as well and P X is three
+// products, P's first part by both of X's and its second by X's first: 5e-4 to 1e-3
+// at every rank.  There a product over k is short, and no box of P has a transpose
+// to be stored, whose place the second part takes.
 #include "zero_tile.cuh"
 #include "zero_walk.cuh"
 
@@ -70,6 +76,7 @@ enum OrthoProduct : int { GRAM = 0, POLY = 1, GROW = 2 };
 
 struct OrthoK {
   int kblocks, bn, bn_log2;
+  int passes, steps;        // over the contraction (GROW: parts of P and X); of them all
   int tiles;                // of one matrix
   int before;               // of a step's products before this one
   int tiles_j;              // GROW: across
@@ -80,7 +87,9 @@ struct OrthoMaps {
   CUtensorMap x_a[2], x_b[2];  // GRAM's operands
   CUtensorMap gram_a, gram_b;  // POLY's
   CUtensorMap poly, x[2];      // GROW's
-  CUtensorMap hi[2], lo, gram, gram_t, poly_out, poly_t;  // boxes; _t of 64 x 64
+  CUtensorMap poly_lo, x_lo[2];
+  // boxes; _t of 64 x 64
+  CUtensorMap hi[2], lo[2], gram, gram_t, poly_out, poly_lo_out, poly_t;
 };
 struct OrthoSteps {
   OrthoMaps maps;
@@ -89,6 +98,7 @@ struct OrthoSteps {
   int cols;                 // of X as stored
   int tall;                 // P's diagonal goes by column
   int side;                 // elements of a diagonal
+  int fine;                 // P too is held in two numbers, and all of X multiplied
   int stages, stage_bytes;  // of the operands' ring
   float *diag_gram, *diag_poly;
   uint32_t* done;           // finished tiles of each matrix, both CTAs'
@@ -188,7 +198,7 @@ __device__ __forceinline__ OrthoNote note_of(const uint4& lo, const uint4& hi) {
 // arithmetic, as many for the counter and 1400 for the fence where copies are in
 // flight, which the loading warp would miss (24 x 1024 x 1024: 508 us for the products so, 457
 // with this warp).
-template <bool ROUNDS>
+template <bool CAREFUL>
 __device__ __forceinline__ void ortho_tasks(const OrthoSteps& s, uint32_t at, uint32_t sfull,
                                             uint32_t sempty, int first, int tasks, int step,
                                             volatile int* dead) {
@@ -196,7 +206,7 @@ __device__ __forceinline__ void ortho_tasks(const OrthoSteps& s, uint32_t at, ui
   bool live = true;
   for (int t = first; t < tasks && live; t += step) {
     const OrthoTask o = ortho_task(s, t);
-    live = ortho_wait(s, o, dead) && bar_wait<ROUNDS>(sempty + 8 * slot, phase, dead);
+    live = ortho_wait(s, o, dead) && bar_wait<CAREFUL>(sempty + 8 * slot, phase, dead);
     live = __all_sync(0xffffffffu, live);
     if (!live) break;
     fence_copies();
@@ -216,9 +226,9 @@ __device__ __forceinline__ void ortho_tasks(const OrthoSteps& s, uint32_t at, ui
 struct OrthoTasks {
   uint32_t at, sfull, sempty, slot = 0, phase = 0;
   OrthoNote o{};
-  template <bool ROUNDS>
+  template <bool CAREFUL>
   __device__ __forceinline__ bool next(volatile int* dead) {
-    bool live = bar_wait<ROUNDS>(sfull + 8 * slot, phase, dead);
+    bool live = bar_wait<CAREFUL>(sfull + 8 * slot, phase, dead);
     live = __all_sync(0xffffffffu, live);
     if (!live) return false;
     o = note_of(lds16(at + slot * 4 * kNoteInts), lds16(at + slot * 4 * kNoteInts + 16));
@@ -277,7 +287,7 @@ struct OrthoSlot {
 // Warp 2: brings the operands of the epilogue's chunks, and before a tile's
 // first the note of the tile, once the epilogue has read the one before
 // (noted).  The epilogue takes it behind that chunk's barrier.
-template <bool ROUNDS>
+template <bool CAREFUL>
 __device__ __forceinline__ void ortho_bring(const OrthoSteps& s, OrthoTasks in, uint32_t boxes,
                                             uint32_t note, uint32_t efull, uint32_t bfree,
                                             uint32_t noted, int first, int tasks, int step,
@@ -286,7 +296,7 @@ __device__ __forceinline__ void ortho_bring(const OrthoSteps& s, OrthoTasks in, 
   bool live = true;
   uint32_t issued = 0, note_phase = 1;
   for (int t = first; t < tasks && live; t += step) {
-    live = in.next<ROUNDS>(dead) && bar_wait<ROUNDS>(noted, note_phase, dead);
+    live = in.next<CAREFUL>(dead) && bar_wait<CAREFUL>(noted, note_phase, dead);
     live = __all_sync(0xffffffffu, live);
     if (!live) break;
     note_phase ^= 1;
@@ -314,7 +324,7 @@ __device__ __forceinline__ void ortho_bring(const OrthoSteps& s, OrthoTasks in, 
     __syncwarp();  // the note is written when the lane below arrives
     const int y = o.b * s.k[o.product].rows_out + o.i0 + half * kRowsCta;
     for (int c = 0; c < o.chunks; ++c) {
-      live = bar_wait<ROUNDS>(bfree + 8 * r.slot, r.phase ^ 1, dead);
+      live = bar_wait<CAREFUL>(bfree + 8 * r.slot, r.phase ^ 1, dead);
       live = __all_sync(0xffffffffu, live);
       if (!live) break;
       const uint32_t at = boxes + r.slot * 2 * kBox, bar = efull + 8 * r.slot;
@@ -324,7 +334,7 @@ __device__ __forceinline__ void ortho_bring(const OrthoSteps& s, OrthoTasks in, 
         if (o.product == POLY) box_load(&s.maps.gram, at, x, y, bar);
         if (o.product == GROW) {
           box_load(&s.maps.hi[o.step & 1], at, x, y, bar);
-          box_load(&s.maps.lo, at + kBox, x, y, bar);
+          box_load(&s.maps.lo[o.step & 1], at + kBox, x, y, bar);
         }
       }
       __syncwarp();
@@ -342,19 +352,19 @@ __device__ __forceinline__ void ortho_bring(const OrthoSteps& s, OrthoTasks in, 
 }
 
 // Warp 3: stores the finished chunks and counts finished tiles.
-template <bool ROUNDS>
+template <bool CAREFUL>
 __device__ __forceinline__ void ortho_store(const OrthoSteps& s, OrthoTasks in, uint32_t boxes,
                                             uint32_t edone, uint32_t bfree, int first, int tasks,
                                             int step, int half, volatile int* dead) {
   OrthoSlot r;
   bool live = true;
   for (int t = first; t < tasks && live; t += step) {
-    live = in.next<ROUNDS>(dead);
+    live = in.next<CAREFUL>(dead);
     if (!live) break;
     const OrthoNote& o = in.o;
     const int row = o.i0 + half * kRowsCta, y = o.b * s.k[o.product].rows_out;
     for (int c = 0; c < o.chunks; ++c) {
-      live = bar_wait<ROUNDS>(edone + 8 * r.slot, r.phase, dead);
+      live = bar_wait<CAREFUL>(edone + 8 * r.slot, r.phase, dead);
       live = __all_sync(0xffffffffu, live);  // the lanes leave together
       if (!live) break;
       const uint32_t at = boxes + r.slot * 2 * kBox;
@@ -362,9 +372,11 @@ __device__ __forceinline__ void ortho_store(const OrthoSteps& s, OrthoTasks in, 
       if (elect()) {
         if (o.product == GROW) {
           box_store(&s.maps.hi[~o.step & 1], at, x, y + row);
-          if (o.step + 1 < s.steps) box_store(&s.maps.lo, at + kBox, x, y + row);
+          if (o.step + 1 < s.steps) box_store(&s.maps.lo[~o.step & 1], at + kBox, x, y + row);
         } else {
           box_store(o.product == GRAM ? &s.maps.gram : &s.maps.poly_out, at, x, y + row);
+          if (CAREFUL && s.fine && o.product == POLY)
+            box_store(&s.maps.poly_lo_out, at + kBox, x, y + row);
           if (o.mirror) {
             const CUtensorMap* m = o.product == GRAM ? &s.maps.gram_t : &s.maps.poly_t;
             box_store(m, at + kBox, row, y + x);
@@ -391,7 +403,7 @@ __device__ __forceinline__ void ortho_store(const OrthoSteps& s, OrthoTasks in, 
 // 16 sums v of row `row` of the box (row `i` of the matrix), columns j.. of the
 // matrix from 16-byte unit `unit` of the box on.
 template <int PRODUCT>
-__device__ __forceinline__ void ortho_piece(float ca, float cb, float cc, bool by_column,
+__device__ __forceinline__ void ortho_piece(float ca, float cb, float cc, bool by_column, bool fine,
                                             const float d[16], float diag_row, float* diag_out,
                                             bool mirror, uint32_t at, int row, int i, int j,
                                             int unit, float v[16]) {
@@ -423,7 +435,12 @@ __device__ __forceinline__ void ortho_piece(float ca, float cb, float cc, bool b
         }
         w[q] = r * kScaleP;
       }
-      sts16(p0, to_halves8(w));
+      if (fine) {  // (one square of 256: nothing is mirrored)
+        sts16(p0, split_halves8(w));
+        sts16(p1, to_halves8(w));
+      } else {
+        sts16(p0, to_halves8(w));
+      }
     } else {
       float x[8], y[8];
       halves8(lds16(p0), x);
@@ -466,14 +483,14 @@ struct OrthoRing {
 // warp took 430 cycles a step of any width (768 x 768 96.3 us, now 86.5; 96 x 8192
 // 196 and 155).  A_C, B_C: boxes along the contraction, else across it, 64 columns
 // each.
-template <bool A_C, bool B_C, bool ROUNDS>
+template <bool A_C, bool B_C, bool CAREFUL>
 __device__ __forceinline__ bool ortho_load(OrthoRing& r, const CUtensorMap* map_a,
                                            const CUtensorMap* map_b, int xa, int ya, int xb,
                                            int yb, int kblocks, bool lead, uint32_t full_lead,
                                            uint32_t bytes, bool wide, volatile int* dead) {
   int c = 0;
   for (int kb = 0; kb < kblocks; ++kb, c += kDeep) {
-    if (!bar_wait<ROUNDS>(r.empty + 8 * r.st, r.ph ^ 1, dead)) return false;
+    if (!bar_wait<CAREFUL>(r.empty + 8 * r.st, r.ph ^ 1, dead)) return false;
     const uint32_t a_at = r.at + r.st * r.stage_bytes, b_at = a_at + kBytesA;
     const uint32_t bar = full_lead + 8 * r.st;
     if (lead) bar_expect(r.full + 8 * r.st, bytes);
@@ -494,13 +511,13 @@ __device__ __forceinline__ bool ortho_load(OrthoRing& r, const CUtensorMap* map_
   return true;
 }
 // A tile's products, by one thread.
-template <bool A_C, bool B_C, bool ROUNDS>
+template <bool A_C, bool B_C, bool CAREFUL>
 __device__ __forceinline__ bool ortho_multiply(OrthoRing& r, uint32_t d, uint32_t idesc,
                                                int kblocks, volatile int* dead) {
   constexpr uint32_t step_a = A_C ? 2 : 128, step_b = B_C ? 2 : 128;
   const uint64_t a0 = operand_desc(r.at, A_C), b0 = operand_desc(r.at + kBytesA, B_C);
   for (int kb = 0; kb < kblocks; ++kb) {
-    if (!bar_wait<ROUNDS>(r.full + 8 * r.st, r.ph, dead)) return false;
+    if (!bar_wait<CAREFUL>(r.full + 8 * r.st, r.ph, dead)) return false;
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint64_t stage = (uint64_t)(r.st * (r.stage_bytes >> 4));  // descriptors count 16 bytes
 #pragma unroll
@@ -522,9 +539,9 @@ static __device__ __noinline__ void ortho_join(uint32_t to, uint32_t from, int c
   }
 }
 
-// ROUNDS: a product has more than kOrthoRound steps.  (One kernel for both takes
-// 768 x 768 in 109.9 us instead of 108.5.)
-template <bool ROUNDS>
+// CAREFUL: a product has more than kOrthoRound steps, or the call is `fine`.  (One
+// kernel for all takes 768 x 768 in 109.9 us instead of 108.5.)
+template <bool CAREFUL>
 __global__ void __launch_bounds__(kOrthoThreads, 1)
     ortho_kernel(const __grid_constant__ OrthoSteps s, int tasks) {
   extern __shared__ __align__(1024) unsigned char ortho_smem[];
@@ -600,7 +617,7 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
     bool live = true;
     const bool one = elect();  // issues all of this warp's copies
     for (int t = first; t < tasks; t += clusters) {
-      live = tasks_in.next<ROUNDS>(&dead);
+      live = tasks_in.next<CAREFUL>(&dead);
       if (!live) break;
       const OrthoNote& o = tasks_in.o;
       const OrthoK& k = s.k[o.product];
@@ -622,15 +639,24 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
         const int xa = i0, xb = j0, row_a = a_c ? ya + i0 : ya, row_b = b_c ? yb + j0 : yb;
         const uint32_t bytes = 2 * (kBytesA + b_bytes);
         const bool lead = half == 0;
-        if (a_c && b_c)
-          live = ortho_load<true, true, ROUNDS>(r, map_a, map_b, xa, row_a, xb, row_b,
-                                                kblocks, lead, full_lead, bytes, wide, &dead);
-        else if (a_c)
-          live = ortho_load<true, false, ROUNDS>(r, map_a, map_b, xa, row_a, xb, row_b,
-                                                 kblocks, lead, full_lead, bytes, wide, &dead);
-        else
-          live = ortho_load<false, false, ROUNDS>(r, map_a, map_b, xa, row_a, xb, row_b,
-                                                  kblocks, lead, full_lead, bytes, wide, &dead);
+        const int passes = CAREFUL ? k.passes : 1;
+        for (int pass = 0; pass < passes && live; ++pass) {
+          if (CAREFUL && pass > 0) {  // GROW: P's second part by X's first, and the other way round
+            const CUtensorMap* poly = pass == 1 ? &s.maps.poly_lo : &s.maps.poly;
+            x = pass == 1 ? &s.maps.x[now] : &s.maps.x_lo[now];
+            map_a = s.tall ? x : poly;
+            map_b = s.tall ? poly : x;
+          }
+          if (a_c && b_c)
+            live = ortho_load<true, true, CAREFUL>(r, map_a, map_b, xa, row_a, xb, row_b, kblocks,
+                                                   lead, full_lead, bytes, wide, &dead);
+          else if (a_c)
+            live = ortho_load<true, false, CAREFUL>(r, map_a, map_b, xa, row_a, xb, row_b, kblocks,
+                                                    lead, full_lead, bytes, wide, &dead);
+          else
+            live = ortho_load<false, false, CAREFUL>(r, map_a, map_b, xa, row_a, xb, row_b,
+                                                     kblocks, lead, full_lead, bytes, wide, &dead);
+        }
       }
       live = __all_sync(0xffffffffu, live);
       if (!live) break;
@@ -649,29 +675,29 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
     if (half == 0) {
       OrthoRing r{ring, full, empty, stages, stage_bytes};
       uint32_t acc = 0, aph = 0;
-      bool live = bar_wait<ROUNDS>(ready, 0, &dead);
+      bool live = bar_wait<CAREFUL>(ready, 0, &dead);
       live = __all_sync(0xffffffffu, live);
       const bool one = elect();  // issues all of the pair's products
       for (int t = first; t < tasks && live; t += clusters) {
-        live = tasks_in.next<ROUNDS>(&dead);
+        live = tasks_in.next<CAREFUL>(&dead);
         if (!live) break;
         const OrthoK& k = s.k[tasks_in.o.product];
         const bool a_c = k.a_c, b_c = k.b_c;
-        const int kblocks = k.kblocks;
+        const int kblocks = CAREFUL ? k.steps : k.kblocks;
         // fp32 sums of fp16 values, M = 256, N = bn
         const uint32_t idesc = (1u << 4) | ((a_c ? 0u : 1u) << 15) | ((b_c ? 0u : 1u) << 16) |
                                ((uint32_t)(k.bn >> 3) << 17) | (16u << 24);
         int left = kblocks;
         do {
-          const int steps = ROUNDS && left > kOrthoRound ? kOrthoRound : left;
+          const int steps = CAREFUL && left > kOrthoRound ? kOrthoRound : left;
           if (one) {
-            live = bar_wait<ROUNDS>(tempty + 8 * acc, aph ^ 1, &dead);
+            live = bar_wait<CAREFUL>(tempty + 8 * acc, aph ^ 1, &dead);
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t d = tmem + acc * 256;
             if (live)
-              live = a_c && b_c ? ortho_multiply<true, true, ROUNDS>(r, d, idesc, steps, &dead)
-                     : a_c ? ortho_multiply<true, false, ROUNDS>(r, d, idesc, steps, &dead)
-                           : ortho_multiply<false, false, ROUNDS>(r, d, idesc, steps, &dead);
+              live = a_c && b_c ? ortho_multiply<true, true, CAREFUL>(r, d, idesc, steps, &dead)
+                     : a_c ? ortho_multiply<true, false, CAREFUL>(r, d, idesc, steps, &dead)
+                           : ortho_multiply<false, false, CAREFUL>(r, d, idesc, steps, &dead);
             if (live) commit_pair(tfull + 8 * acc, 3);
           }
           live = __all_sync(0xffffffffu, live);
@@ -680,19 +706,20 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
             aph ^= 1;
           }
           left -= steps;
-        } while (ROUNDS && live && left > 0);
+        } while (CAREFUL && live && left > 0);
       }
     }
     __syncwarp();
   } else if (warp == 2) {
-    ortho_bring<ROUNDS>(s, tasks_in, boxes, note, efull, bfree, noted, first, tasks, clusters,
+    ortho_bring<CAREFUL>(s, tasks_in, boxes, note, efull, bfree, noted, first, tasks, clusters,
                         (int)half, lane, &dead);
     __syncwarp();
   } else if (warp == 3) {
-    ortho_store<ROUNDS>(s, tasks_in, boxes, edone, bfree, first, tasks, clusters, (int)half, &dead);
+    ortho_store<CAREFUL>(s, tasks_in, boxes, edone, bfree, first, tasks, clusters, (int)half,
+                         &dead);
     __syncwarp();
   } else if (warp == kTaskWarp) {
-    ortho_tasks<ROUNDS>(s, note + kTaskAt, sfull, sempty, first, tasks, clusters, &dead);
+    ortho_tasks<CAREFUL>(s, note + kTaskAt, sfull, sempty, first, tasks, clusters, &dead);
     __syncwarp();
   } else if (warp >= kEpi0) {
     const int w = (warp - kEpi0) & 3, set = (warp - kEpi0) >> 2;
@@ -704,20 +731,20 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
     bool ok = true;
     for (int t = first; t < tasks && ok; t += clusters) {
       // the first chunk's operands, and with them the tile's note
-      ok = bar_wait<ROUNDS>(efull + 8 * eb, eph, &dead);
+      ok = bar_wait<CAREFUL>(efull + 8 * eb, eph, &dead);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       // Rounds: a round's set takes up the sums of the set before, which the round
       // after it fills.  (Ahead of all that has to be kept in registers else.)
-      for (int left = ROUNDS ? s.k[lds16(note).x].kblocks - kOrthoRound : 0; left > 0;
+      for (int left = CAREFUL ? s.k[lds16(note).x].steps - kOrthoRound : 0; left > 0;
            left -= kOrthoRound) {
         const uint32_t before = acc;
-        ok = bar_wait<ROUNDS>(tfull + 8 * acc, aph, &dead);
+        ok = bar_wait<CAREFUL>(tfull + 8 * acc, aph, &dead);
         if (++acc == 2) {
           acc = 0;
           aph ^= 1;
         }
-        ok = ok && bar_wait<ROUNDS>(tfull + 8 * acc, aph, &dead);
+        ok = ok && bar_wait<CAREFUL>(tfull + 8 * acc, aph, &dead);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -748,7 +775,7 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
                                                 (lane & 15))));
       __syncwarp();
       if (lane == 0) bar_arrive(noted);
-      ok = bar_wait<ROUNDS>(tfull + 8 * acc, aph, &dead);
+      ok = bar_wait<CAREFUL>(tfull + 8 * acc, aph, &dead);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -765,7 +792,7 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
           for (int q = 0; q < 16; ++q)
             dc[q] = __shfl_sync(0xffffffffu, c < 2 ? diag_col[0] : diag_col[1],
                                 (c & 1) * 16 + q);
-        ok = bar_wait<ROUNDS>(efull + 8 * b, eph, &dead);
+        ok = bar_wait<CAREFUL>(efull + 8 * b, eph, &dead);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (++eb == kBoxChunks) {
@@ -775,14 +802,14 @@ __global__ void __launch_bounds__(kOrthoThreads, 1)
         const uint32_t at = boxes + b * 2 * kBox;
         const int j = j0 + c * 64 + set * 16;
         if (product == GRAM)
-          ortho_piece<GRAM>(ca, cb, cc, tall, dc, diag_row, diag_out, mirror, at, row, i, j,
-                            set * 2, v);
+          ortho_piece<GRAM>(ca, cb, cc, tall, false, dc, diag_row, diag_out, mirror, at, row, i,
+                            j, set * 2, v);
         else if (product == POLY)
-          ortho_piece<POLY>(ca, cb, cc, tall, dc, diag_row, diag_out, mirror, at, row, i, j,
-                            set * 2, v);
+          ortho_piece<POLY>(ca, cb, cc, tall, CAREFUL && s.fine, dc, diag_row, diag_out, mirror,
+                            at, row, i, j, set * 2, v);
         else
-          ortho_piece<GROW>(ca, cb, cc, tall, dc, diag_row, diag_out, mirror, at, row, i, j,
-                            set * 2, v);
+          ortho_piece<GROW>(ca, cb, cc, tall, false, dc, diag_row, diag_out, mirror, at, row, i,
+                            j, set * 2, v);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) bar_arrive(edone + 8 * b);
@@ -1055,6 +1082,7 @@ OrthoSpace ortho_space(int64_t m, int64_t n, int64_t batch) {
   w.rows = up(m, 256);
   w.ld = up(n, 64);
   w.side = up(k, 256);
+  w.fine = w.side == 256;
   // blocks of a matrix's norm
   const Walk walk = ortho_walk(m, n, batch);
   w.blocks = (int64_t)walk.grid.x * walk.grid.y;
@@ -1067,9 +1095,11 @@ OrthoSpace ortho_space(int64_t m, int64_t n, int64_t batch) {
   const int64_t x = batch * w.rows * w.ld * 2, g = batch * w.side * w.side * 2;
   w.hi[0] = take(x);
   w.hi[1] = take(x);
-  w.lo = take(x);
+  w.lo[0] = take(x);
+  w.lo[1] = w.fine ? take(x) : w.lo[0];
   w.gram = take(g);
   w.poly = take(g);
+  w.poly_lo = w.fine ? take(g) : w.poly;
   w.diag_gram = take(batch * w.side * 4);
   w.diag_poly = take(batch * w.side * 4);
   w.done = take(batch * 4);
@@ -1091,7 +1121,7 @@ static bool half_map(CUtensorMap* map, void* p, int64_t cols, int64_t rows, int 
 }
 
 // Pairs of CTAs that are resident together: what a cooperative launch may have.
-template <bool ROUNDS>
+template <bool CAREFUL>
 static cudaError_t ortho_pairs(cudaLaunchConfig_t& cfg, int* pairs) {
   static std::atomic<int> known[64];
   int dev = 0;
@@ -1099,9 +1129,9 @@ static cudaError_t ortho_pairs(cudaLaunchConfig_t& cfg, int* pairs) {
   if (e != cudaSuccess) return e;
   int n = known[dev & 63].load();
   if (n == 0) {
-    e = cudaFuncSetAttribute(ortho_kernel<ROUNDS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(ortho_kernel<CAREFUL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)cfg.dynamicSmemBytes);
-    if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, ortho_kernel<ROUNDS>, &cfg);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, ortho_kernel<CAREFUL>, &cfg);
     if (e != cudaSuccess) return e;
     if (n < 1) return cudaErrorInvalidConfiguration;
     known[dev & 63].store(n);
@@ -1109,7 +1139,7 @@ static cudaError_t ortho_pairs(cudaLaunchConfig_t& cfg, int* pairs) {
   *pairs = n;
   return cudaSuccess;
 }
-template <bool ROUNDS>
+template <bool CAREFUL>
 static cudaError_t launch_ortho(const OrthoSteps& s, int64_t tasks, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(sm_count() / 2 * 2));
@@ -1125,11 +1155,11 @@ static cudaError_t launch_ortho(const OrthoSteps& s, int64_t tasks, cudaStream_t
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int pairs = 0;
-  cudaError_t e = ortho_pairs<ROUNDS>(cfg, &pairs);
+  cudaError_t e = ortho_pairs<CAREFUL>(cfg, &pairs);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3((unsigned)(2 * (tasks < pairs ? tasks : pairs)));
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, ortho_kernel<ROUNDS>, s, (int)tasks);
+  return cudaLaunchKernelEx(&cfg, ortho_kernel<CAREFUL>, s, (int)tasks);
 }
 
 // Tile width: waves of tiles times a tile's steps (see zero_product.cuh's
@@ -1169,7 +1199,7 @@ cudaError_t launch_orthogonalize(const OrthoCall& c, cudaStream_t st) {
   s.done = reinterpret_cast<uint32_t*>(base + w.done);
   s.partials = reinterpret_cast<double*>(base + w.partials);
   s.hi = reinterpret_cast<uint16_t*>(base + w.hi[0]);
-  s.lo = reinterpret_cast<uint16_t*>(base + w.lo);
+  s.lo = reinterpret_cast<uint16_t*>(base + w.lo[0]);
   const bool wide = s.x.dtype == ZERO_F32;
   auto grid = [&](const Walk& walk) {
     return dim3(walk.grid.x, walk.grid.y, (unsigned)batch);
@@ -1191,28 +1221,33 @@ cudaError_t launch_orthogonalize(const OrthoCall& c, cudaStream_t st) {
     const int64_t sq = batch * squares, kb_far = (far + kDeep - 1) / kDeep,
                   kb_k = (k + kDeep - 1) / kDeep;
     const int bn_gram = tile_width(sq, kb_far, !tall), bn_poly = tile_width(sq, kb_k, true);
-    const int bn_grow = tile_width(batch * rows * (up(w.ld, 256) / 256), kb_k, tall);
+    const int passes = w.fine ? 3 : 1;
+    const int bn_grow = tile_width(batch * rows * (up(w.ld, 256) / 256), passes * kb_k, tall);
     // Operands by rows (boxes of 128 rows, or half a tile's width of them) or,
     // where the contraction runs down the rows, in boxes of 64 of them.
     const int64_t all = batch * w.rows, sides = batch * w.side;
-    void *gram = base + w.gram, *poly = base + w.poly;
+    void *gram = base + w.gram, *poly = base + w.poly, *poly_lo = base + w.poly_lo;
     OrthoMaps& m = p.maps;
     bool ok = true;
     for (int i = 0; i < 2; ++i) {
-      void* hi = base + w.hi[i];
+      void *hi = base + w.hi[i], *lo = base + w.lo[i];
       ok = ok && half_map(&m.x_a[i], hi, w.ld, all, tall ? 64 : kRowsCta) &&
            half_map(&m.x_b[i], hi, w.ld, all, tall ? 64 : bn_gram / 2) &&
            half_map(&m.x[i], hi, w.ld, all, tall ? kRowsCta : 64) &&
-           half_map(&m.hi[i], hi, w.ld, all, kRowsCta);
+           (!w.fine || half_map(&m.x_lo[i], lo, w.ld, all, tall ? kRowsCta : 64)) &&
+           half_map(&m.hi[i], hi, w.ld, all, kRowsCta) &&
+           half_map(&m.lo[i], lo, w.ld, all, kRowsCta);
     }
-    ok = ok && half_map(&m.lo, base + w.lo, w.ld, all, kRowsCta) &&
-         half_map(&m.gram_a, gram, w.side, sides, kRowsCta) &&
+    ok = ok && half_map(&m.gram_a, gram, w.side, sides, kRowsCta) &&
          half_map(&m.gram_b, gram, w.side, sides, bn_poly / 2) &&
          half_map(&m.poly, poly, w.side, sides, tall ? bn_grow / 2 : kRowsCta) &&
          half_map(&m.gram, gram, w.side, sides, kRowsCta) &&
          half_map(&m.gram_t, gram, w.side, sides, 64) &&
          half_map(&m.poly_out, poly, w.side, sides, kRowsCta) &&
          half_map(&m.poly_t, poly, w.side, sides, 64);
+    if (w.fine)
+      ok = ok && half_map(&m.poly_lo, poly_lo, w.side, sides, tall ? bn_grow / 2 : kRowsCta) &&
+           half_map(&m.poly_lo_out, poly_lo, w.side, sides, kRowsCta);
     if (!ok) return cudaErrorInvalidValue;
     OrthoK &g = p.k[GRAM], &q = p.k[POLY], &x = p.k[GROW];
     g.kblocks = (int)kb_far;
@@ -1237,13 +1272,19 @@ cudaError_t launch_orthogonalize(const OrthoCall& c, cudaStream_t st) {
     x.tiles_j = (int)(up(w.ld, x.bn) / x.bn);
     x.tiles = (int)(rows * x.tiles_j);
     x.before = q.before + q.tiles;
-    for (OrthoK* o : {&g, &q, &x}) o->bn_log2 = o->bn == 256 ? 8 : o->bn == 128 ? 7 : 6;
+    x.passes = passes;
+    g.passes = q.passes = 1;
+    for (OrthoK* o : {&g, &q, &x}) {
+      o->bn_log2 = o->bn == 256 ? 8 : o->bn == 128 ? 7 : 6;
+      o->steps = o->passes * o->kblocks;
+    }
     p.steps = c.steps;
     p.batch = (int)batch;
     p.tiles_step = x.before + x.tiles;
     p.cols = (int)w.ld;
     p.tall = tall;
     p.side = (int)w.side;
+    p.fine = w.fine;
     const int widest = std::max(g.bn, std::max(q.bn, x.bn));
     p.stage_bytes = kBytesA + widest * kDeep;
     p.stages = std::min(kRingBytes / p.stage_bytes, kMostOrthoStages);
@@ -1253,7 +1294,8 @@ cudaError_t launch_orthogonalize(const OrthoCall& c, cudaStream_t st) {
     for (int i = 0; i < c.steps; ++i)
       for (int j = 0; j < 3; ++j) p.coef[i][j] = c.coef[i][j];
     const int64_t tasks = (int64_t)p.tiles_step * batch * c.steps;
-    e = kb_far > kOrthoRound ? launch_ortho<true>(p, tasks, st) : launch_ortho<false>(p, tasks, st);
+    e = w.fine || kb_far > kOrthoRound ? launch_ortho<true>(p, tasks, st)
+                                       : launch_ortho<false>(p, tasks, st);
     if (e != cudaSuccess) return e;
   }
   OrthoFinish f = c.finish;
