@@ -765,10 +765,9 @@ typedef struct {
  * device scratch of zero_orthogonalize_workspace() bytes (about six bytes for
  * each element of the batch and four for each of the smaller sides' squares,
  * eight and six where those are 256 or less, in rows rounded up to 256), to be
- * used by one call at a time.  Errors as
- * zero_linear, and EINVAL (ns NULL, steps, eps or coefficients out of range,
- * matrices that overlap, workspace too small), ERANGE (batch of 65536 or
- * more, or 2^31 rows in all). */
+ * used by one call at a time.  Errors as zero_linear, and EINVAL (ns NULL, steps,
+ * eps or coefficients out of range, matrices that overlap, workspace too small),
+ * ERANGE (a side beyond 2^28, batch of 65536 or more, or 2^31 rows in all). */
 int zero_orthogonalize_workspace(int64_t m, int64_t n, int64_t batch, int64_t* bytes);
 int zero_orthogonalize(const void* x, int64_t ldx, int64_t stride_x, zero_dtype_t xdtype,
                        int64_t m, int64_t n, int64_t batch, const zero_newton_schulz_t* ns,

@@ -1062,10 +1062,13 @@ __global__ void __launch_bounds__(kThreads)
 // ------------------------------------------------------------------- host --
 static int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
+constexpr int64_t kMostSide = 1ll << 28;
 bool ortho_fits(int64_t m, int64_t n, int64_t batch) {
-  // rows one below the other, tiles and grids in 32 bits; sizes far from 64
+  // rows one below the other, tiles and grids in 32 bits; sizes far from 64.  A Gram
+  // tile of 2^28 columns takes 4.2 million steps of some 400 cycles, less than half of
+  // what its waiters' limit allows.
   const int64_t k = up(m < n ? m : n, 256), rows = up(m, 256), cols = up(n, 128);
-  return batch < 65536 && rows * batch < (1ll << 31) && k * batch < (1ll << 31) &&
+  return batch < 65536 && (m > n ? m : n) <= kMostSide && rows * batch < (1ll << 31) && k * batch < (1ll << 31) &&
          rows / 256 * (cols / 128) < (1ll << 25) / (batch + 1) &&
          k / 256 * (k / 256 + 1) < (1ll << 25) / (batch + 1);
 }
