@@ -1897,8 +1897,11 @@ static cudaError_t launch_mode(const ProductK& in, cudaStream_t st) {
   // 7.2, 9.8, 15e-7; 2048 x 1024 to 4096 28, 24, 24, 19, 19 us and 2.3, 4.7,
   // 6.4, 10, 10e-7; 2048 x 640 to 4096, one round from 12 on, 22.5, 20, 17.5
   // us and 2.1, 4.3, 6.0e-7.)  bf16 results take them out only where the loss
-  // would come near their own rounding, from 32768 terms on: 4e-5 (6e-5 where
-  // all terms have one sign) against 2e-3.
+  // would come near their own rounding, beyond 32768 terms: 3e-5 (8e-5 where all
+  // terms have one sign) against 2e-3.  What counts is additions: with 4 bits one
+  // takes 64 terms instead of 16, so that a round is 3072 of them and the limit
+  // of bf16 results 131072, where they are off by 2e-5 with terms of one sign;
+  // fp32 results are off by 1.5e-7 at 4096 to 262144 terms of one sign.
   const bool f32 = k.epi.out.dtype == ZERO_F32 || (k.dbias.p && k.dbias.dtype == ZERO_F32);
   const bool exact = f32 ? kblocks > kRound : kblocks > 512;
   g.bias_b = k.dbias.p && k.bias_b;
