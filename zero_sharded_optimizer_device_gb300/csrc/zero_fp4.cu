@@ -26,7 +26,8 @@ __device__ __forceinline__ Whole whole_of(const float* at) {
   Whole w;
   w.g = NV && at ? *(volatile const float*)at : 1.0f;
   w.six_g = __fmul_rn(6.0f, w.g);
-  w.by_six_g = __frcp_rn(w.six_g);
+  // finite whatever g is, so that a block of zeros gets the scale 0
+  w.by_six_g = fminf(__frcp_rn(w.six_g), 3.4028234e38f);
   return w;
 }
 template <bool NV>
@@ -34,7 +35,6 @@ __device__ __forceinline__ uint32_t block_scale(uint32_t top, const Whole& w, fl
   factor = 0.0f;
   if (NV) {
     if (top >= kInfBits) return 0x7Fu;
-    if (top == 0) return 0u;  // whatever g is
     const float most = __uint_as_float(top), t = most * w.by_six_g;
     uint16_t two;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
