@@ -543,8 +543,8 @@ int zero_copy(void* dst, const void* src, int64_t bytes, zero_stream_t stream);
 
 /* zero_async_status: number of bounded waits inside the library's kernels
  * that gave up after about 2 s (the gathers' on a bulk copy, those between the
- * roles of the products of zero_linear*, zero_fp4_linear* and
- * zero_orthogonalize) on the current device since the last reset;
+ * roles of the products of zero_linear*, zero_fp4_linear*, zero_orthogonalize
+ * and zero_muon_step) on the current device since the last reset;
  * nonzero means a result is incomplete.  The call that launched the kernel
  * returned ZERO_OK; the kernel still returns (the context stays usable).  No
  * counterpart on the pages.  Synchronizes the device; reset != 0 clears the

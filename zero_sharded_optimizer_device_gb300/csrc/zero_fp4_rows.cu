@@ -20,9 +20,11 @@
 //       token 5.0 us, 4.9 without any of it, 5.3 with both scales compared at every product,
 //       and 256 x 16384 7.2, 7.2 and 8.1; 7.7 with large scales looked for beforehand.)
 // The eight warps of a block split the contraction and are joined in order.
-// Bound by instructions where the weight is large, 4 a code (of 32 lanes): 4096 x
-// 4096 (9.4 MB) 5.4 us for 1 token and 5.8 for 8 (NV), 1024 x 1024 3.0, of which
-// 2 are the launch and the first bytes' way.  (With dp4a on codes as bytes and the
+// Bound by latencies: at 4096 codes a warp has two pieces for a ring that runs three
+// ahead, and a large weight's blocks take turns, two an SM, each with the way of its
+// first bytes, a join and a start; 39 % of the issue slots are used, 4 instructions a
+// code (of 32 lanes).  4096 x 4096 (9.4 MB) 5.4 us for 1 token and 5.9 for 8 (NV), 1024 x
+// 1024 2.4, of which 2 are the launch and the first bytes' way.  (With dp4a on codes as bytes and the
 // tokens decoded for every four outputs 6.8 and 19.5 us; two groups of 16 outputs
 // a warp, which halve the tokens' decoding but leave the SMs 8 warps, 7.8; the
 // tokens' codes in shared memory 5.6 and 6.9.)
