@@ -1107,6 +1107,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
                    const __grid_constant__ TileK g) {
   constexpr bool GEN = FORM == PATCH_GEN, BOX = FORM == BOX_BF16 || FORM == BOX_F32;
   constexpr bool FP4 = KIND == OF_FP4;
+  constexpr int kOwn = 1 + MODE * 8 + FORM * 2 + KIND;  // a slow wait of its own (see bar_wait)
   constexpr int kWidth = FORM == BOX_F32 ? 32 : 64;  // columns of a chunk
   // The epilogue's warps in sets of four (one per 32 rows); a set takes every
   // kSets-th piece of kPiece columns of a tile.  Boxes want twice the warps,
@@ -1233,7 +1234,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
       if (half == 0) {
         const uint16_t mask = (uint16_t)(3u << leader);
         const RingFp4 r{ring, full, empty, (uint32_t)g.stages, stage_bytes};
-        const bool live = bar_wait(ready, 0, &dead);
+        const bool live = bar_wait<kOwn>(ready, 0, &dead);
         const bool nv = g.scale_deep == 4, two = g.scale_chunks == 2;
         if (elect() && live) {
           if (nv && two)
@@ -1273,7 +1274,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
       const uint32_t bytes = 2 * ((load_a ? kBytesA : 0) + (load_b ? b_bytes : 0));
       for (int kb = kb0; kb < kb1; ++kb) {
         if (live) {
-          live = bar_wait(empty + 8 * s, ph ^ 1, &dead);
+          live = bar_wait<kOwn>(empty + 8 * s, ph ^ 1, &dead);
           end_s = s;
           end_ph = ph;
         }
@@ -1330,19 +1331,19 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
       const int round = g.round, rounds = rounds_of(g, kb1 - kb0);
       const bool fused = MODE == LIN_DWEIGHT && g.bias_fused, bias_b = g.bias_b;
       uint32_t s = 0, ph = 0, acc = 0, aph = 0;
-      bool live = bar_wait(ready, 0, &dead);
+      bool live = bar_wait<kOwn>(ready, 0, &dead);
       for (TileWalk walk(g, first); walk.t < tiles; walk.next(g, clusters)) {
         const int ti = walk.ti, tj = walk.tj;
         const bool sums = fused && (bias_b ? ti : tj) == 0;
         const uint32_t idesc = tj >= 0 ? idesc_n : idesc_1, sb = tj >= 0 ? step_b : 0;
         int kb = kb0;
         for (int r = 0; r < rounds; ++r) {
-          live = live && bar_wait(tempty + 8 * acc, aph ^ 1, &dead);
+          live = live && bar_wait<kOwn>(tempty + 8 * acc, aph ^ 1, &dead);
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           const uint32_t d = tmem + acc * bn, d_bias = tmem + bias_column(g, acc);
           const int start = kb, end = r + 1 < rounds ? kb + round : kb1;
           for (; kb < end; ++kb) {
-            live = live && bar_wait(full + 8 * s, ph, &dead);
+            live = live && bar_wait<kOwn>(full + 8 * s, ph, &dead);
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t a_at = ring + s * stage_bytes;
             const uint64_t da = operand_desc(a_at, a_c);
@@ -1460,7 +1461,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
       // rounds before the last: their sums leave the tensor cores' set, which
       // a later round writes again, for a set of their own
       for (int r = 1; r < rounds && ok; ++r) {
-        ok = bar_wait(tfull + 8 * acc, aph, &dead);
+        ok = bar_wait<kOwn>(tfull + 8 * acc, aph, &dead);
         ok = __all_sync(0xffffffffu, ok);
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         for (int piece = set; piece < pieces; piece += kSets) {
@@ -1483,7 +1484,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
         }
       }
       if (!ok) break;
-      ok = bar_wait(tfull + 8 * acc, aph, &dead);
+      ok = bar_wait<kOwn>(tfull + 8 * acc, aph, &dead);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -1545,7 +1546,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
           // other half passes the chunk's phases too: a wait names its phase
           // by parity alone, and one who skipped a phase of a slot would take
           // the phase before it for the one after.
-          ok = bar_wait(efull + 8 * b, bph, &dead);
+          ok = bar_wait<kOwn>(efull + 8 * b, bph, &dead);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           if (kWidth == 32 && (cc & 1) != set >> 1) {
@@ -1641,7 +1642,8 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
       const bool swap = tj < 0 && bias_b, a = swap ? gen_b : gen_a, b = tj >= 0 && gen_b;
       const uint32_t by = swap ? by_b : by_a;
       for (int kb = kb0; kb < kb1; ++kb) {
-        ok = bar_wait(landed + 8 * rb, rph, &dead) && bar_wait(empty + 8 * s, ph ^ 1, &dead);
+        ok = bar_wait<kOwn>(landed + 8 * rb, rph, &dead) &&
+             bar_wait<kOwn>(empty + 8 * s, ph ^ 1, &dead);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const uint32_t a_at = ring + s * stage_bytes, raw = raw0 + rb * raw_step;
@@ -1683,7 +1685,7 @@ __global__ void __launch_bounds__(threads_of(FORM), 1)
         const int i0 = for_a ? ti * 256 + (int)half * kRowsCta : tj * bn + (int)half * (bn / 2);
         const uint32_t bytes = on ? (uint32_t)lines * (kRawLine * kGenWarps) : 0;
         for (int kb = kb0; kb < kb1; ++kb) {
-          live = live && bar_wait(used + 8 * wb, wph ^ 1, &dead);
+          live = live && bar_wait<kOwn>(used + 8 * wb, wph ^ 1, &dead);
           if (elect() && live) {
             const uint32_t bar = landed + 8 * wb;
             bar_expect(bar, bytes);
