@@ -113,3 +113,22 @@ def test_a_batch_of_low_rank_and_long_sides(cuda, Z):
         assert off(Z, x)[0] < 1.2e-3
         a, b = (torch.stack(result(Z, x)) for _ in range(2))
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("m,n", [(16500, 16640), (16640, 16500)])
+def test_rounds_of_every_product(cuda, Z, m, n):
+    """Both sides beyond a round: some rows (columns of a tall x) of one step, each by products of vectors, y = a x + b G x + c G G x."""
+    x = random(1, m, n, 5)[0]
+    got = result(Z, x[None], 1)[0]
+    (a, b, c), = O.coefficients(1)
+    X = x.to(D) / (x.to(D).norm() + 1e-7)
+    if m > n:
+        X, got = X.T, got.T
+    rows = [0, 1, 127, 255, 256, 4095, 16383, 16384, min(m, n) - 1]
+    gram = lambda v: (v @ X) @ X.T  # noqa: E731
+    e = torch.zeros(len(rows), X.shape[0], dtype=D, device="cuda")
+    e[range(len(rows)), rows] = 1.0
+    want = (a * e + b * gram(e) + c * gram(gram(e))) @ X
+    y = got[rows]
+    assert (y - want).norm() < 1e-3 * want.norm()
+    assert ((y * want).sum() / (want * want).sum()).item() == pytest.approx(1.0, abs=3e-4)

@@ -1068,8 +1068,8 @@ bool ortho_fits(int64_t m, int64_t n, int64_t batch) {
   // tile of 2^28 columns takes 4.2 million steps of some 400 cycles, less than half of
   // what its waiters' limit allows.
   const int64_t k = up(m < n ? m : n, 256), rows = up(m, 256), cols = up(n, 128);
-  return batch < 65536 && (m > n ? m : n) <= kMostSide && rows * batch < (1ll << 31) && k * batch < (1ll << 31) &&
-         rows / 256 * (cols / 128) < (1ll << 25) / (batch + 1) &&
+  return batch < 65536 && (m > n ? m : n) <= kMostSide && rows * batch < (1ll << 31) &&
+         k * batch < (1ll << 31) && rows / 256 * (cols / 128) < (1ll << 25) / (batch + 1) &&
          k / 256 * (k / 256 + 1) < (1ll << 25) / (batch + 1);
 }
 
