@@ -1901,9 +1901,10 @@ static cudaError_t launch_mode(const ProductK& in, cudaStream_t st) {
   // us and 2.1, 4.3, 6.0e-7.)  bf16 results take them out only where the loss
   // would come near their own rounding, beyond 32768 terms: 3e-5 (8e-5 where all
   // terms have one sign) against 2e-3.  What counts is additions: with 4 bits one
-  // takes 64 terms instead of 16, so that a round is 3072 of them and the limit
-  // of bf16 results 131072, where they are off by 2e-5 with terms of one sign;
-  // fp32 results are off by 1.5e-7 at 4096 to 262144 terms of one sign.
+  // takes 64 terms instead of 16, so that a round of 48 additions is four times as
+  // long and the limit of bf16 results 131072 terms, where they are off by 2e-5
+  // with terms of one sign; fp32 results are off by 1.5e-7 at 4096 to 262144 terms
+  // of one sign.
   const bool f32 = k.epi.out.dtype == ZERO_F32 || (k.dbias.p && k.dbias.dtype == ZERO_F32);
   const bool exact = f32 ? kblocks > kRound : kblocks > 512;
   g.bias_b = k.dbias.p && k.bias_b;
